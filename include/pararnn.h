@@ -297,6 +297,162 @@ pararnn_status_t pararnn_solve_gru_noalloc(const pararnn_shape_t *shape, const v
                                            const pararnn_newton_t *opt, pararnn_info_t *info,
                                            void *stream);
 
+/*
+ * Gated linear recurrence: the linear-time companion of the ParaGRU cell,
+ * whose decay depends on the input but not on the state, so that one scan
+ * solves it exactly.  Per channel (b, d), with gate planes u = (u_r, u_i, u_x):
+ *     l_t = -power softplus(lam_d) sig(u_r),   a_t = exp(l_t)
+ *     h_t = k_t a_t h_{t-1} + sqrt(1 - a_t^2) sig(u_i) u_x
+ * k_t = 0 where resets[b][t] is non-zero (the first step of a new document in
+ * a packed row: nothing of the state before it is kept), else 1.
+ *   shape   : u strides for u and du, s strides for h and gh
+ *   u       : 3 planes [B][D][T], dtype u_dtype (F32 or BF16)
+ *   lam     : [D] float32;  power : > 0, finite
+ *   h0      : [B][D] float32, or NULL (zero)
+ *   resets  : [B][T] bytes, dense, or NULL (none)
+ *   h       : [B][D][T] float32 out, the states h_1..h_T
+ *   h_last  : [B][D] float32 out, h_T (h_0 when T = 0), or NULL
+ *   ws      : pararnn_gated_workspace_bytes(shape, 0) bytes (0 is possible)
+ * The same conventions as the solves: device pointers, caller's stream, no
+ * allocation, argument checks before any HIP call, any plane layout whose
+ * elements do not overlap.  Channel-major planes run with a lane's steps
+ * side by side, any other layout with a lane per channel.
+ */
+size_t pararnn_gated_workspace_bytes(const pararnn_shape_t *shape, int adjoint);
+pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *const u[3],
+                                    pararnn_dtype_t u_dtype, const float *lam, float power,
+                                    const float *h0, const uint8_t *resets, float *h,
+                                    float *h_last, void *ws, size_t ws_bytes, void *stream);
+/*
+ * Its backward pass, for L = sum_t <gh_t, h_t> + <gh_last, h_T>.
+ *   h       : the states of the forward pass
+ *   gh      : [B][D][T] float32 (s strides), or NULL (zero)
+ *   gh_last : [B][D] float32, or NULL (zero)
+ *   du      : 3 planes out, dtype u_dtype, u strides
+ *   dlam    : [D] float32 out, summed over batch and time in a fixed order
+ *   dh0     : [B][D] float32 out, or NULL
+ *   ws      : pararnn_gated_workspace_bytes(shape, 1) bytes
+ */
+pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const void *const u[3],
+                                            pararnn_dtype_t u_dtype, const float *lam, float power,
+                                            const float *h0, const uint8_t *resets,
+                                            const float *h, const float *gh,
+                                            const float *gh_last, void *const du[3], float *dlam,
+                                            float *dh0, void *ws, size_t ws_bytes, void *stream);
+/*
+ * One step of it for B requests, their states in a pool: for every row b
+ * with 0 <= slots[b] < pool,
+ *     states[slots[b]] = out[b] = a states[slots[b]] + sqrt(1 - a^2) sig(u_i) u_x
+ * A row whose slot lies outside the pool (-1, say) is idle: its output is
+ * zero and no state changes.  The slots of live rows must be distinct.
+ *   u      : 3 row blocks [B][D], dtype u_dtype, rows u_stride_b elements apart
+ *   slots  : [B] int32, or NULL (row b has slot b)
+ *   states : [pool][D] float32, updated in place;  out : [B][D] float32
+ */
+pararnn_status_t pararnn_gated_step(int64_t B, int64_t D, const void *const u[3],
+                                    pararnn_dtype_t u_dtype, int64_t u_stride_b, const float *lam,
+                                    float power, const int32_t *slots, float *states, int64_t pool,
+                                    float *out, void *stream);
+
+/*
+ * Block boundary: what stands between one recurrent block and the next.  Per
+ * step (b, t), over its D channels,
+ *     v = h silu(gate)                               (v = h without a gate)
+ *     y = x + scale (v rstd_post) w_post,            rstd_post = 1/sqrt(mean v^2 + eps)
+ *     z = (y rstd_pre) w_pre,                        rstd_pre  = 1/sqrt(mean y^2 + eps)
+ * h and gate are [B][D][T]-indexed planes (channel-major from the solves and
+ * the projection); x, y, z are time-major [B][T][D] with the channels
+ * contiguous, as pararnn_project reads them, so the change of layout between
+ * the two happens on the way.
+ *   h      : float32, or NULL: y = x, and only the second norm is computed
+ *            (the first norm of a model); gate and w_post are not read then
+ *   gate   : gate_dtype, or NULL (no gate)
+ *   x, y   : x_dtype (share their strides); y may be NULL if h is
+ *   w_post, w_pre : [D] float32
+ *   scale  : finite;  eps : > 0, finite
+ *   z      : z_dtype
+ *   rstd   : [2][B][T] float32 out (rstd_post, rstd_pre), or NULL; without h
+ *            its first half is not written
+ */
+typedef struct {
+    int64_t B, T, D;
+    int64_t h_stride_b, h_stride_d, h_stride_t; /* h, dh                    */
+    int64_t g_stride_b, g_stride_d, g_stride_t; /* gate, dgate              */
+    int64_t x_stride_b, x_stride_t;             /* x, y, gy, dx             */
+    int64_t z_stride_b, z_stride_t;             /* z, gz                    */
+} pararnn_block_shape_t;
+
+pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const float *h,
+                                    const void *gate, pararnn_dtype_t gate_dtype, const void *x,
+                                    pararnn_dtype_t x_dtype, const float *w_post,
+                                    const float *w_pre, float scale, float eps, void *y, void *z,
+                                    pararnn_dtype_t z_dtype, float *rstd, void *stream);
+/*
+ * Its backward pass from the gradients gy of y and gz of z (either may be
+ * NULL, meaning zero) and the forward's rstd.
+ *   dh, dgate : h's and gate's strides; dgate in gate_dtype, NULL without a
+ *               gate; both NULL without h
+ *   dx        : x_dtype, x's strides
+ *   dw_post   : [D] float32 out, NULL without h;  dw_pre : [D] float32 out;
+ *               both summed over batch and time in a fixed order
+ *   ws        : pararnn_block_workspace_bytes(shape) bytes
+ */
+size_t pararnn_block_workspace_bytes(const pararnn_block_shape_t *shape);
+pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, const float *h,
+                                            const void *gate, pararnn_dtype_t gate_dtype,
+                                            const void *x, pararnn_dtype_t x_dtype,
+                                            const float *w_post, const float *w_pre, float scale,
+                                            const float *rstd, const void *gy, const void *gz,
+                                            pararnn_dtype_t z_dtype, float *dh, void *dgate,
+                                            void *dx, float *dw_post, float *dw_pre, void *ws,
+                                            size_t ws_bytes, void *stream);
+
+/*
+ * Scores of given tokens from logits: with p = softmax(scale logits[n]),
+ *     logprob[n] = log p[tokens[n]],  lse[n] = log sum exp(scale logits[n]),
+ *     entropy[n] = -sum p log p,
+ * and the `top` most likely tokens with their log probabilities, most likely
+ * first, the lower index first among equals.
+ *   logits  : [N][V], dtype F32 or BF16, rows row_stride >= V elements apart
+ *   tokens  : [N] int64.  A negative token is not scored: logprob 0.  One
+ *             past the vocabulary scores NaN.
+ *   top     : 0 .. PARARNN_TOP_MAX
+ *   scale   : inverse temperature, > 0, finite
+ *   logprob, entropy, lse : [N] float32 out (entropy, lse may be NULL)
+ *   top_index, top_logprob : [N][top] int64 / float32 out
+ * A logit of -inf is a masked token: probability 0, never an alternative.
+ * Alternatives a row does not have are index -1 with log probability -inf.
+ * A row whose tokens are all masked has lse -inf, entropy 0 and logprob -inf.
+ * A NaN or +inf among a row's logits makes its log probabilities NaN; NaN
+ * logits are no alternatives.
+ *   ws      : pararnn_logprobs_workspace_bytes(...) bytes (0 is possible)
+ */
+#define PARARNN_TOP_MAX 64
+size_t pararnn_logprobs_workspace_bytes(int64_t N, int64_t V, int32_t top);
+pararnn_status_t pararnn_token_logprobs(int64_t N, int64_t V, const void *logits,
+                                        pararnn_dtype_t dtype, int64_t row_stride,
+                                        const int64_t *tokens, int32_t top, float scale,
+                                        float *logprob, float *entropy, float *lse,
+                                        int64_t *top_index, float *top_logprob, void *ws,
+                                        size_t ws_bytes, void *stream);
+/*
+ * Its gradient for the logits,
+ *     dlogits_j = scale (g_logprob ([j = token] - p_j) + g_lse p_j
+ *                        - g_entropy p_j (log p_j + entropy)),
+ * from the forward's lse and entropy; g_* are [N] float32 or NULL (zero).  A
+ * token that is not scored takes no g_logprob; a masked logit's p_j is 0; the
+ * gradient of a row whose tokens are all masked is zero.  dlogits has the
+ * dtype of the logits, rows d_stride elements apart, and may be the logits'
+ * own memory (same stride).
+ */
+pararnn_status_t pararnn_token_logprobs_adjoint(int64_t N, int64_t V, const void *logits,
+                                                pararnn_dtype_t dtype, int64_t row_stride,
+                                                const int64_t *tokens, float scale,
+                                                const float *lse, const float *entropy,
+                                                const float *g_logprob, const float *g_entropy,
+                                                const float *g_lse, void *dlogits,
+                                                int64_t d_stride, void *stream);
+
 /* Static description of a status code. */
 const char *pararnn_status_string(pararnn_status_t status);
 

@@ -174,3 +174,84 @@ def lstm_time_major(u, a, c0, h0, *, tol=1e-6, max_iters=20, strict=False):
     (gate blocks i, f, g, o), a [4][D], c0, h0 [B][D].  Returns (c, h), each
     [B][T][D]."""
     return _LstmTimeMajor.apply(u, a, c0, h0, tol, max_iters, strict)
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ur, ui, ux, lam, h0, power, resets):
+        h, h_last = pr.gated_scan([ur, ui, ux], lam, h0, power=power, resets=resets)
+        ctx.save_for_backward(ur, ui, ux, lam, h0, resets, h)
+        ctx.power = power
+        ctx.set_materialize_grads(False)
+        return h, h_last
+
+    @staticmethod
+    def backward(ctx, gh, gh_last):
+        ur, ui, ux, lam, h0, resets, h = ctx.saved_tensors
+        out = pr.gated_scan_adjoint([ur, ui, ux], lam, h0, h,
+                                    None if gh is None else _strided_like(gh, h),
+                                    gh_last=None if gh_last is None else gh_last.contiguous(),
+                                    power=ctx.power, resets=resets)
+        return (*out["du"], out["dlam"], None if h0 is None else out["dh0"], None, None)
+
+
+def gated_scan(u, lam, h0=None, *, power=8.0, resets=None):
+    """Differentiable gated linear recurrence (``pararnn.gated_scan``): u =
+    (u_r, u_i, u_x) [B][D][T], lam [D], h0 [B][D] or None.  Returns
+    (h [B][D][T], h_last [B][D])."""
+    ur, ui, ux = u
+    return _GatedScan.apply(ur, ui, ux, lam, h0, power, resets)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, gate, x, w_post, w_pre, scale, eps, z_dtype):
+        y, z, rstd = pr.block_norm(h, x, w_post, w_pre, gate=gate, scale=scale, eps=eps,
+                                   z_dtype=z_dtype)
+        ctx.save_for_backward(h, gate, x, w_post, w_pre, rstd)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return x.view_as(x) if h is None else y, z
+
+    @staticmethod
+    def backward(ctx, gy, gz):
+        h, gate, x, w_post, w_pre, rstd = ctx.saved_tensors
+        out = pr.block_norm_adjoint(h, x, w_post, w_pre, rstd,
+                                    None if gy is None else _strided_like(gy, x),
+                                    None if gz is None else gz.contiguous(), gate=gate,
+                                    scale=ctx.scale)
+        return (out["dh"], out["dgate"], out["dx"], out["dw_post"], out["dw_pre"], None, None,
+                None)
+
+
+def block_norm(h, x, w_post, w_pre, *, gate=None, scale=1.0, eps=1e-6, z_dtype=torch.bfloat16):
+    """Differentiable block boundary (``pararnn.block_norm``).  Returns (y, z)."""
+    return _BlockNorm.apply(h, gate, x, w_post, w_pre, scale, eps, z_dtype)
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top, scale):
+        out = pr.token_logprobs(logits, tokens, top=top, scale=scale)
+        ctx.save_for_backward(logits, tokens, out["lse"], out["entropy"])
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        tops = (out["top_index"], out["top_logprob"]) if top else ()
+        ctx.mark_non_differentiable(*tops)
+        return (out["logprob"], out["entropy"], out["lse"]) + tops
+
+    @staticmethod
+    def backward(ctx, g_logprob, g_entropy, g_lse, *_):
+        logits, tokens, lse, entropy = ctx.saved_tensors
+        g = [None if x is None else x.contiguous() for x in (g_logprob, g_entropy, g_lse)]
+        return (pr.token_logprobs_adjoint(logits, tokens, lse, entropy, g_logprob=g[0],
+                                          g_entropy=g[1], g_lse=g[2], scale=ctx.scale),
+                None, None, None)
+
+
+def token_logprobs(logits, tokens, *, top=0, scale=1.0):
+    """Differentiable token scores (``pararnn.token_logprobs``): gradients for
+    the logits from logprob, entropy and lse; the alternatives carry none."""
+    out = _TokenLogprobs.apply(logits, tokens, int(top), scale)
+    names = ("logprob", "entropy", "lse", "top_index", "top_logprob")
+    return dict(zip(names, out))

@@ -1,0 +1,226 @@
+// Gated linear recurrence: host side of pararnn_gated_scan,
+// pararnn_gated_scan_adjoint and pararnn_gated_step.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "gated.hpp"
+#include "host.hpp"
+
+using namespace pararnn;
+
+namespace {
+
+// How the time axis is cut: spans per channel and their length.
+struct GatedPlan {
+    int64_t channels = 0, seg_len = 0;
+    int32_t nseg = 1;
+    size_t agg = 0, part = 0, total = 0;  // workspace: span maps, dlam partial sums
+};
+
+pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &pl)
+{
+    const pararnn_status_t st = check_shape(sh);
+    if (st != PARARNN_OK) return st;
+    if (sh->B > 0 && sh->D > ((int64_t(1) << 31) - 1) / sh->B) return PARARNN_ERR_UNSUPPORTED;
+    pl.channels = sh->B * sh->D;
+    // Spans of at least 64 steps, as many as give the device 16 waves per CU.
+    const int64_t waves = (pl.channels + kWave - 1) / kWave;
+    int64_t nseg = waves > 0 ? 16 * kComputeUnits / waves : 1;
+    nseg = std::min(nseg, (sh->T + 63) / 64);
+    nseg = std::max<int64_t>(1, std::min<int64_t>(nseg, 4096));
+    pl.seg_len = std::max<int64_t>(1, (sh->T + nseg - 1) / nseg);
+    pl.nseg = (int32_t)std::max<int64_t>(1, (sh->T + pl.seg_len - 1) / pl.seg_len);
+    pl.agg = 0;
+    size_t off = pl.nseg > 1 ? align_up((size_t)pl.nseg * pl.channels * sizeof(float2)) : 0;
+    pl.part = off;
+    if (adjoint) off = align_up(off + (size_t)sh->B * pl.nseg * sh->D * sizeof(float));
+    pl.total = off;
+    return PARARNN_OK;
+}
+
+void gated_args(GatedArgs &A, const pararnn_shape_t *sh, const GatedPlan &pl, const void *const *u,
+                const float *lam, float power, const float *h0, const uint8_t *resets, void *ws)
+{
+    std::memset(&A, 0, sizeof(A));
+    for (int g = 0; g < 3 && u; ++g) A.u[g] = u[g];
+    A.lam = lam;
+    A.power = power;
+    A.h0 = h0;
+    A.resets = resets;
+    A.agg = reinterpret_cast<float2 *>(static_cast<char *>(ws) + pl.agg);
+    A.seg_len = pl.seg_len;
+    A.nseg = pl.nseg;
+    A.B = sh->B;
+    A.T = sh->T;
+    A.D = sh->D;
+    A.channels = pl.channels;
+    A.usb = sh->u_stride_b;
+    A.usd = sh->u_stride_d;
+    A.ust = sh->u_stride_t;
+    A.ssb = sh->s_stride_b;
+    A.ssd = sh->s_stride_d;
+    A.sst = sh->s_stride_t;
+}
+
+pararnn_status_t check_gated(const pararnn_shape_t *sh, const GatedPlan &pl, const void *const *u,
+                             pararnn_dtype_t dt, const float *lam, float power, const void *ws,
+                             size_t ws_bytes)
+{
+    if (dt != PARARNN_F32 && dt != PARARNN_BF16) return PARARNN_ERR_UNSUPPORTED;
+    if (!(power > 0.0f) || std::isinf(power)) return PARARNN_ERR_INVALID;
+    if (pl.channels > 0 && !lam) return PARARNN_ERR_INVALID;
+    if (pl.channels > 0 && sh->T > 0) {
+        if (!u) return PARARNN_ERR_INVALID;
+        for (int g = 0; g < 3; ++g)
+            if (!u[g]) return PARARNN_ERR_INVALID;
+    }
+    if (pl.total > 0 && pl.channels > 0 && (!ws || ws_bytes < pl.total || !aligned16(ws)))
+        return PARARNN_ERR_WORKSPACE;
+    return PARARNN_OK;
+}
+
+hipError_t run_forward(const GatedArgs &A, bool bf16, hipStream_t st)
+{
+    const dim3 grid((unsigned)((A.channels + kWave - 1) / kWave), (unsigned)A.nseg), block(kWave);
+    if (A.nseg > 1) {
+        if (bf16)
+            hipLaunchKernelGGL((gated_channel_kernel<true, true>), grid, block, 0, st, A);
+        else
+            hipLaunchKernelGGL((gated_channel_kernel<false, true>), grid, block, 0, st, A);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (bf16)
+        hipLaunchKernelGGL((gated_channel_kernel<true, false>), grid, block, 0, st, A);
+    else
+        hipLaunchKernelGGL((gated_channel_kernel<false, false>), grid, block, 0, st, A);
+    return hipGetLastError();
+}
+
+hipError_t run_adjoint(const GatedArgs &A, bool bf16, hipStream_t st)
+{
+    const dim3 grid((unsigned)((A.channels + kWave - 1) / kWave), (unsigned)A.nseg), block(kWave);
+    if (A.nseg > 1) {
+        if (bf16)
+            hipLaunchKernelGGL((gated_channel_adjoint_kernel<true, true>), grid, block, 0, st, A);
+        else
+            hipLaunchKernelGGL((gated_channel_adjoint_kernel<false, true>), grid, block, 0, st, A);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (bf16)
+        hipLaunchKernelGGL((gated_channel_adjoint_kernel<true, false>), grid, block, 0, st, A);
+    else
+        hipLaunchKernelGGL((gated_channel_adjoint_kernel<false, false>), grid, block, 0, st, A);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pararnn_gated_workspace_bytes(const pararnn_shape_t *shape, int adjoint)
+{
+    GatedPlan pl;
+    return gated_plan(shape, adjoint != 0, pl) == PARARNN_OK ? pl.total : 0;
+}
+
+pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *const u[3],
+                                    pararnn_dtype_t u_dtype, const float *lam, float power,
+                                    const float *h0, const uint8_t *resets, float *h,
+                                    float *h_last, void *ws, size_t ws_bytes, void *stream)
+{
+    GatedPlan pl;
+    pararnn_status_t st = gated_plan(shape, false, pl);
+    if (st != PARARNN_OK) return st;
+    st = check_gated(shape, pl, u, u_dtype, lam, power, ws, ws_bytes);
+    if (st != PARARNN_OK) return st;
+    if (pl.channels == 0 || (shape->T == 0 && !h_last)) return PARARNN_OK;
+    if (shape->T > 0 && !h) return PARARNN_ERR_INVALID;
+    GatedArgs A;
+    gated_args(A, shape, pl, u, lam, power, h0, resets, ws);
+    A.h = h;
+    A.h_last = h_last;
+    const hipError_t e =
+        run_forward(A, u_dtype == PARARNN_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
+}
+
+pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const void *const u[3],
+                                            pararnn_dtype_t u_dtype, const float *lam, float power,
+                                            const float *h0, const uint8_t *resets,
+                                            const float *h, const float *gh, const float *gh_last,
+                                            void *const du[3], float *dlam, float *dh0, void *ws,
+                                            size_t ws_bytes, void *stream)
+{
+    GatedPlan pl;
+    pararnn_status_t st = gated_plan(shape, true, pl);
+    if (st != PARARNN_OK) return st;
+    st = check_gated(shape, pl, u, u_dtype, lam, power, ws, ws_bytes);
+    if (st != PARARNN_OK) return st;
+    if (shape->D == 0) return PARARNN_OK;
+    if (!dlam || !lam) return PARARNN_ERR_INVALID;
+    if (pl.channels > 0 && shape->T > 0) {
+        if (!h || !du) return PARARNN_ERR_INVALID;
+        for (int g = 0; g < 3; ++g)
+            if (!du[g]) return PARARNN_ERR_INVALID;
+    }
+    hipStream_t strm = static_cast<hipStream_t>(stream);
+    GatedArgs A;
+    gated_args(A, shape, pl, u, lam, power, h0, resets, ws);
+    A.hs = h;
+    A.gh = gh;
+    A.gh_last = gh_last;
+    for (int g = 0; g < 3 && du; ++g) A.du[g] = du[g];
+    A.dlam = dlam;
+    A.dh0 = dh0;
+    A.dlam_part = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part);
+    if (pl.channels > 0 && run_adjoint(A, u_dtype == PARARNN_BF16, strm) != hipSuccess)
+        return PARARNN_ERR_HIP;
+    const int tpb = 256;  // no batch rows: a sum of no terms
+    hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + tpb - 1) / tpb)), dim3(tpb),
+                       0, strm, A);
+    return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
+}
+
+pararnn_status_t pararnn_gated_step(int64_t B, int64_t D, const void *const u[3],
+                                    pararnn_dtype_t u_dtype, int64_t u_stride_b, const float *lam,
+                                    float power, const int32_t *slots, float *states, int64_t pool,
+                                    float *out, void *stream)
+{
+    if (B < 0 || D < 0 || pool < 0) return PARARNN_ERR_INVALID;
+    if (B >= (int64_t(1) << 31) || D >= (int64_t(1) << 31) || pool >= (int64_t(1) << 31))
+        return PARARNN_ERR_UNSUPPORTED;
+    if (u_dtype != PARARNN_F32 && u_dtype != PARARNN_BF16) return PARARNN_ERR_UNSUPPORTED;
+    if (!(power > 0.0f) || std::isinf(power)) return PARARNN_ERR_INVALID;
+    if (B > 1 && u_stride_b < D) return PARARNN_ERR_INVALID;
+    if (B == 0 || D == 0) return PARARNN_OK;
+    if (!u || !lam || !out || (pool > 0 && !states)) return PARARNN_ERR_INVALID;
+    for (int g = 0; g < 3; ++g)
+        if (!u[g]) return PARARNN_ERR_INVALID;
+    GatedStepArgs A;
+    for (int g = 0; g < 3; ++g) A.u[g] = u[g];
+    A.lam = lam;
+    A.slots = slots;
+    A.states = states;
+    A.out = out;
+    A.B = B;
+    A.D = D;
+    A.usb = u_stride_b;
+    A.pool = pool;
+    A.power = power;
+    const dim3 grid((unsigned)((D + kGatedStepThreads - 1) / kGatedStepThreads),
+                    (unsigned)std::min<int64_t>(B, 65535)),
+        block(kGatedStepThreads);
+    hipStream_t strm = static_cast<hipStream_t>(stream);
+    if (u_dtype == PARARNN_BF16)
+        hipLaunchKernelGGL((gated_step_kernel<true>), grid, block, 0, strm, A);
+    else
+        hipLaunchKernelGGL((gated_step_kernel<false>), grid, block, 0, strm, A);
+    return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
+}
+
+}  // extern "C"

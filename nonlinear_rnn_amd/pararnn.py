@@ -8,7 +8,9 @@ is missing, the calls raise.
 
 Names follow the ABI: ``solve_gru``, ``solve_gru_noalloc``, ``solve_lstm``,
 ``adjoint``, ``scan``, ``sequential``, ``project``, ``workspace_bytes``,
-``plan``.
+``plan``; for language models ``gated_scan``, ``gated_scan_adjoint``,
+``gated_step``, ``block_norm``, ``block_norm_adjoint``, ``token_logprobs``,
+``token_logprobs_adjoint``.
 """
 import ctypes
 import os
@@ -44,6 +46,13 @@ class ProjShape(ctypes.Structure):
                 ("M", ctypes.c_int64), ("x_stride_b", ctypes.c_int64),
                 ("x_stride_t", ctypes.c_int64), ("w_stride_m", ctypes.c_int64),
                 ("u_stride_b", ctypes.c_int64), ("u_stride_m", ctypes.c_int64)]
+
+
+class BlockShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("B", "T", "D", "h_stride_b", "h_stride_d", "h_stride_t", "g_stride_b",
+                 "g_stride_d", "g_stride_t", "x_stride_b", "x_stride_t", "z_stride_b",
+                 "z_stride_t")]
 
 
 class Newton(ctypes.Structure):
@@ -94,6 +103,32 @@ def load():
     lib.pararnn_adjoint.restype = i32
     lib.pararnn_adjoint.argtypes = [i32, P(Shape), vp, i32, vp, vp, vp, vp, vp, vp, vp, i32,
                                     vp, vp, P(Newton), vp, sz, vp]
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    lib.pararnn_gated_workspace_bytes.restype = sz
+    lib.pararnn_gated_workspace_bytes.argtypes = [P(Shape), i32]
+    lib.pararnn_gated_scan.restype = i32
+    lib.pararnn_gated_scan.argtypes = [P(Shape), vp, i32, vp, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.pararnn_gated_scan_adjoint.restype = i32
+    lib.pararnn_gated_scan_adjoint.argtypes = [P(Shape), vp, i32, vp, f32, vp, vp, vp, vp, vp, vp,
+                                               vp, vp, vp, sz, vp]
+    lib.pararnn_gated_step.restype = i32
+    lib.pararnn_gated_step.argtypes = [i64, i64, vp, i32, i64, vp, f32, vp, vp, i64, vp, vp]
+    lib.pararnn_block_norm.restype = i32
+    lib.pararnn_block_norm.argtypes = [P(BlockShape), vp, vp, i32, vp, i32, vp, vp, f32, f32, vp,
+                                       vp, i32, vp, vp]
+    lib.pararnn_block_workspace_bytes.restype = sz
+    lib.pararnn_block_workspace_bytes.argtypes = [P(BlockShape)]
+    lib.pararnn_block_norm_adjoint.restype = i32
+    lib.pararnn_block_norm_adjoint.argtypes = [P(BlockShape), vp, vp, i32, vp, i32, vp, vp, f32,
+                                               vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.pararnn_logprobs_workspace_bytes.restype = sz
+    lib.pararnn_logprobs_workspace_bytes.argtypes = [i64, i64, ctypes.c_int32]
+    lib.pararnn_token_logprobs.restype = i32
+    lib.pararnn_token_logprobs.argtypes = [i64, i64, vp, i32, i64, vp, ctypes.c_int32, f32, vp, vp,
+                                           vp, vp, vp, vp, sz, vp]
+    lib.pararnn_token_logprobs_adjoint.restype = i32
+    lib.pararnn_token_logprobs_adjoint.argtypes = [i64, i64, vp, i32, i64, vp, f32, vp, vp, vp, vp,
+                                                   vp, vp, i64, vp]
     _lib = lib
     return lib
 
@@ -644,4 +679,332 @@ def scan(A, b, x0=None, *, reverse=False, out=None, steps_per_lane=0, waves_per_
                             _ptr_array(x0) if x0 is not None else None, _ptr_array(out),
                             1 if reverse else 0, ctypes.byref(newton), _ptr(ws),
                             0 if ws is None else ws.numel(), _stream_handle(stream)))
+    return out
+
+
+# ------------------------------------------- operators of language models ---
+
+TOP_MAX = 64  # PARARNN_TOP_MAX
+
+
+def _code(t, name):
+    """ABI dtype code of a float32 or bfloat16 tensor."""
+    if not _is_tensor(t) or t.dtype not in _U_DTYPES:
+        raise ValueError(f"{name}: must be a float32 or bfloat16 tensor")
+    return BF16 if t.dtype is torch.bfloat16 else F32
+
+
+def _check_resets(resets, B, T):
+    if resets is None:
+        return
+    if not _is_tensor(resets) or tuple(resets.shape) != (B, T):
+        raise ValueError(f"resets: expected a tensor of shape {[B, T]}")
+    if resets.dtype not in (torch.bool, torch.uint8) or not resets.is_contiguous():
+        raise ValueError("resets: must be contiguous bool or uint8")
+
+
+def gated_scan(u, lam, h0=None, *, power=8.0, resets=None, out=None, workspace=None, stream=None):
+    """Gated linear recurrence h_t = k_t a_t h_{t-1} + sqrt(1 - a_t^2) sig(u_i) u_x
+    with a_t = exp(-power softplus(lam) sig(u_r)).  u = [u_r, u_i, u_x] device
+    tensors indexed [B][D][T] (float32 or bfloat16; channel-major is the fast
+    layout), lam [D] float32, h0 [B][D] float32 or None (zero), resets [B][T]
+    bool or None: True (k_t = 0) where a new document starts.  Returns
+    (h [B][D][T], h_last [B][D]), float32."""
+    lib = load()
+    u = list(u)
+    (B, D, T), udt = _gate_planes(u, 3)
+    _check_dense(lam, "lam", (D,))
+    if h0 is not None:
+        _check_dense(h0, "h0", (B, D))
+    _check_resets(resets, B, T)
+    dev = u[0].device
+    us = _strides(u, "u") or (D * T, T, 1)
+    allocated = []
+    if out is None:
+        out = _new_planes(1, B, T, D, us, dev)[0]
+        allocated = [out]
+    _check_planes([out], "out", (B, D, T))
+    ss = _strides([out], "out") or (D * T, T, 1)
+    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
+                                                 ("out", out), ("workspace", workspace)])
+    h_last = torch.empty((B, D), dtype=torch.float32, device=dev)
+    _record_on(stream, allocated + [h_last])
+    shape = make_shape(B, T, D, us, ss)
+    ws = workspace
+    if ws is None:
+        ws = _ws.get(int(lib.pararnn_gated_workspace_bytes(ctypes.byref(shape), 0)), dev, stream)
+    _check(lib.pararnn_gated_scan(ctypes.byref(shape), _ptr_array(u), udt, _ptr(lam), power,
+                                  _ptr(h0), _ptr(resets), _ptr(out), _ptr(h_last), _ptr(ws),
+                                  0 if ws is None else ws.numel(), _stream_handle(stream)))
+    return out, h_last
+
+
+def gated_scan_adjoint(u, lam, h0, h, gh, *, gh_last=None, power=8.0, resets=None, workspace=None,
+                       stream=None):
+    """Backward pass of ``gated_scan`` for L = sum_t <gh_t, h_t> + <gh_last, h_T>.
+    h: the forward's states; gh: their gradient (same strides) or None (zero);
+    gh_last [B][D] or None.  Returns dict(du=[3 planes, u's dtype and strides],
+    dlam [D], dh0 [B][D])."""
+    lib = load()
+    u = list(u)
+    (B, D, T), udt = _gate_planes(u, 3)
+    _check_dense(lam, "lam", (D,))
+    for name, x in (("h0", h0), ("gh_last", gh_last)):
+        if x is not None:
+            _check_dense(x, name, (B, D))
+    _check_resets(resets, B, T)
+    _check_planes([h], "h", (B, D, T))
+    _check_planes([gh], "gh", (B, D, T), allow_none=True)
+    dev = u[0].device
+    us = _strides(u, "u") or (D * T, T, 1)
+    ss = _strides([h, gh], "h and gh") or (D * T, T, 1)
+    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
+                                                 ("h", h), ("gh", gh), ("gh_last", gh_last),
+                                                 ("workspace", workspace)])
+    du = [torch.empty_strided((B, D, T), us, dtype=u[0].dtype, device=dev) for _ in range(3)]
+    dlam = torch.empty((D,), dtype=torch.float32, device=dev)
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
+    _record_on(stream, du + [dlam, dh0])
+    shape = make_shape(B, T, D, us, ss)
+    ws = workspace
+    if ws is None:
+        ws = _ws.get(int(lib.pararnn_gated_workspace_bytes(ctypes.byref(shape), 1)), dev, stream)
+    _check(lib.pararnn_gated_scan_adjoint(ctypes.byref(shape), _ptr_array(u), udt, _ptr(lam), power,
+                                          _ptr(h0), _ptr(resets), _ptr(h), _ptr(gh),
+                                          _ptr(gh_last), _ptr_array(du), _ptr(dlam), _ptr(dh0),
+                                          _ptr(ws), 0 if ws is None else ws.numel(),
+                                          _stream_handle(stream)))
+    return dict(du=du, dlam=dlam, dh0=dh0)
+
+
+def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
+    """One step of the gated linear recurrence for B requests.  u = [u_r, u_i,
+    u_x] tensors [B][D] (rows may be strided), lam [D], states [pool][D]
+    float32, updated in place, slots [B] int32 or None (row b has slot b).  A
+    row whose slot is outside the pool (-1) is idle: it gives zeros and
+    changes no state; live rows need distinct slots.  Returns the new states
+    of the rows, [B][D] float32."""
+    lib = load()
+    u = list(u)
+    _require(len(u) == 3, "expected 3 gate row blocks")
+    udt = _code(u[0], "u")
+    _require(u[0].dim() == 2, "u: row blocks must be [B][D]")
+    B, D = u[0].shape
+    for p in u:
+        if not _is_tensor(p) or tuple(p.shape) != (B, D) or p.dtype is not u[0].dtype:
+            raise ValueError("u: every row block must have the same shape [B][D] and dtype")
+        if p.numel() and D > 1 and p.stride(1) != 1 or B > 1 and p.stride(0) != u[0].stride(0):
+            raise ValueError("u: rows must be contiguous and share their stride")
+    _check_dense(lam, "lam", (D,))
+    if not _is_tensor(states) or states.dim() != 2:
+        raise ValueError("states: expected a tensor [pool][D]")
+    pool = states.shape[0]
+    _check_dense(states, "states", (pool, D))
+    if slots is None:
+        _require(pool >= B, "states: a row for each request, or slots")
+    elif not _is_tensor(slots) or tuple(slots.shape) != (B,) or slots.dtype != torch.int32 or (
+            not slots.is_contiguous()):
+        raise ValueError(f"slots: must be contiguous int32 [{B}]")
+    allocated = []
+    if out is None:
+        out = torch.empty((B, D), dtype=torch.float32, device=u[0].device)
+        allocated = [out]
+    _check_dense(out, "out", (B, D))
+    _check_devices(u[0].device, [("u", p) for p in u] + [("lam", lam), ("states", states),
+                                                         ("slots", slots), ("out", out)])
+    _record_on(stream, allocated)
+    _check(lib.pararnn_gated_step(B, D, _ptr_array(u), udt, u[0].stride(0) if B > 1 else D,
+                                  _ptr(lam), power, _ptr(slots), _ptr(states), pool, _ptr(out),
+                                  _stream_handle(stream)))
+    return out
+
+
+def _row_strides(t, name):
+    """(stride_b, stride_t) of a time-major tensor [B][T][D], channels
+    contiguous; dense ones for dimensions of size one."""
+    B, T, D = t.shape
+    if t.numel() and D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    st = t.stride(1) if T > 1 else D
+    return (t.stride(0) if B > 1 else st * T, st)
+
+
+def _block_shape(h, gate, x, z_strides):
+    """Checks what the block boundary reads; returns its shape record."""
+    if not _is_tensor(x) or x.dim() != 3:
+        raise ValueError("x: expected a tensor [B][T][D]")
+    B, T, D = x.shape
+    dense = (D * T, T, 1)
+    if h is not None:
+        _check_planes([h], "h", (B, D, T))
+    if gate is not None:
+        _require(h is not None, "gate: needs h")
+        _check_planes([gate], "gate", (B, D, T), _U_DTYPES)
+    hs = (_strides([h], "h") if h is not None else None) or dense
+    gs = (_strides([gate], "gate") if gate is not None else None) or dense
+    return BlockShape(B, T, D, *hs, *gs, *_row_strides(x, "x"), *z_strides)
+
+
+def block_norm(h, x, w_post, w_pre, *, gate=None, scale=1.0, eps=1e-6, z_dtype=torch.bfloat16,
+               stream=None):
+    """Block boundary: v = h silu(gate); y = x + scale rmsnorm(v) w_post;
+    z = rmsnorm(y) w_pre.  h [B][D][T] float32 (the states of a solve or scan)
+    or None (y = x: the norm in front of the first block), gate [B][D][T]
+    float32 / bfloat16 or None, x [B][T][D] float32 / bfloat16 (channels
+    contiguous), w_post and w_pre [D] float32 (w_post may be None without h).
+    Returns (y [B][T][D] in x's dtype and strides, z [B][T][D] in z_dtype,
+    rstd [2][B][T] float32); without h, y is x itself."""
+    lib = load()
+    xdt = _code(x, "x")
+    gdt = F32 if gate is None else _code(gate, "gate")
+    _require(z_dtype in _U_DTYPES, "z_dtype must be float32 or bfloat16")
+    _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
+    B, T, D = x.shape
+    shape = _block_shape(h, gate, x, (T * D, D))
+    if h is not None:
+        _check_dense(w_post, "w_post", (D,))
+    _check_dense(w_pre, "w_pre", (D,))
+    dev = x.device
+    _check_devices(dev, [("x", x), ("h", h), ("gate", gate), ("w_post", w_post if h is not None else None),
+                         ("w_pre", w_pre)])
+    y = x if h is None else torch.empty_strided((B, T, D), (shape.x_stride_b, shape.x_stride_t, 1),
+                                                dtype=x.dtype, device=dev)
+    z = torch.empty((B, T, D), dtype=z_dtype, device=dev)
+    rstd = torch.empty((2, B, T), dtype=torch.float32, device=dev)
+    _record_on(stream, [None if h is None else y, z, rstd])
+    _check(lib.pararnn_block_norm(ctypes.byref(shape), _ptr(h), _ptr(gate), gdt, _ptr(x), xdt,
+                                  _ptr(w_post) if h is not None else None, _ptr(w_pre), scale, eps,
+                                  None if h is None else _ptr(y), _ptr(z), _code(z, "z"),
+                                  _ptr(rstd), _stream_handle(stream)))
+    return y, z, rstd
+
+
+def block_norm_adjoint(h, x, w_post, w_pre, rstd, gy, gz, *, gate=None, scale=1.0, workspace=None,
+                       stream=None):
+    """Backward pass of ``block_norm`` from the gradients gy of y (x's dtype and
+    strides) and gz of z (either may be None: zero) and the forward's rstd.
+    Returns dict(dh, dgate, dx, dw_post, dw_pre); dh, dgate and dw_post are
+    None where their input is."""
+    lib = load()
+    xdt = _code(x, "x")
+    gdt = F32 if gate is None else _code(gate, "gate")
+    _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
+    B, T, D = x.shape
+    if gz is not None:
+        _require(_is_tensor(gz) and tuple(gz.shape) == (B, T, D), f"gz: expected {[B, T, D]}")
+    zs = (T * D, D) if gz is None else _row_strides(gz, "gz")
+    zdt = F32 if gz is None else _code(gz, "gz")
+    shape = _block_shape(h, gate, x, zs)
+    if gy is not None:
+        _require(_is_tensor(gy) and tuple(gy.shape) == (B, T, D), f"gy: expected {[B, T, D]}")
+        _require(gy.dtype is x.dtype and _row_strides(gy, "gy") == _row_strides(x, "x"),
+                 "gy: must have x's dtype and strides")
+    if h is not None:
+        _check_dense(w_post, "w_post", (D,))
+    _check_dense(w_pre, "w_pre", (D,))
+    _check_dense(rstd, "rstd", (2, B, T))
+    dev = x.device
+    _check_devices(dev, [("x", x), ("h", h), ("gate", gate), ("w_post", w_post if h is not None else None),
+                         ("w_pre", w_pre), ("rstd", rstd), ("gy", gy), ("gz", gz),
+                         ("workspace", workspace)])
+    xs = (shape.x_stride_b, shape.x_stride_t, 1)
+    dx = torch.empty_strided((B, T, D), xs, dtype=x.dtype, device=dev)
+    dh = dgate = dw_post = None
+    if h is not None:
+        dh = torch.empty_strided((B, D, T), (shape.h_stride_b, shape.h_stride_d, shape.h_stride_t),
+                                 dtype=torch.float32, device=dev)
+        dw_post = torch.empty((D,), dtype=torch.float32, device=dev)
+    if gate is not None:
+        dgate = torch.empty_strided((B, D, T),
+                                    (shape.g_stride_b, shape.g_stride_d, shape.g_stride_t),
+                                    dtype=gate.dtype, device=dev)
+    dw_pre = torch.empty((D,), dtype=torch.float32, device=dev)
+    _record_on(stream, [dx, dh, dgate, dw_post, dw_pre])
+    ws = workspace
+    if ws is None:
+        ws = _ws.get(int(lib.pararnn_block_workspace_bytes(ctypes.byref(shape))), dev, stream)
+    _check(lib.pararnn_block_norm_adjoint(
+        ctypes.byref(shape), _ptr(h), _ptr(gate), gdt, _ptr(x), xdt,
+        _ptr(w_post) if h is not None else None, _ptr(w_pre), scale, _ptr(rstd), _ptr(gy),
+        _ptr(gz), zdt, _ptr(dh), _ptr(dgate), _ptr(dx), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
+        0 if ws is None else ws.numel(), _stream_handle(stream)))
+    return dict(dh=dh, dgate=dgate, dx=dx, dw_post=dw_post, dw_pre=dw_pre)
+
+
+def _logits(logits, tokens):
+    """Checks logits [N][V] and tokens [N]; returns (N, V, row stride, dtype code)."""
+    dt = _code(logits, "logits")
+    _require(logits.dim() == 2, "logits: expected a tensor [N][V]")
+    N, V = logits.shape
+    if logits.numel() and V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: the vocabulary must be contiguous")
+    if not _is_tensor(tokens) or tuple(tokens.shape) != (N,) or tokens.dtype != torch.int64 or (
+            not tokens.is_contiguous()):
+        raise ValueError(f"tokens: must be contiguous int64 [{N}]")
+    return N, V, logits.stride(0) if N > 1 else V, dt
+
+
+def token_logprobs(logits, tokens, *, top=0, scale=1.0, workspace=None, stream=None):
+    """Scores of given tokens under p = softmax(scale logits): logits [N][V]
+    (float32 or bfloat16, the vocabulary contiguous, rows may be strided),
+    tokens [N] int64 (negative: not scored, logprob 0; past the vocabulary:
+    NaN).  Returns dict(logprob, entropy, lse [N] float32) and, for top > 0
+    (at most TOP_MAX), top_index [N][top] int64 and top_logprob [N][top]
+    float32: the most likely tokens, the lower index first among equals; a
+    masked token (-inf) is never one of them, and index -1 with log
+    probability -inf stands where a row has no more."""
+    lib = load()
+    N, V, stride, dt = _logits(logits, tokens)
+    top = int(top)
+    _require(0 <= top <= TOP_MAX, f"top: 0 to {TOP_MAX}")
+    dev = logits.device
+    _check_devices(dev, [("logits", logits), ("tokens", tokens), ("workspace", workspace)])
+    stats = torch.empty((3, N), dtype=torch.float32, device=dev)
+    out = dict(logprob=stats[0], entropy=stats[1], lse=stats[2])
+    allocated = [stats]
+    if top:
+        out["top_index"] = torch.empty((N, top), dtype=torch.int64, device=dev)
+        out["top_logprob"] = torch.empty((N, top), dtype=torch.float32, device=dev)
+        allocated += [out["top_index"], out["top_logprob"]]
+    _record_on(stream, allocated)
+    ws = workspace
+    if ws is None:
+        ws = _ws.get(int(lib.pararnn_logprobs_workspace_bytes(N, V, top)), dev, stream)
+    _check(lib.pararnn_token_logprobs(N, V, _ptr(logits), dt, stride, _ptr(tokens), top, scale,
+                                      _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out["lse"]),
+                                      _ptr(out.get("top_index")), _ptr(out.get("top_logprob")),
+                                      _ptr(ws), 0 if ws is None else ws.numel(),
+                                      _stream_handle(stream)))
+    return out
+
+
+def token_logprobs_adjoint(logits, tokens, lse, entropy=None, *, g_logprob=None, g_entropy=None,
+                           g_lse=None, scale=1.0, out=None, stream=None):
+    """Gradient of ``token_logprobs`` for the logits, from its lse and entropy
+    and the gradients of its outputs ([N] float32 or None: zero; entropy is
+    needed with g_entropy).  ``out`` may be the logits themselves.  Returns
+    dL/dlogits in the logits' dtype."""
+    lib = load()
+    N, V, stride, dt = _logits(logits, tokens)
+    for name, t in (("lse", lse), ("entropy", entropy), ("g_logprob", g_logprob),
+                    ("g_entropy", g_entropy), ("g_lse", g_lse)):
+        if t is not None or name == "lse":
+            _check_dense(t, name, (N,))
+    _require(g_entropy is None or entropy is not None, "g_entropy: needs entropy")
+    allocated = []
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
+        allocated = [out]
+    if not _is_tensor(out) or tuple(out.shape) != (N, V) or out.dtype is not logits.dtype or (
+            out.numel() and V > 1 and out.stride(1) != 1):
+        raise ValueError("out: must be [N][V] in the logits' dtype, the vocabulary contiguous")
+    _check_devices(logits.device, [("logits", logits), ("tokens", tokens), ("lse", lse),
+                                   ("entropy", entropy), ("g_logprob", g_logprob),
+                                   ("g_entropy", g_entropy), ("g_lse", g_lse), ("out", out)])
+    _record_on(stream, allocated)
+    _check(lib.pararnn_token_logprobs_adjoint(N, V, _ptr(logits), dt, stride, _ptr(tokens), scale,
+                                              _ptr(lse), _ptr(entropy), _ptr(g_logprob),
+                                              _ptr(g_entropy), _ptr(g_lse), _ptr(out),
+                                              out.stride(0) if N > 1 else V,
+                                              _stream_handle(stream)))
     return out

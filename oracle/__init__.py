@@ -14,9 +14,12 @@ and this package imports nothing from it.
   per-iteration checks.
 * ``oracle.projection`` — the input projection u = W x + b per batch row in
   float64.
+* ``oracle.language`` — the gated linear recurrence, the block boundary and
+  the token scores, forward and backward, in numpy float64.
 
 Parity status: every function here is pinned by tests in
 ``tests/test_oracle_pins.py`` against library routines (torch.nn.GRUCell /
 LSTMCell with diagonal recurrent weights, scipy.signal.lfilter), closed
-forms, finite differences and brute force; none is "parity unpinned".
+forms, finite differences and brute force (``oracle.language`` in
+``tests/test_language_oracle.py``); none is "parity unpinned".
 """

@@ -13,28 +13,50 @@ using namespace pararnn;
 
 namespace {
 
-// How the time axis is cut: spans per channel and their length.
+// Steps a lane holds in the kernels with lanes in time: one 16-byte load a
+// plane.
+constexpr int kStepsBf16 = 8, kStepsF32 = 4;
+
+// Which kernel, and how the time axis is cut: spans per channel and their
+// length.
 struct GatedPlan {
     int64_t channels = 0, seg_len = 0;
     int32_t nseg = 1;
+    int waves = 0;  // per channel, lanes in time; 0: a lane per channel
     size_t agg = 0, part = 0, total = 0;  // workspace: span maps, dlam partial sums
 };
 
+// The plan goes by the shape alone (not by the dtype), so that a workspace
+// serves either.
 pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &pl)
 {
     const pararnn_status_t st = check_shape(sh);
     if (st != PARARNN_OK) return st;
     if (sh->B > 0 && sh->D > ((int64_t(1) << 31) - 1) / sh->B) return PARARNN_ERR_UNSUPPORTED;
     pl.channels = sh->B * sh->D;
-    // Spans of at least 64 steps, as many as give the device 16 waves per CU.
-    const int64_t waves = (pl.channels + kWave - 1) / kWave;
-    int64_t nseg = waves > 0 ? 16 * kComputeUnits / waves : 1;
-    nseg = std::min(nseg, (sh->T + 63) / 64);
+    const int64_t C = pl.channels, T = sh->T;
+    constexpr int64_t kFull = 8 * kComputeUnits;  // waves that fill the device
+    int64_t nseg = 1, unit = 1;
+    // (a dispatch counts its work-items in 32 bits: 64 a channel)
+    if (T > 16 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
+        // one wave per channel where the channels fill the device, else the
+        // channel's steps over more waves, and over several workgroups where
+        // that is not enough
+        pl.waves = C >= kFull || T <= 64 * kStepsBf16 ? 1 : C >= kFull / 4 || T <= 256 * kStepsBf16 ? 4 : 16;
+        unit = (int64_t)pl.waves * kWave * kStepsBf16;
+        nseg = C > 0 ? (kFull + C * pl.waves - 1) / (C * pl.waves) : 1;
+        nseg = std::min(nseg, (T + 2 * unit - 1) / (2 * unit));
+    } else {
+        // a lane per channel: spans of at least 64 steps
+        const int64_t waves = (C + kWave - 1) / kWave;
+        nseg = waves > 0 ? 2 * kFull / waves : 1;
+        nseg = std::min(nseg, (T + 63) / 64);
+    }
     nseg = std::max<int64_t>(1, std::min<int64_t>(nseg, 4096));
-    pl.seg_len = std::max<int64_t>(1, (sh->T + nseg - 1) / nseg);
-    pl.nseg = (int32_t)std::max<int64_t>(1, (sh->T + pl.seg_len - 1) / pl.seg_len);
+    pl.seg_len = std::max<int64_t>(unit, ((T + nseg - 1) / nseg + unit - 1) / unit * unit);
+    pl.nseg = (int32_t)std::max<int64_t>(1, (T + pl.seg_len - 1) / pl.seg_len);
     pl.agg = 0;
-    size_t off = pl.nseg > 1 ? align_up((size_t)pl.nseg * pl.channels * sizeof(float2)) : 0;
+    size_t off = pl.nseg > 1 ? align_up((size_t)pl.nseg * C * sizeof(float2)) : 0;
     pl.part = off;
     if (adjoint) off = align_up(off + (size_t)sh->B * pl.nseg * sh->D * sizeof(float));
     pl.total = off;
@@ -82,40 +104,39 @@ pararnn_status_t check_gated(const pararnn_shape_t *sh, const GatedPlan &pl, con
     return PARARNN_OK;
 }
 
-hipError_t run_forward(const GatedArgs &A, bool bf16, hipStream_t st)
+// One launch over (channels or groups of 64 of them) x spans.
+template <bool ADJ, bool BF16, bool AGG>
+hipError_t launch_gated(const GatedArgs &A, int waves, hipStream_t st)
 {
-    const dim3 grid((unsigned)((A.channels + kWave - 1) / kWave), (unsigned)A.nseg), block(kWave);
-    if (A.nseg > 1) {
-        if (bf16)
-            hipLaunchKernelGGL((gated_channel_kernel<true, true>), grid, block, 0, st, A);
-        else
-            hipLaunchKernelGGL((gated_channel_kernel<false, true>), grid, block, 0, st, A);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    constexpr int K = BF16 ? kStepsBf16 : kStepsF32;
+    const int64_t groups = waves ? A.channels : (A.channels + kWave - 1) / kWave;
+    const dim3 grid((unsigned)groups, (unsigned)A.nseg),
+        block((unsigned)(kWave * (waves ? waves : 1)));
+#define PARARNN_GATED(NAME, ...)                                                                 \
+    if constexpr (ADJ)                                                                           \
+        hipLaunchKernelGGL((gated_##NAME##_adjoint_kernel<__VA_ARGS__>), grid, block, 0, st, A); \
+    else                                                                                         \
+        hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), grid, block, 0, st, A)
+    switch (waves) {
+    case 16: PARARNN_GATED(time, BF16, K, 16, AGG); break;
+    case 4: PARARNN_GATED(time, BF16, K, 4, AGG); break;
+    case 1: PARARNN_GATED(time, BF16, K, 1, AGG); break;
+    default: PARARNN_GATED(channel, BF16, AGG); break;
     }
-    if (bf16)
-        hipLaunchKernelGGL((gated_channel_kernel<true, false>), grid, block, 0, st, A);
-    else
-        hipLaunchKernelGGL((gated_channel_kernel<false, false>), grid, block, 0, st, A);
+#undef PARARNN_GATED
     return hipGetLastError();
 }
 
-hipError_t run_adjoint(const GatedArgs &A, bool bf16, hipStream_t st)
+template <bool ADJ>
+hipError_t run_gated(const GatedArgs &A, int waves, bool bf16, hipStream_t st)
 {
-    const dim3 grid((unsigned)((A.channels + kWave - 1) / kWave), (unsigned)A.nseg), block(kWave);
     if (A.nseg > 1) {
-        if (bf16)
-            hipLaunchKernelGGL((gated_channel_adjoint_kernel<true, true>), grid, block, 0, st, A);
-        else
-            hipLaunchKernelGGL((gated_channel_adjoint_kernel<false, true>), grid, block, 0, st, A);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = bf16 ? launch_gated<ADJ, true, true>(A, waves, st)
+                                  : launch_gated<ADJ, false, true>(A, waves, st);
         if (e != hipSuccess) return e;
     }
-    if (bf16)
-        hipLaunchKernelGGL((gated_channel_adjoint_kernel<true, false>), grid, block, 0, st, A);
-    else
-        hipLaunchKernelGGL((gated_channel_adjoint_kernel<false, false>), grid, block, 0, st, A);
-    return hipGetLastError();
+    return bf16 ? launch_gated<ADJ, true, false>(A, waves, st)
+                : launch_gated<ADJ, false, false>(A, waves, st);
 }
 
 }  // namespace
@@ -145,7 +166,7 @@ pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *co
     A.h = h;
     A.h_last = h_last;
     const hipError_t e =
-        run_forward(A, u_dtype == PARARNN_BF16, static_cast<hipStream_t>(stream));
+        run_gated<false>(A, pl.waves, u_dtype == PARARNN_BF16, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
@@ -178,7 +199,7 @@ pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const 
     A.dlam = dlam;
     A.dh0 = dh0;
     A.dlam_part = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part);
-    if (pl.channels > 0 && run_adjoint(A, u_dtype == PARARNN_BF16, strm) != hipSuccess)
+    if (pl.channels > 0 && run_gated<true>(A, pl.waves, u_dtype == PARARNN_BF16, strm) != hipSuccess)
         return PARARNN_ERR_HIP;
     const int tpb = 256;  // no batch rows: a sum of no terms
     hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + tpb - 1) / tpb)), dim3(tpb),

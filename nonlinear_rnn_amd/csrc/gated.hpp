@@ -227,6 +227,241 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
     }
 }
 
+// ---------------------------------------------------------- lanes in time ---
+// Time-contiguous planes: a channel's steps side by side in the lanes of W
+// waves, K steps a lane, so that every load and store of a wave is one
+// contiguous run.  Per chunk of 64 K W steps a lane composes its own steps,
+// the wave scans the lanes' maps (DPP), W > 1 waves exchange their totals
+// through LDS (one barrier a chunk, two buffers), and every lane runs its
+// steps again from the state in front of them.  The chunk's last state starts
+// the next one; the next chunk's loads are issued before this one's scan.
+template <int K, bool BF16>
+struct GatedChunk {
+    Raw<BF16, K> u[3];
+    uint32_t cut;
+};
+template <int K, bool BF16>
+__device__ __forceinline__ GatedChunk<K, BF16> load_chunk(const GatedArgs &A, int64_t uo,
+                                                          const uint8_t *rs, int64_t t, int64_t t1)
+{
+    GatedChunk<K, BF16> c;
+#pragma unroll
+    for (int g = 0; g < 3; ++g) c.u[g] = load_raw<BF16, K>(A.u[g], uo, t, t1);
+    c.cut = rs ? load_flags<K>(rs, t, t1) : 0u;
+    return c;
+}
+
+// The state before wave `wave`'s part of the chunk, from the one before the
+// chunk and the waves' maps in order; `carry` moves on to the next chunk.
+template <int W>
+__device__ __forceinline__ float through_waves(const Map1 *maps, int wave, float &carry)
+{
+    float mine = carry;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w == wave) mine = carry;
+        carry = fmaf_(maps[w].a, carry, maps[w].b);
+    }
+    return mine;
+}
+
+template <bool BF16, int K, int W, bool AGG>
+__global__ void __launch_bounds__(W * kWave) gated_time_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[2][W];
+    const int64_t ch = blockIdx.x;
+    const int64_t b = ch / A.D, d = ch - b * A.D;
+    const int32_t seg = blockIdx.y;
+    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
+    const int wave = threadIdx.x / kWave;
+    constexpr int P = K * W * kWave;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+
+    Map1 span = {1.0f, 0.0f};
+    float carry = A.h0 ? A.h0[ch] : 0.0f;
+    if constexpr (!AGG)
+        for (int32_t j = 0; j < seg; ++j) {
+            const float2 m = A.agg[(int64_t)j * A.channels + ch];
+            carry = fmaf_(m.x, carry, m.y);
+        }
+    int64_t t = t0 + (int64_t)threadIdx.x * K;
+    GatedChunk<K, BF16> now = load_chunk<K, BF16>(A, uo, rs, t, t1);
+    int parity = 0;
+    for (int64_t c = t0; c < t1; c += P, t += P, parity ^= 1) {
+        GatedChunk<K, BF16> next;
+        if (c + P < t1) next = load_chunk<K, BF16>(A, uo, rs, t + P, t1);
+        Map1 m[K], own = {1.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            m[k] = gated_map(rate, now.u[0].get(k), now.u[1].get(k), now.u[2].get(k),
+                             now.cut >> k & 1u);
+            m[k] = keep_or_identity(m[k], t + k < t1);
+            own = compose(m[k], own);
+        }
+        const Map1 upto = wave_scan_inclusive(own);
+        float before = carry;
+        if constexpr (W > 1) {
+            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
+            __syncthreads();
+            if constexpr (AGG) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) span = compose(maps[parity][w], span);
+            } else {
+                before = through_waves<W>(maps[parity], wave, carry);
+            }
+        } else if constexpr (AGG) {
+            span = compose(upto, span);  // in the last lane
+        }
+        if constexpr (!AGG) {
+            const Map1 prior = wave_shift_up(upto);
+            float h = fmaf_(prior.a, before, prior.b);
+            float out[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) out[k] = h = fmaf_(m[k].a, h, m[k].b);
+            store_raw<false, K>(A.h, so, t, t1, out);
+            if constexpr (W == 1) carry = __shfl(h, kWave - 1);
+            if (A.h_last && t < A.T && t + K >= A.T)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (t + k == A.T - 1) A.h_last[ch] = out[k];
+        }
+        now = next;
+    }
+    if constexpr (AGG)
+        if (threadIdx.x == W * kWave - 1)
+            A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
+}
+
+// Backward: lanes run backwards in time (lane 0 holds a chunk's last steps),
+// so that the same scan composes the maps of w from the end.
+template <int K, bool BF16>
+struct GatedBackChunk {
+    Raw<BF16, K> u[3];
+    Raw<false, K> h, gh;
+    float before;  // the state in front of the wave's steps
+    uint32_t cut;
+};
+template <int K, bool BF16, bool AGG>
+__device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A, int64_t uo,
+                                                             int64_t so, const uint8_t *rs,
+                                                             int64_t t, int64_t first, int64_t t1,
+                                                             float h0)
+{
+    GatedBackChunk<K, BF16> c;
+    c.u[0] = load_raw<BF16, K>(A.u[0], uo, t, t1);
+    if constexpr (!AGG) {
+        c.u[1] = load_raw<BF16, K>(A.u[1], uo, t, t1);
+        c.u[2] = load_raw<BF16, K>(A.u[2], uo, t, t1);
+        c.h = load_raw<false, K>(A.hs, so, t, t1);
+        c.before = first > 0 && first <= A.T ? A.hs[so + first - 1] : h0;
+    }
+    if (A.gh) {
+        c.gh = load_raw<false, K>(A.gh, so, t, t1);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) c.gh.w[k] = 0u;
+    }
+    c.cut = rs ? load_flags<K>(rs, t, t1) : 0u;
+    return c;
+}
+
+template <bool BF16, int K, int W, bool AGG>
+__global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[2][W];
+    __shared__ float sums[W];
+    const int64_t ch = blockIdx.x;
+    const int64_t b = ch / A.D, d = ch - b * A.D;
+    const int32_t seg = blockIdx.y;
+    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
+    const int wave = threadIdx.x / kWave;
+    constexpr int P = K * W * kWave;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+
+    Map1 span = {1.0f, 0.0f};
+    float carry = A.gh_last ? A.gh_last[ch] : 0.0f, dlam = 0.0f;
+    const float h0 = A.h0 ? A.h0[ch] : 0.0f;
+    if constexpr (!AGG)
+        for (int32_t j = A.nseg - 1; j > seg; --j) {
+            const float2 m = A.agg[(int64_t)j * A.channels + ch];
+            carry = fmaf_(m.x, carry, m.y);
+        }
+    int64_t c = t0 + (t1 - t0 - 1) / P * P;  // the last chunk of the span
+    const int at = W * kWave - 1 - (int)threadIdx.x, wave_at = (W - 1 - wave) * kWave;
+    GatedBackChunk<K, BF16> now =
+        load_back<K, BF16, AGG>(A, uo, so, rs, c + at * K, c + wave_at * K, t1, h0);
+    int parity = 0;
+    for (; c >= t0; c -= P, parity ^= 1) {
+        const int64_t t = c + at * K;
+        GatedBackChunk<K, BF16> next;
+        if (c > t0)
+            next = load_back<K, BF16, AGG>(A, uo, so, rs, t - P, c - P + wave_at * K, t1, h0);
+        Decay v[K];
+        Map1 own = {1.0f, 0.0f};
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            v[k] = decay(rate, now.u[0].get(k));
+            const float ka = now.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
+            own = compose(keep_or_identity(Map1{ka, ka * now.gh.get(k)}, t + k < t1), own);
+        }
+        const Map1 upto = wave_scan_inclusive(own);
+        float after = carry;
+        if constexpr (W > 1) {
+            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
+            __syncthreads();
+            if constexpr (AGG) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) span = compose(maps[parity][w], span);
+            } else {
+                after = through_waves<W>(maps[parity], wave, carry);
+            }
+        } else if constexpr (AGG) {
+            span = compose(upto, span);
+        }
+        if constexpr (!AGG) {
+            const Map1 prior = wave_shift_up(upto);
+            float w = fmaf_(prior.a, after, prior.b);
+            // the state before the lane's first step: the next lane's last one
+            float hp0 = __shfl_down(now.h.get(K - 1), 1);
+            if (threadIdx.x % kWave == kWave - 1) hp0 = now.before;
+            float gr[K], gi[K], gx[K];
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k) {
+                const bool cut = now.cut >> k & 1u, in = t + k < t1;
+                const float G = now.gh.get(k) + w;
+                const GatedGrad g = gated_grad(v[k], now.u[1].get(k), now.u[2].get(k), cut, G,
+                                               k ? now.h.get(k ? k - 1 : 0) : hp0);
+                gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
+                dlam += in ? g.lam : 0.0f;
+                w = in ? (cut ? 0.0f : (1.0f - v[k].m) * G) : w;
+            }
+            store_raw<BF16, K>(A.du[0], uo, t, t1, gr);
+            store_raw<BF16, K>(A.du[1], uo, t, t1, gi);
+            store_raw<BF16, K>(A.du[2], uo, t, t1, gx);
+            if constexpr (W == 1) carry = __shfl(w, kWave - 1);
+            if (A.dh0 && c == 0 && threadIdx.x == W * kWave - 1) A.dh0[ch] = w;
+        }
+        now = next;
+    }
+    if constexpr (AGG) {
+        if (threadIdx.x == W * kWave - 1)
+            A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
+    } else {
+        float s = wave_sum_to_last(dlam);
+        if constexpr (W > 1) {
+            if (threadIdx.x % kWave == kWave - 1) sums[wave] = s;
+            __syncthreads();
+            s = 0.0f;
+            for (int w = 0; w < W; ++w) s += sums[w];
+        }
+        if (threadIdx.x == W * kWave - 1) A.dlam_part[(b * A.nseg + seg) * A.D + d] = s;
+    }
+}
+
 // dL/dlam = -power sig(lam) sum (dL/dl sig(u_r)), the partial sums of the
 // batch rows and spans added in a fixed order.
 __global__ void gated_dlam_kernel(GatedArgs A)

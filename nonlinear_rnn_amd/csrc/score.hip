@@ -16,12 +16,45 @@ pararnn_status_t check_score(int64_t N, int64_t V, pararnn_dtype_t dtype, int64_
                              float scale)
 {
     if (N < 0 || V < 0) return PARARNN_ERR_INVALID;
-    if (N >= (int64_t(1) << 31) || V >= (int64_t(1) << 31)) return PARARNN_ERR_UNSUPPORTED;
+    // a dispatch counts its work-items in 32 bits: 256 a row
+    if (N >= (int64_t(1) << 24) || V >= (int64_t(1) << 31)) return PARARNN_ERR_UNSUPPORTED;
     if (dtype != PARARNN_F32 && dtype != PARARNN_BF16) return PARARNN_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || std::isinf(scale)) return PARARNN_ERR_INVALID;
     if (stride < 0 || (N > 1 && stride < V)) return PARARNN_ERR_INVALID;
     if (N > 0 && stride > INT64_MAX / N) return PARARNN_ERR_INVALID;
     return PARARNN_OK;
+}
+
+// Workgroups a row: one, unless there are too few rows to fill the device (4
+// workgroups a CU); then parts of at least 4096 logits.
+int64_t score_parts(int64_t N, int64_t V)
+{
+    if (N <= 0) return 1;
+    const int64_t want = std::min((4 * kComputeUnits + N - 1) / N, (V + 4095) / 4096);
+    return std::max<int64_t>(1, std::min<int64_t>(want, kScoreParts));
+}
+
+size_t score_stats_bytes(int64_t N, int64_t parts)
+{
+    return align_up((size_t)N * parts * sizeof(float4));
+}
+
+template <bool BF16>
+hipError_t run_score(const ScoreArgs &A, hipStream_t st)
+{
+    const dim3 grid((unsigned)(A.N * A.parts)), wide(kScoreThreads), one(kWave);
+    if (A.parts > 1) {
+        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, true>), grid, wide, 0, st, A);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((score_join_kernel<BF16>), dim3((unsigned)A.N), one, 0, st, A);
+    } else if (A.V <= 2048) {
+        // a row of one to a few vectors a lane: no barriers between waves
+        hipLaunchKernelGGL((score_kernel<BF16, 1, false>), grid, one, 0, st, A);
+    } else {
+        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, false>), grid, wide, 0, st, A);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -30,8 +63,12 @@ extern "C" {
 
 size_t pararnn_logprobs_workspace_bytes(int64_t N, int64_t V, int32_t top)
 {
-    (void)N, (void)V, (void)top;
-    return 0;
+    if (N <= 0 || V <= 0 || top < 0 || top > PARARNN_TOP_MAX || N >= (int64_t(1) << 24) ||
+        V >= (int64_t(1) << 31))
+        return 0;
+    const int64_t parts = score_parts(N, V);
+    if (parts == 1) return 0;
+    return score_stats_bytes(N, parts) + (size_t)N * parts * top * sizeof(uint64_t);
 }
 
 pararnn_status_t pararnn_token_logprobs(int64_t N, int64_t V, const void *logits,
@@ -64,13 +101,15 @@ pararnn_status_t pararnn_token_logprobs(int64_t N, int64_t V, const void *logits
     A.stride = row_stride;
     A.top = top;
     A.scale = scale;
+    A.parts = (int32_t)score_parts(N, V);
+    if (need > 0) {
+        A.part_stats = static_cast<float4 *>(ws);
+        A.part_keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) +
+                                                   score_stats_bytes(N, A.parts));
+    }
     hipStream_t strm = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)std::min<int64_t>(N, 1 << 20)), block(kScoreThreads);
-    if (dtype == PARARNN_BF16)
-        hipLaunchKernelGGL((score_row_kernel<true>), grid, block, 0, strm, A);
-    else
-        hipLaunchKernelGGL((score_row_kernel<false>), grid, block, 0, strm, A);
-    return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
+    const hipError_t e = dtype == PARARNN_BF16 ? run_score<true>(A, strm) : run_score<false>(A, strm);
+    return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
 pararnn_status_t pararnn_token_logprobs_adjoint(int64_t N, int64_t V, const void *logits,
@@ -104,7 +143,11 @@ pararnn_status_t pararnn_token_logprobs_adjoint(int64_t N, int64_t V, const void
     A.dx = dlogits;
     A.dstride = d_stride;
     hipStream_t strm = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)std::min<int64_t>(N, 1 << 20)), block(kScoreThreads);
+    // a row's vectors, one more where it starts off their alignment
+    const int64_t k = dtype == PARARNN_BF16 ? 8 : 4, per = kScoreUnroll * kScoreThreads;
+    A.parts = (int32_t)(((V + k - 1) / k + 1 + per - 1) / per);
+    if (N * A.parts >= (int64_t(1) << 24)) return PARARNN_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(N * A.parts)), block(kScoreThreads);
     if (dtype == PARARNN_BF16)
         hipLaunchKernelGGL((score_adjoint_kernel<true>), grid, block, 0, strm, A);
     else

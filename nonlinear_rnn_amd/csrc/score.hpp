@@ -14,6 +14,7 @@
 #pragma once
 
 #include "elements.hpp"
+#include "pararnn.h"
 
 namespace pararnn {
 
@@ -25,6 +26,9 @@ struct ScoreArgs {
     float *top_logprob;
     int64_t N, V, stride;
     int32_t top;
+    int32_t parts;       // workgroups a row
+    float4 *part_stats;  // [N][parts] m, s, w
+    uint64_t *part_keys; // [N][parts][top]
     float scale;
     // backward
     const float *lse_in, *entropy_in, *g_logprob, *g_entropy, *g_lse;
@@ -32,13 +36,17 @@ struct ScoreArgs {
     int64_t dstride;
 };
 
-// Keys grow with the logit (-0 and +0 alike) and, among equals, fall with
+// Unsigned integers in the order of the floats, -0 and +0 alike.
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+// Keys grow with the logit and, among equals, fall with
 // the token; 0 is below every key.
 __device__ __forceinline__ uint64_t top_key(float x, uint32_t token)
 {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return ((uint64_t)o << 32) | (0xffffffffu - token);
+    return ((uint64_t)ordered(x) << 32) | (0xffffffffu - token);
 }
 __device__ __forceinline__ float key_value(uint64_t k)
 {
@@ -49,111 +57,350 @@ __device__ __forceinline__ uint32_t key_token(uint64_t k) { return 0xffffffffu -
 // A masked or NaN logit is no alternative.
 __device__ __forceinline__ bool may_be_top(float x) { return x > -__builtin_inff(); }
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWaves = kScoreThreads / kWave;
+constexpr int kScoreWaves = 4;
+constexpr int kScoreThreads = kScoreWaves * kWave;
+constexpr int kScoreParts = 32;  // most parts of a row
+// Vectors a lane loads before it uses the first.
+constexpr int kScoreUnroll = 4;
 
-__device__ __forceinline__ float wave_max(float v)
+// Running statistics of part of a row: the largest logit so far and the two
+// sums, in base 2: with c = scale log2(e), s = sum 2^(c (x - m)),
+// w = sum c (x - m) 2^(c (x - m)).  An empty part has the lowest finite m and
+// s = 0, so that joining it changes nothing.
+struct Stats {
+    float m, s, w;
+};
+__device__ __forceinline__ Stats no_stats() { return {-__FLT_MAX__, 0.0f, 0.0f}; }
+// To another reference m: s and w by 2^(c (m_old - m)); the difference is kept
+// finite, since 0 sums must stay 0.
+__device__ __forceinline__ void rebase(Stats &a, float m, float c)
 {
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    const float d = fmaxf(c * (a.m - m), -1e30f);
+    const float f = ex2(d);
+    a.w = f * fmaf_(a.s, d, a.w);
+    a.s *= f;
+    a.m = m;
 }
-__device__ __forceinline__ float wave_sum(float v)
+__device__ __forceinline__ Stats join(Stats a, Stats b, float c)
 {
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    const float m = fmaxf(a.m, b.m);
+    rebase(a, m, c);
+    rebase(b, m, c);
+    return {m, a.s + b.s, a.w + b.w};
 }
-
-// One workgroup per row: a pass for the maximum, one for the sums, and one
-// for each alternative.
-template <bool BF16>
-__global__ void __launch_bounds__(kScoreThreads) score_row_kernel(ScoreArgs A)
+__device__ __forceinline__ Stats wave_join(Stats a, float c)
 {
-    __shared__ float part[3][kScoreWaves];
-    __shared__ uint64_t best[kScoreWaves];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    for (int64_t n = blockIdx.x; n < A.N; n += gridDim.x) {
-        const int64_t row = n * A.stride;
-        float m = -__builtin_inff();
-        for (int64_t j = threadIdx.x; j < A.V; j += kScoreThreads)
-            m = fmaxf(m, load_gate<BF16>(A.x, row + j));
-        m = wave_max(m);
-        __syncthreads();
-        if (lane == 0) part[0][wave] = m;
-        __syncthreads();
-        for (int w = 0; w < kScoreWaves; ++w) m = fmaxf(m, part[0][w]);
-        const float base = m > -__builtin_inff() ? m : 0.0f;
-        float s = 0.0f, ws = 0.0f;
-        for (int64_t j = threadIdx.x; j < A.V; j += kScoreThreads) {
-            const float d = A.scale * (load_gate<BF16>(A.x, row + j) - base);
-            const float e = ex2(kLog2e * d);
-            s += e;
-            if (e > 0.0f) ws = fmaf_(e, d, ws);
-        }
-        s = wave_sum(s);
-        ws = wave_sum(ws);
-        if (lane == 0) part[1][wave] = s, part[2][wave] = ws;
-        __syncthreads();
-        s = ws = 0.0f;
-        for (int w = 0; w < kScoreWaves; ++w) s += part[1][w], ws += part[2][w];
-        const bool empty = s == 0.0f;
-        const float ls = empty ? -__builtin_inff() : logf(s);
-        if (threadIdx.x == 0) {
-            const int64_t t = A.tokens[n];
-            float lp = 0.0f;
-            if (t >= A.V)
-                lp = __builtin_nanf("");
-            else if (t >= 0)
-                lp = empty ? ls : A.scale * (load_gate<BF16>(A.x, row + t) - base) - ls;
-            A.logprob[n] = lp;
-            if (A.lse) A.lse[n] = fmaf_(A.scale, base, ls);
-            if (A.entropy) A.entropy[n] = empty ? 0.0f : ls - ws / s;
-        }
-        uint64_t last = ~0ull;
-        for (int k = 0; k < A.top; ++k) {
-            uint64_t key = 0;
-            if (last)
-                for (int64_t j = threadIdx.x; j < A.V; j += kScoreThreads) {
-                    const float x = load_gate<BF16>(A.x, row + j);
-                    const uint64_t c = may_be_top(x) ? top_key(x, (uint32_t)j) : 0;
-                    if (c < last && c > key) key = c;
-                }
-            for (int o = 32; o > 0; o >>= 1) {
-                const uint64_t c = __shfl_xor(key, o);
-                if (c > key) key = c;
-            }
-            __syncthreads();
-            if (lane == 0) best[wave] = key;
-            __syncthreads();
-            for (int w = 0; w < kScoreWaves; ++w)
-                if (best[w] > key) key = best[w];
-            last = key;
-            if (threadIdx.x == 0) {
-                A.top_index[n * A.top + k] = key ? (int64_t)key_token(key) : -1;
-                A.top_logprob[n * A.top + k] =
-                    key ? A.scale * (key_value(key) - base) - ls : -__builtin_inff();
-            }
-        }
+    float m = a.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    rebase(a, m, c);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        a.s += __shfl_xor(a.s, o);
+        a.w += __shfl_xor(a.w, o);
+    }
+    return a;
+}
+template <int K>
+__device__ __forceinline__ void add_stats(Stats &a, const float (&x)[K], float c)
+{
+    float m = a.m;
+#pragma unroll
+    for (int k = 0; k < K; ++k) m = fmaxf(m, x[k]);
+    rebase(a, m, c);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const float d = c * (x[k] - m);
+        const float e = ex2(d);  // NaN stays NaN in the sum
+        a.s += e;
+        a.w = fmaf_(fmaxf(d, -300.0f), e, a.w);  // -inf times 0 would be NaN
     }
 }
 
-// The gradient, a workgroup per row.
+// A row as 16-byte vectors on their own alignment: vector i holds the
+// elements K i - shift .. + K - 1, the first and the last vector possibly in
+// part.  What lies outside the row reads as -inf and is not touched.
+template <bool BF16>
+struct RowView {
+    static constexpr int K = BF16 ? 8 : 4;
+    const char *row;
+    int shift;
+    int64_t V, vectors;
+    __device__ __forceinline__ RowView(const void *x, int64_t first, int64_t v)
+    {
+        row = static_cast<const char *>(x) + first * (BF16 ? 2 : 4);
+        shift = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / (BF16 ? 2 : 4);
+        V = v;
+        vectors = V > 0 ? (V + shift + K - 1) / K : 0;
+    }
+    __device__ __forceinline__ int64_t element(int64_t i) const { return i * K - shift; }
+    __device__ __forceinline__ void load(int64_t i, float (&x)[K]) const
+    {
+        const int64_t j = element(i);
+        if (j >= 0 && j + K <= V) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + j * (BF16 ? 2 : 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (BF16) {
+                    x[2 * q] = __uint_as_float(w[q] << 16);
+                    x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+                } else {
+                    x[q] = __uint_as_float(w[q]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                x[k] = j + k >= 0 && j + k < V ? load_gate<BF16>(row, j + k) : -__builtin_inff();
+        }
+    }
+};
+
+// The best tokens seen by a wave: lane i holds the i-th best key, 0 where
+// there is none.
+__device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane)
+{
+    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32) |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, lane);
+}
+struct TopList {
+    uint64_t key, floor;  // floor: what a key has to exceed
+    int last;             // the list's last lane
+    __device__ __forceinline__ void start(int top, uint64_t f)
+    {
+        key = 0;
+        floor = f;
+        last = top - 1;
+    }
+    // cand: the same in every lane, above the floor
+    __device__ __forceinline__ void insert(uint64_t cand)
+    {
+        const uint32_t hi = dppu<0x138>(~0u, (uint32_t)(key >> 32));  // the lane above
+        const uint32_t lo = dppu<0x138>(~0u, (uint32_t)key);
+        const uint64_t up = ((uint64_t)hi << 32) | lo;
+        if (key < cand) key = up < cand ? up : cand;
+        const uint64_t k = lane_key(key, last);
+        floor = k > floor ? k : floor;
+    }
+    // one key a lane, in any order
+    __device__ __forceinline__ void offer(uint64_t k)
+    {
+        uint64_t mask = __ballot(k > floor);
+        while (mask) {
+            const int l = __ffsll((unsigned long long)mask) - 1;
+            insert(lane_key(k, l));
+            mask &= mask - 1;
+            mask &= __ballot(k > floor);
+        }
+    }
+};
+// Every key that is not above this is of a masked token.
+constexpr uint64_t kMaskedFloor = 0x007fffffffffffffull;  // ordered(-inf) in the upper half
+
+// The results of row n from its statistics and (lanes 0 .. top - 1) its list.
+template <bool BF16>
+__device__ __forceinline__ void write_scores(const ScoreArgs &A, int64_t n, const Stats &a,
+                                             uint64_t key, int lane)
+{
+    const bool empty = a.s == 0.0f;
+    const float base = empty ? 0.0f : a.m;
+    const float ls = empty ? -__builtin_inff() : logf(a.s);
+    if (lane == 0) {
+        const int64_t t = A.tokens[n];
+        float lp = 0.0f;
+        if (t >= A.V)
+            lp = __builtin_nanf("");
+        else if (t >= 0)
+            lp = empty ? ls : fmaf_(A.scale, load_gate<BF16>(A.x, n * A.stride + t) - base, -ls);
+        A.logprob[n] = lp;
+        if (A.lse) A.lse[n] = fmaf_(A.scale, base, ls);
+        if (A.entropy) A.entropy[n] = empty ? 0.0f : ls - 0.6931471805599453f * (a.w / a.s);
+    }
+    if (lane < A.top) {
+        A.top_index[n * A.top + lane] = key ? (int64_t)key_token(key) : -1;
+        A.top_logprob[n * A.top + lane] =
+            key ? fmaf_(A.scale, key_value(key) - base, -ls) : -__builtin_inff();
+    }
+}
+
+// One workgroup of WAVES waves per row, or per part of a row (PARTS).
+// Statistics: every lane keeps its own running maximum and sums over its
+// vectors; one pass over the row, joined across lanes and waves at the end.
+// Alternatives: a lane's running maximum is the best of its own elements, so
+// the top-th best of the lanes' maxima is a lower bound of the top-th best
+// logit.  Only lanes whose maximum reaches the bound (about `top` of them) read
+// their vectors again, from the cache, and offer what reaches it to the wave's
+// list; wave 0 joins the waves' lists.
+template <bool BF16, int WAVES, bool PARTS>
+__global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
+{
+    using Row = RowView<BF16>;
+    constexpr int K = Row::K, U = kScoreUnroll, kThreads = WAVES * kWave;
+    __shared__ Stats part[WAVES];
+    __shared__ float maxima[kThreads];
+    __shared__ uint64_t lists[WAVES][PARARNN_TOP_MAX];
+    __shared__ uint32_t bound_lds;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
+    const int64_t p = PARTS ? blockIdx.x - n * A.parts : 0;
+    const float c = A.scale * kLog2e;
+    const Row row(A.x, n * A.stride, A.V);
+    const int64_t per = PARTS ? (row.vectors + A.parts - 1) / A.parts : row.vectors;
+    const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
+
+    Stats a = no_stats();
+    int64_t i = v0 + threadIdx.x;
+    for (; i + (U - 1) * kThreads < v1; i += U * kThreads) {
+        float x[U][K];
+#pragma unroll
+        for (int q = 0; q < U; ++q) row.load(i + q * kThreads, x[q]);
+#pragma unroll
+        for (int q = 0; q < U; ++q) add_stats<K>(a, x[q], c);
+    }
+    for (; i < v1; i += kThreads) {
+        float x[K];
+        row.load(i, x);
+        add_stats<K>(a, x, c);
+    }
+    const Stats joined = wave_join(a, c);
+    if (lane == 0) part[wave] = joined;
+    if (A.top) maxima[threadIdx.x] = a.m;
+    __syncthreads();
+    TopList list;
+    list.start(A.top, 0);
+    if (A.top) {
+        if (wave == 0) {
+            // the top-th best maximum, rounded down to 16 bits of its order
+            uint32_t o[WAVES], bound = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) o[w] = ordered(maxima[w * kWave + lane]);
+            for (int bit = 31; bit >= 16; --bit) {
+                const uint32_t trial = bound | 1u << bit;
+                int count = 0;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) count += __popcll(__ballot(o[w] >= trial));
+                if (count >= A.top) bound = trial;
+            }
+            if (lane == 0) bound_lds = bound;
+        }
+        __syncthreads();
+        const uint32_t bound = bound_lds;
+        const uint64_t low = bound ? ((uint64_t)bound << 32) - 1 : 0;
+        list.start(A.top, low > kMaskedFloor ? low : kMaskedFloor);
+        const bool mine = ordered(a.m) >= bound;
+        if (__ballot(mine))
+            for (int64_t j = v0 + threadIdx.x; __ballot(j < v1); j += 2 * kThreads) {
+                float x[2][K];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int64_t jq = j + q * kThreads;
+                    if (mine && jq < v1) {
+                        row.load(jq, x[q]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < K; ++k) x[q][k] = -__builtin_inff();
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float best = x[q][0];
+#pragma unroll
+                    for (int k = 1; k < K; ++k) best = fmaxf(best, x[q][k]);
+                    if (!__ballot(ordered(best) >= (uint32_t)(list.floor >> 32))) continue;
+                    const int64_t e = row.element(j + q * kThreads);
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        list.offer(may_be_top(x[q][k]) ? top_key(x[q][k], (uint32_t)(e + k)) : 0);
+                }
+            }
+        if constexpr (WAVES > 1) {
+            lists[wave][lane] = list.key;
+            __syncthreads();
+        }
+    }
+    if (wave != 0) return;
+    a = part[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        a = join(a, part[w], c);
+        if (A.top) list.offer(lists[w][lane]);
+    }
+    if constexpr (PARTS) {
+        if (lane == 0) A.part_stats[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
+        if (lane < A.top) A.part_keys[(int64_t)blockIdx.x * A.top + lane] = list.key;
+    } else {
+        write_scores<BF16>(A, n, a, list.key, lane);
+    }
+}
+
+// A wave per row joins its parts.
+template <bool BF16>
+__global__ void __launch_bounds__(kWave) score_join_kernel(ScoreArgs A)
+{
+    const int lane = threadIdx.x;
+    const int64_t n = blockIdx.x, first = n * A.parts;
+    const float c = A.scale * kLog2e;
+    Stats a = no_stats();
+    if (lane < A.parts) {
+        const float4 v = A.part_stats[first + lane];
+        a = {v.x, v.y, v.z};
+    }
+    a = wave_join(a, c);
+    TopList list;
+    list.start(A.top, 0);
+    if (A.top) {
+        constexpr int U = 8;
+        for (int p = 0; p < A.parts; p += U) {
+            uint64_t k[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                k[q] = lane < A.top && p + q < A.parts ? A.part_keys[(first + p + q) * A.top + lane] : 0;
+#pragma unroll
+            for (int q = 0; q < U; ++q) list.offer(k[q]);
+        }
+    }
+    write_scores<BF16>(A, n, a, list.key, lane);
+}
+
+// The gradient: U vectors a lane, a workgroup per kThreads * U vectors of a row.
 template <bool BF16>
 __global__ void __launch_bounds__(kScoreThreads) score_adjoint_kernel(ScoreArgs A)
 {
-    for (int64_t n = blockIdx.x; n < A.N; n += gridDim.x) {
-        const int64_t row = n * A.stride, out = n * A.dstride;
-        const float lse = A.lse_in[n], H = A.entropy_in ? A.entropy_in[n] : 0.0f;
-        const int64_t t = A.tokens[n];
-        const float glp = A.g_logprob && t >= 0 ? A.g_logprob[n] : 0.0f;
-        const float gh = A.g_entropy ? A.g_entropy[n] : 0.0f;
-        const float c0 = (A.g_lse ? A.g_lse[n] : 0.0f) - glp;
-        const bool empty = lse == -__builtin_inff();
-        for (int64_t j = threadIdx.x; j < A.V; j += kScoreThreads) {
-            const float lp = fmaf_(A.scale, load_gate<BF16>(A.x, row + j), -lse);
+    using Row = RowView<BF16>;
+    constexpr int K = Row::K, U = kScoreUnroll;
+    const int64_t n = blockIdx.x / A.parts;
+    const Row row(A.x, n * A.stride, A.V);
+    const int64_t i = (blockIdx.x - n * A.parts) * (U * kScoreThreads) + threadIdx.x;
+    float x[U][K];
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+        if (i + q * kScoreThreads < row.vectors) row.load(i + q * kScoreThreads, x[q]);
+    const float lse = A.lse_in[n], H = A.entropy_in ? A.entropy_in[n] : 0.0f;
+    const int64_t t = A.tokens[n];
+    const float glp = A.g_logprob && t >= 0 ? A.g_logprob[n] : 0.0f;
+    const float gh = A.g_entropy ? A.g_entropy[n] : 0.0f;
+    const float c0 = (A.g_lse ? A.g_lse[n] : 0.0f) - glp;
+    const bool empty = lse == -__builtin_inff();
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        if (i + q * kScoreThreads >= row.vectors) break;
+        const int64_t e = row.element(i + q * kScoreThreads);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float lp = fmaf_(A.scale, x[q][k], -lse);
             const float p = empty ? 0.0f : ex2(kLog2e * lp);
+            // p lp -> 0 as p -> 0
             float g = p == 0.0f ? 0.0f : p * fmaf_(-gh, lp + H, c0);
-            if (j == t && !empty) g += glp;
-            store_gate<BF16>(A.dx, out + j, A.scale * g);
+            if (e + k == t && !empty) g += glp;
+            x[q][k] = A.scale * g;
+        }
+        if (e >= 0) {
+            store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, x[q]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, x[q][k]);
         }
     }
 }

@@ -12,9 +12,42 @@ using namespace pararnn;
 
 namespace {
 
-constexpr int64_t kBlockGroups = 8 * kComputeUnits;  // workgroups that stay resident
+// Tilings of the register kernels: waves a workgroup, groups of 4 steps,
+// channel pairs a lane; they hold waves 64 / groups * 2 pairs channels.
+struct Tiling {
+    int waves, groups, pairs;
+    int64_t channels() const { return (int64_t)waves * kWave / groups * 2 * pairs; }
+};
+#define PARARNN_BLOCK_TILINGS(X)                                                                 \
+    X(1, 1, 1) X(4, 1, 1) X(4, 1, 2) X(8, 1, 2) X(16, 1, 2) X(16, 1, 4)                          \
+    X(2, 2, 1) X(4, 2, 1) X(4, 2, 2) X(8, 2, 2) X(16, 2, 2)
+#define PARARNN_TILING_ENTRY(W, G, P) {W, G, P},
+constexpr Tiling kTilings[] = {PARARNN_BLOCK_TILINGS(PARARNN_TILING_ENTRY)};
+constexpr int64_t kStripSteps = 4, kStripGroups = 2 * kComputeUnits;
 
-int block_steps(int64_t T) { return T >= 16 ? 16 : T >= 4 ? 4 : 1; }
+// The narrowest tiling that holds D channels, 8 steps a tile if there are
+// tiles enough for two workgroups a CU, else 4; no waves: the strip kernels.
+struct BlockPlan {
+    Tiling t = {0, 0, 0};
+    int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)
+};
+BlockPlan block_plan(const pararnn_block_shape_t *sh)
+{
+    BlockPlan pl;
+    const bool many = sh->B * ((sh->T + 7) / 8) >= 2 * kComputeUnits;
+    for (const Tiling &t : kTilings)
+        if (t.channels() >= sh->D && (t.groups == 2) <= many &&
+            (!pl.t.waves || t.groups > pl.t.groups ||
+             (t.groups == pl.t.groups && t.channels() < pl.t.channels())))
+            pl.t = t;
+    const int64_t steps = pl.t.waves ? 4 * pl.t.groups : kStripSteps;
+    pl.tiles_per_row = (sh->T + steps - 1) / steps;
+    pl.tiles = sh->B * pl.tiles_per_row;
+    // resident workgroups, 16 waves a CU; a multiple of the 8 XCDs
+    const int64_t fit = pl.t.waves ? 16 / pl.t.waves * kComputeUnits : kStripGroups;
+    pl.groups = std::min((pl.tiles + 7) / 8 * 8, fit);
+    return pl;
+}
 
 // Rows of D contiguous channels, (b, t) apart by the two strides.
 bool rows_disjoint(int64_t B, int64_t T, int64_t D, int64_t sb, int64_t st)
@@ -38,12 +71,7 @@ pararnn_status_t check_block(const pararnn_block_shape_t *sh)
 
 bool known(pararnn_dtype_t d) { return d == PARARNN_F32 || d == PARARNN_BF16; }
 
-int64_t block_tiles(const pararnn_block_shape_t *sh, int tt)
-{
-    return sh->B * ((sh->T + tt - 1) / tt);
-}
-
-void block_args(BlockArgs &A, const pararnn_block_shape_t *sh, int tt)
+void block_args(BlockArgs &A, const pararnn_block_shape_t *sh, const BlockPlan &pl)
 {
     std::memset(&A, 0, sizeof(A));
     A.B = sh->B;
@@ -59,17 +87,43 @@ void block_args(BlockArgs &A, const pararnn_block_shape_t *sh, int tt)
     A.xst = sh->x_stride_t;
     A.zsb = sh->z_stride_b;
     A.zst = sh->z_stride_t;
-    A.tiles_per_row = (sh->T + tt - 1) / tt;
-    A.tiles = block_tiles(sh, tt);
-    A.groups = (int32_t)std::min<int64_t>(A.tiles, kBlockGroups);
+    A.tiles_per_row = pl.tiles_per_row;
+    A.tiles = pl.tiles;
+    A.groups = (int32_t)pl.groups;
 }
 
-#define PARARNN_BLOCK_LAUNCH(KERNEL)                                                             \
-    switch (tt) {                                                                                \
-    case 16: hipLaunchKernelGGL((KERNEL<16>), grid, block, 0, strm, A); break;                   \
-    case 4: hipLaunchKernelGGL((KERNEL<4>), grid, block, 0, strm, A); break;                     \
-    default: hipLaunchKernelGGL((KERNEL<1>), grid, block, 0, strm, A); break;                    \
+// A dispatch counts its work-items in 32 bits.
+bool launchable(const BlockPlan &pl)
+{
+    return (pl.tiles + 7) / 8 * 8 * (pl.t.waves ? pl.t.waves : 1) * kWave < (int64_t(1) << 32);
+}
+
+template <bool ADJ>
+hipError_t launch_block(const BlockArgs &A, const BlockPlan &pl, hipStream_t st)
+{
+    const dim3 grid((unsigned)(ADJ ? pl.groups : (pl.tiles + 7) / 8 * 8)),
+        block((unsigned)(pl.t.waves * kWave));
+    if (!pl.t.waves) {
+        const dim3 few((unsigned)pl.groups), strip(kBlockThreads);
+        if constexpr (ADJ)
+            hipLaunchKernelGGL((block_strip_adjoint_kernel<kStripSteps>), few, strip, 0, st, A);
+        else
+            hipLaunchKernelGGL((block_strip_kernel<kStripSteps>), few, strip, 0, st, A);
+        return hipGetLastError();
     }
+#define PARARNN_TILING_CASE(W, G, P)                                                             \
+    case W * 100 + G * 10 + P:                                                                   \
+        if constexpr (ADJ)                                                                       \
+            hipLaunchKernelGGL((block_tile_adjoint_kernel<W, G, P>), grid, block, 0, st, A);     \
+        else                                                                                     \
+            hipLaunchKernelGGL((block_tile_kernel<W, G, P>), grid, block, 0, st, A);             \
+        break;
+    switch (pl.t.waves * 100 + pl.t.groups * 10 + pl.t.pairs) {
+        PARARNN_BLOCK_TILINGS(PARARNN_TILING_CASE)
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
 
 }  // namespace
 
@@ -88,9 +142,10 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
     if (!std::isfinite(scale) || !(eps > 0.0f) || std::isinf(eps)) return PARARNN_ERR_INVALID;
     if (shape->B == 0 || shape->T == 0 || shape->D == 0) return PARARNN_OK;
     if (!x || !w_pre || !z || (h && (!w_post || !y)) || (!h && gate)) return PARARNN_ERR_INVALID;
-    const int tt = block_steps(shape->T);
+    const BlockPlan pl = block_plan(shape);
+    if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
-    block_args(A, shape, tt);
+    block_args(A, shape, pl);
     A.h = h;
     A.gate = gate;
     A.x = x;
@@ -104,17 +159,14 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
     A.gate_bf16 = gate_dtype == PARARNN_BF16;
     A.x_bf16 = x_dtype == PARARNN_BF16;
     A.z_bf16 = z_dtype == PARARNN_BF16;
-    hipStream_t strm = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)A.groups), block(kBlockThreads);
-    PARARNN_BLOCK_LAUNCH(block_strip_kernel)
-    return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
+    const hipError_t e = launch_block<false>(A, pl, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
 size_t pararnn_block_workspace_bytes(const pararnn_block_shape_t *shape)
 {
     if (check_block(shape) != PARARNN_OK) return 0;
-    const int64_t g = std::min<int64_t>(block_tiles(shape, block_steps(shape->T)), kBlockGroups);
-    return align_up((size_t)g * 2 * shape->D * sizeof(float));
+    return align_up((size_t)block_plan(shape).groups * 2 * shape->D * sizeof(float));
 }
 
 pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, const float *h,
@@ -138,9 +190,10 @@ pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, 
         return PARARNN_ERR_INVALID;
     const size_t need = pararnn_block_workspace_bytes(shape);
     if (work && (!ws || ws_bytes < need || !aligned16(ws))) return PARARNN_ERR_WORKSPACE;
-    const int tt = block_steps(shape->T);
+    const BlockPlan pl = block_plan(shape);
+    if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
-    block_args(A, shape, tt);
+    block_args(A, shape, pl);
     A.h = h;
     A.gate = gate;
     A.x = x;
@@ -160,14 +213,9 @@ pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, 
     A.x_bf16 = x_dtype == PARARNN_BF16;
     A.z_bf16 = z_dtype == PARARNN_BF16;
     hipStream_t strm = static_cast<hipStream_t>(stream);
-    if (work) {
-        const dim3 grid((unsigned)A.groups), block(kBlockThreads);
-        PARARNN_BLOCK_LAUNCH(block_strip_adjoint_kernel)
-        if (hipGetLastError() != hipSuccess) return PARARNN_ERR_HIP;
-    }
-    const int tpb = 256;
-    hipLaunchKernelGGL(block_dw_kernel, dim3((unsigned)((2 * shape->D + tpb - 1) / tpb)), dim3(tpb),
-                       0, strm, A);
+    if (work && launch_block<true>(A, pl, strm) != hipSuccess) return PARARNN_ERR_HIP;
+    hipLaunchKernelGGL(block_dw_kernel, dim3((unsigned)((2 * shape->D + kWave - 1) / kWave)),
+                       dim3(kDwWaves * kWave), 0, strm, A);
     return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 

@@ -32,7 +32,10 @@ __device__ __forceinline__ void store_gate(void *p, int64_t i, float x)
 // gfx9 global memory takes at any alignment (unaligned-access-mode, on for
 // every amdhsa target).
 typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
+typedef uint32_t Words2 __attribute__((ext_vector_type(2)));
 typedef Words4 __attribute__((aligned(2))) Words4Any;
+typedef Words2 __attribute__((aligned(2))) Words2Any;
+typedef uint32_t __attribute__((aligned(2))) Word1Any;
 
 // K elements as loaded: 2 or 4 bytes each.
 template <bool BF16, int K>

@@ -36,7 +36,8 @@ def compile_flags():
 
 SOURCES = ["pararnn.hip", "inst_gru_f32.hip", "inst_gru_bf16.hip", "inst_gru_bf16_seq.hip",
            "inst_lstm_f32.hip", "inst_lstm_bf16.hip", "inst_scan.hip", "inst_seq.hip",
-           "inst_project.hip", "gated.hip", "block.hip", "score.hip"]
+           "inst_project.hip", "gated.hip", "block.hip", "score.hip"] + [
+           f"inst_block_{n}.hip" for n in ("f32", "gate", "stream", "bf16", "args", "norm")]
 
 # Per-unit scheduler choice, by measurement: the block-sequential ParaGRU
 # kernel on bf16 projections that the long, many-channel solves use runs 2%

@@ -5,7 +5,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "block.hpp"
+#include "block_launch.hpp"
 #include "host.hpp"
 
 using namespace pararnn;
@@ -16,27 +16,32 @@ namespace {
 // channel pairs a lane; they hold waves 64 / groups * 2 pairs channels.
 struct Tiling {
     int waves, groups, pairs;
+    bool quads;
     int64_t channels() const { return (int64_t)waves * kWave / groups * 2 * pairs; }
 };
-#define PARARNN_BLOCK_TILINGS(X)                                                                 \
-    X(1, 1, 1) X(4, 1, 1) X(4, 1, 2) X(8, 1, 2) X(16, 1, 2) X(16, 1, 4)                          \
-    X(2, 2, 1) X(4, 2, 1) X(4, 2, 2) X(8, 2, 2) X(16, 2, 2)
-#define PARARNN_TILING_ENTRY(W, G, P) {W, G, P},
+#define PARARNN_TILING_ENTRY(W, G, P, Q) {W, G, P, Q},
 constexpr Tiling kTilings[] = {PARARNN_BLOCK_TILINGS(PARARNN_TILING_ENTRY)};
 constexpr int64_t kStripSteps = 4, kStripGroups = 2 * kComputeUnits;
 
-// The narrowest tiling that holds D channels, 8 steps a tile if there are
-// tiles enough for two workgroups a CU, else 4; no waves: the strip kernels.
+// The narrowest tiling that holds D channels: 4 contiguous steps a load where
+// the planes have them, and then 8 steps a tile if there are tiles enough for
+// two workgroups a CU.  No waves: the strip kernels.
 struct BlockPlan {
-    Tiling t = {0, 0, 0};
+    Tiling t = {0, 0, 0, false};
     int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)
 };
 BlockPlan block_plan(const pararnn_block_shape_t *sh)
 {
     BlockPlan pl;
-    const bool many = sh->B * ((sh->T + 7) / 8) >= 2 * kComputeUnits;
+    const bool quads = sh->h_stride_t == 1 && sh->g_stride_t == 1 && sh->T >= 4;
+    const bool many = quads && sh->T >= 8 && sh->B * ((sh->T + 7) / 8) >= 2 * kComputeUnits;
+    // a lane's offset from the tile's base is 32 bits of bytes
+    const int64_t reach = (int64_t(1) << 29) - 8;
+    const bool near = sh->D >= 2 && sh->h_stride_d <= reach / sh->D &&
+                      sh->g_stride_d <= reach / sh->D && sh->x_stride_t <= reach / 8 &&
+                      sh->z_stride_t <= reach / 8;
     for (const Tiling &t : kTilings)
-        if (t.channels() >= sh->D && (t.groups == 2) <= many &&
+        if (near && t.channels() >= sh->D && t.quads == quads && (t.groups == 2) <= many &&
             (!pl.t.waves || t.groups > pl.t.groups ||
              (t.groups == pl.t.groups && t.channels() < pl.t.channels())))
             pl.t = t;
@@ -98,8 +103,29 @@ bool launchable(const BlockPlan &pl)
     return (pl.tiles + 7) / 8 * 8 * (pl.t.waves ? pl.t.waves : 1) * kWave < (int64_t(1) << 32);
 }
 
+// For the register kernels: a tensor that is not given is read from one that
+// is (and dropped), so that their loads need no condition.
+void stand_ins(BlockArgs &A, bool adjoint)
+{
+    A.has_gate = A.gate != nullptr;
+    A.has_gy = A.gy != nullptr;
+    A.has_gz = A.gz != nullptr;
+    if (A.h && !A.gate) {
+        A.gate = A.h;
+        A.gate_bf16 = 0;
+        A.gsb = A.hsb, A.gsd = A.hsd, A.gst = A.hst;
+    }
+    if (!adjoint) return;
+    if (!A.gy) A.gy = A.x;
+    if (!A.gz) {
+        A.gz = A.x;
+        A.z_bf16 = A.x_bf16;
+        A.zsb = A.xsb, A.zst = A.xst;
+    }
+}
+
 template <bool ADJ>
-hipError_t launch_block(const BlockArgs &A, const BlockPlan &pl, hipStream_t st)
+hipError_t launch_block(BlockArgs A, const BlockPlan &pl, hipStream_t st)
 {
     const dim3 grid((unsigned)(ADJ ? pl.groups : (pl.tiles + 7) / 8 * 8)),
         block((unsigned)(pl.t.waves * kWave));
@@ -111,18 +137,18 @@ hipError_t launch_block(const BlockArgs &A, const BlockPlan &pl, hipStream_t st)
             hipLaunchKernelGGL((block_strip_kernel<kStripSteps>), few, strip, 0, st, A);
         return hipGetLastError();
     }
-#define PARARNN_TILING_CASE(W, G, P)                                                             \
-    case W * 100 + G * 10 + P:                                                                   \
-        if constexpr (ADJ)                                                                       \
-            hipLaunchKernelGGL((block_tile_adjoint_kernel<W, G, P>), grid, block, 0, st, A);     \
-        else                                                                                     \
-            hipLaunchKernelGGL((block_tile_kernel<W, G, P>), grid, block, 0, st, A);             \
-        break;
-    switch (pl.t.waves * 100 + pl.t.groups * 10 + pl.t.pairs) {
-        PARARNN_BLOCK_TILINGS(PARARNN_TILING_CASE)
-    default: return hipErrorInvalidValue;
+    stand_ins(A, ADJ);
+    const int types = A.gate_bf16 * kGateBf16 | A.x_bf16 * kStreamBf16 | A.z_bf16 * kNormedBf16;
+    const int tiling = tiling_code(pl.t.waves, pl.t.groups, pl.t.pairs, pl.t.quads);
+    if (!A.h) return launch_block_norm(ADJ, tiling, grid, block, st, A);
+    switch (types) {
+    case kNormedBf16: return launch_block_f32(ADJ, tiling, grid, block, st, A);
+    case kNormedBf16 | kGateBf16: return launch_block_gate(ADJ, tiling, grid, block, st, A);
+    case kNormedBf16 | kStreamBf16: return launch_block_stream(ADJ, tiling, grid, block, st, A);
+    case kNormedBf16 | kGateBf16 | kStreamBf16:
+        return launch_block_bf16(ADJ, tiling, grid, block, st, A);
+    default: return launch_block_args(ADJ, tiling, grid, block, st, A);
     }
-    return hipGetLastError();
 }
 
 }  // namespace

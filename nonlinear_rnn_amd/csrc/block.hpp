@@ -41,6 +41,7 @@ struct BlockArgs {
     int64_t hsb, hsd, hst, gsb, gsd, gst, xsb, xst, zsb, zst;
     int64_t tiles, tiles_per_row;
     int32_t gate_bf16, x_bf16, z_bf16;
+    int32_t has_gate, has_gy, has_gz;  // register kernels: else read but dropped
     int32_t groups;
 };
 
@@ -236,105 +237,156 @@ __global__ void __launch_bounds__(kBlockThreads) block_strip_adjoint_kernel(Bloc
 }
 
 // ------------------------------------------------------- tile in registers ---
-// Up to 8192 channels: a workgroup keeps its tile of 4 TG steps in registers
+// Up to 4096 channels: a workgroup keeps its tile of 4 TG steps in registers
 // from the first load to the last store, so that every tensor is read once.
-// A lane owns pairs of channels (2 NP of them, the workgroup's pairs apart)
-// and 4 steps: channel-major loads are 16 bytes (8 in bf16) along its steps,
-// time-major ones two channels wide, a wave (or, TG = 2, either half of it)
-// running along the channels.  Lanes of a half wave share steps, so a sum over
-// the channels is a DPP reduction, then one across waves through LDS.
+// A lane owns pairs of channels (NP pairs, the workgroup's pairs apart) and 4
+// steps.  Channel-major loads are 16 bytes (8 in bf16) along its steps, time-
+// major ones two channels wide, a wave (or, TG = 2, either half of it) running
+// along the channels.  Lanes of a half wave share steps, so a sum over the
+// channels is a DPP reduction, then one across waves through LDS.
+//
+// No load is conditional: a lane past the last channel reads the last pair
+// again, is left out of the sums, and stores what that pair's lane stores; a
+// row's last tile is moved back to end with the row, and the steps it shares
+// with the one before are computed but neither stored nor summed.  A gradient
+// or gate that is not given is read from a tensor that is, and dropped.  A
+// tile's base is uniform (scalar registers), a lane's offset from it 32 bits;
+// the host sends planes that reach further to the strip kernels.
+//
+// Planes whose steps are not contiguous, or fewer steps than a tile, load
+// their 4 steps one by one (QUADS false); a missing step repeats the last one.
 //
 // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a contiguous
 // range of tiles, so that the tiles that share a channel's cache lines (4 or
 // 8 of a line's 32 float32 steps each) run together on one L2.
 constexpr int kTileSteps = 4;  // steps of a lane
 
-struct Quad {  // 4 steps of a channel, as loaded
+// The types of a launch: known when it is compiled (gate, stream and normed
+// stream each float32 or bf16), or read from the arguments.
+constexpr int kGateBf16 = 1, kStreamBf16 = 2, kNormedBf16 = 4, kTypesFromArgs = 8;
+constexpr int kNoStates = 16;  // without h: the stream's norm alone
+template <int TYPES>
+struct BlockTypes {
+    static constexpr bool known = (TYPES & kTypesFromArgs) == 0;
+    bool gate, stream, normed;
+    __device__ __forceinline__ explicit BlockTypes(const BlockArgs &A)
+        : gate(known ? (TYPES & kGateBf16) != 0 : A.gate_bf16 != 0),
+          stream(known ? (TYPES & kStreamBf16) != 0 : A.x_bf16 != 0),
+          normed(known ? (TYPES & kNormedBf16) != 0 : A.z_bf16 != 0)
+    {
+    }
+};
+
+__device__ __forceinline__ uint32_t opaque_bits(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+// `bytes` past a uniform address.  The address goes through an empty asm as a
+// scalar register pair in the global address space: the compiler would add
+// the lane's offset to the tensor's address first, to share that sum between
+// rows, and hold 64 vector bits for each tensor.
+#define PARARNN_GLOBAL __attribute__((address_space(1)))
+template <class T>
+__device__ __forceinline__ T load_at(const void *base, uint32_t bytes)
+{
+    uint64_t a = reinterpret_cast<uint64_t>(base);
+    asm("" : "+s"(a));
+    return *(const PARARNN_GLOBAL T *)((const PARARNN_GLOBAL char *)a + bytes);
+}
+template <class T, class V>
+__device__ __forceinline__ void store_at(void *base, uint32_t bytes, V v)
+{
+    uint64_t a = reinterpret_cast<uint64_t>(base);
+    asm("" : "+s"(a), "+v"(bytes));  // the offset too: it is widened where it is used
+    *(PARARNN_GLOBAL T *)((PARARNN_GLOBAL char *)a + bytes) = v;
+}
+__device__ __forceinline__ const void *element_at(const void *p, int64_t i, bool bf16)
+{
+    return static_cast<const char *>(p) + (i << (bf16 ? 1 : 2));
+}
+__device__ __forceinline__ void *element_at(void *p, int64_t i, bool bf16)
+{
+    return static_cast<char *>(p) + (i << (bf16 ? 1 : 2));
+}
+
+struct Quad {  // 4 steps of a channel, as loaded: bf16 in two words, float32 in four
     uint32_t w[4];
 };
-__device__ __forceinline__ Quad load_quad(const void *p, int64_t off, int64_t st, int n, bool bf16)
+// `row`: the uniform address of the lane's channel group at the tile's first
+// step; step k is `step[k]` elements on.
+template <bool QUADS>
+__device__ __forceinline__ Quad load_quad(const void *row, uint32_t off, const int64_t (&step)[4],
+                                          bool bf16)
 {
-    Quad q;
-    if (st == 1 && n >= kTileSteps) {
+    Quad q = {{0u, 0u, 0u, 0u}};
+    if constexpr (QUADS) {
         if (bf16) {
-            const Words2 v = *reinterpret_cast<const Words2Any *>(static_cast<const uint16_t *>(p) + off);
-            q.w[0] = v.x, q.w[1] = v.y, q.w[2] = q.w[3] = 0u;
+            const Words2 v = load_at<Words2Any>(row, off);
+            q.w[0] = v.x, q.w[1] = v.y;
         } else {
-            const Words4 v = *reinterpret_cast<const Words4Any *>(static_cast<const float *>(p) + off);
+            const Words4 v = load_at<Words4Any>(row, off);
             q.w[0] = v.x, q.w[1] = v.y, q.w[2] = v.z, q.w[3] = v.w;
         }
-    } else {
+    } else if (bf16) {
         uint32_t e[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            e[k] = k >= n ? 0u
-                   : bf16 ? static_cast<const uint16_t *>(p)[off + k * st]
-                          : static_cast<const uint32_t *>(p)[off + k * st];
+        for (int k = 0; k < 4; ++k) e[k] = load_at<uint16_t>(element_at(row, step[k], true), off);
+        q.w[0] = e[0] | e[1] << 16, q.w[1] = e[2] | e[3] << 16;
+    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q.w[k] = e[k];
-        if (bf16) q.w[0] = e[0] | e[1] << 16, q.w[1] = e[2] | e[3] << 16;
+        for (int k = 0; k < 4; ++k)
+            q.w[k] = load_at<uint32_t>(element_at(row, step[k], false), off);
     }
     return q;
 }
-__device__ __forceinline__ void quad_values(const Quad &q, bool bf16, float (&v)[4])
+__device__ __forceinline__ float quad_value(const Quad &q, int k, bool bf16)
 {
-    v[0] = __uint_as_float(bf16 ? q.w[0] << 16 : q.w[0]);
-    v[1] = __uint_as_float(bf16 ? q.w[0] & 0xffff0000u : q.w[1]);
-    v[2] = __uint_as_float(bf16 ? q.w[1] << 16 : q.w[2]);
-    v[3] = __uint_as_float(bf16 ? q.w[1] & 0xffff0000u : q.w[3]);
+    if (bf16) return __uint_as_float(k & 1 ? q.w[k / 2] & 0xffff0000u : q.w[k / 2] << 16);
+    return __uint_as_float(q.w[k]);
 }
-__device__ __forceinline__ void store_quad(void *p, int64_t off, int64_t st, int n, bool bf16,
+template <bool QUADS>
+__device__ __forceinline__ void store_quad(void *row, uint32_t off, const int64_t (&step)[4],
+                                           const bool (&own)[4], bool all, bool bf16,
                                            const float (&v)[4])
 {
-    if (st == 1 && n >= kTileSteps) {
+    if (QUADS && all) {
         if (bf16) {
-            const Words2 w = {bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
-                              bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
-            *reinterpret_cast<Words2Any *>(static_cast<uint16_t *>(p) + off) = w;
+            store_at<Words2Any>(row, off, Words2{bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                    bf16_bits(v[2]) | bf16_bits(v[3]) << 16});
         } else {
-            const Words4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                              __float_as_uint(v[3])};
-            *reinterpret_cast<Words4Any *>(static_cast<float *>(p) + off) = w;
+            store_at<Words4Any>(row, off, Words4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                    __float_as_uint(v[2]), __float_as_uint(v[3])});
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < n) store_any(p, off + k * st, v[k], bf16);
+        for (int k = 0; k < 4; ++k) {
+            if (!own[k]) continue;
+            void *e = element_at(row, step[k], bf16);
+            if (bf16)
+                store_at<uint16_t>(e, off, (uint16_t)bf16_bits(v[k]));
+            else
+                store_at<float>(e, off, v[k]);
+        }
     }
 }
-// Two neighbouring channels of a step, the second only if `two`.
-__device__ __forceinline__ Words2 load_pair(const void *p, int64_t off, bool two, bool bf16)
+// Two neighbouring channels of a step.
+__device__ __forceinline__ Words2 load_pair(const void *row, uint32_t off, bool bf16)
 {
-    Words2 r = {0u, 0u};
-    if (bf16) {
-        const uint16_t *a = static_cast<const uint16_t *>(p) + off;
-        r.x = two ? *reinterpret_cast<const Word1Any *>(a) : *a;
-    } else {
-        const uint32_t *a = static_cast<const uint32_t *>(p) + off;
-        if (two)
-            r = *reinterpret_cast<const Words2Any *>(a);
-        else
-            r.x = *a;
-    }
-    return r;
+    if (bf16) return Words2{load_at<Word1Any>(row, off), 0u};
+    return load_at<Words2Any>(row, off);
 }
 __device__ __forceinline__ float pair_value(Words2 w, int i, bool bf16)
 {
     if (bf16) return __uint_as_float(i ? w.x & 0xffff0000u : w.x << 16);
     return __uint_as_float(i ? w.y : w.x);
 }
-__device__ __forceinline__ void store_pair(void *p, int64_t off, bool two, bool bf16, float a,
-                                           float b)
+__device__ __forceinline__ void store_pair(void *row, uint32_t off, bool bf16, float a, float b)
 {
-    if (!two) {
-        store_any(p, off, a, bf16);
-    } else if (bf16) {
-        *reinterpret_cast<Word1Any *>(static_cast<uint16_t *>(p) + off) =
-            bf16_bits(a) | bf16_bits(b) << 16;
-    } else {
-        const Words2 w = {__float_as_uint(a), __float_as_uint(b)};
-        *reinterpret_cast<Words2Any *>(static_cast<float *>(p) + off) = w;
-    }
+    if (bf16)
+        store_at<Word1Any>(row, off, bf16_bits(a) | bf16_bits(b) << 16);
+    else
+        store_at<Words2Any>(row, off, Words2{__float_as_uint(a), __float_as_uint(b)});
 }
 
 // Sums of N values a lane over the lanes that share its steps: the whole
@@ -374,79 +426,124 @@ struct TileSums {
     }
 };
 
-template <int TG>
+// A tile's place: row b, first step t, the lane's steps own[k] (all: every one).
+template <int TG, bool QUADS>
 struct TileAt {
-    int64_t b, t;  // row and the lane's first step
-    int n;         // its steps that exist
+    int64_t b, t;
+    int half;              // TG = 2: the lane's 4 of the tile's 8 steps
+    int64_t k_of[4];       // offset from t of step k (of half 0 where QUADS)
+    bool own[4], all;
     __device__ __forceinline__ TileAt(const BlockArgs &A, int64_t tile)
     {
-        b = tile / A.tiles_per_row;
-        t = (tile - b * A.tiles_per_row) * (kTileSteps * TG);
-        if (TG == 2) t += threadIdx.x % kWave / 32 * kTileSteps;
-        n = (int)max((int64_t)0, min((int64_t)kTileSteps, A.T - t));
+        constexpr int TT = kTileSteps * TG;
+        static_assert(QUADS || TG == 1, "single steps: one group");
+        // tiles fit in 32 bits; the division leaves vector registers, so the
+        // row is made uniform again
+        const uint32_t row = __builtin_amdgcn_readfirstlane((uint32_t)tile / (uint32_t)A.tiles_per_row);
+        b = row;
+        const int64_t want = (tile - b * A.tiles_per_row) * TT;
+        t = QUADS ? min(want, A.T - TT) : want;
+        half = TG == 2 ? (int)(threadIdx.x % kWave / 32) : 0;
+        all = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            k_of[k] = QUADS ? k : min((int64_t)k, A.T - 1 - t);
+            own[k] = QUADS ? t + half * kTileSteps + k >= want : t + k < A.T;
+            all = all && own[k];
+        }
+    }
+    __device__ __forceinline__ void steps(int64_t stride, int64_t (&s)[4]) const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = k_of[k] * stride;
     }
 };
-// The lane's place among the workgroup's channel pairs.
-template <int TG>
-__device__ __forceinline__ int pair_of_lane()
-{
-    return TG == 2 ? (int)(threadIdx.x / kWave * 32 + threadIdx.x % 32) : (int)threadIdx.x;
-}
 
-template <int WAVES, int TG, int NP>
+// The lane's channel pair p.  Past the end, and where the last channel of an
+// odd number stands alone, the pair is (D - 2, D - 1).
+template <int WAVES, int TG>
+struct PairAt {
+    uint32_t d, half;
+    bool first, second;  // which of its channels no other lane has
+    __device__ __forceinline__ PairAt(const BlockArgs &A, int p)
+    {
+        // opaque: what follows from it is cheaper again than kept over a tile
+        const uint32_t thread = opaque_bits(threadIdx.x);
+        const uint32_t lane = TG == 2 ? thread / kWave * 32 + thread % 32 : thread;
+        const uint32_t D = (uint32_t)A.D, want = 2u * (lane + p * (WAVES * kWave / TG));
+        half = TG == 2 ? thread % kWave / 32 : 0u;
+        d = min(want, D - 2);
+        first = want + 1 < D;
+        second = want < D;
+    }
+    // Byte offsets from the tile's base.
+    __device__ __forceinline__ uint32_t in_plane(int64_t stride_d, bool bf16) const
+    {
+        return (d * (uint32_t)stride_d + kTileSteps * half) << (bf16 ? 1 : 2);
+    }
+    __device__ __forceinline__ uint32_t in_row(int64_t stride_t, bool bf16) const
+    {
+        return (d + half * kTileSteps * (uint32_t)stride_t) << (bf16 ? 1 : 2);
+    }
+};
+
+template <int WAVES, int TG, int NP, bool QUADS, int TYPES>
 __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
 {
-    constexpr int kPairs = WAVES * kWave / TG;
     __shared__ TileSums<4, TG, WAVES> sums[2];
     const int64_t tile = tile_of(blockIdx.x, A.tiles);
     if (tile >= A.tiles) return;
-    const TileAt<TG> at(A, tile);
-    const bool gb = A.gate_bf16, xb = A.x_bf16, zb = A.z_bf16;
+    const TileAt<TG, QUADS> at(A, tile);
+    const BlockTypes<TYPES> types(A);
+    const bool gb = types.gate, xb = types.stream, zb = types.normed;
+    constexpr bool kStates = (TYPES & kNoStates) == 0;
+    [[maybe_unused]] const bool has_gate = A.has_gate;
     const float over_d = 1.0f / (float)A.D;
-    const int64_t ho = at.b * A.hsb + at.t * A.hst, go = at.b * A.gsb + at.t * A.gst;
+    int64_t hk[4], gk[4], xk[4], zk[4];
+    at.steps(A.hst, hk), at.steps(A.gst, gk), at.steps(A.xst, xk), at.steps(A.zst, zk);
     const int64_t xo = at.b * A.xsb + at.t * A.xst, zo = at.b * A.zsb + at.t * A.zst;
 
     Quad h[NP][2], g[NP][2];
     Words2 x[NP][4];
     float wp[NP][2], wn[NP][2];
+    const float *h_row = A.h + at.b * A.hsb + at.t * A.hst;
+    const void *g_row = element_at(A.gate, at.b * A.gsb + at.t * A.gst, gb);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+        const PairAt<WAVES, TG> c(A, p);
+        const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int n = d + i < A.D ? at.n : 0;
-            h[p][i] = g[p][i] = Quad{{0u, 0u, 0u, 0u}};
-            if (A.h) h[p][i] = load_quad(A.h, ho + (d + i) * A.hsd, A.hst, n, false);
-            if (A.gate) g[p][i] = load_quad(A.gate, go + (d + i) * A.gsd, A.gst, n, gb);
+            if constexpr (kStates) {
+                h[p][i] = load_quad<QUADS>(h_row + i * A.hsd, hoff, hk, false);
+                g[p][i] = load_quad<QUADS>(element_at(g_row, i * A.gsd, gb), goff, gk, gb);
+            }
         }
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+        const PairAt<WAVES, TG> c(A, p);
+        const uint32_t xoff = c.in_row(A.xst, xb);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[p][k] = Words2{0u, 0u};
-            if (k < at.n && d < A.D) x[p][k] = load_pair(A.x, xo + d + k * A.xst, d + 1 < A.D, xb);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            wp[p][i] = A.h && d + i < A.D ? A.w_post[d + i] : 0.0f;
-            wn[p][i] = d + i < A.D ? A.w_pre[d + i] : 0.0f;
-        }
+        for (int k = 0; k < 4; ++k) x[p][k] = load_pair(element_at(A.x, xo + xk[k], xb), xoff, xb);
+        wn[p][0] = A.w_pre[c.d], wn[p][1] = A.w_pre[c.d + 1];
+        if constexpr (kStates)
+            wp[p][0] = A.scale * A.w_post[c.d], wp[p][1] = A.scale * A.w_post[c.d + 1];
     }
     float v[NP][2][4], r1[4] = {0.0f, 0.0f, 0.0f, 0.0f}, r2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (A.h) {
+    if constexpr (kStates) {
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float hv[4], gv[4];
-                quad_values(h[p][i], false, hv);
-                quad_values(g[p][i], gb, gv);
+                const PairAt<WAVES, TG> c(A, p);
+                const bool counts = i ? c.second : c.first;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    v[p][i][k] = gated_value(hv[k], gv[k], A.gate);
-                    r1[k] = fmaf_(v[p][i][k], v[p][i][k], r1[k]);
+                    v[p][i][k] = gated_value(quad_value(h[p][i], k, false),
+                                             quad_value(g[p][i], k, gb), has_gate);
+                    const float s = counts ? v[p][i][k] : 0.0f;
+                    r1[k] = fmaf_(s, s, r1[k]);
                 }
             }
         sums[0].sum(r1);
@@ -455,19 +552,20 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
     }
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+        const PairAt<WAVES, TG> c(A, p);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            float y[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                y[i] = pair_value(x[p][k], i, xb);
-                if (A.h) y[i] = fmaf_(v[p][i][k] * r1[k], A.scale * wp[p][i], y[i]);
-                r2[k] = fmaf_(y[i], y[i], r2[k]);
-                v[p][i][k] = y[i];
+                float y = pair_value(x[p][k], i, xb);
+                if constexpr (kStates) y = fmaf_(v[p][i][k] * r1[k], wp[p][i], y);
+                const float s = (i ? c.second : c.first) ? y : 0.0f;
+                r2[k] = fmaf_(s, s, r2[k]);
+                v[p][i][k] = y;
             }
-            if (A.y && k < at.n && d < A.D)
-                store_pair(A.y, xo + d + k * A.xst, d + 1 < A.D, xb, y[0], y[1]);
+            if (A.y && (at.all || at.own[k]))
+                store_pair(element_at(A.y, xo + xk[k], xb), c.in_row(A.xst, xb), xb, v[p][0][k],
+                           v[p][1][k]);
         }
     }
     sums[1].sum(r2);
@@ -475,101 +573,126 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
     for (int k = 0; k < 4; ++k) r2[k] = 1.0f / sqrtf(fmaf_(r2[k], over_d, A.eps));
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+        const uint32_t zoff = PairAt<WAVES, TG>(A, p).in_row(A.zst, zb);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (k < at.n && d < A.D)
-                store_pair(A.z, zo + d + k * A.zst, d + 1 < A.D, zb, v[p][0][k] * r2[k] * wn[p][0],
+            if (at.all || at.own[k])
+                store_pair(element_at(A.z, zo + zk[k], zb), zoff, zb, v[p][0][k] * r2[k] * wn[p][0],
                            v[p][1][k] * r2[k] * wn[p][1]);
     }
-    if (A.rstd && pair_of_lane<TG>() == 0)
+    if (A.rstd && threadIdx.x % (TG == 2 ? 32 : kWave) == 0 && threadIdx.x < kWave)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (k < at.n) {
-                if (A.h) A.rstd[at.b * A.T + at.t + k] = r1[k];
-                A.rstd[(A.B + at.b) * A.T + at.t + k] = r2[k];
+            if (at.own[k]) {
+                const int64_t t = at.t + at.half * 4 + k;
+                if (kStates) A.rstd[at.b * A.T + t] = r1[k];
+                A.rstd[(A.B + at.b) * A.T + t] = r2[k];
             }
 }
 
 // Backward.  The means of both norms come from one round of sums: with
 // e = gy + r2 q (dx without its mean),
 //     mean(p n1) = scale (mean(w_post n1 e) - r2 mean(q n2) mean(w_post n1 n2)).
-// The workgroup stays, takes every A.groups-th tile of its XCD's range, and
-// keeps its channels' weight gradients in registers.
-template <int WAVES, int TG, int NP>
+// The workgroup stays, takes every (groups / 8)-th tile of its XCD's range, and
+// keeps its channels' weight gradients.
+template <int WAVES, int TG, int NP, bool QUADS, int TYPES>
 __global__ void __launch_bounds__(WAVES * kWave) block_tile_adjoint_kernel(BlockArgs A)
 {
-    constexpr int kPairs = WAVES * kWave / TG;
     __shared__ TileSums<12, TG, WAVES> sums;
-    const bool gb = A.gate_bf16, xb = A.x_bf16, zb = A.z_bf16;
+    // 16 waves leave a lane 128 registers, which the tile's tensors fill.  So
+    // n2 waits for the sums in LDS, and a lane's weights (scale w_post, w_pre)
+    // and their gradients so far live there too.
+    __shared__ float4 n2_lds[NP * 2][WAVES * kWave];
+    __shared__ float4 w_lds[NP][WAVES * kWave], dw_lds[NP][WAVES * kWave];
+    const BlockTypes<TYPES> types(A);
+    const bool gb = types.gate, xb = types.stream, zb = types.normed;
+    constexpr bool kStates = (TYPES & kNoStates) == 0;
+    [[maybe_unused]] const bool has_gate = A.has_gate;
+    const bool has_gy = A.has_gy, has_gz = A.has_gz;
     const float over_d = 1.0f / (float)A.D;
-    const int64_t per = (A.tiles + 7) >> 3, first = (blockIdx.x & 7) * per;
-    float wp[NP][2], wn[NP][2], s_post[NP][2], s_pre[NP][2];
+    const int64_t per = (A.tiles + 7) >> 3, begin = (blockIdx.x & 7) * per;
+    const int64_t end = min(A.tiles, begin + per);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            wp[p][i] = A.h && d + i < A.D ? A.scale * A.w_post[d + i] : 0.0f;
-            wn[p][i] = d + i < A.D ? A.w_pre[d + i] : 0.0f;
-            s_post[p][i] = s_pre[p][i] = 0.0f;
-        }
+        const PairAt<WAVES, TG> c(A, p);
+        float4 w = make_float4(0.0f, 0.0f, A.w_pre[c.d], A.w_pre[c.d + 1]);
+        if constexpr (kStates) w.x = A.scale * A.w_post[c.d], w.y = A.scale * A.w_post[c.d + 1];
+        w_lds[p][threadIdx.x] = w;
+        dw_lds[p][threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    for (int64_t tile = first + (blockIdx.x >> 3); tile < min(A.tiles, first + per);
-         tile += A.groups >> 3) {
-        const TileAt<TG> at(A, tile);
+    for (int64_t tile = begin + (blockIdx.x >> 3); tile < end; tile += A.groups >> 3) {
+        const TileAt<TG, QUADS> at(A, tile);
+        int64_t hk[4], gk[4], xk[4], zk[4];
+        at.steps(A.hst, hk), at.steps(A.gst, gk), at.steps(A.xst, xk), at.steps(A.zst, zk);
         const int64_t ho = at.b * A.hsb + at.t * A.hst, go = at.b * A.gsb + at.t * A.gst;
         const int64_t xo = at.b * A.xsb + at.t * A.xst, zo = at.b * A.zsb + at.t * A.zst;
         Quad h[NP][2], g[NP][2];
         Words2 x[NP][4], gy[NP][4], gz[NP][4];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+            const PairAt<WAVES, TG> c(A, p);
+            const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
+            const uint32_t xoff = c.in_row(A.xst, xb), zoff = c.in_row(A.zst, zb);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int n = d + i < A.D ? at.n : 0;
-                h[p][i] = g[p][i] = Quad{{0u, 0u, 0u, 0u}};
-                if (A.h) h[p][i] = load_quad(A.h, ho + (d + i) * A.hsd, A.hst, n, false);
-                if (A.gate) g[p][i] = load_quad(A.gate, go + (d + i) * A.gsd, A.gst, n, gb);
+                if constexpr (kStates) {
+                    h[p][i] = load_quad<QUADS>(A.h + ho + i * A.hsd, hoff, hk, false);
+                    g[p][i] = load_quad<QUADS>(element_at(A.gate, go + i * A.gsd, gb), goff, gk, gb);
+                }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool in = k < at.n && d < A.D, two = d + 1 < A.D;
-                x[p][k] = gy[p][k] = gz[p][k] = Words2{0u, 0u};
-                if (in) x[p][k] = load_pair(A.x, xo + d + k * A.xst, two, xb);
-                if (in && A.gy) gy[p][k] = load_pair(A.gy, xo + d + k * A.xst, two, xb);
-                if (in && A.gz) gz[p][k] = load_pair(A.gz, zo + d + k * A.zst, two, zb);
+                x[p][k] = load_pair(element_at(A.x, xo + xk[k], xb), xoff, xb);
+                gy[p][k] = load_pair(element_at(A.gy, xo + xk[k], xb), xoff, xb);
+                gz[p][k] = load_pair(element_at(A.gz, zo + zk[k], zb), zoff, zb);
             }
         }
+        // a step that is not the tile's own has no norms, so it adds nothing to
+        // the weight gradients
         float r1[4], r2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            r1[k] = A.h && k < at.n ? A.rstd_in[at.b * A.T + at.t + k] : 0.0f;
-            r2[k] = k < at.n ? A.rstd_in[(A.B + at.b) * A.T + at.t + k] : 0.0f;
+            const int64_t t = at.t + at.half * 4 + at.k_of[k];
+            const float r = kStates ? A.rstd_in[at.b * A.T + t] : 0.0f;
+            const float q = A.rstd_in[(A.B + at.b) * A.T + t];
+            r1[k] = at.own[k] ? r : 0.0f;
+            r2[k] = at.own[k] ? q : 0.0f;
         }
-        float e[NP][4][2], n2[NP][4][2], s[12];
+        float e[NP][4][2], s[12];
 #pragma unroll
         for (int i = 0; i < 12; ++i) s[i] = 0.0f;
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
+        for (int p = 0; p < NP; ++p) {
+            const PairAt<WAVES, TG> c(A, p);
+            const float4 w = w_lds[p][threadIdx.x];
+            float s_pre[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float hv[4], gv[4];
-                quad_values(h[p][i], false, hv);
-                quad_values(g[p][i], gb, gv);
+                const bool counts = i ? c.second : c.first;
+                const float wp = i ? w.y : w.x, wn = i ? w.w : w.z;
+                float n2[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float wn1 = gated_value(hv[k], gv[k], A.gate) * r1[k] * wp[p][i];
-                    const float b = (wn1 + pair_value(x[p][k], i, xb)) * r2[k];
-                    const float z = pair_value(gz[p][k], i, zb), q = z * wn[p][i];
-                    e[p][k][i] = fmaf_(r2[k], q, pair_value(gy[p][k], i, xb));
-                    n2[p][k][i] = b;
-                    s[k] = fmaf_(q, b, s[k]);
-                    s[4 + k] = fmaf_(wn1, e[p][k][i], s[4 + k]);
-                    s[8 + k] = fmaf_(wn1, b, s[8 + k]);
-                    s_pre[p][i] = fmaf_(z, b, s_pre[p][i]);
+                    float n1w = 0.0f;
+                    if constexpr (kStates)
+                        n1w = gated_value(quad_value(h[p][i], k, false), quad_value(g[p][i], k, gb),
+                                          has_gate) * r1[k] * wp;
+                    n2[k] = (n1w + pair_value(x[p][k], i, xb)) * r2[k];
+                    const float z = has_gz ? pair_value(gz[p][k], i, zb) : 0.0f, q = z * wn;
+                    e[p][k][i] = fmaf_(r2[k], q, has_gy ? pair_value(gy[p][k], i, xb) : 0.0f);
+                    s_pre[i] = fmaf_(z, n2[k], s_pre[i]);
+                    s[k] = fmaf_(counts ? q : 0.0f, n2[k], s[k]);
+                    if constexpr (kStates) {
+                        n1w = counts ? n1w : 0.0f;
+                        s[4 + k] = fmaf_(n1w, e[p][k][i], s[4 + k]);
+                        s[8 + k] = fmaf_(n1w, n2[k], s[8 + k]);
+                    }
                 }
+                n2_lds[2 * p + i][threadIdx.x] = make_float4(n2[0], n2[1], n2[2], n2[3]);
             }
+            dw_lds[p][threadIdx.x].z += s_pre[0];
+            dw_lds[p][threadIdx.x].w += s_pre[1];
+        }
         sums.sum(s);
         float m1[4], m2[4];
 #pragma unroll
@@ -579,50 +702,66 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_adjoint_kernel(Block
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) e[p][k][i] = fmaf_(-m2[k], n2[p][k][i], e[p][k][i]);
-                if (k < at.n && d < A.D)
-                    store_pair(A.dx, xo + d + k * A.xst, d + 1 < A.D, xb, e[p][k][0], e[p][k][1]);
-            }
-            if (!A.h) continue;
+            const PairAt<WAVES, TG> c(A, p);
+            const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
+            const uint32_t xoff = c.in_row(A.xst, xb);
+            const float4 w = w_lds[p][threadIdx.x];
+            float s_post[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float hv[4], gv[4], dh[4], dg[4];
-                quad_values(h[p][i], false, hv);
-                quad_values(g[p][i], gb, gv);
+                const float4 n2 = n2_lds[2 * p + i][threadIdx.x];
+                e[p][0][i] = fmaf_(-m2[0], n2.x, e[p][0][i]);
+                e[p][1][i] = fmaf_(-m2[1], n2.y, e[p][1][i]);
+                e[p][2][i] = fmaf_(-m2[2], n2.z, e[p][2][i]);
+                e[p][3][i] = fmaf_(-m2[3], n2.w, e[p][3][i]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (at.all || at.own[k])
+                    store_pair(element_at(A.dx, xo + xk[k], xb), xoff, xb, e[p][k][0], e[p][k][1]);
+            }
+            if constexpr (!kStates) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float dh[4], dg[4];
+                // opaque: the sigmoids are cheaper again than kept since the sums
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[p][i].w[j] = opaque_bits(g[p][i].w[j]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float sg = A.gate ? sigmoid_q(-kLog2e * gv[k]) : 1.0f;
-                    const float act = A.gate ? gv[k] * sg : 1.0f;
-                    const float n1 = hv[k] * act * r1[k], dx = e[p][k][i];
-                    s_post[p][i] = fmaf_(dx, n1, s_post[p][i]);
-                    const float dv = r1[k] * fmaf_(-n1, m1[k], dx * wp[p][i]);
+                    const float hv = quad_value(h[p][i], k, false), gv = quad_value(g[p][i], k, gb);
+                    const float sg = has_gate ? sigmoid_q(-kLog2e * gv) : 1.0f;
+                    const float act = has_gate ? gv * sg : 1.0f;
+                    const float n1 = hv * act * r1[k], dx = e[p][k][i];
+                    s_post[i] = fmaf_(dx, n1, s_post[i]);
+                    const float dv = r1[k] * fmaf_(-n1, m1[k], dx * (i ? w.y : w.x));
                     dh[k] = dv * act;
-                    dg[k] = dv * hv[k] * (sg * fmaf_(gv[k], 1.0f - sg, 1.0f));
+                    dg[k] = dv * hv * (sg * fmaf_(gv, 1.0f - sg, 1.0f));
                 }
-                const int n = d + i < A.D ? at.n : 0;
-                store_quad(A.dh, ho + (d + i) * A.hsd, A.hst, n, false, dh);
-                if (A.gate) store_quad(A.dgate, go + (d + i) * A.gsd, A.gst, n, gb, dg);
+                store_quad<QUADS>(A.dh + ho + i * A.hsd, hoff, hk, at.own, at.all, false, dh);
+                if (has_gate)
+                    store_quad<QUADS>(element_at(A.dgate, go + i * A.gsd, gb), goff, gk, at.own,
+                                      at.all, gb, dg);
             }
+            dw_lds[p][threadIdx.x].x += s_post[0];
+            dw_lds[p][threadIdx.x].y += s_post[1];
         }
     }
     float *part = A.part + (int64_t)blockIdx.x * 2 * A.D;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int64_t d = 2 * (pair_of_lane<TG>() + p * kPairs);
+        const PairAt<WAVES, TG> c(A, p);
+        const float4 dw = dw_lds[p][threadIdx.x];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float a = s_post[p][i], b = s_pre[p][i];
+            float a = i ? dw.y : dw.x, b = i ? dw.w : dw.z;
             if (TG == 2) {  // the halves hold the same channels
                 a += __shfl_xor(a, 32);
                 b += __shfl_xor(b, 32);
             }
-            if ((TG == 1 || threadIdx.x % kWave < 32) && d + i < A.D) {
-                part[d + i] = A.scale * a;
-                part[A.D + d + i] = b;
+            if ((TG == 1 || threadIdx.x % kWave < 32) && (i ? c.second : c.first)) {
+                part[c.d + i] = A.scale * a;
+                part[A.D + c.d + i] = b;
             }
         }
     }
@@ -631,7 +770,7 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_adjoint_kernel(Block
 // dw_post and dw_pre: the workgroups' partial sums, 64 columns a workgroup,
 // its waves each a contiguous run of the rows; a fixed order.
 constexpr int kDwWaves = 8;
-__global__ void __launch_bounds__(kDwWaves * kWave) block_dw_kernel(BlockArgs A)
+static __global__ void __launch_bounds__(kDwWaves * kWave) block_dw_kernel(BlockArgs A)
 {
     __shared__ float lds[kDwWaves][kWave];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;

@@ -1,0 +1,49 @@
+// Launchers of the block boundary's register kernels, one set per combination
+// of types, each in its own translation unit (inst_block_*.hip) so that they
+// compile in parallel.
+#pragma once
+
+#include "block.hpp"
+
+namespace pararnn {
+
+// (waves, groups of 4 steps, channel pairs a lane, steps loaded 4 at a time)
+#define PARARNN_BLOCK_TILINGS(X)                                                                 \
+    X(1, 1, 1, true) X(4, 1, 1, true) X(8, 1, 1, true) X(16, 1, 1, true) X(16, 1, 2, true)       \
+    X(2, 2, 1, true) X(4, 2, 1, true) X(8, 2, 1, true) X(16, 2, 1, true) X(16, 2, 2, true)       \
+    X(1, 1, 1, false) X(4, 1, 1, false) X(8, 1, 1, false) X(16, 1, 1, false) X(16, 1, 2, false)
+inline int tiling_code(int waves, int groups, int pairs, bool quads)
+{
+    return waves * 1000 + groups * 100 + pairs * 10 + quads;
+}
+
+#define PARARNN_BLOCK_LAUNCHER(NAME)                                                             \
+    hipError_t launch_block_##NAME(bool adjoint, int tiling, dim3 grid, dim3 block,              \
+                                   hipStream_t st, const BlockArgs &A)
+PARARNN_BLOCK_LAUNCHER(f32);
+PARARNN_BLOCK_LAUNCHER(gate);
+PARARNN_BLOCK_LAUNCHER(stream);
+PARARNN_BLOCK_LAUNCHER(bf16);
+PARARNN_BLOCK_LAUNCHER(args);
+PARARNN_BLOCK_LAUNCHER(norm);
+
+#define PARARNN_TILING_CASE(W, G, P, Q)                                                             \
+    case W * 1000 + G * 100 + P * 10 + Q:                                                                   \
+        if (adjoint)                                                                             \
+            hipLaunchKernelGGL((block_tile_adjoint_kernel<W, G, P, Q, kTypes>), grid, block, 0, st,  \
+                               A);                                                               \
+        else                                                                                     \
+            hipLaunchKernelGGL((block_tile_kernel<W, G, P, Q, kTypes>), grid, block, 0, st, A);     \
+        break;
+#define PARARNN_DEFINE_BLOCK_LAUNCHER(NAME, TYPES)                                               \
+    PARARNN_BLOCK_LAUNCHER(NAME)                                                                 \
+    {                                                                                            \
+        constexpr int kTypes = TYPES;                                                            \
+        switch (tiling) {                                                                        \
+            PARARNN_BLOCK_TILINGS(PARARNN_TILING_CASE)                                           \
+        default: return hipErrorInvalidValue;                                                    \
+        }                                                                                        \
+        return hipGetLastError();                                                                \
+    }
+
+}  // namespace pararnn

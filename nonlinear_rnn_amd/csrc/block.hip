@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <iterator>
 
 #include "block_launch.hpp"
 #include "host.hpp"
@@ -21,6 +22,7 @@ struct Tiling {
 };
 #define PARARNN_TILING_ENTRY(W, G, P, Q) {W, G, P, Q},
 constexpr Tiling kTilings[] = {PARARNN_BLOCK_TILINGS(PARARNN_TILING_ENTRY)};
+constexpr Tiling kAdjointTilings[] = {PARARNN_BLOCK_ADJOINT_TILINGS(PARARNN_TILING_ENTRY)};
 constexpr int64_t kStripSteps = 4, kStripGroups = 2 * kComputeUnits;
 
 // The narrowest tiling that holds D channels: 4 contiguous steps a load where
@@ -30,7 +32,7 @@ struct BlockPlan {
     Tiling t = {0, 0, 0, false};
     int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)
 };
-BlockPlan block_plan(const pararnn_block_shape_t *sh)
+BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint)
 {
     BlockPlan pl;
     const bool quads = sh->h_stride_t == 1 && sh->g_stride_t == 1 && sh->T >= 4;
@@ -40,17 +42,23 @@ BlockPlan block_plan(const pararnn_block_shape_t *sh)
     const bool near = sh->D >= 2 && sh->h_stride_d <= reach / sh->D &&
                       sh->g_stride_d <= reach / sh->D && sh->x_stride_t <= reach / 8 &&
                       sh->z_stride_t <= reach / 8;
-    for (const Tiling &t : kTilings)
+    const Tiling *list = adjoint ? kAdjointTilings : kTilings;
+    const size_t count = adjoint ? std::size(kAdjointTilings) : std::size(kTilings);
+    for (size_t i = 0; i < count; ++i) {
+        const Tiling &t = list[i];
         if (near && t.channels() >= sh->D && t.quads == quads && (t.groups == 2) <= many &&
             (!pl.t.waves || t.groups > pl.t.groups ||
              (t.groups == pl.t.groups && t.channels() < pl.t.channels())))
             pl.t = t;
+    }
     const int64_t steps = pl.t.waves ? 4 * pl.t.groups : kStripSteps;
     pl.tiles_per_row = (sh->T + steps - 1) / steps;
     pl.tiles = sh->B * pl.tiles_per_row;
     // resident workgroups, 16 waves a CU; a multiple of the 8 XCDs
     const int64_t fit = pl.t.waves ? 16 / pl.t.waves * kComputeUnits : kStripGroups;
-    pl.groups = std::min((pl.tiles + 7) / 8 * 8, fit);
+    // and as few as take the same number of tiles each
+    const int64_t rounds = (pl.tiles + fit - 1) / fit;
+    if (rounds > 0) pl.groups = std::min(((pl.tiles + rounds - 1) / rounds + 7) / 8 * 8, fit);
     return pl;
 }
 
@@ -168,7 +176,7 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
     if (!std::isfinite(scale) || !(eps > 0.0f) || std::isinf(eps)) return PARARNN_ERR_INVALID;
     if (shape->B == 0 || shape->T == 0 || shape->D == 0) return PARARNN_OK;
     if (!x || !w_pre || !z || (h && (!w_post || !y)) || (!h && gate)) return PARARNN_ERR_INVALID;
-    const BlockPlan pl = block_plan(shape);
+    const BlockPlan pl = block_plan(shape, false);
     if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);
@@ -192,7 +200,7 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
 size_t pararnn_block_workspace_bytes(const pararnn_block_shape_t *shape)
 {
     if (check_block(shape) != PARARNN_OK) return 0;
-    return align_up((size_t)block_plan(shape).groups * 2 * shape->D * sizeof(float));
+    return align_up((size_t)block_plan(shape, true).groups * 2 * shape->D * sizeof(float));
 }
 
 pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, const float *h,
@@ -216,7 +224,7 @@ pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, 
         return PARARNN_ERR_INVALID;
     const size_t need = pararnn_block_workspace_bytes(shape);
     if (work && (!ws || ws_bytes < need || !aligned16(ws))) return PARARNN_ERR_WORKSPACE;
-    const BlockPlan pl = block_plan(shape);
+    const BlockPlan pl = block_plan(shape, true);
     if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);

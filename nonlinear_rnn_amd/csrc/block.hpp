@@ -399,6 +399,10 @@ struct TileSums {
     {
         const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
         const int group = TG == 2 ? lane / 32 : 0;
+        // opaque: else the compiler sinks the sums' products below the stores
+        // here, one sum's after another's, and keeps all their factors
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = opaque(v[i]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float x = v[i];
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
 // The workgroup stays, takes every (groups / 8)-th tile of its XCD's range, and
 // keeps its channels' weight gradients.
 template <int WAVES, int TG, int NP, bool QUADS, int TYPES>
-__global__ void __launch_bounds__(WAVES * kWave) block_tile_adjoint_kernel(BlockArgs A)
+__global__ void __launch_bounds__(WAVES * kWave, 4) block_tile_adjoint_kernel(BlockArgs A)
 {
     __shared__ TileSums<12, TG, WAVES> sums;
     // 16 waves leave a lane 128 registers, which the tile's tensors fill.  So
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_adjoint_kernel(Block
                 float dh[4], dg[4];
                 // opaque: the sigmoids are cheaper again than kept since the sums
 #pragma unroll
-                for (int j = 0; j < 4; ++j) g[p][i].w[j] = opaque_bits(g[p][i].w[j]);
+                for (int j = 0; j < (gb ? 2 : 4); ++j) g[p][i].w[j] = opaque_bits(g[p][i].w[j]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float hv = quad_value(h[p][i], k, false), gv = quad_value(g[p][i], k, gb);

@@ -12,6 +12,10 @@ namespace pararnn {
     X(1, 1, 1, true) X(4, 1, 1, true) X(8, 1, 1, true) X(16, 1, 1, true) X(16, 1, 2, true)       \
     X(2, 2, 1, true) X(4, 2, 1, true) X(8, 2, 1, true) X(16, 2, 1, true) X(16, 2, 2, true)       \
     X(1, 1, 1, false) X(4, 1, 1, false) X(8, 1, 1, false) X(16, 1, 1, false) X(16, 1, 2, false)
+#define PARARNN_BLOCK_ADJOINT_TILINGS(X)                                                         \
+    X(1, 1, 1, true) X(2, 1, 2, true) X(4, 1, 2, true) X(8, 1, 2, true) X(16, 1, 2, true)        \
+    X(2, 2, 1, true) X(2, 2, 2, true) X(4, 2, 2, true) X(8, 2, 2, true) X(16, 2, 2, true)        \
+    X(1, 1, 1, false) X(2, 1, 2, false) X(4, 1, 2, false) X(8, 1, 2, false) X(16, 1, 2, false)
 inline int tiling_code(int waves, int groups, int pairs, bool quads)
 {
     return waves * 1000 + groups * 100 + pairs * 10 + quads;
@@ -27,21 +31,29 @@ PARARNN_BLOCK_LAUNCHER(bf16);
 PARARNN_BLOCK_LAUNCHER(args);
 PARARNN_BLOCK_LAUNCHER(norm);
 
-#define PARARNN_TILING_CASE(W, G, P, Q)                                                             \
-    case W * 1000 + G * 100 + P * 10 + Q:                                                                   \
-        if (adjoint)                                                                             \
-            hipLaunchKernelGGL((block_tile_adjoint_kernel<W, G, P, Q, kTypes>), grid, block, 0, st,  \
-                               A);                                                               \
-        else                                                                                     \
-            hipLaunchKernelGGL((block_tile_kernel<W, G, P, Q, kTypes>), grid, block, 0, st, A);     \
+#define PARARNN_TILING_CASE(W, G, P, Q)                                                          \
+    case W * 1000 + G * 100 + P * 10 + Q:                                                        \
+        hipLaunchKernelGGL((block_tile_kernel<W, G, P, Q, kTypes>), grid, block, 0, st, A);      \
+        break;
+#define PARARNN_ADJOINT_TILING_CASE(W, G, P, Q)                                                  \
+    case W * 1000 + G * 100 + P * 10 + Q:                                                        \
+        hipLaunchKernelGGL((block_tile_adjoint_kernel<W, G, P, Q, kTypes>), grid, block, 0, st,  \
+                           A);                                                                   \
         break;
 #define PARARNN_DEFINE_BLOCK_LAUNCHER(NAME, TYPES)                                               \
     PARARNN_BLOCK_LAUNCHER(NAME)                                                                 \
     {                                                                                            \
         constexpr int kTypes = TYPES;                                                            \
-        switch (tiling) {                                                                        \
-            PARARNN_BLOCK_TILINGS(PARARNN_TILING_CASE)                                           \
-        default: return hipErrorInvalidValue;                                                    \
+        if (adjoint) {                                                                           \
+            switch (tiling) {                                                                    \
+                PARARNN_BLOCK_ADJOINT_TILINGS(PARARNN_ADJOINT_TILING_CASE)                       \
+            default: return hipErrorInvalidValue;                                                \
+            }                                                                                    \
+        } else {                                                                                 \
+            switch (tiling) {                                                                    \
+                PARARNN_BLOCK_TILINGS(PARARNN_TILING_CASE)                                       \
+            default: return hipErrorInvalidValue;                                                \
+            }                                                                                    \
         }                                                                                        \
         return hipGetLastError();                                                                \
     }

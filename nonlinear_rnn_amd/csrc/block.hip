@@ -25,9 +25,9 @@ constexpr Tiling kTilings[] = {PARARNN_BLOCK_TILINGS(PARARNN_TILING_ENTRY)};
 constexpr Tiling kAdjointTilings[] = {PARARNN_BLOCK_ADJOINT_TILINGS(PARARNN_TILING_ENTRY)};
 constexpr int64_t kStripSteps = 4, kStripGroups = 2 * kComputeUnits;
 
-// The narrowest tiling that holds D channels: 4 contiguous steps a load where
-// the planes have them, and then 8 steps a tile if there are tiles enough for
-// two workgroups a CU.  No waves: the strip kernels.
+// The tiling that holds D channels with the most steps a tile that still
+// makes two tiles a CU, and of those the narrowest; single steps where the
+// planes' steps are not contiguous.  No waves: the strip kernels.
 struct BlockPlan {
     Tiling t = {0, 0, 0, false};
     int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)
@@ -36,19 +36,20 @@ BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint)
 {
     BlockPlan pl;
     const bool quads = sh->h_stride_t == 1 && sh->g_stride_t == 1 && sh->T >= 4;
-    const bool many = quads && sh->T >= 8 && sh->B * ((sh->T + 7) / 8) >= 2 * kComputeUnits;
     // a lane's offset from the tile's base is 32 bits of bytes
     const int64_t reach = (int64_t(1) << 29) - 8;
     const bool near = sh->D >= 2 && sh->h_stride_d <= reach / sh->D &&
-                      sh->g_stride_d <= reach / sh->D && sh->x_stride_t <= reach / 8 &&
-                      sh->z_stride_t <= reach / 8;
+                      sh->g_stride_d <= reach / sh->D && sh->x_stride_t <= reach / 16 &&
+                      sh->z_stride_t <= reach / 16;
     const Tiling *list = adjoint ? kAdjointTilings : kTilings;
     const size_t count = adjoint ? std::size(kAdjointTilings) : std::size(kTilings);
     for (size_t i = 0; i < count; ++i) {
         const Tiling &t = list[i];
-        if (near && t.channels() >= sh->D && t.quads == quads && (t.groups == 2) <= many &&
-            (!pl.t.waves || t.groups > pl.t.groups ||
-             (t.groups == pl.t.groups && t.channels() < pl.t.channels())))
+        const int64_t steps = 4 * t.groups;
+        if (!near || t.channels() < sh->D || t.quads != quads) continue;
+        if (t.groups > 1 && (sh->T < steps || sh->B * (sh->T / steps) < 2 * kComputeUnits)) continue;
+        if (!pl.t.waves || t.groups > pl.t.groups ||
+            (t.groups == pl.t.groups && t.channels() < pl.t.channels()))
             pl.t = t;
     }
     const int64_t steps = pl.t.waves ? 4 * pl.t.groups : kStripSteps;

@@ -240,10 +240,9 @@ __global__ void __launch_bounds__(kBlockThreads) block_strip_adjoint_kernel(Bloc
 // Up to 4096 channels: a workgroup keeps its tile of 4 TG steps in registers
 // from the first load to the last store, so that every tensor is read once.
 // A lane owns pairs of channels (NP pairs, the workgroup's pairs apart) and 4
-// steps.  Channel-major loads are 16 bytes (8 in bf16) along its steps, time-
-// major ones two channels wide, a wave (or, TG = 2, either half of it) running
-// along the channels.  Lanes of a half wave share steps, so a sum over the
-// channels is a DPP reduction, then one across waves through LDS.
+// steps; TG neighbouring lanes own the same pairs and 4 steps each.  Channel-
+// major loads are 16 bytes (8 in bf16) along a lane's steps, 16 TG together;
+// time-major ones two channels wide, 64 / TG pairs of a step together.
 //
 // No load is conditional: a lane past the last channel reads the last pair
 // again, is left out of the sums, and stores what that pair's lane stores; a
@@ -389,16 +388,16 @@ __device__ __forceinline__ void store_pair(void *row, uint32_t off, bool bf16, f
         store_at<Words2Any>(row, off, Words2{__float_as_uint(a), __float_as_uint(b)});
 }
 
-// Sums of N values a lane over the lanes that share its steps: the whole
-// workgroup (TG = 1) or the halves of every wave (TG = 2).
+// Sums of N values a lane over the lanes that share its steps (every TG-th
+// lane of the workgroup).  Each row of 16 lanes by DPP, then a wave for each
+// sum over the workgroup's rows, through LDS.
 template <int N, int TG, int WAVES>
 struct TileSums {
-    float part[N * TG][16];
+    float part[N * TG][WAVES * 4];
     float total[TG][(N + 3) / 4 * 4];
     __device__ __forceinline__ void sum(float (&v)[N])
     {
-        const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-        const int group = TG == 2 ? lane / 32 : 0;
+        const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, group = threadIdx.x % TG;
         // opaque: else the compiler sinks the sums' products below the stores
         // here, one sum's after another's, and keeps all their factors
 #pragma unroll
@@ -406,23 +405,16 @@ struct TileSums {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float x = v[i];
-            x += dppf<0x111>(0.0f, x);
-            x += dppf<0x112>(0.0f, x);
+            if constexpr (TG == 1) x += dppf<0x111>(0.0f, x);
+            if constexpr (TG <= 2) x += dppf<0x112>(0.0f, x);
             x += dppf<0x114>(0.0f, x);
             x += dppf<0x118>(0.0f, x);
-            x += dppf<0x142, 0xA>(0.0f, x);
-            if constexpr (TG == 1) x += dppf<0x143, 0xC>(0.0f, x);
-            if (lane % (kWave / TG) == kWave / TG - 1) part[i * TG + group][wave] = x;
+            if (lane % 16 >= 16 - TG) part[i * TG + group][threadIdx.x / 16] = x;
         }
         __syncthreads();
-        for (int r = threadIdx.x / 16; r < N * TG; r += WAVES * kWave / 16) {
-            const int w = threadIdx.x % 16;
-            float x = w < WAVES ? part[r][w] : 0.0f;
-            x += dppf<0x111>(0.0f, x);
-            x += dppf<0x112>(0.0f, x);
-            x += dppf<0x114>(0.0f, x);
-            x += dppf<0x118>(0.0f, x);
-            if (w == 15) total[r % TG][r / TG] = x;
+        for (int r = wave; r < N * TG; r += WAVES) {
+            const float x = wave_sum_to_last(lane < WAVES * 4 ? part[r][lane] : 0.0f);
+            if (lane == kWave - 1) total[r % TG][r / TG] = x;
         }
         __syncthreads();
 #pragma unroll
@@ -434,8 +426,8 @@ struct TileSums {
 template <int TG, bool QUADS>
 struct TileAt {
     int64_t b, t;
-    int half;              // TG = 2: the lane's 4 of the tile's 8 steps
-    int64_t k_of[4];       // offset from t of step k (of half 0 where QUADS)
+    int group;             // the lane's 4 of the tile's steps
+    int64_t k_of[4];       // offset from t of step k (of group 0 where QUADS)
     bool own[4], all;
     __device__ __forceinline__ TileAt(const BlockArgs &A, int64_t tile)
     {
@@ -447,12 +439,12 @@ struct TileAt {
         b = row;
         const int64_t want = (tile - b * A.tiles_per_row) * TT;
         t = QUADS ? min(want, A.T - TT) : want;
-        half = TG == 2 ? (int)(threadIdx.x % kWave / 32) : 0;
+        group = TG > 1 ? (int)(threadIdx.x % TG) : 0;
         all = true;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             k_of[k] = QUADS ? k : min((int64_t)k, A.T - 1 - t);
-            own[k] = QUADS ? t + half * kTileSteps + k >= want : t + k < A.T;
+            own[k] = QUADS ? t + group * kTileSteps + k >= want : t + k < A.T;
             all = all && own[k];
         }
     }
@@ -467,15 +459,14 @@ struct TileAt {
 // odd number stands alone, the pair is (D - 2, D - 1).
 template <int WAVES, int TG>
 struct PairAt {
-    uint32_t d, half;
+    uint32_t d, group;
     bool first, second;  // which of its channels no other lane has
     __device__ __forceinline__ PairAt(const BlockArgs &A, int p)
     {
         // opaque: what follows from it is cheaper again than kept over a tile
         const uint32_t thread = opaque_bits(threadIdx.x);
-        const uint32_t lane = TG == 2 ? thread / kWave * 32 + thread % 32 : thread;
-        const uint32_t D = (uint32_t)A.D, want = 2u * (lane + p * (WAVES * kWave / TG));
-        half = TG == 2 ? thread % kWave / 32 : 0u;
+        const uint32_t D = (uint32_t)A.D, want = 2u * (thread / TG + p * (WAVES * kWave / TG));
+        group = thread % TG;
         d = min(want, D - 2);
         first = want + 1 < D;
         second = want < D;
@@ -483,11 +474,11 @@ struct PairAt {
     // Byte offsets from the tile's base.
     __device__ __forceinline__ uint32_t in_plane(int64_t stride_d, bool bf16) const
     {
-        return (d * (uint32_t)stride_d + kTileSteps * half) << (bf16 ? 1 : 2);
+        return (d * (uint32_t)stride_d + kTileSteps * group) << (bf16 ? 1 : 2);
     }
     __device__ __forceinline__ uint32_t in_row(int64_t stride_t, bool bf16) const
     {
-        return (d + half * kTileSteps * (uint32_t)stride_t) << (bf16 ? 1 : 2);
+        return (d + group * kTileSteps * (uint32_t)stride_t) << (bf16 ? 1 : 2);
     }
 };
 
@@ -584,11 +575,11 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
                 store_pair(element_at(A.z, zo + zk[k], zb), zoff, zb, v[p][0][k] * r2[k] * wn[p][0],
                            v[p][1][k] * r2[k] * wn[p][1]);
     }
-    if (A.rstd && threadIdx.x % (TG == 2 ? 32 : kWave) == 0 && threadIdx.x < kWave)
+    if (A.rstd && threadIdx.x < TG)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (at.own[k]) {
-                const int64_t t = at.t + at.half * 4 + k;
+                const int64_t t = at.t + at.group * 4 + k;
                 if (kStates) A.rstd[at.b * A.T + t] = r1[k];
                 A.rstd[(A.B + at.b) * A.T + t] = r2[k];
             }
@@ -656,7 +647,7 @@ __global__ void __launch_bounds__(WAVES * kWave, 4) block_tile_adjoint_kernel(Bl
         float r1[4], r2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int64_t t = at.t + at.half * 4 + at.k_of[k];
+            const int64_t t = at.t + at.group * 4 + at.k_of[k];
             const float r = kStates ? A.rstd_in[at.b * A.T + t] : 0.0f;
             const float q = A.rstd_in[(A.B + at.b) * A.T + t];
             r1[k] = at.own[k] ? r : 0.0f;
@@ -759,11 +750,12 @@ __global__ void __launch_bounds__(WAVES * kWave, 4) block_tile_adjoint_kernel(Bl
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float a = i ? dw.y : dw.x, b = i ? dw.w : dw.z;
-            if (TG == 2) {  // the halves hold the same channels
-                a += __shfl_xor(a, 32);
-                b += __shfl_xor(b, 32);
+#pragma unroll
+            for (int o = 1; o < TG; o *= 2) {  // the groups hold the same channels
+                a += __shfl_xor(a, o);
+                b += __shfl_xor(b, o);
             }
-            if ((TG == 1 || threadIdx.x % kWave < 32) && (i ? c.second : c.first)) {
+            if (threadIdx.x % TG == 0 && (i ? c.second : c.first)) {
                 part[c.d + i] = A.scale * a;
                 part[A.D + c.d + i] = b;
             }

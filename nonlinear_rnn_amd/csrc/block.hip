@@ -55,8 +55,8 @@ BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint)
     const int64_t steps = pl.t.waves ? 4 * pl.t.groups : kStripSteps;
     pl.tiles_per_row = (sh->T + steps - 1) / steps;
     pl.tiles = sh->B * pl.tiles_per_row;
-    // resident workgroups, 16 waves a CU; a multiple of the 8 XCDs
-    const int64_t fit = pl.t.waves ? 16 / pl.t.waves * kComputeUnits : kStripGroups;
+    // resident workgroups, 8 waves a CU; a multiple of the 8 XCDs
+    const int64_t fit = pl.t.waves ? 8 / std::min(8, pl.t.waves) * kComputeUnits : kStripGroups;
     // and as few as take the same number of tiles each
     const int64_t rounds = (pl.tiles + fit - 1) / fit;
     if (rounds > 0) pl.groups = std::min(((pl.tiles + rounds - 1) / rounds + 7) / 8 * 8, fit);

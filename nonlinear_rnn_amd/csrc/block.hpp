@@ -293,6 +293,20 @@ __device__ __forceinline__ T load_at(const void *base, uint32_t bytes)
     asm("" : "+s"(a));
     return *(const PARARNN_GLOBAL T *)((const PARARNN_GLOBAL char *)a + bytes);
 }
+template <class T>
+__device__ __forceinline__ T load_once(const void *base, uint32_t bytes)
+{
+    uint64_t a = reinterpret_cast<uint64_t>(base);
+    asm("" : "+s"(a));
+    return __builtin_nontemporal_load((const PARARNN_GLOBAL T *)((const PARARNN_GLOBAL char *)a + bytes));
+}
+template <class T, class V>
+__device__ __forceinline__ void store_once(void *base, uint32_t bytes, V v)
+{
+    uint64_t a = reinterpret_cast<uint64_t>(base);
+    asm("" : "+s"(a), "+v"(bytes));
+    __builtin_nontemporal_store((T)v, (PARARNN_GLOBAL T *)((PARARNN_GLOBAL char *)a + bytes));
+}
 template <class T, class V>
 __device__ __forceinline__ void store_at(void *base, uint32_t bytes, V v)
 {
@@ -369,11 +383,21 @@ __device__ __forceinline__ void store_quad(void *row, uint32_t off, const int64_
         }
     }
 }
-// Two neighbouring channels of a step.
-__device__ __forceinline__ Words2 load_pair(const void *row, uint32_t off, bool bf16)
+// Two neighbouring channels of a step.  The stream goes past the L2's other
+// contents (non-temporal), unless it is read again (`kept`): the lines of the
+// channel-major planes have to stay there until all tiles that share one have
+// read or written their part.  B=8 T=4096 D=1024: forward 136 -> 123 us,
+// backward 279 -> 269; with the planes themselves non-temporal the backward
+// takes twice as long.
+__device__ __forceinline__ Words2 load_pair(const void *row, uint32_t off, bool bf16,
+                                            bool kept = false)
 {
-    if (bf16) return Words2{load_at<Word1Any>(row, off), 0u};
-    return load_at<Words2Any>(row, off);
+    if (kept) {
+        if (bf16) return Words2{load_at<Word1Any>(row, off), 0u};
+        return load_at<Words2Any>(row, off);
+    }
+    if (bf16) return Words2{load_once<Word1Any>(row, off), 0u};
+    return load_once<Words2Any>(row, off);
 }
 __device__ __forceinline__ float pair_value(Words2 w, int i, bool bf16)
 {
@@ -383,9 +407,9 @@ __device__ __forceinline__ float pair_value(Words2 w, int i, bool bf16)
 __device__ __forceinline__ void store_pair(void *row, uint32_t off, bool bf16, float a, float b)
 {
     if (bf16)
-        store_at<Word1Any>(row, off, bf16_bits(a) | bf16_bits(b) << 16);
+        store_once<Word1Any>(row, off, bf16_bits(a) | bf16_bits(b) << 16);
     else
-        store_at<Words2Any>(row, off, Words2{__float_as_uint(a), __float_as_uint(b)});
+        store_once<Words2Any>(row, off, Words2{__float_as_uint(a), __float_as_uint(b)});
 }
 
 // Sums of N values a lane over the lanes that share its steps (every TG-th
@@ -589,16 +613,21 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
 // e = gy + r2 q (dx without its mean),
 //     mean(p n1) = scale (mean(w_post n1 e) - r2 mean(q n2) mean(w_post n1 n2)).
 // The workgroup stays, takes every (groups / 8)-th tile of its XCD's range, and
-// keeps its channels' weight gradients.
+// keeps its channels' weight gradients.  The states and the gate stay in
+// registers between the sums and the results, e waits in LDS, and x is read
+// again (just read, and in long runs).  The channel pairs follow one another,
+// the next one's loads issued before the current one is computed.
+template <bool STATES>
+struct StreamPair {
+    Words2 x[4], gy[4], gz[4];
+    float wp[2], wn[2];
+};
+
 template <int WAVES, int TG, int NP, bool QUADS, int TYPES>
-__global__ void __launch_bounds__(WAVES * kWave, 4) block_tile_adjoint_kernel(BlockArgs A)
+__global__ void __launch_bounds__(WAVES * kWave, 2) block_tile_adjoint_kernel(BlockArgs A)
 {
     __shared__ TileSums<12, TG, WAVES> sums;
-    // 16 waves leave a lane 128 registers, which the tile's tensors fill.  So
-    // n2 waits for the sums in LDS, and a lane's weights (scale w_post, w_pre)
-    // and their gradients so far live there too.
-    __shared__ float4 n2_lds[NP * 2][WAVES * kWave];
-    __shared__ float4 w_lds[NP][WAVES * kWave], dw_lds[NP][WAVES * kWave];
+    __shared__ float4 e_lds[NP * 2][WAVES * kWave];
     const BlockTypes<TYPES> types(A);
     const bool gb = types.gate, xb = types.stream, zb = types.normed;
     constexpr bool kStates = (TYPES & kNoStates) == 0;
@@ -607,149 +636,168 @@ __global__ void __launch_bounds__(WAVES * kWave, 4) block_tile_adjoint_kernel(Bl
     const float over_d = 1.0f / (float)A.D;
     const int64_t per = (A.tiles + 7) >> 3, begin = (blockIdx.x & 7) * per;
     const int64_t end = min(A.tiles, begin + per);
+    float s_post[NP][2], s_pre[NP][2];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const PairAt<WAVES, TG> c(A, p);
-        float4 w = make_float4(0.0f, 0.0f, A.w_pre[c.d], A.w_pre[c.d + 1]);
-        if constexpr (kStates) w.x = A.scale * A.w_post[c.d], w.y = A.scale * A.w_post[c.d + 1];
-        w_lds[p][threadIdx.x] = w;
-        dw_lds[p][threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
+    for (int p = 0; p < NP; ++p) s_post[p][0] = s_post[p][1] = s_pre[p][0] = s_pre[p][1] = 0.0f;
+
     for (int64_t tile = begin + (blockIdx.x >> 3); tile < end; tile += A.groups >> 3) {
         const TileAt<TG, QUADS> at(A, tile);
         int64_t hk[4], gk[4], xk[4], zk[4];
         at.steps(A.hst, hk), at.steps(A.gst, gk), at.steps(A.xst, xk), at.steps(A.zst, zk);
         const int64_t ho = at.b * A.hsb + at.t * A.hst, go = at.b * A.gsb + at.t * A.gst;
         const int64_t xo = at.b * A.xsb + at.t * A.xst, zo = at.b * A.zsb + at.t * A.zst;
-        Quad h[NP][2], g[NP][2];
-        Words2 x[NP][4], gy[NP][4], gz[NP][4];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
+        const auto load_stream = [&](int p, bool again) {
             const PairAt<WAVES, TG> c(A, p);
-            const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
             const uint32_t xoff = c.in_row(A.xst, xb), zoff = c.in_row(A.zst, zb);
+            StreamPair<kStates> v;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if constexpr (kStates) {
+            for (int k = 0; k < 4; ++k) {
+                v.x[k] = load_pair(element_at(A.x, xo + xk[k], xb), xoff, xb, !again);
+                if (again) continue;
+                v.gy[k] = load_pair(element_at(A.gy, xo + xk[k], xb), xoff, xb);
+                v.gz[k] = load_pair(element_at(A.gz, zo + zk[k], zb), zoff, zb);
+            }
+            if (!again) {
+                const Words2 w = load_at<Words2Any>(A.w_pre, c.d * 4);
+                v.wn[0] = __uint_as_float(w.x), v.wn[1] = __uint_as_float(w.y);
+            }
+            if constexpr (kStates) {
+                const Words2 w = load_at<Words2Any>(A.w_post, c.d * 4);
+                v.wp[0] = __uint_as_float(w.x), v.wp[1] = __uint_as_float(w.y);
+            }
+            return v;
+        };
+        Quad h[NP][2], g[NP][2];
+        if constexpr (kStates)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const PairAt<WAVES, TG> c(A, p);
+                const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     h[p][i] = load_quad<QUADS>(A.h + ho + i * A.hsd, hoff, hk, false);
                     g[p][i] = load_quad<QUADS>(element_at(A.gate, go + i * A.gsd, gb), goff, gk, gb);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[p][k] = load_pair(element_at(A.x, xo + xk[k], xb), xoff, xb);
-                gy[p][k] = load_pair(element_at(A.gy, xo + xk[k], xb), xoff, xb);
-                gz[p][k] = load_pair(element_at(A.gz, zo + zk[k], zb), zoff, zb);
-            }
-        }
         // a step that is not the tile's own has no norms, so it adds nothing to
         // the weight gradients
         float r1[4], r2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int64_t t = at.t + at.group * 4 + at.k_of[k];
+            const int64_t t = at.t + at.group * kTileSteps + at.k_of[k];
             const float r = kStates ? A.rstd_in[at.b * A.T + t] : 0.0f;
             const float q = A.rstd_in[(A.B + at.b) * A.T + t];
             r1[k] = at.own[k] ? r : 0.0f;
             r2[k] = at.own[k] ? q : 0.0f;
         }
-        float e[NP][4][2], s[12];
+        float s[12];
 #pragma unroll
         for (int i = 0; i < 12; ++i) s[i] = 0.0f;
+        StreamPair<kStates> now = load_stream(0, false);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
+            StreamPair<kStates> next;
+            if (p + 1 < NP) next = load_stream(p + 1, false);
+            __builtin_amdgcn_sched_barrier(0);
             const PairAt<WAVES, TG> c(A, p);
-            const float4 w = w_lds[p][threadIdx.x];
-            float s_pre[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool counts = i ? c.second : c.first;
-                const float wp = i ? w.y : w.x, wn = i ? w.w : w.z;
-                float n2[4];
+                const float wp = kStates ? A.scale * now.wp[i] : 0.0f;
+                float e[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float n1w = 0.0f;
                     if constexpr (kStates)
                         n1w = gated_value(quad_value(h[p][i], k, false), quad_value(g[p][i], k, gb),
                                           has_gate) * r1[k] * wp;
-                    n2[k] = (n1w + pair_value(x[p][k], i, xb)) * r2[k];
-                    const float z = has_gz ? pair_value(gz[p][k], i, zb) : 0.0f, q = z * wn;
-                    e[p][k][i] = fmaf_(r2[k], q, has_gy ? pair_value(gy[p][k], i, xb) : 0.0f);
-                    s_pre[i] = fmaf_(z, n2[k], s_pre[i]);
-                    s[k] = fmaf_(counts ? q : 0.0f, n2[k], s[k]);
+                    const float n2 = (n1w + pair_value(now.x[k], i, xb)) * r2[k];
+                    const float z = has_gz ? pair_value(now.gz[k], i, zb) : 0.0f, q = z * now.wn[i];
+                    e[k] = fmaf_(r2[k], q, has_gy ? pair_value(now.gy[k], i, xb) : 0.0f);
+                    s_pre[p][i] = fmaf_(z, n2, s_pre[p][i]);
+                    s[k] = fmaf_(counts ? q : 0.0f, n2, s[k]);
                     if constexpr (kStates) {
                         n1w = counts ? n1w : 0.0f;
-                        s[4 + k] = fmaf_(n1w, e[p][k][i], s[4 + k]);
-                        s[8 + k] = fmaf_(n1w, n2[k], s[8 + k]);
+                        s[4 + k] = fmaf_(n1w, e[k], s[4 + k]);
+                        s[8 + k] = fmaf_(n1w, n2, s[8 + k]);
                     }
                 }
-                n2_lds[2 * p + i][threadIdx.x] = make_float4(n2[0], n2[1], n2[2], n2[3]);
+                e_lds[2 * p + i][threadIdx.x] = make_float4(e[0], e[1], e[2], e[3]);
             }
-            dw_lds[p][threadIdx.x].z += s_pre[0];
-            dw_lds[p][threadIdx.x].w += s_pre[1];
+            // opaque: else the sums' products sink below the next pair, and
+            // their factors are kept
+#pragma unroll
+            for (int i = 0; i < 12; ++i) s[i] = opaque(s[i]);
+            s_pre[p][0] = opaque(s_pre[p][0]), s_pre[p][1] = opaque(s_pre[p][1]);
+            now = next;
         }
+        now = load_stream(0, true);
         sums.sum(s);
         float m1[4], m2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            m2[k] = r2[k] * (s[k] * over_d);
-            m1[k] = over_d * fmaf_(-m2[k], s[8 + k], s[4 + k]);
+            m2[k] = r2[k] * r2[k] * (s[k] * over_d);
+            m1[k] = over_d * fmaf_(-r2[k] * (s[k] * over_d), s[8 + k], s[4 + k]);
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
+            StreamPair<kStates> next;
+            if (p + 1 < NP) next = load_stream(p + 1, true);
+            __builtin_amdgcn_sched_barrier(0);
             const PairAt<WAVES, TG> c(A, p);
-            const uint32_t hoff = c.in_plane(A.hsd, false), goff = c.in_plane(A.gsd, gb);
-            const uint32_t xoff = c.in_row(A.xst, xb);
-            const float4 w = w_lds[p][threadIdx.x];
-            float s_post[2] = {0.0f, 0.0f};
+            float dx[4][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float4 n2 = n2_lds[2 * p + i][threadIdx.x];
-                e[p][0][i] = fmaf_(-m2[0], n2.x, e[p][0][i]);
-                e[p][1][i] = fmaf_(-m2[1], n2.y, e[p][1][i]);
-                e[p][2][i] = fmaf_(-m2[2], n2.z, e[p][2][i]);
-                e[p][3][i] = fmaf_(-m2[3], n2.w, e[p][3][i]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (at.all || at.own[k])
-                    store_pair(element_at(A.dx, xo + xk[k], xb), xoff, xb, e[p][k][0], e[p][k][1]);
-            }
-            if constexpr (!kStates) continue;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
+                const float4 e4 = e_lds[2 * p + i][threadIdx.x];
+                const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+                const float wp = kStates ? A.scale * now.wp[i] : 0.0f;
                 float dh[4], dg[4];
                 // opaque: the sigmoids are cheaper again than kept since the sums
+                if constexpr (kStates)
 #pragma unroll
-                for (int j = 0; j < (gb ? 2 : 4); ++j) g[p][i].w[j] = opaque_bits(g[p][i].w[j]);
+                    for (int j = 0; j < (gb ? 2 : 4); ++j) g[p][i].w[j] = opaque_bits(g[p][i].w[j]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float hv = quad_value(h[p][i], k, false), gv = quad_value(g[p][i], k, gb);
-                    const float sg = has_gate ? sigmoid_q(-kLog2e * gv) : 1.0f;
-                    const float act = has_gate ? gv * sg : 1.0f;
-                    const float n1 = hv * act * r1[k], dx = e[p][k][i];
-                    s_post[i] = fmaf_(dx, n1, s_post[i]);
-                    const float dv = r1[k] * fmaf_(-n1, m1[k], dx * (i ? w.y : w.x));
-                    dh[k] = dv * act;
-                    dg[k] = dv * hv * (sg * fmaf_(gv, 1.0f - sg, 1.0f));
+                    float hv = 0.0f, gv = 0.0f, sg = 1.0f, act = 1.0f, n1 = 0.0f;
+                    float y = pair_value(now.x[k], i, xb);
+                    if constexpr (kStates) {
+                        hv = quad_value(h[p][i], k, false), gv = quad_value(g[p][i], k, gb);
+                        if (has_gate) sg = sigmoid_q(-kLog2e * gv), act = gv * sg;
+                        n1 = hv * act * r1[k];
+                        y = fmaf_(n1, wp, y);
+                    }
+                    dx[k][i] = fmaf_(-m2[k], y, e[k]);
+                    if constexpr (kStates) {
+                        s_post[p][i] = fmaf_(dx[k][i], n1, s_post[p][i]);
+                        const float dv = r1[k] * fmaf_(-n1, m1[k], dx[k][i] * wp);
+                        dh[k] = dv * act;
+                        dg[k] = dv * hv * (sg * fmaf_(gv, 1.0f - sg, 1.0f));
+                    }
                 }
-                store_quad<QUADS>(A.dh + ho + i * A.hsd, hoff, hk, at.own, at.all, false, dh);
-                if (has_gate)
-                    store_quad<QUADS>(element_at(A.dgate, go + i * A.gsd, gb), goff, gk, at.own,
-                                      at.all, gb, dg);
+                if constexpr (kStates) {
+                    store_quad<QUADS>(A.dh + ho + i * A.hsd, c.in_plane(A.hsd, false), hk, at.own,
+                                      at.all, false, dh);
+                    if (has_gate)
+                        store_quad<QUADS>(element_at(A.dgate, go + i * A.gsd, gb),
+                                          c.in_plane(A.gsd, gb), gk, at.own, at.all, gb, dg);
+                }
             }
-            dw_lds[p][threadIdx.x].x += s_post[0];
-            dw_lds[p][threadIdx.x].y += s_post[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (at.all || at.own[k])
+                    store_pair(element_at(A.dx, xo + xk[k], xb), c.in_row(A.xst, xb), xb, dx[k][0],
+                               dx[k][1]);
+            s_post[p][0] = opaque(s_post[p][0]), s_post[p][1] = opaque(s_post[p][1]);
+            now = next;
         }
     }
     float *part = A.part + (int64_t)blockIdx.x * 2 * A.D;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const PairAt<WAVES, TG> c(A, p);
-        const float4 dw = dw_lds[p][threadIdx.x];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float a = i ? dw.y : dw.x, b = i ? dw.w : dw.z;
+            float a = s_post[p][i], b = s_pre[p][i];
 #pragma unroll
             for (int o = 1; o < TG; o *= 2) {  // the groups hold the same channels
                 a += __shfl_xor(a, o);

@@ -346,13 +346,16 @@ class Workspace:
     def __init__(self):
         self.buf = {}
 
-    def get(self, nbytes, device, stream=None):
+    def get(self, nbytes, device, stream=None, key=None):
+        """``key``: (device index, stream handle), where the caller knows it."""
         if nbytes == 0:
             return None
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        key = (torch.device(device).index, s.cuda_stream)
+        if key is None:
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            key = (torch.device(device).index, s.cuda_stream)
         b = self.buf.pop(key, None)
         if b is None or b.numel() < nbytes:
+            s = stream if stream is not None else torch.cuda.current_stream(device)
             with torch.cuda.stream(s):
                 b = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.buf[key] = b  # most recent last
@@ -683,8 +686,42 @@ def scan(A, b, x0=None, *, reverse=False, out=None, steps_per_lane=0, waves_per_
 
 
 # ------------------------------------------- operators of language models ---
+# A call of these is a few microseconds of device time at its smallest, so the
+# host has to be quick too: the argument checks depend on the tensors' shapes,
+# strides, dtypes and devices alone, so they run once for each combination of
+# those, which then names a prepared record (the ABI's shape, the workspace
+# size).
 
 TOP_MAX = 64  # PARARNN_TOP_MAX
+
+_plans = {}  # prepared records by signature
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _signature(*tensors):
+    """What the argument checks depend on; None if something is no tensor."""
+    try:
+        return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+                      for t in tensors])
+    except (AttributeError, TypeError):
+        return None
+
+
+def _planned(key, make, *args):
+    """The record of `key`; on its first use `make(*args)` checks the arguments
+    and prepares it."""
+    plan = _plans.get(key)
+    if plan is None:
+        plan = make(*args)
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _where(dev, stream):
+    """(device index, stream handle) of a call."""
+    return dev.index, (_raw_stream(dev.index) if stream is None else stream.cuda_stream)
 
 
 def _code(t, name):
@@ -703,6 +740,30 @@ def _check_resets(resets, B, T):
         raise ValueError("resets: must be contiguous bool or uint8")
 
 
+def _scan_plan(u, lam, h0, resets, h, gh, gh_last, workspace, adjoint):
+    (B, D, T), udt = _gate_planes(u, 3)
+    _check_dense(lam, "lam", (D,))
+    for name, x in (("h0", h0), ("gh_last", gh_last)):
+        if x is not None:
+            _check_dense(x, name, (B, D))
+    _check_resets(resets, B, T)
+    dense = (D * T, T, 1)
+    us = _strides(u, "u") or dense
+    if h is None and not adjoint:
+        ss = _dense(B, T, D, us)
+    else:
+        _check_planes([h], "h" if adjoint else "out", (B, D, T))
+        _check_planes([gh], "gh", (B, D, T), allow_none=True)
+        ss = _strides([h, gh], "h and gh") or dense
+    dev = u[0].device
+    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
+                                                 ("h", h), ("gh", gh), ("gh_last", gh_last),
+                                                 ("workspace", workspace)])
+    shape = ctypes.byref(make_shape(B, T, D, us, ss))
+    nws = int(load().pararnn_gated_workspace_bytes(shape, 1 if adjoint else 0))
+    return B, T, D, udt, us, ss, shape, nws, dev
+
+
 def gated_scan(u, lam, h0=None, *, power=8.0, resets=None, out=None, workspace=None, stream=None):
     """Gated linear recurrence h_t = k_t a_t h_{t-1} + sqrt(1 - a_t^2) sig(u_i) u_x
     with a_t = exp(-power softplus(lam) sig(u_r)).  u = [u_r, u_i, u_x] device
@@ -712,30 +773,20 @@ def gated_scan(u, lam, h0=None, *, power=8.0, resets=None, out=None, workspace=N
     (h [B][D][T], h_last [B][D]), float32."""
     lib = load()
     u = list(u)
-    (B, D, T), udt = _gate_planes(u, 3)
-    _check_dense(lam, "lam", (D,))
-    if h0 is not None:
-        _check_dense(h0, "h0", (B, D))
-    _check_resets(resets, B, T)
-    dev = u[0].device
-    us = _strides(u, "u") or (D * T, T, 1)
+    key = ("scan", _signature(*u, lam, h0, resets, out, workspace))
+    B, T, D, udt, us, ss, shape, nws, dev = _planned(
+        key, _scan_plan, u, lam, h0, resets, out, None, None, workspace, False)
     allocated = []
     if out is None:
-        out = _new_planes(1, B, T, D, us, dev)[0]
+        out = torch.empty_strided((B, D, T), ss, dtype=torch.float32, device=dev)
         allocated = [out]
-    _check_planes([out], "out", (B, D, T))
-    ss = _strides([out], "out") or (D * T, T, 1)
-    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
-                                                 ("out", out), ("workspace", workspace)])
     h_last = torch.empty((B, D), dtype=torch.float32, device=dev)
     _record_on(stream, allocated + [h_last])
-    shape = make_shape(B, T, D, us, ss)
-    ws = workspace
-    if ws is None:
-        ws = _ws.get(int(lib.pararnn_gated_workspace_bytes(ctypes.byref(shape), 0)), dev, stream)
-    _check(lib.pararnn_gated_scan(ctypes.byref(shape), _ptr_array(u), udt, _ptr(lam), power,
-                                  _ptr(h0), _ptr(resets), _ptr(out), _ptr(h_last), _ptr(ws),
-                                  0 if ws is None else ws.numel(), _stream_handle(stream)))
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _check(lib.pararnn_gated_scan(shape, _ptr_array(u), udt, lam.data_ptr(), power, _ptr(h0),
+                                  _ptr(resets), out.data_ptr(), h_last.data_ptr(), _ptr(ws),
+                                  0 if ws is None else ws.numel(), at[1]))
     return out, h_last
 
 
@@ -747,45 +798,25 @@ def gated_scan_adjoint(u, lam, h0, h, gh, *, gh_last=None, power=8.0, resets=Non
     dlam [D], dh0 [B][D])."""
     lib = load()
     u = list(u)
-    (B, D, T), udt = _gate_planes(u, 3)
-    _check_dense(lam, "lam", (D,))
-    for name, x in (("h0", h0), ("gh_last", gh_last)):
-        if x is not None:
-            _check_dense(x, name, (B, D))
-    _check_resets(resets, B, T)
-    _check_planes([h], "h", (B, D, T))
-    _check_planes([gh], "gh", (B, D, T), allow_none=True)
-    dev = u[0].device
-    us = _strides(u, "u") or (D * T, T, 1)
-    ss = _strides([h, gh], "h and gh") or (D * T, T, 1)
-    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
-                                                 ("h", h), ("gh", gh), ("gh_last", gh_last),
-                                                 ("workspace", workspace)])
-    du = [torch.empty_strided((B, D, T), us, dtype=u[0].dtype, device=dev) for _ in range(3)]
+    key = ("scan_adjoint", _signature(*u, lam, h0, resets, h, gh, gh_last, workspace))
+    B, T, D, udt, us, ss, shape, nws, dev = _planned(
+        key, _scan_plan, u, lam, h0, resets, h, gh, gh_last, workspace, True)
+    dt = u[0].dtype
+    du = [torch.empty_strided((B, D, T), us, dtype=dt, device=dev) for _ in range(3)]
     dlam = torch.empty((D,), dtype=torch.float32, device=dev)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
     _record_on(stream, du + [dlam, dh0])
-    shape = make_shape(B, T, D, us, ss)
-    ws = workspace
-    if ws is None:
-        ws = _ws.get(int(lib.pararnn_gated_workspace_bytes(ctypes.byref(shape), 1)), dev, stream)
-    _check(lib.pararnn_gated_scan_adjoint(ctypes.byref(shape), _ptr_array(u), udt, _ptr(lam), power,
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _check(lib.pararnn_gated_scan_adjoint(shape, _ptr_array(u), udt, lam.data_ptr(), power,
                                           _ptr(h0), _ptr(resets), _ptr(h), _ptr(gh),
-                                          _ptr(gh_last), _ptr_array(du), _ptr(dlam), _ptr(dh0),
-                                          _ptr(ws), 0 if ws is None else ws.numel(),
-                                          _stream_handle(stream)))
+                                          _ptr(gh_last), _ptr_array(du), dlam.data_ptr(),
+                                          dh0.data_ptr(), _ptr(ws),
+                                          0 if ws is None else ws.numel(), at[1]))
     return dict(du=du, dlam=dlam, dh0=dh0)
 
 
-def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
-    """One step of the gated linear recurrence for B requests.  u = [u_r, u_i,
-    u_x] tensors [B][D] (rows may be strided), lam [D], states [pool][D]
-    float32, updated in place, slots [B] int32 or None (row b has slot b).  A
-    row whose slot is outside the pool (-1) is idle: it gives zeros and
-    changes no state; live rows need distinct slots.  Returns the new states
-    of the rows, [B][D] float32."""
-    lib = load()
-    u = list(u)
+def _step_plan(u, lam, states, slots, out):
     _require(len(u) == 3, "expected 3 gate row blocks")
     udt = _code(u[0], "u")
     _require(u[0].dim() == 2, "u: row blocks must be [B][D]")
@@ -793,7 +824,7 @@ def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
     for p in u:
         if not _is_tensor(p) or tuple(p.shape) != (B, D) or p.dtype is not u[0].dtype:
             raise ValueError("u: every row block must have the same shape [B][D] and dtype")
-        if p.numel() and D > 1 and p.stride(1) != 1 or B > 1 and p.stride(0) != u[0].stride(0):
+        if p.numel() and (D > 1 and p.stride(1) != 1 or B > 1 and p.stride(0) != u[0].stride(0)):
             raise ValueError("u: rows must be contiguous and share their stride")
     _check_dense(lam, "lam", (D,))
     if not _is_tensor(states) or states.dim() != 2:
@@ -805,17 +836,30 @@ def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
     elif not _is_tensor(slots) or tuple(slots.shape) != (B,) or slots.dtype != torch.int32 or (
             not slots.is_contiguous()):
         raise ValueError(f"slots: must be contiguous int32 [{B}]")
-    allocated = []
-    if out is None:
-        out = torch.empty((B, D), dtype=torch.float32, device=u[0].device)
-        allocated = [out]
-    _check_dense(out, "out", (B, D))
+    if out is not None:
+        _check_dense(out, "out", (B, D))
     _check_devices(u[0].device, [("u", p) for p in u] + [("lam", lam), ("states", states),
                                                          ("slots", slots), ("out", out)])
-    _record_on(stream, allocated)
-    _check(lib.pararnn_gated_step(B, D, _ptr_array(u), udt, u[0].stride(0) if B > 1 else D,
-                                  _ptr(lam), power, _ptr(slots), _ptr(states), pool, _ptr(out),
-                                  _stream_handle(stream)))
+    return B, D, pool, udt, u[0].stride(0) if B > 1 else D, u[0].device
+
+
+def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
+    """One step of the gated linear recurrence for B requests.  u = [u_r, u_i,
+    u_x] tensors [B][D] (rows may be strided), lam [D], states [pool][D]
+    float32, updated in place, slots [B] int32 or None (row b has slot b).  A
+    row whose slot is outside the pool (-1) is idle: it gives zeros and
+    changes no state; live rows need distinct slots.  Returns the new states
+    of the rows, [B][D] float32."""
+    lib = load()
+    u = list(u)
+    B, D, pool, udt, stride, dev = _planned(("step", _signature(*u, lam, states, slots, out)),
+                                            _step_plan, u, lam, states, slots, out)
+    if out is None:
+        out = torch.empty((B, D), dtype=torch.float32, device=dev)
+        _record_on(stream, [out])
+    _check(lib.pararnn_gated_step(B, D, _ptr_array(u), udt, stride, lam.data_ptr(), power,
+                                  _ptr(slots), states.data_ptr(), pool, out.data_ptr(),
+                                  _where(dev, stream)[1]))
     return out
 
 
@@ -829,20 +873,41 @@ def _row_strides(t, name):
     return (t.stride(0) if B > 1 else st * T, st)
 
 
-def _block_shape(h, gate, x, z_strides):
-    """Checks what the block boundary reads; returns its shape record."""
-    if not _is_tensor(x) or x.dim() != 3:
-        raise ValueError("x: expected a tensor [B][T][D]")
+def _block_plan(h, gate, x, w_post, w_pre, rstd, gy, gz, z_dtype, workspace, adjoint):
+    xdt = _code(x, "x")
+    _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
     B, T, D = x.shape
-    dense = (D * T, T, 1)
+    dense, zs = (D * T, T, 1), (T * D, D)
+    gdt = F32 if gate is None else _code(gate, "gate")
     if h is not None:
         _check_planes([h], "h", (B, D, T))
+        _check_dense(w_post, "w_post", (D,))
     if gate is not None:
         _require(h is not None, "gate: needs h")
         _check_planes([gate], "gate", (B, D, T), _U_DTYPES)
+    _check_dense(w_pre, "w_pre", (D,))
+    if adjoint:
+        _check_dense(rstd, "rstd", (2, B, T))
+        zdt = F32
+        if gz is not None:
+            _require(_is_tensor(gz) and tuple(gz.shape) == (B, T, D), f"gz: expected {[B, T, D]}")
+            zs, zdt = _row_strides(gz, "gz"), _code(gz, "gz")
+        if gy is not None:
+            _require(_is_tensor(gy) and tuple(gy.shape) == (B, T, D), f"gy: expected {[B, T, D]}")
+            _require(gy.dtype is x.dtype and _row_strides(gy, "gy") == _row_strides(x, "x"),
+                     "gy: must have x's dtype and strides")
+    else:
+        _require(z_dtype in _U_DTYPES, "z_dtype must be float32 or bfloat16")
+        zdt = BF16 if z_dtype is torch.bfloat16 else F32
     hs = (_strides([h], "h") if h is not None else None) or dense
     gs = (_strides([gate], "gate") if gate is not None else None) or dense
-    return BlockShape(B, T, D, *hs, *gs, *_row_strides(x, "x"), *z_strides)
+    xs = _row_strides(x, "x")
+    _check_devices(x.device, [("x", x), ("h", h), ("gate", gate),
+                              ("w_post", w_post if h is not None else None), ("w_pre", w_pre),
+                              ("rstd", rstd), ("gy", gy), ("gz", gz), ("workspace", workspace)])
+    shape = ctypes.byref(BlockShape(B, T, D, *hs, *gs, *xs, *zs))
+    nws = int(load().pararnn_block_workspace_bytes(shape)) if adjoint else 0
+    return B, T, D, xdt, gdt, zdt, hs, gs, xs + (1,), shape, nws, x.device
 
 
 def block_norm(h, x, w_post, w_pre, *, gate=None, scale=1.0, eps=1e-6, z_dtype=torch.bfloat16,
@@ -855,27 +920,18 @@ def block_norm(h, x, w_post, w_pre, *, gate=None, scale=1.0, eps=1e-6, z_dtype=t
     Returns (y [B][T][D] in x's dtype and strides, z [B][T][D] in z_dtype,
     rstd [2][B][T] float32); without h, y is x itself."""
     lib = load()
-    xdt = _code(x, "x")
-    gdt = F32 if gate is None else _code(gate, "gate")
-    _require(z_dtype in _U_DTYPES, "z_dtype must be float32 or bfloat16")
-    _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
-    B, T, D = x.shape
-    shape = _block_shape(h, gate, x, (T * D, D))
-    if h is not None:
-        _check_dense(w_post, "w_post", (D,))
-    _check_dense(w_pre, "w_pre", (D,))
-    dev = x.device
-    _check_devices(dev, [("x", x), ("h", h), ("gate", gate), ("w_post", w_post if h is not None else None),
-                         ("w_pre", w_pre)])
-    y = x if h is None else torch.empty_strided((B, T, D), (shape.x_stride_b, shape.x_stride_t, 1),
-                                                dtype=x.dtype, device=dev)
+    if h is None:
+        w_post = None
+    B, T, D, xdt, gdt, zdt, hs, gs, xs, shape, _, dev = _planned(
+        ("block", z_dtype, _signature(h, gate, x, w_post, w_pre)), _block_plan, h, gate, x, w_post,
+        w_pre, None, None, None, z_dtype, None, False)
+    y = x if h is None else torch.empty_strided((B, T, D), xs, dtype=x.dtype, device=dev)
     z = torch.empty((B, T, D), dtype=z_dtype, device=dev)
     rstd = torch.empty((2, B, T), dtype=torch.float32, device=dev)
     _record_on(stream, [None if h is None else y, z, rstd])
-    _check(lib.pararnn_block_norm(ctypes.byref(shape), _ptr(h), _ptr(gate), gdt, _ptr(x), xdt,
-                                  _ptr(w_post) if h is not None else None, _ptr(w_pre), scale, eps,
-                                  None if h is None else _ptr(y), _ptr(z), _code(z, "z"),
-                                  _ptr(rstd), _stream_handle(stream)))
+    _check(lib.pararnn_block_norm(shape, _ptr(h), _ptr(gate), gdt, x.data_ptr(), xdt, _ptr(w_post),
+                                  w_pre.data_ptr(), scale, eps, None if h is None else y.data_ptr(),
+                                  z.data_ptr(), zdt, rstd.data_ptr(), _where(dev, stream)[1]))
     return y, z, rstd
 
 
@@ -886,53 +942,31 @@ def block_norm_adjoint(h, x, w_post, w_pre, rstd, gy, gz, *, gate=None, scale=1.
     Returns dict(dh, dgate, dx, dw_post, dw_pre); dh, dgate and dw_post are
     None where their input is."""
     lib = load()
-    xdt = _code(x, "x")
-    gdt = F32 if gate is None else _code(gate, "gate")
-    _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
-    B, T, D = x.shape
-    if gz is not None:
-        _require(_is_tensor(gz) and tuple(gz.shape) == (B, T, D), f"gz: expected {[B, T, D]}")
-    zs = (T * D, D) if gz is None else _row_strides(gz, "gz")
-    zdt = F32 if gz is None else _code(gz, "gz")
-    shape = _block_shape(h, gate, x, zs)
-    if gy is not None:
-        _require(_is_tensor(gy) and tuple(gy.shape) == (B, T, D), f"gy: expected {[B, T, D]}")
-        _require(gy.dtype is x.dtype and _row_strides(gy, "gy") == _row_strides(x, "x"),
-                 "gy: must have x's dtype and strides")
-    if h is not None:
-        _check_dense(w_post, "w_post", (D,))
-    _check_dense(w_pre, "w_pre", (D,))
-    _check_dense(rstd, "rstd", (2, B, T))
-    dev = x.device
-    _check_devices(dev, [("x", x), ("h", h), ("gate", gate), ("w_post", w_post if h is not None else None),
-                         ("w_pre", w_pre), ("rstd", rstd), ("gy", gy), ("gz", gz),
-                         ("workspace", workspace)])
-    xs = (shape.x_stride_b, shape.x_stride_t, 1)
+    if h is None:
+        w_post = None
+    B, T, D, xdt, gdt, zdt, hs, gs, xs, shape, nws, dev = _planned(
+        ("block_adjoint", _signature(h, gate, x, w_post, w_pre, rstd, gy, gz, workspace)),
+        _block_plan, h, gate, x, w_post, w_pre, rstd, gy, gz, None, workspace, True)
     dx = torch.empty_strided((B, T, D), xs, dtype=x.dtype, device=dev)
     dh = dgate = dw_post = None
     if h is not None:
-        dh = torch.empty_strided((B, D, T), (shape.h_stride_b, shape.h_stride_d, shape.h_stride_t),
-                                 dtype=torch.float32, device=dev)
+        dh = torch.empty_strided((B, D, T), hs, dtype=torch.float32, device=dev)
         dw_post = torch.empty((D,), dtype=torch.float32, device=dev)
     if gate is not None:
-        dgate = torch.empty_strided((B, D, T),
-                                    (shape.g_stride_b, shape.g_stride_d, shape.g_stride_t),
-                                    dtype=gate.dtype, device=dev)
+        dgate = torch.empty_strided((B, D, T), gs, dtype=gate.dtype, device=dev)
     dw_pre = torch.empty((D,), dtype=torch.float32, device=dev)
     _record_on(stream, [dx, dh, dgate, dw_post, dw_pre])
-    ws = workspace
-    if ws is None:
-        ws = _ws.get(int(lib.pararnn_block_workspace_bytes(ctypes.byref(shape))), dev, stream)
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
     _check(lib.pararnn_block_norm_adjoint(
-        ctypes.byref(shape), _ptr(h), _ptr(gate), gdt, _ptr(x), xdt,
-        _ptr(w_post) if h is not None else None, _ptr(w_pre), scale, _ptr(rstd), _ptr(gy),
-        _ptr(gz), zdt, _ptr(dh), _ptr(dgate), _ptr(dx), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
-        0 if ws is None else ws.numel(), _stream_handle(stream)))
+        shape, _ptr(h), _ptr(gate), gdt, x.data_ptr(), xdt, _ptr(w_post), w_pre.data_ptr(), scale,
+        rstd.data_ptr(), _ptr(gy), _ptr(gz), zdt, _ptr(dh), _ptr(dgate), dx.data_ptr(),
+        _ptr(dw_post), dw_pre.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), at[1]))
     return dict(dh=dh, dgate=dgate, dx=dx, dw_post=dw_post, dw_pre=dw_pre)
 
 
-def _logits(logits, tokens):
-    """Checks logits [N][V] and tokens [N]; returns (N, V, row stride, dtype code)."""
+def _score_plan(logits, tokens, vectors, out, workspace, top):
+    """Logits [N][V], tokens [N]; `vectors`: (name, [N] float32 or None)."""
     dt = _code(logits, "logits")
     _require(logits.dim() == 2, "logits: expected a tensor [N][V]")
     N, V = logits.shape
@@ -941,7 +975,19 @@ def _logits(logits, tokens):
     if not _is_tensor(tokens) or tuple(tokens.shape) != (N,) or tokens.dtype != torch.int64 or (
             not tokens.is_contiguous()):
         raise ValueError(f"tokens: must be contiguous int64 [{N}]")
-    return N, V, logits.stride(0) if N > 1 else V, dt
+    _require(0 <= top <= TOP_MAX, f"top: 0 to {TOP_MAX}")
+    for name, t in vectors:
+        if t is not None or name == "lse":
+            _check_dense(t, name, (N,))
+    if out is not None and (not _is_tensor(out) or tuple(out.shape) != (N, V)
+                            or out.dtype is not logits.dtype
+                            or (out.numel() and V > 1 and out.stride(1) != 1)):
+        raise ValueError("out: must be [N][V] in the logits' dtype, the vocabulary contiguous")
+    _check_devices(logits.device, [("logits", logits), ("tokens", tokens), ("out", out),
+                                   ("workspace", workspace)] + list(vectors))
+    nws = int(load().pararnn_logprobs_workspace_bytes(N, V, top))
+    out_stride = V if out is None or N <= 1 else out.stride(0)
+    return N, V, logits.stride(0) if N > 1 else V, dt, out_stride, nws, logits.device
 
 
 def token_logprobs(logits, tokens, *, top=0, scale=1.0, workspace=None, stream=None):
@@ -954,27 +1000,25 @@ def token_logprobs(logits, tokens, *, top=0, scale=1.0, workspace=None, stream=N
     masked token (-inf) is never one of them, and index -1 with log
     probability -inf stands where a row has no more."""
     lib = load()
-    N, V, stride, dt = _logits(logits, tokens)
     top = int(top)
-    _require(0 <= top <= TOP_MAX, f"top: 0 to {TOP_MAX}")
-    dev = logits.device
-    _check_devices(dev, [("logits", logits), ("tokens", tokens), ("workspace", workspace)])
+    N, V, stride, dt, _, nws, dev = _planned(
+        ("score", top, _signature(logits, tokens, workspace)), _score_plan, logits, tokens, (),
+        None, workspace, top)
     stats = torch.empty((3, N), dtype=torch.float32, device=dev)
-    out = dict(logprob=stats[0], entropy=stats[1], lse=stats[2])
-    allocated = [stats]
+    logprob, entropy, lse = stats.unbind(0)
+    out = dict(logprob=logprob, entropy=entropy, lse=lse)
+    first = stats.data_ptr()
+    index = value = None
     if top:
-        out["top_index"] = torch.empty((N, top), dtype=torch.int64, device=dev)
-        out["top_logprob"] = torch.empty((N, top), dtype=torch.float32, device=dev)
-        allocated += [out["top_index"], out["top_logprob"]]
-    _record_on(stream, allocated)
-    ws = workspace
-    if ws is None:
-        ws = _ws.get(int(lib.pararnn_logprobs_workspace_bytes(N, V, top)), dev, stream)
-    _check(lib.pararnn_token_logprobs(N, V, _ptr(logits), dt, stride, _ptr(tokens), top, scale,
-                                      _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out["lse"]),
-                                      _ptr(out.get("top_index")), _ptr(out.get("top_logprob")),
-                                      _ptr(ws), 0 if ws is None else ws.numel(),
-                                      _stream_handle(stream)))
+        out["top_index"] = index = torch.empty((N, top), dtype=torch.int64, device=dev)
+        out["top_logprob"] = value = torch.empty((N, top), dtype=torch.float32, device=dev)
+    _record_on(stream, [stats, index, value])
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _check(lib.pararnn_token_logprobs(N, V, logits.data_ptr(), dt, stride, tokens.data_ptr(), top,
+                                      scale, first, first + 4 * N, first + 8 * N, _ptr(index),
+                                      _ptr(value), _ptr(ws), 0 if ws is None else ws.numel(),
+                                      at[1]))
     return out
 
 
@@ -985,26 +1029,19 @@ def token_logprobs_adjoint(logits, tokens, lse, entropy=None, *, g_logprob=None,
     needed with g_entropy).  ``out`` may be the logits themselves.  Returns
     dL/dlogits in the logits' dtype."""
     lib = load()
-    N, V, stride, dt = _logits(logits, tokens)
-    for name, t in (("lse", lse), ("entropy", entropy), ("g_logprob", g_logprob),
-                    ("g_entropy", g_entropy), ("g_lse", g_lse)):
-        if t is not None or name == "lse":
-            _check_dense(t, name, (N,))
     _require(g_entropy is None or entropy is not None, "g_entropy: needs entropy")
-    allocated = []
+    N, V, stride, dt, out_stride, _, dev = _planned(
+        ("score_adjoint",
+         _signature(logits, tokens, lse, entropy, g_logprob, g_entropy, g_lse, out)),
+        _score_plan, logits, tokens,
+        (("lse", lse), ("entropy", entropy), ("g_logprob", g_logprob), ("g_entropy", g_entropy),
+         ("g_lse", g_lse)), out, None, 0)
     if out is None:
-        out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
-        allocated = [out]
-    if not _is_tensor(out) or tuple(out.shape) != (N, V) or out.dtype is not logits.dtype or (
-            out.numel() and V > 1 and out.stride(1) != 1):
-        raise ValueError("out: must be [N][V] in the logits' dtype, the vocabulary contiguous")
-    _check_devices(logits.device, [("logits", logits), ("tokens", tokens), ("lse", lse),
-                                   ("entropy", entropy), ("g_logprob", g_logprob),
-                                   ("g_entropy", g_entropy), ("g_lse", g_lse), ("out", out)])
-    _record_on(stream, allocated)
-    _check(lib.pararnn_token_logprobs_adjoint(N, V, _ptr(logits), dt, stride, _ptr(tokens), scale,
-                                              _ptr(lse), _ptr(entropy), _ptr(g_logprob),
-                                              _ptr(g_entropy), _ptr(g_lse), _ptr(out),
-                                              out.stride(0) if N > 1 else V,
-                                              _stream_handle(stream)))
+        out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        _record_on(stream, [out])
+    _check(lib.pararnn_token_logprobs_adjoint(N, V, logits.data_ptr(), dt, stride,
+                                              tokens.data_ptr(), scale, lse.data_ptr(),
+                                              _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
+                                              _ptr(g_lse), out.data_ptr(), out_stride,
+                                              _where(dev, stream)[1]))
     return out

@@ -47,7 +47,8 @@ hipError_t run_score(const ScoreArgs &A, hipStream_t st)
         hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, true>), grid, wide, 0, st, A);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((score_join_kernel<BF16>), dim3((unsigned)A.N), one, 0, st, A);
+        hipLaunchKernelGGL((score_join_kernel<BF16>), dim3((unsigned)A.N), dim3(kJoinThreads), 0, st,
+                           A);
     } else if (A.V <= 2048) {
         // a row of one to a few vectors a lane: no barriers between waves
         hipLaunchKernelGGL((score_kernel<BF16, 1, false>), grid, one, 0, st, A);

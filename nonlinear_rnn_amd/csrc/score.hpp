@@ -62,6 +62,8 @@ constexpr int kScoreThreads = kScoreWaves * kWave;
 constexpr int kScoreParts = 32;  // most parts of a row
 // Vectors a lane loads before it uses the first.
 constexpr int kScoreUnroll = 4;
+// The same where it reads again, from wherever the row has gone meanwhile.
+constexpr int kScoreAgain = 8;
 
 // Running statistics of part of a row: the largest logit so far and the two
 // sums, in base 2: with c = scale log2(e), s = sum 2^(c (x - m)),
@@ -134,27 +136,41 @@ struct RowView {
         vectors = V > 0 ? (V + shift + K - 1) / K : 0;
     }
     __device__ __forceinline__ int64_t element(int64_t i) const { return i * K - shift; }
-    __device__ __forceinline__ void load(int64_t i, float (&x)[K]) const
+    __device__ __forceinline__ uint4 load_raw(int64_t i) const
     {
         const int64_t j = element(i);
-        if (j >= 0 && j + K <= V) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(row + j * (BF16 ? 2 : 4));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (j >= 0 && j + K <= V) return *reinterpret_cast<const uint4 *>(row + j * (BF16 ? 2 : 4));
+        uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (BF16) {
-                    x[2 * q] = __uint_as_float(w[q] << 16);
-                    x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-                } else {
-                    x[q] = __uint_as_float(w[q]);
-                }
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (BF16) {
+                w[q] = 0xff80u | 0xff800000u;  // -inf twice
+                const int64_t e = j + 2 * q;
+                if (e >= 0 && e < V)
+                    w[q] = (w[q] & 0xffff0000u) | reinterpret_cast<const uint16_t *>(row)[e];
+                if (e + 1 >= 0 && e + 1 < V)
+                    w[q] = (w[q] & 0xffffu) | (uint32_t)reinterpret_cast<const uint16_t *>(row)[e + 1] << 16;
+            } else {
+                w[q] = j + q >= 0 && j + q < V ? reinterpret_cast<const uint32_t *>(row)[j + q]
+                                               : 0xff800000u;
             }
-        } else {
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void values(const uint4 &v, float (&x)[K])
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                x[k] = j + k >= 0 && j + k < V ? load_gate<BF16>(row, j + k) : -__builtin_inff();
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (BF16) {
+                x[2 * q] = __uint_as_float(w[q] << 16);
+                x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+            } else {
+                x[q] = __uint_as_float(w[q]);
+            }
         }
     }
+    __device__ __forceinline__ void load(int64_t i, float (&x)[K]) const { values(load_raw(i), x); }
 };
 
 // The best tokens seen by a wave: lane i holds the i-th best key, 0 where
@@ -198,30 +214,71 @@ struct TopList {
 // Every key that is not above this is of a masked token.
 constexpr uint64_t kMaskedFloor = 0x007fffffffffffffull;  // ordered(-inf) in the upper half
 
-// The results of row n from its statistics and (lanes 0 .. top - 1) its list.
-template <bool BF16>
-__device__ __forceinline__ void write_scores(const ScoreArgs &A, int64_t n, const Stats &a,
-                                             uint64_t key, int lane)
+// How many of n <= PARARNN_TOP_MAX falling keys are above `key`.
+__device__ __forceinline__ int keys_above(const uint64_t *list, int n, uint64_t key)
 {
-    const bool empty = a.s == 0.0f;
-    const float base = empty ? 0.0f : a.m;
-    const float ls = empty ? -__builtin_inff() : logf(a.s);
-    if (lane == 0) {
-        const int64_t t = A.tokens[n];
-        float lp = 0.0f;
-        if (t >= A.V)
-            lp = __builtin_nanf("");
-        else if (t >= 0)
-            lp = empty ? ls : fmaf_(A.scale, load_gate<BF16>(A.x, n * A.stride + t) - base, -ls);
-        A.logprob[n] = lp;
-        if (A.lse) A.lse[n] = fmaf_(A.scale, base, ls);
-        if (A.entropy) A.entropy[n] = empty ? 0.0f : ls - 0.6931471805599453f * (a.w / a.s);
+    static_assert(PARARNN_TOP_MAX < 128, "the first step");
+    int above = 0;
+#pragma unroll
+    for (int step = 64; step > 0; step >>= 1)
+        if (above + step <= n && list[above + step - 1] > key) above += step;
+    return above;
+}
+// Joins `count` lists of `top` falling keys in LDS two by two, between `a` and
+// `b`: a key's place is its own index and the number of keys above it in the
+// other list (keys 0, behind all others, may meet there: they are equal).
+// Returns the buffer with the joined list.
+__device__ __forceinline__ uint64_t *join_lists(uint64_t *a, uint64_t *b, int count, int top,
+                                                int threads)
+{
+    for (; count > 1; count = (count + 1) >> 1) {
+        __syncthreads();
+        for (int t = threadIdx.x; t < count * top; t += threads) {
+            const int list = t / top, other = list ^ 1;
+            const uint64_t key = a[t];
+            int place = t - list * top;
+            if (other < count) place += keys_above(a + other * top, top, key);
+            if (place < top) b[(list >> 1) * top + place] = key;
+        }
+        uint64_t *const joined = b;
+        b = a;
+        a = joined;
     }
-    if (lane < A.top) {
-        A.top_index[n * A.top + lane] = key ? (int64_t)key_token(key) : -1;
-        A.top_logprob[n * A.top + lane] =
-            key ? fmaf_(A.scale, key_value(key) - base, -ls) : -__builtin_inff();
+    __syncthreads();
+    return a;
+}
+
+// The results of row n from its statistics.
+struct RowScores {
+    float base, ls;
+    bool empty;
+    __device__ __forceinline__ explicit RowScores(const Stats &a)
+        : base(a.s == 0.0f ? 0.0f : a.m), ls(a.s == 0.0f ? -__builtin_inff() : logf(a.s)),
+          empty(a.s == 0.0f)
+    {
     }
+};
+template <bool BF16>
+__device__ __forceinline__ void write_scores(const ScoreArgs &A, int64_t n, const Stats &a)
+{
+    const RowScores r(a);
+    const int64_t t = A.tokens[n];
+    float lp = 0.0f;
+    if (t >= A.V)
+        lp = __builtin_nanf("");
+    else if (t >= 0)
+        lp = r.empty ? r.ls
+                     : fmaf_(A.scale, load_gate<BF16>(A.x, n * A.stride + t) - r.base, -r.ls);
+    A.logprob[n] = lp;
+    if (A.lse) A.lse[n] = fmaf_(A.scale, r.base, r.ls);
+    if (A.entropy) A.entropy[n] = r.empty ? 0.0f : r.ls - 0.6931471805599453f * (a.w / a.s);
+}
+__device__ __forceinline__ void write_top(const ScoreArgs &A, int64_t n, const RowScores &r, int place,
+                                          uint64_t key)
+{
+    A.top_index[n * A.top + place] = key ? (int64_t)key_token(key) : -1;
+    A.top_logprob[n * A.top + place] =
+        key ? fmaf_(A.scale, key_value(key) - r.base, -r.ls) : -__builtin_inff();
 }
 
 // One workgroup of WAVES waves per row, or per part of a row (PARTS).
@@ -231,7 +288,7 @@ __device__ __forceinline__ void write_scores(const ScoreArgs &A, int64_t n, cons
 // the top-th best of the lanes' maxima is a lower bound of the top-th best
 // logit.  Only lanes whose maximum reaches the bound (about `top` of them) read
 // their vectors again, from the cache, and offer what reaches it to the wave's
-// list; wave 0 joins the waves' lists.
+// list; the waves' lists are joined at the end.
 template <bool BF16, int WAVES, bool PARTS>
 __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
 {
@@ -239,7 +296,7 @@ __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
     constexpr int K = Row::K, U = kScoreUnroll, kThreads = WAVES * kWave;
     __shared__ Stats part[WAVES];
     __shared__ float maxima[kThreads];
-    __shared__ uint64_t lists[WAVES][PARARNN_TOP_MAX];
+    __shared__ uint64_t lists[2][WAVES * PARARNN_TOP_MAX];
     __shared__ uint32_t bound_lds;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
@@ -290,77 +347,73 @@ __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
         list.start(A.top, low > kMaskedFloor ? low : kMaskedFloor);
         const bool mine = ordered(a.m) >= bound;
         if (__ballot(mine))
-            for (int64_t j = v0 + threadIdx.x; __ballot(j < v1); j += 2 * kThreads) {
-                float x[2][K];
+            for (int64_t j = v0 + threadIdx.x; __ballot(j < v1); j += kScoreAgain * kThreads) {
+                uint4 raw[kScoreAgain];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int64_t jq = j + q * kThreads;
-                    if (mine && jq < v1) {
-                        row.load(jq, x[q]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < K; ++k) x[q][k] = -__builtin_inff();
-                    }
+                for (int q = 0; q < kScoreAgain; ++q) {
+                    raw[q] = make_uint4(~0u, ~0u, ~0u, ~0u);  // NaN: no alternative
+                    if (mine && j + q * kThreads < v1) raw[q] = row.load_raw(j + q * kThreads);
                 }
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float best = x[q][0];
+                for (int q = 0; q < kScoreAgain; ++q) {
+                    float x[K], best = -__builtin_inff();
+                    Row::values(raw[q], x);
 #pragma unroll
-                    for (int k = 1; k < K; ++k) best = fmaxf(best, x[q][k]);
+                    for (int k = 0; k < K; ++k) best = fmaxf(best, x[k]);
                     if (!__ballot(ordered(best) >= (uint32_t)(list.floor >> 32))) continue;
                     const int64_t e = row.element(j + q * kThreads);
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        list.offer(may_be_top(x[q][k]) ? top_key(x[q][k], (uint32_t)(e + k)) : 0);
+                        list.offer(may_be_top(x[k]) ? top_key(x[k], (uint32_t)(e + k)) : 0);
                 }
             }
-        if constexpr (WAVES > 1) {
-            lists[wave][lane] = list.key;
-            __syncthreads();
-        }
     }
-    if (wave != 0) return;
+    // the workgroup's statistics, in every thread
     a = part[0];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
-        a = join(a, part[w], c);
-        if (A.top) list.offer(lists[w][lane]);
-    }
+    for (int w = 1; w < WAVES; ++w) a = join(a, part[w], c);
     if constexpr (PARTS) {
-        if (lane == 0) A.part_stats[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
-        if (lane < A.top) A.part_keys[(int64_t)blockIdx.x * A.top + lane] = list.key;
+        if (threadIdx.x == 0) A.part_stats[blockIdx.x] = make_float4(a.m, a.s, a.w, 0.0f);
     } else {
-        write_scores<BF16>(A, n, a, list.key, lane);
+        if (threadIdx.x == 0) write_scores<BF16>(A, n, a);
+    }
+    if (!A.top) return;
+    [[maybe_unused]] const RowScores scores(a);
+    const auto put = [&](int place, uint64_t key) {
+        if constexpr (PARTS)
+            A.part_keys[(int64_t)blockIdx.x * A.top + place] = key;
+        else
+            write_top(A, n, scores, place, key);
+    };
+    if constexpr (WAVES == 1) {
+        if (lane < A.top) put(lane, list.key);
+    } else {
+        if (lane < A.top) lists[0][wave * A.top + lane] = list.key;
+        const uint64_t *joined = join_lists(lists[0], lists[1], WAVES, A.top, kThreads);
+        if (threadIdx.x < A.top) put(threadIdx.x, joined[threadIdx.x]);
     }
 }
 
-// A wave per row joins its parts.
+// A workgroup per row joins its parts.
+constexpr int kJoinThreads = 256;
 template <bool BF16>
-__global__ void __launch_bounds__(kWave) score_join_kernel(ScoreArgs A)
+__global__ void __launch_bounds__(kJoinThreads) score_join_kernel(ScoreArgs A)
 {
-    const int lane = threadIdx.x;
+    __shared__ uint64_t lists[2][kScoreParts * PARARNN_TOP_MAX];
     const int64_t n = blockIdx.x, first = n * A.parts;
-    const float c = A.scale * kLog2e;
+    const int lane = threadIdx.x % kWave;
+    for (int t = threadIdx.x; t < A.parts * A.top; t += kJoinThreads)
+        lists[0][t] = A.part_keys[first * A.top + t];
     Stats a = no_stats();
     if (lane < A.parts) {
         const float4 v = A.part_stats[first + lane];
         a = {v.x, v.y, v.z};
     }
-    a = wave_join(a, c);
-    TopList list;
-    list.start(A.top, 0);
-    if (A.top) {
-        constexpr int U = 8;
-        for (int p = 0; p < A.parts; p += U) {
-            uint64_t k[U];
-#pragma unroll
-            for (int q = 0; q < U; ++q)
-                k[q] = lane < A.top && p + q < A.parts ? A.part_keys[(first + p + q) * A.top + lane] : 0;
-#pragma unroll
-            for (int q = 0; q < U; ++q) list.offer(k[q]);
-        }
-    }
-    write_scores<BF16>(A, n, a, list.key, lane);
+    a = wave_join(a, A.scale * kLog2e);
+    if (threadIdx.x == 0) write_scores<BF16>(A, n, a);
+    if (!A.top) return;
+    const uint64_t *joined = join_lists(lists[0], lists[1], A.parts, A.top, kJoinThreads);
+    if (threadIdx.x < A.top) write_top(A, n, RowScores(a), threadIdx.x, joined[threadIdx.x]);
 }
 
 // The gradient: U vectors a lane, a workgroup per kThreads * U vectors of a row.

@@ -39,23 +39,28 @@ size_t score_stats_bytes(int64_t N, int64_t parts)
     return align_up((size_t)N * parts * sizeof(float4));
 }
 
-template <bool BF16>
+template <bool BF16, bool TOP>
 hipError_t run_score(const ScoreArgs &A, hipStream_t st)
 {
     const dim3 grid((unsigned)(A.N * A.parts)), wide(kScoreThreads), one(kWave);
     if (A.parts > 1) {
-        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, true>), grid, wide, 0, st, A);
+        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, true, TOP>), grid, wide, 0, st, A);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((score_join_kernel<BF16>), dim3((unsigned)A.N), dim3(kJoinThreads), 0, st,
                            A);
     } else if (A.V <= 2048) {
         // a row of one to a few vectors a lane: no barriers between waves
-        hipLaunchKernelGGL((score_kernel<BF16, 1, false>), grid, one, 0, st, A);
+        hipLaunchKernelGGL((score_kernel<BF16, 1, false, TOP>), grid, one, 0, st, A);
     } else {
-        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, false>), grid, wide, 0, st, A);
+        hipLaunchKernelGGL((score_kernel<BF16, kScoreWaves, false, TOP>), grid, wide, 0, st, A);
     }
     return hipGetLastError();
+}
+template <bool BF16>
+hipError_t run_score(const ScoreArgs &A, hipStream_t st)
+{
+    return A.top ? run_score<BF16, true>(A, st) : run_score<BF16, false>(A, st);
 }
 
 }  // namespace

@@ -103,12 +103,27 @@ __device__ __forceinline__ Stats wave_join(Stats a, float c)
     }
     return a;
 }
-template <int K>
-__device__ __forceinline__ void add_stats(Stats &a, const float (&x)[K], float c)
+// The two vectors of a lane with the largest logits, and the largest logit of
+// all its other ones (the first one's is the statistics' m).
+struct BestVectors {
+    float second, rest;
+    int first_at, second_at;  // -1: none
+};
+template <int K, bool TOP>
+__device__ __forceinline__ void add_stats(Stats &a, BestVectors &v, const float (&x)[K], int at,
+                                          float c)
 {
-    float m = a.m;
+    float m = x[0];
 #pragma unroll
-    for (int k = 0; k < K; ++k) m = fmaxf(m, x[k]);
+    for (int k = 1; k < K; ++k) m = fmaxf(m, x[k]);
+    if constexpr (TOP) {
+        const bool over_first = m > a.m, over_second = m > v.second;
+        v.rest = fmaxf(v.rest, fminf(v.second, m));
+        v.second_at = over_first ? v.first_at : over_second ? at : v.second_at;
+        v.second = over_first ? a.m : over_second ? m : v.second;
+        v.first_at = over_first ? at : v.first_at;
+    }
+    m = fmaxf(a.m, m);
     rebase(a, m, c);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -284,20 +299,21 @@ __device__ __forceinline__ void write_top(const ScoreArgs &A, int64_t n, const R
 // One workgroup of WAVES waves per row, or per part of a row (PARTS).
 // Statistics: every lane keeps its own running maximum and sums over its
 // vectors; one pass over the row, joined across lanes and waves at the end.
-// Alternatives: a lane's running maximum is the best of its own elements, so
-// the top-th best of the lanes' maxima is a lower bound of the top-th best
-// logit.  Only lanes whose maximum reaches the bound (about `top` of them) read
-// their vectors again, from the cache, and offer what reaches it to the wave's
-// list; the waves' lists are joined at the end.
-template <bool BF16, int WAVES, bool PARTS>
+// Alternatives (TOP): a lane's maximum is the best of its own elements, so the
+// top-th best of the lanes' maxima is a lower bound of the top-th best logit.
+// Of its vectors a lane remembers the two with the largest logits, and the
+// largest logit of the others: only the vectors that reach the bound are read
+// again, and a lane goes through all its vectors again only if the others
+// reach it.  What reaches it is offered to the wave's list, and the waves'
+// lists are joined at the end.
+template <bool BF16, int WAVES, bool PARTS, bool TOP>
 __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
 {
     using Row = RowView<BF16>;
     constexpr int K = Row::K, U = kScoreUnroll, kThreads = WAVES * kWave;
     __shared__ Stats part[WAVES];
-    __shared__ float maxima[kThreads];
-    __shared__ uint64_t lists[2][WAVES * PARARNN_TOP_MAX];
-    __shared__ uint32_t bound_lds;
+    __shared__ float maxima[TOP ? kThreads : 1];
+    __shared__ uint64_t lists[2][TOP ? WAVES * PARARNN_TOP_MAX : 1];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
     const int64_t p = PARTS ? blockIdx.x - n * A.parts : 0;
@@ -307,65 +323,69 @@ __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
     const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
 
     Stats a = no_stats();
+    BestVectors best = {a.m, a.m, -1, -1};
     int64_t i = v0 + threadIdx.x;
     for (; i + (U - 1) * kThreads < v1; i += U * kThreads) {
         float x[U][K];
 #pragma unroll
         for (int q = 0; q < U; ++q) row.load(i + q * kThreads, x[q]);
 #pragma unroll
-        for (int q = 0; q < U; ++q) add_stats<K>(a, x[q], c);
+        for (int q = 0; q < U; ++q) add_stats<K, TOP>(a, best, x[q], (int)i + q * kThreads, c);
     }
     for (; i < v1; i += kThreads) {
         float x[K];
         row.load(i, x);
-        add_stats<K>(a, x, c);
+        add_stats<K, TOP>(a, best, x, (int)i, c);
     }
     const Stats joined = wave_join(a, c);
     if (lane == 0) part[wave] = joined;
-    if (A.top) maxima[threadIdx.x] = a.m;
+    if constexpr (TOP) maxima[threadIdx.x] = a.m;
     __syncthreads();
-    TopList list;
-    list.start(A.top, 0);
-    if (A.top) {
-        if (wave == 0) {
-            // the top-th best maximum, rounded down to 16 bits of its order
-            uint32_t o[WAVES], bound = 0;
+    [[maybe_unused]] TopList list;
+    if constexpr (TOP) {
+        // the top-th best maximum, rounded down to 16 bits of its order
+        uint32_t o[WAVES], bound = 0;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) o[w] = ordered(maxima[w * kWave + lane]);
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t trial = bound | 1u << bit;
-                int count = 0;
+        for (int w = 0; w < WAVES; ++w) o[w] = ordered(maxima[w * kWave + lane]);
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t trial = bound | 1u << bit;
+            int count = 0;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) count += __popcll(__ballot(o[w] >= trial));
-                if (count >= A.top) bound = trial;
-            }
-            if (lane == 0) bound_lds = bound;
+            for (int w = 0; w < WAVES; ++w) count += __popcll(__ballot(o[w] >= trial));
+            if (count >= A.top) bound = trial;
         }
-        __syncthreads();
-        const uint32_t bound = bound_lds;
         const uint64_t low = bound ? ((uint64_t)bound << 32) - 1 : 0;
         list.start(A.top, low > kMaskedFloor ? low : kMaskedFloor);
-        const bool mine = ordered(a.m) >= bound;
-        if (__ballot(mine))
+        const auto offer = [&](const uint4 &raw, int64_t vector) {
+            float x[K], m = -__builtin_inff();
+            Row::values(raw, x);
+#pragma unroll
+            for (int k = 0; k < K; ++k) m = fmaxf(m, x[k]);
+            if (!__ballot(ordered(m) >= (uint32_t)(list.floor >> 32))) return;
+            const int64_t e = row.element(vector);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                list.offer(may_be_top(x[k]) ? top_key(x[k], (uint32_t)(e + k)) : 0);
+        };
+        const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);  // NaN: no alternative
+        uint4 raw[2] = {none, none};
+        if (best.first_at >= 0 && ordered(a.m) >= bound) raw[0] = row.load_raw(best.first_at);
+        if (best.second_at >= 0 && ordered(best.second) >= bound) raw[1] = row.load_raw(best.second_at);
+        offer(raw[0], best.first_at);
+        offer(raw[1], best.second_at);
+        const bool again = ordered(best.rest) >= bound;
+        if (__ballot(again))
             for (int64_t j = v0 + threadIdx.x; __ballot(j < v1); j += kScoreAgain * kThreads) {
-                uint4 raw[kScoreAgain];
+                uint4 more[kScoreAgain];
 #pragma unroll
                 for (int q = 0; q < kScoreAgain; ++q) {
-                    raw[q] = make_uint4(~0u, ~0u, ~0u, ~0u);  // NaN: no alternative
-                    if (mine && j + q * kThreads < v1) raw[q] = row.load_raw(j + q * kThreads);
+                    const int64_t jq = j + q * kThreads;
+                    more[q] = none;
+                    if (again && jq < v1 && jq != best.first_at && jq != best.second_at)
+                        more[q] = row.load_raw(jq);
                 }
 #pragma unroll
-                for (int q = 0; q < kScoreAgain; ++q) {
-                    float x[K], best = -__builtin_inff();
-                    Row::values(raw[q], x);
-#pragma unroll
-                    for (int k = 0; k < K; ++k) best = fmaxf(best, x[k]);
-                    if (!__ballot(ordered(best) >= (uint32_t)(list.floor >> 32))) continue;
-                    const int64_t e = row.element(j + q * kThreads);
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        list.offer(may_be_top(x[k]) ? top_key(x[k], (uint32_t)(e + k)) : 0);
-                }
+                for (int q = 0; q < kScoreAgain; ++q) offer(more[q], j + q * kThreads);
             }
     }
     // the workgroup's statistics, in every thread
@@ -377,17 +397,17 @@ __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
     } else {
         if (threadIdx.x == 0) write_scores<BF16>(A, n, a);
     }
-    if (!A.top) return;
+    if constexpr (!TOP) return;
     [[maybe_unused]] const RowScores scores(a);
-    const auto put = [&](int place, uint64_t key) {
+    [[maybe_unused]] const auto put = [&](int place, uint64_t key) {
         if constexpr (PARTS)
             A.part_keys[(int64_t)blockIdx.x * A.top + place] = key;
         else
             write_top(A, n, scores, place, key);
     };
-    if constexpr (WAVES == 1) {
+    if constexpr (TOP && WAVES == 1) {
         if (lane < A.top) put(lane, list.key);
-    } else {
+    } else if constexpr (TOP) {
         if (lane < A.top) lists[0][wave * A.top + lane] = list.key;
         const uint64_t *joined = join_lists(lists[0], lists[1], WAVES, A.top, kThreads);
         if (threadIdx.x < A.top) put(threadIdx.x, joined[threadIdx.x]);

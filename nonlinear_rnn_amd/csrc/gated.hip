@@ -40,11 +40,14 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     // (a dispatch counts its work-items in 32 bits: 64 a channel)
     if (T > 16 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
         // one wave per channel where the channels fill the device, else the
-        // channel's steps over more waves, and over several workgroups where
-        // that is not enough
-        pl.waves = C >= kFull || T <= 64 * kStepsBf16 ? 1 : C >= kFull / 4 || T <= 256 * kStepsBf16 ? 4 : 16;
+        // channel's steps over 4 or 8 waves, and over workgroups where those
+        // leave the device less than full (spans read their projections twice:
+        // then as many as 32 waves a CU)
+        pl.waves = C >= kFull || T <= 64 * kStepsBf16       ? 1
+                   : C >= kFull / 4 || T <= 256 * kStepsBf16 ? 4
+                                                             : 8;
         unit = (int64_t)pl.waves * kWave * kStepsBf16;
-        nseg = C > 0 ? (kFull + C * pl.waves - 1) / (C * pl.waves) : 1;
+        if (C > 0 && C * pl.waves < kFull) nseg = (4 * kFull + C * pl.waves - 1) / (C * pl.waves);
         nseg = std::min(nseg, (T + 2 * unit - 1) / (2 * unit));
     } else {
         // a lane per channel: spans of at least 64 steps
@@ -110,7 +113,8 @@ hipError_t launch_gated(const GatedArgs &A, int waves, hipStream_t st)
 {
     constexpr int K = BF16 ? kStepsBf16 : kStepsF32;
     const int64_t groups = waves ? A.channels : (A.channels + kWave - 1) / kWave;
-    const dim3 grid((unsigned)groups, (unsigned)A.nseg),
+    // (the last span's map, or backwards the first one's, is nobody's carry)
+    const dim3 grid((unsigned)groups, (unsigned)(A.nseg - (AGG ? 1 : 0))),
         block((unsigned)(kWave * (waves ? waves : 1)));
 #define PARARNN_GATED(NAME, ...)                                                                 \
     if constexpr (ADJ)                                                                           \
@@ -118,7 +122,7 @@ hipError_t launch_gated(const GatedArgs &A, int waves, hipStream_t st)
     else                                                                                         \
         hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), grid, block, 0, st, A)
     switch (waves) {
-    case 16: PARARNN_GATED(time, BF16, K, 16, AGG); break;
+    case 8: PARARNN_GATED(time, BF16, K, 8, AGG); break;
     case 4: PARARNN_GATED(time, BF16, K, 4, AGG); break;
     case 1: PARARNN_GATED(time, BF16, K, 1, AGG); break;
     default: PARARNN_GATED(channel, BF16, AGG); break;

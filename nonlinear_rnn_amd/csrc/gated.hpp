@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
     const int64_t ch = (int64_t)blockIdx.x * kWave + threadIdx.x;
     if (ch >= A.channels) return;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y;
+    const int32_t seg = blockIdx.y + (AGG ? 1 : 0);
     const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
     __shared__ float sums[W];
     const int64_t ch = blockIdx.x;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y;
+    const int32_t seg = blockIdx.y + (AGG ? 1 : 0);
     const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const int wave = threadIdx.x / kWave;
     constexpr int P = K * W * kWave;

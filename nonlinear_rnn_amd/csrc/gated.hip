@@ -38,7 +38,7 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     constexpr int64_t kFull = 8 * kComputeUnits;  // waves that fill the device
     int64_t nseg = 1, unit = 1;
     // (a dispatch counts its work-items in 32 bits: 64 a channel)
-    if (T > 16 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
+    if (T > 2 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
         // one wave per channel where the channels fill the device, else the
         // channel's steps over 4 or 8 waves, and over workgroups where those
         // leave the device less than full (spans read their projections twice:
@@ -121,6 +121,21 @@ hipError_t launch_gated(const GatedArgs &A, int waves, hipStream_t st)
         hipLaunchKernelGGL((gated_##NAME##_adjoint_kernel<__VA_ARGS__>), grid, block, 0, st, A); \
     else                                                                                         \
         hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), grid, block, 0, st, A)
+    if constexpr (!AGG)
+        if (waves == 1 && A.nseg == 1 && A.T <= 16 * K) {
+            const int lanes = A.T <= 4 * K ? 4 : 16;
+            const dim3 few((unsigned)((A.channels * lanes + kShortThreads - 1) / kShortThreads)),
+                wide(kShortThreads);
+            if (lanes == 4 && ADJ)
+                hipLaunchKernelGGL((gated_short_adjoint_kernel<BF16, K, 4>), few, wide, 0, st, A);
+            else if (lanes == 4)
+                hipLaunchKernelGGL((gated_short_kernel<BF16, K, 4>), few, wide, 0, st, A);
+            else if (ADJ)
+                hipLaunchKernelGGL((gated_short_adjoint_kernel<BF16, K, 16>), few, wide, 0, st, A);
+            else
+                hipLaunchKernelGGL((gated_short_kernel<BF16, K, 16>), few, wide, 0, st, A);
+            return hipGetLastError();
+        }
     switch (waves) {
     case 8: PARARNN_GATED(time, BF16, K, 8, AGG); break;
     case 4: PARARNN_GATED(time, BF16, K, 4, AGG); break;

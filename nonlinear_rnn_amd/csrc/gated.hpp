@@ -462,6 +462,107 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
     }
 }
 
+// --------------------------------------------------- lanes in time, short ---
+// At most G K steps: G lanes a channel and 64 / G channels a wave, each lane's
+// K steps in one access as above.  (With a wave a channel, T = 100 of 64000
+// channels left 7 of 8 lanes idle.)
+constexpr int kShortThreads = 256;
+
+// Inclusive scan of the maps over groups of G neighbouring lanes, each group's
+// first lane first (its last, REVERSE); then the map in front of the lane's own.
+template <int G, bool REVERSE>
+__device__ __forceinline__ Map1 group_scan_exclusive(Map1 x)
+{
+    const int lane = threadIdx.x % G, at = REVERSE ? G - 1 - lane : lane;
+#pragma unroll
+    for (int o = 1; o < G; o *= 2) {
+        const Map1 y = REVERSE ? Map1{__shfl_down(x.a, o), __shfl_down(x.b, o)}
+                               : Map1{__shfl_up(x.a, o), __shfl_up(x.b, o)};
+        if (at >= o) x = compose(x, y);
+    }
+    const Map1 y = REVERSE ? Map1{__shfl_down(x.a, 1), __shfl_down(x.b, 1)}
+                           : Map1{__shfl_up(x.a, 1), __shfl_up(x.b, 1)};
+    return at > 0 ? y : Map1{1.0f, 0.0f};
+}
+
+template <bool BF16, int K, int G>
+__global__ void __launch_bounds__(kShortThreads) gated_short_kernel(GatedArgs A)
+{
+    const int64_t ch = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) / G;
+    const bool here = ch < A.channels;  // the others follow along for the shuffles
+    const int64_t b = here ? ch / A.D : 0, d = here ? ch - b * A.D : 0;
+    const int64_t t = (int64_t)(threadIdx.x % G) * K, end = here ? A.T : 0;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+    const GatedChunk<K, BF16> c = load_chunk<K, BF16>(A, uo, rs, t, end);
+    const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
+    Map1 m[K], own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        m[k] = gated_map(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
+        m[k] = keep_or_identity(m[k], t + k < end);
+        own = compose(m[k], own);
+    }
+    const Map1 prior = group_scan_exclusive<G, false>(own);
+    float h = fmaf_(prior.a, h0, prior.b), out[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) out[k] = h = fmaf_(m[k].a, h, m[k].b);
+    if (t >= end) return;
+    store_raw<false, K>(A.h, so, t, end, out);
+    if (A.h_last)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (t + k == A.T - 1) A.h_last[ch] = out[k];
+}
+
+template <bool BF16, int K, int G>
+__global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(GatedArgs A)
+{
+    const int64_t ch = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) / G;
+    const bool here = ch < A.channels;
+    const int64_t b = here ? ch / A.D : 0, d = here ? ch - b * A.D : 0;
+    const int64_t t = (int64_t)(threadIdx.x % G) * K, end = here ? A.T : 0;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+    const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
+    const GatedBackChunk<K, BF16> c = load_back<K, BF16, false>(A, uo, so, rs, t, 0, end, h0);
+    const float after = A.gh_last && here ? A.gh_last[ch] : 0.0f;
+    Decay v[K];
+    Map1 own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        v[k] = decay(rate, c.u[0].get(k));
+        const float ka = c.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
+        own = compose(keep_or_identity(Map1{ka, ka * c.gh.get(k)}, t + k < end), own);
+    }
+    const Map1 prior = group_scan_exclusive<G, true>(own);
+    float w = fmaf_(prior.a, after, prior.b);
+    float hp = __shfl_up(c.h.get(K - 1), 1);
+    if (threadIdx.x % G == 0) hp = h0;
+    float gr[K], gi[K], gx[K], dlam = 0.0f;
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        const bool cut = c.cut >> k & 1u, in = t + k < end;
+        const float g_total = c.gh.get(k) + w;
+        const GatedGrad g = gated_grad(v[k], c.u[1].get(k), c.u[2].get(k), cut, g_total,
+                                       k ? c.h.get(k ? k - 1 : 0) : hp);
+        gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
+        dlam += in ? g.lam : 0.0f;
+        w = in ? (cut ? 0.0f : (1.0f - v[k].m) * g_total) : w;
+    }
+#pragma unroll
+    for (int o = 1; o < G; o *= 2) dlam += __shfl_xor(dlam, o);
+    if (t >= end) return;
+    store_raw<BF16, K>(A.du[0], uo, t, end, gr);
+    store_raw<BF16, K>(A.du[1], uo, t, end, gi);
+    store_raw<BF16, K>(A.du[2], uo, t, end, gx);
+    if (t > 0) return;
+    if (A.dh0) A.dh0[ch] = w;
+    A.dlam_part[b * A.D + d] = dlam;  // one span
+}
+
 // dL/dlam = -power sig(lam) sum (dL/dl sig(u_r)), the partial sums of the
 // batch rows and spans added in a fixed order.
 __global__ void gated_dlam_kernel(GatedArgs A)

@@ -63,6 +63,7 @@ def close(got, exact, tol, bf16=False):
 
 
 SHAPES = [(1, 1, 1), (2, 1, 130), (1, 2, 3), (3, 7, 65), (2, 63, 5), (2, 64, 64), (1, 65, 2),
+          (3, 4, 20), (2, 16, 70), (2, 17, 33), (2, 32, 9), (1, 33, 130), (2, 128, 21),
           (2, 300, 33), (1, 513, 9), (2, 1025, 3), (1, 4100, 2), (1, 20011, 1), (5, 129, 200)]
 
 

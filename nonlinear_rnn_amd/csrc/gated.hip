@@ -17,14 +17,18 @@ namespace {
 // plane.
 constexpr int kStepsBf16 = 8, kStepsF32 = 4;
 
-// Which kernel, and how the time axis is cut: spans per channel and their
-// length.
+// Which kernel, and how the time axis is cut.
+enum GatedKernel { kLanePerChannel, kWavePerChannel, kGroupPerChannel, kLookBack };
+constexpr int kLookWaves = 8;
 struct GatedPlan {
-    int64_t channels = 0, seg_len = 0;
+    GatedKernel kernel = kLanePerChannel;
+    int64_t channels = 0;
+    int64_t seg_len = 0;   // a lane per channel: spans
     int32_t nseg = 1;
-    int waves = 0;  // per channel, lanes in time; 0: a lane per channel
-    size_t agg = 0, part = 0, total = 0;  // workspace: span maps, dlam partial sums
+    size_t records = 0, words = 0;  // look back: the records' place, words in all
+    size_t part = 0, total = 0;  // workspace: span maps or records, then dlam partial sums
 };
+int64_t chunks_of(int64_t T, int steps) { return (T + kLookWaves * kWave * steps - 1) / (kLookWaves * kWave * steps); }
 
 // The plan goes by the shape alone (not by the dtype), so that a workspace
 // serves either.
@@ -36,33 +40,37 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     pl.channels = sh->B * sh->D;
     const int64_t C = pl.channels, T = sh->T;
     constexpr int64_t kFull = 8 * kComputeUnits;  // waves that fill the device
-    int64_t nseg = 1, unit = 1;
+    int64_t rows = sh->B;  // of dlam partial sums
     // (a dispatch counts its work-items in 32 bits: 64 a channel)
     if (T > 2 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
-        // one wave per channel where the channels fill the device, else the
-        // channel's steps over 4 or 8 waves, and over workgroups where those
-        // leave the device less than full (spans read their projections twice:
-        // then as many as 32 waves a CU)
-        pl.waves = C >= kFull || T <= 64 * kStepsBf16       ? 1
-                   : C >= kFull / 4 || T <= 256 * kStepsBf16 ? 4
-                                                             : 8;
-        unit = (int64_t)pl.waves * kWave * kStepsBf16;
-        if (C > 0 && C * pl.waves < kFull) nseg = (4 * kFull + C * pl.waves - 1) / (C * pl.waves);
-        nseg = std::min(nseg, (T + 2 * unit - 1) / (2 * unit));
+        // a wave per channel where the channels fill the device or are short;
+        // else 4 waves, and where those do not fill it either, a channel's
+        // chunks side by side (B=1 T=262144 D=64 float32: 84 us in two launches
+        // that each read the projections)
+        const int64_t chunks = chunks_of(T, kStepsF32);
+        pl.kernel = C >= kFull || T <= kWave * kStepsBf16 ? kWavePerChannel
+                    : C >= kFull / 4 || chunks <= 1       ? kGroupPerChannel
+                                                          : kLookBack;
+        // fewer than kFull / 4 channels: the ticket's 32 bits hold their chunks
+        // unless a channel has millions
+        if (pl.kernel == kLookBack && C * chunks >= (int64_t(1) << 23)) pl.kernel = kGroupPerChannel;
+        if (pl.kernel == kLookBack) {
+            pl.records = align_up((size_t)C * kTicketWords * sizeof(uint32_t));
+            pl.part = align_up(pl.records + (size_t)(C * chunks) * sizeof(GatedRecord));
+            pl.words = pl.part / sizeof(uint64_t);
+            rows = sh->B * chunks;
+        }
     } else {
         // a lane per channel: spans of at least 64 steps
         const int64_t waves = (C + kWave - 1) / kWave;
-        nseg = waves > 0 ? 2 * kFull / waves : 1;
-        nseg = std::min(nseg, (T + 63) / 64);
+        int64_t nseg = waves > 0 ? 2 * kFull / waves : 1;
+        nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, (T + 63) / 64, 4096}));
+        pl.seg_len = std::max<int64_t>(1, (T + nseg - 1) / nseg);
+        pl.nseg = (int32_t)std::max<int64_t>(1, (T + pl.seg_len - 1) / pl.seg_len);
+        pl.part = pl.nseg > 1 ? align_up((size_t)pl.nseg * C * sizeof(float2)) : 0;
+        rows = sh->B * pl.nseg;
     }
-    nseg = std::max<int64_t>(1, std::min<int64_t>(nseg, 4096));
-    pl.seg_len = std::max<int64_t>(unit, ((T + nseg - 1) / nseg + unit - 1) / unit * unit);
-    pl.nseg = (int32_t)std::max<int64_t>(1, (T + pl.seg_len - 1) / pl.seg_len);
-    pl.agg = 0;
-    size_t off = pl.nseg > 1 ? align_up((size_t)pl.nseg * C * sizeof(float2)) : 0;
-    pl.part = off;
-    if (adjoint) off = align_up(off + (size_t)sh->B * pl.nseg * sh->D * sizeof(float));
-    pl.total = off;
+    pl.total = adjoint ? align_up(pl.part + (size_t)rows * sh->D * sizeof(float)) : pl.part;
     return PARARNN_OK;
 }
 
@@ -75,7 +83,9 @@ void gated_args(GatedArgs &A, const pararnn_shape_t *sh, const GatedPlan &pl, co
     A.power = power;
     A.h0 = h0;
     A.resets = resets;
-    A.agg = reinterpret_cast<float2 *>(static_cast<char *>(ws) + pl.agg);
+    A.agg = static_cast<float2 *>(ws);
+    A.ticket = static_cast<uint32_t *>(ws);
+    A.records = reinterpret_cast<GatedRecord *>(static_cast<char *>(ws) + pl.records);
     A.seg_len = pl.seg_len;
     A.nseg = pl.nseg;
     A.B = sh->B;
@@ -107,56 +117,61 @@ pararnn_status_t check_gated(const pararnn_shape_t *sh, const GatedPlan &pl, con
     return PARARNN_OK;
 }
 
-// One launch over (channels or groups of 64 of them) x spans.
-template <bool ADJ, bool BF16, bool AGG>
-hipError_t launch_gated(const GatedArgs &A, int waves, hipStream_t st)
+#define PARARNN_GATED(NAME, GRID, BLOCK, ...)                                                    \
+    if constexpr (ADJ)                                                                           \
+        hipLaunchKernelGGL((gated_##NAME##_adjoint_kernel<__VA_ARGS__>), GRID, BLOCK, 0, st, A); \
+    else                                                                                         \
+        hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), GRID, BLOCK, 0, st, A)
+
+// `rows`: of dlam partial sums.
+template <bool ADJ, bool BF16>
+hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, int64_t &rows, hipStream_t st)
 {
     constexpr int K = BF16 ? kStepsBf16 : kStepsF32;
-    const int64_t groups = waves ? A.channels : (A.channels + kWave - 1) / kWave;
-    // (the last span's map, or backwards the first one's, is nobody's carry)
-    const dim3 grid((unsigned)groups, (unsigned)(A.nseg - (AGG ? 1 : 0))),
-        block((unsigned)(kWave * (waves ? waves : 1)));
-#define PARARNN_GATED(NAME, ...)                                                                 \
-    if constexpr (ADJ)                                                                           \
-        hipLaunchKernelGGL((gated_##NAME##_adjoint_kernel<__VA_ARGS__>), grid, block, 0, st, A); \
-    else                                                                                         \
-        hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), grid, block, 0, st, A)
-    if constexpr (!AGG)
-        if (waves == 1 && A.nseg == 1 && A.T <= 16 * K) {
-            const int lanes = A.T <= 4 * K ? 4 : 16;
-            const dim3 few((unsigned)((A.channels * lanes + kShortThreads - 1) / kShortThreads)),
-                wide(kShortThreads);
-            if (lanes == 4 && ADJ)
-                hipLaunchKernelGGL((gated_short_adjoint_kernel<BF16, K, 4>), few, wide, 0, st, A);
-            else if (lanes == 4)
-                hipLaunchKernelGGL((gated_short_kernel<BF16, K, 4>), few, wide, 0, st, A);
-            else if (ADJ)
-                hipLaunchKernelGGL((gated_short_adjoint_kernel<BF16, K, 16>), few, wide, 0, st, A);
-            else
-                hipLaunchKernelGGL((gated_short_kernel<BF16, K, 16>), few, wide, 0, st, A);
-            return hipGetLastError();
+    rows = A.B * A.nseg;
+    switch (pl.kernel) {
+    case kLanePerChannel: {
+        const unsigned groups = (unsigned)((A.channels + kWave - 1) / kWave);
+        if (A.nseg > 1) {
+            // (the last span's map, or backwards the first one's, is nobody's carry)
+            PARARNN_GATED(channel, dim3(groups, (unsigned)A.nseg - 1), dim3(kWave), BF16, true);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
-    switch (waves) {
-    case 8: PARARNN_GATED(time, BF16, K, 8, AGG); break;
-    case 4: PARARNN_GATED(time, BF16, K, 4, AGG); break;
-    case 1: PARARNN_GATED(time, BF16, K, 1, AGG); break;
-    default: PARARNN_GATED(channel, BF16, AGG); break;
+        PARARNN_GATED(channel, dim3(groups, (unsigned)A.nseg), dim3(kWave), BF16, false);
+        break;
     }
-#undef PARARNN_GATED
+    case kWavePerChannel:
+        if (A.T <= 16 * K) {  // several channels a wave
+            const int lanes = A.T <= 4 * K ? 4 : 16;
+            const dim3 grid((unsigned)((A.channels * lanes + kShortThreads - 1) / kShortThreads));
+            if (lanes == 4) {
+                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, K, 4);
+            } else {
+                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, K, 16);
+            }
+        } else {
+            PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(kWave), BF16, K, 1);
+        }
+        break;
+    case kGroupPerChannel:
+        PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(4 * kWave), BF16, K, 4);
+        break;
+    case kLookBack: {
+        const int64_t chunks = chunks_of(A.T, K);
+        rows = A.B * chunks;
+        hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)((pl.words + 255) / 256)), dim3(256),
+                           0, st, A, (int64_t)pl.words);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        PARARNN_GATED(look, dim3((unsigned)(A.channels * chunks)), dim3(kLookWaves * kWave), BF16, K,
+                      kLookWaves);
+        break;
+    }
+    }
     return hipGetLastError();
 }
-
-template <bool ADJ>
-hipError_t run_gated(const GatedArgs &A, int waves, bool bf16, hipStream_t st)
-{
-    if (A.nseg > 1) {
-        const hipError_t e = bf16 ? launch_gated<ADJ, true, true>(A, waves, st)
-                                  : launch_gated<ADJ, false, true>(A, waves, st);
-        if (e != hipSuccess) return e;
-    }
-    return bf16 ? launch_gated<ADJ, true, false>(A, waves, st)
-                : launch_gated<ADJ, false, false>(A, waves, st);
-}
+#undef PARARNN_GATED
 
 }  // namespace
 
@@ -184,8 +199,10 @@ pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *co
     gated_args(A, shape, pl, u, lam, power, h0, resets, ws);
     A.h = h;
     A.h_last = h_last;
-    const hipError_t e =
-        run_gated<false>(A, pl.waves, u_dtype == PARARNN_BF16, static_cast<hipStream_t>(stream));
+    hipStream_t strm = static_cast<hipStream_t>(stream);
+    int64_t rows;
+    const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<false, true>(A, pl, rows, strm)
+                                                 : run_gated<false, false>(A, pl, rows, strm);
     return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
@@ -218,11 +235,14 @@ pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const 
     A.dlam = dlam;
     A.dh0 = dh0;
     A.dlam_part = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part);
-    if (pl.channels > 0 && run_gated<true>(A, pl.waves, u_dtype == PARARNN_BF16, strm) != hipSuccess)
-        return PARARNN_ERR_HIP;
-    const int tpb = 256;  // no batch rows: a sum of no terms
-    hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + tpb - 1) / tpb)), dim3(tpb),
-                       0, strm, A);
+    int64_t rows = 0;  // no batch rows: a sum of no terms
+    if (pl.channels > 0) {
+        const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<true, true>(A, pl, rows, strm)
+                                                     : run_gated<true, false>(A, pl, rows, strm);
+        if (e != hipSuccess) return PARARNN_ERR_HIP;
+    }
+    hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + kWave - 1) / kWave)),
+                       dim3(kDlamWaves * kWave), 0, strm, A, rows);
     return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 

@@ -33,9 +33,11 @@ struct GatedArgs {
     const float *gh_last;   // or null
     void *du[3];
     float *dlam, *dh0;
-    float *dlam_part;       // [B][nseg][D]
-    // spans of the time axis
+    float *dlam_part;       // [B][nseg][D], look back: [place][B][D]
+    // the time axis in parts: spans (a lane per channel) or chunks (look back)
     float2 *agg;            // [nseg][channels]
+    uint32_t *ticket;       // a line a channel
+    struct GatedRecord *records;  // [place][channels]
     int64_t seg_len;
     int32_t nseg;
     float power;
@@ -264,74 +266,78 @@ __device__ __forceinline__ float through_waves(const Map1 *maps, int wave, float
     }
     return mine;
 }
+template <int W>
+__device__ __forceinline__ Map1 all_waves(const Map1 *maps)
+{
+    Map1 m = maps[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = compose(maps[w], m);
+    return m;
+}
 
-template <bool BF16, int K, int W, bool AGG>
+// A lane's maps, and their composition.
+template <int K, bool BF16>
+__device__ __forceinline__ Map1 chunk_maps(const GatedChunk<K, BF16> &c, float rate, int64_t t,
+                                           int64_t end, Map1 (&m)[K])
+{
+    Map1 own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        m[k] = gated_map(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
+        m[k] = keep_or_identity(m[k], t + k < end);
+        own = compose(m[k], own);
+    }
+    return own;
+}
+// A lane's states from the one before them; returns the last.
+template <int K>
+__device__ __forceinline__ float chunk_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
+                                              const Map1 (&m)[K], float h)
+{
+    float out[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) out[k] = h = fmaf_(m[k].a, h, m[k].b);
+    if (t >= A.T) return h;
+    store_raw<false, K>(A.h, so, t, A.T, out);
+    if (A.h_last && t + K >= A.T)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (t + k == A.T - 1) A.h_last[ch] = out[k];
+    return h;
+}
+
+// Every channel's steps one chunk after the other, in one workgroup.
+template <bool BF16, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_time_kernel(GatedArgs A)
 {
     __shared__ Map1 maps[2][W];
     const int64_t ch = blockIdx.x;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y;
-    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const int wave = threadIdx.x / kWave;
     constexpr int P = K * W * kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
-
-    Map1 span = {1.0f, 0.0f};
     float carry = A.h0 ? A.h0[ch] : 0.0f;
-    if constexpr (!AGG)
-        for (int32_t j = 0; j < seg; ++j) {
-            const float2 m = A.agg[(int64_t)j * A.channels + ch];
-            carry = fmaf_(m.x, carry, m.y);
-        }
-    int64_t t = t0 + (int64_t)threadIdx.x * K;
-    GatedChunk<K, BF16> now = load_chunk<K, BF16>(A, uo, rs, t, t1);
+    int64_t t = (int64_t)threadIdx.x * K;
+    GatedChunk<K, BF16> now = load_chunk<K, BF16>(A, uo, rs, t, A.T);
     int parity = 0;
-    for (int64_t c = t0; c < t1; c += P, t += P, parity ^= 1) {
+    for (int64_t c = 0; c < A.T; c += P, t += P, parity ^= 1) {
         GatedChunk<K, BF16> next;
-        if (c + P < t1) next = load_chunk<K, BF16>(A, uo, rs, t + P, t1);
-        Map1 m[K], own = {1.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            m[k] = gated_map(rate, now.u[0].get(k), now.u[1].get(k), now.u[2].get(k),
-                             now.cut >> k & 1u);
-            m[k] = keep_or_identity(m[k], t + k < t1);
-            own = compose(m[k], own);
-        }
-        const Map1 upto = wave_scan_inclusive(own);
+        if (c + P < A.T) next = load_chunk<K, BF16>(A, uo, rs, t + P, A.T);
+        Map1 m[K];
+        const Map1 upto = wave_scan_inclusive(chunk_maps<K, BF16>(now, rate, t, A.T, m));
         float before = carry;
         if constexpr (W > 1) {
             if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
             __syncthreads();
-            if constexpr (AGG) {
-#pragma unroll
-                for (int w = 0; w < W; ++w) span = compose(maps[parity][w], span);
-            } else {
-                before = through_waves<W>(maps[parity], wave, carry);
-            }
-        } else if constexpr (AGG) {
-            span = compose(upto, span);  // in the last lane
+            before = through_waves<W>(maps[parity], wave, carry);
         }
-        if constexpr (!AGG) {
-            const Map1 prior = wave_shift_up(upto);
-            float h = fmaf_(prior.a, before, prior.b);
-            float out[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) out[k] = h = fmaf_(m[k].a, h, m[k].b);
-            store_raw<false, K>(A.h, so, t, t1, out);
-            if constexpr (W == 1) carry = __shfl(h, kWave - 1);
-            if (A.h_last && t < A.T && t + K >= A.T)
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (t + k == A.T - 1) A.h_last[ch] = out[k];
-        }
+        const Map1 prior = wave_shift_up(upto);
+        const float h = chunk_states<K>(A, so, ch, t, m, fmaf_(prior.a, before, prior.b));
+        if constexpr (W == 1) carry = __shfl(h, kWave - 1);
         now = next;
     }
-    if constexpr (AGG)
-        if (threadIdx.x == W * kWave - 1)
-            A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
 }
 
 // Backward: lanes run backwards in time (lane 0 holds a chunk's last steps),
@@ -343,123 +349,294 @@ struct GatedBackChunk {
     float before;  // the state in front of the wave's steps
     uint32_t cut;
 };
-template <int K, bool BF16, bool AGG>
+template <int K, bool BF16>
 __device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A, int64_t uo,
                                                              int64_t so, const uint8_t *rs,
-                                                             int64_t t, int64_t first, int64_t t1,
+                                                             int64_t t, int64_t first, int64_t end,
                                                              float h0)
 {
     GatedBackChunk<K, BF16> c;
-    c.u[0] = load_raw<BF16, K>(A.u[0], uo, t, t1);
-    if constexpr (!AGG) {
-        c.u[1] = load_raw<BF16, K>(A.u[1], uo, t, t1);
-        c.u[2] = load_raw<BF16, K>(A.u[2], uo, t, t1);
-        c.h = load_raw<false, K>(A.hs, so, t, t1);
-        c.before = first > 0 && first <= A.T ? A.hs[so + first - 1] : h0;
-    }
+#pragma unroll
+    for (int g = 0; g < 3; ++g) c.u[g] = load_raw<BF16, K>(A.u[g], uo, t, end);
+    c.h = load_raw<false, K>(A.hs, so, t, end);
+    c.before = first > 0 && first <= A.T ? A.hs[so + first - 1] : h0;
     if (A.gh) {
-        c.gh = load_raw<false, K>(A.gh, so, t, t1);
+        c.gh = load_raw<false, K>(A.gh, so, t, end);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) c.gh.w[k] = 0u;
     }
-    c.cut = rs ? load_flags<K>(rs, t, t1) : 0u;
+    c.cut = rs ? load_flags<K>(rs, t, end) : 0u;
     return c;
 }
+template <int K, bool BF16>
+__device__ __forceinline__ Map1 back_maps(const GatedBackChunk<K, BF16> &c, float rate, int64_t t,
+                                          int64_t end, Decay (&v)[K])
+{
+    Map1 own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        v[k] = decay(rate, c.u[0].get(k));
+        const float ka = c.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
+        own = compose(keep_or_identity(Map1{ka, ka * c.gh.get(k)}, t + k < end), own);
+    }
+    return own;
+}
+// A lane's gradients from the w behind them and the state before its first
+// step; returns its own w, and adds to dlam.
+template <int K, bool BF16>
+__device__ __forceinline__ float chunk_gradients(const GatedArgs &A, int64_t uo, int64_t t,
+                                                 int64_t end, const GatedBackChunk<K, BF16> &c,
+                                                 const Decay (&v)[K], float w, float hp,
+                                                 float &dlam)
+{
+    float gr[K], gi[K], gx[K];
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        const bool cut = c.cut >> k & 1u, in = t + k < end;
+        const float G = c.gh.get(k) + w;
+        const GatedGrad g = gated_grad(v[k], c.u[1].get(k), c.u[2].get(k), cut, G,
+                                       k ? c.h.get(k ? k - 1 : 0) : hp);
+        gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
+        dlam += in ? g.lam : 0.0f;
+        w = in ? (cut ? 0.0f : (1.0f - v[k].m) * G) : w;
+    }
+    if (t >= end) return w;
+    store_raw<BF16, K>(A.du[0], uo, t, end, gr);
+    store_raw<BF16, K>(A.du[1], uo, t, end, gi);
+    store_raw<BF16, K>(A.du[2], uo, t, end, gx);
+    return w;
+}
+// The workgroup's sum of dlam, in its last thread.
+template <int W>
+__device__ __forceinline__ float dlam_sum(float dlam, float *lds)
+{
+    float s = wave_sum_to_last(dlam);
+    if constexpr (W > 1) {
+        if (threadIdx.x % kWave == kWave - 1) lds[threadIdx.x / kWave] = s;
+        __syncthreads();
+        s = 0.0f;
+        for (int w = 0; w < W; ++w) s += lds[w];
+    }
+    return s;
+}
 
-template <bool BF16, int K, int W, bool AGG>
+template <bool BF16, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs A)
 {
     __shared__ Map1 maps[2][W];
     __shared__ float sums[W];
     const int64_t ch = blockIdx.x;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y + (AGG ? 1 : 0);
-    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const int wave = threadIdx.x / kWave;
     constexpr int P = K * W * kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
-
-    Map1 span = {1.0f, 0.0f};
     float carry = A.gh_last ? A.gh_last[ch] : 0.0f, dlam = 0.0f;
     const float h0 = A.h0 ? A.h0[ch] : 0.0f;
-    if constexpr (!AGG)
-        for (int32_t j = A.nseg - 1; j > seg; --j) {
-            const float2 m = A.agg[(int64_t)j * A.channels + ch];
-            carry = fmaf_(m.x, carry, m.y);
-        }
-    int64_t c = t0 + (t1 - t0 - 1) / P * P;  // the last chunk of the span
+    int64_t c = (A.T - 1) / P * P;  // the last chunk
     const int at = W * kWave - 1 - (int)threadIdx.x, wave_at = (W - 1 - wave) * kWave;
     GatedBackChunk<K, BF16> now =
-        load_back<K, BF16, AGG>(A, uo, so, rs, c + at * K, c + wave_at * K, t1, h0);
+        load_back<K, BF16>(A, uo, so, rs, c + at * K, c + wave_at * K, A.T, h0);
     int parity = 0;
-    for (; c >= t0; c -= P, parity ^= 1) {
+    for (; c >= 0; c -= P, parity ^= 1) {
         const int64_t t = c + at * K;
         GatedBackChunk<K, BF16> next;
-        if (c > t0)
-            next = load_back<K, BF16, AGG>(A, uo, so, rs, t - P, c - P + wave_at * K, t1, h0);
+        if (c > 0) next = load_back<K, BF16>(A, uo, so, rs, t - P, c - P + wave_at * K, A.T, h0);
         Decay v[K];
-        Map1 own = {1.0f, 0.0f};
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k) {
-            v[k] = decay(rate, now.u[0].get(k));
-            const float ka = now.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
-            own = compose(keep_or_identity(Map1{ka, ka * now.gh.get(k)}, t + k < t1), own);
-        }
-        const Map1 upto = wave_scan_inclusive(own);
+        const Map1 upto = wave_scan_inclusive(back_maps<K, BF16>(now, rate, t, A.T, v));
         float after = carry;
         if constexpr (W > 1) {
             if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
             __syncthreads();
-            if constexpr (AGG) {
-#pragma unroll
-                for (int w = 0; w < W; ++w) span = compose(maps[parity][w], span);
-            } else {
-                after = through_waves<W>(maps[parity], wave, carry);
-            }
-        } else if constexpr (AGG) {
-            span = compose(upto, span);
+            after = through_waves<W>(maps[parity], wave, carry);
         }
-        if constexpr (!AGG) {
-            const Map1 prior = wave_shift_up(upto);
-            float w = fmaf_(prior.a, after, prior.b);
-            // the state before the lane's first step: the next lane's last one
-            float hp0 = __shfl_down(now.h.get(K - 1), 1);
-            if (threadIdx.x % kWave == kWave - 1) hp0 = now.before;
-            float gr[K], gi[K], gx[K];
-#pragma unroll
-            for (int k = K - 1; k >= 0; --k) {
-                const bool cut = now.cut >> k & 1u, in = t + k < t1;
-                const float G = now.gh.get(k) + w;
-                const GatedGrad g = gated_grad(v[k], now.u[1].get(k), now.u[2].get(k), cut, G,
-                                               k ? now.h.get(k ? k - 1 : 0) : hp0);
-                gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
-                dlam += in ? g.lam : 0.0f;
-                w = in ? (cut ? 0.0f : (1.0f - v[k].m) * G) : w;
-            }
-            store_raw<BF16, K>(A.du[0], uo, t, t1, gr);
-            store_raw<BF16, K>(A.du[1], uo, t, t1, gi);
-            store_raw<BF16, K>(A.du[2], uo, t, t1, gx);
-            if constexpr (W == 1) carry = __shfl(w, kWave - 1);
-            if (A.dh0 && c == 0 && threadIdx.x == W * kWave - 1) A.dh0[ch] = w;
-        }
+        const Map1 prior = wave_shift_up(upto);
+        // the state before the lane's first step: the next lane's last one
+        float hp = __shfl_down(now.h.get(K - 1), 1);
+        if (threadIdx.x % kWave == kWave - 1) hp = now.before;
+        const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, now, v,
+                                                 fmaf_(prior.a, after, prior.b), hp, dlam);
+        if constexpr (W == 1) carry = __shfl(w, kWave - 1);
+        if (A.dh0 && t == 0) A.dh0[ch] = w;
         now = next;
     }
-    if constexpr (AGG) {
-        if (threadIdx.x == W * kWave - 1)
-            A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
-    } else {
-        float s = wave_sum_to_last(dlam);
-        if constexpr (W > 1) {
-            if (threadIdx.x % kWave == kWave - 1) sums[wave] = s;
-            __syncthreads();
-            s = 0.0f;
-            for (int w = 0; w < W; ++w) s += sums[w];
+    const float s = dlam_sum<W>(dlam, sums);
+    if (threadIdx.x == W * kWave - 1) A.dlam_part[b * A.D + d] = s;
+}
+
+// ------------------------------------------------ lanes in time, look back ---
+// Few channels: a channel's chunks run side by side, each in a workgroup of its
+// own, and are read once.  A workgroup publishes its chunk's composed map, then
+// looks back: 64 predecessors at a time, a lane each, until one has published
+// the state behind it (or the start is reached), and composes the maps in
+// between onto that state.  It publishes its own state, and runs its steps.
+// A channel's chunks are handed out by its ticket in the order of their places,
+// so every predecessor is already running and the wait ends.  (One ticket for
+// all channels: 8192 chunks took 113 us, most of it in line for that word.)
+//
+// A published word is 64 bits, the value and a tag that is zero before, stored
+// and loaded in one device-coherent access: no word is seen half written, and
+// none needs the others' order.  The words are cleared by gated_clear_kernel.
+struct GatedRecord {
+    uint64_t a, b;  // the chunk's map
+    uint64_t h;     // the state behind the chunk
+    uint64_t unused;
+};
+__device__ __forceinline__ void publish(uint64_t *word, float v)
+{
+    __hip_atomic_store(word, (1ull << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t published(const uint64_t *word)
+{
+    return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float word_value(uint64_t w) { return __uint_as_float((uint32_t)w); }
+
+__global__ void gated_clear_kernel(GatedArgs A, int64_t words)
+{
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < words) reinterpret_cast<uint64_t *>(A.ticket)[i] = 0;
+}
+
+// A wave: the state behind place - 1 of channel ch, `start` before place 0.
+__device__ __forceinline__ float look_back(const GatedRecord *records, int64_t channels, int64_t ch,
+                                           int64_t place, float start)
+{
+    const int lane = threadIdx.x % kWave;
+    Map1 acc = {1.0f, 0.0f};
+    for (int64_t near = place - 1;; near -= kWave) {
+        const int64_t at = near - lane;
+        const GatedRecord *r = records + at * channels + ch;
+        Map1 m;
+        int stop;
+        for (;;) {
+            bool ready = true, state = at < 0;
+            m = {at < 0 ? 0.0f : 1.0f, at < 0 ? start : 0.0f};
+            if (at >= 0) {
+                const uint64_t h = published(&r->h);
+                state = h != 0;
+                if (state) {
+                    m = {0.0f, word_value(h)};
+                } else {
+                    const uint64_t a = published(&r->a), b = published(&r->b);
+                    ready = a != 0 && b != 0;
+                    m = {word_value(a), word_value(b)};
+                }
+            }
+            // up to the nearest state, every lane has to be ready
+            const uint64_t states = __ballot(state), missing = __ballot(!ready);
+            stop = states ? __ffsll((unsigned long long)states) - 1 : kWave;
+            const uint64_t wanted = stop >= kWave ? ~0ull : (2ull << stop) - 1;
+            if (!(missing & wanted)) break;
+            __builtin_amdgcn_s_sleep(1);
         }
-        if (threadIdx.x == W * kWave - 1) A.dlam_part[(b * A.nseg + seg) * A.D + d] = s;
+        if (lane > stop) m = {1.0f, 0.0f};
+        // lane 0's map is the latest: it is applied last
+#pragma unroll
+        for (int o = 1; o < kWave; o *= 2) {
+            const Map1 y = {__shfl_down(m.a, o), __shfl_down(m.b, o)};
+            if (lane + o < kWave) m = compose(m, y);
+        }
+        m = {__shfl(m.a, 0), __shfl(m.b, 0)};
+        acc = compose(acc, m);
+        if (stop < kWave) return acc.b;  // a state's map is constant: acc.a = 0
     }
+}
+
+// This workgroup's place in its channel.  A ticket has a line of its own.
+constexpr int kTicketWords = 32;
+__device__ __forceinline__ uint32_t take_ticket(const GatedArgs &A, int64_t ch, uint32_t *lds)
+{
+    if (threadIdx.x == 0) *lds = atomicAdd(A.ticket + ch * kTicketWords, 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);
+}
+// Publishes the chunk's map and state and returns the state before the chunk,
+// in every thread.
+template <int W>
+__device__ __forceinline__ float chunk_carry(const GatedArgs &A, const Map1 *maps, int64_t ch,
+                                             int64_t place, float start, float *lds)
+{
+    if (threadIdx.x < kWave) {
+        GatedRecord *r = A.records + place * A.channels + ch;
+        const Map1 all = all_waves<W>(maps);
+        if (place > 0 && threadIdx.x == 0) {
+            publish(&r->a, all.a);
+            publish(&r->b, all.b);
+        }
+        const float before = place > 0 ? look_back(A.records, A.channels, ch, place, start) : start;
+        if (threadIdx.x == 0) {
+            publish(&r->h, fmaf_(all.a, before, all.b));
+            *lds = before;
+        }
+    }
+    __syncthreads();
+    return *lds;
+}
+
+template <bool BF16, int K, int W>
+__global__ void __launch_bounds__(W * kWave) gated_look_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[W];
+    __shared__ uint32_t ticket;
+    __shared__ float carry_lds;
+    const int64_t ch = blockIdx.x % (uint32_t)A.channels;
+    const int64_t place = take_ticket(A, ch, &ticket);
+    const int64_t b = ch / A.D, d = ch - b * A.D;
+    const int wave = threadIdx.x / kWave;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+    const int64_t t = place * (K * W * kWave) + (int64_t)threadIdx.x * K;
+    const GatedChunk<K, BF16> c = load_chunk<K, BF16>(A, uo, rs, t, A.T);
+    Map1 m[K];
+    const Map1 upto = wave_scan_inclusive(chunk_maps<K, BF16>(c, rate, t, A.T, m));
+    if (threadIdx.x % kWave == kWave - 1) maps[wave] = upto;
+    __syncthreads();
+    float carry = chunk_carry<W>(A, maps, ch, place, A.h0 ? A.h0[ch] : 0.0f, &carry_lds);
+    const float before = through_waves<W>(maps, wave, carry);
+    const Map1 prior = wave_shift_up(upto);
+    chunk_states<K>(A, so, ch, t, m, fmaf_(prior.a, before, prior.b));
+}
+
+template <bool BF16, int K, int W>
+__global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[W];
+    __shared__ float sums[W];
+    __shared__ uint32_t ticket;
+    __shared__ float carry_lds;
+    const int64_t ch = blockIdx.x % (uint32_t)A.channels;
+    const int64_t place = take_ticket(A, ch, &ticket);
+    const int64_t b = ch / A.D, d = ch - b * A.D;
+    const int wave = threadIdx.x / kWave;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
+    const float h0 = A.h0 ? A.h0[ch] : 0.0f;
+    constexpr int P = K * W * kWave;
+    const int64_t c0 = ((A.T + P - 1) / P - 1 - place) * P;  // places count from the end
+    const int at = W * kWave - 1 - (int)threadIdx.x;
+    const int64_t t = c0 + at * K;
+    const GatedBackChunk<K, BF16> c =
+        load_back<K, BF16>(A, uo, so, rs, t, c0 + (W - 1 - wave) * (kWave * K), A.T, h0);
+    Decay v[K];
+    const Map1 upto = wave_scan_inclusive(back_maps<K, BF16>(c, rate, t, A.T, v));
+    if (threadIdx.x % kWave == kWave - 1) maps[wave] = upto;
+    __syncthreads();
+    float carry = chunk_carry<W>(A, maps, ch, place, A.gh_last ? A.gh_last[ch] : 0.0f, &carry_lds);
+    const float after = through_waves<W>(maps, wave, carry);
+    const Map1 prior = wave_shift_up(upto);
+    float hp = __shfl_down(c.h.get(K - 1), 1), dlam = 0.0f;
+    if (threadIdx.x % kWave == kWave - 1) hp = c.before;
+    const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, c, v, fmaf_(prior.a, after, prior.b), hp,
+                                             dlam);
+    if (A.dh0 && t == 0) A.dh0[ch] = w;
+    const float s = dlam_sum<W>(dlam, sums);
+    if (threadIdx.x == W * kWave - 1) A.dlam_part[(place * A.B + b) * A.D + d] = s;
 }
 
 // --------------------------------------------------- lanes in time, short ---
@@ -497,23 +674,9 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_kernel(GatedArgs A)
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const GatedChunk<K, BF16> c = load_chunk<K, BF16>(A, uo, rs, t, end);
     const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
-    Map1 m[K], own = {1.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        m[k] = gated_map(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
-        m[k] = keep_or_identity(m[k], t + k < end);
-        own = compose(m[k], own);
-    }
-    const Map1 prior = group_scan_exclusive<G, false>(own);
-    float h = fmaf_(prior.a, h0, prior.b), out[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) out[k] = h = fmaf_(m[k].a, h, m[k].b);
-    if (t >= end) return;
-    store_raw<false, K>(A.h, so, t, end, out);
-    if (A.h_last)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (t + k == A.T - 1) A.h_last[ch] = out[k];
+    Map1 m[K];
+    const Map1 prior = group_scan_exclusive<G, false>(chunk_maps<K, BF16>(c, rate, t, end, m));
+    if (here) chunk_states<K>(A, so, ch, t, m, fmaf_(prior.a, h0, prior.b));
 }
 
 template <bool BF16, int K, int G>
@@ -527,51 +690,39 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(Gate
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
-    const GatedBackChunk<K, BF16> c = load_back<K, BF16, false>(A, uo, so, rs, t, 0, end, h0);
+    const GatedBackChunk<K, BF16> c = load_back<K, BF16>(A, uo, so, rs, t, 0, end, h0);
     const float after = A.gh_last && here ? A.gh_last[ch] : 0.0f;
     Decay v[K];
-    Map1 own = {1.0f, 0.0f};
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-        v[k] = decay(rate, c.u[0].get(k));
-        const float ka = c.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
-        own = compose(keep_or_identity(Map1{ka, ka * c.gh.get(k)}, t + k < end), own);
-    }
-    const Map1 prior = group_scan_exclusive<G, true>(own);
-    float w = fmaf_(prior.a, after, prior.b);
-    float hp = __shfl_up(c.h.get(K - 1), 1);
+    const Map1 prior = group_scan_exclusive<G, true>(back_maps<K, BF16>(c, rate, t, end, v));
+    float hp = __shfl_up(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % G == 0) hp = h0;
-    float gr[K], gi[K], gx[K], dlam = 0.0f;
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-        const bool cut = c.cut >> k & 1u, in = t + k < end;
-        const float g_total = c.gh.get(k) + w;
-        const GatedGrad g = gated_grad(v[k], c.u[1].get(k), c.u[2].get(k), cut, g_total,
-                                       k ? c.h.get(k ? k - 1 : 0) : hp);
-        gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
-        dlam += in ? g.lam : 0.0f;
-        w = in ? (cut ? 0.0f : (1.0f - v[k].m) * g_total) : w;
-    }
+    const float w = chunk_gradients<K, BF16>(A, uo, t, end, c, v, fmaf_(prior.a, after, prior.b), hp,
+                                             dlam);
 #pragma unroll
     for (int o = 1; o < G; o *= 2) dlam += __shfl_xor(dlam, o);
-    if (t >= end) return;
-    store_raw<BF16, K>(A.du[0], uo, t, end, gr);
-    store_raw<BF16, K>(A.du[1], uo, t, end, gi);
-    store_raw<BF16, K>(A.du[2], uo, t, end, gx);
-    if (t > 0) return;
+    if (t > 0 || !here) return;
     if (A.dh0) A.dh0[ch] = w;
     A.dlam_part[b * A.D + d] = dlam;  // one span
 }
 
-// dL/dlam = -power sig(lam) sum (dL/dl sig(u_r)), the partial sums of the
-// batch rows and spans added in a fixed order.
-__global__ void gated_dlam_kernel(GatedArgs A)
+// dL/dlam = -power sig(lam) sum (dL/dl sig(u_r)): 64 channels a workgroup, its
+// waves each a contiguous run of the partial sums' rows; a fixed order.
+constexpr int kDlamWaves = 8;
+__global__ void __launch_bounds__(kDlamWaves * kWave) gated_dlam_kernel(GatedArgs A, int64_t rows)
 {
-    const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= A.D) return;
+    __shared__ float lds[kDlamWaves][kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int64_t d = (int64_t)blockIdx.x * kWave + lane;
+    const int64_t per = (rows + kDlamWaves - 1) / kDlamWaves;
     float s = 0.0f;
-    const int64_t n = A.B * A.nseg;
-    for (int64_t j = 0; j < n; ++j) s += A.dlam_part[j * A.D + d];
+    if (d < A.D)
+#pragma unroll 4
+        for (int64_t j = wave * per; j < min(rows, (wave + 1) * per); ++j)
+            s += A.dlam_part[j * A.D + d];
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || d >= A.D) return;
+    for (int w = 1; w < kDlamWaves; ++w) s += lds[w][lane];
     A.dlam[d] = -A.power * sigmoid_q(-kLog2e * A.lam[d]) * s;
 }
 

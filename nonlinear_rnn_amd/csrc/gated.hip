@@ -16,10 +16,12 @@ namespace {
 // Steps a lane holds in the kernels with lanes in time: one 16-byte load a
 // plane.
 constexpr int kStepsBf16 = 8, kStepsF32 = 4;
+// Look back: what a chunk costs beside its bytes wants it long.  Float32,
+// 1x262144x64: 8 waves of 4 steps a lane 74.7 us, 4 of 8 64.4, 8 of 8 58.5.
+constexpr int kLookWaves = 8, kLookSteps = 8, kLookChunk = kLookWaves * kWave * kLookSteps;
 
 // Which kernel, and how the time axis is cut.
 enum GatedKernel { kLanePerChannel, kWavePerChannel, kGroupPerChannel, kLookBack };
-constexpr int kLookWaves = 8;
 struct GatedPlan {
     GatedKernel kernel = kLanePerChannel;
     int64_t channels = 0;
@@ -28,7 +30,6 @@ struct GatedPlan {
     size_t records = 0, words = 0;  // look back: the records' place, words in all
     size_t part = 0, total = 0;  // workspace: span maps or records, then dlam partial sums
 };
-int64_t chunks_of(int64_t T, int steps) { return (T + kLookWaves * kWave * steps - 1) / (kLookWaves * kWave * steps); }
 
 // The plan goes by the shape alone (not by the dtype), so that a workspace
 // serves either.
@@ -47,7 +48,7 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
         // else 4 waves, and where those do not fill it either, a channel's
         // chunks side by side (B=1 T=262144 D=64 float32: 84 us in two launches
         // that each read the projections)
-        const int64_t chunks = chunks_of(T, kStepsF32);
+        const int64_t chunks = (T + kLookChunk - 1) / kLookChunk;
         pl.kernel = C >= kFull || T <= kWave * kStepsBf16 ? kWavePerChannel
                     : C >= kFull / 4 || chunks <= 1       ? kGroupPerChannel
                                                           : kLookBack;
@@ -158,13 +159,13 @@ hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, int64_t &rows, hip
         PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(4 * kWave), BF16, K, 4);
         break;
     case kLookBack: {
-        const int64_t chunks = chunks_of(A.T, K);
+        const int64_t chunks = (A.T + kLookChunk - 1) / kLookChunk;
         rows = A.B * chunks;
         hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)((pl.words + 255) / 256)), dim3(256),
                            0, st, A, (int64_t)pl.words);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        PARARNN_GATED(look, dim3((unsigned)(A.channels * chunks)), dim3(kLookWaves * kWave), BF16, K,
+        PARARNN_GATED(look, dim3((unsigned)(A.channels * chunks)), dim3(kLookWaves * kWave), BF16, kLookSteps,
                       kLookWaves);
         break;
     }

@@ -20,15 +20,17 @@ constexpr int kStepsBf16 = 8, kStepsF32 = 4;
 // 1x262144x64: 8 waves of 4 steps a lane 74.7 us, 4 of 8 64.4, 8 of 8 58.5.
 constexpr int kLookWaves = 8, kLookSteps = 8, kLookChunk = kLookWaves * kWave * kLookSteps;
 
+// A dispatch's work-items in 32 bits, 512 a chunk.
+constexpr int64_t kMostChunks = int64_t(1) << 23;
+
 // Which kernel, and how the time axis is cut.
-enum GatedKernel { kLanePerChannel, kWavePerChannel, kGroupPerChannel, kLookBack };
+enum GatedKernel { kLanePerChannel, kLaneLookBack, kWavePerChannel, kGroupPerChannel, kLookBack };
 struct GatedPlan {
     GatedKernel kernel = kLanePerChannel;
     int64_t channels = 0;
-    int64_t seg_len = 0;   // a lane per channel: spans
-    int32_t nseg = 1;
-    size_t records = 0, words = 0;  // look back: the records' place, words in all
-    size_t part = 0, total = 0;  // workspace: span maps or records, then dlam partial sums
+    int64_t chunks = 1;  // look back: places
+    // workspace: tickets, the records' place, dlam partial sums
+    size_t records = 0, part = 0, total = 0;
 };
 
 // The plan goes by the shape alone (not by the dtype), so that a workspace
@@ -41,7 +43,7 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     pl.channels = sh->B * sh->D;
     const int64_t C = pl.channels, T = sh->T;
     constexpr int64_t kFull = 8 * kComputeUnits;  // waves that fill the device
-    int64_t rows = sh->B;  // of dlam partial sums
+    size_t record = 0, lines = 0;
     // (a dispatch counts its work-items in 32 bits: 64 a channel)
     if (T > 2 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
         // a wave per channel where the channels fill the device or are short;
@@ -52,26 +54,21 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
         pl.kernel = C >= kFull || T <= kWave * kStepsBf16 ? kWavePerChannel
                     : C >= kFull / 4 || chunks <= 1       ? kGroupPerChannel
                                                           : kLookBack;
-        // fewer than kFull / 4 channels: the ticket's 32 bits hold their chunks
-        // unless a channel has millions
-        if (pl.kernel == kLookBack && C * chunks >= (int64_t(1) << 23)) pl.kernel = kGroupPerChannel;
-        if (pl.kernel == kLookBack) {
-            pl.records = align_up((size_t)C * kTicketWords * sizeof(uint32_t));
-            pl.part = align_up(pl.records + (size_t)(C * chunks) * sizeof(GatedRecord));
-            pl.words = pl.part / sizeof(uint64_t);
-            rows = sh->B * chunks;
-        }
+        if (pl.kernel == kLookBack && C * chunks >= kMostChunks) pl.kernel = kGroupPerChannel;
+        if (pl.kernel == kLookBack) pl.chunks = chunks, record = sizeof(GatedRecord), lines = C;
     } else {
-        // a lane per channel: spans of at least 64 steps
-        const int64_t waves = (C + kWave - 1) / kWave;
-        int64_t nseg = waves > 0 ? 2 * kFull / waves : 1;
-        nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, (T + 63) / 64, 4096}));
-        pl.seg_len = std::max<int64_t>(1, (T + nseg - 1) / nseg);
-        pl.nseg = (int32_t)std::max<int64_t>(1, (T + pl.seg_len - 1) / pl.seg_len);
-        pl.part = pl.nseg > 1 ? align_up((size_t)pl.nseg * C * sizeof(float2)) : 0;
-        rows = sh->B * pl.nseg;
+        // a lane per channel: one wave for the whole length where that is one
+        // batch of loads or the channels fill the device
+        const int64_t groups = (C + kWave - 1) / kWave, chunks = (T + kSpanChunk - 1) / kSpanChunk;
+        if (T > kGatedSteps && groups < kFull && groups * chunks < kMostChunks) {
+            pl.kernel = kLaneLookBack;
+            pl.chunks = chunks;
+            if (chunks > 1) record = 3 * sizeof(uint64_t), lines = groups;
+        }
     }
-    pl.total = adjoint ? align_up(pl.part + (size_t)rows * sh->D * sizeof(float)) : pl.part;
+    pl.records = align_up(lines * kTicketWords * sizeof(uint32_t));
+    pl.part = align_up(pl.records + (size_t)(pl.chunks * C) * record);
+    pl.total = adjoint ? align_up(pl.part + (size_t)(pl.chunks * C) * sizeof(float)) : pl.part;
     return PARARNN_OK;
 }
 
@@ -84,11 +81,8 @@ void gated_args(GatedArgs &A, const pararnn_shape_t *sh, const GatedPlan &pl, co
     A.power = power;
     A.h0 = h0;
     A.resets = resets;
-    A.agg = static_cast<float2 *>(ws);
     A.ticket = static_cast<uint32_t *>(ws);
-    A.records = reinterpret_cast<GatedRecord *>(static_cast<char *>(ws) + pl.records);
-    A.seg_len = pl.seg_len;
-    A.nseg = pl.nseg;
+    if (pl.part) A.words = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + pl.records);
     A.B = sh->B;
     A.T = sh->T;
     A.D = sh->D;
@@ -124,24 +118,25 @@ pararnn_status_t check_gated(const pararnn_shape_t *sh, const GatedPlan &pl, con
     else                                                                                         \
         hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), GRID, BLOCK, 0, st, A)
 
-// `rows`: of dlam partial sums.
 template <bool ADJ, bool BF16>
-hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, int64_t &rows, hipStream_t st)
+hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, hipStream_t st)
 {
     constexpr int K = BF16 ? kStepsBf16 : kStepsF32;
-    rows = A.B * A.nseg;
-    switch (pl.kernel) {
-    case kLanePerChannel: {
-        const unsigned groups = (unsigned)((A.channels + kWave - 1) / kWave);
-        if (A.nseg > 1) {
-            // (the last span's map, or backwards the first one's, is nobody's carry)
-            PARARNN_GATED(channel, dim3(groups, (unsigned)A.nseg - 1), dim3(kWave), BF16, true);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
-        PARARNN_GATED(channel, dim3(groups, (unsigned)A.nseg), dim3(kWave), BF16, false);
-        break;
+    const unsigned groups = (unsigned)((A.channels + kWave - 1) / kWave);
+    if (pl.part) {  // tickets and words
+        const size_t words = pl.part / sizeof(uint64_t);
+        hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0,
+                           st, A, (int64_t)words);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
+    switch (pl.kernel) {
+    case kLanePerChannel:
+        PARARNN_GATED(channel, dim3(groups), dim3(kWave), BF16);
+        break;
+    case kLaneLookBack:
+        PARARNN_GATED(span, dim3((unsigned)(groups * pl.chunks)), dim3(kSpanWaves * kWave), BF16);
+        break;
     case kWavePerChannel:
         if (A.T <= 16 * K) {  // several channels a wave
             const int lanes = A.T <= 4 * K ? 4 : 16;
@@ -158,17 +153,10 @@ hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, int64_t &rows, hip
     case kGroupPerChannel:
         PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(4 * kWave), BF16, K, 4);
         break;
-    case kLookBack: {
-        const int64_t chunks = (A.T + kLookChunk - 1) / kLookChunk;
-        rows = A.B * chunks;
-        hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)((pl.words + 255) / 256)), dim3(256),
-                           0, st, A, (int64_t)pl.words);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        PARARNN_GATED(look, dim3((unsigned)(A.channels * chunks)), dim3(kLookWaves * kWave), BF16, kLookSteps,
-                      kLookWaves);
+    case kLookBack:
+        PARARNN_GATED(look, dim3((unsigned)(A.channels * pl.chunks)), dim3(kLookWaves * kWave), BF16,
+                      kLookSteps, kLookWaves);
         break;
-    }
     }
     return hipGetLastError();
 }
@@ -201,9 +189,8 @@ pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *co
     A.h = h;
     A.h_last = h_last;
     hipStream_t strm = static_cast<hipStream_t>(stream);
-    int64_t rows;
-    const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<false, true>(A, pl, rows, strm)
-                                                 : run_gated<false, false>(A, pl, rows, strm);
+    const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<false, true>(A, pl, strm)
+                                                 : run_gated<false, false>(A, pl, strm);
     return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
@@ -236,14 +223,13 @@ pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const 
     A.dlam = dlam;
     A.dh0 = dh0;
     A.dlam_part = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part);
-    int64_t rows = 0;  // no batch rows: a sum of no terms
     if (pl.channels > 0) {
-        const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<true, true>(A, pl, rows, strm)
-                                                     : run_gated<true, false>(A, pl, rows, strm);
+        const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<true, true>(A, pl, strm)
+                                                     : run_gated<true, false>(A, pl, strm);
         if (e != hipSuccess) return PARARNN_ERR_HIP;
     }
     hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + kWave - 1) / kWave)),
-                       dim3(kDlamWaves * kWave), 0, strm, A, rows);
+                       dim3(kDlamWaves * kWave), 0, strm, A, shape->B * pl.chunks);
     return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 

@@ -33,13 +33,13 @@ struct GatedArgs {
     const float *gh_last;   // or null
     void *du[3];
     float *dlam, *dh0;
-    float *dlam_part;       // [B][nseg][D], look back: [place][B][D]
-    // the time axis in parts: spans (a lane per channel) or chunks (look back)
-    float2 *agg;            // [nseg][channels]
-    uint32_t *ticket;       // a line a channel
-    struct GatedRecord *records;  // [place][channels]
-    int64_t seg_len;
-    int32_t nseg;
+    float *dlam_part;       // [place][B][D]
+    // look back
+    uint32_t *ticket;       // a line a channel, or a group of 64
+    union {
+        struct GatedRecord *records;  // [place][channels]
+        uint64_t *words;              // [place][3][channels]; null: one place
+    };
     float power;
     int64_t B, T, D, channels;
     int64_t usb, usd, ust, ssb, ssd, sst;
@@ -106,127 +106,313 @@ __device__ __forceinline__ GatedGrad gated_grad(const Decay &v, float ui, float 
     return g;
 }
 
+// -------------------------------------------------------------- look back ---
+// Where there are too few channels to fill the device, the time axis is cut
+// into chunks that run side by side, and the projections are still read once.
+// A workgroup publishes its chunk's composed map, then looks back over a window
+// of predecessors until one has published the state behind it and all nearer
+// ones their maps, and applies these maps in order.  It publishes its own
+// state, and runs its steps.  A state is always the one before it under the
+// chunk's map, rounded once: the results do not depend on how far a workgroup
+// had to look.  A channel's chunks are handed out by its ticket in the order of
+// their places, so every predecessor is already running and the wait ends.
+// (One ticket for all channels: 8192 chunks took 113 us, most of it in line for
+// that word.)
+//
+// A published word is 64 bits, the value and a tag that is zero before, stored
+// and loaded in one device-coherent access: no word is seen half written, and
+// none needs the others' order.  Tickets and words are cleared by
+// gated_clear_kernel.
+__device__ __forceinline__ void publish(uint64_t *word, float v)
+{
+    __hip_atomic_store(word, (1ull << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t published(const uint64_t *word)
+{
+    return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float word_value(uint64_t w) { return __uint_as_float((uint32_t)w); }
+
+__global__ void gated_clear_kernel(GatedArgs A, int64_t words)
+{
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < words) reinterpret_cast<uint64_t *>(A.ticket)[i] = 0;
+}
+
+// This workgroup's place in its channel.  A ticket has a line of its own.
+constexpr int kTicketWords = 32;
+__device__ __forceinline__ uint32_t take_ticket(const GatedArgs &A, int64_t ch, uint32_t *lds)
+{
+    if (threadIdx.x == 0) *lds = atomicAdd(A.ticket + ch * kTicketWords, 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);
+}
 // ------------------------------------------------------ lane per channel ---
 // Any layout: lane = channel, so time-major planes load coalesced, and a
-// single token of many requests is one step of every lane.  kSteps steps are
-// loaded before the first is used.  With few channels the time axis is cut
-// into spans: one launch composes every span's map (AGG), the next applies
-// the maps of the spans before it and runs the span again.
+// single token of many requests is one step of every lane.  kGatedSteps steps
+// are loaded before the first is used.
 constexpr int kGatedSteps = 8;
 
-template <bool BF16, bool AGG>
+template <int K>
+struct LaneSteps {
+    float u[3][K];
+    bool cut[K];
+};
+// Steps t .. t + K - 1; those from T on repeat the last.
+template <bool BF16, int K>
+__device__ __forceinline__ LaneSteps<K> lane_steps(const GatedArgs &A, int64_t uo,
+                                                   const uint8_t *rs, int64_t t)
+{
+    LaneSteps<K> c;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t tk = min(t + k, A.T - 1);
+#pragma unroll
+        for (int g = 0; g < 3; ++g) c.u[g][k] = load_gate<BF16>(A.u[g], uo + tk * A.ust);
+        c.cut[k] = rs && rs[tk] != 0;
+    }
+    return c;
+}
+// The states of steps t .. t + K - 1 from the one before them.
+template <int K>
+__device__ __forceinline__ float lane_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
+                                             const Map1 (&m)[K], float h)
+{
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (t + k >= A.T) continue;
+        h = fmaf_(m[k].a, h, m[k].b);
+        A.h[so + (t + k) * A.sst] = h;
+        if (A.h_last && t + k == A.T - 1) A.h_last[ch] = h;
+    }
+    return h;
+}
+template <int K>
+struct LaneBack {
+    float hp[K], gh[K];  // the state before each step, its gradient
+};
+template <int K>
+__device__ __forceinline__ LaneBack<K> lane_back(const GatedArgs &A, int64_t so, int64_t t, float h0)
+{
+    LaneBack<K> c;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t tk = min(t + k, A.T - 1);
+        c.gh[k] = A.gh ? A.gh[so + tk * A.sst] : 0.0f;
+        c.hp[k] = tk > 0 ? A.hs[so + (tk - 1) * A.sst] : h0;
+    }
+    return c;
+}
+// The gradients of steps t + K - 1 .. t from w behind them: with w_t =
+// dL/dh_{t-1} through step t alone,
+//     w_t = k_t a_t (gh_t + w_{t+1}),  w_{T+1} = gh_last,  dL/dh_0 = w_1,
+// again affine maps, composed from the last step to the first.
+template <bool BF16, int K>
+__device__ __forceinline__ float lane_gradients(const GatedArgs &A, int64_t uo, int64_t t,
+                                                const LaneSteps<K> &c, const LaneBack<K> &e,
+                                                const Decay (&v)[K], float w, float &dlam)
+{
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        if (t + k >= A.T) continue;
+        const float G = e.gh[k] + w;
+        w = c.cut[k] ? 0.0f : (1.0f - v[k].m) * G;
+        const GatedGrad g = gated_grad(v[k], c.u[1][k], c.u[2][k], c.cut[k], G, e.hp[k]);
+        const int64_t o = uo + (t + k) * A.ust;
+        store_gate<BF16>(A.du[0], o, g.r);
+        store_gate<BF16>(A.du[1], o, g.i);
+        store_gate<BF16>(A.du[2], o, g.x);
+        dlam += g.lam;
+    }
+    return w;
+}
+
+// Single tokens and short runs, or channels that fill the device: one lane runs
+// its channel from end to end.
+template <bool BF16>
 __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
 {
     const int64_t ch = (int64_t)blockIdx.x * kWave + threadIdx.x;
     if (ch >= A.channels) return;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y;
-    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
-
-    Map1 span = {1.0f, 0.0f};
     float h = A.h0 ? A.h0[ch] : 0.0f;
-    if constexpr (!AGG)
-        for (int32_t j = 0; j < seg; ++j) {
-            const float2 m = A.agg[(int64_t)j * A.channels + ch];
-            h = fmaf_(m.x, h, m.y);
-        }
-    for (int64_t t = t0; t < t1; t += kGatedSteps) {
-        float u[3][kGatedSteps];
-        bool cut[kGatedSteps];
+    if (A.T == 0 && A.h_last) A.h_last[ch] = h;
+    for (int64_t t = 0; t < A.T; t += kGatedSteps) {
+        const auto c = lane_steps<BF16, kGatedSteps>(A, uo, rs, t);
+        Map1 m[kGatedSteps];
 #pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) {
-            const bool in = t + k < t1;
-            const int64_t o = uo + (in ? t + k : t) * A.ust;
-#pragma unroll
-            for (int g = 0; g < 3; ++g) u[g][k] = load_gate<BF16>(A.u[g], o);
-            cut[k] = rs && rs[in ? t + k : t] != 0;
-        }
-#pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) {
-            if (t + k >= t1) break;
-            const Map1 m = gated_map(rate, u[0][k], u[1][k], u[2][k], cut[k]);
-            if constexpr (AGG) {
-                span = compose(m, span);
-            } else {
-                h = fmaf_(m.a, h, m.b);
-                A.h[so + (t + k) * A.sst] = h;
-            }
-        }
+        for (int k = 0; k < kGatedSteps; ++k)
+            m[k] = gated_map(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
+        h = lane_states<kGatedSteps>(A, so, ch, t, m, h);
     }
-    if constexpr (AGG)
-        A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
-    else if (A.h_last && seg == A.nseg - 1)
-        A.h_last[ch] = h;
 }
-
-// Backward: with w_t = dL/dh_{t-1} through step t alone,
-//     w_t = k_t a_t (gh_t + w_{t+1}),  w_{T+1} = gh_last,  dL/dh_0 = w_1,
-// again affine maps, composed from the last span to the first.
-template <bool BF16, bool AGG>
+template <bool BF16>
 __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs A)
 {
     const int64_t ch = (int64_t)blockIdx.x * kWave + threadIdx.x;
     if (ch >= A.channels) return;
     const int64_t b = ch / A.D, d = ch - b * A.D;
-    const int32_t seg = blockIdx.y + (AGG ? 1 : 0);
-    const int64_t t0 = seg * A.seg_len, t1 = min(A.T, t0 + A.seg_len);
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
-
-    Map1 span = {1.0f, 0.0f};
-    float w = A.gh_last ? A.gh_last[ch] : 0.0f;
-    if constexpr (!AGG)
-        for (int32_t j = A.nseg - 1; j > seg; --j) {
-            const float2 m = A.agg[(int64_t)j * A.channels + ch];
-            w = fmaf_(m.x, w, m.y);
-        }
     const float h0 = A.h0 ? A.h0[ch] : 0.0f;
-    float dlam = 0.0f;
-    for (int64_t t = t1 - 1; t >= t0; t -= kGatedSteps) {
-        float u[3][kGatedSteps], hp[kGatedSteps], gh[kGatedSteps];
-        bool cut[kGatedSteps];
+    float w = A.gh_last ? A.gh_last[ch] : 0.0f, dlam = 0.0f;
+    for (int64_t t = (A.T - 1) / kGatedSteps * kGatedSteps; t >= 0 && A.T > 0; t -= kGatedSteps) {
+        const auto c = lane_steps<BF16, kGatedSteps>(A, uo, rs, t);
+        const auto e = lane_back<kGatedSteps>(A, so, t, h0);
+        Decay v[kGatedSteps];
 #pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) {
-            const int64_t tk = t - k >= t0 ? t - k : t;
-            const int64_t o = uo + tk * A.ust;
-            u[0][k] = load_gate<BF16>(A.u[0], o);
-            cut[k] = rs && rs[tk] != 0;
-            gh[k] = A.gh ? A.gh[so + tk * A.sst] : 0.0f;
-            if constexpr (!AGG) {
-                u[1][k] = load_gate<BF16>(A.u[1], o);
-                u[2][k] = load_gate<BF16>(A.u[2], o);
-                hp[k] = tk > 0 ? A.hs[so + (tk - 1) * A.sst] : h0;
+        for (int k = 0; k < kGatedSteps; ++k) v[k] = decay(rate, c.u[0][k]);
+        w = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
+    }
+    A.dlam_part[ch] = dlam;
+    if (A.dh0) A.dh0[ch] = w;
+}
+
+// Else: a chunk of 64 steps of 64 channels a workgroup, 8 steps of each a wave.
+// Every step is in registers once; the waves' maps meet in shared memory.
+constexpr int kSpanWaves = 8, kSpanChunk = kSpanWaves * kGatedSteps;
+
+// A lane: the state behind place - 1 > -1 of channel ch, from the words of the
+// nearest kLookAhead predecessors, which are loaded together.
+constexpr int kLookAhead = 6;
+__device__ __forceinline__ float lane_look_back(const uint64_t *words, int64_t channels, int64_t ch,
+                                                int64_t place)
+{
+    for (;;) {
+        uint64_t h[kLookAhead], a[kLookAhead], b[kLookAhead];
+#pragma unroll
+        for (int j = 0; j < kLookAhead; ++j) {
+            const uint64_t *r = words + max(place - 1 - j, int64_t(0)) * 3 * channels + ch;
+            h[j] = published(r);
+            if (j + 1 < kLookAhead) a[j] = published(r + channels), b[j] = published(r + 2 * channels);
+        }
+        bool found = false;
+        float state = 0.0f;
+#pragma unroll
+        for (int j = kLookAhead - 1; j >= 0; --j) {
+            if (place - 1 - j < 0) continue;
+            if (h[j]) {
+                found = true, state = word_value(h[j]);
+            } else if (j + 1 < kLookAhead) {
+                found = found && a[j] && b[j];
+                state = fmaf_(word_value(a[j]), state, word_value(b[j]));
             }
         }
+        if (found) return state;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// The chunk's place, the workgroup's channels, and after carry() the state
+// before this wave's steps.
+struct SpanPlace {
+    int64_t place, ch;
+    bool here;
+    int wave, lane;
+};
+__device__ __forceinline__ SpanPlace span_place(const GatedArgs &A, uint32_t *ticket)
+{
+    const uint32_t groups = (uint32_t)((A.channels + kWave - 1) / kWave);
+    const int64_t group = blockIdx.x % groups;
+    SpanPlace s;
+    s.place = A.words ? take_ticket(A, group, ticket) : 0;
+    s.wave = threadIdx.x / kWave, s.lane = threadIdx.x % kWave;
+    s.ch = group * kWave + s.lane;
+    s.here = s.ch < A.channels;
+    s.ch = min(s.ch, A.channels - 1);
+    return s;
+}
+__device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace &s, const Map1 &own,
+                                            float start, Map1 (*maps)[kWave], float *carry)
+{
+    maps[s.wave][s.lane] = own;
+    __syncthreads();
+    if (s.wave == 0 && A.words) {
+        if (s.here) {
+            Map1 all = maps[0][s.lane];
 #pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) {
-            if (t - k < t0) break;
-            const Decay v = decay(rate, u[0][k]);
-            const float ka = cut[k] ? 0.0f : 1.0f - v.m;
-            if constexpr (AGG) {
-                span = compose({ka, ka * gh[k]}, span);
-            } else {
-                const float G = gh[k] + w;
-                w = ka * G;
-                const GatedGrad g = gated_grad(v, u[1][k], u[2][k], cut[k], G, hp[k]);
-                const int64_t o = uo + (t - k) * A.ust;
-                store_gate<BF16>(A.du[0], o, g.r);
-                store_gate<BF16>(A.du[1], o, g.i);
-                store_gate<BF16>(A.du[2], o, g.x);
-                dlam += g.lam;
+            for (int w = 1; w < kSpanWaves; ++w) all = compose(maps[w][s.lane], all);
+            uint64_t *r = A.words + s.place * 3 * A.channels + s.ch;
+            if (s.place > 0) {
+                publish(r + A.channels, all.a);
+                publish(r + 2 * A.channels, all.b);
             }
+            const float before =
+                s.place > 0 ? lane_look_back(A.words, A.channels, s.ch, s.place) : start;
+            publish(r, fmaf_(all.a, before, all.b));
+            carry[s.lane] = before;
         }
     }
-    if constexpr (AGG) {
-        A.agg[(int64_t)seg * A.channels + ch] = make_float2(span.a, span.b);
-    } else {
-        A.dlam_part[(b * A.nseg + seg) * A.D + d] = dlam;
-        if (A.dh0 && seg == 0) A.dh0[ch] = w;
+    __syncthreads();
+    float h = A.words ? carry[s.lane] : start;
+    for (int w = 0; w < s.wave; ++w) h = fmaf_(maps[w][s.lane].a, h, maps[w][s.lane].b);
+    return h;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[kSpanWaves][kWave];
+    __shared__ float carry[kWave];
+    __shared__ uint32_t ticket;
+    const SpanPlace s = span_place(A, &ticket);
+    const int64_t b = s.ch / A.D, d = s.ch - b * A.D;
+    const int64_t t = s.place * kSpanChunk + s.wave * kGatedSteps;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const auto c = lane_steps<BF16, kGatedSteps>(A, uo, A.resets ? A.resets + b * A.T : nullptr, t);
+    Map1 m[kGatedSteps], own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kGatedSteps; ++k) {
+        m[k] = gated_map(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
+        m[k] = keep_or_identity(m[k], t + k < A.T);
+        own = compose(m[k], own);
     }
+    const float h = span_carry(A, s, own, A.h0 ? A.h0[s.ch] : 0.0f, maps, carry);
+    if (s.here) lane_states<kGatedSteps>(A, so, s.ch, t, m, h);
+}
+
+// Backward: places and waves count from the end.
+template <bool BF16>
+__global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(GatedArgs A)
+{
+    __shared__ Map1 maps[kSpanWaves][kWave];
+    __shared__ float carry[kWave], sums[kSpanWaves][kWave];
+    __shared__ uint32_t ticket;
+    const SpanPlace s = span_place(A, &ticket);
+    const int64_t b = s.ch / A.D, d = s.ch - b * A.D;
+    const int64_t chunk = (A.T + kSpanChunk - 1) / kSpanChunk - 1 - s.place;
+    const int64_t t = chunk * kSpanChunk + (kSpanWaves - 1 - s.wave) * kGatedSteps;
+    const float rate = decay_rate(A.lam[d], A.power);
+    const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
+    const auto c = lane_steps<BF16, kGatedSteps>(A, uo, A.resets ? A.resets + b * A.T : nullptr, t);
+    const auto e = lane_back<kGatedSteps>(A, so, t, A.h0 ? A.h0[s.ch] : 0.0f);
+    Decay v[kGatedSteps];
+    Map1 own = {1.0f, 0.0f};
+#pragma unroll
+    for (int k = kGatedSteps - 1; k >= 0; --k) {
+        v[k] = decay(rate, c.u[0][k]);
+        const float ka = c.cut[k] ? 0.0f : 1.0f - v[k].m;
+        own = compose(keep_or_identity(Map1{ka, ka * e.gh[k]}, t + k < A.T), own);
+    }
+    float w = span_carry(A, s, own, A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
+    if (s.here) w = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
+    sums[s.wave][s.lane] = dlam;
+    __syncthreads();
+    if (!s.here) return;
+    if (A.dh0 && t == 0) A.dh0[s.ch] = w;
+    if (s.wave != 0) return;
+    for (int j = 1; j < kSpanWaves; ++j) dlam += sums[j][s.lane];
+    A.dlam_part[s.place * A.channels + s.ch] = dlam;
 }
 
 // ---------------------------------------------------------- lanes in time ---
@@ -463,97 +649,39 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
         now = next;
     }
     const float s = dlam_sum<W>(dlam, sums);
-    if (threadIdx.x == W * kWave - 1) A.dlam_part[b * A.D + d] = s;
+    if (threadIdx.x == W * kWave - 1) A.dlam_part[ch] = s;
 }
 
 // ------------------------------------------------ lanes in time, look back ---
 // Few channels: a channel's chunks run side by side, each in a workgroup of its
-// own, and are read once.  A workgroup publishes its chunk's composed map, then
-// looks back: 64 predecessors at a time, a lane each, until one has published
-// the state behind it (or the start is reached), and composes the maps in
-// between onto that state.  It publishes its own state, and runs its steps.
-// A channel's chunks are handed out by its ticket in the order of their places,
-// so every predecessor is already running and the wait ends.  (One ticket for
-// all channels: 8192 chunks took 113 us, most of it in line for that word.)
-//
-// A published word is 64 bits, the value and a tag that is zero before, stored
-// and loaded in one device-coherent access: no word is seen half written, and
-// none needs the others' order.  The words are cleared by gated_clear_kernel.
+// own.  A wave looks back over 64 predecessors, a lane each.
 struct GatedRecord {
     uint64_t a, b;  // the chunk's map
     uint64_t h;     // the state behind the chunk
     uint64_t unused;
 };
-__device__ __forceinline__ void publish(uint64_t *word, float v)
-{
-    __hip_atomic_store(word, (1ull << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t published(const uint64_t *word)
-{
-    return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float word_value(uint64_t w) { return __uint_as_float((uint32_t)w); }
-
-__global__ void gated_clear_kernel(GatedArgs A, int64_t words)
-{
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < words) reinterpret_cast<uint64_t *>(A.ticket)[i] = 0;
-}
-
-// A wave: the state behind place - 1 of channel ch, `start` before place 0.
+// A wave: the state behind place - 1 > -1 of channel ch.
 __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t channels, int64_t ch,
-                                           int64_t place, float start)
+                                           int64_t place)
 {
-    const int lane = threadIdx.x % kWave;
-    Map1 acc = {1.0f, 0.0f};
-    for (int64_t near = place - 1;; near -= kWave) {
-        const int64_t at = near - lane;
-        const GatedRecord *r = records + at * channels + ch;
-        Map1 m;
-        int stop;
-        for (;;) {
-            bool ready = true, state = at < 0;
-            m = {at < 0 ? 0.0f : 1.0f, at < 0 ? start : 0.0f};
-            if (at >= 0) {
-                const uint64_t h = published(&r->h);
-                state = h != 0;
-                if (state) {
-                    m = {0.0f, word_value(h)};
-                } else {
-                    const uint64_t a = published(&r->a), b = published(&r->b);
-                    ready = a != 0 && b != 0;
-                    m = {word_value(a), word_value(b)};
-                }
-            }
-            // up to the nearest state, every lane has to be ready
-            const uint64_t states = __ballot(state), missing = __ballot(!ready);
-            stop = states ? __ffsll((unsigned long long)states) - 1 : kWave;
-            const uint64_t wanted = stop >= kWave ? ~0ull : (2ull << stop) - 1;
-            if (!(missing & wanted)) break;
-            __builtin_amdgcn_s_sleep(1);
+    const int64_t at = place - 1 - threadIdx.x % kWave;
+    const GatedRecord *r = records + max(at, int64_t(0)) * channels + ch;
+    for (;;) {
+        const uint64_t h = published(&r->h), a = published(&r->a), b = published(&r->b);
+        // up to the nearest state, every lane has to be ready
+        const uint64_t states = __ballot(h != 0), ready = __ballot(a != 0 && b != 0);
+        const uint64_t nearer = (states & -states) - 1;
+        if (states && (ready & nearer) == nearer) {
+            int lane = __ffsll((unsigned long long)states) - 1;
+            float state = read_lane(word_value(h), lane);
+            while (--lane >= 0)
+                state = fmaf_(read_lane(word_value(a), lane), state, read_lane(word_value(b), lane));
+            return state;
         }
-        if (lane > stop) m = {1.0f, 0.0f};
-        // lane 0's map is the latest: it is applied last
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) {
-            const Map1 y = {__shfl_down(m.a, o), __shfl_down(m.b, o)};
-            if (lane + o < kWave) m = compose(m, y);
-        }
-        m = {__shfl(m.a, 0), __shfl(m.b, 0)};
-        acc = compose(acc, m);
-        if (stop < kWave) return acc.b;  // a state's map is constant: acc.a = 0
+        __builtin_amdgcn_s_sleep(1);
     }
 }
 
-// This workgroup's place in its channel.  A ticket has a line of its own.
-constexpr int kTicketWords = 32;
-__device__ __forceinline__ uint32_t take_ticket(const GatedArgs &A, int64_t ch, uint32_t *lds)
-{
-    if (threadIdx.x == 0) *lds = atomicAdd(A.ticket + ch * kTicketWords, 1u);
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*lds);
-}
 // Publishes the chunk's map and state and returns the state before the chunk,
 // in every thread.
 template <int W>
@@ -567,7 +695,7 @@ __device__ __forceinline__ float chunk_carry(const GatedArgs &A, const Map1 *map
             publish(&r->a, all.a);
             publish(&r->b, all.b);
         }
-        const float before = place > 0 ? look_back(A.records, A.channels, ch, place, start) : start;
+        const float before = place > 0 ? look_back(A.records, A.channels, ch, place) : start;
         if (threadIdx.x == 0) {
             publish(&r->h, fmaf_(all.a, before, all.b));
             *lds = before;
@@ -636,7 +764,7 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
                                              dlam);
     if (A.dh0 && t == 0) A.dh0[ch] = w;
     const float s = dlam_sum<W>(dlam, sums);
-    if (threadIdx.x == W * kWave - 1) A.dlam_part[(place * A.B + b) * A.D + d] = s;
+    if (threadIdx.x == W * kWave - 1) A.dlam_part[place * A.channels + ch] = s;
 }
 
 // --------------------------------------------------- lanes in time, short ---

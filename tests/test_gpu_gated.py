@@ -91,6 +91,31 @@ def test_scan_and_adjoint(B, T, D, dtype, layout):
     assert (np.abs(f64(got["dlam"]) - want["dlam"]) <= tol * np.maximum(1.0, want["dlam_terms"])).all()
 
 
+# many parts of one channel, of few and of some, a part with one step, and
+# channels that fill the device
+PARTS = [(1, 290000, 1, "channel"), (3, 12289, 5, "channel"), (1, 4097, 300, "padded"),
+         (1, 30000, 70, "time"), (3, 65, 130, "mixed"), (2, 64, 100, "time"), (1, 17, 131100, "time")]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,D,layout", PARTS)
+def test_parts_of_the_time_axis(B, T, D, layout, dtype):
+    test_scan_and_adjoint(B, T, D, dtype, layout)
+
+
+@pytest.mark.parametrize("B,T,D,layout", PARTS[:5])
+def test_same_bits_every_time(B, T, D, layout):
+    c = case(B, T, D, torch.bfloat16, layout, docs=0.0002)
+    first = None
+    for _ in range(4):
+        h, last = pr.gated_scan(c["u"], c["lam"], c["h0"], power=c["power"], resets=c["resets"])
+        g = pr.gated_scan_adjoint(c["u"], c["lam"], c["h0"], h, None, gh_last=c["gl"], power=c["power"],
+                                  resets=c["resets"])
+        now = [h, last, *g["du"], g["dh0"], g["dlam"]]
+        first = first or now
+        assert all(torch.equal(x, y) for x, y in zip(now, first))
+
+
 @pytest.mark.parametrize("layout", ["channel", "time"])
 def test_every_step_a_new_document(layout):
     c = case(2, 150, 66, layout=layout, docs="all")

@@ -97,6 +97,14 @@ def test_block(B, T, D, gdt, xdt, zdt):
     check(inputs(B, T, D, gdt, xdt), zdt)
 
 
+# enough steps for the longest tiles, at every width of theirs
+@pytest.mark.parametrize("B,T,D", [(3, 2741, 7), (3, 2741, 65), (2, 4103, 130), (2, 4103, 192), (1, 8209, 301),
+                                   (2, 4101, 520), (1, 8195, 770), (2, 4103, 1030), (1, 8200, 1540),
+                                   (2, 2053, 2050), (2, 2053, 3333)])
+def test_long_tiles(B, T, D):
+    check(inputs(B, T, D, H if D % 2 else F, H if D % 3 else F), H if D % 5 else F)
+
+
 @pytest.mark.parametrize("layout", ["time", "padded"])
 @pytest.mark.parametrize("B,T,D", [(2, 1, 100), (2, 5, 70), (2, 40, 513), (1, 21, 4096)])
 @pytest.mark.parametrize("dt", [F, H])

@@ -45,22 +45,35 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     constexpr int64_t kFull = 8 * kComputeUnits;  // waves that fill the device
     size_t record = 0, lines = 0;
     // (a dispatch counts its work-items in 32 bits: 64 a channel)
-    if (T > 2 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
-        // a wave per channel where the channels fill the device or are short;
-        // else 4 waves, and where those do not fill it either, a channel's
-        // chunks side by side (B=1 T=262144 D=64 float32: 84 us in two launches
-        // that each read the projections)
+    if (T > 6 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
+        // Lanes in time; up to 6 steps a lane has all of its channel's (512
+        // requests of 1024 channels: 6 steps bfloat16 47 us with lanes in time,
+        // 14 with a lane per channel, 8 steps float32 29 and 32).
+        // One wave a channel for sequences up to 512 steps, and up to 4095
+        // where the channels fill the device (16 x 1024 channels of 600 steps
+        // float32 36 us, with 4 waves 42; 8 x 1024 of 4096 steps, backward, 221
+        // and 207), or longer if 4 waves' last chunk is mostly empty (4500 steps
+        // bfloat16, backward, 183 and 240).  4 waves, and where they do not fill
+        // the device, the channel's chunks side by side (2x65536x128 float32
+        // 75 us with 4 waves, 54 looking back; 4x8192x256 bfloat16, 1024
+        // channels, 22 and 27).
         const int64_t chunks = (T + kLookChunk - 1) / kLookChunk;
-        pl.kernel = C >= kFull || T <= kWave * kStepsBf16 ? kWavePerChannel
-                    : C >= kFull / 4 || chunks <= 1       ? kGroupPerChannel
-                                                          : kLookBack;
+        constexpr int64_t four = 4 * kWave * kStepsBf16;
+        const bool full = T >= 4096 && (T + four - 1) / four * four - T <= T / 8;
+        pl.kernel = T <= kWave * kStepsBf16 || (C >= kFull && !full) ? kWavePerChannel
+                    : C >= kFull / 4 || chunks <= 1                  ? kGroupPerChannel
+                                                                     : kLookBack;
         if (pl.kernel == kLookBack && C * chunks >= kMostChunks) pl.kernel = kGroupPerChannel;
         if (pl.kernel == kLookBack) pl.chunks = chunks, record = sizeof(GatedRecord), lines = C;
     } else {
-        // a lane per channel: one wave for the whole length where that is one
-        // batch of loads or the channels fill the device
+        // A lane per channel, one for the whole length of a short sequence
+        // (64 x 1024 time-major channels float32, 16 steps, backward: 22 us, in
+        // chunks 27; 32 steps 12.0 and 13.1) or where the channels fill the
+        // device (20x1000x4096 time-major float32: forward 297 us, in chunks
+        // 321, 10x2000x4096 454 and 316; backward, of more bytes a step,
+        // 20x1000x4096 782 and 649).
         const int64_t groups = (C + kWave - 1) / kWave, chunks = (T + kSpanChunk - 1) / kSpanChunk;
-        if (T > kGatedSteps && groups < kFull && groups * chunks < kMostChunks) {
+        if (T > 32 && groups < (adjoint ? kFull : kFull / 2) && groups * chunks < kMostChunks) {
             pl.kernel = kLaneLookBack;
             pl.chunks = chunks;
             if (chunks > 1) record = 3 * sizeof(uint64_t), lines = groups;

@@ -94,7 +94,9 @@ def test_scan_and_adjoint(B, T, D, dtype, layout):
 # many parts of one channel, of few and of some, a part with one step, and
 # channels that fill the device
 PARTS = [(1, 290000, 1, "channel"), (3, 12289, 5, "channel"), (1, 4097, 300, "padded"),
-         (1, 30000, 70, "time"), (3, 65, 130, "mixed"), (2, 64, 100, "time"), (1, 17, 131100, "time")]
+         (1, 30000, 70, "time"), (3, 65, 130, "mixed"), (2, 64, 100, "time"), (1, 40, 131100, "time"),
+         (1, 4099, 2049, "channel"), (1, 6139, 2048, "padded"),
+         (1, 600, 2100, "channel")]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -84,6 +84,12 @@ def test_scores(N, V, dtype, top):
     check(x, tokens, top, adjoint=top == 7)
 
 
+@pytest.mark.parametrize("N,V", [(1100, 2049), (600, 8192), (600, 8193)])
+@pytest.mark.parametrize("top", [0, 20])
+def test_rows_of_a_wave(N, V, top):
+    test_scores(N, V, torch.float32, top)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("stride", [1001, 1003, 1024])
 def test_padded_rows(dtype, stride):

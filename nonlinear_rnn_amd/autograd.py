@@ -16,6 +16,9 @@ Two layouts: ``gru``/``lstm`` take one [B][D][T]-indexed tensor per gate
 passed to the kernels as strided views (no transpose copy), and the
 gradient for u comes back as one [B][T][G*D] tensor written by the adjoint.
 
+``gated_scan``, ``block_norm`` and ``token_logprobs`` are the differentiable
+forms of the operators of recurrent language models.
+
 Non-convergence is not an error in the solve; pass ``strict=True`` to raise
 when a solve stops at the iteration cap without reaching the tolerance (this
 reads the device info record, i.e. synchronises).

@@ -28,6 +28,9 @@ constexpr int64_t kStripSteps = 4, kStripGroups = 2 * kComputeUnits;
 // The tiling that holds D channels with the most steps a tile that still
 // makes two tiles a CU, and of those the narrowest; single steps where the
 // planes' steps are not contiguous.  No waves: the strip kernels.
+// (Two tiles a CU, not one or four: B=2 T=3000 D=1024 28 us, one 34, four 33;
+// B=1 T=6000 D=512 15, 19 and 18.)  The backward pass keeps 8 waves a CU, what
+// its registers allow.
 struct BlockPlan {
     Tiling t = {0, 0, 0, false};
     int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)

@@ -233,7 +233,8 @@ __device__ __forceinline__ float lane_gradients(const GatedArgs &A, int64_t uo, 
 }
 
 // Single tokens and short runs, or channels that fill the device: one lane runs
-// its channel from end to end.
+// its channel from end to end.  512x1x4096 time-major bfloat16 20 us; bound by
+// the launch, and by the bytes where there are many channels.
 template <bool BF16>
 __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
 {
@@ -279,6 +280,12 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
 
 // Else: a chunk of 64 steps of 64 channels a workgroup, 8 steps of each a wave.
 // Every step is in registers once; the waves' maps meet in shared memory.
+// 11x153600x64 time-major float32 500 us (3.5 TB/s), 8x4096x1024 bfloat16
+// 137 us (2.5 TB/s).  Bound by the registers that its single-element loads and
+// their addresses take (2 workgroups a CU, backward 1), and with few channels
+// by the steps of looking back: chunks of 128 steps take 447 us of the first,
+// but 313 us instead of 264 of the second's backward pass; capped at 3 and 2
+// workgroups' registers it spills and takes 611 and 261.
 constexpr int kSpanWaves = 8, kSpanChunk = kSpanWaves * kGatedSteps;
 
 // A lane: the state behind place - 1 > -1 of channel ch, from the words of the
@@ -423,6 +430,9 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
 // through LDS (one barrier a chunk, two buffers), and every lane runs its
 // steps again from the state in front of them.  The chunk's last state starts
 // the next one; the next chunk's loads are issued before this one's scan.
+// Bound by HBM: every plane goes once, 4x16384x4096 bfloat16 531 us (5.1 TB/s,
+// a large copy's rate), backward 8x4096x1024 bfloat16 135 us (5.0 TB/s); a
+// lane per channel took 19.8 ms and 5.0 ms of these.
 template <int K, bool BF16>
 struct GatedChunk {
     Raw<BF16, K> u[3];
@@ -654,7 +664,9 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
 
 // ------------------------------------------------ lanes in time, look back ---
 // Few channels: a channel's chunks run side by side, each in a workgroup of its
-// own.  A wave looks back over 64 predecessors, a lane each.
+// own.  A wave looks back over 64 predecessors, a lane each.  1x262144x64
+// float32 60 us (4.4 TB/s), bfloat16 50; backward 131 and 96.  Bound by HBM,
+// and by the time a chunk waits for its loads and then for its predecessor.
 struct GatedRecord {
     uint64_t a, b;  // the chunk's map
     uint64_t h;     // the state behind the chunk
@@ -770,7 +782,9 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
 // --------------------------------------------------- lanes in time, short ---
 // At most G K steps: G lanes a channel and 64 / G channels a wave, each lane's
 // K steps in one access as above.  (With a wave a channel, T = 100 of 64000
-// channels left 7 of 8 lanes idle.)
+// channels left 7 of 8 lanes idle: 64x100x1000 bfloat16 100 us, here 30;
+// 64x32x1024 float32 43 and 16.)  Bound by partial lines of odd lengths and by
+// the launch.
 constexpr int kShortThreads = 256;
 
 // Inclusive scan of the maps over groups of G neighbouring lanes, each group's
@@ -834,7 +848,8 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(Gate
 }
 
 // dL/dlam = -power sig(lam) sum (dL/dl sig(u_r)): 64 channels a workgroup, its
-// waves each a contiguous run of the partial sums' rows; a fixed order.
+// waves each a contiguous run of the partial sums' rows; a fixed order.  Bound
+// by latency: a wave has 4 rows of loads in flight.
 constexpr int kDlamWaves = 8;
 __global__ void __launch_bounds__(kDlamWaves * kWave) gated_dlam_kernel(GatedArgs A, int64_t rows)
 {
@@ -855,6 +870,9 @@ __global__ void __launch_bounds__(kDlamWaves * kWave) gated_dlam_kernel(GatedArg
 }
 
 // ----------------------------------------------------------- one step ---
+// A lane per channel of a request, its state read and written in its slot of
+// the pool; no scan.  64 requests x 1024 channels: 3 us on the device, the
+// launch's own time; the call itself takes 9.
 struct GatedStepArgs {
     const void *u[3];
     const float *lam;

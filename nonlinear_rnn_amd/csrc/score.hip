@@ -26,7 +26,8 @@ pararnn_status_t check_score(int64_t N, int64_t V, pararnn_dtype_t dtype, int64_
 }
 
 // Workgroups a row: one, unless there are too few rows to fill the device (4
-// workgroups a CU); then parts of at least 4096 logits.
+// workgroups a CU); then parts of at least 4096 logits (2048 and 16384 take the
+// same time within 1 us for 16 rows of 65536 and 512 of 50003).
 int64_t score_parts(int64_t N, int64_t V)
 {
     if (N <= 0) return 1;

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
 // through LDS (one barrier a chunk, two buffers), and every lane runs its
 // steps again from the state in front of them.  The chunk's last state starts
 // the next one; the next chunk's loads are issued before this one's scan.
-// Bound by HBM: every plane goes once, 4x16384x4096 bfloat16 531 us (5.1 TB/s,
+// Bound by HBM: every plane goes once, 4x16384x4096 bfloat16 511 us (5.2 TB/s,
 // a large copy's rate), backward 8x4096x1024 bfloat16 135 us (5.0 TB/s); a
 // lane per channel took 19.8 ms and 5.0 ms of these.
 template <int K, bool BF16>
@@ -665,8 +665,9 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
 // ------------------------------------------------ lanes in time, look back ---
 // Few channels: a channel's chunks run side by side, each in a workgroup of its
 // own.  A wave looks back over 64 predecessors, a lane each.  1x262144x64
-// float32 60 us (4.4 TB/s), bfloat16 50; backward 131 and 96.  Bound by HBM,
-// and by the time a chunk waits for its loads and then for its predecessor.
+// float32 72 us from HBM (3.7 TB/s; 60 where part of it is still cached),
+// backward 131.  Bound by the time a chunk waits for its loads and then for its
+// predecessor, with 4 chunks a CU.
 struct GatedRecord {
     uint64_t a, b;  // the chunk's map
     uint64_t h;     // the state behind the chunk

@@ -630,9 +630,10 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
 // B=16 T=2048 D=4096: 997 us of 684 at a copy's rate.  4.5 GB go instead of
 // 3.5, at 4.5 TB/s: x twice, and dh and dgate in parts of lines (without their
 // stores 726 us).  A CU's registers hold 8 steps of 4096 channels, 32 bytes of
-// a line, and the L2 has to put the parts together.  B=3 T=1531 D=2000 float32: 101 us of 54, 576 tiles on 256
-// CUs.  Tiles of 4 steps that keep x too took 1141 us, reading the gradients
-// again as well 1880, a kernel for the sums and one to apply them 1404.
+// a line, and the L2 has to put the parts together.  B=3 T=1531 D=2000 float32:
+// 101 us of 54, 576 tiles on 256 CUs.  Tiles of 4 steps that keep x too took
+// 1141 us of the first, reading the gradients again as well 1880, a kernel for
+// the sums and one to apply them 1404.
 struct StreamPair {
     Words2 x[4], gy[4], gz[4];
     float wp[2], wn[2];

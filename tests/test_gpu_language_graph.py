@@ -21,6 +21,17 @@ def scan_case():
     return fn, u
 
 
+def time_major_scan_case():
+    u = [torch.randn((2, 2000, 70), device=DEV).transpose(1, 2) for _ in range(3)]  # several chunks
+    lam, h0 = torch.randn(70, device=DEV), torch.randn((2, 70), device=DEV)
+    gh = torch.randn((2, 2000, 70), device=DEV).transpose(1, 2)
+
+    def fn():
+        h, last = pr.gated_scan(u, lam, h0)
+        return h, last, pr.gated_scan_adjoint(u, lam, h0, h, gh)
+    return fn, u
+
+
 def step_case():
     u = [torch.randn((5, 300), device=DEV) for _ in range(3)]
     lam, start = torch.randn(300, device=DEV), torch.randn((9, 300), device=DEV)
@@ -54,7 +65,7 @@ def score_case():
     return fn, [x]
 
 
-@pytest.mark.parametrize("case", [scan_case, step_case, block_case, score_case])
+@pytest.mark.parametrize("case", [scan_case, time_major_scan_case, step_case, block_case, score_case])
 def test_replays(case):
     fn, inputs = case()
     graph, out = capture(fn)

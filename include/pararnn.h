@@ -33,7 +33,9 @@
  *     A call enqueues kernel launches only (per-launch state is cleared by
  *     a kernel, not by a memset), so it can be captured into a HIP graph;
  *     a captured call keeps its workspace, and two replays that overlap in
- *     time must not share one.
+ *     time must not share one.  A call may be several launches that meet in
+ *     its workspace, so neither may calls on different streams, nor threads
+ *     whose calls on one stream are not kept apart by a lock.
  *   - Layout: per-time-step planes are indexed (b, d, t); element offset of
  *     (b, d, t) = b*stride_b + d*stride_d + t*stride_t.  Planes of `u` (and
  *     of `du`) use u_stride_*; state, gradient and lambda planes use

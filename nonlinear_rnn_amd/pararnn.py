@@ -15,6 +15,7 @@ Names follow the ABI: ``solve_gru``, ``solve_gru_noalloc``, ``solve_lstm``,
 import ctypes
 import os
 import struct
+import threading
 
 import torch  # loads the HIP runtime the library then shares
 
@@ -334,12 +335,14 @@ def decode_info(raw) -> dict:
                 iters_sum=isum, units=units, iters_mean=(isum / units) if units else 0.0)
 
 
-class Workspace:
-    """Grow-only device scratch buffers (torch-allocated), one per device
-    and stream: the kernels' per-launch state (tickets, flags, records,
+class Workspace(threading.local):
+    """Grow-only device scratch buffers (torch-allocated), one per thread,
+    device and stream: the kernels' per-launch state (tickets, flags, records,
     partial sums) lives there, so launches on different streams must not
-    share one.  Each buffer is allocated on its own stream, so torch's
-    allocator orders its reuse after that stream's work."""
+    share one, and neither must threads on one stream: a call is several
+    launches, and another thread's may come between them.  Each buffer is
+    allocated on its own stream, so torch's allocator orders its reuse after
+    that stream's work; a thread's buffers go with it."""
 
     MAX_STREAMS = 8  # buffers kept for the most recently used streams
 

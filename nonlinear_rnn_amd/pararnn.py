@@ -335,6 +335,18 @@ def decode_info(raw) -> dict:
                 iters_sum=isum, units=units, iters_mean=(isum / units) if units else 0.0)
 
 
+def _capturing(device, stream):
+    """Whether what is enqueued on `stream` (None: the device's current one) goes
+    into a graph."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        return False
+    if stream is None and device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class Workspace(threading.local):
     """Grow-only device scratch buffers (torch-allocated), one per thread,
     device and stream: the kernels' per-launch state (tickets, flags, records,
@@ -342,7 +354,12 @@ class Workspace(threading.local):
     share one, and neither must threads on one stream: a call is several
     launches, and another thread's may come between them.  Each buffer is
     allocated on its own stream, so torch's allocator orders its reuse after
-    that stream's work; a thread's buffers go with it."""
+    that stream's work; a thread's buffers go with it.
+
+    A captured call's workspace belongs to its graph, which reads and writes it
+    at every replay: it is allocated during the capture, from the graph's own
+    pool, and is not kept here, where a larger call would give it up and a
+    second graph find it."""
 
     MAX_STREAMS = 8  # buffers kept for the most recently used streams
 
@@ -353,6 +370,10 @@ class Workspace(threading.local):
         """``key``: (device index, stream handle), where the caller knows it."""
         if nbytes == 0:
             return None
+        if _capturing(device, stream):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            with torch.cuda.stream(s):
+                return torch.empty(nbytes, dtype=torch.uint8, device=device)
         if key is None:
             s = stream if stream is not None else torch.cuda.current_stream(device)
             key = (torch.device(device).index, s.cuda_stream)

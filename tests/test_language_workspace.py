@@ -40,3 +40,17 @@ def test_threads_do_not_share_a_workspace():
     assert not {b.data_ptr() for b in got["here"]} & {b.data_ptr() for b in got["there"]}
     assert ws.get(64, "cpu", Stream(1)) is got["here"][0]
 
+
+
+def test_a_captured_call_has_a_workspace_of_its_own(monkeypatch):
+    """A graph's launches keep their workspace for as long as it is replayed: it
+    is neither taken from the buffers that other calls use nor left among them."""
+    ws = pr.Workspace()
+    cached = ws.get(64, "cpu", Stream(1))
+    monkeypatch.setattr(pr, "_capturing", lambda device, stream: True)
+    first, second = ws.get(64, "cpu", Stream(1)), ws.get(64, "cpu", Stream(1))
+    other = ws.get(64, "cpu", Stream(2))
+    assert len({b.data_ptr() for b in (cached, first, second, other)}) == 4
+    assert list(ws.buf) == [(None, 1)] and ws.buf[(None, 1)] is cached
+    monkeypatch.setattr(pr, "_capturing", lambda device, stream: False)
+    assert ws.get(64, "cpu", Stream(1)) is cached

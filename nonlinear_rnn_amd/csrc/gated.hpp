@@ -8,11 +8,13 @@
 // §1.3, level 2, is the same scan with the Newton system's maps).
 //
 // Numbers.  Slow channels have a_t close to 1, where exp(l) in float32 has
-// lost l.  So the decay is computed as m = 1 - exp(l) from
+// lost l.  So m = 1 - exp(l) is computed from
 //     exp(l) - 1 = 2 exp(l/2) sinh(l/2),
 // with sinh's odd polynomial below |l| = 1 (first term left out: 1e-8 of the
 // sum) and 1 - exp(l/2)^2 above, where nothing cancels.  Then
-// 1 - a^2 = m (2 - m) holds full relative precision too.  Everything is
+// 1 - a^2 = m (2 - m) holds full relative precision too.  The decay itself is
+// 1 - m below |l| = 1 and exp(l/2)^2 above, where 1 - m would have lost it: the
+// states of fast channels keep their relative precision.  Everything is
 // float32; only bf16 gradients are rounded, once, when they are stored.
 #pragma once
 
@@ -56,7 +58,7 @@ __device__ __forceinline__ float decay_rate(float lam, float power)
 struct Decay {
     float q;   // sig(u_r)
     float l2;  // log2 a
-    float m;   // 1 - a
+    float a;
     float y;   // 1 - a^2
 };
 __device__ __forceinline__ Decay decay(float rate, float r)
@@ -68,8 +70,10 @@ __device__ __forceinline__ Decay decay(float rate, float r)
     const float t = ex2(0.5f * v.l2);             // exp(l / 2)
     const float s = x * x;
     const float p = fmaf_(s, fmaf_(s, fmaf_(s, 1.9841270e-4f, 8.3333333e-3f), 0.16666667f), 1.0f);
-    v.m = x > -0.5f ? -2.0f * t * (x * p) : fmaf_(-t, t, 1.0f);
-    v.y = fmaf_(-v.m, v.m, 2.0f * v.m);
+    const bool slow = x > -0.5f;
+    const float m = slow ? -2.0f * t * (x * p) : fmaf_(-t, t, 1.0f);
+    v.a = slow ? 1.0f - m : t * t;
+    v.y = fmaf_(-m, m, 2.0f * m);
     return v;
 }
 
@@ -77,7 +81,7 @@ __device__ __forceinline__ Decay decay(float rate, float r)
 __device__ __forceinline__ Map1 gated_map(float rate, float r, float i, float x, bool reset)
 {
     const Decay v = decay(rate, r);
-    return {reset ? 0.0f : 1.0f - v.m,
+    return {reset ? 0.0f : v.a,
             __builtin_amdgcn_sqrtf(v.y) * sigmoid_q(-kLog2e * i) * x};
 }
 
@@ -95,12 +99,11 @@ __device__ __forceinline__ GatedGrad gated_grad(const Decay &v, float ui, float 
     const float inv = v.y > 1e-30f ? __builtin_amdgcn_rsqf(v.y) : 0.0f;
     const float gain = v.y * inv;
     const float si = sigmoid_q(-kLog2e * ui);
-    const float a = 1.0f - v.m;
     GatedGrad g;
     g.x = G * gain * si;
     g.i = g.x * ux * (1.0f - si);
-    const float carried = reset ? 0.0f : a * hp;
-    const float dl = G * (carried - fmaf_(-v.y, inv, inv) * (si * ux));
+    const float carried = reset ? 0.0f : v.a * hp;
+    const float dl = G * (carried - v.a * v.a * inv * (si * ux));
     g.lam = dl * v.q;
     g.r = dl * (v.l2 * 0.6931471805599453f) * (1.0f - v.q);
     return g;
@@ -221,7 +224,7 @@ __device__ __forceinline__ float lane_gradients(const GatedArgs &A, int64_t uo, 
     for (int k = K - 1; k >= 0; --k) {
         if (t + k >= A.T) continue;
         const float G = e.gh[k] + w;
-        w = c.cut[k] ? 0.0f : (1.0f - v[k].m) * G;
+        w = c.cut[k] ? 0.0f : v[k].a * G;
         const GatedGrad g = gated_grad(v[k], c.u[1][k], c.u[2][k], c.cut[k], G, e.hp[k]);
         const int64_t o = uo + (t + k) * A.ust;
         store_gate<BF16>(A.du[0], o, g.r);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
 #pragma unroll
     for (int k = kGatedSteps - 1; k >= 0; --k) {
         v[k] = decay(rate, c.u[0][k]);
-        const float ka = c.cut[k] ? 0.0f : 1.0f - v[k].m;
+        const float ka = c.cut[k] ? 0.0f : v[k].a;
         own = compose(keep_or_identity(Map1{ka, ka * e.gh[k]}, t + k < A.T), own);
     }
     float w = span_carry(A, s, own, A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
@@ -573,7 +576,7 @@ __device__ __forceinline__ Map1 back_maps(const GatedBackChunk<K, BF16> &c, floa
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
         v[k] = decay(rate, c.u[0].get(k));
-        const float ka = c.cut >> k & 1u ? 0.0f : 1.0f - v[k].m;
+        const float ka = c.cut >> k & 1u ? 0.0f : v[k].a;
         own = compose(keep_or_identity(Map1{ka, ka * c.gh.get(k)}, t + k < end), own);
     }
     return own;
@@ -595,7 +598,7 @@ __device__ __forceinline__ float chunk_gradients(const GatedArgs &A, int64_t uo,
                                        k ? c.h.get(k ? k - 1 : 0) : hp);
         gr[k] = g.r, gi[k] = g.i, gx[k] = g.x;
         dlam += in ? g.lam : 0.0f;
-        w = in ? (cut ? 0.0f : (1.0f - v[k].m) * G) : w;
+        w = in ? (cut ? 0.0f : v[k].a * G) : w;
     }
     if (t >= end) return w;
     store_raw<BF16, K>(A.du[0], uo, t, end, gr);

@@ -80,3 +80,24 @@ def test_fast_decays_of_one_step():
     exact_l = -4.0 * np.logaddexp(0.0, f64(lam))
     want = 1.5 * np.exp(exact_l)[None].repeat(2, 0)
     assert (np.abs(f64(states) - want) <= want * U * (8 * np.abs(exact_l) + 8)).all()
+
+
+@pytest.mark.parametrize("B,T,D,layout,chunk", [(1, 262144, 4, "channel", 512), (1, 65536, 2100, "channel", 512),
+                                                (1, 65536, 600, "channel", 512), (1, 262144, 64, "time", 64)])
+@pytest.mark.parametrize("ur", [-6.0, -8.0, -10.0])
+def test_long_memory(B, T, D, layout, chunk, ur):
+    """A steady gate near no decay, over a long sequence: what is left of h0 at
+    its end, and of the last state's gradient at its start."""
+    decay = 0.9 + 0.099 * np.random.default_rng(D).random(D)
+    lam = torch.from_numpy(np.log(np.expm1(-np.log(decay) / 8.0))).float().to(DEV)
+    u = planes(B, T, D, layout, [ur, 0.0, 0.0])
+    one = torch.ones((B, D), device=DEV)
+    h, last = pr.gated_scan(u, lam, one)
+    total = -8.0 * np.logaddexp(0.0, f64(lam)) / (1.0 + np.exp(-ur)) * T
+    want = np.exp(total)[None].repeat(B, 0)
+    tol = want * U * (8 * np.abs(total) + 4 * T / chunk + 64)
+    fine = want > 1e-30
+    assert fine.any()
+    assert (np.abs(f64(last) - want) <= tol)[fine].all(), float((np.abs(f64(last) - want) / want)[fine].max())
+    got = pr.gated_scan_adjoint(u, lam, one, h, None, gh_last=one)
+    assert (np.abs(f64(got["dh0"]) - want) <= tol)[fine].all()

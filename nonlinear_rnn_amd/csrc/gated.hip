@@ -133,7 +133,7 @@ pararnn_status_t check_gated(const pararnn_shape_t *sh, const GatedPlan &pl, con
     else                                                                                         \
         hipLaunchKernelGGL((gated_##NAME##_kernel<__VA_ARGS__>), GRID, BLOCK, 0, st, A)
 
-template <bool ADJ, bool BF16>
+template <bool ADJ, bool BF16, bool DOCS>
 hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, hipStream_t st)
 {
     constexpr int K = BF16 ? kStepsBf16 : kStepsF32;
@@ -147,35 +147,43 @@ hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, hipStream_t st)
     }
     switch (pl.kernel) {
     case kLanePerChannel:
-        PARARNN_GATED(channel, dim3(groups), dim3(kWave), BF16);
+        PARARNN_GATED(channel, dim3(groups), dim3(kWave), BF16, DOCS);
         break;
     case kLaneLookBack:
-        PARARNN_GATED(span, dim3((unsigned)(groups * pl.chunks)), dim3(kSpanWaves * kWave), BF16);
+        PARARNN_GATED(span, dim3((unsigned)(groups * pl.chunks)), dim3(kSpanWaves * kWave), BF16,
+                      DOCS);
         break;
     case kWavePerChannel:
         if (A.T <= 16 * K) {  // several channels a wave
             const int lanes = A.T <= 4 * K ? 4 : 16;
             const dim3 grid((unsigned)((A.channels * lanes + kShortThreads - 1) / kShortThreads));
             if (lanes == 4) {
-                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, K, 4);
+                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, DOCS, K, 4);
             } else {
-                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, K, 16);
+                PARARNN_GATED(short, grid, dim3(kShortThreads), BF16, DOCS, K, 16);
             }
         } else {
-            PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(kWave), BF16, K, 1);
+            PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(kWave), BF16, DOCS, K, 1);
         }
         break;
     case kGroupPerChannel:
-        PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(4 * kWave), BF16, K, 4);
+        PARARNN_GATED(time, dim3((unsigned)A.channels), dim3(4 * kWave), BF16, DOCS, K, 4);
         break;
     case kLookBack:
         PARARNN_GATED(look, dim3((unsigned)(A.channels * pl.chunks)), dim3(kLookWaves * kWave), BF16,
-                      kLookSteps, kLookWaves);
+                      DOCS, kLookSteps, kLookWaves);
         break;
     }
     return hipGetLastError();
 }
 #undef PARARNN_GATED
+
+template <bool ADJ>
+hipError_t run_gated(const GatedArgs &A, const GatedPlan &pl, bool bf16, hipStream_t st)
+{
+    if (A.resets) return bf16 ? run_gated<ADJ, true, true>(A, pl, st) : run_gated<ADJ, false, true>(A, pl, st);
+    return bf16 ? run_gated<ADJ, true, false>(A, pl, st) : run_gated<ADJ, false, false>(A, pl, st);
+}
 
 }  // namespace
 
@@ -204,8 +212,7 @@ pararnn_status_t pararnn_gated_scan(const pararnn_shape_t *shape, const void *co
     A.h = h;
     A.h_last = h_last;
     hipStream_t strm = static_cast<hipStream_t>(stream);
-    const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<false, true>(A, pl, strm)
-                                                 : run_gated<false, false>(A, pl, strm);
+    const hipError_t e = run_gated<false>(A, pl, u_dtype == PARARNN_BF16, strm);
     return e == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP;
 }
 
@@ -239,9 +246,7 @@ pararnn_status_t pararnn_gated_scan_adjoint(const pararnn_shape_t *shape, const 
     A.dh0 = dh0;
     A.dlam_part = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part);
     if (pl.channels > 0) {
-        const hipError_t e = u_dtype == PARARNN_BF16 ? run_gated<true, true>(A, pl, strm)
-                                                     : run_gated<true, false>(A, pl, strm);
-        if (e != hipSuccess) return PARARNN_ERR_HIP;
+        if (run_gated<true>(A, pl, u_dtype == PARARNN_BF16, strm) != hipSuccess) return PARARNN_ERR_HIP;
     }
     hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((shape->D + kWave - 1) / kWave)),
                        dim3(kDlamWaves * kWave), 0, strm, A, shape->B * pl.chunks);

@@ -77,55 +77,44 @@ __device__ __forceinline__ Decay decay(float rate, float r)
     return v;
 }
 
-constexpr float kNoMemory = -__builtin_inff();  // log2 of a decay of 0
-
-// A step: h -> a h + b, and l = log2 a.
-struct GatedStep {
+// A step, or a span of steps: x -> a x + b, with l = log2 a.  Near a = 1 a
+// product of decays loses at every step what its factors have lost; their
+// logarithms add up in full.  So a span's a is 2^l, l the sum of its steps'.
+// (A steady gate at -8 over 262144 steps: what is left of h_0 was off by 0.8%
+// with products, by 1e-5 with sums.)
+struct Span {
     float a, b, l;
 };
-__device__ __forceinline__ GatedStep forward_step(float rate, float r, float i, float x,
-                                                  bool reset)
+constexpr float kNoMemory = -__builtin_inff();  // l where a = 0
+__device__ __forceinline__ float through(const Map1 &m, float x) { return fmaf_(m.a, x, m.b); }
+__device__ __forceinline__ float through(const Span &m, float x) { return fmaf_(m.a, x, m.b); }
+__device__ __forceinline__ Span span_of(float l, float b) { return {ex2(l), b, l}; }
+
+// The span of the steps, or spans, added so far.
+struct Running {
+    float l = 0.0f, b = 0.0f;
+    __device__ __forceinline__ void add(const Span &m)
+    {
+        b = through(m, b);
+        l += m.l;
+    }
+    __device__ __forceinline__ Span span() const { return span_of(l, b); }
+};
+
+__device__ __forceinline__ Span forward_step(float rate, float r, float i, float x, bool reset)
 {
     const Decay v = decay(rate, r);
     return {reset ? 0.0f : v.a, __builtin_amdgcn_sqrtf(v.y) * sigmoid_q(-kLog2e * i) * x,
             reset ? kNoMemory : v.l2};
 }
-// Backwards, of w: w -> a (gh + w).
-__device__ __forceinline__ GatedStep backward_step(const Decay &v, float gh, bool reset)
+// Backwards, of w: w -> a (gh + w).  A step past the end (not `in`, gh = 0) comes
+// before all others and leaves w, which is 0 in a span so far, as it is.
+// (Forward, steps past the end come last, and no one asks for what is behind
+// them.)
+__device__ __forceinline__ Span backward_step(const Decay &v, float gh, bool reset, bool in)
 {
     const float a = reset ? 0.0f : v.a;
-    return {a, a * gh, reset ? kNoMemory : v.l2};
-}
-__device__ __forceinline__ GatedStep step_or_identity(const GatedStep &m, bool keep)
-{
-    return {keep ? m.a : 1.0f, keep ? m.b : 0.0f, keep ? m.l : 0.0f};
-}
-__device__ __forceinline__ float through(const GatedStep &m, float x) { return fmaf_(m.a, x, m.b); }
-
-// A span of steps: x -> 2^l x + b, l the sum of their log2 a.  Near a = 1 a
-// product of decays would lose at every step what its factors have lost; their
-// logarithms add up in full.  A steady gate at -8 over 262144 steps: what is
-// left of h_0 was off by 0.8% with products, by 1e-5 with sums.
-struct alignas(8) SpanMap {
-    float l, b;
-};
-__device__ __forceinline__ float through(const SpanMap &m, float x)
-{
-    return fmaf_(ex2(m.l), x, m.b);
-}
-__device__ __forceinline__ SpanMap compose(const SpanMap &L, const SpanMap &E)
-{
-    return {L.l + E.l, through(L, E.b)};
-}
-// The span with one more step behind it.
-__device__ __forceinline__ SpanMap compose(const GatedStep &m, const SpanMap &E)
-{
-    return {m.l + E.l, through(m, E.b)};
-}
-template <int CTRL, int RM = 0xF>
-__device__ __forceinline__ SpanMap dpp_map(const SpanMap &x)
-{
-    return {dppf<CTRL, RM>(0.0f, x.l), dppf<CTRL, RM>(0.0f, x.b)};
+    return {a, a * gh, in ? (reset ? kNoMemory : v.l2) : 0.0f};
 }
 
 // Gradients of one step from G = dL/dh_t (total) and h_{t-1}.  With
@@ -182,10 +171,6 @@ __device__ __forceinline__ float read_lane(float v, int lane)
 {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
-__device__ __forceinline__ SpanMap last_lane(const SpanMap &m)
-{
-    return {read_lane(m.l, kWave - 1), read_lane(m.b, kWave - 1)};
-}
 __device__ __forceinline__ float word_value(uint64_t w) { return __uint_as_float((uint32_t)w); }
 
 __global__ void gated_clear_kernel(GatedArgs A, int64_t words)
@@ -214,9 +199,9 @@ struct LaneSteps {
     bool cut[K];
 };
 // Steps t .. t + K - 1; those from T on repeat the last.
-template <bool BF16, int K>
-__device__ __forceinline__ LaneSteps<K> lane_steps(const GatedArgs &A, int64_t uo,
-                                                   const uint8_t *rs, int64_t t)
+template <bool BF16, bool DOCS, int K>
+__device__ __forceinline__ LaneSteps<K> lane_steps(const GatedArgs &A, int64_t uo, int64_t b,
+                                                   int64_t t)
 {
     LaneSteps<K> c;
 #pragma unroll
@@ -224,14 +209,14 @@ __device__ __forceinline__ LaneSteps<K> lane_steps(const GatedArgs &A, int64_t u
         const int64_t tk = min(t + k, A.T - 1);
 #pragma unroll
         for (int g = 0; g < 3; ++g) c.u[g][k] = load_gate<BF16>(A.u[g], uo + tk * A.ust);
-        c.cut[k] = rs && rs[tk] != 0;
+        c.cut[k] = DOCS && A.resets[b * A.T + tk] != 0;
     }
     return c;
 }
 // The states of steps t .. t + K - 1 from the one before them.
 template <int K>
 __device__ __forceinline__ void lane_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
-                                            const GatedStep (&m)[K], float h)
+                                            const Span (&m)[K], float h)
 {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -253,6 +238,7 @@ __device__ __forceinline__ LaneBack<K> lane_back(const GatedArgs &A, int64_t so,
     for (int k = 0; k < K; ++k) {
         const int64_t tk = min(t + k, A.T - 1);
         c.gh[k] = A.gh ? A.gh[so + tk * A.sst] : 0.0f;
+        if (t + k >= A.T) c.gh[k] = 0.0f;
         c.hp[k] = tk > 0 ? A.hs[so + (tk - 1) * A.sst] : h0;
     }
     return c;
@@ -284,7 +270,7 @@ __device__ __forceinline__ float lane_gradients(const GatedArgs &A, int64_t uo, 
 // Single tokens and short runs, or channels that fill the device: one lane runs
 // its channel from end to end.  512x1x4096 time-major bfloat16 20 us; bound by
 // the launch, and by the bytes where there are many channels.
-template <bool BF16>
+template <bool BF16, bool DOCS>
 __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
 {
     const int64_t ch = (int64_t)blockIdx.x * kWave + threadIdx.x;
@@ -292,23 +278,30 @@ __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
     const int64_t b = ch / A.D, d = ch - b * A.D;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     float h = A.h0 ? A.h0[ch] : 0.0f;
     if (A.T == 0 && A.h_last) A.h_last[ch] = h;
-    for (int64_t t = 0; t < A.T; t += kGatedSteps) {
-        const auto c = lane_steps<BF16, kGatedSteps>(A, uo, rs, t);
-        GatedStep m[kGatedSteps];
-        SpanMap own = {0.0f, 0.0f};
+    Span m[kGatedSteps];
+    const auto load = [&](int64_t t) {
+        const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
 #pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) {
+        for (int k = 0; k < kGatedSteps; ++k)
             m[k] = forward_step(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
-            own = compose(m[k], own);
-        }
+    };
+    int64_t t = 0;
+    for (; t + kGatedSteps < A.T; t += kGatedSteps) {
+        load(t);
         lane_states<kGatedSteps>(A, so, ch, t, m, h);
-        h = through(own, h);
+        Running own;
+#pragma unroll
+        for (int k = 0; k < kGatedSteps; ++k) own.add(m[k]);
+        h = through(own.span(), h);
+    }
+    if (t < A.T) {
+        load(t);
+        lane_states<kGatedSteps>(A, so, ch, t, m, h);
     }
 }
-template <bool BF16>
+template <bool BF16, bool DOCS>
 __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs A)
 {
     const int64_t ch = (int64_t)blockIdx.x * kWave + threadIdx.x;
@@ -316,21 +309,24 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
     const int64_t b = ch / A.D, d = ch - b * A.D;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const float h0 = A.h0 ? A.h0[ch] : 0.0f;
     float w = A.gh_last ? A.gh_last[ch] : 0.0f, dlam = 0.0f;
     for (int64_t t = (A.T - 1) / kGatedSteps * kGatedSteps; t >= 0 && A.T > 0; t -= kGatedSteps) {
-        const auto c = lane_steps<BF16, kGatedSteps>(A, uo, rs, t);
+        const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
         const auto e = lane_back<kGatedSteps>(A, so, t, h0);
         Decay v[kGatedSteps];
 #pragma unroll
         for (int k = 0; k < kGatedSteps; ++k) v[k] = decay(rate, c.u[0][k]);
-        SpanMap own = {0.0f, 0.0f};
+        const float first = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
+        if (t == 0) {
+            w = first;
+            break;
+        }
+        Running own;
 #pragma unroll
         for (int k = kGatedSteps - 1; k >= 0; --k)
-            own = compose(step_or_identity(backward_step(v[k], e.gh[k], c.cut[k]), t + k < A.T), own);
-        lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
-        w = through(own, w);
+            own.add(backward_step(v[k], e.gh[k], c.cut[k], t + k < A.T));
+        w = through(own.span(), w);
     }
     A.dlam_part[ch] = dlam;
     if (A.dh0) A.dh0[ch] = w;
@@ -369,7 +365,7 @@ __device__ __forceinline__ float lane_look_back(const uint64_t *words, int64_t c
                 found = true, state = word_value(h[j]);
             } else if (j + 1 < kLookAhead) {
                 found = found && l[j] && b[j];
-                state = through(SpanMap{word_value(l[j]), word_value(b[j])}, state);
+                state = through(span_of(word_value(l[j]), word_value(b[j])), state);
             }
         }
         if (found) return state;
@@ -396,17 +392,17 @@ __device__ __forceinline__ SpanPlace span_place(const GatedArgs &A, uint32_t *ti
     s.ch = min(s.ch, A.channels - 1);
     return s;
 }
-__device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace &s, const SpanMap &own,
-                                            float start, SpanMap (*maps)[kWave],
-                                            float *carry)
+__device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace &s, const Span &own,
+                                            float start, Span (*maps)[kWave], float *carry)
 {
     maps[s.wave][s.lane] = own;
     __syncthreads();
     if (s.wave == 0 && A.words) {
         if (s.here) {
-            SpanMap all = maps[0][s.lane];
+            Running sum;
 #pragma unroll
-            for (int w = 1; w < kSpanWaves; ++w) all = compose(maps[w][s.lane], all);
+            for (int w = 0; w < kSpanWaves; ++w) sum.add(maps[w][s.lane]);
+            const Span all = sum.span();
             uint64_t *r = A.words + s.place * 3 * A.channels + s.ch;
             if (s.place > 0) {
                 publish(r + A.channels, all.l);
@@ -424,10 +420,10 @@ __device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace 
     return h;
 }
 
-template <bool BF16>
+template <bool BF16, bool DOCS>
 __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[kSpanWaves][kWave];
+    __shared__ Span maps[kSpanWaves][kWave];
     __shared__ float carry[kWave];
     __shared__ uint32_t ticket;
     const SpanPlace s = span_place(A, &ticket);
@@ -435,24 +431,23 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_kernel(GatedArg
     const int64_t t = s.place * kSpanChunk + s.wave * kGatedSteps;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const auto c = lane_steps<BF16, kGatedSteps>(A, uo, A.resets ? A.resets + b * A.T : nullptr, t);
-    GatedStep m[kGatedSteps];
-    SpanMap own = {0.0f, 0.0f};
+    const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
+    Span m[kGatedSteps];
+    Running own;
 #pragma unroll
     for (int k = 0; k < kGatedSteps; ++k) {
         m[k] = forward_step(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
-        m[k] = step_or_identity(m[k], t + k < A.T);
-        own = compose(m[k], own);
+        own.add(m[k]);
     }
-    const float h = span_carry(A, s, own, A.h0 ? A.h0[s.ch] : 0.0f, maps, carry);
+    const float h = span_carry(A, s, own.span(), A.h0 ? A.h0[s.ch] : 0.0f, maps, carry);
     if (s.here) lane_states<kGatedSteps>(A, so, s.ch, t, m, h);
 }
 
 // Backward: places and waves count from the end.
-template <bool BF16>
+template <bool BF16, bool DOCS>
 __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[kSpanWaves][kWave];
+    __shared__ Span maps[kSpanWaves][kWave];
     __shared__ float carry[kWave], sums[kSpanWaves][kWave];
     __shared__ uint32_t ticket;
     const SpanPlace s = span_place(A, &ticket);
@@ -461,16 +456,16 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
     const int64_t t = chunk * kSpanChunk + (kSpanWaves - 1 - s.wave) * kGatedSteps;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const auto c = lane_steps<BF16, kGatedSteps>(A, uo, A.resets ? A.resets + b * A.T : nullptr, t);
+    const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
     const auto e = lane_back<kGatedSteps>(A, so, t, A.h0 ? A.h0[s.ch] : 0.0f);
     Decay v[kGatedSteps];
-    SpanMap own = {0.0f, 0.0f};
+    Running own;
 #pragma unroll
     for (int k = kGatedSteps - 1; k >= 0; --k) {
         v[k] = decay(rate, c.u[0][k]);
-        own = compose(step_or_identity(backward_step(v[k], e.gh[k], c.cut[k]), t + k < A.T), own);
+        own.add(backward_step(v[k], e.gh[k], c.cut[k], t + k < A.T));
     }
-    float w = span_carry(A, s, own, A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
+    float w = span_carry(A, s, own.span(), A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
     if (s.here) w = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
     sums[s.wave][s.lane] = dlam;
     __syncthreads();
@@ -497,21 +492,21 @@ struct GatedChunk {
     Raw<BF16, K> u[3];
     uint32_t cut;
 };
-template <int K, bool BF16>
-__device__ __forceinline__ GatedChunk<K, BF16> load_chunk(const GatedArgs &A, int64_t uo,
-                                                          const uint8_t *rs, int64_t t, int64_t t1)
+template <int K, bool BF16, bool DOCS>
+__device__ __forceinline__ GatedChunk<K, BF16> load_chunk(const GatedArgs &A, int64_t uo, int64_t b,
+                                                          int64_t t, int64_t t1)
 {
     GatedChunk<K, BF16> c;
 #pragma unroll
     for (int g = 0; g < 3; ++g) c.u[g] = load_raw<BF16, K>(A.u[g], uo, t, t1);
-    c.cut = rs ? load_flags<K>(rs, t, t1) : 0u;
+    c.cut = DOCS ? load_flags<K>(A.resets + b * A.T, t, t1) : 0u;
     return c;
 }
 
 // The state before wave `wave`'s part of the chunk, from the one before the
 // chunk and the waves' maps in order; `carry` moves on to the next chunk.
 template <int W>
-__device__ __forceinline__ float through_waves(const SpanMap *maps, int wave, float &carry)
+__device__ __forceinline__ float through_waves(const Span *maps, int wave, float &carry)
 {
     float mine = carry;
 #pragma unroll
@@ -522,32 +517,51 @@ __device__ __forceinline__ float through_waves(const SpanMap *maps, int wave, fl
     return mine;
 }
 template <int W>
-__device__ __forceinline__ SpanMap all_waves(const SpanMap *maps)
+__device__ __forceinline__ Span all_waves(const Span *maps)
 {
-    SpanMap m = maps[0];
+    Running all;
 #pragma unroll
-    for (int w = 1; w < W; ++w) m = compose(maps[w], m);
-    return m;
+    for (int w = 0; w < W; ++w) all.add(maps[w]);
+    return all.span();
 }
 
-// A lane's maps, and their composition.
+// A lane's steps, and the span they make.
 template <int K, bool BF16>
-__device__ __forceinline__ SpanMap chunk_maps(const GatedChunk<K, BF16> &c, float rate, int64_t t,
-                                              int64_t end, GatedStep (&m)[K])
+__device__ __forceinline__ Span chunk_maps(const GatedChunk<K, BF16> &c, float rate, Span (&m)[K])
 {
-    SpanMap own = {0.0f, 0.0f};
+    Running own;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         m[k] = forward_step(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
-        m[k] = step_or_identity(m[k], t + k < end);
-        own = compose(m[k], own);
+        own.add(m[k]);
     }
-    return own;
+    return own.span();
 }
+// The wave's lanes up to each one, from its lanes' spans: products of at most 64
+// decays, good for the states within the wave.  And its whole span (in the last
+// lane), which goes on to the steps behind it.
+struct WaveSpans {
+    Map1 upto;
+    Span all;
+    __device__ __forceinline__ explicit WaveSpans(const Span &own)
+        : upto(wave_scan_inclusive(Map1{own.a, own.b})), all(span_of(wave_sum_to_last(own.l), upto.b))
+    {
+    }
+    // the state, or w, before the lane's steps
+    __device__ __forceinline__ float before_lane(float before_wave) const
+    {
+        return through(wave_shift_up(upto), before_wave);
+    }
+    // behind the wave's
+    __device__ __forceinline__ float behind(float before_wave) const
+    {
+        return through(Map1{read_lane(all.a, kWave - 1), read_lane(all.b, kWave - 1)}, before_wave);
+    }
+};
 // A lane's states from the one before them.
 template <int K>
 __device__ __forceinline__ void chunk_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
-                                             const GatedStep (&m)[K], float h)
+                                             const Span (&m)[K], float h)
 {
     float out[K];
 #pragma unroll
@@ -561,35 +575,33 @@ __device__ __forceinline__ void chunk_states(const GatedArgs &A, int64_t so, int
 }
 
 // Every channel's steps one chunk after the other, in one workgroup.
-template <bool BF16, int K, int W>
+template <bool BF16, bool DOCS, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_time_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[2][W];
+    __shared__ Span maps[2][W];
     const int64_t ch = blockIdx.x;
     const int64_t b = ch / A.D, d = ch - b * A.D;
     const int wave = threadIdx.x / kWave;
     constexpr int P = K * W * kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     float carry = A.h0 ? A.h0[ch] : 0.0f;
     int64_t t = (int64_t)threadIdx.x * K;
-    GatedChunk<K, BF16> now = load_chunk<K, BF16>(A, uo, rs, t, A.T);
+    GatedChunk<K, BF16> now = load_chunk<K, BF16, DOCS>(A, uo, b, t, A.T);
     int parity = 0;
     for (int64_t c = 0; c < A.T; c += P, t += P, parity ^= 1) {
         GatedChunk<K, BF16> next;
-        if (c + P < A.T) next = load_chunk<K, BF16>(A, uo, rs, t + P, A.T);
-        GatedStep m[K];
-        const SpanMap upto = wave_scan_inclusive(chunk_maps<K, BF16>(now, rate, t, A.T, m));
+        if (c + P < A.T) next = load_chunk<K, BF16, DOCS>(A, uo, b, t + P, A.T);
+        Span m[K];
+        const WaveSpans spans(chunk_maps<K, BF16>(now, rate, m));
         float before = carry;
         if constexpr (W > 1) {
-            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
+            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = spans.all;
             __syncthreads();
             before = through_waves<W>(maps[parity], wave, carry);
         }
-        const SpanMap prior = wave_shift_up(upto);
-        chunk_states<K>(A, so, ch, t, m, through(prior, before));
-        if constexpr (W == 1) carry = through(last_lane(upto), carry);
+        chunk_states<K>(A, so, ch, t, m, spans.before_lane(before));
+        if constexpr (W == 1) carry = spans.behind(carry);
         now = next;
     }
 }
@@ -603,9 +615,9 @@ struct GatedBackChunk {
     float before;  // the state in front of the wave's steps
     uint32_t cut;
 };
-template <int K, bool BF16>
+template <int K, bool BF16, bool DOCS>
 __device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A, int64_t uo,
-                                                             int64_t so, const uint8_t *rs,
+                                                             int64_t so, int64_t b,
                                                              int64_t t, int64_t first, int64_t end,
                                                              float h0)
 {
@@ -620,21 +632,20 @@ __device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A,
 #pragma unroll
         for (int k = 0; k < K; ++k) c.gh.w[k] = 0u;
     }
-    c.cut = rs ? load_flags<K>(rs, t, end) : 0u;
+    c.cut = DOCS ? load_flags<K>(A.resets + b * A.T, t, end) : 0u;
     return c;
 }
 template <int K, bool BF16>
-__device__ __forceinline__ SpanMap back_maps(const GatedBackChunk<K, BF16> &c, float rate, int64_t t,
-                                             int64_t end, Decay (&v)[K])
+__device__ __forceinline__ Span back_maps(const GatedBackChunk<K, BF16> &c, float rate, int64_t t,
+                                          int64_t end, Decay (&v)[K])
 {
-    SpanMap own = {0.0f, 0.0f};
+    Running own;
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
         v[k] = decay(rate, c.u[0].get(k));
-        own = compose(step_or_identity(backward_step(v[k], c.gh.get(k), c.cut >> k & 1u), t + k < end),
-                      own);
+        own.add(backward_step(v[k], c.gh.get(k), c.cut >> k & 1u, t + k < end));
     }
-    return own;
+    return own.span();
 }
 // A lane's gradients from the w behind them and the state before its first
 // step; returns its own w, and adds to dlam.
@@ -675,10 +686,10 @@ __device__ __forceinline__ float dlam_sum(float dlam, float *lds)
     return s;
 }
 
-template <bool BF16, int K, int W>
+template <bool BF16, bool DOCS, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[2][W];
+    __shared__ Span maps[2][W];
     __shared__ float sums[W];
     const int64_t ch = blockIdx.x;
     const int64_t b = ch / A.D, d = ch - b * A.D;
@@ -686,33 +697,31 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
     constexpr int P = K * W * kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     float carry = A.gh_last ? A.gh_last[ch] : 0.0f, dlam = 0.0f;
     const float h0 = A.h0 ? A.h0[ch] : 0.0f;
     int64_t c = (A.T - 1) / P * P;  // the last chunk
     const int at = W * kWave - 1 - (int)threadIdx.x, wave_at = (W - 1 - wave) * kWave;
     GatedBackChunk<K, BF16> now =
-        load_back<K, BF16>(A, uo, so, rs, c + at * K, c + wave_at * K, A.T, h0);
+        load_back<K, BF16, DOCS>(A, uo, so, b, c + at * K, c + wave_at * K, A.T, h0);
     int parity = 0;
     for (; c >= 0; c -= P, parity ^= 1) {
         const int64_t t = c + at * K;
         GatedBackChunk<K, BF16> next;
-        if (c > 0) next = load_back<K, BF16>(A, uo, so, rs, t - P, c - P + wave_at * K, A.T, h0);
+        if (c > 0) next = load_back<K, BF16, DOCS>(A, uo, so, b, t - P, c - P + wave_at * K, A.T, h0);
         Decay v[K];
-        const SpanMap upto = wave_scan_inclusive(back_maps<K, BF16>(now, rate, t, A.T, v));
+        const WaveSpans spans(back_maps<K, BF16>(now, rate, t, A.T, v));
         float after = carry;
         if constexpr (W > 1) {
-            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = upto;
+            if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = spans.all;
             __syncthreads();
             after = through_waves<W>(maps[parity], wave, carry);
         }
-        const SpanMap prior = wave_shift_up(upto);
         // the state before the lane's first step: the next lane's last one
         float hp = __shfl_down(now.h.get(K - 1), 1);
         if (threadIdx.x % kWave == kWave - 1) hp = now.before;
         const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, now, v,
-                                                 through(prior, after), hp, dlam);
-        if constexpr (W == 1) carry = through(last_lane(upto), carry);
+                                                 spans.before_lane(after), hp, dlam);
+        if constexpr (W == 1) carry = spans.behind(carry);
         if (A.dh0 && t == 0) A.dh0[ch] = w;
         now = next;
     }
@@ -745,9 +754,9 @@ __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t c
         if (states && (ready & nearer) == nearer) {
             int lane = __ffsll((unsigned long long)states) - 1;
             float state = read_lane(word_value(h), lane);
+            const Span m = span_of(word_value(l), word_value(b));
             while (--lane >= 0)
-                state = through(
-                    SpanMap{read_lane(word_value(l), lane), read_lane(word_value(b), lane)}, state);
+                state = through(Map1{read_lane(m.a, lane), read_lane(m.b, lane)}, state);
             return state;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -757,12 +766,12 @@ __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t c
 // Publishes the chunk's map and state and returns the state before the chunk,
 // in every thread.
 template <int W>
-__device__ __forceinline__ float chunk_carry(const GatedArgs &A, const SpanMap *maps, int64_t ch,
+__device__ __forceinline__ float chunk_carry(const GatedArgs &A, const Span *maps, int64_t ch,
                                              int64_t place, float start, float *lds)
 {
     if (threadIdx.x < kWave) {
         GatedRecord *r = A.records + place * A.channels + ch;
-        const SpanMap all = all_waves<W>(maps);
+        const Span all = all_waves<W>(maps);
         if (place > 0 && threadIdx.x == 0) {
             publish(&r->l, all.l);
             publish(&r->b, all.b);
@@ -777,10 +786,10 @@ __device__ __forceinline__ float chunk_carry(const GatedArgs &A, const SpanMap *
     return *lds;
 }
 
-template <bool BF16, int K, int W>
+template <bool BF16, bool DOCS, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_look_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[W];
+    __shared__ Span maps[W];
     __shared__ uint32_t ticket;
     __shared__ float carry_lds;
     const int64_t ch = blockIdx.x % (uint32_t)A.channels;
@@ -789,23 +798,21 @@ __global__ void __launch_bounds__(W * kWave) gated_look_kernel(GatedArgs A)
     const int wave = threadIdx.x / kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const int64_t t = place * (K * W * kWave) + (int64_t)threadIdx.x * K;
-    const GatedChunk<K, BF16> c = load_chunk<K, BF16>(A, uo, rs, t, A.T);
-    GatedStep m[K];
-    const SpanMap upto = wave_scan_inclusive(chunk_maps<K, BF16>(c, rate, t, A.T, m));
-    if (threadIdx.x % kWave == kWave - 1) maps[wave] = upto;
+    const GatedChunk<K, BF16> c = load_chunk<K, BF16, DOCS>(A, uo, b, t, A.T);
+    Span m[K];
+    const WaveSpans spans(chunk_maps<K, BF16>(c, rate, m));
+    if (threadIdx.x % kWave == kWave - 1) maps[wave] = spans.all;
     __syncthreads();
     float carry = chunk_carry<W>(A, maps, ch, place, A.h0 ? A.h0[ch] : 0.0f, &carry_lds);
     const float before = through_waves<W>(maps, wave, carry);
-    const SpanMap prior = wave_shift_up(upto);
-    chunk_states<K>(A, so, ch, t, m, through(prior, before));
+    chunk_states<K>(A, so, ch, t, m, spans.before_lane(before));
 }
 
-template <bool BF16, int K, int W>
+template <bool BF16, bool DOCS, int K, int W>
 __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs A)
 {
-    __shared__ SpanMap maps[W];
+    __shared__ Span maps[W];
     __shared__ float sums[W];
     __shared__ uint32_t ticket;
     __shared__ float carry_lds;
@@ -815,24 +822,22 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
     const int wave = threadIdx.x / kWave;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const float h0 = A.h0 ? A.h0[ch] : 0.0f;
     constexpr int P = K * W * kWave;
     const int64_t c0 = ((A.T + P - 1) / P - 1 - place) * P;  // places count from the end
     const int at = W * kWave - 1 - (int)threadIdx.x;
     const int64_t t = c0 + at * K;
     const GatedBackChunk<K, BF16> c =
-        load_back<K, BF16>(A, uo, so, rs, t, c0 + (W - 1 - wave) * (kWave * K), A.T, h0);
+        load_back<K, BF16, DOCS>(A, uo, so, b, t, c0 + (W - 1 - wave) * (kWave * K), A.T, h0);
     Decay v[K];
-    const SpanMap upto = wave_scan_inclusive(back_maps<K, BF16>(c, rate, t, A.T, v));
-    if (threadIdx.x % kWave == kWave - 1) maps[wave] = upto;
+    const WaveSpans spans(back_maps<K, BF16>(c, rate, t, A.T, v));
+    if (threadIdx.x % kWave == kWave - 1) maps[wave] = spans.all;
     __syncthreads();
     float carry = chunk_carry<W>(A, maps, ch, place, A.gh_last ? A.gh_last[ch] : 0.0f, &carry_lds);
     const float after = through_waves<W>(maps, wave, carry);
-    const SpanMap prior = wave_shift_up(upto);
     float hp = __shfl_down(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % kWave == kWave - 1) hp = c.before;
-    const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, c, v, through(prior, after), hp,
+    const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, c, v, spans.before_lane(after), hp,
                                              dlam);
     if (A.dh0 && t == 0) A.dh0[ch] = w;
     const float s = dlam_sum<W>(dlam, sums);
@@ -850,21 +855,22 @@ constexpr int kShortThreads = 256;
 // Inclusive scan of the maps over groups of G neighbouring lanes, each group's
 // first lane first (its last, REVERSE); then the map in front of the lane's own.
 template <int G, bool REVERSE>
-__device__ __forceinline__ SpanMap group_scan_exclusive(SpanMap x)
+__device__ __forceinline__ Map1 group_scan_exclusive(const Span &own)
 {
     const int lane = threadIdx.x % G, at = REVERSE ? G - 1 - lane : lane;
+    Map1 x = {own.a, own.b};
 #pragma unroll
     for (int o = 1; o < G; o *= 2) {
-        const SpanMap y = REVERSE ? SpanMap{__shfl_down(x.l, o), __shfl_down(x.b, o)}
-                                  : SpanMap{__shfl_up(x.l, o), __shfl_up(x.b, o)};
+        const Map1 y = REVERSE ? Map1{__shfl_down(x.a, o), __shfl_down(x.b, o)}
+                               : Map1{__shfl_up(x.a, o), __shfl_up(x.b, o)};
         if (at >= o) x = compose(x, y);
     }
-    const SpanMap y = REVERSE ? SpanMap{__shfl_down(x.l, 1), __shfl_down(x.b, 1)}
-                              : SpanMap{__shfl_up(x.l, 1), __shfl_up(x.b, 1)};
-    return at > 0 ? y : SpanMap{0.0f, 0.0f};
+    const Map1 y = REVERSE ? Map1{__shfl_down(x.a, 1), __shfl_down(x.b, 1)}
+                           : Map1{__shfl_up(x.a, 1), __shfl_up(x.b, 1)};
+    return at > 0 ? y : Map1{1.0f, 0.0f};
 }
 
-template <bool BF16, int K, int G>
+template <bool BF16, bool DOCS, int K, int G>
 __global__ void __launch_bounds__(kShortThreads) gated_short_kernel(GatedArgs A)
 {
     const int64_t ch = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) / G;
@@ -873,15 +879,14 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_kernel(GatedArgs A)
     const int64_t t = (int64_t)(threadIdx.x % G) * K, end = here ? A.T : 0;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
-    const GatedChunk<K, BF16> c = load_chunk<K, BF16>(A, uo, rs, t, end);
+    const GatedChunk<K, BF16> c = load_chunk<K, BF16, DOCS>(A, uo, b, t, end);
     const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
-    GatedStep m[K];
-    const SpanMap prior = group_scan_exclusive<G, false>(chunk_maps<K, BF16>(c, rate, t, end, m));
+    Span m[K];
+    const Map1 prior = group_scan_exclusive<G, false>(chunk_maps<K, BF16>(c, rate, m));
     if (here) chunk_states<K>(A, so, ch, t, m, through(prior, h0));
 }
 
-template <bool BF16, int K, int G>
+template <bool BF16, bool DOCS, int K, int G>
 __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(GatedArgs A)
 {
     const int64_t ch = ((int64_t)blockIdx.x * kShortThreads + threadIdx.x) / G;
@@ -890,12 +895,11 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(Gate
     const int64_t t = (int64_t)(threadIdx.x % G) * K, end = here ? A.T : 0;
     const float rate = decay_rate(A.lam[d], A.power);
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
-    const uint8_t *rs = A.resets ? A.resets + b * A.T : nullptr;
     const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
-    const GatedBackChunk<K, BF16> c = load_back<K, BF16>(A, uo, so, rs, t, 0, end, h0);
+    const GatedBackChunk<K, BF16> c = load_back<K, BF16, DOCS>(A, uo, so, b, t, 0, end, h0);
     const float after = A.gh_last && here ? A.gh_last[ch] : 0.0f;
     Decay v[K];
-    const SpanMap prior = group_scan_exclusive<G, true>(back_maps<K, BF16>(c, rate, t, end, v));
+    const Map1 prior = group_scan_exclusive<G, true>(back_maps<K, BF16>(c, rate, t, end, v));
     float hp = __shfl_up(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % G == 0) hp = h0;
     const float w = chunk_gradients<K, BF16>(A, uo, t, end, c, v, through(prior, after), hp,
@@ -955,7 +959,7 @@ __global__ void __launch_bounds__(kGatedStepThreads) gated_step_kernel(GatedStep
             continue;
         }
         const int64_t o = b * A.usb + d;
-        const GatedStep m = forward_step(decay_rate(A.lam[d], A.power), load_gate<BF16>(A.u[0], o),
+        const Span m = forward_step(decay_rate(A.lam[d], A.power), load_gate<BF16>(A.u[0], o),
                                  load_gate<BF16>(A.u[1], o), load_gate<BF16>(A.u[2], o), false);
         float *s = A.states + slot * A.D + d;
         const float h = through(m, *s);

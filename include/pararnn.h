@@ -306,7 +306,8 @@ pararnn_status_t pararnn_solve_gru_noalloc(const pararnn_shape_t *shape, const v
  *     l_t = -power softplus(lam_d) sig(u_r),   a_t = exp(l_t)
  *     h_t = k_t a_t h_{t-1} + sqrt(1 - a_t^2) sig(u_i) u_x
  * k_t = 0 where resets[b][t] is non-zero (the first step of a new document in
- * a packed row: nothing of the state before it is kept), else 1.
+ * a packed row: nothing of the state before it is kept, also if that state is
+ * not finite, and no gradient of the document goes back past it), else 1.
  *   shape   : u strides for u and du, s strides for h and gh
  *   u       : 3 planes [B][D][T], dtype u_dtype (F32 or BF16)
  *   lam     : [D] float32;  power : > 0, finite

@@ -82,39 +82,90 @@ __device__ __forceinline__ Decay decay(float rate, float r)
 // logarithms add up in full.  So a span's a is 2^l, l the sum of its steps'.
 // (A steady gate at -8 over 262144 steps: what is left of h_0 was off by 0.8%
 // with products, by 1e-5 with sums.)
+//
+// A reset cuts: what is before it is not multiplied by 0, which would keep a
+// NaN or an infinity, but left out.  A cut span has a = -0 (decays are not
+// negative, and +0 where they underflow) and l = -inf.  Where every number is
+// finite the product with -0 does the same: forward with lanes in time, and in
+// the lanes' scan, it is done that way first, and once more, CAREFUL, where a
+// lane of the wave ends with a number that is not finite, as any does that met
+// one.  (Careful at once, 16x600x1024 float32 takes 42 us instead of 38.  With a
+// lane a channel, and backward where registers are scarce, the first pass does
+// not pay: 512x1x4096 bfloat16 28 us with it, 18 without; 8x4096x1024 bfloat16
+// backward 165 and 142; but looking back, 1x262144x64 backward, 93 and 99.)  Kernels without
+// resets (DOCS false) look for neither.
 struct Span {
     float a, b, l;
 };
-constexpr float kNoMemory = -__builtin_inff();  // l where a = 0
-__device__ __forceinline__ float through(const Map1 &m, float x) { return fmaf_(m.a, x, m.b); }
-__device__ __forceinline__ float through(const Span &m, float x) { return fmaf_(m.a, x, m.b); }
-__device__ __forceinline__ Span span_of(float l, float b) { return {ex2(l), b, l}; }
+constexpr float kCut = -0.0f, kNoMemory = -__builtin_inff();
+template <bool DOCS>
+__device__ __forceinline__ bool is_cut(float a)
+{
+    return DOCS && __float_as_uint(a) == 0x80000000u;
+}
+__device__ __forceinline__ bool any_not_finite(float x)
+{
+    return __ballot(!(fabsf(x) < __builtin_inff())) != 0;
+}
+template <bool CAREFUL, class M>
+__device__ __forceinline__ float through(const M &m, float x)
+{
+    return is_cut<CAREFUL>(m.a) ? m.b : fmaf_(m.a, x, m.b);
+}
+template <bool DOCS>
+__device__ __forceinline__ Span span_of(float l, float b)
+{
+    return {DOCS && l == kNoMemory ? kCut : ex2(l), b, l};
+}
+// L behind E, by the product of their decays; that of a cut E is -0 as well.
+template <bool CAREFUL>
+__device__ __forceinline__ Map1 joined(const Map1 &L, const Map1 &E)
+{
+    return {is_cut<CAREFUL>(L.a) ? L.a : L.a * E.a, through<CAREFUL>(L, E.b)};
+}
 
 // The span of the steps, or spans, added so far.
+template <bool DOCS, bool CAREFUL>
 struct Running {
     float l = 0.0f, b = 0.0f;
     __device__ __forceinline__ void add(const Span &m)
     {
-        b = through(m, b);
-        l += m.l;
+        b = through<CAREFUL>(m, b);
+        l = is_cut<DOCS>(m.a) ? kNoMemory : l + m.l;
     }
-    __device__ __forceinline__ Span span() const { return span_of(l, b); }
 };
+// `add_all` adds the steps in order; TWICE: without care first.
+template <bool DOCS, bool TWICE, class F>
+__device__ __forceinline__ Span sum_of(const F &add_all)
+{
+    Running<DOCS, DOCS && !TWICE> r;
+    add_all(r);
+    if constexpr (DOCS && TWICE) {
+        if (any_not_finite(r.b)) {
+            Running<DOCS, true> c;
+            add_all(c);
+            return span_of<DOCS>(c.l, c.b);
+        }
+    }
+    return span_of<DOCS>(r.l, r.b);
+}
 
+template <bool DOCS>
 __device__ __forceinline__ Span forward_step(float rate, float r, float i, float x, bool reset)
 {
     const Decay v = decay(rate, r);
-    return {reset ? 0.0f : v.a, __builtin_amdgcn_sqrtf(v.y) * sigmoid_q(-kLog2e * i) * x,
-            reset ? kNoMemory : v.l2};
+    return {DOCS && reset ? kCut : v.a, __builtin_amdgcn_sqrtf(v.y) * sigmoid_q(-kLog2e * i) * x,
+            v.l2};
 }
 // Backwards, of w: w -> a (gh + w).  A step past the end (not `in`, gh = 0) comes
 // before all others and leaves w, which is 0 in a span so far, as it is.
 // (Forward, steps past the end come last, and no one asks for what is behind
 // them.)
+template <bool DOCS>
 __device__ __forceinline__ Span backward_step(const Decay &v, float gh, bool reset, bool in)
 {
-    const float a = reset ? 0.0f : v.a;
-    return {a, a * gh, in ? (reset ? kNoMemory : v.l2) : 0.0f};
+    const bool cut = DOCS && reset && in;
+    return {cut ? kCut : v.a, cut ? 0.0f : v.a * gh, in ? v.l2 : 0.0f};
 }
 
 // Gradients of one step from G = dL/dh_t (total) and h_{t-1}.  With
@@ -214,14 +265,14 @@ __device__ __forceinline__ LaneSteps<K> lane_steps(const GatedArgs &A, int64_t u
     return c;
 }
 // The states of steps t .. t + K - 1 from the one before them.
-template <int K>
+template <bool DOCS, int K>
 __device__ __forceinline__ void lane_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
                                             const Span (&m)[K], float h)
 {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         if (t + k >= A.T) continue;
-        h = through(m[k], h);
+        h = through<DOCS>(m[k], h);
         A.h[so + (t + k) * A.sst] = h;
         if (A.h_last && t + k == A.T - 1) A.h_last[ch] = h;
     }
@@ -285,20 +336,21 @@ __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
         const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
 #pragma unroll
         for (int k = 0; k < kGatedSteps; ++k)
-            m[k] = forward_step(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
+            m[k] = forward_step<DOCS>(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
     };
     int64_t t = 0;
     for (; t + kGatedSteps < A.T; t += kGatedSteps) {
         load(t);
-        lane_states<kGatedSteps>(A, so, ch, t, m, h);
-        Running own;
+        lane_states<DOCS, kGatedSteps>(A, so, ch, t, m, h);
+        const Span own = sum_of<DOCS, false>([&](auto &sum) {
 #pragma unroll
-        for (int k = 0; k < kGatedSteps; ++k) own.add(m[k]);
-        h = through(own.span(), h);
+            for (int k = 0; k < kGatedSteps; ++k) sum.add(m[k]);
+        });
+        h = through<DOCS>(own, h);
     }
     if (t < A.T) {
         load(t);
-        lane_states<kGatedSteps>(A, so, ch, t, m, h);
+        lane_states<DOCS, kGatedSteps>(A, so, ch, t, m, h);
     }
 }
 template <bool BF16, bool DOCS>
@@ -322,11 +374,12 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
             w = first;
             break;
         }
-        Running own;
+        const Span own = sum_of<DOCS, false>([&](auto &sum) {
 #pragma unroll
-        for (int k = kGatedSteps - 1; k >= 0; --k)
-            own.add(backward_step(v[k], e.gh[k], c.cut[k], t + k < A.T));
-        w = through(own.span(), w);
+            for (int k = kGatedSteps - 1; k >= 0; --k)
+                sum.add(backward_step<DOCS>(v[k], e.gh[k], c.cut[k], t + k < A.T));
+        });
+        w = through<DOCS>(own, w);
     }
     A.dlam_part[ch] = dlam;
     if (A.dh0) A.dh0[ch] = w;
@@ -345,6 +398,7 @@ constexpr int kSpanWaves = 8, kSpanChunk = kSpanWaves * kGatedSteps;
 // A lane: the state behind place - 1 > -1 of channel ch, from the words of the
 // nearest kLookAhead predecessors, which are loaded together.
 constexpr int kLookAhead = 6;
+template <bool DOCS>
 __device__ __forceinline__ float lane_look_back(const uint64_t *words, int64_t channels, int64_t ch,
                                                 int64_t place)
 {
@@ -365,7 +419,7 @@ __device__ __forceinline__ float lane_look_back(const uint64_t *words, int64_t c
                 found = true, state = word_value(h[j]);
             } else if (j + 1 < kLookAhead) {
                 found = found && l[j] && b[j];
-                state = through(span_of(word_value(l[j]), word_value(b[j])), state);
+                state = through<DOCS>(span_of<DOCS>(word_value(l[j]), word_value(b[j])), state);
             }
         }
         if (found) return state;
@@ -392,6 +446,7 @@ __device__ __forceinline__ SpanPlace span_place(const GatedArgs &A, uint32_t *ti
     s.ch = min(s.ch, A.channels - 1);
     return s;
 }
+template <bool DOCS>
 __device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace &s, const Span &own,
                                             float start, Span (*maps)[kWave], float *carry)
 {
@@ -399,24 +454,24 @@ __device__ __forceinline__ float span_carry(const GatedArgs &A, const SpanPlace 
     __syncthreads();
     if (s.wave == 0 && A.words) {
         if (s.here) {
-            Running sum;
+            const Span all = sum_of<DOCS, false>([&](auto &sum) {
 #pragma unroll
-            for (int w = 0; w < kSpanWaves; ++w) sum.add(maps[w][s.lane]);
-            const Span all = sum.span();
+                for (int w = 0; w < kSpanWaves; ++w) sum.add(maps[w][s.lane]);
+            });
             uint64_t *r = A.words + s.place * 3 * A.channels + s.ch;
             if (s.place > 0) {
                 publish(r + A.channels, all.l);
                 publish(r + 2 * A.channels, all.b);
             }
             const float before =
-                s.place > 0 ? lane_look_back(A.words, A.channels, s.ch, s.place) : start;
-            publish(r, through(all, before));
+                s.place > 0 ? lane_look_back<DOCS>(A.words, A.channels, s.ch, s.place) : start;
+            publish(r, through<DOCS>(all, before));
             carry[s.lane] = before;
         }
     }
     __syncthreads();
     float h = A.words ? carry[s.lane] : start;
-    for (int w = 0; w < s.wave; ++w) h = through(maps[w][s.lane], h);
+    for (int w = 0; w < s.wave; ++w) h = through<DOCS>(maps[w][s.lane], h);
     return h;
 }
 
@@ -433,14 +488,15 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_kernel(GatedArg
     const int64_t uo = b * A.usb + d * A.usd, so = b * A.ssb + d * A.ssd;
     const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
     Span m[kGatedSteps];
-    Running own;
 #pragma unroll
-    for (int k = 0; k < kGatedSteps; ++k) {
-        m[k] = forward_step(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
-        own.add(m[k]);
-    }
-    const float h = span_carry(A, s, own.span(), A.h0 ? A.h0[s.ch] : 0.0f, maps, carry);
-    if (s.here) lane_states<kGatedSteps>(A, so, s.ch, t, m, h);
+    for (int k = 0; k < kGatedSteps; ++k)
+        m[k] = forward_step<DOCS>(rate, c.u[0][k], c.u[1][k], c.u[2][k], c.cut[k]);
+    const Span own = sum_of<DOCS, false>([&](auto &sum) {
+#pragma unroll
+        for (int k = 0; k < kGatedSteps; ++k) sum.add(m[k]);
+    });
+    const float h = span_carry<DOCS>(A, s, own, A.h0 ? A.h0[s.ch] : 0.0f, maps, carry);
+    if (s.here) lane_states<DOCS, kGatedSteps>(A, so, s.ch, t, m, h);
 }
 
 // Backward: places and waves count from the end.
@@ -459,13 +515,14 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
     const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
     const auto e = lane_back<kGatedSteps>(A, so, t, A.h0 ? A.h0[s.ch] : 0.0f);
     Decay v[kGatedSteps];
-    Running own;
 #pragma unroll
-    for (int k = kGatedSteps - 1; k >= 0; --k) {
-        v[k] = decay(rate, c.u[0][k]);
-        own.add(backward_step(v[k], e.gh[k], c.cut[k], t + k < A.T));
-    }
-    float w = span_carry(A, s, own.span(), A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
+    for (int k = 0; k < kGatedSteps; ++k) v[k] = decay(rate, c.u[0][k]);
+    const Span own = sum_of<DOCS, false>([&](auto &sum) {
+#pragma unroll
+        for (int k = kGatedSteps - 1; k >= 0; --k)
+            sum.add(backward_step<DOCS>(v[k], e.gh[k], c.cut[k], t + k < A.T));
+    });
+    float w = span_carry<DOCS>(A, s, own, A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
     if (s.here) w = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
     sums[s.wave][s.lane] = dlam;
     __syncthreads();
@@ -505,67 +562,97 @@ __device__ __forceinline__ GatedChunk<K, BF16> load_chunk(const GatedArgs &A, in
 
 // The state before wave `wave`'s part of the chunk, from the one before the
 // chunk and the waves' maps in order; `carry` moves on to the next chunk.
-template <int W>
+template <bool DOCS, int W>
 __device__ __forceinline__ float through_waves(const Span *maps, int wave, float &carry)
 {
     float mine = carry;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         if (w == wave) mine = carry;
-        carry = through(maps[w], carry);
+        carry = through<DOCS>(maps[w], carry);
     }
     return mine;
 }
-template <int W>
+template <bool DOCS, int W>
 __device__ __forceinline__ Span all_waves(const Span *maps)
 {
-    Running all;
+    return sum_of<DOCS, true>([&](auto &sum) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) all.add(maps[w]);
-    return all.span();
+        for (int w = 0; w < W; ++w) sum.add(maps[w]);
+    });
 }
 
 // A lane's steps, and the span they make.
-template <int K, bool BF16>
+template <int K, bool BF16, bool DOCS>
 __device__ __forceinline__ Span chunk_maps(const GatedChunk<K, BF16> &c, float rate, Span (&m)[K])
 {
-    Running own;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        m[k] = forward_step(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
-        own.add(m[k]);
-    }
-    return own.span();
+    for (int k = 0; k < K; ++k)
+        m[k] = forward_step<DOCS>(rate, c.u[0].get(k), c.u[1].get(k), c.u[2].get(k), c.cut >> k & 1u);
+    return sum_of<DOCS, true>([&](auto &sum) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) sum.add(m[k]);
+    });
 }
 // The wave's lanes up to each one, from its lanes' spans: products of at most 64
 // decays, good for the states within the wave.  And its whole span (in the last
 // lane), which goes on to the steps behind it.
+__device__ __forceinline__ Map1 careful_scan(Map1 x)
+{
+    x = joined<true>(x, dpp_map<0x111>(x));
+    x = joined<true>(x, dpp_map<0x112>(x));
+    x = joined<true>(x, dpp_map<0x114>(x));
+    x = joined<true>(x, dpp_map<0x118>(x));
+    x = joined<true>(x, dpp_map<0x142, 0xA>(x));
+    return joined<true>(x, dpp_map<0x143, 0xC>(x));
+}
+template <bool DOCS>
 struct WaveSpans {
     Map1 upto;
     Span all;
+    uint64_t cuts = 0;  // the cut lanes (a product of two -0 is +0)
     __device__ __forceinline__ explicit WaveSpans(const Span &own)
-        : upto(wave_scan_inclusive(Map1{own.a, own.b})), all(span_of(wave_sum_to_last(own.l), upto.b))
     {
+        const Map1 x = {own.a, own.b};
+        if constexpr (DOCS) cuts = __ballot(is_cut<DOCS>(own.a));
+        upto = wave_scan_inclusive(x);
+        if (DOCS && any_not_finite(upto.b)) upto = careful_scan(x);
+        // (a NaN in front of a cut is in the sum)
+        const float l = wave_sum_to_last(own.l);
+        all = span_of<DOCS>(cuts ? kNoMemory : l, upto.b);
     }
     // the state, or w, before the lane's steps
     __device__ __forceinline__ float before_lane(float before_wave) const
     {
-        return through(wave_shift_up(upto), before_wave);
+        const Map1 x = wave_shift_up(upto);
+        if (DOCS && any_not_finite(before_wave) &&
+            __builtin_amdgcn_mbcnt_hi((uint32_t)(cuts >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)cuts, 0u)))
+            return x.b;
+        return through<false>(x, before_wave);
     }
     // behind the wave's
     __device__ __forceinline__ float behind(float before_wave) const
     {
-        return through(Map1{read_lane(all.a, kWave - 1), read_lane(all.b, kWave - 1)}, before_wave);
+        return through<DOCS>(Map1{read_lane(all.a, kWave - 1), read_lane(all.b, kWave - 1)},
+                             before_wave);
     }
 };
+
 // A lane's states from the one before them.
-template <int K>
+template <bool DOCS, int K>
 __device__ __forceinline__ void chunk_states(const GatedArgs &A, int64_t so, int64_t ch, int64_t t,
                                              const Span (&m)[K], float h)
 {
-    float out[K];
+    float out[K], last = h;
 #pragma unroll
-    for (int k = 0; k < K; ++k) out[k] = h = through(m[k], h);
+    for (int k = 0; k < K; ++k) out[k] = last = through<false>(m[k], last);
+    if constexpr (DOCS) {
+        if (any_not_finite(last)) {
+            last = h;
+#pragma unroll
+            for (int k = 0; k < K; ++k) out[k] = last = through<true>(m[k], last);
+        }
+    }
     if (t >= A.T) return;
     store_raw<false, K>(A.h, so, t, A.T, out);
     if (A.h_last && t + K >= A.T)
@@ -593,14 +680,14 @@ __global__ void __launch_bounds__(W * kWave) gated_time_kernel(GatedArgs A)
         GatedChunk<K, BF16> next;
         if (c + P < A.T) next = load_chunk<K, BF16, DOCS>(A, uo, b, t + P, A.T);
         Span m[K];
-        const WaveSpans spans(chunk_maps<K, BF16>(now, rate, m));
+        const WaveSpans<DOCS> spans(chunk_maps<K, BF16, DOCS>(now, rate, m));
         float before = carry;
         if constexpr (W > 1) {
             if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = spans.all;
             __syncthreads();
-            before = through_waves<W>(maps[parity], wave, carry);
+            before = through_waves<DOCS, W>(maps[parity], wave, carry);
         }
-        chunk_states<K>(A, so, ch, t, m, spans.before_lane(before));
+        chunk_states<DOCS, K>(A, so, ch, t, m, spans.before_lane(before));
         if constexpr (W == 1) carry = spans.behind(carry);
         now = next;
     }
@@ -635,17 +722,17 @@ __device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A,
     c.cut = DOCS ? load_flags<K>(A.resets + b * A.T, t, end) : 0u;
     return c;
 }
-template <int K, bool BF16>
+template <int K, bool BF16, bool DOCS, bool TWICE>
 __device__ __forceinline__ Span back_maps(const GatedBackChunk<K, BF16> &c, float rate, int64_t t,
                                           int64_t end, Decay (&v)[K])
 {
-    Running own;
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-        v[k] = decay(rate, c.u[0].get(k));
-        own.add(backward_step(v[k], c.gh.get(k), c.cut >> k & 1u, t + k < end));
-    }
-    return own.span();
+    for (int k = 0; k < K; ++k) v[k] = decay(rate, c.u[0].get(k));
+    return sum_of<DOCS, TWICE>([&](auto &sum) {
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k)
+            sum.add(backward_step<DOCS>(v[k], c.gh.get(k), c.cut >> k & 1u, t + k < end));
+    });
 }
 // A lane's gradients from the w behind them and the state before its first
 // step; returns its own w, and adds to dlam.
@@ -709,12 +796,12 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
         GatedBackChunk<K, BF16> next;
         if (c > 0) next = load_back<K, BF16, DOCS>(A, uo, so, b, t - P, c - P + wave_at * K, A.T, h0);
         Decay v[K];
-        const WaveSpans spans(back_maps<K, BF16>(now, rate, t, A.T, v));
+        const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS, false>(now, rate, t, A.T, v));
         float after = carry;
         if constexpr (W > 1) {
             if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = spans.all;
             __syncthreads();
-            after = through_waves<W>(maps[parity], wave, carry);
+            after = through_waves<DOCS, W>(maps[parity], wave, carry);
         }
         // the state before the lane's first step: the next lane's last one
         float hp = __shfl_down(now.h.get(K - 1), 1);
@@ -741,6 +828,7 @@ struct GatedRecord {
     uint64_t unused;
 };
 // A wave: the state behind place - 1 > -1 of channel ch.
+template <bool DOCS>
 __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t channels, int64_t ch,
                                            int64_t place)
 {
@@ -754,9 +842,9 @@ __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t c
         if (states && (ready & nearer) == nearer) {
             int lane = __ffsll((unsigned long long)states) - 1;
             float state = read_lane(word_value(h), lane);
-            const Span m = span_of(word_value(l), word_value(b));
+            const Span m = span_of<DOCS>(word_value(l), word_value(b));
             while (--lane >= 0)
-                state = through(Map1{read_lane(m.a, lane), read_lane(m.b, lane)}, state);
+                state = through<DOCS>(Map1{read_lane(m.a, lane), read_lane(m.b, lane)}, state);
             return state;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -765,20 +853,20 @@ __device__ __forceinline__ float look_back(const GatedRecord *records, int64_t c
 
 // Publishes the chunk's map and state and returns the state before the chunk,
 // in every thread.
-template <int W>
+template <bool DOCS, int W>
 __device__ __forceinline__ float chunk_carry(const GatedArgs &A, const Span *maps, int64_t ch,
                                              int64_t place, float start, float *lds)
 {
     if (threadIdx.x < kWave) {
         GatedRecord *r = A.records + place * A.channels + ch;
-        const Span all = all_waves<W>(maps);
+        const Span all = all_waves<DOCS, W>(maps);
         if (place > 0 && threadIdx.x == 0) {
             publish(&r->l, all.l);
             publish(&r->b, all.b);
         }
-        const float before = place > 0 ? look_back(A.records, A.channels, ch, place) : start;
+        const float before = place > 0 ? look_back<DOCS>(A.records, A.channels, ch, place) : start;
         if (threadIdx.x == 0) {
-            publish(&r->h, through(all, before));
+            publish(&r->h, through<DOCS>(all, before));
             *lds = before;
         }
     }
@@ -801,12 +889,12 @@ __global__ void __launch_bounds__(W * kWave) gated_look_kernel(GatedArgs A)
     const int64_t t = place * (K * W * kWave) + (int64_t)threadIdx.x * K;
     const GatedChunk<K, BF16> c = load_chunk<K, BF16, DOCS>(A, uo, b, t, A.T);
     Span m[K];
-    const WaveSpans spans(chunk_maps<K, BF16>(c, rate, m));
+    const WaveSpans<DOCS> spans(chunk_maps<K, BF16, DOCS>(c, rate, m));
     if (threadIdx.x % kWave == kWave - 1) maps[wave] = spans.all;
     __syncthreads();
-    float carry = chunk_carry<W>(A, maps, ch, place, A.h0 ? A.h0[ch] : 0.0f, &carry_lds);
-    const float before = through_waves<W>(maps, wave, carry);
-    chunk_states<K>(A, so, ch, t, m, spans.before_lane(before));
+    float carry = chunk_carry<DOCS, W>(A, maps, ch, place, A.h0 ? A.h0[ch] : 0.0f, &carry_lds);
+    const float before = through_waves<DOCS, W>(maps, wave, carry);
+    chunk_states<DOCS, K>(A, so, ch, t, m, spans.before_lane(before));
 }
 
 template <bool BF16, bool DOCS, int K, int W>
@@ -830,11 +918,11 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
     const GatedBackChunk<K, BF16> c =
         load_back<K, BF16, DOCS>(A, uo, so, b, t, c0 + (W - 1 - wave) * (kWave * K), A.T, h0);
     Decay v[K];
-    const WaveSpans spans(back_maps<K, BF16>(c, rate, t, A.T, v));
+    const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS, true>(c, rate, t, A.T, v));
     if (threadIdx.x % kWave == kWave - 1) maps[wave] = spans.all;
     __syncthreads();
-    float carry = chunk_carry<W>(A, maps, ch, place, A.gh_last ? A.gh_last[ch] : 0.0f, &carry_lds);
-    const float after = through_waves<W>(maps, wave, carry);
+    float carry = chunk_carry<DOCS, W>(A, maps, ch, place, A.gh_last ? A.gh_last[ch] : 0.0f, &carry_lds);
+    const float after = through_waves<DOCS, W>(maps, wave, carry);
     float hp = __shfl_down(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % kWave == kWave - 1) hp = c.before;
     const float w = chunk_gradients<K, BF16>(A, uo, t, A.T, c, v, spans.before_lane(after), hp,
@@ -854,20 +942,36 @@ constexpr int kShortThreads = 256;
 
 // Inclusive scan of the maps over groups of G neighbouring lanes, each group's
 // first lane first (its last, REVERSE); then the map in front of the lane's own.
-template <int G, bool REVERSE>
-__device__ __forceinline__ Map1 group_scan_exclusive(const Span &own)
+template <bool CAREFUL, int G, bool REVERSE>
+__device__ __forceinline__ Map1 group_scan(Map1 x)
 {
     const int lane = threadIdx.x % G, at = REVERSE ? G - 1 - lane : lane;
-    Map1 x = {own.a, own.b};
 #pragma unroll
     for (int o = 1; o < G; o *= 2) {
         const Map1 y = REVERSE ? Map1{__shfl_down(x.a, o), __shfl_down(x.b, o)}
                                : Map1{__shfl_up(x.a, o), __shfl_up(x.b, o)};
-        if (at >= o) x = compose(x, y);
+        if (at >= o) x = joined<CAREFUL>(x, y);
     }
+    return x;
+}
+// `start` through the group's spans in front of the lane's own.
+template <bool DOCS, int G, bool REVERSE>
+__device__ __forceinline__ float before_lane(const Span &own, float start)
+{
+    const int lane = threadIdx.x % G, at = REVERSE ? G - 1 - lane : lane;
+    Map1 x = group_scan<false, G, REVERSE>(Map1{own.a, own.b});
+    if (DOCS && any_not_finite(x.b)) x = group_scan<true, G, REVERSE>(Map1{own.a, own.b});
+    const uint64_t wave_cuts = DOCS ? __ballot(is_cut<DOCS>(own.a)) : 0;
     const Map1 y = REVERSE ? Map1{__shfl_down(x.a, 1), __shfl_down(x.b, 1)}
                            : Map1{__shfl_up(x.a, 1), __shfl_up(x.b, 1)};
-    return at > 0 ? y : Map1{1.0f, 0.0f};
+    if (at == 0) return start;
+    if constexpr (DOCS) {
+        // the group's cut lanes, and those in front of this one
+        const uint32_t cuts = (uint32_t)(wave_cuts >> (threadIdx.x % kWave - lane)) & ((1u << G) - 1);
+        if (REVERSE ? cuts >> (lane + 1) : cuts & ((1u << lane) - 1))
+            if (!(fabsf(start) < __builtin_inff())) return y.b;
+    }
+    return through<false>(y, start);
 }
 
 template <bool BF16, bool DOCS, int K, int G>
@@ -882,8 +986,8 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_kernel(GatedArgs A)
     const GatedChunk<K, BF16> c = load_chunk<K, BF16, DOCS>(A, uo, b, t, end);
     const float h0 = A.h0 && here ? A.h0[ch] : 0.0f;
     Span m[K];
-    const Map1 prior = group_scan_exclusive<G, false>(chunk_maps<K, BF16>(c, rate, m));
-    if (here) chunk_states<K>(A, so, ch, t, m, through(prior, h0));
+    const float h = before_lane<DOCS, G, false>(chunk_maps<K, BF16, DOCS>(c, rate, m), h0);
+    if (here) chunk_states<DOCS, K>(A, so, ch, t, m, h);
 }
 
 template <bool BF16, bool DOCS, int K, int G>
@@ -899,10 +1003,10 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(Gate
     const GatedBackChunk<K, BF16> c = load_back<K, BF16, DOCS>(A, uo, so, b, t, 0, end, h0);
     const float after = A.gh_last && here ? A.gh_last[ch] : 0.0f;
     Decay v[K];
-    const Map1 prior = group_scan_exclusive<G, true>(back_maps<K, BF16>(c, rate, t, end, v));
+    const float behind = before_lane<DOCS, G, true>(back_maps<K, BF16, DOCS, false>(c, rate, t, end, v), after);
     float hp = __shfl_up(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % G == 0) hp = h0;
-    const float w = chunk_gradients<K, BF16>(A, uo, t, end, c, v, through(prior, after), hp,
+    const float w = chunk_gradients<K, BF16>(A, uo, t, end, c, v, behind, hp,
                                              dlam);
 #pragma unroll
     for (int o = 1; o < G; o *= 2) dlam += __shfl_xor(dlam, o);
@@ -959,10 +1063,10 @@ __global__ void __launch_bounds__(kGatedStepThreads) gated_step_kernel(GatedStep
             continue;
         }
         const int64_t o = b * A.usb + d;
-        const Span m = forward_step(decay_rate(A.lam[d], A.power), load_gate<BF16>(A.u[0], o),
+        const Span m = forward_step<false>(decay_rate(A.lam[d], A.power), load_gate<BF16>(A.u[0], o),
                                  load_gate<BF16>(A.u[1], o), load_gate<BF16>(A.u[2], o), false);
         float *s = A.states + slot * A.D + d;
-        const float h = through(m, *s);
+        const float h = through<false>(m, *s);
         *s = h;
         A.out[b * A.D + d] = h;
     }

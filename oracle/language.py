@@ -25,8 +25,9 @@ def gated_scan(u, lam, h0, power, resets=None):
     h = np.zeros((B, D)) if h0 is None else np.asarray(h0, np.float64).copy()
     out = np.empty((B, D, T))
     for t in range(T):
-        keep = 1.0 if resets is None else 1.0 - np.asarray(resets[:, t], np.float64)[:, None]
-        h = keep * a[..., t] * h + gain[..., t] * _sig(ui[..., t]) * ux[..., t]
+        if resets is not None:  # nothing of the state is kept, also where it is not finite
+            h = np.where(np.asarray(resets[:, t], bool)[:, None], 0.0, h)
+        h = a[..., t] * h + gain[..., t] * _sig(ui[..., t]) * ux[..., t]
         out[..., t] = h
     return out
 
@@ -44,20 +45,21 @@ def gated_scan_adjoint(u, lam, h0, h, gh, power, resets=None, gh_last=None):
     carry = np.zeros((B, D)) if gh_last is None else np.asarray(gh_last, np.float64).copy()
     dl_q, dl_q_abs, G_max = np.zeros((B, D)), np.zeros((B, D)), 0.0
     for t in range(T - 1, -1, -1):
-        keep = 1.0 if resets is None else 1.0 - np.asarray(resets[:, t], np.float64)[:, None]
+        cut = np.zeros((B, 1), bool) if resets is None else np.asarray(resets[:, t], bool)[:, None]
         G = carry + (0.0 if gh is None else np.asarray(gh[..., t], np.float64))
         G_max = max(G_max, float(np.abs(G).max(initial=0.0)))
         before = h[..., t - 1] if t else (np.zeros((B, D)) if h0 is None else np.asarray(h0, np.float64))
+        before = np.where(cut, 0.0, before)
         at, gt, st, xt = a[..., t], gain[..., t], si[..., t], ux[..., t]
         # d sqrt(1 - e^{2l}) / dl = -e^{2l} / sqrt(1 - e^{2l}); its product with l -> 0 as l -> 0
         slope = np.divide(at * at, gt, out=np.zeros_like(gt), where=gt > 1e-15)
-        dl = G * (keep * at * before - slope * st * xt)
+        dl = G * (at * before - slope * st * xt)
         du[0][..., t] = dl * l[..., t] * (1 - q[..., t])
         du[1][..., t] = G * gt * xt * st * (1 - st)
         du[2][..., t] = G * gt * st
         dl_q += dl * q[..., t]
-        dl_q_abs += np.abs(G * keep * at * before * q[..., t]) + np.abs(G * slope * st * xt * q[..., t])
-        carry = keep * at * G
+        dl_q_abs += np.abs(G * at * before * q[..., t]) + np.abs(G * slope * st * xt * q[..., t])
+        carry = np.where(cut, 0.0, at * G)
     factor = -power * _sig(lam)
     return dict(du=du, dlam=factor * dl_q.sum(0), dh0=carry, G_max=G_max,
                 dlam_terms=np.abs(factor) * dl_q_abs.sum(0))

@@ -101,3 +101,51 @@ def test_long_memory(B, T, D, layout, chunk, ur):
     assert (np.abs(f64(last) - want) <= tol)[fine].all(), float((np.abs(f64(last) - want) / want)[fine].max())
     got = pr.gated_scan_adjoint(u, lam, one, h, None, gh_last=one)
     assert (np.abs(f64(got["dh0"]) - want) <= tol)[fine].all()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("B,T,D,layout", WAYS)
+def test_a_new_document_keeps_nothing_of_a_bad_one(B, T, D, layout, bad):
+    """A document of states that are not finite, between two others: the next one
+    is what it is alone, forward; backward, gradients that are not finite stay
+    in the documents they come from."""
+    r = np.random.default_rng(T)
+    u = [p.copy_(torch.from_numpy(r.standard_normal((B, D, T)))) for p in planes(B, T, D, layout, [0.0] * 3)]
+    lam, h0 = torch.randn(D, device=DEV), torch.randn((B, D), device=DEV)
+    first, second = T // 3, max(T // 3 + 1, 2 * T // 3)
+    resets = torch.zeros((B, T), dtype=torch.bool, device=DEV)
+    resets[:, first] = resets[:, second] = True
+    clean, _ = pr.gated_scan(u, lam, h0, resets=resets)
+    back = pr.gated_scan_adjoint(u, lam, h0, clean, torch.ones_like(clean), resets=resets)
+    for g in (0, 2):  # a gate's NaN is in the decay and the input; an input's in the state alone
+        spoilt = [p.clone(memory_format=torch.preserve_format) for p in u]
+        spoilt[g][:, :, first] = bad if g == 2 else NAN
+        h, _ = pr.gated_scan(spoilt, lam, h0, resets=resets)
+        assert torch.equal(h[..., :first], clean[..., :first])
+        assert not torch.isfinite(h[..., first:second]).any()
+        assert torch.equal(h[..., second:], clean[..., second:])
+    # h0 that is not finite ends with the row's first document
+    h, _ = pr.gated_scan(u, lam, torch.full_like(h0, bad), resets=resets)
+    assert torch.equal(h[..., first:], clean[..., first:])
+    # a gradient in the middle document: the first and the last one do not see it
+    gh = torch.ones_like(clean)
+    gh[..., second - 1] = bad
+    got = pr.gated_scan_adjoint(u, lam, h0, clean, gh, resets=resets)
+    for a, b in zip(got["du"], back["du"]):
+        assert torch.equal(a[..., :first], b[..., :first]) and torch.equal(a[..., second:], b[..., second:])
+        assert not torch.isfinite(a[..., second - 1]).all()
+    if first > 0:
+        assert torch.equal(got["dh0"], back["dh0"])
+    # and states that are not finite, in the gradients of their own document only
+    states = clean.clone(memory_format=torch.preserve_format)
+    states[..., first:second] = bad
+    got = pr.gated_scan_adjoint(u, lam, h0, states, torch.ones_like(clean), resets=resets)
+    for a, b in zip(got["du"], back["du"]):
+        assert torch.equal(a[..., :first], b[..., :first]) and torch.equal(a[..., second:], b[..., second:])
+
+
+def test_the_oracle_cuts_as_well():
+    u = [np.zeros((1, 1, 4)) for _ in range(3)]
+    resets = np.array([[False, False, True, False]])
+    h = ref.gated_scan(u, np.zeros(1), np.full((1, 1), np.nan), 8.0, resets)
+    assert np.isnan(h[0, 0, :2]).all() and np.isfinite(h[0, 0, 2:]).all()

@@ -341,8 +341,8 @@ def _capturing(device, stream):
     device = torch.device(device)
     if device.type != "cuda":
         return False
-    if stream is None and device.index == torch.cuda.current_device():
-        return torch.cuda.is_current_stream_capturing()
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_isCurrentStreamCapturing()
     with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
         return torch.cuda.is_current_stream_capturing()
 
@@ -1028,21 +1028,22 @@ def token_logprobs(logits, tokens, *, top=0, scale=1.0, workspace=None, stream=N
     N, V, stride, dt, _, nws, dev = _planned(
         ("score", top, _signature(logits, tokens, workspace)), _score_plan, logits, tokens, (),
         None, workspace, top)
-    stats = torch.empty((3, N), dtype=torch.float32, device=dev)
-    logprob, entropy, lse = stats.unbind(0)
+    # a tensor each: views of one could not be edited in place
+    logprob = torch.empty(N, dtype=torch.float32, device=dev)
+    entropy = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
     out = dict(logprob=logprob, entropy=entropy, lse=lse)
-    first = stats.data_ptr()
     index = value = None
     if top:
-        out["top_index"] = index = torch.empty((N, top), dtype=torch.int64, device=dev)
-        out["top_logprob"] = value = torch.empty((N, top), dtype=torch.float32, device=dev)
-    _record_on(stream, [stats, index, value])
+        out["top_index"] = index = torch.empty(N, top, dtype=torch.int64, device=dev)
+        out["top_logprob"] = value = torch.empty(N, top, dtype=torch.float32, device=dev)
+    _record_on(stream, [logprob, entropy, lse, index, value])
     at = _where(dev, stream)
     ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
     _check(lib.pararnn_token_logprobs(N, V, logits.data_ptr(), dt, stride, tokens.data_ptr(), top,
-                                      scale, first, first + 4 * N, first + 8 * N, _ptr(index),
-                                      _ptr(value), _ptr(ws), 0 if ws is None else ws.numel(),
-                                      at[1]))
+                                      scale, logprob.data_ptr(), entropy.data_ptr(),
+                                      lse.data_ptr(), _ptr(index), _ptr(value), _ptr(ws),
+                                      0 if ws is None else ws.numel(), at[1]))
     return out
 
 

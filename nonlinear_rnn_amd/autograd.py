@@ -17,12 +17,15 @@ passed to the kernels as strided views (no transpose copy), and the
 gradient for u comes back as one [B][T][G*D] tensor written by the adjoint.
 
 ``gated_scan``, ``block_norm`` and ``token_logprobs`` are the differentiable
-forms of the operators of recurrent language models.
+forms of the operators of recurrent language models.  They have first
+derivatives: differentiating a gradient of theirs raises.
 
 Non-convergence is not an error in the solve; pass ``strict=True`` to raise
 when a solve stops at the iteration cap without reaching the tolerance (this
 reads the device info record, i.e. synchronises).
 """
+import functools
+
 import torch
 
 from . import pararnn as pr
@@ -179,6 +182,42 @@ def lstm_time_major(u, a, c0, h0, *, tol=1e-6, max_iters=20, strict=False):
     return _LstmTimeMajor.apply(u, a, c0, h0, tol, max_iters, strict)
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Its outputs, whose own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, _, *tensors):
+        return tuple(t.view_as(t) for t in tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("trying to differentiate twice: the operators of recurrent language "
+                           "models have first derivatives only")
+
+
+def _once(backward):
+    """A backward pass under ``create_graph`` gives gradients that cannot be
+    differentiated, rather than constants.  (torch's ``once_differentiable``
+    does so only where an incoming gradient depends on something: not for a
+    sum of the outputs, though its gradient depends on the inputs.)"""
+    @functools.wraps(backward)
+    def wrapper(ctx, *grads):
+        second = torch.is_grad_enabled()
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        out = out if isinstance(out, tuple) else (out,)
+        if not second:
+            return out
+        given = [i for i, t in enumerate(out) if t is not None]
+        marked = _NoSecondDerivative.apply(torch.empty(0, requires_grad=True),
+                                           *(out[i] for i in given))
+        out = list(out)
+        for i, t in zip(given, marked):
+            out[i] = t
+        return tuple(out)
+    return wrapper
+
+
 class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ur, ui, ux, lam, h0, power, resets):
@@ -189,6 +228,7 @@ class _GatedScan(torch.autograd.Function):
         return h, h_last
 
     @staticmethod
+    @_once
     def backward(ctx, gh, gh_last):
         ur, ui, ux, lam, h0, resets, h = ctx.saved_tensors
         out = pr.gated_scan_adjoint([ur, ui, ux], lam, h0, h,
@@ -217,6 +257,7 @@ class _BlockNorm(torch.autograd.Function):
         return x.view_as(x) if h is None else y, z
 
     @staticmethod
+    @_once
     def backward(ctx, gy, gz):
         h, gate, x, w_post, w_pre, rstd = ctx.saved_tensors
         out = pr.block_norm_adjoint(h, x, w_post, w_pre, rstd,
@@ -244,6 +285,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return (out["logprob"], out["entropy"], out["lse"]) + tops
 
     @staticmethod
+    @_once
     def backward(ctx, g_logprob, g_entropy, g_lse, *_):
         logits, tokens, lse, entropy = ctx.saved_tensors
         g = [None if x is None else x.contiguous() for x in (g_logprob, g_entropy, g_lse)]

@@ -44,3 +44,22 @@ def test_outputs_of_a_score_are_tensors_of_their_own():
     out["logprob"].fill_(7.0)
     for k in ("entropy", "lse", "top_index", "top_logprob"):
         assert torch.equal(out[k], before[k]) and out[k]._version == versions[k]
+
+
+def second_derivative(loss, leaf):
+    (first,) = torch.autograd.grad(loss, leaf, create_graph=True)
+    (first.square().sum() + leaf.square().sum()).backward()
+
+
+def test_a_second_derivative_is_refused():
+    """Not left out: with a penalty on the gradient, the part that goes through the
+    operator would be missing."""
+    x, tokens = scores()
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        second_derivative(pag.token_logprobs(x, tokens)["logprob"].sum(), x)
+    u = [torch.randn((2, 3, 20), device=DEV, requires_grad=True) for _ in range(3)]
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        second_derivative(pag.gated_scan(u, torch.randn(3, device=DEV))[0].square().sum(), u[0])
+    x = torch.randn((2, 5, 8), device=DEV, requires_grad=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        second_derivative(pag.block_norm(None, x, None, torch.ones(8, device=DEV))[1].square().sum(), x)

@@ -764,7 +764,38 @@ def _check_resets(resets, B, T):
         raise ValueError("resets: must be contiguous bool or uint8")
 
 
-def _scan_plan(u, lam, h0, resets, h, gh, gh_last, workspace, adjoint):
+def _side_by_side(n, dims, strides):
+    """(distance, elements) that put `n` planes of these dims and strides next to
+    each other in one allocation, between the rows that the strides leave apart:
+    gates that lie side by side in one projection.  None where they have no room."""
+    reach, distance = 1, None  # elements that the dimensions so far span
+    for stride, size in sorted((s, d) for s, d in zip(strides, dims) if d > 1):
+        if distance is None and stride >= n * reach:
+            distance, reach = reach, n * reach
+        if stride < reach:
+            return None
+        reach += (size - 1) * stride
+    return None if distance is None else (distance, reach)
+
+
+def _gradient_planes(n, dims, strides, dtype, dev):
+    """New planes with these strides.  Each by itself would take up the room of
+    all that lies between its rows."""
+    place = _side_by_side(n, dims, strides) if 0 not in dims else None
+    if place is None:
+        return [torch.empty_strided(dims, strides, dtype=dtype, device=dev) for _ in range(n)]
+    buffer = torch.empty(place[1], dtype=dtype, device=dev)
+    return [buffer.as_strided(dims, strides, g * place[0]) for g in range(n)]
+
+
+def _check_gradient(given, like, name):
+    """An output for the gradient of `like`: its shape, dtype and strides."""
+    if not _is_tensor(given) or given.shape != like.shape or given.dtype is not like.dtype or (
+            given.numel() and given.stride() != like.stride()):
+        raise ValueError(f"{name}: must have the shape, dtype and strides of what it is the gradient of")
+
+
+def _scan_plan(u, lam, h0, resets, h, gh, gh_last, workspace, adjoint, du=None):
     (B, D, T), udt = _gate_planes(u, 3)
     _check_dense(lam, "lam", (D,))
     for name, x in (("h0", h0), ("gh_last", gh_last)):
@@ -779,8 +810,13 @@ def _scan_plan(u, lam, h0, resets, h, gh, gh_last, workspace, adjoint):
         _check_planes([h], "h" if adjoint else "out", (B, D, T))
         _check_planes([gh], "gh", (B, D, T), allow_none=True)
         ss = _strides([h, gh], "h and gh") or dense
+    if du is not None:
+        _require(len(du) == 3, "du: one plane for each gate")
+        for p in du:
+            _check_gradient(p, u[0], "du")
     dev = u[0].device
-    _check_devices(dev, [("u", p) for p in u] + [("lam", lam), ("h0", h0), ("resets", resets),
+    _check_devices(dev, [("u", p) for p in u] + [("du", p) for p in du or ()]
+                   + [("lam", lam), ("h0", h0), ("resets", resets),
                                                  ("h", h), ("gh", gh), ("gh_last", gh_last),
                                                  ("workspace", workspace)])
     shape = ctypes.byref(make_shape(B, T, D, us, ss))
@@ -814,22 +850,26 @@ def gated_scan(u, lam, h0=None, *, power=8.0, resets=None, out=None, workspace=N
     return out, h_last
 
 
-def gated_scan_adjoint(u, lam, h0, h, gh, *, gh_last=None, power=8.0, resets=None, workspace=None,
-                       stream=None):
+def gated_scan_adjoint(u, lam, h0, h, gh, *, gh_last=None, power=8.0, resets=None, du=None,
+                       workspace=None, stream=None):
     """Backward pass of ``gated_scan`` for L = sum_t <gh_t, h_t> + <gh_last, h_T>.
     h: the forward's states; gh: their gradient (same strides) or None (zero);
-    gh_last [B][D] or None.  Returns dict(du=[3 planes, u's dtype and strides],
-    dlam [D], dh0 [B][D])."""
+    gh_last [B][D] or None; du: 3 planes to write the gates' gradients to (u's
+    dtype and strides: slices of one projection's gradient, say), or None (new
+    ones).  Returns dict(du=[3 planes, u's dtype and strides], dlam [D],
+    dh0 [B][D])."""
     lib = load()
     u = list(u)
-    key = ("scan_adjoint", _signature(*u, lam, h0, resets, h, gh, gh_last, workspace))
+    du = None if du is None else list(du)
+    key = ("scan_adjoint", _signature(*u, lam, h0, resets, h, gh, gh_last, workspace, *(du or ())))
     B, T, D, udt, us, ss, shape, nws, dev = _planned(
-        key, _scan_plan, u, lam, h0, resets, h, gh, gh_last, workspace, True)
-    dt = u[0].dtype
-    du = [torch.empty_strided((B, D, T), us, dtype=dt, device=dev) for _ in range(3)]
+        key, _scan_plan, u, lam, h0, resets, h, gh, gh_last, workspace, True, du)
+    if du is None:
+        du = _gradient_planes(3, (B, D, T), us, u[0].dtype, dev)
+        _record_on(stream, du)
     dlam = torch.empty((D,), dtype=torch.float32, device=dev)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
-    _record_on(stream, du + [dlam, dh0])
+    _record_on(stream, [dlam, dh0])
     at = _where(dev, stream)
     ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
     _check(lib.pararnn_gated_scan_adjoint(shape, _ptr_array(u), udt, lam.data_ptr(), power,
@@ -897,7 +937,7 @@ def _row_strides(t, name):
     return (t.stride(0) if B > 1 else st * T, st)
 
 
-def _block_plan(h, gate, x, w_post, w_pre, rstd, gy, gz, z_dtype, workspace, adjoint):
+def _block_plan(h, gate, x, w_post, w_pre, rstd, gy, gz, z_dtype, workspace, adjoint, dgate=None):
     xdt = _code(x, "x")
     _require(x.dim() == 3, "x: expected a tensor [B][T][D]")
     B, T, D = x.shape
@@ -909,6 +949,9 @@ def _block_plan(h, gate, x, w_post, w_pre, rstd, gy, gz, z_dtype, workspace, adj
     if gate is not None:
         _require(h is not None, "gate: needs h")
         _check_planes([gate], "gate", (B, D, T), _U_DTYPES)
+    if dgate is not None:
+        _require(gate is not None, "dgate: needs a gate")
+        _check_gradient(dgate, gate, "dgate")
     _check_dense(w_pre, "w_pre", (D,))
     if adjoint:
         _check_dense(rstd, "rstd", (2, B, T))
@@ -926,7 +969,7 @@ def _block_plan(h, gate, x, w_post, w_pre, rstd, gy, gz, z_dtype, workspace, adj
     hs = (_strides([h], "h") if h is not None else None) or dense
     gs = (_strides([gate], "gate") if gate is not None else None) or dense
     xs = _row_strides(x, "x")
-    _check_devices(x.device, [("x", x), ("h", h), ("gate", gate),
+    _check_devices(x.device, [("x", x), ("h", h), ("gate", gate), ("dgate", dgate),
                               ("w_post", w_post if h is not None else None), ("w_pre", w_pre),
                               ("rstd", rstd), ("gy", gy), ("gz", gz), ("workspace", workspace)])
     shape = ctypes.byref(BlockShape(B, T, D, *hs, *gs, *xs, *zs))
@@ -959,27 +1002,30 @@ def block_norm(h, x, w_post, w_pre, *, gate=None, scale=1.0, eps=1e-6, z_dtype=t
     return y, z, rstd
 
 
-def block_norm_adjoint(h, x, w_post, w_pre, rstd, gy, gz, *, gate=None, scale=1.0, workspace=None,
-                       stream=None):
+def block_norm_adjoint(h, x, w_post, w_pre, rstd, gy, gz, *, gate=None, scale=1.0, dgate=None,
+                       workspace=None, stream=None):
     """Backward pass of ``block_norm`` from the gradients gy of y (x's dtype and
     strides) and gz of z (either may be None: zero) and the forward's rstd.
+    dgate: where to write the gate's gradient (its dtype and strides: a slice of
+    one projection's gradient, say), or None (a new plane).
     Returns dict(dh, dgate, dx, dw_post, dw_pre); dh, dgate and dw_post are
     None where their input is."""
     lib = load()
     if h is None:
         w_post = None
     B, T, D, xdt, gdt, zdt, hs, gs, xs, shape, nws, dev = _planned(
-        ("block_adjoint", _signature(h, gate, x, w_post, w_pre, rstd, gy, gz, workspace)),
-        _block_plan, h, gate, x, w_post, w_pre, rstd, gy, gz, None, workspace, True)
+        ("block_adjoint", _signature(h, gate, x, w_post, w_pre, rstd, gy, gz, workspace, dgate)),
+        _block_plan, h, gate, x, w_post, w_pre, rstd, gy, gz, None, workspace, True, dgate)
     dx = torch.empty_strided((B, T, D), xs, dtype=x.dtype, device=dev)
-    dh = dgate = dw_post = None
+    dh = dw_post = None
     if h is not None:
         dh = torch.empty_strided((B, D, T), hs, dtype=torch.float32, device=dev)
         dw_post = torch.empty((D,), dtype=torch.float32, device=dev)
-    if gate is not None:
+    if gate is not None and dgate is None:
         dgate = torch.empty_strided((B, D, T), gs, dtype=gate.dtype, device=dev)
+        _record_on(stream, [dgate])
     dw_pre = torch.empty((D,), dtype=torch.float32, device=dev)
-    _record_on(stream, [dx, dh, dgate, dw_post, dw_pre])
+    _record_on(stream, [dx, dh, dw_post, dw_pre])
     at = _where(dev, stream)
     ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
     _check(lib.pararnn_block_norm_adjoint(

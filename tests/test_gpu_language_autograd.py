@@ -63,3 +63,30 @@ def test_a_second_derivative_is_refused():
     x = torch.randn((2, 5, 8), device=DEV, requires_grad=True)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         second_derivative(pag.block_norm(None, x, None, torch.ones(8, device=DEV))[1].square().sum(), x)
+
+
+@pytest.mark.parametrize("layout", ["channel", "time"])
+def test_gradients_of_one_projection(layout):
+    """Gates that are slices of one projection: gradients next to each other, or
+    written to the slices of one tensor, are those of separate planes."""
+    B, D, T = 3, 20, 70
+    u = torch.randn((B, 4 * D, T) if layout == "channel" else (B, T, 4 * D), device=DEV)
+    du = torch.empty_like(u)
+    u, du = (p if layout == "channel" else p.transpose(1, 2) for p in (u, du))
+    gates, dgates = ([p[:, g * D:(g + 1) * D] for g in range(4)] for p in (u, du))
+    lam, x = torch.randn(D, device=DEV), torch.randn((B, T, D), device=DEV)
+    w = torch.rand(D, device=DEV) + 0.5
+    h, _ = pr.gated_scan(gates[:3], lam)
+    _, _, rstd = pr.block_norm(h, x, w, w, gate=gates[3])
+    gh, gy = torch.empty_strided(h.shape, h.stride(), device=DEV).normal_(), torch.randn_like(x)
+    one = pr.gated_scan_adjoint(gates[:3], lam, None, h, gh)
+    two = pr.gated_scan_adjoint([p.clone(memory_format=torch.contiguous_format) for p in gates[:3]], lam, None,
+                                h.contiguous(), gh.contiguous()) if layout == "channel" else one
+    into = pr.gated_scan_adjoint(gates[:3], lam, None, h, gh, du=dgates[:3])
+    for a, b, c, d in zip(one["du"], two["du"], into["du"], dgates):
+        assert torch.equal(a, b) and torch.equal(a, c) and c.data_ptr() == d.data_ptr()
+    kw = dict(gate=gates[3])
+    new = pr.block_norm_adjoint(h, x, w, w, rstd, gy, None, **kw)
+    into = pr.block_norm_adjoint(h, x, w, w, rstd, gy, None, dgate=dgates[3], **kw)
+    assert into["dgate"].data_ptr() == dgates[3].data_ptr() and torch.equal(dgates[3], new["dgate"])
+    assert all(torch.equal(a, b) for a, b in zip(one["du"], dgates))  # and nothing of its neighbours

@@ -1,5 +1,6 @@
-"""Who shares a workspace, on the CPU: several launches of one call meet in it,
-so no other call's launches may come between them."""
+"""The binding's memory, on the CPU.  Who shares a workspace: several launches of
+one call meet in it, so no other call's launches may come between them.  And
+what gradients take up."""
 import contextlib
 import threading
 
@@ -54,3 +55,62 @@ def test_a_captured_call_has_a_workspace_of_its_own(monkeypatch):
     assert list(ws.buf) == [(None, 1)] and ws.buf[(None, 1)] is cached
     monkeypatch.setattr(pr, "_capturing", lambda device, stream: False)
     assert ws.get(64, "cpu", Stream(1)) is cached
+
+
+def gate_slices(B, D, T, gates, layout):
+    u = torch.zeros((B, gates * D, T) if layout == "channel" else (B, T, gates * D))
+    u = u if layout == "channel" else u.transpose(1, 2)
+    return [u[:, g * D:(g + 1) * D] for g in range(3)]
+
+
+@pytest.mark.parametrize("layout", ["channel", "time"])
+@pytest.mark.parametrize("B,D,T,gates", [(7, 5, 6, 4), (7, 5, 6, 3), (1, 5, 6, 4), (2, 1, 6, 4), (4, 5, 1, 4), (1, 1, 1, 3)])
+def test_gradients_of_gates_take_up_what_the_gates_do(B, D, T, gates, layout):
+    """Gates that are slices of one projection: their gradients have the slices'
+    strides, no element in common, and together no more room than the projection."""
+    u = gate_slices(B, D, T, gates, layout)
+    du = pr._gradient_planes(3, (B, D, T), u[0].stride(), torch.float32, "cpu")
+    for g, p in enumerate(du):
+        assert p.shape == (B, D, T) and p.stride() == u[0].stride()
+        p.fill_(float(g))
+    assert all(bool((p == g).all()) for g, p in enumerate(du))
+    room = {p.untyped_storage().data_ptr(): p.untyped_storage().nbytes() for p in du}
+    assert sum(room.values()) <= 4 * B * gates * D * T
+
+
+@pytest.mark.parametrize("strides", [(30, 6, 1), (48, 8, 1), (1, 8, 48), (30, 1, 5), (36, 1, 6), (90, 1, 17)])
+def test_gradients_of_other_planes_have_no_element_in_common(strides):
+    dims = (8, 5, 6)
+    du = pr._gradient_planes(3, dims, strides, torch.float32, "cpu")
+    for g, p in enumerate(du):
+        assert p.shape == dims and p.stride() == strides
+        p.fill_(float(g))
+    assert all(bool((p == g).all()) for g, p in enumerate(du))
+
+
+def adjoint(**kw):
+    u = gate_slices(2, 3, 5, 4, "channel")
+    pr.gated_scan_adjoint(u, torch.zeros(3), None, torch.zeros(2, 3, 5), None, **kw)
+
+
+def block_adjoint(gate=torch.zeros(2, 3, 5), **kw):
+    pr.block_norm_adjoint(torch.zeros(2, 3, 5), torch.zeros(2, 5, 3), torch.ones(3), torch.ones(3),
+                          torch.ones(2, 2, 5), None, None, gate=gate, **kw)
+
+
+@pytest.mark.parametrize("call,message", [
+    (lambda: adjoint(du=gate_slices(2, 3, 5, 4, "channel")[:2]), "du"),
+    (lambda: adjoint(du=gate_slices(2, 3, 5, 3, "channel")), "du"),
+    (lambda: adjoint(du=[p.double() for p in gate_slices(2, 3, 5, 4, "channel")]), "du"),
+    (lambda: adjoint(du=[1, 2, 3]), "du"),
+    (lambda: adjoint(du=gate_slices(2, 3, 5, 4, "channel")), "GPU"),
+    (lambda: block_adjoint(dgate=torch.zeros(2, 3, 6)), "dgate"),
+    (lambda: block_adjoint(dgate=torch.zeros(2, 3, 5).bfloat16()), "dgate"),
+    (lambda: block_adjoint(dgate=torch.zeros(2, 5, 3).transpose(1, 2)), "dgate"),
+    (lambda: block_adjoint(gate=None, dgate=torch.zeros(2, 3, 5)), "dgate"),
+    (lambda: block_adjoint(dgate=torch.zeros(2, 3, 5)), "GPU"),
+])
+def test_gradients_to_write_to_are_checked(call, message):
+    for _ in range(2):
+        with pytest.raises(ValueError, match=message):
+            call()

@@ -35,15 +35,21 @@ struct BlockPlan {
     Tiling t = {0, 0, 0, false};
     int64_t tiles_per_row = 0, tiles = 0, groups = 0;  // groups: workgroups that stay (backward)
 };
-BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint)
+// The tensors that are there; the others' strides say nothing.  (Forward, z
+// always is.)
+struct BlockParts {
+    bool h, gate, z;
+};
+BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint, BlockParts in)
 {
     BlockPlan pl;
-    const bool quads = sh->h_stride_t == 1 && sh->g_stride_t == 1 && sh->T >= 4;
+    const bool quads =
+        (!in.h || sh->h_stride_t == 1) && (!in.gate || sh->g_stride_t == 1) && sh->T >= 4;
     // a lane's offset from the tile's base is 32 bits of bytes
     const int64_t reach = (int64_t(1) << 29) - 8;
-    const bool near = sh->D >= 2 && sh->h_stride_d <= reach / sh->D &&
-                      sh->g_stride_d <= reach / sh->D && sh->x_stride_t <= reach / 16 &&
-                      sh->z_stride_t <= reach / 16;
+    const bool near = sh->D >= 2 && (!in.h || sh->h_stride_d <= reach / sh->D) &&
+                      (!in.gate || sh->g_stride_d <= reach / sh->D) &&
+                      sh->x_stride_t <= reach / 16 && (!in.z || sh->z_stride_t <= reach / 16);
     const Tiling *list = adjoint ? kAdjointTilings : kTilings;
     const size_t count = adjoint ? std::size(kAdjointTilings) : std::size(kTilings);
     for (size_t i = 0; i < count; ++i) {
@@ -180,7 +186,7 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
     if (!std::isfinite(scale) || !(eps > 0.0f) || std::isinf(eps)) return PARARNN_ERR_INVALID;
     if (shape->B == 0 || shape->T == 0 || shape->D == 0) return PARARNN_OK;
     if (!x || !w_pre || !z || (h && (!w_post || !y)) || (!h && gate)) return PARARNN_ERR_INVALID;
-    const BlockPlan pl = block_plan(shape, false);
+    const BlockPlan pl = block_plan(shape, false, {h != nullptr, gate != nullptr, true});
     if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);
@@ -204,7 +210,11 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
 size_t pararnn_block_workspace_bytes(const pararnn_block_shape_t *shape)
 {
     if (check_block(shape) != PARARNN_OK) return 0;
-    return align_up((size_t)block_plan(shape, true).groups * 2 * shape->D * sizeof(float));
+    int64_t groups = 0;  // enough for any of the tensors left out
+    for (const bool z : {false, true})
+        for (const BlockParts in : {BlockParts{false, false, z}, {true, false, z}, {true, true, z}})
+            groups = std::max(groups, block_plan(shape, true, in).groups);
+    return align_up((size_t)groups * 2 * shape->D * sizeof(float));
 }
 
 pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, const float *h,
@@ -228,7 +238,7 @@ pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, 
         return PARARNN_ERR_INVALID;
     const size_t need = pararnn_block_workspace_bytes(shape);
     if (work && (!ws || ws_bytes < need || !aligned16(ws))) return PARARNN_ERR_WORKSPACE;
-    const BlockPlan pl = block_plan(shape, true);
+    const BlockPlan pl = block_plan(shape, true, {h != nullptr, gate != nullptr, gz != nullptr});
     if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);

@@ -61,9 +61,18 @@ BlockPlan block_plan(const pararnn_block_shape_t *sh, bool adjoint, BlockParts i
             (t.groups == pl.t.groups && t.channels() < pl.t.channels()))
             pl.t = t;
     }
-    const int64_t steps = pl.t.waves ? 4 * pl.t.groups : kStripSteps;
-    pl.tiles_per_row = (sh->T + steps - 1) / steps;
-    pl.tiles = sh->B * pl.tiles_per_row;
+    const auto cut = [&](int64_t steps) {
+        pl.tiles_per_row = (sh->T + steps - 1) / steps;
+        pl.tiles = sh->B * pl.tiles_per_row;
+    };
+    // the register kernels number their tiles, and forward a dispatch its
+    // work-items, in 32 bits; the strip kernels' workgroups go on to the next tile
+    constexpr int64_t k32 = int64_t(1) << 32;
+    cut(pl.t.waves ? 4 * pl.t.groups : kStripSteps);
+    if (pl.t.waves && (adjoint ? pl.tiles : (pl.tiles + 7) / 8 * 8 * pl.t.waves * kWave) >= k32) {
+        pl.t = {0, 0, 0, false};
+        cut(kStripSteps);
+    }
     // resident workgroups, 8 waves a CU; a multiple of the 8 XCDs
     const int64_t fit = pl.t.waves ? 8 / std::min(8, pl.t.waves) * kComputeUnits : kStripGroups;
     // and as few as take the same number of tiles each
@@ -113,12 +122,6 @@ void block_args(BlockArgs &A, const pararnn_block_shape_t *sh, const BlockPlan &
     A.tiles_per_row = pl.tiles_per_row;
     A.tiles = pl.tiles;
     A.groups = (int32_t)pl.groups;
-}
-
-// A dispatch counts its work-items in 32 bits.
-bool launchable(const BlockPlan &pl)
-{
-    return (pl.tiles + 7) / 8 * 8 * (pl.t.waves ? pl.t.waves : 1) * kWave < (int64_t(1) << 32);
 }
 
 // For the register kernels: a tensor that is not given is read from one that
@@ -187,7 +190,6 @@ pararnn_status_t pararnn_block_norm(const pararnn_block_shape_t *shape, const fl
     if (shape->B == 0 || shape->T == 0 || shape->D == 0) return PARARNN_OK;
     if (!x || !w_pre || !z || (h && (!w_post || !y)) || (!h && gate)) return PARARNN_ERR_INVALID;
     const BlockPlan pl = block_plan(shape, false, {h != nullptr, gate != nullptr, true});
-    if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);
     A.h = h;
@@ -239,7 +241,6 @@ pararnn_status_t pararnn_block_norm_adjoint(const pararnn_block_shape_t *shape, 
     const size_t need = pararnn_block_workspace_bytes(shape);
     if (work && (!ws || ws_bytes < need || !aligned16(ws))) return PARARNN_ERR_WORKSPACE;
     const BlockPlan pl = block_plan(shape, true, {h != nullptr, gate != nullptr, gz != nullptr});
-    if (!launchable(pl)) return PARARNN_ERR_UNSUPPORTED;
     BlockArgs A;
     block_args(A, shape, pl);
     A.h = h;

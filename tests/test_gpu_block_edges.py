@@ -1,6 +1,6 @@
 """The block boundary at the edges of what its kernels reach: long rows without
-states, offsets near 32 bits, time-major planes that give every compute unit
-work.
+states, offsets near 32 bits, more tiles than a dispatch can count, time-major
+planes that give every compute unit work.
 
 Tolerances as in test_gpu_block.py: 2^-24 (D / 64 + 64) of the largest value."""
 import numpy as np
@@ -40,6 +40,27 @@ def test_the_first_norm_of_a_long_row_is_the_short_ones():
         dp = pr.block_norm_adjoint(None, part, None, w, rp, None, gz[:, t:t + 2 ** 14])["dx"]
         assert torch.equal(dx[:, t:t + 2 ** 14], dp)
     near(pr.block_norm(None, x[:, -64:], None, w, z_dtype=F)[1], normed(x[:, -64:], w), D)
+
+
+@pytest.mark.parametrize("D", [1, 2])
+def test_more_tiles_than_a_dispatch_counts(D):
+    """2^28 steps and a few of one or two channels."""
+    T = 2 ** 28 + 5
+    x = torch.empty((1, T, D), device=DEV).normal_()
+    w = torch.rand(D, device=DEV) + 0.5
+    _, z, rstd = pr.block_norm(None, x, None, w, z_dtype=F, eps=1e-2)
+    ends = [slice(0, 4099), slice(T - 4099, T)]
+    for s in ends:
+        near(z[:, s], normed(x[:, s], w, 1e-2), D)
+    got = pr.block_norm_adjoint(None, x, None, w, rstd, None, z)
+    for s in ends:
+        n2, q = x[:, s].double() * rstd[1, :, s, None], z[:, s].double() * w.double()
+        want = rstd[1, :, s, None].double() * (q - n2 * (q * n2).mean(-1, keepdim=True))
+        near(got["dx"][:, s], want, D)
+    dw = sum(float((z[:, i:i + 2 ** 24].double() * x[:, i:i + 2 ** 24].double()
+                    * rstd[1, :, i:i + 2 ** 24, None]).sum()) for i in range(0, T, 2 ** 24))
+    # chains of at most T / (512 2 D) steps of positive terms, rounded at random; all of them at worst
+    assert abs(float(got["dw_pre"].double().sum()) - dw) <= EPS * 2 ** 19 * abs(dw)
 
 
 @pytest.mark.parametrize("dt", [F, H])

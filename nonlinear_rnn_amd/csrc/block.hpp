@@ -96,7 +96,7 @@ __device__ __forceinline__ float gated_value(float h, float g, bool has_gate)
 
 // Any width: the channels are taken in strips of the workgroup's lanes, and
 // read once for each of the two norms and once more for the result.  What the
-// kernels below cannot hold comes here: one channel, more than 4096, planes
+// kernels below cannot hold comes here: one channel, more than 8192, planes
 // that reach past 32 bits.  Bound by the re-reads and 4-byte loads: B=8 T=4096
 // D=1024 takes 1099 us here, 129 below.
 template <int TT>
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kBlockThreads) block_strip_adjoint_kernel(Bloc
 }
 
 // ------------------------------------------------------- tile in registers ---
-// Up to 4096 channels: a workgroup keeps its tile of 4 TG steps in registers
+// Up to 8192 channels: a workgroup keeps its tile of 4 TG steps in registers
 // from the first load to the last store, so that every tensor is read once.
 // A lane owns pairs of channels (NP pairs, the workgroup's pairs apart) and 4
 // steps; TG neighbouring lanes own the same pairs and 4 steps each.  Channel-
@@ -634,6 +634,12 @@ __global__ void __launch_bounds__(WAVES * kWave) block_tile_kernel(BlockArgs A)
 // 101 us of 54, 576 tiles on 256 CUs.  Tiles of 4 steps that keep x too took
 // 1141 us of the first, reading the gradients again as well 1880, a kernel for
 // the sums and one to apply them 1404.
+//
+// 4097 to 8192 channels: 16 waves, and 128 registers a lane for them; 18 to 86
+// are spilled.  B=4 T=2048 D=8192 bf16 gate, float32 stream 706 us (strip
+// kernel 6243), forward, which spills none, 311 (2979).  With a float32 normed
+// stream, types read from the arguments, the tilings of 8 pairs spill 7 to 19 of
+// 256; with float32 gate and stream those of 2048 and 4096 channels 3 and 4.
 struct StreamPair {
     Words2 x[4], gy[4], gz[4];
     float wp[2], wn[2];

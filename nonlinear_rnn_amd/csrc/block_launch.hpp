@@ -17,12 +17,14 @@ namespace pararnn {
     X(2, 2, 1, true) X(8, 2, 1, true) X(16, 2, 1, true) X(16, 2, 2, true) X(16, 2, 4, true)      \
     X(4, 4, 1, true) X(8, 4, 1, true) X(16, 4, 1, true) X(16, 4, 2, true) X(16, 4, 4, true)      \
     X(6, 4, 1, true) X(12, 4, 1, true) X(12, 4, 2, true) X(12, 4, 4, true) X(12, 2, 4, true)     \
+    X(16, 1, 4, true) X(16, 1, 4, false)                                                         \
     X(1, 1, 1, false) X(4, 1, 1, false) X(8, 1, 1, false) X(16, 1, 1, false) X(16, 1, 2, false)
 #define PARARNN_BLOCK_ADJOINT_TILINGS(X)                                                         \
     X(1, 1, 1, true) X(2, 1, 2, true) X(4, 1, 2, true) X(8, 1, 2, true) X(8, 1, 4, true)         \
     X(2, 2, 2, true) X(4, 2, 2, true) X(4, 2, 4, true) X(8, 2, 4, true) X(8, 2, 8, true)         \
     X(4, 4, 2, true) X(4, 4, 4, true) X(4, 4, 8, true) X(8, 4, 8, true)                          \
     X(3, 4, 2, true) X(3, 4, 4, true) X(3, 4, 8, true) X(6, 4, 8, true) X(6, 2, 8, true)         \
+    X(16, 1, 4, true) X(16, 1, 4, false)                                                         \
     X(1, 1, 1, false) X(2, 1, 2, false) X(4, 1, 2, false) X(8, 1, 2, false) X(8, 1, 4, false)
 inline int tiling_code(int waves, int groups, int pairs, bool quads)
 {

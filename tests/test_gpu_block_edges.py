@@ -111,3 +111,28 @@ def test_wide_rows_near_32_bits():
 @pytest.mark.parametrize("dt", [F, H])
 def test_time_major_planes_with_work_for_every_unit(B, T, D, dt):
     check(inputs(B, T, D, dt, F if D % 4 else dt, layout="time"), F if D % 5 else H)
+
+
+@pytest.mark.parametrize("B,T,D,layout", [(1, 1, 8192, "channel"), (2, 9, 6001, "channel"), (1, 700, 8191, "channel"),
+                                          (2, 30, 5120, "time"), (1, 5, 8192, "padded"), (1, 33, 8193, "channel")])
+@pytest.mark.parametrize("gdt,xdt,zdt", [(F, F, F), (H, F, H), (H, H, H)])
+def test_more_than_4096_channels(B, T, D, layout, gdt, xdt, zdt):
+    check(inputs(B, T, D, gdt, xdt, layout=layout), zdt)
+
+
+def test_more_than_4096_channels_with_parts_left_out():
+    for use in (("gy", "gz"), ("h", "gy"), ("h", "gate", "gz")):
+        check(inputs(1, 21, 7000), use=use)
+
+
+def test_more_than_4096_channels_repeat():
+    """Tiles of 8192 channels have one workgroup's order of sums: the same bits each
+    time, and for a row among others as by itself."""
+    c = inputs(2, 40, 8000, H, F)
+    run = [pr.block_norm(c["h"], c["x"], c["wp"], c["wn"], gate=c["gate"]) for _ in range(2)]
+    alone = pr.block_norm(c["h"][1:], c["x"][1:], c["wp"], c["wn"], gate=c["gate"][1:])
+    for a, b in zip(*run):
+        assert torch.equal(a, b)
+    y, z, rstd = run[0]
+    for a, b in zip((y[1:], z[1:], rstd[:, 1:]), alone):
+        assert torch.equal(a, b)

@@ -157,16 +157,21 @@ __device__ __forceinline__ Span forward_step(float rate, float r, float i, float
     return {DOCS && reset ? kCut : v.a, __builtin_amdgcn_sqrtf(v.y) * sigmoid_q(-kLog2e * i) * x,
             v.l2};
 }
-// Backwards, of w: w -> a (gh + w).  A step past the end (not `in`, gh = 0) comes
-// before all others and leaves w, which is 0 in a span so far, as it is.
-// (Forward, steps past the end come last, and no one asks for what is behind
-// them.)
+// Backwards, of w: w -> a (gh + w), from a span's last step to its first.  A step
+// past the end (not `in`, gh = 0) comes before all others and leaves w, which is
+// 0 in a span so far, as it is.  (Forward, steps past the end come last, and no
+// one asks for what is behind them.)
 template <bool DOCS>
-__device__ __forceinline__ Span backward_step(const Decay &v, float gh, bool reset, bool in)
-{
-    const bool cut = DOCS && reset && in;
-    return {cut ? kCut : v.a, cut ? 0.0f : v.a * gh, in ? v.l2 : 0.0f};
-}
+struct RunningBack {
+    float l = 0.0f, b = 0.0f;
+    __device__ __forceinline__ void add(const Decay &v, float gh, bool reset, bool in)
+    {
+        const bool cut = DOCS && reset && in;
+        b = cut ? 0.0f : v.a * (gh + b);
+        l = cut ? kNoMemory : l + (in ? v.l2 : 0.0f);
+    }
+    __device__ __forceinline__ Span span() const { return span_of<DOCS>(l, b); }
+};
 
 // Gradients of one step from G = dL/dh_t (total) and h_{t-1}.  With
 // a' = k a: dL/dl = G (a' h_{t-1} - a^2 / sqrt(1 - a^2) sig(u_i) u_x).  Where
@@ -374,12 +379,10 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
             w = first;
             break;
         }
-        const Span own = sum_of<DOCS, false>([&](auto &sum) {
+        RunningBack<DOCS> own;
 #pragma unroll
-            for (int k = kGatedSteps - 1; k >= 0; --k)
-                sum.add(backward_step<DOCS>(v[k], e.gh[k], c.cut[k], t + k < A.T));
-        });
-        w = through<DOCS>(own, w);
+        for (int k = kGatedSteps - 1; k >= 0; --k) own.add(v[k], e.gh[k], c.cut[k], t + k < A.T);
+        w = through<DOCS>(own.span(), w);
     }
     A.dlam_part[ch] = dlam;
     if (A.dh0) A.dh0[ch] = w;
@@ -515,14 +518,13 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
     const auto c = lane_steps<BF16, DOCS, kGatedSteps>(A, uo, b, t);
     const auto e = lane_back<kGatedSteps>(A, so, t, A.h0 ? A.h0[s.ch] : 0.0f);
     Decay v[kGatedSteps];
+    RunningBack<DOCS> own;
 #pragma unroll
-    for (int k = 0; k < kGatedSteps; ++k) v[k] = decay(rate, c.u[0][k]);
-    const Span own = sum_of<DOCS, false>([&](auto &sum) {
-#pragma unroll
-        for (int k = kGatedSteps - 1; k >= 0; --k)
-            sum.add(backward_step<DOCS>(v[k], e.gh[k], c.cut[k], t + k < A.T));
-    });
-    float w = span_carry<DOCS>(A, s, own, A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
+    for (int k = kGatedSteps - 1; k >= 0; --k) {
+        v[k] = decay(rate, c.u[0][k]);
+        own.add(v[k], e.gh[k], c.cut[k], t + k < A.T);
+    }
+    float w = span_carry<DOCS>(A, s, own.span(), A.gh_last ? A.gh_last[s.ch] : 0.0f, maps, carry), dlam = 0.0f;
     if (s.here) w = lane_gradients<BF16, kGatedSteps>(A, uo, t, c, e, v, w, dlam);
     sums[s.wave][s.lane] = dlam;
     __syncthreads();
@@ -722,17 +724,17 @@ __device__ __forceinline__ GatedBackChunk<K, BF16> load_back(const GatedArgs &A,
     c.cut = DOCS ? load_flags<K>(A.resets + b * A.T, t, end) : 0u;
     return c;
 }
-template <int K, bool BF16, bool DOCS, bool TWICE>
+template <int K, bool BF16, bool DOCS>
 __device__ __forceinline__ Span back_maps(const GatedBackChunk<K, BF16> &c, float rate, int64_t t,
                                           int64_t end, Decay (&v)[K])
 {
+    RunningBack<DOCS> own;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = decay(rate, c.u[0].get(k));
-    return sum_of<DOCS, TWICE>([&](auto &sum) {
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k)
-            sum.add(backward_step<DOCS>(v[k], c.gh.get(k), c.cut >> k & 1u, t + k < end));
-    });
+    for (int k = K - 1; k >= 0; --k) {
+        v[k] = decay(rate, c.u[0].get(k));
+        own.add(v[k], c.gh.get(k), c.cut >> k & 1u, t + k < end);
+    }
+    return own.span();
 }
 // A lane's gradients from the w behind them and the state before its first
 // step; returns its own w, and adds to dlam.
@@ -796,7 +798,7 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
         GatedBackChunk<K, BF16> next;
         if (c > 0) next = load_back<K, BF16, DOCS>(A, uo, so, b, t - P, c - P + wave_at * K, A.T, h0);
         Decay v[K];
-        const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS, false>(now, rate, t, A.T, v));
+        const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS>(now, rate, t, A.T, v));
         float after = carry;
         if constexpr (W > 1) {
             if (threadIdx.x % kWave == kWave - 1) maps[parity][wave] = spans.all;
@@ -918,7 +920,7 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
     const GatedBackChunk<K, BF16> c =
         load_back<K, BF16, DOCS>(A, uo, so, b, t, c0 + (W - 1 - wave) * (kWave * K), A.T, h0);
     Decay v[K];
-    const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS, true>(c, rate, t, A.T, v));
+    const WaveSpans<DOCS> spans(back_maps<K, BF16, DOCS>(c, rate, t, A.T, v));
     if (threadIdx.x % kWave == kWave - 1) maps[wave] = spans.all;
     __syncthreads();
     float carry = chunk_carry<DOCS, W>(A, maps, ch, place, A.gh_last ? A.gh_last[ch] : 0.0f, &carry_lds);
@@ -1003,7 +1005,7 @@ __global__ void __launch_bounds__(kShortThreads) gated_short_adjoint_kernel(Gate
     const GatedBackChunk<K, BF16> c = load_back<K, BF16, DOCS>(A, uo, so, b, t, 0, end, h0);
     const float after = A.gh_last && here ? A.gh_last[ch] : 0.0f;
     Decay v[K];
-    const float behind = before_lane<DOCS, G, true>(back_maps<K, BF16, DOCS, false>(c, rate, t, end, v), after);
+    const float behind = before_lane<DOCS, G, true>(back_maps<K, BF16, DOCS>(c, rate, t, end, v), after);
     float hp = __shfl_up(c.h.get(K - 1), 1), dlam = 0.0f;
     if (threadIdx.x % G == 0) hp = h0;
     const float w = chunk_gradients<K, BF16>(A, uo, t, end, c, v, behind, hp,

@@ -113,10 +113,15 @@ __device__ __forceinline__ uint32_t load_flags(const uint8_t *p, int64_t first, 
     static_assert(K == 4 || K == 8, "one access");
     uint32_t m = 0;
     if (first + K <= end) {
-        uint32_t w[2];
+        uint32_t w[K / 4];
         __builtin_memcpy(w, p + first, K);
 #pragma unroll
-        for (int k = 0; k < K; ++k) m |= ((w[k / 4] >> (8 * (k % 4))) & 0xffu) ? 1u << k : 0u;
+        for (int j = 0; j < K / 4; ++j) {
+            // each byte to its 1 or 0, then bytes 0..3 to bits 28..31 (no two
+            // products of the multiplication share a bit)
+            const uint32_t one = (((w[j] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w[j]) >> 7 & 0x01010101u;
+            m |= (one * 0x10204080u >> 28) << (4 * j);
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)

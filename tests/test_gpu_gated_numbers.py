@@ -149,3 +149,18 @@ def test_the_oracle_cuts_as_well():
     resets = np.array([[False, False, True, False]])
     h = ref.gated_scan(u, np.zeros(1), np.full((1, 1), np.nan), 8.0, resets)
     assert np.isnan(h[0, 0, :2]).all() and np.isfinite(h[0, 0, 2:]).all()
+
+
+@pytest.mark.parametrize("B,T,D,layout", WAYS)
+def test_any_byte_but_zero_is_a_reset(B, T, D, layout):
+    r = np.random.default_rng(T)
+    u = [p.copy_(torch.from_numpy(r.standard_normal((B, D, T)))) for p in planes(B, T, D, layout, [0.0] * 3)]
+    lam, h0 = torch.randn(D, device=DEV), torch.randn((B, D), device=DEV)
+    values = torch.from_numpy(r.choice(np.array([0, 0, 1, 2, 64, 128, 255], np.uint8), (B, T))).to(DEV)
+    h, _ = pr.gated_scan(u, lam, h0, resets=values)
+    want, _ = pr.gated_scan(u, lam, h0, resets=values != 0)
+    assert torch.equal(h, want)
+    # and they cut where they stand: a step alone from nothing
+    alone, _ = pr.gated_scan(u, lam, None, resets=torch.ones_like(values))
+    where = (values != 0)[:, None].expand_as(h)
+    assert torch.equal(h[where], alone[where])

@@ -335,6 +335,9 @@ def decode_info(raw) -> dict:
                 iters_sum=isum, units=units, iters_mean=(isum / units) if units else 0.0)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _capturing(device, stream):
     """Whether what is enqueued on `stream` (None: the device's current one) goes
     into a graph."""
@@ -375,8 +378,11 @@ class Workspace(threading.local):
             with torch.cuda.stream(s):
                 return torch.empty(nbytes, dtype=torch.uint8, device=device)
         if key is None:
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            key = (torch.device(device).index, s.cuda_stream)
+            index = torch.device(device).index
+            if stream is not None:
+                key = (index, stream.cuda_stream)
+            else:
+                key = (index, _raw_stream(torch.cuda.current_device() if index is None else index))
         b = self.buf.pop(key, None)
         if b is None or b.numel() < nbytes:
             s = stream if stream is not None else torch.cuda.current_stream(device)
@@ -395,8 +401,7 @@ _ws_sizes = {}  # (shape record, options record, workspace bytes) by solve argum
 
 
 def _stream_handle(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _u_dtype(planes):
@@ -719,7 +724,6 @@ def scan(A, b, x0=None, *, reverse=False, out=None, steps_per_lane=0, waves_per_
 TOP_MAX = 64  # PARARNN_TOP_MAX
 
 _plans = {}  # prepared records by signature
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _signature(*tensors):

@@ -444,7 +444,10 @@ pararnn_status_t pararnn_token_logprobs(int64_t N, int64_t V, const void *logits
  *                        - g_entropy p_j (log p_j + entropy)),
  * from the forward's lse and entropy; g_* are [N] float32 or NULL (zero).  A
  * token that is not scored takes no g_logprob; a masked logit's p_j is 0; the
- * gradient of a row whose tokens are all masked is zero.  dlogits has the
+ * gradient of a row whose tokens are all masked is zero.  p comes from lse, a
+ * float32: it is within half an ulp of |lse| of itself, which for logits beyond
+ * 1e5 is a percent and for a row of the type's lowest value all of it (give
+ * such a row no gradient).  dlogits has the
  * dtype of the logits, rows d_stride elements apart, and may be the logits'
  * own memory (same stride).
  */

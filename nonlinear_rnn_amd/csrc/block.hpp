@@ -14,9 +14,10 @@
 //
 // The states and the gate are channel-major (a channel's steps contiguous),
 // the stream is time-major (a step's channels contiguous).  A workgroup takes
-// TT consecutive steps of one row: a lane owns a channel and holds its TT
-// steps, so channel-major loads use a lane's contiguous steps and time-major
-// ones the wave's contiguous channels, and no transpose goes through LDS.
+// consecutive steps of one row.  A lane holds some steps of its channels (one
+// channel in the strip kernels, pairs of neighbours in the register kernels),
+// so channel-major loads use a lane's contiguous steps and time-major ones the
+// wave's contiguous channels, and no transpose goes through LDS.
 #pragma once
 
 #include "elements.hpp"
@@ -395,9 +396,8 @@ __device__ __forceinline__ void store_quad(void *row, uint32_t off, const int64_
 // Two neighbouring channels of a step.  The stream goes past the L2's other
 // contents (non-temporal), unless it is read again (`kept`): the lines of the
 // channel-major planes have to stay there until all tiles that share one have
-// read or written their part.  B=8 T=4096 D=1024: forward 136 -> 123 us,
-// backward 279 -> 269; with the planes themselves non-temporal the backward
-// takes twice as long.
+// read or written their part.  B=8 T=4096 D=1024 backward 279 -> 262 us; with
+// the planes themselves non-temporal it takes twice as long.
 __device__ __forceinline__ Words2 load_pair(const void *row, uint32_t off, bool bf16,
                                             bool kept = false)
 {

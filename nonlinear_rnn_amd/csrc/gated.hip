@@ -17,9 +17,10 @@ namespace {
 // plane.
 constexpr int kStepsBf16 = 8, kStepsF32 = 4;
 // Look back: what a chunk costs beside its bytes wants it long.  Float32,
-// 1x262144x64: 8 waves of 4 steps a lane 74.7 us, 4 of 8 64.4, 8 of 8 58.5.
-// 16 waves of 8 take 65 us from HBM where 8 take 72, but more elsewhere
-// (bfloat16: backward 106 and 95, 2x16577x91 22 and 18).
+// 1x262144x64 with part of its inputs still cached: 8 waves of 4 steps a lane
+// 74.7 us, 4 of 8 64.4, 8 of 8 58.5 (from HBM 72).  16 waves of 8 take 65 us from
+// HBM, but more than 8 elsewhere (bfloat16: backward 106 and 95, 2x16577x91 22
+// and 18).
 constexpr int kLookWaves = 8, kLookSteps = 8, kLookChunk = kLookWaves * kWave * kLookSteps;
 
 // A dispatch's work-items in 32 bits, 512 a chunk.
@@ -50,15 +51,15 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     if (T > 6 && sh->u_stride_t == 1 && sh->s_stride_t == 1 && C < (int64_t(1) << 26)) {
         // Lanes in time; up to 6 steps a lane has all of its channel's (512
         // requests of 1024 channels: 6 steps bfloat16 47 us with lanes in time,
-        // 14 with a lane per channel, 8 steps float32 29 and 32).
+        // 13 with a lane per channel, 8 steps float32 25 and 31).
         // One wave a channel for sequences up to 512 steps, and up to 4095
         // where the channels fill the device (16 x 1024 channels of 600 steps
-        // float32 36 us, with 4 waves 42; 8 x 1024 of 4096 steps, backward, 221
-        // and 207), or longer if 4 waves' last chunk is mostly empty (4500 steps
-        // bfloat16, backward, 183 and 240).  4 waves, and where they do not fill
+        // float32 35 us, with 4 waves 41; 8 x 1024 of 4096 steps, backward, 146
+        // and 128), or longer if 4 waves' last chunk is mostly empty (4500 steps
+        // bfloat16, backward, 178 and 219).  4 waves, and where they do not fill
         // the device, the channel's chunks side by side (2x65536x128 float32
-        // 75 us with 4 waves, 54 looking back; 4x8192x256 bfloat16, 1024
-        // channels, 22 and 27).
+        // 95 us with 4 waves, 58 looking back; 4x8192x256 bfloat16, 1024
+        // channels, 19 and 24).
         const int64_t chunks = (T + kLookChunk - 1) / kLookChunk;
         constexpr int64_t four = 4 * kWave * kStepsBf16;
         const bool full = T >= 4096 && (T + four - 1) / four * four - T <= T / 8;
@@ -70,12 +71,12 @@ pararnn_status_t gated_plan(const pararnn_shape_t *sh, bool adjoint, GatedPlan &
     } else {
         // A lane per channel, one for the whole length of a short sequence
         // (64 x 1024 time-major channels float32, 16 steps, backward: 22 us, in
-        // chunks 27; 32 steps 12.0 and 13.1) or where the channels fill the
-        // device (20x1000x4096 time-major float32: forward 297 us, in chunks
-        // 321, 10x2000x4096 454 and 316; backward, of more bytes a step,
-        // 20x1000x4096 782 and 649).
+        // chunks 24; 32 steps 10.4 and 11.0) or where the channels fill the
+        // device (time-major float32: 20x1000x4096 forward 293 us, in chunks 306,
+        // backward 563 and 655, 16x1200x4096 backward 533 and 616; 10x2000x4096
+        // 458 and 296, backward 722 and 646).
         const int64_t groups = (C + kWave - 1) / kWave, chunks = (T + kSpanChunk - 1) / kSpanChunk;
-        if (T > 32 && groups < (adjoint ? kFull : kFull / 2) && groups * chunks < kMostChunks) {
+        if (T > 32 && groups < kFull / 2 && groups * chunks < kMostChunks) {
             pl.kernel = kLaneLookBack;
             pl.chunks = chunks;
             if (chunks > 1) record = 3 * sizeof(uint64_t), lines = groups;

@@ -81,7 +81,7 @@ __device__ __forceinline__ Decay decay(float rate, float r)
 // product of decays loses at every step what its factors have lost; their
 // logarithms add up in full.  So a span's a is 2^l, l the sum of its steps'.
 // (A steady gate at -8 over 262144 steps: what is left of h_0 was off by 0.8%
-// with products, by 1e-5 with sums.)
+// with products, with sums by 1e-5, in chunks of 64 steps by 1.5e-4.)
 //
 // A reset cuts: what is before it is not multiplied by 0, which would keep a
 // NaN or an infinity, but left out.  A cut span has a = -0 (decays are not
@@ -90,10 +90,8 @@ __device__ __forceinline__ Decay decay(float rate, float r)
 // the lanes' scan, it is done that way first, and once more, CAREFUL, where a
 // lane of the wave ends with a number that is not finite, as any does that met
 // one.  (Careful at once, 16x600x1024 float32 takes 42 us instead of 38.  With a
-// lane a channel, and backward where registers are scarce, the first pass does
-// not pay: 512x1x4096 bfloat16 28 us with it, 18 without; 8x4096x1024 bfloat16
-// backward 165 and 142; but looking back, 1x262144x64 backward, 93 and 99.)  Kernels without
-// resets (DOCS false) look for neither.
+// lane a channel a first pass does not pay: 512x1x4096 bfloat16 28 us with it, 18
+// without.)  Kernels without resets (DOCS false) do not look for cuts.
 struct Span {
     float a, b, l;
 };
@@ -324,8 +322,11 @@ __device__ __forceinline__ float lane_gradients(const GatedArgs &A, int64_t uo, 
 }
 
 // Single tokens and short runs, or channels that fill the device: one lane runs
-// its channel from end to end.  512x1x4096 time-major bfloat16 20 us; bound by
-// the launch, and by the bytes where there are many channels.
+// its channel from end to end.  512x1x4096 time-major bfloat16 17 us; bound by
+// the launch, and by the bytes where there are many channels (20x1000x4096
+// float32 293 us, 4.5 TB/s).  The state goes on by 8 steps at a time: what a
+// steady gate near no decay leaves of it after T steps is within 2^-22 T / 8 of
+// itself.
 template <bool BF16, bool DOCS>
 __global__ void __launch_bounds__(kWave) gated_channel_kernel(GatedArgs A)
 {
@@ -390,12 +391,13 @@ __global__ void __launch_bounds__(kWave) gated_channel_adjoint_kernel(GatedArgs 
 
 // Else: a chunk of 64 steps of 64 channels a workgroup, 8 steps of each a wave.
 // Every step is in registers once; the waves' maps meet in shared memory.
-// 11x153600x64 time-major float32 500 us (3.5 TB/s), 8x4096x1024 bfloat16
-// 137 us (2.5 TB/s).  Bound by the registers that its single-element loads and
-// their addresses take (2 workgroups a CU, backward 1), and with few channels
-// by the steps of looking back: chunks of 128 steps take 447 us of the first,
-// but 313 us instead of 264 of the second's backward pass; capped at 3 and 2
-// workgroups' registers it spills and takes 611 and 261.
+// 11x153600x64 time-major float32 468 us (3.7 TB/s), with documents 519;
+// 8x4096x1024 bfloat16 115 us (2.9 TB/s), backward 254.  Bound by the registers
+// that its single-element loads and their addresses take (2 workgroups a CU,
+// backward 1), and with few channels by the steps of looking back: when these
+// took 500 and 264 us, chunks of 128 steps took 447 of the first, but 313 of the
+// backward pass; capped at 3 and 2 workgroups' registers it spilled and took 611
+// and 261.
 constexpr int kSpanWaves = 8, kSpanChunk = kSpanWaves * kGatedSteps;
 
 // A lane: the state behind place - 1 > -1 of channel ch, from the words of the
@@ -543,9 +545,10 @@ __global__ void __launch_bounds__(kSpanWaves * kWave) gated_span_adjoint_kernel(
 // through LDS (one barrier a chunk, two buffers), and every lane runs its
 // steps again from the state in front of them.  The chunk's last state starts
 // the next one; the next chunk's loads are issued before this one's scan.
-// Bound by HBM: every plane goes once, 4x16384x4096 bfloat16 511 us (5.2 TB/s,
-// a large copy's rate), backward 8x4096x1024 bfloat16 135 us (5.0 TB/s); a
-// lane per channel took 19.8 ms and 5.0 ms of these.
+// Bound by HBM: every plane goes once, 4x16384x4096 bfloat16 510 us (5.3 TB/s,
+// a large copy's rate), backward 8x4096x1024 bfloat16 129 us (5.2 TB/s), with
+// documents 138 (the steps take more operations, and registers allow 3 waves a
+// SIMD); a lane per channel took 19.8 ms and 5.0 ms of these.
 template <int K, bool BF16>
 struct GatedChunk {
     Raw<BF16, K> u[3];
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(W * kWave) gated_time_adjoint_kernel(GatedArgs
 // Few channels: a channel's chunks run side by side, each in a workgroup of its
 // own.  A wave looks back over 64 predecessors, a lane each.  1x262144x64
 // float32 72 us from HBM (3.7 TB/s; 60 where part of it is still cached),
-// backward 131.  Bound by the time a chunk waits for its loads and then for its
+// backward 124.  Bound by the time a chunk waits for its loads and then for its
 // predecessor, with 4 chunks a CU.
 struct GatedRecord {
     uint64_t l, b;  // the chunk's map
@@ -937,8 +940,8 @@ __global__ void __launch_bounds__(W * kWave) gated_look_adjoint_kernel(GatedArgs
 // --------------------------------------------------- lanes in time, short ---
 // At most G K steps: G lanes a channel and 64 / G channels a wave, each lane's
 // K steps in one access as above.  (With a wave a channel, T = 100 of 64000
-// channels left 7 of 8 lanes idle: 64x100x1000 bfloat16 100 us, here 30;
-// 64x32x1024 float32 43 and 16.)  Bound by partial lines of odd lengths and by
+// channels left 7 of 8 lanes idle: 64x100x1000 bfloat16 100 us, here 27;
+// 64x32x1024 float32 43 and 14.)  Bound by partial lines of odd lengths and by
 // the launch.
 constexpr int kShortThreads = 256;
 

@@ -309,8 +309,8 @@ __device__ __forceinline__ void write_top(const ScoreArgs &A, int64_t n, const R
 // Bound by HBM: 4096 rows of 50003 bfloat16 with 8 alternatives 89 us (4.6
 // TB/s; without alternatives 76, with 64 of rows of random numbers 123, where
 // the second reading of vectors shows).  Where rows are few, by latency: 16 rows
-// of 65536 float32 with 20 alternatives 16 us in two launches, 12.6 of them the
-// call's own.
+// of 65536 float32 with 20 alternatives 16.8 us a call, two launches of 10.2 and
+// 5.5 us on the device.
 template <bool BF16, int WAVES, bool PARTS, bool TOP>
 __global__ void __launch_bounds__(WAVES * kWave) score_kernel(ScoreArgs A)
 {

@@ -104,6 +104,8 @@ def load():
     lib.pararnn_adjoint.restype = i32
     lib.pararnn_adjoint.argtypes = [i32, P(Shape), vp, i32, vp, vp, vp, vp, vp, vp, vp, i32,
                                     vp, vp, P(Newton), vp, sz, vp]
+    lib.hipStreamIsCapturing.restype = i32  # of the runtime the library is linked with
+    lib.hipStreamIsCapturing.argtypes = [vp, P(i32)]
     f32, i64 = ctypes.c_float, ctypes.c_int64
     lib.pararnn_gated_workspace_bytes.restype = sz
     lib.pararnn_gated_workspace_bytes.argtypes = [P(Shape), i32]
@@ -338,16 +340,15 @@ def decode_info(raw) -> dict:
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _capturing(device, stream):
-    """Whether what is enqueued on `stream` (None: the device's current one) goes
-    into a graph."""
-    device = torch.device(device)
-    if device.type != "cuda":
+def _capturing(device, handle):
+    """Whether what is enqueued on the stream goes into a graph.  Asked of the
+    runtime by handle: making the stream the current one to ask torch would take
+    longer than a small solve's launch."""
+    if torch.device(device).type != "cuda":
         return False
-    if stream is None and device.index == torch._C._cuda_getDevice():
-        return torch._C._cuda_isCurrentStreamCapturing()
-    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-        return torch.cuda.is_current_stream_capturing()
+    status = ctypes.c_int(0)
+    load().hipStreamIsCapturing(handle, ctypes.byref(status))
+    return status.value != 0
 
 
 class Workspace(threading.local):
@@ -373,16 +374,16 @@ class Workspace(threading.local):
         """``key``: (device index, stream handle), where the caller knows it."""
         if nbytes == 0:
             return None
-        if _capturing(device, stream):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            with torch.cuda.stream(s):
-                return torch.empty(nbytes, dtype=torch.uint8, device=device)
         if key is None:
             index = torch.device(device).index
             if stream is not None:
                 key = (index, stream.cuda_stream)
             else:
                 key = (index, _raw_stream(torch.cuda.current_device() if index is None else index))
+        if key[1] and _capturing(device, key[1]):  # (the default stream, 0, cannot be captured)
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            with torch.cuda.stream(s):
+                return torch.empty(nbytes, dtype=torch.uint8, device=device)
         b = self.buf.pop(key, None)
         if b is None or b.numel() < nbytes:
             s = stream if stream is not None else torch.cuda.current_stream(device)

@@ -459,6 +459,80 @@ pararnn_status_t pararnn_token_logprobs_adjoint(int64_t N, int64_t V, const void
                                                 const float *g_lse, void *dlogits,
                                                 int64_t d_stride, void *stream);
 
+/*
+ * Gated delta rule: a recurrence whose state is a matrix for each head, which
+ * stores values under keys.  Per row b and value head h (key head h Hk / Hv:
+ * Hv is a multiple of Hk, neighbouring value heads share a key head),
+ *     S <- a S,  w = beta (v - k^T S),  S <- S + k w^T,  o = scale q^T S
+ * with S [dk][dv] and a = exp(log_decay).  The state keeps its size where
+ * |k|^2 beta <= 2 and a <= 1: keys of unit length and beta in [0, 2], say.
+ *   q, k    : [B][Hk][dk][T]-indexed, v [B][Hv][dv][T], dtype F32 or BF16
+ *   beta, log_decay : [B][Hv][T]-indexed float32; log_decay NULL: no decay
+ *   h0      : [B][Hv][dk][dv] float32, dense, or NULL (zero)
+ *   resets  : [B][T] bytes, dense, or NULL: non-zero at the first step of a
+ *             new document.  It keeps nothing of the state before it, also if
+ *             that is not finite, and no gradient goes back past it.  A log
+ *             decay below -104, whose exponential is 0 in float32, does the
+ *             same in its head; the gradient for it is 0.
+ *   o       : [B][Hv][dv][T]-indexed float32 out
+ *   last    : [B][Hv][dk][dv] float32 out, the last state (h0 at T = 0), or NULL
+ *   ws      : pararnn_delta_workspace_bytes(shape, dtype, 0) bytes
+ * Strides are of (b, h, d, t), and of (b, h, t) for the gates.  The fast
+ * layouts have the steps side by side (stride 1 along t) or the channels
+ * (stride 1 along d), the same for all; inputs may repeat elements (stride
+ * 0), outputs not.  dk is at most PARARNN_DELTA_KEY_MAX.
+ */
+#define PARARNN_DELTA_KEY_MAX 256
+typedef struct {
+    int64_t B, T, Hk, Hv, dk, dv;
+    int64_t q_stride[4], k_stride[4], v_stride[4];
+    int64_t o_stride[4];    /* o, and its gradient */
+    int64_t gate_stride[3]; /* beta and log_decay  */
+} pararnn_delta_shape_t;
+
+size_t pararnn_delta_workspace_bytes(const pararnn_delta_shape_t *shape, pararnn_dtype_t dtype,
+                                     int adjoint);
+pararnn_status_t pararnn_delta_scan(const pararnn_delta_shape_t *shape, const void *q,
+                                    const void *k, const void *v, pararnn_dtype_t dtype,
+                                    const float *beta, const float *log_decay, const float *h0,
+                                    const uint8_t *resets, float scale, float *o, float *last,
+                                    void *ws, size_t ws_bytes, void *stream);
+/*
+ * Its backward pass, for L = sum <go, o> + <g_last, last>.
+ *   go      : o's strides, or NULL (zero);  g_last : dense, or NULL (zero)
+ *   dq, dk, dv : dtype, their own strides; heads that share a key head are
+ *             summed in a fixed order
+ *   dbeta, dlog_decay : [B][Hv][T] float32, dense (dlog_decay NULL without one)
+ *   dh0     : [B][Hv][dk][dv] float32, or NULL
+ *   ws      : pararnn_delta_workspace_bytes(shape, dtype, 1) bytes
+ */
+typedef struct {
+    void *dq, *dk, *dv;
+    int64_t dq_stride[4], dk_stride[4], dv_stride[4];
+    float *dbeta, *dlog_decay, *dh0;
+} pararnn_delta_grads_t;
+
+pararnn_status_t pararnn_delta_scan_adjoint(const pararnn_delta_shape_t *shape, const void *q,
+                                            const void *k, const void *v, pararnn_dtype_t dtype,
+                                            const float *beta, const float *log_decay,
+                                            const float *h0, const uint8_t *resets, float scale,
+                                            const float *go, const float *g_last,
+                                            const pararnn_delta_grads_t *grads, void *ws,
+                                            size_t ws_bytes, void *stream);
+/*
+ * One step of it for B requests, their states in a pool, updated in place
+ * (shape->T is 1, its time strides are not read): as for the gated recurrence,
+ * a row whose slot lies outside the pool is idle, its output zero, and the
+ * slots of live rows must be distinct.
+ *   slots  : [B] int32, or NULL (row b has slot b)
+ *   states : [pool][Hv][dk][dv] float32;  o : [B][Hv][dv]-indexed float32 out
+ */
+pararnn_status_t pararnn_delta_step(const pararnn_delta_shape_t *shape, const void *q,
+                                    const void *k, const void *v, pararnn_dtype_t dtype,
+                                    const float *beta, const float *log_decay,
+                                    const int32_t *slots, float *states, int64_t pool, float scale,
+                                    float *o, void *stream);
+
 /* Static description of a status code. */
 const char *pararnn_status_string(pararnn_status_t status);
 

@@ -246,6 +246,38 @@ def gated_scan(u, lam, h0=None, *, power=8.0, resets=None):
     return _GatedScan.apply(ur, ui, ux, lam, h0, power, resets)
 
 
+class _DeltaScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, beta, log_decay, h0, scale, resets):
+        if log_decay is not None and log_decay.stride() != beta.stride():
+            beta, log_decay = beta.contiguous(), log_decay.contiguous()
+        o, last = pr.delta_scan(q, k, v, beta, log_decay, h0, scale=scale, resets=resets)
+        ctx.save_for_backward(q, k, v, beta, log_decay, h0, resets)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, last
+
+    @staticmethod
+    @_once
+    def backward(ctx, go, g_last):
+        q, k, v, beta, log_decay, h0, resets = ctx.saved_tensors
+        if go is not None:  # elements of their own, side by side as v's are
+            strides = pr._like_steps(*v.shape, v)
+            if go.stride() != strides:
+                go = torch.empty_strided(go.shape, strides, dtype=go.dtype, device=go.device).copy_(go)
+        out = pr.delta_scan_adjoint(q, k, v, beta, log_decay, h0, go,
+                                    g_last=None if g_last is None else g_last.contiguous(), scale=ctx.scale,
+                                    resets=resets)
+        return (out["dq"], out["dk"], out["dv"], out["dbeta"], out["dlog_decay"], out["dh0"], None, None)
+
+
+def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=None):
+    """Differentiable gated delta rule (``pararnn.delta_scan``): gradients for q,
+    k, v, beta, log_decay and h0.  Returns (o [B][Hv][dv][T],
+    last [B][Hv][dk][dv])."""
+    return _DeltaScan.apply(q, k, v, beta, log_decay, h0, scale, resets)
+
+
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, gate, x, w_post, w_pre, scale, eps, z_dtype):

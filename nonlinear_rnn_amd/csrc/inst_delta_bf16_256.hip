@@ -1,0 +1,9 @@
+// Delta rule: kernels for bfloat16 inputs, keys of up to 256 channels.
+#include "delta_inst.hpp"
+
+namespace pararnn {
+namespace delta {
+template pararnn_status_t run_scan<true, 256>(const Args &, bool, void *);
+template pararnn_status_t run_adjoint<true, 256>(const Args &, bool, void *);
+}  // namespace delta
+}  // namespace pararnn

@@ -1,0 +1,9 @@
+// Delta rule: kernels for float32 inputs, keys of up to 128 channels.
+#include "delta_inst.hpp"
+
+namespace pararnn {
+namespace delta {
+template pararnn_status_t run_scan<false, 128>(const Args &, bool, void *);
+template pararnn_status_t run_adjoint<false, 128>(const Args &, bool, void *);
+}  // namespace delta
+}  // namespace pararnn

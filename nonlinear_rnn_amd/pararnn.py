@@ -9,7 +9,8 @@ is missing, the calls raise.
 Names follow the ABI: ``solve_gru``, ``solve_gru_noalloc``, ``solve_lstm``,
 ``adjoint``, ``scan``, ``sequential``, ``project``, ``workspace_bytes``,
 ``plan``; for language models ``gated_scan``, ``gated_scan_adjoint``,
-``gated_step``, ``block_norm``, ``block_norm_adjoint``, ``token_logprobs``,
+``gated_step``, ``delta_scan``, ``delta_scan_adjoint``, ``delta_step``,
+``block_norm``, ``block_norm_adjoint``, ``token_logprobs``,
 ``token_logprobs_adjoint``.
 """
 import ctypes
@@ -54,6 +55,18 @@ class BlockShape(ctypes.Structure):
                 ("B", "T", "D", "h_stride_b", "h_stride_d", "h_stride_t", "g_stride_b",
                  "g_stride_d", "g_stride_t", "x_stride_b", "x_stride_t", "z_stride_b",
                  "z_stride_t")]
+
+
+class DeltaShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hk", "Hv", "dk", "dv")] + [
+        (n, ctypes.c_int64 * 4) for n in ("q_stride", "k_stride", "v_stride", "o_stride")] + [
+        ("gate_stride", ctypes.c_int64 * 3)]
+
+
+class DeltaGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv")] + [
+        (n, ctypes.c_int64 * 4) for n in ("dq_stride", "dk_stride", "dv_stride")] + [
+        (n, ctypes.c_void_p) for n in ("dbeta", "dlog_decay", "dh0")]
 
 
 class Newton(ctypes.Structure):
@@ -132,6 +145,16 @@ def load():
     lib.pararnn_token_logprobs_adjoint.restype = i32
     lib.pararnn_token_logprobs_adjoint.argtypes = [i64, i64, vp, i32, i64, vp, f32, vp, vp, vp, vp,
                                                    vp, vp, i64, vp]
+    lib.pararnn_delta_workspace_bytes.restype = sz
+    lib.pararnn_delta_workspace_bytes.argtypes = [P(DeltaShape), i32, i32]
+    lib.pararnn_delta_scan.restype = i32
+    lib.pararnn_delta_scan.argtypes = [P(DeltaShape), vp, vp, vp, i32, vp, vp, vp, vp, f32, vp, vp, vp,
+                                       sz, vp]
+    lib.pararnn_delta_scan_adjoint.restype = i32
+    lib.pararnn_delta_scan_adjoint.argtypes = [P(DeltaShape), vp, vp, vp, i32, vp, vp, vp, vp, f32, vp,
+                                               vp, P(DeltaGrads), vp, sz, vp]
+    lib.pararnn_delta_step.restype = i32
+    lib.pararnn_delta_step.argtypes = [P(DeltaShape), vp, vp, vp, i32, vp, vp, vp, vp, i64, f32, vp, vp]
     _lib = lib
     return lib
 
@@ -723,6 +746,7 @@ def scan(A, b, x0=None, *, reverse=False, out=None, steps_per_lane=0, waves_per_
 # size).
 
 TOP_MAX = 64  # PARARNN_TOP_MAX
+DELTA_KEY_MAX = 256  # PARARNN_DELTA_KEY_MAX
 
 _plans = {}  # prepared records by signature
 
@@ -929,6 +953,173 @@ def gated_step(u, lam, states, *, slots=None, power=8.0, out=None, stream=None):
     _check(lib.pararnn_gated_step(B, D, _ptr_array(u), udt, stride, lam.data_ptr(), power,
                                   _ptr(slots), states.data_ptr(), pool, out.data_ptr(),
                                   _where(dev, stream)[1]))
+    return out
+
+
+def _call(dev, function, *args):
+    """Runs a library call with `dev` the current device: the default stream's
+    handle names the current device's."""
+    if dev.index == torch.cuda.current_device():
+        _check(function(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(function(*args))
+
+
+def _delta_shape(q, k, v, beta, log_decay, o):
+    """Checks what all of the delta rule's calls take, with a last dimension of
+    one step for `delta_step`; (shape record, dtype code).  o: strides."""
+    dt = _code(q, "q")
+    _require(q.dim() == 4, "q: expected a tensor [B][Hk][dk][T]")
+    _require(_is_tensor(k) and k.shape == q.shape, "k: must have q's shape")
+    _require(_is_tensor(v) and v.dim() == 4, "v: expected a tensor [B][Hv][dv][T]")
+    _require(k.dtype is q.dtype and v.dtype is q.dtype, "q, k and v must share their dtype")
+    B, Hk, dk, T = q.shape
+    Hv, dv = v.shape[1:3]
+    _require(v.shape[0] == B and v.shape[3] == T, "v: must have q's batch and time")
+    _require(Hk > 0 and Hv > 0 and Hv % Hk == 0, "v: its heads must be a multiple of q's")
+    _require(0 < dk <= DELTA_KEY_MAX and dv > 0, f"keys of 1 to {DELTA_KEY_MAX} channels, values of 1 or more")
+    for name, t in (("beta", beta), ("log_decay", log_decay)):
+        if t is None and name == "log_decay":
+            continue
+        if not _is_tensor(t) or tuple(t.shape) != (B, Hv, T) or t.dtype != torch.float32:
+            raise ValueError(f"{name}: must be float32 {[B, Hv, T]}")
+        if t.numel() and t.stride() != beta.stride():
+            raise ValueError("beta and log_decay must share their strides")
+    four, three = ctypes.c_int64 * 4, ctypes.c_int64 * 3
+    return DeltaShape(B, T, Hk, Hv, dk, dv, four(*q.stride()), four(*k.stride()), four(*v.stride()),
+                      four(*o), three(*beta.stride())), dt
+
+
+def _like_steps(B, H, d, T, like):
+    """Dense strides of a tensor indexed [B][H][d][T], its channels side by side
+    where those of `like` are, else its steps."""
+    if T > 1 and d > 1 and like.stride(2) == 1 and like.stride(3) != 1:
+        return (T * H * d, d, 1, H * d)
+    return (H * d * T, d * T, T, 1)
+
+
+def _delta_plan(q, k, v, beta, log_decay, h0, resets, out, go, g_last, workspace, adjoint):
+    for name, t in (("out", out), ("go", go)):
+        if t is not None and (not _is_tensor(t) or t.dtype != torch.float32 or t.shape != v.shape):
+            raise ValueError(f"{name}: must be float32 of v's shape")
+    given = go if adjoint else out
+    _require(_is_tensor(v) and v.dim() == 4, "v: expected a tensor [B][Hv][dv][T]")
+    os = _like_steps(*v.shape, v) if given is None else given.stride()
+    shape, dt = _delta_shape(q, k, v, beta, log_decay, os)
+    B, Hv, dv, T = v.shape
+    dk = q.shape[2]
+    for name, t in (("h0", h0), ("g_last", g_last)):
+        if t is not None:
+            _check_dense(t, name, (B, Hv, dk, dv))
+    _check_resets(resets, B, T)
+    _check_devices(q.device, [("q", q), ("k", k), ("v", v), ("beta", beta), ("log_decay", log_decay),
+                              ("h0", h0), ("resets", resets), ("out", out), ("go", go),
+                              ("g_last", g_last), ("workspace", workspace)])
+    ref = ctypes.byref(shape)
+    nws = int(load().pararnn_delta_workspace_bytes(ref, dt, 1 if adjoint else 0))
+    return ref, dt, os, nws, q.device
+
+
+def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=None, out=None,
+               workspace=None, stream=None):
+    """Gated delta rule: per head, with S [dk][dv] the state,
+    S <- exp(log_decay) S, w = beta (v - k^T S), S <- S + k w^T, o = scale q^T S.
+    q, k [B][Hk][dk][T], v [B][Hv][dv][T] float32 or bfloat16 (Hv a multiple of
+    Hk: neighbouring value heads share a key head; steps or channels side by
+    side are the fast layouts), beta and log_decay [B][Hv][T] float32 (None: no
+    decay), h0 [B][Hv][dk][dv] float32 or None (zero), scale None: dk ** -0.5,
+    resets [B][T] bool or None: True where a new document starts.  Returns
+    (o [B][Hv][dv][T], last [B][Hv][dk][dv]), float32; ``o.flatten(1, 2)`` is
+    the plane that ``block_norm`` takes."""
+    lib = load()
+    shape, dt, os, nws, dev = _planned(
+        ("delta", _signature(q, k, v, beta, log_decay, h0, resets, out, workspace)),
+        _delta_plan, q, k, v, beta, log_decay, h0, resets, out, None, None, workspace, False)
+    if out is None:
+        out = torch.empty_strided(v.shape, os, dtype=torch.float32, device=dev)
+        _record_on(stream, [out])
+    last = torch.empty((v.shape[0], v.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32, device=dev)
+    _record_on(stream, [last])
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _call(dev, lib.pararnn_delta_scan, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+          beta.data_ptr(), _ptr(log_decay), _ptr(h0), _ptr(resets),
+          q.shape[2] ** -0.5 if scale is None else scale, out.data_ptr(), last.data_ptr(), _ptr(ws),
+          0 if ws is None else ws.numel(), at[1])
+    return out, last
+
+
+def delta_scan_adjoint(q, k, v, beta, log_decay, h0, go, *, g_last=None, scale=None, resets=None,
+                       workspace=None, stream=None):
+    """Backward pass of ``delta_scan`` for L = sum <go, o> + <g_last, last>; go
+    [B][Hv][dv][T] float32 or None (zero), g_last [B][Hv][dk][dv] or None.
+    Returns dict(dq, dk, dv in the inputs' dtype, dbeta, dlog_decay [B][Hv][T],
+    dh0 [B][Hv][dk][dv]); dlog_decay and dh0 are None where their input is."""
+    lib = load()
+    shape, dt, _, nws, dev = _planned(
+        ("delta_adjoint", _signature(q, k, v, beta, log_decay, h0, resets, go, g_last, workspace)),
+        _delta_plan, q, k, v, beta, log_decay, h0, resets, None, go, g_last, workspace, True)
+    dq, dk, dv = (torch.empty_strided(x.shape, _like_steps(*x.shape, x), dtype=x.dtype, device=dev)
+                  for x in (q, k, v))
+    dbeta = torch.empty(beta.shape, dtype=torch.float32, device=dev)
+    dlog = None if log_decay is None else torch.empty(beta.shape, dtype=torch.float32, device=dev)
+    dh0 = None if h0 is None else torch.empty(h0.shape, dtype=torch.float32, device=dev)
+    _record_on(stream, [dq, dk, dv, dbeta, dlog, dh0])
+    four = ctypes.c_int64 * 4
+    grads = DeltaGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), four(*dq.stride()), four(*dk.stride()),
+                       four(*dv.stride()), dbeta.data_ptr(), _ptr(dlog), _ptr(dh0))
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _call(dev, lib.pararnn_delta_scan_adjoint, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+          beta.data_ptr(), _ptr(log_decay), _ptr(h0), _ptr(resets),
+          q.shape[2] ** -0.5 if scale is None else scale, _ptr(go), _ptr(g_last), ctypes.byref(grads),
+          _ptr(ws), 0 if ws is None else ws.numel(), at[1])
+    return dict(dq=dq, dk=dk, dv=dv, dbeta=dbeta, dlog_decay=dlog, dh0=dh0)
+
+
+def _delta_step_plan(q, k, v, beta, log_decay, states, slots, out):
+    for name, t, n in (("q", q, 3), ("k", k, 3), ("v", v, 3), ("beta", beta, 2), ("log_decay", log_decay, 2)):
+        if t is None and name == "log_decay":
+            continue
+        if not _is_tensor(t) or t.dim() != n:
+            raise ValueError(f"{name}: expected a tensor " + ("[B][H][d]" if n == 3 else "[B][Hv]"))
+    B, Hv, dv = v.shape
+    os = (Hv * dv, dv, 1, 1)
+    if out is not None:
+        _check_dense(out, "out", (B, Hv, dv))
+    shape, dt = _delta_shape(q[..., None], k[..., None], v[..., None], beta[..., None],
+                             None if log_decay is None else log_decay[..., None], os)
+    _require(_is_tensor(states) and states.dim() == 4, "states: expected a tensor [pool][Hv][dk][dv]")
+    pool = states.shape[0]
+    _check_dense(states, "states", (pool, Hv, q.shape[2], dv))
+    if slots is None:
+        _require(pool >= B, "states: a row for each request, or slots")
+    elif not _is_tensor(slots) or tuple(slots.shape) != (B,) or slots.dtype != torch.int32 or (
+            not slots.is_contiguous()):
+        raise ValueError(f"slots: must be contiguous int32 [{B}]")
+    _check_devices(q.device, [("q", q), ("k", k), ("v", v), ("beta", beta), ("log_decay", log_decay),
+                              ("states", states), ("slots", slots), ("out", out)])
+    return ctypes.byref(shape), dt, pool, q.device
+
+
+def delta_step(q, k, v, beta, log_decay, states, *, slots=None, scale=None, out=None, stream=None):
+    """One step of the gated delta rule for B requests: q, k [B][Hk][dk], v
+    [B][Hv][dv], beta and log_decay [B][Hv] (None: no decay), states
+    [pool][Hv][dk][dv] float32, updated in place, slots [B] int32 or None (row
+    b has slot b).  A row whose slot is outside the pool (-1) is idle: it gives
+    zeros and changes no state; live rows need distinct slots.  Returns o
+    [B][Hv][dv] float32."""
+    lib = load()
+    shape, dt, pool, dev = _planned(
+        ("delta_step", _signature(q, k, v, beta, log_decay, states, slots, out)),
+        _delta_step_plan, q, k, v, beta, log_decay, states, slots, out)
+    if out is None:
+        out = torch.empty(v.shape, dtype=torch.float32, device=dev)
+        _record_on(stream, [out])
+    _call(dev, lib.pararnn_delta_step, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, beta.data_ptr(),
+          _ptr(log_decay), _ptr(slots), states.data_ptr(), pool,
+          q.shape[2] ** -0.5 if scale is None else scale, out.data_ptr(), _where(dev, stream)[1])
     return out
 
 

@@ -533,6 +533,87 @@ pararnn_status_t pararnn_delta_step(const pararnn_delta_shape_t *shape, const vo
                                     const int32_t *slots, float *states, int64_t pool, float scale,
                                     float *o, void *stream);
 
+/*
+ * Distillation from a teacher's most likely tokens, as pararnn_token_logprobs
+ * lists them.  Per row, with p_e = exp(top_logprob[e]) the teacher's
+ * probability of the token top_index[e], P their sum, and q = softmax(scale
+ * logits) the student's,
+ *     loss = sum_e p_e (log p_e - log q[top_index[e]])
+ *            + r (log r - log q_rest)                     where tail is not 0,
+ * r = 1 - P (taken as 0 below 1e-6, what rounding can leave of a full list) and
+ * q_rest the student's probability of all tokens that are not listed.
+ *   logits  : [N][V], dtype F32 or BF16, rows row_stride >= V elements apart
+ *   top_index, top_logprob : [N][top] int64 / float32, top at most
+ *             PARARNN_DISTILL_MAX.  A negative index is no entry.  A token
+ *             that is listed twice counts once in q_rest, each time in the
+ *             sums over e.  An index past the vocabulary makes the loss NaN.
+ *   scale   : inverse temperature, > 0, finite
+ *   loss, lse, log_rest : [N] float32 out (lse of scale logits; log q_rest)
+ * A row without an entry has loss 0 and gradient 0.  A listed token of p_e > 0
+ * whose logit is -inf makes the loss inf, and so does an r > 0 where the
+ * student allows no other token.
+ *   ws      : pararnn_distill_workspace_bytes(N, V) bytes (0 is possible)
+ */
+#define PARARNN_DISTILL_MAX 1024
+size_t pararnn_distill_workspace_bytes(int64_t N, int64_t V);
+pararnn_status_t pararnn_distill_top(int64_t N, int64_t V, const void *logits,
+                                     pararnn_dtype_t dtype, int64_t row_stride,
+                                     const int64_t *top_index, const float *top_logprob,
+                                     int32_t top, int tail, float scale, float *loss, float *lse,
+                                     float *log_rest, void *ws, size_t ws_bytes, void *stream);
+/*
+ * Its gradient for the logits,
+ *     g_loss scale (q_j (P + r) - p_j)            for listed tokens,
+ *     g_loss scale q_j (P + r - r / q_rest)       for the others
+ * (r = 0 without a tail), from the forward's lse and log_rest.  A row whose
+ * logits are all -inf has gradient 0.  dlogits has the dtype of the logits,
+ * rows d_stride elements apart, and may be the logits' own memory (same
+ * stride).
+ */
+pararnn_status_t pararnn_distill_top_adjoint(int64_t N, int64_t V, const void *logits,
+                                             pararnn_dtype_t dtype, int64_t row_stride,
+                                             const int64_t *top_index, const float *top_logprob,
+                                             int32_t top, int tail, float scale, const float *lse,
+                                             const float *log_rest, const float *g_loss,
+                                             void *dlogits, int64_t d_stride, void *stream);
+
+/*
+ * What is done to logits before a token is sampled from them.  Per row n and
+ * token j, in this order, in float32 and rounded once:
+ *   - j in the row's history (the first lengths[n] of its tokens): x / repetition
+ *     where x > 0, else x repetition;
+ *   - j there c > 0 times from place prompt[n] on: x - frequency c - presence;
+ *   - j in the row's bias list: x + its value, the last one if it is listed twice;
+ *   - bit j of the row's mask 0: -inf.
+ *   logits, out : [N][V], dtype F32 or BF16; out may be the logits (same stride)
+ *   tokens  : [N][length] int64, rows token_stride apart; tokens outside the
+ *             vocabulary (negative ones, say) are passed over
+ *   lengths, prompt : [N] int32 or NULL (length; 0)
+ *   repetition, presence, frequency : [N] float32 or NULL (1; 0; 0)
+ *   bias_index, bias_value : [N][biases] int64 / float32; indices outside the
+ *             vocabulary are passed over
+ *   allowed : [allowed_count][allowed_stride] words of 32 bits, token j the bit
+ *             j % 32 of word j / 32, or NULL; allowed_rows [N] int32 the mask of
+ *             each row (one that is not there: none), or NULL (row n has mask n)
+ */
+typedef struct {
+    const int64_t *tokens;
+    int64_t token_stride, length;
+    const int32_t *lengths, *prompt;
+    const float *repetition, *presence, *frequency;
+    const int64_t *bias_index;
+    const float *bias_value;
+    int64_t biases;
+    const int32_t *allowed;
+    int64_t allowed_stride, allowed_count;
+    const int32_t *allowed_rows;
+} pararnn_adjust_t;
+
+pararnn_status_t pararnn_adjust_logits(int64_t N, int64_t V, const void *logits,
+                                       pararnn_dtype_t dtype, int64_t row_stride,
+                                       const pararnn_adjust_t *how, void *out, int64_t out_stride,
+                                       void *stream);
+
 /* Static description of a status code. */
 const char *pararnn_status_string(pararnn_status_t status);
 

@@ -16,8 +16,9 @@ Two layouts: ``gru``/``lstm`` take one [B][D][T]-indexed tensor per gate
 passed to the kernels as strided views (no transpose copy), and the
 gradient for u comes back as one [B][T][G*D] tensor written by the adjoint.
 
-``gated_scan``, ``block_norm`` and ``token_logprobs`` are the differentiable
-forms of the operators of recurrent language models.  They have first
+``gated_scan``, ``delta_scan``, ``block_norm``, ``token_logprobs`` and
+``distill_top`` are the differentiable forms of the operators of recurrent
+language models.  They have first
 derivatives: differentiating a gradient of theirs raises.
 
 Non-convergence is not an error in the solve; pass ``strict=True`` to raise
@@ -332,3 +333,28 @@ def token_logprobs(logits, tokens, *, top=0, scale=1.0):
     out = _TokenLogprobs.apply(logits, tokens, int(top), scale)
     names = ("logprob", "entropy", "lse", "top_index", "top_logprob")
     return dict(zip(names, out))
+
+
+class _DistillTop(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_index, top_logprob, tail, scale):
+        out = pr.distill_top(logits, top_index, top_logprob, tail=tail, scale=scale)
+        ctx.save_for_backward(logits, top_index, top_logprob, out["lse"], out["log_rest"])
+        ctx.tail, ctx.scale = tail, scale
+        ctx.mark_non_differentiable(out["lse"], out["log_rest"])
+        return out["loss"], out["lse"], out["log_rest"]
+
+    @staticmethod
+    @_once
+    def backward(ctx, g_loss, *_):
+        logits, top_index, top_logprob, lse, log_rest = ctx.saved_tensors
+        return (pr.distill_top_adjoint(logits, top_index, top_logprob, lse, log_rest, g_loss.contiguous(),
+                                       tail=ctx.tail, scale=ctx.scale), None, None, None, None)
+
+
+def distill_top(logits, top_index, top_logprob, *, tail=True, scale=1.0):
+    """Differentiable distillation loss (``pararnn.distill_top``): the gradient
+    of the loss for the student's logits; lse and log_rest carry none, and the
+    teacher's list is taken as given."""
+    loss, lse, log_rest = _DistillTop.apply(logits, top_index, top_logprob, tail, scale)
+    return dict(loss=loss, lse=lse, log_rest=log_rest)

@@ -37,7 +37,7 @@ def compile_flags():
 SOURCES = ["pararnn.hip", "inst_gru_f32.hip", "inst_gru_bf16.hip", "inst_gru_bf16_seq.hip",
            "inst_lstm_f32.hip", "inst_lstm_bf16.hip", "inst_scan.hip", "inst_seq.hip",
            "inst_project.hip", "gated.hip", "block.hip", "score.hip"] + [
-           f"inst_block_{n}.hip" for n in ("f32", "gate", "stream", "bf16", "args", "norm")] + ["delta.hip"] + [
+           f"inst_block_{n}.hip" for n in ("f32", "gate", "stream", "bf16", "args", "norm")] + ["delta.hip", "distill.hip", "adjust.hip"] + [
            f"inst_delta_{t}_{n}.hip" for t in ("bf16", "f32") for n in (64, 128, 256)]
 
 # Per-unit scheduler choice, by measurement: the block-sequential ParaGRU

@@ -1,0 +1,308 @@
+// Distillation from a teacher's most likely tokens: per row, with p_e the
+// teacher's probabilities of the listed tokens j_e, r = 1 - sum p_e what they
+// leave, and q = softmax(scale x) the student's probabilities,
+//     loss = sum_e p_e (log p_e - log q_{j_e}) + r (log r - log q_rest),
+// q_rest the sum of q over the tokens that are not listed (without `tail` the
+// second term is left out).  The gradient for the student's logits is
+//     scale (q_j (P + r) - p_j)                 for listed tokens, P = sum p_e,
+//     scale q_j (P + r - r / q_rest)            for the others.
+// q_rest is summed over the tokens themselves: as 1 - sum q_{j_e} it would be
+// lost where the student agrees with the teacher.  Sums are float32 relative
+// to a running maximum; those of the short list float64.
+#pragma once
+
+#include "score.hpp"
+
+namespace pararnn {
+namespace distill {
+
+constexpr int kWaves = 4, kThreads = kWaves * kWave;
+constexpr int kParts = 32;              // most parts of a row
+constexpr int kSection = 16384;         // vectors whose listed elements are marked at once
+constexpr int kMost = PARARNN_DISTILL_MAX, kEach = (kMost + kThreads - 1) / kThreads;
+constexpr float kRest = 1e-6f;          // a smaller r is what rounding left of the list
+
+struct Args {
+    const void *x;
+    const int64_t *index;
+    const float *logprob;
+    int64_t N, V, stride;
+    int32_t count, parts, tail;
+    float scale;
+    float *loss, *lse, *log_rest;
+    float2 *part_stats;  // [N][parts]
+    // backward
+    const float *lse_in, *log_rest_in, *g_loss;
+    void *dx;
+    int64_t dstride;
+};
+
+// The largest element and the sum of 2^(c (x - m)); an empty part has the
+// lowest finite m and s = 0.
+struct Sum {
+    float m, s;
+};
+__device__ __forceinline__ Sum no_sum() { return {-__FLT_MAX__, 0.0f}; }
+__device__ __forceinline__ void rebase(Sum &a, float m, float c)
+{
+    a.s *= ex2(fmaxf(c * (a.m - m), -1e30f));  // finite: 0 stays 0
+    a.m = m;
+}
+__device__ __forceinline__ Sum join(Sum a, Sum b, float c)
+{
+    const float m = fmaxf(a.m, b.m);
+    rebase(a, m, c);
+    rebase(b, m, c);
+    return {m, a.s + b.s};
+}
+// Of all threads of the workgroup, in every thread, joined in a fixed order.
+__device__ __forceinline__ Sum join_all(Sum a, float c, Sum (&part)[kWaves])
+{
+    float m = a.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    rebase(a, m, c);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) a.s += __shfl_xor(a.s, o);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = a;
+    __syncthreads();
+    a = part[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) a = join(a, part[w], c);
+    return a;
+}
+__device__ __forceinline__ double add_all(double x, double (&part)[kWaves])
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
+    __syncthreads();
+    x = part[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) x += part[w];
+    return x;
+}
+
+struct Shared {
+    Sum sums[kWaves];
+    double adds[kWaves];
+    int64_t list[kMost];
+};
+// The row's list to LDS; an unused entry is -1.
+__device__ __forceinline__ void load_list(const Args &A, int64_t n, Shared &sh)
+{
+    for (int e = threadIdx.x; e < A.count; e += kThreads) {
+        const int64_t j = A.index[n * A.count + e];
+        sh.list[e] = j < 0 ? -1 : j;
+    }
+}
+// Whether no entry before e names the same token.
+__device__ __forceinline__ bool leads(const Shared &sh, int e)
+{
+    for (int i = 0; i < e; ++i)
+        if (sh.list[i] == sh.list[e]) return false;
+    return true;
+}
+// The row's results from the sum over the tokens that are not listed.
+template <bool BF16>
+__device__ __forceinline__ void finish(const Args &A, int64_t n, Sum rest, Shared &sh)
+{
+    const float c = A.scale * kLog2e;
+    Sum all = no_sum();
+    bool past = false, any = false;
+    for (int e = threadIdx.x; e < A.count; e += kThreads) {
+        const int64_t j = sh.list[e];
+        any |= j >= 0;
+        past |= j >= A.V;
+        if (j < 0 || j >= A.V || !leads(sh, e)) continue;
+        const float x = load_gate<BF16>(A.x, n * A.stride + j);
+        Sum one = {fmaxf(x, -__FLT_MAX__), x == -__builtin_inff() ? 0.0f : 1.0f};
+        if (!(x < __builtin_inff())) one.s = __builtin_nanf("");  // as in the other tokens' sum
+        all = join(all, one, c);
+    }
+    all = join(join_all(all, c, sh.sums), rest, c);
+    const bool empty = all.s == 0.0f;
+    const float ls = logf(all.s);
+    const float lse = empty ? -__builtin_inff() : fmaf_(A.scale, all.m, ls);
+    const float log_rest = rest.s == 0.0f ? -__builtin_inff() : fmaf_(A.scale, rest.m - all.m, logf(rest.s) - ls);
+    double P = 0.0, loss = 0.0;
+    for (int e = threadIdx.x; e < A.count; e += kThreads) {
+        const int64_t j = sh.list[e];
+        if (j < 0 || j >= A.V) continue;
+        const float lp = A.logprob[n * A.count + e], p = expf(lp);
+        const float x = load_gate<BF16>(A.x, n * A.stride + j);
+        const float lq = empty || x == -__builtin_inff() ? -__builtin_inff() : fmaf_(A.scale, x - all.m, -ls);
+        P += p;
+        if (p != 0.0f) loss += (double)p * ((double)lp - lq);
+    }
+    P = add_all(P, sh.adds);
+    loss = add_all(loss, sh.adds);
+    if (A.tail) {
+        const float r = (float)(1.0 - P);
+        if (!(r < kRest)) loss += (double)r * ((double)logf(r) - log_rest);
+    }
+    past = __syncthreads_or(past);
+    any = __syncthreads_or(any);
+    if (threadIdx.x == 0) {
+        A.loss[n] = past ? __builtin_nanf("") : any ? (float)loss : 0.0f;
+        A.lse[n] = lse;
+        A.log_rest[n] = log_rest;
+    }
+}
+
+// A workgroup per row, or per part of a row (PARTS) where there are few.  The
+// listed tokens are marked in LDS, a byte for each 16-byte vector of the row,
+// and left out of the sum; they join it at the end.  Bound by HBM.
+template <bool BF16, bool PARTS>
+__global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
+{
+    using Row = RowView<BF16>;
+    constexpr int K = Row::K, U = kScoreUnroll;
+    __shared__ Shared sh;
+    __shared__ uint32_t marks[kSection / 4];
+    const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
+    const int64_t p = PARTS ? blockIdx.x - n * A.parts : 0;
+    const float c = A.scale * kLog2e;
+    const Row row(A.x, n * A.stride, A.V);
+    const int64_t per = PARTS ? (row.vectors + A.parts - 1) / A.parts : row.vectors;
+    const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
+    load_list(A, n, sh);
+
+    Sum a = no_sum();
+    const auto add = [&](float (&x)[K], uint32_t mark) {
+        float m = a.m;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (mark >> k & 1) x[k] = -__builtin_inff();
+            m = fmaxf(m, x[k]);
+        }
+        rebase(a, m, c);
+#pragma unroll
+        for (int k = 0; k < K; ++k) a.s += ex2(c * (x[k] - m));
+    };
+    for (int64_t s0 = v0; s0 < v1; s0 += kSection) {
+        const int64_t s1 = min(v1, s0 + kSection);
+        __syncthreads();
+        for (int i = threadIdx.x; i < (int)((s1 - s0 + 3) / 4); i += kThreads) marks[i] = 0;
+        __syncthreads();
+        for (int e = threadIdx.x; e < A.count; e += kThreads) {
+            const int64_t j = sh.list[e] + row.shift, at = j / K - s0;
+            if (sh.list[e] >= 0 && sh.list[e] < A.V && at >= 0 && at < s1 - s0)
+                atomicOr(&marks[at / 4], 1u << (8 * (at % 4) + j % K));
+        }
+        __syncthreads();
+        const auto mark = [&](int64_t i) { return marks[(i - s0) / 4] >> (8 * ((i - s0) % 4)) & 0xffu; };
+        int64_t i = s0 + threadIdx.x;
+        for (; i + (U - 1) * kThreads < s1; i += U * kThreads) {
+            float x[U][K];
+#pragma unroll
+            for (int q = 0; q < U; ++q) row.load(i + q * kThreads, x[q]);
+#pragma unroll
+            for (int q = 0; q < U; ++q) add(x[q], mark(i + q * kThreads));
+        }
+        for (; i < s1; i += kThreads) {
+            float x[K];
+            row.load(i, x);
+            add(x, mark(i));
+        }
+    }
+    a = join_all(a, c, sh.sums);
+    if constexpr (PARTS) {
+        if (threadIdx.x == 0) A.part_stats[blockIdx.x] = make_float2(a.m, a.s);
+    } else {
+        finish<BF16>(A, n, a, sh);
+    }
+}
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) distill_join_kernel(Args A)
+{
+    __shared__ Shared sh;
+    const int64_t n = blockIdx.x;
+    load_list(A, n, sh);
+    Sum a = no_sum();
+    if ((int)threadIdx.x < A.parts) {
+        const float2 v = A.part_stats[n * A.parts + threadIdx.x];
+        a = {v.x, v.y};
+    }
+    finish<BF16>(A, n, join_all(a, A.scale * kLog2e, sh.sums), sh);
+}
+
+// The gradient, U vectors a lane as in the scores' gradient: every token as
+// one that is not listed; then, behind a wait for these stores, the list's
+// tokens once more.  Their logits are read before anything is written, for the
+// gradient may take the logits' place.  Bound by HBM.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
+{
+    using Row = RowView<BF16>;
+    constexpr int K = Row::K, U = kScoreUnroll;
+    __shared__ Shared sh;
+    const int64_t n = blockIdx.x / A.parts;
+    const Row row(A.x, n * A.stride, A.V);
+    const int64_t first = (blockIdx.x - n * A.parts) * (U * kThreads), i = first + threadIdx.x;
+    float x[U][K];
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+        if (i + q * kThreads < row.vectors) row.load(i + q * kThreads, x[q]);
+    load_list(A, n, sh);
+    __syncthreads();
+    // the part's entries
+    const int64_t e0 = row.element(first), e1 = row.element(first + U * kThreads);
+    float mine[kEach];
+    double P = 0.0;
+    bool any = false;
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        const int e = s * kThreads + threadIdx.x;
+        mine[s] = 0.0f;
+        if (e >= A.count || sh.list[e] < 0) continue;
+        const int64_t j = sh.list[e];
+        any = true;
+        P += expf(A.logprob[n * A.count + e]);
+        if (j >= e0 && j < e1 && j < A.V) mine[s] = load_gate<BF16>(A.x, n * A.stride + j);
+    }
+    P = add_all(P, sh.adds);
+    any = __syncthreads_or(any);
+    const float lse = A.lse_in[n], g = A.scale * A.g_loss[n];
+    const bool none = !any || lse == -__builtin_inff();
+    float r = A.tail ? (float)(1.0 - P) : 0.0f;
+    if (r < kRest) r = 0.0f;
+    const float listed = (float)P + r, other = r == 0.0f ? listed : listed - r * expf(-A.log_rest_in[n]);
+    const auto q_of = [&](float v) { return none ? 0.0f : ex2(kLog2e * fmaf_(A.scale, v, -lse)); };
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        if (i + q * kThreads >= row.vectors) break;
+        const int64_t e = row.element(i + q * kThreads);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float p = q_of(x[q][k]);
+            x[q][k] = p == 0.0f ? 0.0f : g * (p * other);  // 0 times an infinite factor
+        }
+        if (e >= 0) {
+            store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, x[q]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, x[q][k]);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
+    __syncthreads();
+    if (none) return;
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        const int e = s * kThreads + threadIdx.x;
+        if (e >= A.count) break;
+        const int64_t j = sh.list[e];
+        if (j < 0 || j >= A.V || j < e0 || j >= e1 || !leads(sh, e)) continue;
+        float p = 0.0f;
+        for (int d = e; d < A.count; ++d)
+            if (sh.list[d] == j) p += expf(A.logprob[n * A.count + d]);
+        store_gate<BF16>(A.dx, n * A.dstride + j, g * fmaf_(q_of(mine[s]), listed, -p));
+    }
+}
+
+}  // namespace distill
+}  // namespace pararnn

@@ -11,7 +11,8 @@ Names follow the ABI: ``solve_gru``, ``solve_gru_noalloc``, ``solve_lstm``,
 ``plan``; for language models ``gated_scan``, ``gated_scan_adjoint``,
 ``gated_step``, ``delta_scan``, ``delta_scan_adjoint``, ``delta_step``,
 ``block_norm``, ``block_norm_adjoint``, ``token_logprobs``,
-``token_logprobs_adjoint``.
+``token_logprobs_adjoint``, ``distill_top``, ``distill_top_adjoint``,
+``adjust_logits``.
 """
 import ctypes
 import os
@@ -67,6 +68,14 @@ class DeltaGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv")] + [
         (n, ctypes.c_int64 * 4) for n in ("dq_stride", "dk_stride", "dv_stride")] + [
         (n, ctypes.c_void_p) for n in ("dbeta", "dlog_decay", "dh0")]
+
+
+class Adjust(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("length", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("lengths", "prompt", "repetition", "presence", "frequency",
+                                       "bias_index", "bias_value")] + [
+        ("biases", ctypes.c_int64), ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64),
+        ("allowed_count", ctypes.c_int64), ("allowed_rows", ctypes.c_void_p)]
 
 
 class Newton(ctypes.Structure):
@@ -155,6 +164,16 @@ def load():
                                                vp, P(DeltaGrads), vp, sz, vp]
     lib.pararnn_delta_step.restype = i32
     lib.pararnn_delta_step.argtypes = [P(DeltaShape), vp, vp, vp, i32, vp, vp, vp, vp, i64, f32, vp, vp]
+    lib.pararnn_distill_workspace_bytes.restype = sz
+    lib.pararnn_distill_workspace_bytes.argtypes = [i64, i64]
+    lib.pararnn_distill_top.restype = i32
+    lib.pararnn_distill_top.argtypes = [i64, i64, vp, i32, i64, vp, vp, ctypes.c_int32, i32, f32, vp, vp, vp,
+                                        vp, sz, vp]
+    lib.pararnn_distill_top_adjoint.restype = i32
+    lib.pararnn_distill_top_adjoint.argtypes = [i64, i64, vp, i32, i64, vp, vp, ctypes.c_int32, i32, f32, vp,
+                                                vp, vp, vp, i64, vp]
+    lib.pararnn_adjust_logits.restype = i32
+    lib.pararnn_adjust_logits.argtypes = [i64, i64, vp, i32, i64, P(Adjust), vp, i64, vp]
     _lib = lib
     return lib
 
@@ -747,6 +766,7 @@ def scan(A, b, x0=None, *, reverse=False, out=None, steps_per_lane=0, waves_per_
 
 TOP_MAX = 64  # PARARNN_TOP_MAX
 DELTA_KEY_MAX = 256  # PARARNN_DELTA_KEY_MAX
+DISTILL_MAX = 1024  # PARARNN_DISTILL_MAX
 
 _plans = {}  # prepared records by signature
 
@@ -1311,4 +1331,152 @@ def token_logprobs_adjoint(logits, tokens, lse, entropy=None, *, g_logprob=None,
                                               _ptr(entropy), _ptr(g_logprob), _ptr(g_entropy),
                                               _ptr(g_lse), out.data_ptr(), out_stride,
                                               _where(dev, stream)[1]))
+    return out
+
+
+def _check_logits(logits, out):
+    """Logits [N][V] and an output like them or None; (N, V, row stride, dtype
+    code, output's row stride)."""
+    dt = _code(logits, "logits")
+    _require(logits.dim() == 2, "logits: expected a tensor [N][V]")
+    N, V = logits.shape
+    if logits.numel() and V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: the vocabulary must be contiguous")
+    if out is not None and (not _is_tensor(out) or tuple(out.shape) != (N, V)
+                            or out.dtype is not logits.dtype
+                            or (out.numel() and V > 1 and out.stride(1) != 1)):
+        raise ValueError("out: must be [N][V] in the logits' dtype, the vocabulary contiguous")
+    return N, V, logits.stride(0) if N > 1 else V, dt, V if out is None or N <= 1 else out.stride(0)
+
+
+def _check_rows(t, name, shape, dtype):
+    if not _is_tensor(t) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous {str(dtype)[6:]} {list(shape)}")
+
+
+def _distill_plan(logits, top_index, top_logprob, vectors, out, workspace):
+    N, V, stride, dt, out_stride = _check_logits(logits, out)
+    _require(_is_tensor(top_index) and top_index.dim() == 2, "top_index: expected a tensor [N][top]")
+    top = top_index.shape[1]
+    _require(top <= DISTILL_MAX, f"top_index: at most {DISTILL_MAX} tokens a row")
+    _check_rows(top_index, "top_index", (N, top), torch.int64)
+    _check_rows(top_logprob, "top_logprob", (N, top), torch.float32)
+    for name, t in vectors:
+        _check_dense(t, name, (N,))
+    _check_devices(logits.device, [("logits", logits), ("top_index", top_index), ("top_logprob", top_logprob),
+                                   ("out", out), ("workspace", workspace)] + list(vectors))
+    return N, V, stride, dt, out_stride, top, int(load().pararnn_distill_workspace_bytes(N, V)), logits.device
+
+
+def distill_top(logits, top_index, top_logprob, *, tail=True, scale=1.0, workspace=None, stream=None):
+    """Loss of a student's logits [N][V] (float32 or bfloat16, the vocabulary
+    contiguous, rows may be strided) against a teacher's most likely tokens,
+    top_index [N][top] int64 (negative: no entry) and top_logprob [N][top]
+    float32, as ``token_logprobs`` gives them:
+    sum_e p_e (log p_e - log q_e) + r (log r - log q_rest) with q = softmax(scale
+    logits), r what the list leaves and q_rest the student's probability of the
+    tokens not listed (the second term only with ``tail``).  Returns dict(loss,
+    lse, log_rest), [N] float32; a row without an entry has loss 0."""
+    lib = load()
+    N, V, stride, dt, _, top, nws, dev = _planned(
+        ("distill", _signature(logits, top_index, top_logprob, workspace)), _distill_plan, logits, top_index,
+        top_logprob, (), None, workspace)
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    log_rest = torch.empty(N, dtype=torch.float32, device=dev)
+    _record_on(stream, [loss, lse, log_rest])
+    at = _where(dev, stream)
+    ws = workspace if workspace is not None else _ws.get(nws, dev, stream, at)
+    _call(dev, lib.pararnn_distill_top, N, V, logits.data_ptr(), dt, stride, top_index.data_ptr(),
+          top_logprob.data_ptr(), top, 1 if tail else 0, scale, loss.data_ptr(), lse.data_ptr(),
+          log_rest.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), at[1])
+    return dict(loss=loss, lse=lse, log_rest=log_rest)
+
+
+def distill_top_adjoint(logits, top_index, top_logprob, lse, log_rest, g_loss, *, tail=True, scale=1.0,
+                        out=None, stream=None):
+    """Gradient of ``distill_top``'s loss for the logits, from its lse and
+    log_rest and the loss's gradient g_loss [N] float32.  ``out`` may be the
+    logits themselves.  Returns dL/dlogits in the logits' dtype."""
+    lib = load()
+    N, V, stride, dt, out_stride, top, _, dev = _planned(
+        ("distill_adjoint", _signature(logits, top_index, top_logprob, lse, log_rest, g_loss, out)),
+        _distill_plan, logits, top_index, top_logprob, (("lse", lse), ("log_rest", log_rest), ("g_loss", g_loss)),
+        out, None)
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        _record_on(stream, [out])
+    _call(dev, lib.pararnn_distill_top_adjoint, N, V, logits.data_ptr(), dt, stride, top_index.data_ptr(),
+          top_logprob.data_ptr(), top, 1 if tail else 0, scale, lse.data_ptr(), log_rest.data_ptr(),
+          g_loss.data_ptr(), out.data_ptr(), out_stride, _where(dev, stream)[1])
+    return out
+
+
+def _adjust_plan(logits, tokens, lengths, prompt, repetition, presence, frequency, bias_index, bias_value,
+                 allowed, allowed_rows, out):
+    N, V, stride, dt, out_stride = _check_logits(logits, out)
+    how = Adjust()
+    if tokens is not None:
+        if not _is_tensor(tokens) or tokens.dim() != 2 or tokens.shape[0] != N or tokens.dtype != torch.int64 or (
+                tokens.numel() and tokens.shape[1] > 1 and tokens.stride(1) != 1):
+            raise ValueError(f"tokens: must be int64 [{N}][length], a row's tokens contiguous")
+        how.length = tokens.shape[1]
+        how.token_stride = tokens.stride(0) if N > 1 else how.length
+    for name, t, dtype in (("lengths", lengths, torch.int32), ("prompt", prompt, torch.int32),
+                           ("repetition", repetition, torch.float32), ("presence", presence, torch.float32),
+                           ("frequency", frequency, torch.float32)):
+        if t is not None:
+            _require(tokens is not None, f"{name}: needs tokens")
+            _check_rows(t, name, (N,), dtype)
+    if bias_index is not None:
+        _require(_is_tensor(bias_index) and bias_index.dim() == 2, "bias: expected index and value [N][biases]")
+        _check_rows(bias_index, "bias index", (N, bias_index.shape[1]), torch.int64)
+        _check_rows(bias_value, "bias value", bias_index.shape, torch.float32)
+        how.biases = bias_index.shape[1]
+    if allowed is not None:
+        words = (V + 31) // 32
+        if not _is_tensor(allowed) or allowed.dim() != 2 or allowed.shape[1] != words or (
+                allowed.dtype != torch.int32 or (allowed.numel() and words > 1 and allowed.stride(1) != 1)):
+            raise ValueError(f"allowed: must be int32 [masks][{words}], a mask's words contiguous")
+        how.allowed_count = allowed.shape[0]
+        how.allowed_stride = allowed.stride(0) if allowed.shape[0] > 1 else words
+        _require(how.allowed_stride >= words, "allowed: its masks must not overlap")
+        if allowed_rows is None:
+            _require(how.allowed_count >= N, "allowed: a mask for each row, or allowed_rows")
+    if allowed_rows is not None:
+        _require(allowed is not None, "allowed_rows: needs allowed")
+        _check_rows(allowed_rows, "allowed_rows", (N,), torch.int32)
+    _check_devices(logits.device, [
+        ("logits", logits), ("tokens", tokens), ("lengths", lengths), ("prompt", prompt),
+        ("repetition", repetition), ("presence", presence), ("frequency", frequency), ("bias", bias_index),
+        ("bias", bias_value), ("allowed", allowed), ("allowed_rows", allowed_rows), ("out", out)])
+    return N, V, stride, dt, out_stride, how, logits.device
+
+
+def adjust_logits(logits, *, tokens=None, lengths=None, prompt=None, repetition=None, presence=None,
+                  frequency=None, bias=None, allowed=None, allowed_rows=None, out=None, stream=None):
+    """Logits [N][V] (float32 or bfloat16) as a token is to be sampled from them.
+    For the tokens of a row's history (tokens [N][length] int64, the first
+    lengths [N] int32 of them): x / repetition where x > 0, else x repetition;
+    then x - frequency c - presence for those that stand there c > 0 times from
+    place prompt [N] int32 on; then the row's biases, ``bias`` = (index [N][M]
+    int64, value [N][M] float32; the last one of a token); then -inf where the
+    bit of the row's mask is 0: allowed [masks][(V + 31) // 32] int32, of which
+    row n takes allowed_rows[n] (int32, negative: none) or n.  repetition,
+    presence and frequency are [N] float32; None leaves a step out, tokens
+    outside the vocabulary are passed over.  ``out`` may be the logits
+    themselves.  Returns the logits in their dtype."""
+    lib = load()
+    index, value = (None, None) if bias is None else bias
+    tensors = (logits, tokens, lengths, prompt, repetition, presence, frequency, index, value, allowed,
+               allowed_rows, out)
+    N, V, stride, dt, out_stride, plan, dev = _planned(("adjust", _signature(*tensors)), _adjust_plan, *tensors)
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        _record_on(stream, [out])
+    how = Adjust(_ptr(tokens), plan.token_stride, plan.length, _ptr(lengths), _ptr(prompt), _ptr(repetition),
+                 _ptr(presence), _ptr(frequency), _ptr(index), _ptr(value), plan.biases, _ptr(allowed),
+                 plan.allowed_stride, plan.allowed_count, _ptr(allowed_rows))
+    _call(dev, lib.pararnn_adjust_logits, N, V, logits.data_ptr(), dt, stride, ctypes.byref(how),
+          out.data_ptr(), out_stride, _where(dev, stream)[1])
     return out

@@ -69,6 +69,12 @@ pararnn_status_t check_delta(const pararnn_delta_shape_t *s, pararnn_dtype_t dty
     return PARARNN_OK;
 }
 
+// Wide workgroups where the chains are many.
+bool wide_chains(const pararnn_delta_shape_t *s)
+{
+    return room_of(s->dk) < 256 && s->dv > kNarrow && s->B * s->Hv * ((s->dv + kWide - 1) / kWide) >= kComputeUnits;
+}
+
 struct Layout {
     size_t inverse, inverse_t, states, dstates, w, x, xv, total;
 };
@@ -84,14 +90,15 @@ Layout layout(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool adjoin
         return first;
     };
     std::memset(&l, 0, sizeof(l));
-    l.inverse = take(items * C * C * 4);
+    const size_t slots = C == 64 ? Slots<64>::kCount : Slots<32>::kCount;
+    l.inverse = take(items * slots * sizeof(Fragment));
     if (adjoint) {
-        l.inverse_t = take(items * C * C * 4);
+        l.inverse_t = take(items * slots * sizeof(Fragment));
         l.states = take(items * room * pad * 4);
         l.dstates = take(items * room * pad * 4);
         l.w = take(items * C * pad * 4);
         l.x = take(items * C * pad * 4);
-        l.xv = take(items * C * (pad / value_block((int)room)) * 4);
+        l.xv = take(items * C * (pad / 16) * 4);
     }
     l.total = at;
     return l;
@@ -126,12 +133,13 @@ pararnn_status_t prepare(Args &A, const pararnn_delta_shape_t *s, pararnn_dtype_
     A.key = (int32_t)s->dk, A.value = (int32_t)s->dv;
     A.chunks = (s->T + chunk_of(dtype) - 1) / chunk_of(dtype);
     A.value_pad = (int32_t)((s->dv + 31) / 32 * 32);
-    A.blocks = A.value_pad / value_block(room_of(s->dk));
+    const int columns = wide_chains(s) ? kWide : kNarrow;
+    A.blocks = (A.value_pad + columns - 1) / columns;
     A.scale = scale;
     char *const base = static_cast<char *>(ws);
-    A.inverse = base + l.inverse;
+    A.inverse = reinterpret_cast<Fragment *>(base + l.inverse);
     if (adjoint) {
-        A.inverse_t = base + l.inverse_t;
+        A.inverse_t = reinterpret_cast<Fragment *>(base + l.inverse_t);
         A.states = reinterpret_cast<float *>(base + l.states);
         A.dstates = reinterpret_cast<float *>(base + l.dstates);
         A.w = reinterpret_cast<float *>(base + l.w);
@@ -148,11 +156,11 @@ bool time_first(const pararnn_delta_shape_t *s) { return s->k_stride[3] == 1 || 
 template <bool ADJOINT, bool HALF>
 pararnn_status_t run(const Args &A, const pararnn_delta_shape_t *s, void *stream)
 {
-    const bool tf = time_first(s);
+    const bool tf = time_first(s), w = wide_chains(s);
     switch (room_of(s->dk)) {
-    case 64: return ADJOINT ? run_adjoint<HALF, 64>(A, tf, stream) : run_scan<HALF, 64>(A, tf, stream);
-    case 128: return ADJOINT ? run_adjoint<HALF, 128>(A, tf, stream) : run_scan<HALF, 128>(A, tf, stream);
-    default: return ADJOINT ? run_adjoint<HALF, 256>(A, tf, stream) : run_scan<HALF, 256>(A, tf, stream);
+    case 64: return ADJOINT ? run_adjoint<HALF, 64>(A, tf, w, stream) : run_scan<HALF, 64>(A, tf, w, stream);
+    case 128: return ADJOINT ? run_adjoint<HALF, 128>(A, tf, w, stream) : run_scan<HALF, 128>(A, tf, w, stream);
+    default: return ADJOINT ? run_adjoint<HALF, 256>(A, tf, w, stream) : run_scan<HALF, 256>(A, tf, w, stream);
     }
 }
 

@@ -42,6 +42,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "delta_step.hpp"
 #include "elements.hpp"
 #include "pararnn.h"
@@ -71,13 +73,13 @@ struct Args {
     float *dbeta, *ddecay;            // [B][Hv][T]
     int64_t B, T, chunks;
     int32_t Hk, Hv, key, value;       // key, value: dk, dv
-    int32_t value_pad, blocks;        // columns of the workspace's rows; blocks of them
+    int32_t value_pad, blocks;        // columns of the workspace's rows; the chains' workgroups a head
     float scale;
     // workspace
-    void *inverse, *inverse_t;        // [b h][chunk][C][C] operands
+    struct Fragment *inverse, *inverse_t;  // [b h][chunk][slot] operands
     float *states, *dstates;          // [b h][chunk][DK][value_pad]
     float *w, *x;                     // [b h][chunk * C][value_pad]
-    float *xv;                        // [b h][chunk * C][blocks]: X . V of a block of columns
+    float *xv;                        // [b h][chunk * C][value_pad / 16]: X . V of 16 columns
 };
 
 // ---------------------------------------------------------------- numbers ---
@@ -107,29 +109,80 @@ struct Num<false> {
 using Bf = Num<true>;
 using Fl = Num<false>;
 
-__device__ __forceinline__ f32x4 mma(f32x4 c, bf16x8 a, bf16x8 b)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mma(f32x4 c, bf16x8 a, const Bf::Wide &b)
-{
-    return mma(mma(c, a, b.lo), a, b.hi);
-}
-__device__ __forceinline__ f32x4 mma(f32x4 c, const Bf::Wide &a, bf16x8 b)
-{
-    return mma(mma(c, a.lo, b), a.hi, b);
-}
-__device__ __forceinline__ f32x4 mma(f32x4 c, const Bf::Wide &a, const Bf::Wide &b)
-{
-    return mma(mma(mma(c, a.lo, b.hi), a.hi, b.lo), a.hi, b.hi);
-}
-// Eight instructions of 4 terms: the j-th takes the j-th element of every
+// A product as the instructions it takes, so that those of several results can take
+// turns: one result's wait for each other.  kParts of them, the smallest terms first.
+template <class A, class B>
+struct Product;
+template <>
+struct Product<bf16x8, bf16x8> {
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ f32x4 part(int, f32x4 c, bf16x8 a, bf16x8 b)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Product<bf16x8, Bf::Wide> {
+    static constexpr int kParts = 2;
+    static __device__ __forceinline__ f32x4 part(int i, f32x4 c, bf16x8 a, const Bf::Wide &b)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, i == 0 ? b.lo : b.hi, c, 0, 0, 0);
+    }
+};
+template <>
+struct Product<Bf::Wide, bf16x8> {
+    static constexpr int kParts = 2;
+    static __device__ __forceinline__ f32x4 part(int i, f32x4 c, const Bf::Wide &a, bf16x8 b)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(i == 0 ? a.lo : a.hi, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Product<Bf::Wide, Bf::Wide> {
+    static constexpr int kParts = 3;
+    static __device__ __forceinline__ f32x4 part(int i, f32x4 c, const Bf::Wide &a, const Bf::Wide &b)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(i == 0 ? a.lo : a.hi, i == 1 ? b.lo : b.hi, c, 0, 0, 0);
+    }
+};
+// Eight instructions of 4 terms: the i-th takes the i-th element of every
 // lane's eight, a permutation of the sum that both operands share.
-__device__ __forceinline__ f32x4 mma(f32x4 c, const Fl::Exact &a, const Fl::Exact &b)
+template <>
+struct Product<Fl::Exact, Fl::Exact> {
+    static constexpr int kParts = 8;
+    static __device__ __forceinline__ f32x4 part(int i, f32x4 c, const Fl::Exact &a, const Fl::Exact &b)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[i], b.x[i], c, 0, 0, 0);
+    }
+};
+template <class A, class B>
+__device__ __forceinline__ f32x4 mma(f32x4 c, const A &a, const B &b)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[j], b.x[j], c, 0, 0, 0);
+    for (int i = 0; i < Product<A, B>::kParts; ++i) c = Product<A, B>::part(i, c, a, b);
     return c;
+}
+// c_t + a_t b for several t
+template <class A, class B, int M>
+__device__ __forceinline__ void mma_rows(f32x4 (&c)[M], const A (&a)[M], const B &b)
+{
+#pragma unroll
+    for (int i = 0; i < Product<A, B>::kParts; ++i)
+#pragma unroll
+        for (int t = 0; t < M; ++t) c[t] = Product<A, B>::part(i, c[t], a[t], b);
+}
+
+// Results that are used behind a branch.  They can be read 8 (bfloat16) or 10
+// wait states after the instruction; the compiler does not count these along a
+// branch that is taken at once (rows 3 of 4 came out without their last terms).
+template <int M>
+__device__ __forceinline__ void settle(f32x4 (&x)[M])
+{
+    static_assert(M == 2 || M == 4, "one statement for all");
+    if constexpr (M == 4)
+        asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]));
+    else
+        asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]));
 }
 
 // A float32 as the bfloat16 next to it and the one next to what that leaves.
@@ -174,25 +227,29 @@ struct WideTile {
     alignas(16) typename Num<HALF>::Elem at[(HALF ? 2 : 1) * ROWS * kPitch];
 };
 
-// Operands of a 16x16 product: lane l holds row (or column) i0 + l % 16 and
-// the terms k0 + 8 (l / 16) .. + 7 of the sum.
+// Operands of a 16x16 product over 32 terms: lane l holds row (or column) i0 +
+// l % 16 and, with g = l / 16, the terms k0 + 4 g .. + 3 and k0 + 16 + 4 g .. + 3.
+// This order is that of two results one above the other (lane l of a result
+// holds column l % 16, rows 4 g .. + 3), so what a wave has computed it can
+// multiply with, without the LDS.
 // along: the terms lie side by side in the tile's rows.
 __device__ __forceinline__ bf16x8 operand_along(const uint16_t *at, int pitch, int i0, int k0)
 {
     const int lane = threadIdx.x % kWave;
-    const uint4 v = *reinterpret_cast<const uint4 *>(at + (i0 + lane % 16) * pitch + k0 + 8 * (lane / 16));
+    const uint16_t *p = at + (i0 + lane % 16) * pitch + k0 + 4 * (lane / 16);
     bf16x8 r;
-    __builtin_memcpy(&r, &v, 16);
+    __builtin_memcpy(&r, p, 8);
+    __builtin_memcpy(reinterpret_cast<char *>(&r) + 8, p + 16, 8);
     return r;
 }
 __device__ __forceinline__ Fl::Exact operand_along(const float *at, int pitch, int i0, int k0)
 {
     const int lane = threadIdx.x % kWave;
-    const float *p = at + (i0 + lane % 16) * pitch + k0 + 8 * (lane / 16);
+    const float *p = at + (i0 + lane % 16) * pitch + k0 + 4 * (lane / 16);
     Fl::Exact r;
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p + j);
+        const float4 v = *reinterpret_cast<const float4 *>(p + 4 * j);
         r.x[j] = v.x, r.x[j + 1] = v.y, r.x[j + 2] = v.z, r.x[j + 3] = v.w;
     }
     return r;
@@ -208,8 +265,8 @@ __device__ __forceinline__ s16x4 read_transposed(const uint16_t *p)
 __device__ __forceinline__ bf16x8 operand_across(const uint16_t *at, int pitch, int i0, int k0)
 {
     const int lane = threadIdx.x % kWave, i = lane % 16;
-    const uint16_t *p = at + (k0 + 8 * (lane / 16) + i / 4) * pitch + i0 + 4 * (i % 4);
-    const s16x4 a = read_transposed(p), b = read_transposed(p + 4 * pitch);
+    const uint16_t *p = at + (k0 + 4 * (lane / 16) + i / 4) * pitch + i0 + 4 * (i % 4);
+    const s16x4 a = read_transposed(p), b = read_transposed(p + 16 * pitch);
     bf16x8 r;
     __builtin_memcpy(&r, &a, 8);
     __builtin_memcpy(reinterpret_cast<char *>(&r) + 8, &b, 8);
@@ -218,10 +275,10 @@ __device__ __forceinline__ bf16x8 operand_across(const uint16_t *at, int pitch, 
 __device__ __forceinline__ Fl::Exact operand_across(const float *at, int pitch, int i0, int k0)
 {
     const int lane = threadIdx.x % kWave;
-    const float *p = at + (k0 + 8 * (lane / 16)) * pitch + i0 + lane % 16;
+    const float *p = at + (k0 + 4 * (lane / 16)) * pitch + i0 + lane % 16;
     Fl::Exact r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.x[j] = p[j * pitch];
+    for (int j = 0; j < 8; ++j) r.x[j] = p[(j < 4 ? j : 12 + j) * pitch];
     return r;
 }
 template <bool ALONG, bool HALF, int ROWS, int COLS>
@@ -275,10 +332,62 @@ __device__ __forceinline__ void clear(WideTile<HALF, ROWS, COLS> &t)
     for (int i = threadIdx.x; i < (int)(sizeof(t.at) / 4); i += blockDim.x) w[i] = 0;
 }
 
+// A wide operand as it lies in the lanes' registers, in LDS or in memory.
+struct Fragment {
+    uint4 a[kWave], b[kWave];  // the rounded values and what that leaves; of float32 the two halves
+};
+__device__ __forceinline__ void store_fragment(Fragment &f, const Bf::Wide &w)
+{
+    const int lane = threadIdx.x % kWave;
+    __builtin_memcpy(&f.a[lane], &w.hi, 16);
+    __builtin_memcpy(&f.b[lane], &w.lo, 16);
+}
+__device__ __forceinline__ void store_fragment(Fragment &f, const Fl::Wide &w)
+{
+    const int lane = threadIdx.x % kWave;
+    __builtin_memcpy(&f.a[lane], w.x, 16);
+    __builtin_memcpy(&f.b[lane], w.x + 4, 16);
+}
+__device__ __forceinline__ Bf::Wide load_fragment(const Fragment &f, Bf)
+{
+    const uint4 a = f.a[threadIdx.x % kWave], b = f.b[threadIdx.x % kWave];
+    Bf::Wide w;
+    __builtin_memcpy(&w.hi, &a, 16);
+    __builtin_memcpy(&w.lo, &b, 16);
+    return w;
+}
+__device__ __forceinline__ Fl::Wide load_fragment(const Fragment &f, Fl)
+{
+    const uint4 a = f.a[threadIdx.x % kWave], b = f.b[threadIdx.x % kWave];
+    Fl::Wide w;
+    __builtin_memcpy(w.x, &a, 16);
+    __builtin_memcpy(w.x + 4, &b, 16);
+    return w;
+}
+// Two results one above the other as an operand.
+template <bool HALF>
+__device__ __forceinline__ typename Num<HALF>::Wide stacked(f32x4 a, f32x4 b)
+{
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split(x, typename Num<HALF>::Wide());
+}
+// Operands of a triangular matrix [C][C], 16 rows and 32 terms each: those that
+// are not zero, row by row.  lower: terms up to the row; upper: from the row on.
+template <int C>
+struct Slots {
+    static constexpr int kCount = C == 64 ? 6 : 2;
+    static_assert(C == 64 || C == 32, "chunks");
+    static constexpr int lower(int row, int terms) { return C == 32 || row < 2 ? row : 2 * row - 2 + terms; }
+    static constexpr int upper(int row, int terms) { return C == 32 ? row : row < 2 ? 2 * row + terms : 2 + row; }
+    static constexpr bool in_lower(int row, int terms) { return 2 * terms <= row; }
+    static constexpr bool in_upper(int row, int terms) { return 2 * terms + 1 >= row; }
+};
+
 // --------------------------------------------------- inputs and documents ---
 
 // A chunk of queries or keys, DK channels of C steps, as 16-byte pieces in
-// registers and then in LDS, the steps side by side (TF) or the channels.
+// THREADS threads' registers and then in LDS, the steps side by side (TF) or the
+// channels.
 // Channels from `key` and steps from T on are zero and not read.
 template <bool HALF, int DK, bool TF, int THREADS>
 struct Pieces {
@@ -296,100 +405,165 @@ struct Pieces {
         else
             return __float_as_uint(*p);
     }
-    // base: the head's first element; d0: the first channel; t0: the chunk's first step
-    __device__ __forceinline__ void load(const Plane &x, const void *base, int d0, int64_t t0, int key, int64_t T)
+    // base: the head's first element; d0: the first channel; t0: the chunk's first
+    // step.  Nothing here depends on the lane but addresses, which are kept inside
+    // the tensor, so that all loads are under way at once; store() drops what lies
+    // outside.
+    __device__ __forceinline__ void load(const Plane &x, const Elem *base, int d0, int64_t t0, int key, int64_t T,
+                                         int tid)
     {
+        constexpr int kRows = THREADS / kPerRow;  // between a thread's pieces
+        static_assert(THREADS % kPerRow == 0, "a thread's pieces in one column");
+        const int row = tid / kPerRow, col = tid % kPerRow * E;
+        const int64_t stride = TF ? x.d : x.t;
+        if (t0 + C <= T && (TF ? x.t == 1 : x.d == 1 && key % E == 0) && stride < 1 << 24) {
+            // one address for the workgroup, 32 bits a lane
+            const char *p = reinterpret_cast<const char *>(base + (TF ? d0 * x.d + t0 : d0 + t0 * x.t));
+            const uint32_t at = (uint32_t)(row * (int)stride + col) * (uint32_t)sizeof(Elem);
+            const bool all = d0 + DK <= key;
+#pragma unroll
+            for (int n = 0; n < kCount; ++n) {
+                // (a piece whose channels are not there takes the first ones)
+                const bool here = all || (TF ? d0 + row + n * kRows < key : d0 + col < key);
+                const Words4 w = *reinterpret_cast<const Words4Any *>(
+                    p + (here ? at : 0u) + (TF && !here ? 0 : n * kRows * stride * (int64_t)sizeof(Elem)));
+                u[n] = make_uint4(w.x, w.y, w.z, w.w);
+            }
+            return;
+        }
 #pragma unroll
         for (int n = 0; n < kCount; ++n) {
-            const int i = n * THREADS + threadIdx.x, row = i / kPerRow, col = i % kPerRow * E;
-            const int d = d0 + (TF ? row : col);
-            const int64_t t = t0 + (TF ? col : row);
-            const Elem *p = static_cast<const Elem *>(base) + d * x.d + t * x.t;
-            u[n] = make_uint4(0, 0, 0, 0);
-            const bool whole = TF ? d < key && t + E <= T && x.t == 1 : t < T && d + E <= key && x.d == 1;
-            if (whole) {
-                const Words4 w = *reinterpret_cast<const Words4Any *>(p);
-                u[n] = make_uint4(w.x, w.y, w.z, w.w);
-            } else if (d < key && t < T) {
-                const int64_t step = TF ? x.t : x.d, left = TF ? T - t : key - d;
-                uint32_t w[4] = {0, 0, 0, 0};
+            const int d = d0 + (TF ? row + n * kRows : col);
+            const int64_t t = t0 + (TF ? col : row + n * kRows);
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (e < left) {
-                        if constexpr (HALF)
-                            w[e / 2] |= element(p + e * step) << (16 * (e % 2));
-                        else
-                            w[e] = element(p + e * step);
-                    }
-                u[n] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < E; ++e) {
+                const int de = min(TF ? d : d + e, key - 1);
+                const uint32_t v = element(base + de * x.d + min(TF ? t + e : t, T - 1) * x.t);
+                if constexpr (HALF)
+                    w[e / 2] |= v << (16 * (e % 2));
+                else
+                    w[e] = v;
             }
+            u[n] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    // Steps outside r0 .. r1 - 1 of the chunk are zero.
-    __device__ __forceinline__ void store(Lds &lds, int r0, int r1) const
+    // To LDS; steps outside r0 .. r1 - 1 of the chunk and channels from `key` on
+    // (counted from the tile's first) are zero.
+    __device__ __forceinline__ void store(Lds &lds, int r0, int r1, int key, int tid) const
     {
+        constexpr int kRows = THREADS / kPerRow;
+        const int row = tid / kPerRow, col = tid % kPerRow * E;
+        auto *const p = lds.at + row * lds.kPitch + col;
+        if (r0 == 0 && r1 == C && key >= DK) {
+#pragma unroll
+            for (int n = 0; n < kCount; ++n) *reinterpret_cast<uint4 *>(p + n * kRows * lds.kPitch) = u[n];
+            return;
+        }
+        const int first = TF ? r0 : 0, end = TF ? r1 : key;  // of the piece's own direction
 #pragma unroll
         for (int n = 0; n < kCount; ++n) {
-            const int i = n * THREADS + threadIdx.x, row = i / kPerRow, col = i % kPerRow * E;
             uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
-            if constexpr (TF) {
-                if (col < r0 || col + E > r1) {
+            const int r = row + n * kRows;
+            const bool out = TF ? r >= key : r < r0 || r >= r1;
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (col + e < r0 || col + e >= r1) {
-                            if constexpr (HALF)
-                                w[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
-                            else
-                                w[e] = 0;
-                        }
+            for (int e = 0; e < E; ++e)
+                if (out || col + e < first || col + e >= end) {
+                    if constexpr (HALF)
+                        w[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
+                    else
+                        w[e] = 0;
                 }
-            } else if (row < r0 || row >= r1) {
-                w[0] = w[1] = w[2] = w[3] = 0;
-            }
-            *reinterpret_cast<uint4 *>(lds.at + row * lds.kPitch + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(p + n * kRows * lds.kPitch) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 };
 
-// Four consecutive steps of one channel: elements at p, p + step, ..., those of
-// steps first .. end - 1 (counted from the first of the four); others read as 0.
-template <bool HALF>
-__device__ __forceinline__ f32x4 load_steps(const void *base, int64_t off, int64_t step, int first, int end)
+// A wave's 16 columns of C steps as results hold them: lane l has column l % 16
+// and, of each 16 steps, 4 (l / 16) .. + 3.  Kept as loaded, so that nothing waits
+// for them before their use.  As above, all loads are under way at once.
+template <bool HALF, int C>
+struct Columns {
+    static constexpr int TT = C / 16;
+    using Elem = typename Num<HALF>::Elem;
+    uint32_t w[TT][HALF ? 2 : 4];
+    // base: the lane's column (one that is there); t0: the chunk's first step
+    __device__ __forceinline__ void load(const Elem *base, int64_t step, int64_t t0, int64_t T)
+    {
+        const int row4 = threadIdx.x % kWave / 16 * 4;
+        if (t0 + C <= T && step == 1) {
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+                const Elem *p = base + t0 + 16 * i + row4;
+                if constexpr (HALF) {
+                    const Words2 v = *reinterpret_cast<const Words2Any *>(p);
+                    w[i][0] = v.x, w[i][1] = v.y;
+                } else {
+                    const Words4 v = *reinterpret_cast<const Words4Any *>(p);
+                    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const int64_t t = t0 + 16 * i + row4;
+            uint32_t e[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const Elem *p = base + min(t + r, T - 1) * step;
+                if constexpr (HALF)
+                    e[r] = *p;
+                else
+                    e[r] = __float_as_uint(*p);
+            }
+            if constexpr (HALF)
+                w[i][0] = e[0] | e[1] << 16, w[i][1] = e[2] | e[3] << 16;
+            else
+                w[i][0] = e[0], w[i][1] = e[1], w[i][2] = e[2], w[i][3] = e[3];
+        }
+    }
+    __device__ __forceinline__ f32x4 get(int i) const
+    {
+        f32x4 x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (HALF)
+                x[r] = __uint_as_float(r % 2 ? w[i][r / 2] & 0xffff0000u : w[i][r / 2] << 16);
+            else
+                x[r] = __uint_as_float(w[i][r]);
+        }
+        return x;
+    }
+};
+// Four values at p, p + step, ...; those of `first` .. `end` - 1 are there.
+__device__ __forceinline__ f32x4 load_four(const float *p, int64_t step, int first, int end)
 {
     f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (first <= 0 && end >= 4 && step == 1) {
-        if constexpr (HALF) {
-            const Words2 w = *reinterpret_cast<const Words2Any *>(static_cast<const uint16_t *>(base) + off);
-            x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
-            x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-            const Words4 w = *reinterpret_cast<const Words4Any *>(static_cast<const float *>(base) + off);
-            x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y);
-            x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-        }
-    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r >= first && r < end) x[r] = load_gate<HALF>(base, off + r * step);
-    }
+    for (int r = 0; r < 4; ++r)
+        if (r >= first && r < end) x[r] = p[r * step];
     return x;
 }
+// Four results to the lane's column: rows t .. t + 3, `step` elements apart, as far
+// as they are rows r0 .. r1 - 1.  whole: they all are.
 template <bool HALF>
-__device__ __forceinline__ void store_steps(void *base, int64_t off, int64_t step, int first, int end, f32x4 x)
+__device__ __forceinline__ void store_column(typename Num<HALF>::Elem *base, int64_t step, int t, int r0, int r1,
+                                             bool whole, f32x4 x)
 {
-    if (first <= 0 && end >= 4 && step == 1) {
+    if (whole && step == 1) {
         if constexpr (HALF) {
             const Words2 w = {bf16_bits(x[0]) | bf16_bits(x[1]) << 16, bf16_bits(x[2]) | bf16_bits(x[3]) << 16};
-            *reinterpret_cast<Words2Any *>(static_cast<uint16_t *>(base) + off) = w;
+            *reinterpret_cast<Words2Any *>(base + t) = w;
         } else {
             const Words4 w = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                               __float_as_uint(x[3])};
-            *reinterpret_cast<Words4Any *>(static_cast<float *>(base) + off) = w;
+            *reinterpret_cast<Words4Any *>(base + t) = w;
         }
     } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (r >= first && r < end) store_gate<HALF>(base, off + r * step, x[r]);
+            if (whole || (t + r >= r0 && t + r < r1)) store_gate<HALF>(base, (t + r) * step, x[r]);
     }
 }
 
@@ -399,20 +573,32 @@ struct StepGates {
     uint64_t cut;  // steps that keep nothing of the state before them
     int rows;      // the chunk's steps
 };
+struct LoadedGates {
+    float g, beta;
+    uint32_t reset;
+};
 template <int C>
-__device__ __forceinline__ StepGates load_gates(const Args &A, int64_t b, int64_t h, int64_t t0)
+__device__ __forceinline__ LoadedGates fetch_gates(const Args &A, int64_t b, int64_t h, int64_t t0)
 {
     const int lane = threadIdx.x % kWave;
     const int64_t t = t0 + lane, at = b * A.gate_b + h * A.gate_h + t * A.gate_t;
-    StepGates s = {0.0f, 0.0f, 0, (int)(A.T - t0 < C ? A.T - t0 : C)};
-    bool cut = false;
-    if (lane < s.rows) {
-        if (A.decay) s.g = A.decay[at];
-        s.beta = A.beta[at];
-        cut = (A.resets && A.resets[b * A.T + t]) || s.g < kForget;
+    LoadedGates l = {0.0f, 0.0f, 0};
+    if (lane < C && t < A.T) {
+        if (A.decay) l.g = A.decay[at];
+        l.beta = A.beta[at];
+        if (A.resets) l.reset = A.resets[b * A.T + t];
     }
-    s.cut = __ballot(cut);
-    return s;
+    return l;
+}
+template <int C>
+__device__ __forceinline__ StepGates use_gates(const Args &A, const LoadedGates &l, int64_t t0)
+{
+    return {l.g, l.beta, __ballot(l.reset != 0 || l.g < kForget), (int)(A.T - t0 < C ? A.T - t0 : C)};
+}
+template <int C>
+__device__ __forceinline__ StepGates load_gates(const Args &A, int64_t b, int64_t h, int64_t t0)
+{
+    return use_gates<C>(A, fetch_gates<C>(A, b, h, t0), t0);
 }
 __device__ __forceinline__ uint64_t steps_below(int n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
 // The first step after r0 that starts a document, or `rows`.
@@ -428,19 +614,32 @@ __device__ __forceinline__ int document_start(uint64_t cut, int r1)
     const uint64_t upto = cut & steps_below(r1);
     return upto ? 63 - __builtin_clzll(upto) : 0;
 }
+// Sums over the lanes up to each lane: by rows of 16, then across them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double x)
+{
+    const uint64_t u = __double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __longlong_as_double((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_upto(double x)
+{
+    x += moved<0x111, 0xf>(x);  // from 1, 2, 4 and 8 lanes below
+    x += moved<0x112, 0xf>(x);
+    x += moved<0x114, 0xf>(x);
+    x += moved<0x118, 0xf>(x);
+    x += moved<0x142, 0xa>(x);  // the row's last lane to the next row
+    x += moved<0x143, 0xc>(x);  // lane 31 to the upper half
+    return x;
+}
 // Sums of the document's log decays (base 2) up to each step, from its first
 // step in the chunk; steps of other documents take the value at their side.
 __device__ __forceinline__ double decay_sum(const StepGates &s, int r0, int r1)
 {
     const int lane = threadIdx.x % kWave;
     const bool mine = lane >= r0 && lane < r1 && !(s.cut >> lane & 1);
-    double G = mine ? (double)s.g * 1.4426950408889634 : 0.0;
-#pragma unroll
-    for (int off = 1; off < kWave; off *= 2) {
-        const double before = __shfl_up(G, off);
-        if (lane >= off) G += before;
-    }
-    return G;
+    return sum_upto(mine ? (double)s.g * 1.4426950408889634 : 0.0);
 }
 // What a visit's steps multiply with, in LDS.
 template <int C>
@@ -466,13 +665,28 @@ __device__ __forceinline__ void write_factors(Factors<C> &F, const StepGates &s,
     }
     if (lane == 0) F.across[0] = ex2((float)total);
 }
-// exp(G_i - G_j)
-template <int C>
-__device__ __forceinline__ float decay_between(const Factors<C> &F, int i, int j)
-{
-    return ex2((F.hi[i] - F.hi[j]) + (F.lo[i] - F.lo[j]));
-}
 __device__ __forceinline__ f32x4 four(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+// exp(G_i - G_j) for i .. i + 3, and for j .. j + 3
+template <int C>
+__device__ __forceinline__ f32x4 decays_from(const Factors<C> &F, int i, int j)
+{
+    const f32x4 hi = four(F.hi + i), lo = four(F.lo + i);
+    const float h = F.hi[j], l = F.lo[j];
+    f32x4 d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = ex2((hi[e] - h) + (lo[e] - l));
+    return d;
+}
+template <int C>
+__device__ __forceinline__ f32x4 decays_to(const Factors<C> &F, int i, int j)
+{
+    const f32x4 hi = four(F.hi + j), lo = four(F.lo + j);
+    const float h = F.hi[i], l = F.lo[i];
+    f32x4 d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = ex2((h - hi[e]) + (l - lo[e]));
+    return d;
+}
 // x where the step is one of the visit's, else 0, whatever x is.
 __device__ __forceinline__ f32x4 only_steps(f32x4 x, int first, int r0, int r1)
 {
@@ -523,52 +737,60 @@ __device__ __forceinline__ f32x4 block_mma(f32x4 c, f32x4 a, f32x4 b)
     return c;
 }
 
-// A wave for a head's chunk.  K K^T on the matrix cores, 32 channels at a
+// Four waves for a head's chunk.  K K^T on the matrix cores, 64 channels at a
 // time.  The 16x16 blocks of the diagonal are inverted column by column, a
 // lane each; then inverses are joined two by two,
 //     [L 0; B R]^-1 = [L^-1 0; -R^-1 B L^-1 R^-1],
-// in float32 products.  (A lane for a whole column of 64 needs every element
-// of A in every lane: 500 wide LDS reads a chunk, or 1600 spilled registers.)
-// Entries between documents are set to zero rather than computed.
+// in float32 products, in the matrix's own place.  (A lane for a whole column of
+// 64 needs every element of A in every lane: 500 wide LDS reads a chunk, or 1600
+// spilled registers.)  Entries between documents are set to zero rather than
+// computed.
+constexpr int kInverseThreads = 4 * kWave;
 template <bool HALF, bool TF>
-__global__ void __launch_bounds__(kWave) delta_inverse_kernel(Args A)
+__global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
 {
-    constexpr int C = Num<HALF>::kChunk, TT = C / 16, kTiles = TT * (TT + 1) / 2, kPitch = C + 4;
-    using Keys = Pieces<HALF, 32, TF, kWave>;
-    // all by columns: A, its inverse, and a product on the way
+    using N = Num<HALF>;
+    using S = Slots<N::kChunk>;
+    constexpr int C = N::kChunk, TT = C / 16, kTiles = TT * (TT + 1) / 2, kPitch = C + 4, kMine = (kTiles + 3) / 4;
+    using Keys = Pieces<HALF, 64, TF, kInverseThreads>;
     __shared__ union {
         typename Keys::Lds keys;
         struct {
-            alignas(16) float a[C * kPitch], m[C * kPitch], p[C / 2 * kPitch];
+            alignas(16) float m[C * kPitch], p[C / 2 * kPitch];  // by columns: A, then its inverse; a product
         };
     } sh;
     __shared__ Factors<C> F;
-    const int lane = threadIdx.x, row4 = 4 * (lane / 16), col = lane % 16;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t item = blockIdx.x, bh = item / A.chunks, n = item % A.chunks;
     const int64_t b = bh / A.Hv, h = bh % A.Hv, t0 = n * C;
-    const StepGates gates = load_gates<C>(A, b, h, t0);
-    const auto *keys = static_cast<const typename Num<HALF>::Elem *>(A.k.p) + b * A.k.b + h / (A.Hv / A.Hk) * A.k.h;
+    const LoadedGates loaded = fetch_gates<C>(A, b, h, t0);
+    const auto *keys = static_cast<const typename N::Elem *>(A.k.p) + b * A.k.b + h / (A.Hv / A.Hk) * A.k.h;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
-    f32x4 acc[kTiles];
+    f32x4 acc[kMine];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) acc[i] = zero;
-    for (int d0 = 0; d0 < A.key; d0 += 32) {
-        Keys raw;
-        raw.load(A.k, keys, d0, t0, A.key, A.T);
+    for (int m = 0; m < kMine; ++m) acc[m] = zero;
+    const int gates_rows = (int)min((int64_t)C, A.T - t0);
+    Keys raw;
+    raw.load(A.k, keys, 0, t0, A.key, A.T, threadIdx.x);
+    for (int d0 = 0; d0 < A.key; d0 += 64) {
         __syncthreads();
-        raw.store(sh.keys, 0, C);
+        raw.store(sh.keys, 0, gates_rows, A.key - d0, threadIdx.x);
+        if (d0 + 64 < A.key) raw.load(A.k, keys, d0 + 64, t0, A.key, A.T, threadIdx.x);
         __syncthreads();
-        typename Num<HALF>::Exact f[TT];
 #pragma unroll
-        for (int i = 0; i < TT; ++i) f[i] = operand<!TF>(sh.keys, 16 * i, 0);
+        for (int m = 0; m < kMine; ++m) {
+            const int p = wave + 4 * m;
+            if (p >= kTiles) break;
+            int i, j;
+            lower_pair(p, i, j);
 #pragma unroll
-        for (int p = 0, i = 0; i < TT; ++i)
-#pragma unroll
-            for (int j = 0; j <= i; ++j, ++p) acc[p] = mma(acc[p], f[i], f[j]);
+            for (int d = 0; d < 64; d += 32)
+                acc[m] = mma(acc[m], operand<!TF>(sh.keys, 16 * i, d), operand<!TF>(sh.keys, 16 * j, d));
+        }
     }
-    // every document's sums by themselves: a number that is not finite stays in its own
-    {
+    const StepGates gates = use_gates<C>(A, loaded, t0);
+    if (wave == 0) {  // every document's sums by themselves: a number that is not finite stays in its own
         const int first = document_start(gates.cut, lane + 1);
         double G = lane < gates.rows && !(gates.cut >> lane & 1) ? (double)gates.g * 1.4426950408889634 : 0.0;
 #pragma unroll
@@ -587,19 +809,21 @@ __global__ void __launch_bounds__(kWave) delta_inverse_kernel(Args A)
         return !(gates.cut & steps_below(i + 1) & ~steps_below(j + 1));
     };
 #pragma unroll
-    for (int p = 0, it = 0; it < TT; ++it)
+    for (int m = 0; m < kMine; ++m) {
+        const int p = wave + 4 * m;
+        if (p >= kTiles) break;
+        int it, jt;
+        lower_pair(p, it, jt);
+        const int i = 16 * it + row4, j = 16 * jt + col;
+        const f32x4 d = decays_from(F, i, j), beta = four(F.beta + i);
+        f32x4 a;
 #pragma unroll
-        for (int jt = 0; jt <= it; ++jt, ++p) {
-            const int i = 16 * it + row4, j = 16 * jt + col;
-            f32x4 a;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                a[r] = i + r > j && joined(i + r, j) ? F.beta[i + r] * acc[p][r] * decay_between(F, i + r, j) : 0.0f;
-            *reinterpret_cast<f32x4 *>(sh.a + j * kPitch + i) = a;
-        }
+        for (int r = 0; r < 4; ++r) a[r] = i + r > j && joined(i + r, j) ? beta[r] * acc[m][r] * d[r] : 0.0f;
+        *reinterpret_cast<f32x4 *>(sh.m + j * kPitch + i) = a;
+    }
     __syncthreads();
-    if (lane < C) {
-        const int first = lane / 16 * 16;
+    if (wave < TT && lane < 16) {
+        const int first = 16 * wave;
         f32x4 m[4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i / 4][i % 4] = i == col ? 1.0f : 0.0f;
@@ -608,7 +832,7 @@ __global__ void __launch_bounds__(kWave) delta_inverse_kernel(Args A)
             if (l < col) m[l / 4][l % 4] = 0.0f;  // also where an earlier document made it a NaN
 #pragma unroll
             for (int i = (l + 1) / 4; i < 4; ++i) {
-                const f32x4 a = four(sh.a + (first + l) * kPitch + first + 4 * i);
+                const f32x4 a = four(sh.m + (first + l) * kPitch + first + 4 * i);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     if (4 * i + r > l) m[i][r] = fmaf_(-a[r], m[l / 4][l % 4], m[i][r]);
@@ -618,457 +842,815 @@ __global__ void __launch_bounds__(kWave) delta_inverse_kernel(Args A)
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) m[i][r] = 4 * i + r < col ? 0.0f : m[i][r];
-            *reinterpret_cast<f32x4 *>(sh.m + lane * kPitch + first + 4 * i) = m[i];
+            *reinterpret_cast<f32x4 *>(sh.m + (first + col) * kPitch + first + 4 * i) = m[i];
         }
     }
+    // inverses of `size` blocks joined: a wave for a tile of the block below the diagonal
 #pragma unroll
-    for (int size = 1; size < TT; size *= 2)  // 16x16 blocks of one inverse
-#pragma unroll
-        for (int at = 0; at < TT; at += 2 * size) {
-            __syncthreads();
-            // p = B L^-1, rows of the right inverse's blocks
-#pragma unroll
-            for (int i = 0; i < size; ++i)
-#pragma unroll
-                for (int j = 0; j < size; ++j) {
-                    f32x4 c = zero;
-#pragma unroll
-                    for (int l = j; l < size; ++l)
-                        c = block_mma(c, block_operand<false>(sh.a, kPitch, 16 * (at + size + i), 16 * (at + l)),
-                                      block_operand<true>(sh.m, kPitch, 16 * (at + j), 16 * (at + l)));
-                    *reinterpret_cast<f32x4 *>(sh.p + (16 * j + col) * kPitch + 16 * i + row4) = c;
-                }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < size; ++i)
-#pragma unroll
-                for (int j = 0; j < size; ++j) {
-                    f32x4 c = zero;
-#pragma unroll
-                    for (int l = 0; l <= i; ++l)
-                        c = block_mma(c, block_operand<false>(sh.m, kPitch, 16 * (at + size + i), 16 * (at + size + l)),
-                                      block_operand<true>(sh.p, kPitch, 16 * j, 16 * l));
-                    *reinterpret_cast<f32x4 *>(sh.m + (16 * (at + j) + col) * kPitch + 16 * (at + size + i) + row4) = -c;
-                }
+    for (int size = 1; size < TT; size *= 2) {
+        const int per = size * size, at = wave / per * 2 * size, i = wave % per / size, j = wave % size;
+        const bool mine = at < TT;
+        __syncthreads();
+        if (mine) {
+            f32x4 c = zero;
+            for (int l = j; l < size; ++l)
+                c = block_mma(c, block_operand<false>(sh.m, kPitch, 16 * (at + size + i), 16 * (at + l)),
+                              block_operand<true>(sh.m, kPitch, 16 * (at + j), 16 * (at + l)));
+            *reinterpret_cast<f32x4 *>(sh.p + (16 * (at / 2 + j) + col) * kPitch + 16 * i + row4) = c;
         }
+        __syncthreads();
+        if (mine) {
+            f32x4 c = zero;
+            for (int l = 0; l <= i; ++l)
+                c = block_mma(c, block_operand<false>(sh.m, kPitch, 16 * (at + size + i), 16 * (at + size + l)),
+                              block_operand<true>(sh.p, kPitch, 16 * (at / 2 + j), 16 * l));
+            *reinterpret_cast<f32x4 *>(sh.m + (16 * (at + j) + col) * kPitch + 16 * (at + size + i) + row4) = -c;
+        }
+    }
     __syncthreads();
-    // rows (and for the backward pass columns) of 8 elements a lane
-    const auto put = [&](void *out, bool by_columns) {
-        for (int u = lane; u < C * C / 8; u += kWave) {
-            const int row = u / (C / 8), c8 = u % (C / 8) * 8;
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = by_columns ? c8 + e : row, j = by_columns ? row : c8 + e;
-                x[e] = i >= j && joined(i, j) ? sh.m[j * kPitch + i] : 0.0f;
-            }
-            if constexpr (HALF) {
-                const Bf::Wide w = split(x, Bf::Wide());
-                __bf16 *p = static_cast<__bf16 *>(out) + 2 * item * C * C + row * C + c8;
-                *reinterpret_cast<bf16x8 *>(p) = w.hi;
-                *reinterpret_cast<bf16x8 *>(p + C * C) = w.lo;
-            } else {
-                float *p = static_cast<float *>(out) + item * C * C + row * C + c8;
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) *reinterpret_cast<f32x4 *>(p + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
-            }
+    // as operands: its own rows, and for the backward pass its columns
+    for (int f = wave; f < (A.inverse_t ? 2 : 1) * S::kCount; f += 4) {
+        const bool columns = f >= S::kCount;
+        const int s = columns ? f - S::kCount : f;
+        int rt = s, kt = 0;
+        if constexpr (C == 64) {
+            rt = columns ? (s < 4 ? s / 2 : s - 2) : s < 2 ? s : s / 2 + 1;
+            kt = columns ? (s < 4 ? s % 2 : 1) : s < 2 ? 0 : s % 2;
         }
-    };
-    put(A.inverse, false);
-    if (A.inverse_t) put(A.inverse_t, true);
-}
-// An operand from such a matrix in memory.
-__device__ __forceinline__ Bf::Wide operand_of(const void *m, int64_t item, int i0, int k0, Bf)
-{
-    constexpr int C = Bf::kChunk;
-    const int lane = threadIdx.x % kWave;
-    const __bf16 *p = static_cast<const __bf16 *>(m) + 2 * item * C * C + (i0 + lane % 16) * C + k0 + 8 * (lane / 16);
-    return {*reinterpret_cast<const bf16x8 *>(p), *reinterpret_cast<const bf16x8 *>(p + C * C)};
-}
-__device__ __forceinline__ Fl::Wide operand_of(const void *m, int64_t item, int i0, int k0, Fl)
-{
-    constexpr int C = Fl::kChunk;
-    const int lane = threadIdx.x % kWave;
-    const float *p = static_cast<const float *>(m) + item * C * C + (i0 + lane % 16) * C + k0 + 8 * (lane / 16);
-    Fl::Wide r;
+        const int row = 16 * rt + col;
+        float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-        const f32x4 v = four(p + j);
-        r.x[j] = v[0], r.x[j + 1] = v[1], r.x[j + 2] = v[2], r.x[j + 3] = v[3];
+        for (int e = 0; e < 8; ++e) {
+            const int k = 32 * kt + row4 + (e < 4 ? e : 12 + e), i = columns ? k : row, j = columns ? row : k;
+            x[e] = i >= j && joined(i, j) ? sh.m[j * kPitch + i] : 0.0f;
+        }
+        Fragment *const out = (columns ? A.inverse_t : A.inverse) + item * S::kCount + s;
+        store_fragment(*out, split(x, typename N::Wide()));
     }
-    return r;
 }
 
-// A state's tiles in a wave's registers: tile wave + 8 n, of DT x VT.
-template <int DK, int VB>
+// A state's 16 columns in a wave's registers, DT tiles of 16 channels.
+template <int DK>
 struct State {
-    static constexpr int DT = DK / 16, VT = VB / 16, kCount = (DT * VT + kWaves - 1) / kWaves;
-    f32x4 s[kCount];
-    static __device__ __forceinline__ bool tile(int n, int wave, int &d0, int &v0)
-    {
-        const int i = wave + kWaves * n;
-        d0 = 16 * (i / VT);
-        v0 = 16 * (i % VT);
-        return i < DT * VT;
-    }
+    static constexpr int DT = DK / 16;
+    f32x4 s[DT];
     __device__ __forceinline__ void zero()
     {
 #pragma unroll
-        for (int n = 0; n < kCount; ++n) s[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < DT; ++i) s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    // rows of `pitch` values, those from `key` and `value` on not there
-    __device__ __forceinline__ void load(const float *p, int wave, int lane, int64_t v_first, int key, int64_t value)
+    // S <- across S + channels times w
+    template <class Exact, class Wide, int KC>
+    __device__ __forceinline__ void advance(float across, const Exact (&k)[KC][DT], const Wide (&w)[KC])
     {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[d][r] *= across;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) mma_rows(s, k[i], w[i]);
+    }
+    // rows of `pitch` values; channels from `key` on, and all without `here`, are not there
+    __device__ __forceinline__ void load(const float *p, int64_t v, bool here, int key, int64_t pitch)
+    {
+        const int row4 = threadIdx.x % kWave / 16 * 4;
         zero();
+        if (!here) return;
 #pragma unroll
-        for (int n = 0; n < kCount; ++n) {
-            int d0, v0;
-            if (!tile(n, wave, d0, v0)) break;
-            const int64_t v = v_first + v0 + lane % 16;
+        for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = d0 + 4 * (lane / 16) + r;
-                if (d < key && v < value) s[n][r] = p[d * value + v];
-            }
-        }
+            for (int r = 0; r < 4; ++r)
+                if (16 * i + row4 + r < key) s[i][r] = p[(16 * i + row4 + r) * pitch + v];
     }
-    __device__ __forceinline__ void store(float *p, int wave, int lane, int64_t v_first, int key, int64_t value,
-                                          int64_t pitch) const
+    __device__ __forceinline__ void store(float *p, int64_t v, bool here, int key, int64_t pitch) const
     {
+        const int row4 = threadIdx.x % kWave / 16 * 4;
+        if (!here) return;
 #pragma unroll
-        for (int n = 0; n < kCount; ++n) {
-            int d0, v0;
-            if (!tile(n, wave, d0, v0)) break;
-            const int64_t v = v_first + v0 + lane % 16;
+        for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = d0 + 4 * (lane / 16) + r;
-                if (d < key && v < value) p[d * pitch + v] = s[n][r];
-            }
-        }
-    }
-    template <bool HALF>
-    __device__ __forceinline__ void to_lds(WideTile<HALF, VB, DK> &t, int wave, int lane) const
-    {
-#pragma unroll
-        for (int n = 0; n < kCount; ++n) {
-            int d0, v0;
-            if (!tile(n, wave, d0, v0)) break;
-            store4(t, v0 + lane % 16, d0 + 4 * (lane / 16), s[n]);
-        }
+            for (int r = 0; r < 4; ++r)
+                if (16 * i + row4 + r < key) p[(16 * i + row4 + r) * pitch + v] = s[i][r];
     }
 };
 
+// Products whose operands are read from LDS all at once, before the first is used:
+// left to itself the compiler reads two, waits for the LDS and multiplies.
+// x_t = the rows 16 t .. of a tile of steps times what `s` holds, over the channels.
+template <bool ALONG, class In, class Wide, int TT, int KD>
+__device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide (&s)[KD])
+{
+    constexpr int B = KD < 4 ? KD : 4;  // the registers of 16 operands at a time
+    decltype(operand<ALONG>(tile, 0, 0)) k[B][TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) x[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int d0 = 0; d0 < KD; d0 += B) {
+#pragma unroll
+        for (int d = 0; d < B; ++d)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) k[d][t] = operand<ALONG>(tile, 16 * t, 32 * (d0 + d));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < B; ++d) mma_rows(x, k[d], s[d0 + d]);
+        if (d0 + B < KD) __builtin_amdgcn_sched_barrier(0);
+    }
+    settle(x);
+}
+// x_t = the rows of a triangular matrix [C][C] times `s`; LOWER, or its transpose
+template <bool LOWER, int C, class Wide, int TT, int KC>
+__device__ __forceinline__ void triangle_times(f32x4 (&x)[TT], const Wide (&m)[Slots<C>::kCount], const Wide (&s)[KC])
+{
+    using Sl = Slots<C>;
+    using P = Product<Wide, Wide>;
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+#pragma unroll
+        for (int i = 0; i < P::kParts; ++i)
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+                if (LOWER ? Sl::in_lower(t, k) : Sl::in_upper(t, k))
+                    x[t] = P::part(i, x[t], m[LOWER ? Sl::lower(t, k) : Sl::upper(t, k)], s[k]);
+    settle(x);
+}
+// The operands of a tile's channels, their terms the steps.
+template <bool ALONG, class In, class Exact, int DT, int KC>
+__device__ __forceinline__ void read_channels(Exact (&k)[KC][DT], const In &tile)
+{
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int s = 0; s < KC; ++s) k[s][d] = operand<ALONG>(tile, 16 * d, 32 * s);
+}
+
 // ------------------------------------------------------------- the chain ---
 
-// A workgroup for a head and VB columns, chunk after chunk.  The products'
-// tiles are dealt to the waves: a wave that owns a tile of [C][VB] computes
-// k^T S, q^T S, then R, W and the output of it, all of them the tiles of P and
-// of the state.  STATES: for the backward pass, the states before each chunk
-// and W instead of the outputs.
-template <bool HALF, int DK, int VB, bool TF, bool STATES>
-__global__ void __launch_bounds__(kThreads) delta_chain_kernel(Args A)
+// The chains' waves.  A workgroup has a head and 16 NC columns of the values: NC
+// waves with 16 columns of the state each in their registers, and as many
+// helpers, each beside one of them.  A wave multiplies what it has computed
+// from its registers, so between two chunks only the state itself is waited
+// for: the helpers bring the next keys and queries to LDS and take over the
+// products that the state does not need.  A `visit` is a chunk, or one document
+// of it.
+
+// A workgroup's head and columns.
+struct Place {
+    int64_t bh, b, h, hk;
+    int first;  // its first 16 columns
+};
+template <int NC>
+__device__ __forceinline__ Place place_of(const Args &A)
 {
-    using N = Num<HALF>;
-    constexpr int C = N::kChunk, TT = C / 16, VT = VB / 16, kOwners = TT * VT;
-    using In = Pieces<HALF, DK, TF, kThreads>;
-    using St = State<DK, VB>;
-    static_assert(kOwners <= kWaves, "a tile a wave");
-    __shared__ typename In::Lds keys, queries;
-    __shared__ WideTile<HALF, VB, DK> state;
-    __shared__ WideTile<HALF, VB, C> rhs, write, carry;
-    __shared__ WideTile<HALF, C, C> scores;
-    __shared__ Factors<C> F;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
-    int64_t bh;
+    Place p;
     int block;
-    head_and_block(A.B * A.Hv, A.blocks, bh, block);
-    const int64_t b = bh / A.Hv, h = bh % A.Hv, hk = h / (A.Hv / A.Hk), v_first = (int64_t)block * VB;
-    const bool owner = wave < kOwners;
-    const int tt = 16 * (wave / VT), vt = 16 * (wave % VT);  // the owner's tile
-    const int64_t v = v_first + vt + col;
-    const bool has_v = owner && v < A.value;
-    const int64_t v_at = b * A.v.b + h * A.v.h + v * A.v.d, o_at = b * A.o.b + h * A.o.h + v * A.o.d;
-    using Elem = typename N::Elem;
-    const Elem *const kb = static_cast<const Elem *>(A.k.p) + b * A.k.b + hk * A.k.h;
-    const Elem *const qb = static_cast<const Elem *>(A.q.p) + b * A.q.b + hk * A.q.h;
+    head_and_block(A.B * A.Hv, A.blocks, p.bh, block);
+    p.b = p.bh / A.Hv;
+    p.h = p.bh % A.Hv;
+    p.hk = p.h / (A.Hv / A.Hk);
+    p.first = block * NC;
+    return p;
+}
+// Of the operands of a triangular matrix [C][C], those that helper c of NC makes.
+template <int C, int NC>
+__device__ __forceinline__ int first_slot(int c)
+{
+    constexpr int kCount = Slots<C>::kCount;
+    if constexpr (kCount == 6 && NC == 4)
+        return c < 2 ? 2 * c : 2 + c;  // two of one or two tiles, then one of two
+    else
+        return kCount * c / NC;
+}
 
-    St S;
-    S.zero();
-    if (A.h0) S.load(A.h0 + bh * A.key * A.value, wave, lane, v_first, A.key, A.value);
-    S.to_lds(state, wave, lane);
-    if constexpr (!STATES) clear(scores);
-    for (int64_t n = 0; n < A.chunks; ++n) {
-        const int64_t t0 = n * C, item = bh * A.chunks + n;
-        const StepGates gates = load_gates<C>(A, b, h, t0);
-        In k_raw;
-        [[maybe_unused]] In q_raw;
-        k_raw.load(A.k, kb, 0, t0, A.key, A.T);
-        if constexpr (!STATES) q_raw.load(A.q, qb, 0, t0, A.key, A.T);
-        if constexpr (STATES)
-            S.store(A.states + item * DK * A.value_pad, wave, lane, v_first, DK, A.value_pad, A.value_pad);
-        for (int r0 = 0; r0 < gates.rows;) {
-            const int r1 = document_end(gates.cut, r0, gates.rows);
-            if (gates.cut >> r0 & 1) {
-                S.zero();
-                S.to_lds(state, wave, lane);
-            }
-            k_raw.store(keys, r0, r1);
-            if constexpr (!STATES) q_raw.store(queries, r0, r1);
-            if (wave == 0) write_factors(F, gates, r0, r1);
-            f32x4 value = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (has_v)
-                value = load_steps<HALF>(A.v.p, v_at + (t0 + tt + row4) * A.v.t, A.v.t, r0 - tt - row4,
-                                         r1 - tt - row4);
-            __syncthreads();
-
-            f32x4 ks = {0.0f, 0.0f, 0.0f, 0.0f};
-            [[maybe_unused]] f32x4 qs = ks;
-            if (owner) {
-#pragma unroll
-                for (int d = 0; d < DK; d += 32) {
-                    const auto s = operand<true>(state, vt, d);
-                    ks = mma(ks, operand<!TF>(keys, tt, d), s);
-                    if constexpr (!STATES) qs = mma(qs, operand<!TF>(queries, tt, d), s);
-                }
-                const f32x4 start = four(F.start + tt + row4), beta = four(F.beta + tt + row4);
-                f32x4 r;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    r[e] = beta[e] * fmaf_(-start[e], ks[e], value[e]);
-                    if constexpr (!STATES) qs[e] *= A.scale * start[e];
-                }
-                store4(rhs, vt + col, tt + row4, only_steps(r, tt + row4, r0, r1));
-            }
-            if constexpr (!STATES) {
-                // P by rows of t: its tile (s, t) as keys times queries, four s side by side
-                for (int p = wave; p < TT * (TT + 1) / 2; p += kWaves) {
-                    int ti, si;
-                    lower_pair(p, ti, si);
-                    ti *= 16, si *= 16;
-                    f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int d = 0; d < DK; d += 32) c = mma(c, operand<!TF>(keys, si, d), operand<!TF>(queries, ti, d));
-                    const int t = ti + col, s = si + row4;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e] = s + e <= t ? A.scale * c[e] * decay_between(F, t, s + e) : 0.0f;
-                    store4(scores, t, s, c);
-                }
-            }
-            __syncthreads();
-
-            if (owner) {
-                f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < C; s += 32)
-                    if (s <= tt) w = mma(w, operand_of(A.inverse, item, tt, s, N()), operand<true>(rhs, vt, s));
-                w = only_steps(w, tt + row4, r0, r1);
-                const f32x4 end = four(F.end + tt + row4);
-                if constexpr (STATES) {
-                    float *p = A.w + (item * C + tt + row4) * A.value_pad + v_first + vt + col;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (tt + row4 + e >= r0 && tt + row4 + e < r1) p[e * A.value_pad] = w[e];
-                } else {
-                    store4(write, vt + col, tt + row4, w);
-                }
-                f32x4 c;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = end[e] * w[e];
-                store4(carry, vt + col, tt + row4, only_steps(c, tt + row4, r0, r1));
-            }
-            __syncthreads();
-
-            if constexpr (!STATES) {
-                if (owner) {
-#pragma unroll
-                    for (int s = 0; s < C; s += 32)
-                        if (s <= tt) qs = mma(qs, operand<true>(scores, tt, s), operand<true>(write, vt, s));
-                    if (has_v)
-                        store_steps<false>(A.o.p, o_at + (t0 + tt + row4) * A.o.t, A.o.t, r0 - tt - row4,
-                                           r1 - tt - row4, qs);
-                }
-            }
-            const float across = F.across[0];
-#pragma unroll
-            for (int i = 0; i < St::kCount; ++i) {
-                int d0, v0;
-                if (!St::tile(i, wave, d0, v0)) break;
-                f32x4 c;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = across * S.s[i][e];
-#pragma unroll
-                for (int s = 0; s < C; s += 32) c = mma(c, operand<TF>(keys, d0, s), operand<true>(carry, v0, s));
-                S.s[i] = c;
-            }
-            S.to_lds(state, wave, lane);
-            __syncthreads();
-            r0 = r1;
+// A visit: steps r0 .. r1 - 1 of chunk n (-1: no more).
+struct Visit {
+    int n, r0, r1, flags;
+    static constexpr int kFresh = 1, kEnters = 2, kLeaves = 4;  // starts a document; the chunk's first, its last
+    __device__ __forceinline__ bool here() const { return n >= 0; }
+    __device__ __forceinline__ bool fresh() const { return flags & kFresh; }
+    __device__ __forceinline__ bool enters() const { return flags & kEnters; }
+    __device__ __forceinline__ bool leaves() const { return flags & kLeaves; }
+};
+__device__ __forceinline__ Visit read_visit(const Visit &v)
+{
+    return {__builtin_amdgcn_readfirstlane(v.n), __builtin_amdgcn_readfirstlane(v.r0),
+            __builtin_amdgcn_readfirstlane(v.r1), __builtin_amdgcn_readfirstlane(v.flags)};
+}
+// The wave that finds the visits one after the other, for all of its workgroup.
+template <int C, bool BACK>
+struct Planner {
+    int n, r0, r1;
+    StepGates gates;
+    LoadedGates next;  // of the chunk after this one
+    __device__ __forceinline__ bool beyond(const Args &A) const { return BACK ? n > 0 : n + 1 < A.chunks; }
+    __device__ __forceinline__ void start(const Args &A, const Place &at)
+    {
+        n = BACK ? (int)A.chunks - 1 : 0;
+        gates = load_gates<C>(A, at.b, at.h, (int64_t)n * C);
+        enter(A, at);
+    }
+    __device__ __forceinline__ void enter(const Args &A, const Place &at)
+    {
+        r0 = BACK ? document_start(gates.cut, gates.rows) : 0;
+        r1 = BACK ? gates.rows : document_end(gates.cut, 0, gates.rows);
+        if (beyond(A)) next = fetch_gates<C>(A, at.b, at.h, (int64_t)(BACK ? n - 1 : n + 1) * C);
+    }
+    __device__ __forceinline__ void advance(const Args &A, const Place &at)
+    {
+        if (BACK ? r0 > 0 : r1 < gates.rows) {
+            if (BACK)
+                r1 = r0, r0 = document_start(gates.cut, r1);
+            else
+                r0 = r1, r1 = document_end(gates.cut, r0, gates.rows);
+        } else if (beyond(A)) {
+            n += BACK ? -1 : 1;
+            gates = use_gates<C>(A, next, (int64_t)n * C);
+            enter(A, at);
+        } else {
+            n = -1;
         }
     }
-    if constexpr (!STATES)
-        if (A.last)
-            S.store(A.last + bh * A.key * A.value, wave, lane, v_first, A.key, A.value, A.value);
+    // to LDS: the visit, and what its steps multiply with
+    __device__ __forceinline__ void write(Visit &v, Factors<C> &F) const
+    {
+        if (n >= 0) write_factors(F, gates, r0, r1);
+        const bool first = BACK ? r1 == gates.rows : r0 == 0, last = BACK ? r0 == 0 : r1 == gates.rows;
+        if (threadIdx.x % kWave == 0)
+            v = {n, r0, r1,
+                 (gates.cut >> r0 & 1 ? Visit::kFresh : 0) | (first ? Visit::kEnters : 0) | (last ? Visit::kLeaves : 0)};
+    }
+};
+
+// What the chains' waves share: keys and queries of two visits (with 256
+// channels there is room for one), their factors, and what passes between a
+// state's wave and its helper.
+template <bool HALF, int DK, int NC, bool TF>
+struct Staged {
+    static constexpr int C = Num<HALF>::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32;
+    static constexpr bool kTwo = DK < 256;
+    using In = Pieces<HALF, DK, TF, NC * kWave>;
+    typename In::Lds keys[kTwo ? 2 : 1];
+    Factors<C> factors[2];
+    Visit visits[2];
+    __device__ __forceinline__ const typename In::Lds &keys_of(int buffer) const { return keys[kTwo ? buffer : 0]; }
+};
+template <bool HALF, int DK, int NC, bool TF>
+struct Forward : Staged<HALF, DK, NC, TF> {
+    using Base = Staged<HALF, DK, NC, TF>;
+    typename Base::In::Lds queries;
+    Fragment scores[Slots<Base::C>::kCount], state[NC][Base::KD], write[NC][Base::KC];
+};
+template <bool HALF, int DK, int NC, bool TF>
+struct Backward : Staged<HALF, DK, NC, TF> {
+    using Base = Staged<HALF, DK, NC, TF>;
+    typename Base::In::Lds queries[Base::kTwo ? 2 : 1];
+    f32x4 by_scores[NC][Base::TT][kWave], by_queries[NC][Base::DT][kWave];
+    __device__ __forceinline__ const typename Base::In::Lds &queries_of(int buffer) const
+    {
+        return queries[Base::kTwo ? buffer : 0];
+    }
+};
+template <bool HALF>
+__device__ __forceinline__ const typename Num<HALF>::Elem *head_of(const Plane &x, int64_t b, int64_t h)
+{
+    return static_cast<const typename Num<HALF>::Elem *>(x.p) + b * x.b + h * x.h;
+}
+
+// Forward.  A helper: P, q^T S and the outputs, from S and W as operands in LDS.
+// Without QUERIES it only brings the keys.
+template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
+__device__ __forceinline__ void chain_helper(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+{
+    using N = Num<HALF>;
+    using Wide = typename N::Wide;
+    using In = Pieces<HALF, DK, TF, NC * kWave>;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, KD = DK / 32;
+    using Sl = Slots<C>;
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16, tid = c * kWave + lane;
+    const int64_t v = 16 * (int64_t)(at.first + c) + col;
+    const bool has_v = v < A.value;
+    float *const o = static_cast<float *>(A.o.p) + at.b * A.o.b + at.h * A.o.h + v * A.o.d;
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    In k_raw;
+    [[maybe_unused]] In q_raw;
+    const auto load = [&](int64_t n) {
+        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+        if constexpr (QUERIES) q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+    };
+    const auto stage = [&](int buffer, int r0, int r1) {
+        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
+        if constexpr (QUERIES) q_raw.store(sh.queries, r0, r1, A.key, tid);
+    };
+    Planner<C, false> plan;
+    load(0);
+    if (c == NC - 1) {
+        plan.start(A, at);
+        plan.write(sh.visits[0], sh.factors[0]);
+    }
+    __syncthreads();
+    Visit now = read_visit(sh.visits[0]);
+    stage(0, now.r0, now.r1);
+    load(now.leaves() && A.chunks > 1 ? 1 : 0);
+    __syncthreads();
+    for (int buffer = 0; now.here(); buffer ^= 1) {
+        const int64_t t0 = (int64_t)now.n * C;
+        if (c == NC - 1) {
+            plan.advance(A, at);
+            plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
+        }
+        [[maybe_unused]] f32x4 out[TT];
+        if constexpr (QUERIES) {
+            const Factors<C> &F = sh.factors[buffer];
+            const auto &K = sh.keys_of(buffer);
+            // P, its tile (s, t) as keys times queries: row t of the operand, four s
+            for (int s = first_slot<C, NC>(c); s < first_slot<C, NC>(c + 1); ++s) {
+                int tt = s, ss = 0;
+                if constexpr (C == 64) {
+                    tt = s < 2 ? s : s / 2 + 1;
+                    ss = s < 2 ? 0 : s % 2;
+                }
+                f32x4 p[2] = {zero, zero};
+                typename N::Exact q[KD], k[2][KD];
+#pragma unroll
+                for (int d = 0; d < KD; ++d) {
+                    q[d] = operand<!TF>(sh.queries, 16 * tt, 32 * d);
+                    k[0][d] = operand<!TF>(K, 32 * ss, 32 * d);
+                    k[1][d] = operand<!TF>(K, 32 * ss + 16, 32 * d);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < KD; ++d)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) p[i] = mma(p[i], k[i][d], q[d]);
+                const int t = 16 * tt + col;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = 32 * ss + 16 * i + row4;
+                    const f32x4 d = decays_to(F, t, j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[i][e] = j + e <= t ? A.scale * p[i][e] * d[e] : 0.0f;
+                }
+                store_fragment(sh.scores[s], stacked<HALF>(p[0], p[1]));
+            }
+            Wide s[KD];
+#pragma unroll
+            for (int d = 0; d < KD; ++d) s[d] = load_fragment(sh.state[c][d], N());
+            times<!TF>(out, sh.queries, s);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const f32x4 start = four(F.start + 16 * t + row4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[t][e] *= A.scale * start[e];
+            }
+        }
+        __syncthreads();
+        const Visit then = read_visit(sh.visits[buffer ^ 1]);
+        const auto prepare = [&]() {
+            if (!then.here()) return;
+            stage(buffer ^ 1, then.r0, then.r1);
+            load(then.leaves() && then.n + 1 < A.chunks ? then.n + 1 : then.n);
+        };
+        if constexpr (QUERIES) {
+            Wide x[KC], p[Sl::kCount];
+#pragma unroll
+            for (int s = 0; s < KC; ++s) x[s] = load_fragment(sh.write[c][s], N());
+#pragma unroll
+            for (int s = 0; s < Sl::kCount; ++s) p[s] = load_fragment(sh.scores[s], N());
+            if (sh.kTwo) prepare();
+            triangle_times<true, C>(out, p, x);
+            const bool whole = now.r0 == 0 && now.r1 == C;
+            if (has_v)
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    store_column<false>(o + t0 * A.o.t, A.o.t, 16 * t + row4, now.r0, now.r1, whole, out[t]);
+        } else {
+            if (sh.kTwo) prepare();
+        }
+        if (!sh.kTwo) {
+            __syncthreads();
+            prepare();
+        }
+        __syncthreads();
+        now = then;
+    }
+}
+// A state's wave: k^T S, R, W, S'.  OUTPUT: S and W for the helper, and the last
+// state; else for the backward pass, the states before each chunk and W to memory.
+template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
+__device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+{
+    using N = Num<HALF>;
+    using Wide = typename N::Wide;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32;
+    using Sl = Slots<C>;
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const int64_t v = 16 * (int64_t)(at.first + c) + col;
+    const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
+    State<DK> S;
+    Wide operands[KD], inverse[Sl::kCount];
+    Columns<HALF, C> value;
+    const auto *const values = head_of<HALF>(A.v, at.b, at.h) + min(v, (int64_t)A.value - 1) * A.v.d;
+    const auto load_value = [&](int64_t n) { value.load(values, A.v.t, n * C, A.T); };
+    const auto load_inverse = [&](int64_t n) {
+#pragma unroll
+        for (int s = 0; s < Sl::kCount; ++s)
+            inverse[s] = load_fragment(A.inverse[(at.bh * A.chunks + n) * Sl::kCount + s], N());
+    };
+    const auto make_operands = [&]() {
+#pragma unroll
+        for (int d = 0; d < KD; ++d) {
+            operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
+            if constexpr (OUTPUT) store_fragment(sh.state[c][d], operands[d]);
+        }
+    };
+    const auto keep = [&](int64_t n) {
+        S.store(A.states + (at.bh * A.chunks + n) * DK * A.value_pad, v, in_row, DK, A.value_pad);
+    };
+
+    S.load(A.h0 + at.bh * A.key * A.value, v, A.h0 && has_v, A.key, A.value);
+    load_value(0);
+    load_inverse(0);
+    if constexpr (!OUTPUT) keep(0);
+    __syncthreads();
+    Visit now = read_visit(sh.visits[0]);
+    if (now.fresh()) S.zero();
+    make_operands();
+    __syncthreads();
+    for (int buffer = 0; now.here(); buffer ^= 1) {
+        const Factors<C> &F = sh.factors[buffer];
+        const auto &K = sh.keys_of(buffer);
+        const bool whole = now.r0 == 0 && now.r1 == C;
+        // what the next visit reads, also where it is what this one has: a load that
+        // may not be under way would have everything behind it waited for
+        const int64_t after = now.leaves() && now.n + 1 < A.chunks ? now.n + 1 : now.n;
+        f32x4 x[TT];
+        times<!TF>(x, K, operands);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const f32x4 start = four(F.start + 16 * t + row4), beta = four(F.beta + 16 * t + row4);
+            const f32x4 val = value.get(t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] = beta[e] * fmaf_(-start[e], x[t][e], val[e]);
+        }
+        if (!whole || !all_v)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, has_v ? now.r0 : C, now.r1);
+        load_value(after);
+        typename N::Exact kt[KC][DT];
+        read_channels<TF>(kt, K);
+        Wide rhs[KC];
+#pragma unroll
+        for (int s = 0; s < KC; ++s) rhs[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) x[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        triangle_times<true, C>(x, inverse, rhs);
+        if (!whole)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        load_inverse(after);
+        if constexpr (OUTPUT) {
+#pragma unroll
+            for (int s = 0; s < KC; ++s) store_fragment(sh.write[c][s], stacked<HALF>(x[2 * s], x[2 * s + 1]));
+        } else {
+            if (in_row)
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    store_column<false>(A.w + (at.bh * A.chunks + now.n) * C * A.value_pad + v, A.value_pad, 16 * t + row4,
+                                        now.r0, now.r1, whole, x[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const f32x4 end = four(F.end + 16 * t + row4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] *= end[e];
+            if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        }
+        Wide carry[KC];
+#pragma unroll
+        for (int s = 0; s < KC; ++s) carry[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+        __syncthreads();
+        const Visit then = read_visit(sh.visits[buffer ^ 1]);
+        const float across = F.across[0];
+        S.advance(across, kt, carry);
+        if (then.here()) {
+            if constexpr (!OUTPUT)
+                if (then.enters()) keep(then.n);
+            if (then.fresh()) S.zero();
+            make_operands();
+        }
+        if (!sh.kTwo) __syncthreads();
+        __syncthreads();
+        now = then;
+    }
+    if constexpr (OUTPUT)
+        if (A.last) S.store(A.last + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+}
+template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
+__global__ void __launch_bounds__(2 * NC * kWave) delta_chain_kernel(Args A)
+{
+    __shared__ Forward<HALF, DK, NC, TF> sh;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Place at = place_of<NC>(A);
+    if (A.chunks == 0) {  // the state goes through
+        State<DK> S;
+        const int64_t v = 16 * (int64_t)(at.first + wave) + threadIdx.x % 16;
+        const bool here = wave < NC && v < A.value && A.last;
+        S.load(A.h0 + at.bh * A.key * A.value, v, here && A.h0, A.key, A.value);
+        S.store(A.last + at.bh * A.key * A.value, v, here, A.key, A.value);
+        return;
+    }
+    if (wave < NC)
+        chain_state<HALF, DK, NC, TF, OUTPUT>(A, sh, at, wave);
+    else
+        chain_helper<HALF, DK, NC, TF, OUTPUT>(A, sh, at, wave - NC);
+}
+
+// Sums over the 16 lanes of a group, of M values each: at the end a lane holds
+// the sum of value `which`, for M = 8 two lanes the same one.  Half of the values
+// go to the neighbour at each step.
+template <int M>
+__device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
+{
+    static_assert(M == 16 || M == 8, "one or two lanes a value");
+    const int lane = threadIdx.x % kWave;
+    which = 0;
+    const auto halve = [&](auto half, int bit) {
+        constexpr int m = decltype(half)::value;
+        const bool upper = lane & bit;
+        which += upper ? m : 0;
+#pragma unroll
+        for (int i = 0; i < m; ++i) x[i] = (upper ? x[i + m] : x[i]) + __shfl_xor(upper ? x[i] : x[i + m], bit);
+    };
+    if constexpr (M == 16) {
+        halve(std::integral_constant<int, 8>(), 8);
+    }
+    halve(std::integral_constant<int, 4>(), 1);
+    halve(std::integral_constant<int, 2>(), 2);
+    halve(std::integral_constant<int, 1>(), 4);
+    if constexpr (M == 8) x[0] += __shfl_xor(x[0], 8);
+    return x[0];
 }
 
 // The chain backwards: the gradient of the state, from the last chunk to the
-// first, and X, the gradient of R.  Writes the state's gradient behind each
-// chunk, X, dV = b X and the rows' sums of X V over the block's columns.
-template <bool HALF, int DK, int VB, bool TF>
-__global__ void __launch_bounds__(kThreads) delta_back_kernel(Args A)
+// first, and X, the gradient of R.  A helper: P^T dO, and scale (exp(G) Q)^T dO,
+// which joins the state a visit later.
+template <bool HALF, int DK, int NC, bool TF>
+__device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC, TF> &sh, const Place &at, int c)
 {
     using N = Num<HALF>;
-    constexpr int C = N::kChunk, TT = C / 16, VT = VB / 16, kOwners = TT * VT;
-    using In = Pieces<HALF, DK, TF, kThreads>;
-    using St = State<DK, VB>;
-    static_assert(kOwners <= kWaves, "a tile a wave");
-    __shared__ typename In::Lds keys, queries;
-    __shared__ WideTile<HALF, VB, DK> state;
-    __shared__ WideTile<HALF, VB, C> out, out_q, write, carry;  // dO, its part for S, dW, X's part for S
-    __shared__ WideTile<HALF, C, C> scores;                     // P by columns
-    __shared__ Factors<C> F;
-    __shared__ float products[C * VT];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
-    int64_t bh;
-    int block;
-    head_and_block(A.B * A.Hv, A.blocks, bh, block);
-    const int64_t b = bh / A.Hv, h = bh % A.Hv, hk = h / (A.Hv / A.Hk), v_first = (int64_t)block * VB;
-    const bool owner = wave < kOwners;
-    const int tt = 16 * (wave / VT), vt = 16 * (wave % VT);
-    const int64_t v = v_first + vt + col;
-    const bool has_v = owner && v < A.value;
-    const int64_t v_at = b * A.v.b + h * A.v.h + v * A.v.d, o_at = b * A.o.b + h * A.o.h + v * A.o.d;
-    const int64_t dv_at = b * A.dv.b + h * A.dv.h + v * A.dv.d;
-    using Elem = typename N::Elem;
-    const Elem *const kb = static_cast<const Elem *>(A.k.p) + b * A.k.b + hk * A.k.h;
-    const Elem *const qb = static_cast<const Elem *>(A.q.p) + b * A.q.b + hk * A.q.h;
-
-    St S;
-    S.zero();
-    if (A.g_last) S.load(A.g_last + bh * A.key * A.value, wave, lane, v_first, A.key, A.value);
-    S.to_lds(state, wave, lane);
-    clear(scores);
-    for (int64_t n = A.chunks - 1; n >= 0; --n) {
-        const int64_t t0 = n * C, item = bh * A.chunks + n;
-        const StepGates gates = load_gates<C>(A, b, h, t0);
-        In k_raw, q_raw;
-        k_raw.load(A.k, kb, 0, t0, A.key, A.T);
-        q_raw.load(A.q, qb, 0, t0, A.key, A.T);
-        S.store(A.dstates + item * DK * A.value_pad, wave, lane, v_first, DK, A.value_pad, A.value_pad);
-        for (int r1 = gates.rows; r1 > 0;) {
-            const int r0 = document_start(gates.cut, r1);
-            k_raw.store(keys, r0, r1);
-            q_raw.store(queries, r0, r1);
-            if (wave == 0) write_factors(F, gates, r0, r1);
-            f32x4 value = {0.0f, 0.0f, 0.0f, 0.0f}, go = value;
-            if (has_v) {
-                value = load_steps<HALF>(A.v.p, v_at + (t0 + tt + row4) * A.v.t, A.v.t, r0 - tt - row4,
-                                         r1 - tt - row4);
-                if (A.o.p)
-                    go = load_steps<false>(A.o.p, o_at + (t0 + tt + row4) * A.o.t, A.o.t, r0 - tt - row4,
-                                           r1 - tt - row4);
-                go = only_steps(go, tt + row4, r0, r1);
-                value = only_steps(value, tt + row4, r0, r1);
-            }
-            if (owner) store4(out, vt + col, tt + row4, go);
-            __syncthreads();
-
-            f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (owner) {
-#pragma unroll
-                for (int d = 0; d < DK; d += 32) w = mma(w, operand<!TF>(keys, tt, d), operand<true>(state, vt, d));
-                const f32x4 start = four(F.start + tt + row4), end = four(F.end + tt + row4);
-                f32x4 g;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] *= end[e];
-                    g[e] = A.scale * start[e] * go[e];
-                }
-                store4(out_q, vt + col, tt + row4, only_steps(g, tt + row4, r0, r1));
-            }
-            // P by rows of the keys' steps t: its tile (t, s), s >= t, four s side by side
-            for (int p = wave; p < TT * (TT + 1) / 2; p += kWaves) {
-                int si, ti;
-                lower_pair(p, si, ti);
-                si *= 16, ti *= 16;
-                f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int d = 0; d < DK; d += 32) c = mma(c, operand<!TF>(queries, si, d), operand<!TF>(keys, ti, d));
-                const int t = ti + col, s = si + row4;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = s + e >= t ? A.scale * c[e] * decay_between(F, s + e, t) : 0.0f;
-                store4(scores, t, s, c);
-            }
-            __syncthreads();
-
-            if (owner) {
-#pragma unroll
-                for (int s = 0; s < C; s += 32)
-                    if (s + 32 > tt) w = mma(w, operand<true>(scores, tt, s), operand<true>(out, vt, s));
-                store4(write, vt + col, tt + row4, only_steps(w, tt + row4, r0, r1));
-            }
-            __syncthreads();
-
-            if (owner) {
-                f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < C; s += 32)
-                    if (s + 32 > tt) x = mma(x, operand_of(A.inverse_t, item, tt, s, N()), operand<true>(write, vt, s));
-                x = only_steps(x, tt + row4, r0, r1);
-                const f32x4 start = four(F.start + tt + row4), beta = four(F.beta + tt + row4);
-                float *p = A.x + (item * C + tt + row4) * A.value_pad + v_first + vt + col;
-                f32x4 c, bx, xv;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (tt + row4 + e >= r0 && tt + row4 + e < r1) p[e * A.value_pad] = x[e];
-                    bx[e] = beta[e] * x[e];
-                    c[e] = -start[e] * bx[e];
-                    xv[e] = x[e] * value[e];
-                }
-                store4(carry, vt + col, tt + row4, only_steps(c, tt + row4, r0, r1));
-                if (has_v)
-                    store_steps<HALF>(A.dv.p, dv_at + (t0 + tt + row4) * A.dv.t, A.dv.t, r0 - tt - row4,
-                                      r1 - tt - row4, bx);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                    for (int o = 1; o < 16; o *= 2) xv[e] += __shfl_xor(xv[e], o);
-                    if (col == 0) products[(tt + row4 + e) * VT + vt / 16] = xv[e];
-                }
-            }
-            __syncthreads();
-
-            if ((int)threadIdx.x >= r0 && (int)threadIdx.x < r1) {
-                float s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < VT; ++i) s += products[threadIdx.x * VT + i];
-                A.xv[(item * C + threadIdx.x) * A.blocks + block] = s;
-            }
-            if (gates.cut >> r0 & 1) {  // the state before this document's is no part of it
-                S.zero();
-            } else {
-                const float across = F.across[0];
-#pragma unroll
-                for (int i = 0; i < St::kCount; ++i) {
-                    int d0, v0;
-                    if (!St::tile(i, wave, d0, v0)) break;
-                    f32x4 c;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e] = across * S.s[i][e];
-#pragma unroll
-                    for (int s = 0; s < C; s += 32) {
-                        c = mma(c, operand<TF>(queries, d0, s), operand<true>(out_q, v0, s));
-                        c = mma(c, operand<TF>(keys, d0, s), operand<true>(carry, v0, s));
-                    }
-                    S.s[i] = c;
-                }
-            }
-            S.to_lds(state, wave, lane);
-            __syncthreads();
-            r1 = r0;
-        }
+    using Wide = typename N::Wide;
+    using In = Pieces<HALF, DK, TF, NC * kWave>;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32;
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16, tid = c * kWave + lane;
+    const int64_t v = 16 * (int64_t)(at.first + c) + col;
+    const bool has_o = v < A.value && A.o.p, all_o = 16 * (at.first + c + 1) <= A.value && A.o.p;
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    In k_raw, q_raw;
+    Columns<false, C> go;
+    const auto load = [&](int64_t n) {
+        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+        q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+    };
+    const float *const gos = head_of<false>(A.o, at.b, at.h) + min(v, (int64_t)A.value - 1) * A.o.d;
+    const auto load_go = [&](int64_t n) {
+        if (A.o.p) go.load(gos, A.o.t, n * C, A.T);
+    };
+    const auto stage = [&](int buffer, int r0, int r1) {
+        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
+        q_raw.store(sh.queries[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
+    };
+    Planner<C, true> plan;
+    const int last = (int)A.chunks - 1;
+    load(last);
+    load_go(last);
+    if (c == NC - 1) {
+        plan.start(A, at);
+        plan.write(sh.visits[0], sh.factors[0]);
     }
-    if (A.dh0) S.store(A.dh0 + bh * A.key * A.value, wave, lane, v_first, A.key, A.value, A.value);
+    __syncthreads();
+    Visit now = read_visit(sh.visits[0]);
+    stage(0, now.r0, now.r1);
+    load(now.leaves() && last > 0 ? last - 1 : last);
+    __syncthreads();
+    for (int buffer = 0; now.here(); buffer ^= 1) {
+        if (c == NC - 1) {
+            plan.advance(A, at);
+            plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
+        }
+        const Factors<C> &F = sh.factors[buffer];
+        const auto &K = sh.keys_of(buffer);
+        const auto &Q = sh.queries_of(buffer);
+        const bool whole = now.r0 == 0 && now.r1 == C;
+        f32x4 x[TT], y[TT];
+        Wide g[KC];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            x[t] = go.get(t);
+            if (!whole || !all_o) x[t] = only_steps(x[t], 16 * t + row4, has_o ? now.r0 : C, now.r1);
+            y[t] = zero;
+        }
+#pragma unroll
+        for (int s = 0; s < KC; ++s) g[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+        // P^T: its tile (s, t) as queries times keys, row t of the operand, four s
+        typename N::Exact k[TT][KD], q[2][KD];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int d = 0; d < KD; ++d) k[t][d] = operand<!TF>(K, 16 * t, 32 * d);
+#pragma unroll
+        for (int ss = 0; ss < KC; ++ss) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int d = 0; d < KD; ++d) q[i][d] = operand<!TF>(Q, 32 * ss + 16 * i, 32 * d);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < 2 * ss + 2; ++t) {
+                f32x4 a[2] = {zero, zero};
+#pragma unroll
+                for (int d = 0; d < KD; ++d)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (2 * ss + i >= t) a[i] = mma(a[i], q[i][d], k[t][d]);
+                const int j = 16 * t + col;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (2 * ss + i < t) continue;
+                    const int s = 32 * ss + 16 * i + row4;
+                    const f32x4 d = decays_from(F, s, j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[i][e] = s + e >= j ? A.scale * a[i][e] * d[e] : 0.0f;
+                }
+                y[t] = mma(y[t], stacked<HALF>(a[0], a[1]), g[ss]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) sh.by_scores[c][t][lane] = y[t];
+        __syncthreads();
+        const Visit then = read_visit(sh.visits[buffer ^ 1]);
+        const auto prepare = [&]() {
+            if (!then.here()) return;
+            stage(buffer ^ 1, then.r0, then.r1);
+            load(then.leaves() && then.n > 0 ? then.n - 1 : then.n);
+        };
+        if (sh.kTwo) prepare();
+        if (!now.fresh()) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const f32x4 start = four(F.start + 16 * t + row4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][e] *= A.scale * start[e];
+                if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+            }
+            load_go(then.here() ? then.n : now.n);
+#pragma unroll
+            for (int s = 0; s < KC; ++s) g[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+            typename N::Exact qt[KC][DT];
+            read_channels<TF>(qt, Q);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 part[DT];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) part[d] = zero;
+#pragma unroll
+            for (int s = 0; s < KC; ++s) mma_rows(part, qt[s], g[s]);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) sh.by_queries[c][d][lane] = part[d];
+        } else {
+            load_go(then.here() ? then.n : now.n);
+        }
+        if (!sh.kTwo) {
+            __syncthreads();
+            prepare();
+        }
+        __syncthreads();
+        now = then;
+    }
+}
+// A state's wave: K dS', X, dS.  Writes dS' behind each chunk, X, dV = b X and the
+// sums of X V over its columns.
+template <bool HALF, int DK, int NC, bool TF>
+__device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+{
+    using N = Num<HALF>;
+    using Wide = typename N::Wide;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32;
+    using Sl = Slots<C>;
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const int64_t v = 16 * (int64_t)(at.first + c) + col;
+    const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
+    auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h + v * A.dv.d;
+    State<DK> S;
+    Wide inverse[Sl::kCount];
+    Columns<HALF, C> value;
+    const auto *const values = head_of<HALF>(A.v, at.b, at.h) + min(v, (int64_t)A.value - 1) * A.v.d;
+    const auto load_value = [&](int64_t n) { value.load(values, A.v.t, n * C, A.T); };
+    const auto load_inverse = [&](int64_t n) {
+#pragma unroll
+        for (int s = 0; s < Sl::kCount; ++s)
+            inverse[s] = load_fragment(A.inverse_t[(at.bh * A.chunks + n) * Sl::kCount + s], N());
+    };
+    bool behind = false;  // the helper has a part of the state's gradient
+    const auto join = [&]() {
+        if (behind)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) S.s[d] += sh.by_queries[c][d][lane];
+    };
+
+    S.load(A.g_last + at.bh * A.key * A.value, v, A.g_last && has_v, A.key, A.value);
+    load_value(A.chunks - 1);
+    load_inverse(A.chunks - 1);
+    __syncthreads();
+    Visit now = read_visit(sh.visits[0]);
+    __syncthreads();
+    for (int buffer = 0; now.here(); buffer ^= 1) {
+        const int64_t item = at.bh * A.chunks + now.n;
+        const Factors<C> &F = sh.factors[buffer];
+        const auto &K = sh.keys_of(buffer);
+        const bool whole = now.r0 == 0 && now.r1 == C;
+        const int64_t after = now.leaves() && now.n > 0 ? now.n - 1 : now.n;
+        f32x4 x[TT];
+        join();
+        if (now.enters()) S.store(A.dstates + item * DK * A.value_pad, v, in_row, DK, A.value_pad);
+        Wide operands[KD];
+#pragma unroll
+        for (int d = 0; d < KD; ++d) operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
+        times<!TF>(x, K, operands);
+        typename N::Exact kt[KC][DT];
+        read_channels<TF>(kt, K);
+        __syncthreads();
+        const Visit then = read_visit(sh.visits[buffer ^ 1]);
+        Wide p[KC];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const f32x4 end = four(F.end + 16 * t + row4), y = sh.by_scores[c][t][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[e], x[t][e], y[e]);
+            if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        }
+#pragma unroll
+        for (int s = 0; s < KC; ++s) p[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) x[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        triangle_times<false, C>(x, inverse, p);
+        if (!whole)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        load_inverse(after);
+        float sums[4 * TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const f32x4 start = four(F.start + 16 * t + row4), beta = four(F.beta + 16 * t + row4);
+            f32x4 val = value.get(t), bx;
+            if (!whole || !all_v) val = only_steps(val, 16 * t + row4, has_v ? now.r0 : C, now.r1);
+            if (in_row)
+                store_column<false>(A.x + item * C * A.value_pad + v, A.value_pad, 16 * t + row4, now.r0, now.r1, whole, x[t]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sums[4 * t + e] = x[t][e] * val[e];
+                bx[e] = beta[e] * x[t][e];
+                x[t][e] = -start[e] * bx[e];
+            }
+            if (has_v)
+                store_column<HALF>(dv + (int64_t)now.n * C * A.dv.t, A.dv.t, 16 * t + row4, now.r0, now.r1, whole, bx);
+            if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        }
+        load_value(after);
+        if (now.fresh()) {  // the state before this document's is no part of it
+            S.zero();
+        } else {
+#pragma unroll
+            for (int s = 0; s < KC; ++s) p[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
+            S.advance(F.across[0], kt, p);
+        }
+        behind = !now.fresh();
+        int which;
+        const float sum = sum_columns(sums, which);
+        const int row = 16 * (which / 4) + row4 + which % 4;
+        if (in_row && row >= now.r0 && row < now.r1) A.xv[(item * C + row) * (A.value_pad / 16) + at.first + c] = sum;
+        if (!sh.kTwo) __syncthreads();
+        __syncthreads();
+        now = then;
+    }
+    join();
+    if (A.dh0) S.store(A.dh0 + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+}
+template <bool HALF, int DK, int NC, bool TF>
+__global__ void __launch_bounds__(2 * NC * kWave) delta_back_kernel(Args A)
+{
+    __shared__ Backward<HALF, DK, NC, TF> sh;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Place at = place_of<NC>(A);
+    if (A.chunks == 0) {
+        State<DK> S;
+        const int64_t v = 16 * (int64_t)(at.first + wave) + threadIdx.x % 16;
+        const bool here = wave < NC && v < A.value && A.dh0;
+        S.load(A.g_last + at.bh * A.key * A.value, v, here && A.g_last, A.key, A.value);
+        S.store(A.dh0 + at.bh * A.key * A.value, v, here, A.key, A.value);
+        return;
+    }
+    if (wave < NC)
+        back_state<HALF, DK, NC, TF>(A, sh, at, wave);
+    else
+        back_helper<HALF, DK, NC, TF>(A, sh, at, wave - NC);
 }
 
 // -------------------------------------------------------- the gradients ---
@@ -1112,8 +1694,8 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
     In k_raw, q_raw;
-    k_raw.load(A.k, static_cast<const Elem *>(A.k.p) + b * A.k.b + hk * A.k.h, 0, t0, A.key, A.T);
-    q_raw.load(A.q, static_cast<const Elem *>(A.q.p) + b * A.q.b + hk * A.q.h, 0, t0, A.key, A.T);
+    k_raw.load(A.k, static_cast<const Elem *>(A.k.p) + b * A.k.b + hk * A.k.h, 0, t0, A.key, A.T, threadIdx.x);
+    q_raw.load(A.q, static_cast<const Elem *>(A.q.p) + b * A.q.b + hk * A.q.h, 0, t0, A.key, A.T, threadIdx.x);
     clear(e_t);
     clear(h_t);
     f32x4 dq[NT][ND], dk[NT][ND];
@@ -1130,8 +1712,8 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
             r1 = document_end(gates.cut, r0, gates.rows);
             const bool before = !(gates.cut >> r0 & 1), behind = r1 == gates.rows;
             __syncthreads();
-            k_raw.store(keys, r0, r1);
-            q_raw.store(queries, r0, r1);
+            k_raw.store(keys, r0, r1, A.key, threadIdx.x);
+            q_raw.store(queries, r0, r1, A.key, threadIdx.x);
             if (wave == 0) write_factors(F, gates, r0, r1);
 
             f32x4 U[NT][ND], Y[NT][ND], Z[NT][ND], ow[NP], xw[NP];
@@ -1158,25 +1740,25 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                     if constexpr (TF) {
                         const int v = u / (C / 4), t4 = u % (C / 4) * 4;
                         if (A.o.p && v0 + v < A.value)
-                            x = load_steps<false>(A.o.p, b * A.o.b + h * A.o.h + (v0 + v) * A.o.d + (t0 + t4) * A.o.t,
-                                                  A.o.t, r0 - t4, r1 - t4);
+                            x = load_four(head_of<false>(A.o, b, h) + (v0 + v) * A.o.d + (t0 + t4) * A.o.t, A.o.t,
+                                          r0 - t4, r1 - t4);
                         store4(out, v, t4, only_steps(x, t4, r0, r1));
                     } else {
                         if (A.o.p && row >= r0 && row < r1)
-                            x = load_steps<false>(A.o.p, b * A.o.b + h * A.o.h + (v0 + v4) * A.o.d + (t0 + row) * A.o.t,
-                                                  A.o.d, 0, A.value - v0 - v4);
+                            x = load_four(head_of<false>(A.o, b, h) + (v0 + v4) * A.o.d + (t0 + row) * A.o.t, A.o.d, 0,
+                                          A.value - v0 - v4);
                         store4(out, row, v4, x);
                     }
                 }
                 __syncthreads();
 #pragma unroll
                 for (int c = 0; c < ND; ++c) {
-                    const int64_t at = (int64_t)(wd + 16 * c + col) * A.value_pad + v0 + 8 * (lane / 16);
+                    const int64_t at = (int64_t)(wd + 16 * c + col) * A.value_pad + v0 + row4;
                     float s[8], g[8];
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
-                        const f32x4 p = before ? four(s_before + at + j) : zero;
-                        const f32x4 q = behind ? four(s_behind + at + j) : zero;
+                        const f32x4 p = before ? four(s_before + at + 4 * j) : zero;
+                        const f32x4 q = behind ? four(s_behind + at + 4 * j) : zero;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             s[j + e] = p[e];
@@ -1223,12 +1805,12 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                 const f32x4 beta = four(F.beta + i);
                 f32x4 E, H, hs, bs;
                 float cs = 0.0f;
+                const f32x4 d = decays_from(F, i, j);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const bool mine = i + e >= r0 && i + e < r1 && j >= r0 && j <= i + e;
-                    const float d = decay_between(F, i + e, j);
-                    E[e] = mine ? A.scale * ow[m][e] * d : 0.0f;
-                    H[e] = mine && j < i + e ? -xw[m][e] * d : 0.0f;
+                    E[e] = mine ? A.scale * ow[m][e] * d[e] : 0.0f;
+                    H[e] = mine && j < i + e ? -xw[m][e] * d[e] : 0.0f;
                     hs[e] = mine ? H[e] * kk[e] : 0.0f;
                     bs[e] = mine ? fmaf_(E[e], qk[e], beta[e] * hs[e]) : 0.0f;
                     H[e] *= beta[e];
@@ -1338,7 +1920,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                         dG += row_sum[p];
                     }
                     for (int i = tile; i < TT; ++i) dG -= col_sum[(i * (i + 1) / 2 + tile) * 16 + row % 16];
-                    for (int j = 0; j < A.blocks; ++j) xv += A.xv[(item * C + row) * A.blocks + j];
+                    for (int j = 0; j < (A.value + 15) / 16; ++j) xv += A.xv[(item * C + row) * (A.value_pad / 16) + j];
                     const float y = F.start[row] * ky;
                     z = (double)F.end[row] * kz;
                     dG += (double)(A.scale * F.start[row]) * qu - (double)F.beta[row] * y - z;
@@ -1370,9 +1952,13 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
             const int d = wd + 16 * c + col;
             const int64_t t = t0 + wt + 16 * a + row4;
             const int left = (int)(A.T - t < 4 ? A.T - t : 4);
-            if (d >= A.key || left <= 0) continue;
-            store_steps<HALF>(A.dq.p, dq_at + d * A.dq.d + t * A.dq.t, A.dq.t, 0, left, dq[a][c]);
-            store_steps<HALF>(A.dk.p, dk_at + d * A.dk.d + t * A.dk.t, A.dk.t, 0, left, dk[a][c]);
+            if (d >= A.key) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) {
+                    store_gate<HALF>(A.dq.p, dq_at + d * A.dq.d + (t + e) * A.dq.t, dq[a][c][e]);
+                    store_gate<HALF>(A.dk.p, dk_at + d * A.dk.d + (t + e) * A.dk.t, dk[a][c][e]);
+                }
         }
 }
 

@@ -9,15 +9,16 @@ namespace delta {
 
 struct Args;
 
-// Columns of the values a workgroup of the chains takes: their state's share
-// and the operands made from it fill the LDS at 256 channels.
-constexpr int value_block(int room) { return room > 128 ? 16 : 32; }
+// Columns of the values a workgroup of the chains takes, 16 a pair of waves.  A
+// chain goes along its chunks one after the other, so narrow ones while that
+// gives more workgroups than CUs have none of.
+constexpr int kNarrow = 32, kWide = 64;
 
 // time_first: the steps of queries and keys lie side by side.
 template <bool HALF, int DK>
-pararnn_status_t run_scan(const Args &A, bool time_first, void *stream);
+pararnn_status_t run_scan(const Args &A, bool time_first, bool wide, void *stream);
 template <bool HALF, int DK>
-pararnn_status_t run_adjoint(const Args &A, bool time_first, void *stream);
+pararnn_status_t run_adjoint(const Args &A, bool time_first, bool wide, void *stream);
 
 
 }  // namespace delta

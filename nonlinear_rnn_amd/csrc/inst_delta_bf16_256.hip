@@ -3,7 +3,7 @@
 
 namespace pararnn {
 namespace delta {
-template pararnn_status_t run_scan<true, 256>(const Args &, bool, void *);
-template pararnn_status_t run_adjoint<true, 256>(const Args &, bool, void *);
+template pararnn_status_t run_scan<true, 256>(const Args &, bool, bool, void *);
+template pararnn_status_t run_adjoint<true, 256>(const Args &, bool, bool, void *);
 }  // namespace delta
 }  // namespace pararnn

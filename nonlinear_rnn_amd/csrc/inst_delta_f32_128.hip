@@ -3,7 +3,7 @@
 
 namespace pararnn {
 namespace delta {
-template pararnn_status_t run_scan<false, 128>(const Args &, bool, void *);
-template pararnn_status_t run_adjoint<false, 128>(const Args &, bool, void *);
+template pararnn_status_t run_scan<false, 128>(const Args &, bool, bool, void *);
+template pararnn_status_t run_adjoint<false, 128>(const Args &, bool, bool, void *);
 }  // namespace delta
 }  // namespace pararnn

@@ -54,7 +54,6 @@ namespace delta {
 constexpr int kWaves = 8, kThreads = kWaves * kWave;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -185,23 +184,29 @@ __device__ __forceinline__ void settle(f32x4 (&x)[M])
         asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]));
 }
 
-// A float32 as the bfloat16 next to it and the one next to what that leaves.
-__device__ __forceinline__ void split(float x, __bf16 &hi, __bf16 &lo)
+// Two float32 as the bfloat16 next to them and the ones next to what that leaves.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t rounded(float a, float b)
 {
-    hi = (__bf16)x;
-    lo = (__bf16)(x - (float)hi);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = rounded(a, b);
+    lo = rounded(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 __device__ __forceinline__ Bf::Wide split(const float (&x)[8], Bf::Wide)
 {
-    Bf::Wide w;
+    Words4 hi, lo;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        __bf16 h, l;
-        split(x[j], h, l);
-        w.hi[j] = h;
-        w.lo[j] = l;
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h, l;
+        split(x[2 * j], x[2 * j + 1], h, l);
+        hi[j] = h;
+        lo[j] = l;
     }
-    return w;
+    return {__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, lo)};
 }
 __device__ __forceinline__ Fl::Wide split(const float (&x)[8], Fl::Wide)
 {
@@ -311,16 +316,11 @@ __device__ __forceinline__ void store4(WideTile<HALF, ROWS, COLS> &t, int row, i
 {
     auto *p = t.at + row * t.kPitch + col;
     if constexpr (HALF) {
-        bf16x4 hi, lo;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            __bf16 h, l;
-            split(x[r], h, l);
-            hi[r] = h;
-            lo[r] = l;
-        }
-        __builtin_memcpy(p, &hi, 8);
-        __builtin_memcpy(p + ROWS * t.kPitch, &lo, 8);
+        uint32_t hi[2], lo[2];
+        split(x[0], x[1], hi[0], lo[0]);
+        split(x[2], x[3], hi[1], lo[1]);
+        __builtin_memcpy(p, hi, 8);
+        __builtin_memcpy(p + ROWS * t.kPitch, lo, 8);
     } else {
         __builtin_memcpy(p, &x, 16);
     }
@@ -467,13 +467,13 @@ struct Pieces {
             const int r = row + n * kRows;
             const bool out = TF ? r >= key : r < r0 || r >= r1;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (out || col + e < first || col + e >= end) {
-                    if constexpr (HALF)
-                        w[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
-                    else
-                        w[e] = 0;
-                }
+            for (int e = 0; e < E; ++e) {
+                const bool in = !out & (col + e >= first) & (col + e < end);
+                if constexpr (HALF)
+                    w[e / 2] &= in ? ~0u : e % 2 ? 0x0000ffffu : 0xffff0000u;
+                else
+                    w[e] = in ? w[e] : 0;
+            }
             *reinterpret_cast<uint4 *>(p + n * kRows * lds.kPitch) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -647,29 +647,44 @@ struct alignas(16) Factors {
     float hi[C], lo[C];  // the decay's sum, in two floats
     float start[C];      // exp(G_i)
     float end[C];        // exp(G_C - G_i)
+    float back[C];       // exp(-G_i), if all sums are near zero
     float beta[C];
     float across[4];     // exp(G_C)
 };
+// Within 2^+-kNear, where a factor exp(G_i - G_j) may be the product of two.
+constexpr double kNear = 32.0;
+// 2^x, its argument's rounding made good
+__device__ __forceinline__ float power_of_two(double x)
+{
+    const float hi = (float)x, f = ex2(hi);
+    return fmaf_(f, 0.6931472f * (float)(x - hi), f);
+}
+// Returns whether all sums are near zero.
 template <int C>
-__device__ __forceinline__ void write_factors(Factors<C> &F, const StepGates &s, int r0, int r1)
+__device__ __forceinline__ bool write_factors(Factors<C> &F, const StepGates &s, int r0, int r1)
 {
     const int lane = threadIdx.x % kWave;
     const double G = decay_sum(s, r0, r1), total = __shfl(G, kWave - 1);
+    const bool near = !__ballot(!(fabs(G) <= kNear));
     if (lane < C) {
         const float hi = (float)G;
         F.hi[lane] = hi;
         F.lo[lane] = (float)(G - hi);
-        F.start[lane] = ex2(hi);
-        F.end[lane] = ex2((float)(total - G));
+        F.start[lane] = power_of_two(G);
+        F.end[lane] = power_of_two(total - G);
+        F.back[lane] = power_of_two(-G);
         F.beta[lane] = lane >= r0 && lane < r1 ? s.beta : 0.0f;
     }
-    if (lane == 0) F.across[0] = ex2((float)total);
+    if (lane == 0) F.across[0] = power_of_two(total);
+    return near;
 }
 __device__ __forceinline__ f32x4 four(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-// exp(G_i - G_j) for i .. i + 3, and for j .. j + 3
+// exp(G_i - G_j) for i .. i + 3, and for j .. j + 3.  An exponential takes as long
+// as four products.
 template <int C>
-__device__ __forceinline__ f32x4 decays_from(const Factors<C> &F, int i, int j)
+__device__ __forceinline__ f32x4 decays_from(const Factors<C> &F, int i, int j, bool near = false)
 {
+    if (near) return four(F.start + i) * F.back[j];
     const f32x4 hi = four(F.hi + i), lo = four(F.lo + i);
     const float h = F.hi[j], l = F.lo[j];
     f32x4 d;
@@ -678,8 +693,9 @@ __device__ __forceinline__ f32x4 decays_from(const Factors<C> &F, int i, int j)
     return d;
 }
 template <int C>
-__device__ __forceinline__ f32x4 decays_to(const Factors<C> &F, int i, int j)
+__device__ __forceinline__ f32x4 decays_to(const Factors<C> &F, int i, int j, bool near = false)
 {
+    if (near) return four(F.back + j) * F.start[i];
     const f32x4 hi = four(F.hi + j), lo = four(F.lo + j);
     const float h = F.hi[i], l = F.lo[i];
     f32x4 d;
@@ -937,8 +953,9 @@ struct State {
 // Products whose operands are read from LDS all at once, before the first is used:
 // left to itself the compiler reads two, waits for the LDS and multiplies.
 // x_t = the rows 16 t .. of a tile of steps times what `s` holds, over the channels.
-template <bool ALONG, class In, class Wide, int TT, int KD>
-__device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide (&s)[KD])
+// `meanwhile` is what else is to be read meanwhile.
+template <bool ALONG, class In, class Wide, int TT, int KD, class F>
+__device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide (&s)[KD], const F &meanwhile)
 {
     constexpr int B = KD < 4 ? KD : 4;  // the registers of 16 operands at a time
     decltype(operand<ALONG>(tile, 0, 0)) k[B][TT];
@@ -950,6 +967,7 @@ __device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide
         for (int d = 0; d < B; ++d)
 #pragma unroll
             for (int t = 0; t < TT; ++t) k[d][t] = operand<ALONG>(tile, 16 * t, 32 * (d0 + d));
+        if (d0 == 0) meanwhile();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < B; ++d) mma_rows(x, k[d], s[d0 + d]);
@@ -1010,25 +1028,16 @@ __device__ __forceinline__ Place place_of(const Args &A)
     p.first = block * NC;
     return p;
 }
-// Of the operands of a triangular matrix [C][C], those that helper c of NC makes.
-template <int C, int NC>
-__device__ __forceinline__ int first_slot(int c)
-{
-    constexpr int kCount = Slots<C>::kCount;
-    if constexpr (kCount == 6 && NC == 4)
-        return c < 2 ? 2 * c : 2 + c;  // two of one or two tiles, then one of two
-    else
-        return kCount * c / NC;
-}
-
 // A visit: steps r0 .. r1 - 1 of chunk n (-1: no more).
 struct Visit {
     int n, r0, r1, flags;
-    static constexpr int kFresh = 1, kEnters = 2, kLeaves = 4;  // starts a document; the chunk's first, its last
+    // starts a document; the chunk's first, its last; sums of log decays near zero
+    static constexpr int kFresh = 1, kEnters = 2, kLeaves = 4, kNear = 8;
     __device__ __forceinline__ bool here() const { return n >= 0; }
     __device__ __forceinline__ bool fresh() const { return flags & kFresh; }
     __device__ __forceinline__ bool enters() const { return flags & kEnters; }
     __device__ __forceinline__ bool leaves() const { return flags & kLeaves; }
+    __device__ __forceinline__ bool near() const { return flags & kNear; }
 };
 __device__ __forceinline__ Visit read_visit(const Visit &v)
 {
@@ -1072,11 +1081,12 @@ struct Planner {
     // to LDS: the visit, and what its steps multiply with
     __device__ __forceinline__ void write(Visit &v, Factors<C> &F) const
     {
-        if (n >= 0) write_factors(F, gates, r0, r1);
+        const bool near = n >= 0 && write_factors(F, gates, r0, r1);
         const bool first = BACK ? r1 == gates.rows : r0 == 0, last = BACK ? r0 == 0 : r1 == gates.rows;
         if (threadIdx.x % kWave == 0)
             v = {n, r0, r1,
-                 (gates.cut >> r0 & 1 ? Visit::kFresh : 0) | (first ? Visit::kEnters : 0) | (last ? Visit::kLeaves : 0)};
+                 (gates.cut >> r0 & 1 ? Visit::kFresh : 0) | (first ? Visit::kEnters : 0) |
+                     (last ? Visit::kLeaves : 0) | (near ? Visit::kNear : 0)};
     }
 };
 
@@ -1115,119 +1125,188 @@ __device__ __forceinline__ const typename Num<HALF>::Elem *head_of(const Plane &
     return static_cast<const typename Num<HALF>::Elem *>(x.p) + b * x.b + h * x.h;
 }
 
-// Forward.  A helper: P, q^T S and the outputs, from S and W as operands in LDS.
-// Without QUERIES it only brings the keys.
+// P = scale (q . k) D as operands, slots first .. end - 1: its tile (s, t) as keys times
+// queries, row t of the operand, four s.
+template <bool HALF, int DK, int NC, bool TF>
+__device__ __forceinline__ void make_scores(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, bool near,
+                                            int first, int end)
+{
+    using N = Num<HALF>;
+    constexpr int C = N::kChunk, KD = DK / 32;
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const Factors<C> &F = sh.factors[buffer];
+    const auto &K = sh.keys_of(buffer);
+    for (int s = first; s < end; ++s) {
+        int tt = s, ss = 0;
+        if constexpr (C == 64) {
+            tt = s < 2 ? s : s / 2 + 1;
+            ss = s < 2 ? 0 : s % 2;
+        }
+        f32x4 p[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        typename N::Exact q[KD], k[KD][2];
+#pragma unroll
+        for (int d = 0; d < KD; ++d) {
+            q[d] = operand<!TF>(sh.queries, 16 * tt, 32 * d);
+            k[d][0] = operand<!TF>(K, 32 * ss, 32 * d);
+            k[d][1] = operand<!TF>(K, 32 * ss + 16, 32 * d);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < KD; ++d) mma_rows(p, k[d], q[d]);
+        settle(p);
+        const int t = 16 * tt + col;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = 32 * ss + 16 * i + row4;
+            const f32x4 d = decays_to(F, t, j, near);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[i][e] = j + e <= t ? A.scale * p[i][e] * d[e] : 0.0f;
+        }
+        store_fragment(sh.scores[s], stacked<HALF>(p[0], p[1]));
+    }
+}
+
+// How the chains' waves share the work.  NC state's waves; as many that compute the
+// outputs; and with NC = 2 two that bring keys and queries and plan the visits, which
+// may wait for memory (they have 16 pieces a tensor each) while the others do not.
+// With NC = 4 the waves of the outputs do this too, as there is no room for more
+// waves' registers.
+template <int NC>
+struct Roles {
+    static constexpr bool kApart = NC == 2;
+    static constexpr int kServers = NC, kServer = kApart ? 2 * NC : NC;  // their first wave
+    static constexpr int waves(bool output) { return NC + (output ? NC : 0) + (kApart || !output ? kServers : 0); }
+    static constexpr int server(bool output) { return output ? kServer : NC; }
+};
+
+// Forward.  Brings keys and queries (QUERIES), plans the visits.
 template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
-__device__ __forceinline__ void chain_helper(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+struct Server {
+    using In = Pieces<HALF, DK, TF, Roles<NC>::kServers * kWave>;
+    static constexpr int C = Num<HALF>::kChunk;
+    In k_raw, q_raw;
+    Planner<C, false> plan;
+    __device__ __forceinline__ void load(const Args &A, const Place &at, int64_t n, int tid)
+    {
+        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+        if constexpr (QUERIES) q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
+    }
+    __device__ __forceinline__ void stage(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, const Visit &v,
+                                          int tid)
+    {
+        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], v.r0, v.r1, A.key, tid);
+        if constexpr (QUERIES) q_raw.store(sh.queries, v.r0, v.r1, A.key, tid);
+        // (also where the next visit has the same chunk: see the state's wave)
+        load(A, at_, v.leaves() && v.n + 1 < A.chunks ? v.n + 1 : v.n, tid);
+    }
+    Place at_;
+    __device__ __forceinline__ Visit start(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c, int tid)
+    {
+        at_ = at;
+        load(A, at, 0, tid);
+        if (c == 0) {
+            plan.start(A, at);
+            plan.write(sh.visits[0], sh.factors[0]);
+        }
+        __syncthreads();
+        const Visit now = read_visit(sh.visits[0]);
+        stage(A, sh, 0, now, tid);
+        __syncthreads();
+        return now;
+    }
+    __device__ __forceinline__ void look(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, int c)
+    {
+        if (c != 0) return;
+        plan.advance(A, at_);
+        plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
+    }
+};
+template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
+__device__ __forceinline__ void chain_server(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+{
+    const int tid = c * kWave + threadIdx.x % kWave;
+    constexpr int kSlots = Slots<Num<HALF>::kChunk>::kCount;
+    Server<HALF, DK, NC, TF, QUERIES> server;
+    Visit now = server.start(A, sh, at, c, tid);
+    for (int buffer = 0; now.here(); buffer ^= 1) {
+        server.look(A, sh, buffer, c);
+        if constexpr (QUERIES)  // two slots of three to these
+            make_scores(A, sh, buffer, now.near(), kSlots == 6 ? 2 * c : c, kSlots == 6 ? 2 * c + 2 : c + 1);
+        __syncthreads();
+        const Visit then = read_visit(sh.visits[buffer ^ 1]);
+        if (sh.kTwo && then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
+        if (!sh.kTwo) {
+            __syncthreads();
+            if (then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
+        }
+        __syncthreads();
+        now = then;
+    }
+}
+// P, q^T S and the outputs, from S and W as operands in LDS.  SERVES: also what a
+// server does.
+template <bool HALF, int DK, int NC, bool TF, bool SERVES>
+__device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
-    using In = Pieces<HALF, DK, TF, NC * kWave>;
-    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, KD = DK / 32;
-    using Sl = Slots<C>;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, KD = DK / 32, kSlots = Slots<C>::kCount;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16, tid = c * kWave + lane;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value;
     float *const o = static_cast<float *>(A.o.p) + at.b * A.o.b + at.h * A.o.h + v * A.o.d;
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    In k_raw;
-    [[maybe_unused]] In q_raw;
-    const auto load = [&](int64_t n) {
-        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-        if constexpr (QUERIES) q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-    };
-    const auto stage = [&](int buffer, int r0, int r1) {
-        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
-        if constexpr (QUERIES) q_raw.store(sh.queries, r0, r1, A.key, tid);
-    };
-    Planner<C, false> plan;
-    load(0);
-    if (c == NC - 1) {
-        plan.start(A, at);
-        plan.write(sh.visits[0], sh.factors[0]);
+    // its slots of P: with servers one of the last two; else a share of all
+    int s0 = kSlots == 6 ? 4 + c : 0, s1 = kSlots == 6 ? 5 + c : 0;
+    if constexpr (SERVES) {
+        s0 = kSlots == 6 ? (c < 2 ? 2 * c : 2 + c) : min(c, 2);
+        s1 = kSlots == 6 ? (c < 2 ? 2 * c + 2 : 3 + c) : min(c + 1, 2);
     }
-    __syncthreads();
-    Visit now = read_visit(sh.visits[0]);
-    stage(0, now.r0, now.r1);
-    load(now.leaves() && A.chunks > 1 ? 1 : 0);
-    __syncthreads();
+    [[maybe_unused]] Server<HALF, DK, NC, TF, true> server;
+    Visit now;
+    if constexpr (SERVES) {
+        now = server.start(A, sh, at, c, tid);
+    } else {
+        __syncthreads();
+        now = read_visit(sh.visits[0]);
+        __syncthreads();
+    }
     for (int buffer = 0; now.here(); buffer ^= 1) {
-        const int64_t t0 = (int64_t)now.n * C;
-        if (c == NC - 1) {
-            plan.advance(A, at);
-            plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
-        }
-        [[maybe_unused]] f32x4 out[TT];
-        if constexpr (QUERIES) {
-            const Factors<C> &F = sh.factors[buffer];
-            const auto &K = sh.keys_of(buffer);
-            // P, its tile (s, t) as keys times queries: row t of the operand, four s
-            for (int s = first_slot<C, NC>(c); s < first_slot<C, NC>(c + 1); ++s) {
-                int tt = s, ss = 0;
-                if constexpr (C == 64) {
-                    tt = s < 2 ? s : s / 2 + 1;
-                    ss = s < 2 ? 0 : s % 2;
-                }
-                f32x4 p[2] = {zero, zero};
-                typename N::Exact q[KD], k[2][KD];
-#pragma unroll
-                for (int d = 0; d < KD; ++d) {
-                    q[d] = operand<!TF>(sh.queries, 16 * tt, 32 * d);
-                    k[0][d] = operand<!TF>(K, 32 * ss, 32 * d);
-                    k[1][d] = operand<!TF>(K, 32 * ss + 16, 32 * d);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int d = 0; d < KD; ++d)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) p[i] = mma(p[i], k[i][d], q[d]);
-                const int t = 16 * tt + col;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = 32 * ss + 16 * i + row4;
-                    const f32x4 d = decays_to(F, t, j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[i][e] = j + e <= t ? A.scale * p[i][e] * d[e] : 0.0f;
-                }
-                store_fragment(sh.scores[s], stacked<HALF>(p[0], p[1]));
-            }
+        const Factors<C> &F = sh.factors[buffer];
+        if constexpr (SERVES) server.look(A, sh, buffer, c);
+        make_scores(A, sh, buffer, now.near(), s0, s1);
+        f32x4 out[TT];
+        {
             Wide s[KD];
 #pragma unroll
             for (int d = 0; d < KD; ++d) s[d] = load_fragment(sh.state[c][d], N());
-            times<!TF>(out, sh.queries, s);
+            f32x4 start[TT];
+            times<!TF>(out, sh.queries, s, [&]() {
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const f32x4 start = four(F.start + 16 * t + row4);
+                for (int t = 0; t < TT; ++t) start[t] = four(F.start + 16 * t + row4);
+            });
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out[t][e] *= A.scale * start[e];
-            }
+            for (int t = 0; t < TT; ++t) out[t] *= A.scale * start[t];
         }
         __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
-        const auto prepare = [&]() {
-            if (!then.here()) return;
-            stage(buffer ^ 1, then.r0, then.r1);
-            load(then.leaves() && then.n + 1 < A.chunks ? then.n + 1 : then.n);
-        };
-        if constexpr (QUERIES) {
-            Wide x[KC], p[Sl::kCount];
+        Wide x[KC], p[kSlots];
 #pragma unroll
-            for (int s = 0; s < KC; ++s) x[s] = load_fragment(sh.write[c][s], N());
+        for (int s = 0; s < KC; ++s) x[s] = load_fragment(sh.write[c][s], N());
 #pragma unroll
-            for (int s = 0; s < Sl::kCount; ++s) p[s] = load_fragment(sh.scores[s], N());
-            if (sh.kTwo) prepare();
-            triangle_times<true, C>(out, p, x);
-            const bool whole = now.r0 == 0 && now.r1 == C;
-            if (has_v)
+        for (int s = 0; s < kSlots; ++s) p[s] = load_fragment(sh.scores[s], N());
+        if constexpr (SERVES)
+            if (sh.kTwo && then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
+        triangle_times<true, C>(out, p, x);
+        const bool whole = now.r0 == 0 && now.r1 == C;
+        if (has_v)
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
-                    store_column<false>(o + t0 * A.o.t, A.o.t, 16 * t + row4, now.r0, now.r1, whole, out[t]);
-        } else {
-            if (sh.kTwo) prepare();
-        }
+            for (int t = 0; t < TT; ++t)
+                store_column<false>(o + (int64_t)now.n * C * A.o.t, A.o.t, 16 * t + row4, now.r0,
+                                    now.r1, whole, out[t]);
         if (!sh.kTwo) {
             __syncthreads();
-            prepare();
+            if constexpr (SERVES)
+                if (then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
         }
         __syncthreads();
         now = then;
@@ -1245,6 +1324,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
+    constexpr bool kEarly = DK < 256 && NC == 2 && !OUTPUT;  // registers for all of the keys' operands
     State<DK> S;
     Wide operands[KD], inverse[Sl::kCount];
     Columns<HALF, C> value;
@@ -1283,20 +1363,27 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         // may not be under way would have everything behind it waited for
         const int64_t after = now.leaves() && now.n + 1 < A.chunks ? now.n + 1 : now.n;
         f32x4 x[TT];
-        times<!TF>(x, K, operands);
+        f32x4 start[TT], beta[TT];
+        typename N::Exact kt[KC][DT];
+        times<!TF>(x, K, operands, [&]() {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                start[t] = four(F.start + 16 * t + row4);
+                beta[t] = four(F.beta + 16 * t + row4);
+            }
+            if (kEarly) read_channels<TF>(kt, K);
+        });
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const f32x4 start = four(F.start + 16 * t + row4), beta = four(F.beta + 16 * t + row4);
             const f32x4 val = value.get(t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = beta[e] * fmaf_(-start[e], x[t][e], val[e]);
+            for (int e = 0; e < 4; ++e) x[t][e] = beta[t][e] * fmaf_(-start[t][e], x[t][e], val[e]);
         }
         if (!whole || !all_v)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, has_v ? now.r0 : C, now.r1);
         load_value(after);
-        typename N::Exact kt[KC][DT];
-        read_channels<TF>(kt, K);
+        if (!kEarly) read_channels<TF>(kt, K);
         Wide rhs[KC];
 #pragma unroll
         for (int s = 0; s < KC; ++s) rhs[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
@@ -1318,12 +1405,10 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
                                         now.r0, now.r1, whole, x[t]);
         }
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const f32x4 end = four(F.end + 16 * t + row4);
+        for (int t = 0; t < TT; ++t) x[t] *= four(F.end + 16 * t + row4);
+        if (!whole)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] *= end[e];
-            if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
-        }
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
         Wide carry[KC];
 #pragma unroll
         for (int s = 0; s < KC; ++s) carry[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
@@ -1345,9 +1430,10 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         if (A.last) S.store(A.last + at.bh * A.key * A.value, v, has_v, A.key, A.value);
 }
 template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
-__global__ void __launch_bounds__(2 * NC * kWave) delta_chain_kernel(Args A)
+__global__ void __launch_bounds__(Roles<NC>::waves(OUTPUT) * kWave) delta_chain_kernel(Args A)
 {
     __shared__ Forward<HALF, DK, NC, TF> sh;
+    using R = Roles<NC>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Place at = place_of<NC>(A);
     if (A.chunks == 0) {  // the state goes through
@@ -1358,10 +1444,18 @@ __global__ void __launch_bounds__(2 * NC * kWave) delta_chain_kernel(Args A)
         S.store(A.last + at.bh * A.key * A.value, v, here, A.key, A.value);
         return;
     }
-    if (wave < NC)
+    if (wave < NC) {
         chain_state<HALF, DK, NC, TF, OUTPUT>(A, sh, at, wave);
-    else
-        chain_helper<HALF, DK, NC, TF, OUTPUT>(A, sh, at, wave - NC);
+    } else if constexpr (!OUTPUT) {
+        chain_server<HALF, DK, NC, TF, false>(A, sh, at, wave - NC);
+    } else if constexpr (R::kApart) {
+        if (wave < R::kServer)
+            chain_output<HALF, DK, NC, TF, false>(A, sh, at, wave - NC);
+        else
+            chain_server<HALF, DK, NC, TF, true>(A, sh, at, wave - R::kServer);
+    } else {
+        chain_output<HALF, DK, NC, TF, true>(A, sh, at, wave - NC);
+    }
 }
 
 // Sums over the 16 lanes of a group, of M values each: at the end a lane holds
@@ -1476,7 +1570,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
                 for (int i = 0; i < 2; ++i) {
                     if (2 * ss + i < t) continue;
                     const int s = 32 * ss + 16 * i + row4;
-                    const f32x4 d = decays_from(F, s, j);
+                    const f32x4 d = decays_from(F, s, j, now.near());
 #pragma unroll
                     for (int e = 0; e < 4; ++e) a[i][e] = s + e >= j ? A.scale * a[i][e] * d[e] : 0.0f;
                 }
@@ -1538,6 +1632,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
     auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h + v * A.dv.d;
+    constexpr bool kEarly = DK < 256 && NC == 2;
     State<DK> S;
     Wide inverse[Sl::kCount];
     Columns<HALF, C> value;
@@ -1573,19 +1668,30 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         Wide operands[KD];
 #pragma unroll
         for (int d = 0; d < KD; ++d) operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
-        times<!TF>(x, K, operands);
+        f32x4 start[TT], beta[TT], end[TT];
         typename N::Exact kt[KC][DT];
-        read_channels<TF>(kt, K);
+        times<!TF>(x, K, operands, [&]() {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                start[t] = four(F.start + 16 * t + row4);
+                beta[t] = four(F.beta + 16 * t + row4);
+                end[t] = four(F.end + 16 * t + row4);
+            }
+            if (kEarly) read_channels<TF>(kt, K);
+        });
+        if (!kEarly) read_channels<TF>(kt, K);
         __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
         Wide p[KC];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const f32x4 end = four(F.end + 16 * t + row4), y = sh.by_scores[c][t][lane];
+            const f32x4 y = sh.by_scores[c][t][lane];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[e], x[t][e], y[e]);
-            if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+            for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[t][e], x[t][e], y[e]);
         }
+        if (!whole)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
 #pragma unroll
         for (int s = 0; s < KC; ++s) p[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
@@ -1598,7 +1704,6 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         float sums[4 * TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const f32x4 start = four(F.start + 16 * t + row4), beta = four(F.beta + 16 * t + row4);
             f32x4 val = value.get(t), bx;
             if (!whole || !all_v) val = only_steps(val, 16 * t + row4, has_v ? now.r0 : C, now.r1);
             if (in_row)
@@ -1606,8 +1711,8 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 sums[4 * t + e] = x[t][e] * val[e];
-                bx[e] = beta[e] * x[t][e];
-                x[t][e] = -start[e] * bx[e];
+                bx[e] = beta[t][e] * x[t][e];
+                x[t][e] = -start[t][e] * bx[e];
             }
             if (has_v)
                 store_column<HALF>(dv + (int64_t)now.n * C * A.dv.t, A.dv.t, 16 * t + row4, now.r0, now.r1, whole, bx);

@@ -18,11 +18,12 @@ pararnn_status_t run_chain(const Args &A, bool wide, hipStream_t s)
         const pararnn_status_t st = launched();
         if (st != PARARNN_OK) return st;
     }
+    constexpr int W = DK < 256 ? 4 : 2;
     const dim3 grid((unsigned)(A.B * A.Hv * A.blocks));
-    if (wide && DK < 256)
-        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, DK < 256 ? 4 : 2, TF, OUTPUT>), grid, dim3(8 * kWave), 0, s, A);
+    if (wide)
+        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, W, TF, OUTPUT>), grid, dim3(Roles<W>::waves(OUTPUT) * kWave), 0, s, A);
     else
-        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, 2, TF, OUTPUT>), grid, dim3(4 * kWave), 0, s, A);
+        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, 2, TF, OUTPUT>), grid, dim3(Roles<2>::waves(OUTPUT) * kWave), 0, s, A);
     return launched();
 }
 template <bool HALF, int DK, bool TF>
@@ -33,8 +34,9 @@ pararnn_status_t run_back(const Args &A, bool wide, hipStream_t s)
         if (st != PARARNN_OK) return st;
     }
     const dim3 grid((unsigned)(A.B * A.Hv * A.blocks));
-    if (wide && DK < 256)
-        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, DK < 256 ? 4 : 2, TF>), grid, dim3(8 * kWave), 0, s, A);
+    constexpr int W = DK < 256 ? 4 : 2;
+    if (wide)
+        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, W, TF>), grid, dim3(2 * W * kWave), 0, s, A);
     else
         hipLaunchKernelGGL((delta_back_kernel<HALF, DK, 2, TF>), grid, dim3(4 * kWave), 0, s, A);
     const pararnn_status_t st = launched();

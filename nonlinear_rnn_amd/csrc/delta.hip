@@ -74,9 +74,20 @@ bool wide_chains(const pararnn_delta_shape_t *s)
 {
     return room_of(s->dk) < 256 && s->dv > kNarrow && s->B * s->Hv * ((s->dv + kWide - 1) / kWide) >= kComputeUnits;
 }
+// Segments of a chain.  Two passes and a way along the segments instead of one way
+// along the chunks: as many as fill the device twice, while a segment has 8 chunks,
+// and so that the two ways are about as long.
+int64_t segments_of(const pararnn_delta_shape_t *s, int64_t chunks)
+{
+    const int64_t chains = s->B * s->Hv * ((s->dv + kNarrow - 1) / kNarrow);
+    if (chains == 0 || chunks < 32) return 1;
+    const int64_t most = std::min<int64_t>({2 * kComputeUnits / chains, chunks / 8, (int64_t)std::sqrt(2.0 * chunks)});
+    return most < 4 ? 1 : most;
+}
 
 struct Layout {
-    size_t inverse, inverse_t, states, dstates, w, x, xv, total;
+    size_t inverse, inverse_t, states, dstates, w, x, xv, maps, marks, cuts, total;
+    int64_t per, segments;  // chunks a segment
 };
 Layout layout(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool adjoint)
 {
@@ -99,6 +110,15 @@ Layout layout(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool adjoin
         l.w = take(items * C * pad * 4);
         l.x = take(items * C * pad * 4);
         l.xv = take(items * C * (pad / 16) * 4);
+    }
+    const int64_t chunks = (s->T + C - 1) / C, want = segments_of(s, chunks);
+    l.per = std::max<int64_t>(1, (chunks + want - 1) / want);
+    l.segments = std::max<int64_t>(1, (chunks + l.per - 1) / l.per);
+    if (l.segments > 1) {
+        const size_t chains = (size_t)(s->B * s->Hv * l.segments), key_pad = (size_t)(s->dk + 15) / 16 * 16;
+        l.maps = take(chains * room * (pad + key_pad) * 4);
+        l.marks = take(chains * room * pad * 4);
+        l.cuts = take(chains * 4);
     }
     l.total = at;
     return l;
@@ -137,6 +157,13 @@ pararnn_status_t prepare(Args &A, const pararnn_delta_shape_t *s, pararnn_dtype_
     A.blocks = (A.value_pad + columns - 1) / columns;
     A.scale = scale;
     char *const base = static_cast<char *>(ws);
+    A.key_pad = (A.key + 15) / 16 * 16;
+    A.per = (int32_t)l.per, A.segments = (int32_t)l.segments;
+    if (l.segments > 1) {
+        A.maps = reinterpret_cast<float *>(base + l.maps);
+        A.marks = reinterpret_cast<float *>(base + l.marks);
+        A.cuts = reinterpret_cast<int32_t *>(base + l.cuts);
+    }
     A.inverse = reinterpret_cast<Fragment *>(base + l.inverse);
     if (adjoint) {
         A.inverse_t = reinterpret_cast<Fragment *>(base + l.inverse_t);

@@ -74,11 +74,18 @@ struct Args {
     int32_t Hk, Hv, key, value;       // key, value: dk, dv
     int32_t value_pad, blocks;        // columns of the workspace's rows; the chains' workgroups a head
     float scale;
+    // segments of `per` chunks, chained at once (1: the whole chain)
+    int32_t segments, per;
+    int32_t ends;      // only the segments' maps: their ends from zero, and from the identity
     // workspace
     struct Fragment *inverse, *inverse_t;  // [b h][chunk][slot] operands
     float *states, *dstates;          // [b h][chunk][DK][value_pad]
     float *w, *x;                     // [b h][chunk * C][value_pad]
     float *xv;                        // [b h][chunk * C][value_pad / 16]: X . V of 16 columns
+    float *maps;                      // [b h][segment][DK][value_pad + key_pad]: ends from zero, from the identity
+    float *marks;                     // [b h][segment][DK][value_pad]: the state before, the gradient behind
+    int32_t *cuts;                    // [b h][segment]: whether a document starts in it
+    int32_t key_pad;                  // `key`, whole tiles
 };
 
 // ---------------------------------------------------------------- numbers ---
@@ -926,6 +933,15 @@ struct State {
 #pragma unroll
         for (int i = 0; i < KC; ++i) mma_rows(s, k[i], w[i]);
     }
+    // column j of the identity
+    __device__ __forceinline__ void identity(int j)
+    {
+        const int row4 = threadIdx.x % kWave / 16 * 4;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[i][r] = 16 * i + row4 + r == j ? 1.0f : 0.0f;
+    }
     // rows of `pitch` values; channels from `key` on, and all without `here`, are not there
     __device__ __forceinline__ void load(const float *p, int64_t v, bool here, int key, int64_t pitch)
     {
@@ -1011,23 +1027,31 @@ __device__ __forceinline__ void read_channels(Exact (&k)[KC][DT], const In &tile
 // products that the state does not need.  A `visit` is a chunk, or one document
 // of it.
 
-// A workgroup's head and columns.
+// A workgroup's head, columns and segment.
 struct Place {
     int64_t bh, b, h, hk;
-    int first;  // its first 16 columns
+    int first;    // its first 16 columns
+    int seg;
+    int n0, n1;   // chunks n0 .. n1 - 1
 };
 template <int NC>
 __device__ __forceinline__ Place place_of(const Args &A)
 {
     Place p;
     int block;
-    head_and_block(A.B * A.Hv, A.blocks, p.bh, block);
+    int64_t chain;
+    head_and_block(A.B * A.Hv * A.segments, A.blocks, chain, block);
+    p.bh = chain / A.segments;
+    p.seg = (int)(chain % A.segments);
     p.b = p.bh / A.Hv;
     p.h = p.bh % A.Hv;
     p.hk = p.h / (A.Hv / A.Hk);
     p.first = block * NC;
+    p.n0 = p.seg * A.per;
+    p.n1 = (int)min((int64_t)p.n0 + A.per, A.chunks);
     return p;
 }
+
 // A visit: steps r0 .. r1 - 1 of chunk n (-1: no more).
 struct Visit {
     int n, r0, r1, flags;
@@ -1050,10 +1074,12 @@ struct Planner {
     int n, r0, r1;
     StepGates gates;
     LoadedGates next;  // of the chunk after this one
-    __device__ __forceinline__ bool beyond(const Args &A) const { return BACK ? n > 0 : n + 1 < A.chunks; }
+    bool cut;  // a document has started
+    __device__ __forceinline__ bool beyond(const Place &at) const { return BACK ? n > at.n0 : n + 1 < at.n1; }
     __device__ __forceinline__ void start(const Args &A, const Place &at)
     {
-        n = BACK ? (int)A.chunks - 1 : 0;
+        n = BACK ? at.n1 - 1 : at.n0;
+        cut = false;
         gates = load_gates<C>(A, at.b, at.h, (int64_t)n * C);
         enter(A, at);
     }
@@ -1061,7 +1087,8 @@ struct Planner {
     {
         r0 = BACK ? document_start(gates.cut, gates.rows) : 0;
         r1 = BACK ? gates.rows : document_end(gates.cut, 0, gates.rows);
-        if (beyond(A)) next = fetch_gates<C>(A, at.b, at.h, (int64_t)(BACK ? n - 1 : n + 1) * C);
+        cut |= gates.cut != 0;
+        if (beyond(at)) next = fetch_gates<C>(A, at.b, at.h, (int64_t)(BACK ? n - 1 : n + 1) * C);
     }
     __device__ __forceinline__ void advance(const Args &A, const Place &at)
     {
@@ -1070,7 +1097,7 @@ struct Planner {
                 r1 = r0, r0 = document_start(gates.cut, r1);
             else
                 r0 = r1, r1 = document_end(gates.cut, r0, gates.rows);
-        } else if (beyond(A)) {
+        } else if (beyond(at)) {
             n += BACK ? -1 : 1;
             gates = use_gates<C>(A, next, (int64_t)n * C);
             enter(A, at);
@@ -1197,13 +1224,13 @@ struct Server {
         k_raw.store(sh.keys[sh.kTwo ? buffer : 0], v.r0, v.r1, A.key, tid);
         if constexpr (QUERIES) q_raw.store(sh.queries, v.r0, v.r1, A.key, tid);
         // (also where the next visit has the same chunk: see the state's wave)
-        load(A, at_, v.leaves() && v.n + 1 < A.chunks ? v.n + 1 : v.n, tid);
+        load(A, at_, v.leaves() && v.n + 1 < at_.n1 ? v.n + 1 : v.n, tid);
     }
     Place at_;
     __device__ __forceinline__ Visit start(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c, int tid)
     {
         at_ = at;
-        load(A, at, 0, tid);
+        load(A, at, at.n0, tid);
         if (c == 0) {
             plan.start(A, at);
             plan.write(sh.visits[0], sh.factors[0]);
@@ -1219,6 +1246,8 @@ struct Server {
         if (c != 0) return;
         plan.advance(A, at_);
         plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
+        if (A.ends && plan.n < 0 && at_.first == 0 && threadIdx.x % kWave == 0)
+            A.cuts[at_.bh * A.segments + at_.seg] = plan.cut;
     }
 };
 template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
@@ -1323,7 +1352,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     using Sl = Slots<C>;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
-    const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
+    const bool has_v = v < A.value, in_row = v < A.value_pad && !A.ends;
     constexpr bool kEarly = DK < 256 && NC == 2 && !OUTPUT;  // registers for all of the keys' operands
     State<DK> S;
     Wide operands[KD], inverse[Sl::kCount];
@@ -1346,10 +1375,16 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         S.store(A.states + (at.bh * A.chunks + n) * DK * A.value_pad, v, in_row, DK, A.value_pad);
     };
 
-    S.load(A.h0 + at.bh * A.key * A.value, v, A.h0 && has_v, A.key, A.value);
-    load_value(0);
-    load_inverse(0);
-    if constexpr (!OUTPUT) keep(0);
+    if (!OUTPUT && A.ends) {
+        S.identity((int)min(v - A.value_pad, (int64_t)A.key));  // zero in the values' columns
+    } else if (A.segments > 1) {
+        S.load(A.marks + (at.bh * A.segments + at.seg) * DK * A.value_pad, v, v < A.value_pad, DK, A.value_pad);
+    } else {
+        S.load(A.h0 + at.bh * A.key * A.value, v, A.h0 && has_v, A.key, A.value);
+    }
+    load_value(at.n0);
+    load_inverse(at.n0);
+    if constexpr (!OUTPUT) keep(at.n0);
     __syncthreads();
     Visit now = read_visit(sh.visits[0]);
     if (now.fresh()) S.zero();
@@ -1361,7 +1396,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         const bool whole = now.r0 == 0 && now.r1 == C;
         // what the next visit reads, also where it is what this one has: a load that
         // may not be under way would have everything behind it waited for
-        const int64_t after = now.leaves() && now.n + 1 < A.chunks ? now.n + 1 : now.n;
+        const int64_t after = now.leaves() && now.n + 1 < at.n1 ? now.n + 1 : now.n;
         f32x4 x[TT];
         f32x4 start[TT], beta[TT];
         typename N::Exact kt[KC][DT];
@@ -1377,11 +1412,11 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         for (int t = 0; t < TT; ++t) {
             const f32x4 val = value.get(t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = beta[t][e] * fmaf_(-start[t][e], x[t][e], val[e]);
+            for (int e = 0; e < 4; ++e) x[t][e] = beta[t][e] * fmaf_(-start[t][e], x[t][e], has_v ? val[e] : 0.0f);
         }
-        if (!whole || !all_v)
+        if (!whole)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, has_v ? now.r0 : C, now.r1);
+            for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
         load_value(after);
         if (!kEarly) read_channels<TF>(kt, K);
         Wide rhs[KC];
@@ -1426,8 +1461,12 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         __syncthreads();
         now = then;
     }
-    if constexpr (OUTPUT)
-        if (A.last) S.store(A.last + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+    if constexpr (OUTPUT) {
+        if (A.last && at.n1 == A.chunks) S.store(A.last + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+    } else if (A.ends) {
+        const int columns = A.value_pad + A.key_pad;
+        S.store(A.maps + (at.bh * A.segments + at.seg) * DK * columns, v, v < columns, DK, columns);
+    }
 }
 template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
 __global__ void __launch_bounds__(Roles<NC>::waves(OUTPUT) * kWave) delta_chain_kernel(Args A)
@@ -1513,7 +1552,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
         q_raw.store(sh.queries[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
     };
     Planner<C, true> plan;
-    const int last = (int)A.chunks - 1;
+    const int last = at.n1 - 1;
     load(last);
     load_go(last);
     if (c == NC - 1) {
@@ -1523,7 +1562,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
     __syncthreads();
     Visit now = read_visit(sh.visits[0]);
     stage(0, now.r0, now.r1);
-    load(now.leaves() && last > 0 ? last - 1 : last);
+    load(now.leaves() && last > at.n0 ? last - 1 : last);
     __syncthreads();
     for (int buffer = 0; now.here(); buffer ^= 1) {
         if (c == NC - 1) {
@@ -1584,7 +1623,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
         const auto prepare = [&]() {
             if (!then.here()) return;
             stage(buffer ^ 1, then.r0, then.r1);
-            load(then.leaves() && then.n > 0 ? then.n - 1 : then.n);
+            load(then.leaves() && then.n > at.n0 ? then.n - 1 : then.n);
         };
         if (sh.kTwo) prepare();
         if (!now.fresh()) {
@@ -1630,7 +1669,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     using Sl = Slots<C>;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
-    const bool has_v = v < A.value, in_row = v < A.value_pad, all_v = 16 * (at.first + c + 1) <= A.value;
+    const bool has_v = v < A.value && !A.ends, in_row = v < A.value_pad && !A.ends, all_v = 16 * (at.first + c + 1) <= A.value;
     auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h + v * A.dv.d;
     constexpr bool kEarly = DK < 256 && NC == 2;
     State<DK> S;
@@ -1650,9 +1689,15 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             for (int d = 0; d < DT; ++d) S.s[d] += sh.by_queries[c][d][lane];
     };
 
-    S.load(A.g_last + at.bh * A.key * A.value, v, A.g_last && has_v, A.key, A.value);
-    load_value(A.chunks - 1);
-    load_inverse(A.chunks - 1);
+    if (A.ends) {
+        S.zero();
+    } else if (A.segments > 1) {
+        S.load(A.marks + (at.bh * A.segments + at.seg) * DK * A.value_pad, v, in_row, DK, A.value_pad);
+    } else {
+        S.load(A.g_last + at.bh * A.key * A.value, v, A.g_last && has_v, A.key, A.value);
+    }
+    load_value(at.n1 - 1);
+    load_inverse(at.n1 - 1);
     __syncthreads();
     Visit now = read_visit(sh.visits[0]);
     __syncthreads();
@@ -1661,7 +1706,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         const Factors<C> &F = sh.factors[buffer];
         const auto &K = sh.keys_of(buffer);
         const bool whole = now.r0 == 0 && now.r1 == C;
-        const int64_t after = now.leaves() && now.n > 0 ? now.n - 1 : now.n;
+        const int64_t after = now.leaves() && now.n > at.n0 ? now.n - 1 : now.n;
         f32x4 x[TT];
         join();
         if (now.enters()) S.store(A.dstates + item * DK * A.value_pad, v, in_row, DK, A.value_pad);
@@ -1736,7 +1781,12 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         now = then;
     }
     join();
-    if (A.dh0) S.store(A.dh0 + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+    if (A.ends) {
+        const int columns = A.value_pad + A.key_pad;
+        S.store(A.maps + (at.bh * A.segments + at.seg) * DK * columns, v, v < A.value_pad, DK, columns);
+    } else if (A.dh0 && at.n0 == 0) {
+        S.store(A.dh0 + at.bh * A.key * A.value, v, has_v, A.key, A.value);
+    }
 }
 template <bool HALF, int DK, int NC, bool TF>
 __global__ void __launch_bounds__(2 * NC * kWave) delta_back_kernel(Args A)
@@ -1756,6 +1806,71 @@ __global__ void __launch_bounds__(2 * NC * kWave) delta_back_kernel(Args A)
         back_state<HALF, DK, NC, TF>(A, sh, at, wave);
     else
         back_helper<HALF, DK, NC, TF>(A, sh, at, wave - NC);
+}
+
+// ------------------------------------------------------------ segments ---
+
+// Long chains of few heads, chained in segments at once.  A segment takes the state
+// S before it to M S + N: with `ends` the forward chain computes N as its end from
+// zero and M, in further columns without values, as its end from the identity; the
+// backward chain's map has M transposed.  This kernel goes along the segments and
+// leaves the state before each (BACK: the state's gradient behind each) in `marks`;
+// then the chains run again from there.  Where a document starts in a segment
+// nothing of S is kept, whatever is in it.  A workgroup for a head and 16 columns,
+// float32 products.
+template <int DK, bool BACK>
+__global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
+{
+    constexpr int DT = DK / 16, kMine = (DT + 3) / 4, kPitch = DK + 4;
+    __shared__ f32x4 state4[16 * kPitch / 4];
+    float *const state = reinterpret_cast<float *>(state4);
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const int tiles = A.value_pad / 16;
+    const int64_t bh = blockIdx.x / tiles, v = 16 * (blockIdx.x % tiles) + col;
+    const int columns = A.value_pad + A.key_pad;
+    const float *const first = BACK ? A.g_last : A.h0;
+    // the state by columns, in LDS: rows of DK channels
+    f32x4 S[kMine];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int d0 = 16 * (wave + 4 * m) + row4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[m][r] = first && d0 + r < A.key && v < A.value ? first[(bh * A.key + d0 + r) * A.value + v] : 0.0f;
+    }
+    for (int i = 0; i < A.segments; ++i) {
+        const int64_t seg = bh * A.segments + (BACK ? A.segments - 1 - i : i);
+        const float *const map = A.maps + seg * DK * columns;
+        const bool cut = A.cuts[seg] != 0;
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int d0 = 16 * (wave + 4 * m) + row4;
+            if (d0 >= DK) break;
+            *reinterpret_cast<f32x4 *>(state + col * kPitch + d0) = S[m];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                A.marks[(seg * DK + d0 + r) * A.value_pad + v] = S[m][r];
+                S[m][r] = map[(int64_t)(d0 + r) * columns + v];
+            }
+        }
+        __syncthreads();
+        if (cut) continue;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int d0 = 16 * (wave + 4 * m);
+            if (d0 >= A.key_pad) break;
+            for (int k0 = 0; k0 < A.key_pad; k0 += 16) {
+                f32x4 a;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int d = d0 + col, k = k0 + row4 + j;
+                    a[j] = map[(int64_t)(BACK ? k : d) * columns + A.value_pad + (BACK ? d : k)];
+                }
+                S[m] = block_mma(S[m], a, four(state + col * kPitch + k0 + row4));
+            }
+        }
+    }
 }
 
 // -------------------------------------------------------- the gradients ---

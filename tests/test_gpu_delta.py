@@ -157,6 +157,47 @@ def test_equal_keys_and_full_rates(half):
         dc.check(last, S, 4 * dc.FORWARD[half], "last")
 
 
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("size,decay,docs", [
+    ((1, 2500, 1, 2, 32, 40), "mild", 0.0), ((1, 4100, 1, 1, 64, 16), "mild", 0.0005), ((2, 2113, 1, 1, 100, 33), "none", 0.0),
+    ((1, 3000, 1, 3, 200, 20), "mild", 0.002), ((1, 2300, 2, 2, 16, 16), "forget", 0.0), ((1, 2048, 1, 1, 128, 128), "mild", 0.02)])
+def test_long_chains_of_few_heads(size, decay, docs, half):
+    """Chained in segments at once: from their maps the state before each."""
+    c = dc.inputs(*size, half, decay=decay, docs=docs)
+    t = dc.tensors(c, half, "channel", DEV)
+    if decay == "mild":  # long memory, so that a segment's state matters to the next
+        c["log_decay"] = np.float32(0.02 * c["log_decay"]).astype(np.float64)
+        t["log_decay"] = torch.from_numpy(np.float32(c["log_decay"])).to(DEV)
+    args = [t[n] for n in ("q", "k", "v", "beta", "log_decay", "h0")]
+    o, last = pr.delta_scan(*args, resets=t["resets"])
+    scale = size[4] ** -0.5
+    want, S = dc.oracle(c, scale)
+    dc.check(o, want, dc.FORWARD[half], "o")
+    dc.check(last, S, dc.FORWARD[half], "last")
+    out = pr.delta_scan_adjoint(*args, t["go"], g_last=t["g_last"], resets=t["resets"])
+    check_gradients(out, dc.oracle(c, scale, True), half)
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_segments_of_a_document_that_is_not_finite(half):
+    """NaN in the first of two documents, many segments long: nothing of it in the second."""
+    c = dc.inputs(1, 4000, 1, 1, 32, 32, half)
+    c["resets"] = np.arange(4000)[None] == 2001
+    t = dc.tensors(c, half, "channel", DEV)
+    args = [t[n] for n in ("q", "k", "v", "beta", "log_decay", "h0")]
+
+    def run():
+        o, last = pr.delta_scan(*args, resets=t["resets"])
+        return o, last, pr.delta_scan_adjoint(*args, t["go"], g_last=t["g_last"], resets=t["resets"])
+    good = run()
+    t["v"][..., :2001] = float("nan")
+    t["go"][..., :2001] = float("inf")
+    got = run()
+    assert torch.equal(good[0][..., 2001:], got[0][..., 2001:]) and torch.equal(good[1], got[1])
+    for n in ("dq", "dk", "dv", "dbeta", "dlog_decay"):
+        assert torch.equal(good[2][n][..., 2001:], got[2][n][..., 2001:]), n
+
+
 def test_no_gradients_given_and_empty():
     c = dc.inputs(1, 70, 1, 1, 16, 16, True)
     t = dc.tensors(c, True, "channel", DEV)

@@ -184,11 +184,26 @@ __device__ __forceinline__ void mma_rows(f32x4 (&c)[M], const A (&a)[M], const B
 template <int M>
 __device__ __forceinline__ void settle(f32x4 (&x)[M])
 {
-    static_assert(M == 2 || M == 4, "one statement for all");
+    static_assert(M == 1 || M == 2 || M == 4, "one statement for all");
     if constexpr (M == 4)
         asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]));
-    else
+    else if constexpr (M == 2)
         asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]));
+    else
+        asm volatile("s_nop 9" : "+v"(x[0]));
+}
+
+// A stride as if it were new here: what a rare path makes of it is then computed
+// there, and not kept in registers through the loops around.
+__device__ __forceinline__ int64_t afresh(int64_t stride)
+{
+    asm volatile("" : "+s"(stride));
+    return stride;
+}
+__device__ __forceinline__ int lane_afresh(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
 }
 
 // Two float32 as the bfloat16 next to them and the ones next to what that leaves.
@@ -438,6 +453,8 @@ struct Pieces {
             }
             return;
         }
+        const int64_t by_d = afresh(x.d), by_t = afresh(x.t), last = afresh(T) - 1;
+        const int top = (int)afresh(key) - 1;
 #pragma unroll
         for (int n = 0; n < kCount; ++n) {
             const int d = d0 + (TF ? row + n * kRows : col);
@@ -445,8 +462,8 @@ struct Pieces {
             uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int de = min(TF ? d : d + e, key - 1);
-                const uint32_t v = element(base + de * x.d + min(TF ? t + e : t, T - 1) * x.t);
+                const int de = min(TF ? d : d + e, top);
+                const uint32_t v = element(base + de * by_d + min(TF ? t + e : t, last) * by_t);
                 if constexpr (HALF)
                     w[e / 2] |= v << (16 * (e % 2));
                 else
@@ -568,6 +585,7 @@ __device__ __forceinline__ void store_column(typename Num<HALF>::Elem *base, int
             *reinterpret_cast<Words4Any *>(base + t) = w;
         }
     } else {
+        step = afresh(step);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (whole || (t + r >= r0 && t + r < r1)) store_gate<HALF>(base, (t + r) * step, x[r]);
@@ -1498,12 +1516,12 @@ __global__ void __launch_bounds__(Roles<NC>::waves(OUTPUT) * kWave) delta_chain_
 }
 
 // Sums over the 16 lanes of a group, of M values each: at the end a lane holds
-// the sum of value `which`, for M = 8 two lanes the same one.  Half of the values
-// go to the neighbour at each step.
+// the sum of value `which` (with M < 16 several lanes the same one).  Half of the
+// values go to the neighbour at each step.
 template <int M>
 __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 {
-    static_assert(M == 16 || M == 8, "one or two lanes a value");
+    static_assert(M == 16 || M == 8 || M == 4, "halves");
     const int lane = threadIdx.x % kWave;
     which = 0;
     const auto halve = [&](auto half, int bit) {
@@ -1513,13 +1531,12 @@ __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 #pragma unroll
         for (int i = 0; i < m; ++i) x[i] = (upper ? x[i + m] : x[i]) + __shfl_xor(upper ? x[i] : x[i + m], bit);
     };
-    if constexpr (M == 16) {
-        halve(std::integral_constant<int, 8>(), 8);
-    }
-    halve(std::integral_constant<int, 4>(), 1);
-    halve(std::integral_constant<int, 2>(), 2);
-    halve(std::integral_constant<int, 1>(), 4);
-    if constexpr (M == 8) x[0] += __shfl_xor(x[0], 8);
+    if constexpr (M == 16) halve(std::integral_constant<int, 8>(), 8);
+    if constexpr (M >= 8) halve(std::integral_constant<int, 4>(), 4);
+    halve(std::integral_constant<int, 2>(), 1);
+    halve(std::integral_constant<int, 1>(), 2);
+    if constexpr (M <= 4) x[0] += __shfl_xor(x[0], 4);
+    if constexpr (M <= 8) x[0] += __shfl_xor(x[0], 8);
     return x[0];
 }
 
@@ -1873,6 +1890,25 @@ __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
     }
 }
 
+// Four steps t .. t + 3 of channel d of a tile of queries or keys.
+template <bool TF, bool HALF, int ROWS, int COLS>
+__device__ __forceinline__ f32x4 steps_of(const Tile<HALF, ROWS, COLS> &x, int d, int t)
+{
+    f32x4 r;
+    if constexpr (TF && HALF) {
+        uint32_t w[2];
+        __builtin_memcpy(w, x.at + d * x.kPitch + t, 8);
+        r = f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                  __uint_as_float(w[1] & 0xffff0000u)};
+    } else if constexpr (TF) {
+        r = four(x.at + d * x.kPitch + t);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = load_gate<HALF>(x.at, (t + e) * x.kPitch + d);
+    }
+    return r;
+}
+
 // -------------------------------------------------------- the gradients ---
 
 // A workgroup for a key head's chunk: for each value head that shares it, with
@@ -1887,42 +1923,59 @@ __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
 //     dG_i = scale exp(G_i) q_i . U_i - b_i exp(G_i) k_i . Y_i - z_i
 //            + sum_j B_ij - sum_j B_ji,  B_ij = E_ij (q_i . k_j) + b_i H_ij (k_i . k_j),
 //     z_i = exp(G_C - G_i) k_i . Z_i,  dG_C += sum_i z_i + exp(G_C) <S, dS'>.
+// Two halves of the steps by four parts of the channels: a wave's rows of dO, X and
+// W are read once for all its channels (a wave for a part of the channels and all
+// steps reads twice as much from LDS, which bounds it then).  32 columns of the
+// values at a time; the next ones are loaded meanwhile.  SHARED: several value heads
+// share a key head, whose gradients are summed in registers.
 template <bool HALF, int DK, bool TF>
+struct Gradients {
+    using N = Num<HALF>;
+    static constexpr int C = N::kChunk, TT = C / 16, DT = DK / 16, VB = 32, kT = 2, kD = 4, kPairs = TT * kD;
+    using In = Pieces<HALF, DK, TF, kThreads>;
+    typename In::Lds keys, queries;
+    union {
+        struct {
+            WideTile<HALF, TF ? VB : C, TF ? C : VB> out;
+            WideTile<HALF, C, VB> x, w;
+        } block[2];
+        struct {
+            WideTile<HALF, C, C> e, h;  // E and b H by columns
+        } t;
+    };
+    Factors<C> F;
+    float row_sum[kPairs * 16], col_sum[kPairs * 16], h_sum[kPairs * 16];
+    float dots[3][kD][C], xv[C], inner[kWaves];
+};
+template <bool HALF, int DK, bool TF, bool SHARED>
 __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
-    constexpr int C = N::kChunk, TT = C / 16, DT = DK / 16, kPairs = TT * (TT + 1) / 2;
-    constexpr int kD = DT < kWaves ? DT : kWaves, kT = kWaves / kD;  // waves along channels and steps
-    constexpr int ND = DT / kD, NT = TT / kT, NP = (kPairs + kWaves - 1) / kWaves;
-    static_assert(ND * kD == DT && NT * kT == TT, "whole tiles a wave");
-    constexpr int VB = 32;  // columns of the values at a time
-    using In = Pieces<HALF, DK, TF, kThreads>;
-    __shared__ typename In::Lds keys, queries;
-    __shared__ WideTile<HALF, C, C> e_t, h_t;  // E and b H by columns
-    __shared__ WideTile<HALF, TF ? VB : C, TF ? C : VB> out;
-    __shared__ WideTile<HALF, C, VB> xs, ws;
-    __shared__ Factors<C> F;
-    __shared__ float row_sum[kPairs * 16], col_sum[kPairs * 16], h_sum[kPairs * 16];
-    __shared__ float dots[3][kD][C], inner[kWaves];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
-    const int64_t n = blockIdx.x % A.chunks, bk = blockIdx.x / A.chunks, b = bk / A.Hk, hk = bk % A.Hk;
-    const int64_t t0 = n * C;
-    const int group = A.Hv / A.Hk;
-    const int wd = 16 * ND * (wave % kD), wt = 16 * NT * (wave / kD);  // the wave's first channel and step
+    using Exact = typename N::Exact;
+    using L = Gradients<HALF, DK, TF>;
+    using In = typename L::In;
+    using Sl = Slots<N::kChunk>;
+    constexpr int C = L::C, TT = L::TT, KC = C / 32, KD = DK / 32, kT = L::kT, kD = L::kD, VB = L::VB;
+    constexpr int ND = L::DT / kD, NT = TT / kT;
+    constexpr bool kAhead = ND <= 2;  // registers for the next states' parts
+    __shared__ L sh;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), pd = wave % kD, pt = wave / kD;
+    const unsigned chunks = (unsigned)A.chunks, heads = (unsigned)A.Hk, bk = blockIdx.x / chunks;
+    const int64_t n = blockIdx.x % chunks, b = bk / heads, hk = bk % heads, t0 = n * C;
+    const int group = SHARED ? A.Hv / A.Hk : 1;
+    const int wd = 16 * ND * pd, wt = 16 * NT * pt;  // the wave's first channel and step
     using Elem = typename N::Elem;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    Elem *const dq_at = static_cast<Elem *>(A.dq.p) + b * A.dq.b + hk * A.dq.h + t0 * A.dq.t;
+    Elem *const dk_at = static_cast<Elem *>(A.dk.p) + b * A.dk.b + hk * A.dk.h + t0 * A.dk.t;
 
-    In k_raw, q_raw;
-    k_raw.load(A.k, static_cast<const Elem *>(A.k.p) + b * A.k.b + hk * A.k.h, 0, t0, A.key, A.T, threadIdx.x);
-    q_raw.load(A.q, static_cast<const Elem *>(A.q.p) + b * A.q.b + hk * A.q.h, 0, t0, A.key, A.T, threadIdx.x);
-    clear(e_t);
-    clear(h_t);
-    f32x4 dq[NT][ND], dk[NT][ND];
+    [[maybe_unused]] f32x4 dq[NT][ND], dk[NT][ND];
+    if constexpr (SHARED)
 #pragma unroll
-    for (int a = 0; a < NT; ++a)
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
-        for (int c = 0; c < ND; ++c) dq[a][c] = dk[a][c] = zero;
+            for (int c = 0; c < ND; ++c) dq[a][c] = dk[a][c] = zero;
     for (int head = 0; head < group; ++head) {
         const int64_t h = hk * group + head, bh = b * A.Hv + h, item = bh * A.chunks + n;
         const StepGates gates = load_gates<C>(A, b, h, t0);
@@ -1930,228 +1983,313 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
         const float *const s_behind = A.dstates + item * DK * A.value_pad;
         for (int r0 = 0, r1; r0 < gates.rows; r0 = r1) {
             r1 = document_end(gates.cut, r0, gates.rows);
-            const bool before = !(gates.cut >> r0 & 1), behind = r1 == gates.rows;
-            __syncthreads();
-            k_raw.store(keys, r0, r1, A.key, threadIdx.x);
-            q_raw.store(queries, r0, r1, A.key, threadIdx.x);
-            if (wave == 0) write_factors(F, gates, r0, r1);
-
-            f32x4 U[NT][ND], Y[NT][ND], Z[NT][ND], ow[NP], xw[NP];
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int c = 0; c < ND; ++c) U[a][c] = Y[a][c] = Z[a][c] = zero;
-#pragma unroll
-            for (int m = 0; m < NP; ++m) ow[m] = xw[m] = zero;
-            float ss = 0.0f;
-            for (int v0 = 0; v0 < A.value; v0 += VB) {
-                __syncthreads();
-                for (int u = threadIdx.x; u < C * VB / 4; u += kThreads) {
-                    const int row = u / (VB / 4), v4 = u % (VB / 4) * 4;
-                    f32x4 x = zero, w = zero;
-                    if (row >= r0 && row < r1) {
-                        const int64_t at = (item * C + row) * A.value_pad + v0 + v4;
-                        x = four(A.x + at);
-                        w = four(A.w + at);
-                    }
-                    store4(xs, row, v4, x);
-                    store4(ws, row, v4, w);
-                    x = zero;
+            const int lane = lane_afresh(threadIdx.x % kWave), row4 = 4 * (lane / 16), col = lane % 16;
+            const bool before = !(gates.cut >> r0 & 1), behind = r1 == gates.rows, whole = r0 == 0 && r1 == C;
+            // a block of columns as loaded: a piece a thread, and the states' operands
+            constexpr bool kAll = C * VB / 4 == kThreads;  // a piece for every thread
+            const int u = wave * kWave + lane, row = u / (VB / 4), v4 = u % (VB / 4) * 4;
+            const bool loads = kAll || u < C * VB / 4, mine = loads && row >= r0 && row < r1;
+            f32x4 xr, wr, orr, sr[ND][2], gr[ND][2];
+            const auto load_block = [&](int v0) {
+                const int64_t at = (item * C + min(row, C - 1)) * A.value_pad + v0 + v4;
+                xr = four(A.x + at);
+                wr = four(A.w + at);
+                orr = zero;
+                if (A.o.p && loads) {
                     if constexpr (TF) {
                         const int v = u / (C / 4), t4 = u % (C / 4) * 4;
-                        if (A.o.p && v0 + v < A.value)
-                            x = load_four(head_of<false>(A.o, b, h) + (v0 + v) * A.o.d + (t0 + t4) * A.o.t, A.o.t,
-                                          r0 - t4, r1 - t4);
-                        store4(out, v, t4, only_steps(x, t4, r0, r1));
+                        const float *p = head_of<false>(A.o, b, h) + min(v0 + v, A.value - 1) * A.o.d + t0 * A.o.t;
+                        if (A.o.t == 1 && t0 + C <= A.T) {
+                            const Words4 q = *reinterpret_cast<const Words4Any *>(p + t4);
+                            orr = __builtin_bit_cast(f32x4, q);
+                        } else {
+                            const int64_t step = afresh(A.o.t);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) orr[e] = p[min((int64_t)t4 + e, A.T - 1 - t0) * step];
+                        }
                     } else {
-                        if (A.o.p && row >= r0 && row < r1)
-                            x = load_four(head_of<false>(A.o, b, h) + (v0 + v4) * A.o.d + (t0 + row) * A.o.t, A.o.d, 0,
-                                          A.value - v0 - v4);
-                        store4(out, row, v4, x);
+                        const float *p = head_of<false>(A.o, b, h) + (t0 + min((int64_t)row, A.T - 1 - t0)) * A.o.t;
+                        if (A.o.d == 1 && v0 + VB <= A.value) {
+                            const Words4 q = *reinterpret_cast<const Words4Any *>(p + v0 + v4);
+                            orr = __builtin_bit_cast(f32x4, q);
+                        } else {
+                            const int64_t step = afresh(A.o.d);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) orr[e] = p[min(v0 + v4 + e, A.value - 1) * step];
+                        }
                     }
                 }
-                __syncthreads();
+            };
+            const auto load_states = [&](int v0) {
 #pragma unroll
                 for (int c = 0; c < ND; ++c) {
                     const int64_t at = (int64_t)(wd + 16 * c + col) * A.value_pad + v0 + row4;
-                    float s[8], g[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        const f32x4 p = before ? four(s_before + at + 4 * j) : zero;
-                        const f32x4 q = behind ? four(s_behind + at + 4 * j) : zero;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            s[j + e] = p[e];
-                            g[j + e] = q[e];
-                            ss = fmaf_(p[e], q[e], ss);
-                        }
-                    }
-                    const Wide sw = split(s, Wide()), gw = split(g, Wide());
-#pragma unroll
-                    for (int a = 0; a < NT; ++a) {
-                        U[a][c] = mma(U[a][c], operand<!TF>(out, wt + 16 * a, 0), sw);
-                        Y[a][c] = mma(Y[a][c], operand<true>(xs, wt + 16 * a, 0), sw);
-                        Z[a][c] = mma(Z[a][c], operand<true>(ws, wt + 16 * a, 0), gw);
+                    for (int i = 0; i < 2; ++i) {
+                        sr[c][i] = four(s_before + at + 16 * i);
+                        gr[c][i] = four(s_behind + at + 16 * i);
                     }
                 }
+            };
+            const auto store_block = [&](int buffer, int v0) {
+                if (!loads) return;
+                auto &B = sh.block[buffer];
+                store4(B.x, row, v4, mine ? xr : zero);
+                store4(B.w, row, v4, mine ? wr : zero);
+                if constexpr (TF) {
+                    const int v = u / (C / 4), t4 = u % (C / 4) * 4;
+                    f32x4 o = v0 + v < A.value ? orr : zero;
+                    if (!whole) o = only_steps(o, t4, r0, r1);
+                    store4(B.out, v, t4, o);
+                } else {
+                    f32x4 o;
 #pragma unroll
-                for (int m = 0; m < NP; ++m) {
-                    const int p = wave + kWaves * m;
-                    if (p >= kPairs) break;
-                    int it, jt;
-                    lower_pair(p, it, jt);
-                    const Wide w = operand<true>(ws, 16 * jt, 0);
-                    ow[m] = mma(ow[m], operand<!TF>(out, 16 * it, 0), w);
-                    xw[m] = mma(xw[m], operand<true>(xs, 16 * it, 0), w);
+                    for (int e = 0; e < 4; ++e) o[e] = mine && v0 + v4 + e < A.value ? orr[e] : 0.0f;
+                    store4(B.out, row, v4, o);
+                }
+            };
+            {
+                In k_raw, q_raw;
+                k_raw.load(A.k, head_of<HALF>(A.k, b, hk), 0, t0, A.key, A.T, u);
+                q_raw.load(A.q, head_of<HALF>(A.q, b, hk), 0, t0, A.key, A.T, u);
+                load_block(0);
+                if (kAhead) load_states(0);
+                // X_i . v_i: eight lanes for a step, from its parts of 16 columns
+                const int r = u / 8, parts = A.value_pad / 16;
+                const float *const p = A.xv + (item * C + min(r, C - 1)) * parts;
+                const int j = u % 8;
+                const float first = p[min(j, parts - 1)], second = p[min(j + 8, parts - 1)];
+                __syncthreads();
+                k_raw.store(sh.keys, r0, r1, A.key, u);
+                q_raw.store(sh.queries, r0, r1, A.key, u);
+                float xv = (16 * j < A.value ? first : 0.0f) + (16 * (j + 8) < A.value ? second : 0.0f);
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2) xv += __shfl_xor(xv, o);
+                if (j == 0 && r < C) sh.xv[r] = xv;
+            }
+            if (wave == 0) write_factors(sh.F, gates, r0, r1);
+            const Factors<C> &F = sh.F;
+
+            f32x4 U[NT][ND], Y[NT][ND], Z[NT][ND], ow[NT], xw[NT];
+#pragma unroll
+            for (int a = 0; a < NT; ++a) {
+                ow[a] = xw[a] = zero;
+#pragma unroll
+                for (int c = 0; c < ND; ++c) U[a][c] = Y[a][c] = Z[a][c] = zero;
+            }
+            float ss = 0.0f;
+            for (int v0 = 0, buffer = 0; v0 < A.value; v0 += VB, buffer ^= 1) {
+                store_block(buffer, v0);
+                if (!kAhead) load_states(v0);
+                Wide sw[ND], gw[ND];
+#pragma unroll
+                for (int c = 0; c < ND; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!before) sr[c][i] = zero;
+                        if (!behind) gr[c][i] = zero;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ss = fmaf_(sr[c][i][e], gr[c][i][e], ss);
+                    }
+                    sw[c] = stacked<HALF>(sr[c][0], sr[c][1]);
+                    gw[c] = stacked<HALF>(gr[c][0], gr[c][1]);
+                }
+                __syncthreads();
+                if (v0 + VB < A.value) {
+                    load_block(v0 + VB);
+                    if (kAhead) load_states(v0 + VB);
+                }
+                const auto &B = sh.block[buffer];
+                const Wide wj = operand<true>(B.w, 16 * (pd < TT ? pd : 0), 0);
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    using P = Product<Wide, Wide>;
+                    const Wide oo = operand<!TF>(B.out, wt + 16 * a, 0), xo = operand<true>(B.x, wt + 16 * a, 0),
+                               wo = operand<true>(B.w, wt + 16 * a, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < P::kParts; ++i) {
+#pragma unroll
+                        for (int c = 0; c < ND; ++c) {
+                            U[a][c] = P::part(i, U[a][c], oo, sw[c]);
+                            Y[a][c] = P::part(i, Y[a][c], xo, sw[c]);
+                            Z[a][c] = P::part(i, Z[a][c], wo, gw[c]);
+                        }
+                        ow[a] = P::part(i, ow[a], oo, wj);
+                        xw[a] = P::part(i, xw[a], xo, wj);
+                    }
                 }
             }
+            settle(ow);
+            settle(xw);
 
-            // E and H, and the sums of their rows and columns
+            // E and H of the wave's rows and 16 columns, the sums of their rows and
+            // columns (the LDS of the blocks is theirs from here)
+            __syncthreads();
+            for (int i = u; i < (int)(sizeof(sh.t) / 16); i += kThreads)
+                reinterpret_cast<uint4 *>(&sh.t)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
 #pragma unroll
-            for (int m = 0; m < NP; ++m) {
-                const int p = wave + kWaves * m;
-                if (p >= kPairs) break;
-                int it, jt;
-                lower_pair(p, it, jt);
-                it *= 16, jt *= 16;
-                f32x4 qk = zero, kk = zero;
+            for (int a = 0; a < NT; ++a) {
+                const int it = pt * NT + a, jt = pd;
+                if (jt > it) continue;
+                f32x4 qk[1] = {zero}, kk[1] = {zero};
+                Exact kj[KD], qi[KD], ki[KD];
 #pragma unroll
-                for (int d = 0; d < DK; d += 32) {
-                    const auto kj = operand<!TF>(keys, jt, d);
-                    qk = mma(qk, operand<!TF>(queries, it, d), kj);
-                    kk = mma(kk, operand<!TF>(keys, it, d), kj);
+                for (int d = 0; d < KD; ++d) {
+                    kj[d] = operand<!TF>(sh.keys, 16 * jt, 32 * d);
+                    qi[d] = operand<!TF>(sh.queries, 16 * it, 32 * d);
+                    ki[d] = operand<!TF>(sh.keys, 16 * it, 32 * d);
                 }
-                const int i = it + row4, j = jt + col;
-                const f32x4 beta = four(F.beta + i);
-                f32x4 E, H, hs, bs;
-                float cs = 0.0f;
-                const f32x4 d = decays_from(F, i, j);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < KD; ++d) {
+                    qk[0] = mma(qk[0], qi[d], kj[d]);
+                    kk[0] = mma(kk[0], ki[d], kj[d]);
+                }
+                const int i = 16 * it + row4, j = 16 * jt + col, p = (it * kD + jt) * 16;
+                const f32x4 beta = four(F.beta + i), d = decays_from(F, i, j);
+                f32x4 E, H;
+                float hs[4], bs[4], cs = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool mine = i + e >= r0 && i + e < r1 && j >= r0 && j <= i + e;
-                    E[e] = mine ? A.scale * ow[m][e] * d[e] : 0.0f;
-                    H[e] = mine && j < i + e ? -xw[m][e] * d[e] : 0.0f;
-                    hs[e] = mine ? H[e] * kk[e] : 0.0f;
-                    bs[e] = mine ? fmaf_(E[e], qk[e], beta[e] * hs[e]) : 0.0f;
+                    const bool in = i + e >= r0 && i + e < r1 && j >= r0 && j <= i + e;
+                    E[e] = in ? A.scale * ow[a][e] * d[e] : 0.0f;
+                    H[e] = in && j < i + e ? -xw[a][e] * d[e] : 0.0f;
+                    hs[e] = in ? H[e] * kk[0][e] : 0.0f;
+                    bs[e] = in ? fmaf_(E[e], qk[0][e], beta[e] * hs[e]) : 0.0f;
                     H[e] *= beta[e];
                     cs += bs[e];
                 }
-                store4(e_t, j, i, E);
-                store4(h_t, j, i, H);
-#pragma unroll
-                for (int o = 1; o < 16; o *= 2)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        hs[e] += __shfl_xor(hs[e], o);
-                        bs[e] += __shfl_xor(bs[e], o);
-                    }
+                store4(sh.t.e, j, i, E);
+                store4(sh.t.h, j, i, H);
+                int which;
+                const float hsum = sum_columns(hs, which), bsum = sum_columns(bs, which);
+                sh.h_sum[p + row4 + which] = hsum;
+                sh.row_sum[p + row4 + which] = bsum;
                 cs += __shfl_xor(cs, 16);
                 cs += __shfl_xor(cs, 32);
-                if (col == 0) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h_sum[p * 16 + row4 + e] = hs[e];
-                        row_sum[p * 16 + row4 + e] = bs[e];
-                    }
-                }
-                if (lane < 16) col_sum[p * 16 + lane] = cs;
+                if (lane < 16) sh.col_sum[p + lane] = cs;
             }
             // the rows' products with U, Y and Z, and these as the gradients' first parts
+            {
+                float qu[4 * NT], ky[4 * NT], kz[4 * NT];
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    const int t = wt + 16 * a + row4;
+                    const f32x4 start = four(F.start + t), end = four(F.end + t), beta = four(F.beta + t);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qu[4 * a + e] = ky[4 * a + e] = kz[4 * a + e] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < ND; ++c) {
+                        const f32x4 q = steps_of<TF>(sh.queries, wd + 16 * c + col, t);
+                        const f32x4 k = steps_of<TF>(sh.keys, wd + 16 * c + col, t);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            qu[4 * a + e] = fmaf_(q[e], U[a][c][e], qu[4 * a + e]);
+                            ky[4 * a + e] = fmaf_(k[e], Y[a][c][e], ky[4 * a + e]);
+                            kz[4 * a + e] = fmaf_(k[e], Z[a][c][e], kz[4 * a + e]);
+                        }
+                        U[a][c] *= A.scale * start;
+                        Z[a][c] = end * Z[a][c] - beta * start * Y[a][c];
+                    }
+                }
+                int which;
+                const float sums[3] = {sum_columns(qu, which), sum_columns(ky, which), sum_columns(kz, which)};
+                const int t = wt + 16 * (which / 4) + row4 + which % 4;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) sh.dots[i][pd][t] = sums[i];
+            }
+            if (pt != 0) ss = 0.0f;  // another wave's channels
+#pragma unroll
+            for (int o = 1; o < kWave; o *= 2) ss += __shfl_xor(ss, o);
+            if (lane == 0) sh.inner[wave] = ss;
+            __syncthreads();
+
+            Exact kt[KC][ND], qt[KC][ND];
+#pragma unroll
+            for (int s = 0; s < KC; ++s)
+#pragma unroll
+                for (int c = 0; c < ND; ++c) {
+                    kt[s][c] = operand<TF>(sh.keys, wd + 16 * c, 32 * s);
+                    qt[s][c] = operand<TF>(sh.queries, wd + 16 * c, 32 * s);
+                }
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                const int t = wt + 16 * a + row4;
-                const f32x4 start = four(F.start + t), end = four(F.end + t), beta = four(F.beta + t);
-                f32x4 qu = zero, ky = zero, kz = zero;
+                const int t = wt + 16 * a, tile = pt * NT + a;
+                using P = Product<Wide, Exact>;
 #pragma unroll
-                for (int c = 0; c < ND; ++c)
+                for (int s = 0; s < KC; ++s) {
+                    if (Sl::in_lower(tile, s)) {
+                        const Wide e = operand<false>(sh.t.e, t, 32 * s), h = operand<false>(sh.t.h, t, 32 * s);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = wd + 16 * c + col;
-                        const int at = TF ? d * In::Lds::kPitch + t + e : (t + e) * In::Lds::kPitch + d;
-                        const float q = load_gate<HALF>(queries.at, at), k = load_gate<HALF>(keys.at, at);
-                        qu[e] = fmaf_(q, U[a][c][e], qu[e]);
-                        ky[e] = fmaf_(k, Y[a][c][e], ky[e]);
-                        kz[e] = fmaf_(k, Z[a][c][e], kz[e]);
-                        U[a][c][e] *= A.scale * start[e];
-                        Z[a][c][e] = end[e] * Z[a][c][e] - beta[e] * start[e] * Y[a][c][e];
+                        for (int i = 0; i < P::kParts; ++i)
+#pragma unroll
+                            for (int c = 0; c < ND; ++c) {
+                                U[a][c] = P::part(i, U[a][c], e, kt[s][c]);
+                                Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
+                            }
                     }
+                    if (Sl::in_upper(tile, s)) {
+                        const Wide e = operand<true>(sh.t.e, t, 32 * s), h = operand<true>(sh.t.h, t, 32 * s);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                        for (int i = 0; i < P::kParts; ++i)
 #pragma unroll
-                    for (int o = 1; o < 16; o *= 2) {
-                        qu[e] += __shfl_xor(qu[e], o);
-                        ky[e] += __shfl_xor(ky[e], o);
-                        kz[e] += __shfl_xor(kz[e], o);
-                    }
-                    if (col == 0) {
-                        dots[0][wave % kD][t + e] = qu[e];
-                        dots[1][wave % kD][t + e] = ky[e];
-                        dots[2][wave % kD][t + e] = kz[e];
+                            for (int c = 0; c < ND; ++c) {
+                                Z[a][c] = P::part(i, Z[a][c], e, qt[s][c]);
+                                Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
+                            }
                     }
                 }
             }
-            if (wt != 0) ss = 0.0f;  // another wave's channels
 #pragma unroll
-            for (int o = 1; o < kWave; o *= 2) ss += __shfl_xor(ss, o);
-            if (lane == 0) inner[wave] = ss;
-            __syncthreads();
-
+            for (int c = 0; c < ND; ++c) {
+                const int64_t q_step = afresh(A.dq.d), k_step = afresh(A.dk.d);
+                f32x4 rows[2][NT];
 #pragma unroll
-            for (int a = 0; a < NT; ++a) {
-                const int t = wt + 16 * a;
+                for (int a = 0; a < NT; ++a) rows[0][a] = U[a][c], rows[1][a] = Z[a][c];
+                settle(rows[0]);
+                settle(rows[1]);
+                const int d = wd + 16 * c + col;
 #pragma unroll
-                for (int c = 0; c < ND; ++c) {
-                    const int d = wd + 16 * c;
-#pragma unroll
-                    for (int s = 0; s < C; s += 32) {
-                        const auto k = operand<TF>(keys, d, s);
-                        if (s <= t) {
-                            U[a][c] = mma(U[a][c], operand<false>(e_t, t, s), k);
-                            Z[a][c] = mma(Z[a][c], operand<false>(h_t, t, s), k);
-                        }
-                        if (s + 32 > t) {
-                            Z[a][c] = mma(Z[a][c], operand<true>(e_t, t, s), operand<TF>(queries, d, s));
-                            Z[a][c] = mma(Z[a][c], operand<true>(h_t, t, s), k);
-                        }
-                    }
-                    const f32x4 u = only_steps(U[a][c], t + row4, r0, r1), z = only_steps(Z[a][c], t + row4, r0, r1);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dq[a][c][e] += u[e];
-                        dk[a][c][e] += z[e];
+                for (int a = 0; a < NT; ++a) {
+                    if constexpr (SHARED) {
+                        dq[a][c] += only_steps(rows[0][a], wt + 16 * a + row4, r0, r1);
+                        dk[a][c] += only_steps(rows[1][a], wt + 16 * a + row4, r0, r1);
+                    } else if (d < A.key) {
+                        store_column<HALF>(dq_at + d * q_step, A.dq.t, wt + 16 * a + row4, r0, r1, whole, rows[0][a]);
+                        store_column<HALF>(dk_at + d * k_step, A.dk.t, wt + 16 * a + row4, r0, r1, whole, rows[1][a]);
                     }
                 }
             }
             if (wave == 0) {
                 const int row = lane;
-                const bool mine = row >= r0 && row < r1;
+                const bool in = row >= r0 && row < r1;
                 double dG = 0.0, z = 0.0;
-                if (mine) {
+                if (in) {
                     const int tile = row / 16;
-                    float qu = 0.0f, ky = 0.0f, kz = 0.0f, hs = 0.0f, xv = 0.0f;
+                    float qu = 0.0f, ky = 0.0f, kz = 0.0f, hs = 0.0f;
                     for (int w = 0; w < kD; ++w) {
-                        qu += dots[0][w][row];
-                        ky += dots[1][w][row];
-                        kz += dots[2][w][row];
+                        qu += sh.dots[0][w][row];
+                        ky += sh.dots[1][w][row];
+                        kz += sh.dots[2][w][row];
                     }
                     for (int j = 0; j <= tile; ++j) {
-                        const int p = (tile * (tile + 1) / 2 + j) * 16 + row % 16;
-                        hs += h_sum[p];
-                        dG += row_sum[p];
+                        hs += sh.h_sum[(tile * kD + j) * 16 + row % 16];
+                        dG += sh.row_sum[(tile * kD + j) * 16 + row % 16];
                     }
-                    for (int i = tile; i < TT; ++i) dG -= col_sum[(i * (i + 1) / 2 + tile) * 16 + row % 16];
-                    for (int j = 0; j < (A.value + 15) / 16; ++j) xv += A.xv[(item * C + row) * (A.value_pad / 16) + j];
+                    for (int i = tile; i < TT; ++i) dG -= sh.col_sum[(i * kD + tile) * 16 + row % 16];
                     const float y = F.start[row] * ky;
                     z = (double)F.end[row] * kz;
                     dG += (double)(A.scale * F.start[row]) * qu - (double)F.beta[row] * y - z;
-                    A.dbeta[bh * A.T + t0 + row] = xv - y + hs;
+                    A.dbeta[bh * A.T + t0 + row] = sh.xv[row] - y + hs;
                 }
                 double all = z, suffix;
 #pragma unroll
                 for (int o = 1; o < kWave; o *= 2) all += __shfl_xor(all, o);
                 if (row == r1 - 1) {
                     double inside = 0.0;
-                    for (int w = 0; w < kWaves; ++w) inside += inner[w];
+                    for (int w = 0; w < kWaves; ++w) inside += sh.inner[w];
                     dG += all + (double)F.across[0] * inside;
                 }
                 suffix = dG;
@@ -2160,26 +2298,24 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                     const double after = __shfl_down(suffix, o);
                     if (row + o < kWave) suffix += after;
                 }
-                if (mine && A.ddecay) A.ddecay[bh * A.T + t0 + row] = gates.cut >> row & 1 ? 0.0f : (float)suffix;
+                if (in && A.ddecay) A.ddecay[bh * A.T + t0 + row] = gates.cut >> row & 1 ? 0.0f : (float)suffix;
             }
         }
     }
-    const int64_t dq_at = b * A.dq.b + hk * A.dq.h, dk_at = b * A.dk.b + hk * A.dk.h;
-#pragma unroll
-    for (int a = 0; a < NT; ++a)
+    if constexpr (SHARED) {
+        const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+        const int rows = (int)min((int64_t)C, A.T - t0);
 #pragma unroll
         for (int c = 0; c < ND; ++c) {
             const int d = wd + 16 * c + col;
-            const int64_t t = t0 + wt + 16 * a + row4;
-            const int left = (int)(A.T - t < 4 ? A.T - t : 4);
             if (d >= A.key) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) {
-                    store_gate<HALF>(A.dq.p, dq_at + d * A.dq.d + (t + e) * A.dq.t, dq[a][c][e]);
-                    store_gate<HALF>(A.dk.p, dk_at + d * A.dk.d + (t + e) * A.dk.t, dk[a][c][e]);
-                }
+            for (int a = 0; a < NT; ++a) {
+                store_column<HALF>(dq_at + d * A.dq.d, A.dq.t, wt + 16 * a + row4, 0, rows, rows == C, dq[a][c]);
+                store_column<HALF>(dk_at + d * A.dk.d, A.dk.t, wt + 16 * a + row4, 0, rows, rows == C, dk[a][c]);
+            }
         }
+    }
 }
 
 }  // namespace delta

@@ -71,8 +71,11 @@ pararnn_status_t run_back(const Args &A, bool wide, hipStream_t s)
     }
     if (st == PARARNN_OK) st = run_back_chain<HALF, DK, TF>(A, wide, s);
     if (st != PARARNN_OK || A.chunks == 0) return st;
-    hipLaunchKernelGGL((delta_grad_kernel<HALF, DK, TF>), dim3((unsigned)(A.B * A.Hk * A.chunks)), dim3(kThreads), 0,
-                       s, A);
+    const dim3 grid((unsigned)(A.B * A.Hk * A.chunks));
+    if (A.Hv == A.Hk)
+        hipLaunchKernelGGL((delta_grad_kernel<HALF, DK, TF, false>), grid, dim3(kThreads), 0, s, A);
+    else
+        hipLaunchKernelGGL((delta_grad_kernel<HALF, DK, TF, true>), grid, dim3(kThreads), 0, s, A);
     return launched();
 }
 template <bool HALF, int DK>

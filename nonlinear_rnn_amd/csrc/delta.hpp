@@ -184,8 +184,16 @@ __device__ __forceinline__ void mma_rows(f32x4 (&c)[M], const A (&a)[M], const B
 template <int M>
 __device__ __forceinline__ void settle(f32x4 (&x)[M])
 {
-    static_assert(M == 1 || M == 2 || M == 4, "one statement for all");
-    if constexpr (M == 4)
+    static_assert(M == 1 || M == 2 || M == 4 || M == 8 || M == 16, "one statement for all");
+    if constexpr (M == 16)
+        asm volatile("s_nop 9"
+                     : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]), "+v"(x[6]), "+v"(x[7]),
+                       "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]),
+                       "+v"(x[15]));
+    else if constexpr (M == 8)
+        asm volatile("s_nop 9"
+                     : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]), "+v"(x[6]), "+v"(x[7]));
+    else if constexpr (M == 4)
         asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]));
     else if constexpr (M == 2)
         asm volatile("s_nop 9" : "+v"(x[0]), "+v"(x[1]));
@@ -199,6 +207,15 @@ __device__ __forceinline__ int64_t afresh(int64_t stride)
 {
     asm volatile("" : "+s"(stride));
     return stride;
+}
+// The same for the addresses in LDS: without it the loops keep dozens of them in
+// registers, spill some, and every reload waits for the loads under way.
+template <class T>
+__device__ __forceinline__ T &lds_afresh(T &shared)
+{
+    auto *p = (__attribute__((address_space(3))) T *)&shared;
+    asm volatile("" : "+s"(p));
+    return *(T *)p;
 }
 __device__ __forceinline__ int lane_afresh(int lane)
 {
@@ -802,7 +819,8 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
     } sh;
     __shared__ Factors<C> F;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
-    const int64_t item = blockIdx.x, bh = item / A.chunks, n = item % A.chunks;
+    const unsigned chunks = (unsigned)A.chunks;
+    const int64_t item = blockIdx.x, bh = blockIdx.x / chunks, n = blockIdx.x % chunks;
     const int64_t b = bh / A.Hv, h = bh % A.Hv, t0 = n * C;
     const LoadedGates loaded = fetch_gates<C>(A, b, h, t0);
     const auto *keys = static_cast<const typename N::Elem *>(A.k.p) + b * A.k.b + h / (A.Hv / A.Hk) * A.k.h;
@@ -975,12 +993,15 @@ struct State {
     __device__ __forceinline__ void store(float *p, int64_t v, bool here, int key, int64_t pitch) const
     {
         const int row4 = threadIdx.x % kWave / 16 * 4;
+        const uint32_t at = (uint32_t)(row4 * (int)pitch + (int)v) * 4u;  // dv <= 2^20
         if (!here) return;
+        pitch = afresh(pitch);
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (16 * i + row4 + r < key) p[(16 * i + row4 + r) * pitch + v] = s[i][r];
+                if (16 * i + row4 + r < key)
+                    *reinterpret_cast<float *>(reinterpret_cast<char *>(p + (16 * i + r) * pitch) + at) = s[i][r];
     }
 };
 
@@ -1001,10 +1022,16 @@ __device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide
         for (int d = 0; d < B; ++d)
 #pragma unroll
             for (int t = 0; t < TT; ++t) k[d][t] = operand<ALONG>(tile, 16 * t, 32 * (d0 + d));
-        if (d0 == 0) meanwhile();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = 0; d < B; ++d) mma_rows(x, k[d], s[d0 + d]);
+        for (int d = 0; d < B; ++d) {
+            mma_rows(x, k[d], s[d0 + d]);
+            if (d0 + d == KD - 2) {  // half of the operands' registers are free
+                __builtin_amdgcn_sched_barrier(0);
+                meanwhile();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
         if (d0 + B < KD) __builtin_amdgcn_sched_barrier(0);
     }
     settle(x);
@@ -1146,24 +1173,28 @@ struct Staged {
     typename In::Lds keys[kTwo ? 2 : 1];
     Factors<C> factors[2];
     Visit visits[2];
-    __device__ __forceinline__ const typename In::Lds &keys_of(int buffer) const { return keys[kTwo ? buffer : 0]; }
+    __device__ __forceinline__ typename In::Lds &keys_of(int buffer) { return keys[kTwo ? buffer : 0]; }
 };
 template <bool HALF, int DK, int NC, bool TF>
 struct Forward : Staged<HALF, DK, NC, TF> {
     using Base = Staged<HALF, DK, NC, TF>;
-    typename Base::In::Lds queries;
+    typename Base::In::Lds queries[1];
     Fragment scores[Slots<Base::C>::kCount], state[NC][Base::KD], write[NC][Base::KC];
+    __device__ __forceinline__ typename Base::In::Lds &queries_of(int) { return queries[0]; }
 };
 template <bool HALF, int DK, int NC, bool TF>
 struct Backward : Staged<HALF, DK, NC, TF> {
     using Base = Staged<HALF, DK, NC, TF>;
     typename Base::In::Lds queries[Base::kTwo ? 2 : 1];
+    Fragment scores[Slots<Base::C>::kCount];
     f32x4 by_scores[NC][Base::TT][kWave], by_queries[NC][Base::DT][kWave];
-    __device__ __forceinline__ const typename Base::In::Lds &queries_of(int buffer) const
+    __device__ __forceinline__ typename Base::In::Lds &queries_of(int buffer)
     {
         return queries[Base::kTwo ? buffer : 0];
     }
 };
+template <bool BACK, bool HALF, int DK, int NC, bool TF>
+using Chained = std::conditional_t<BACK, Backward<HALF, DK, NC, TF>, Forward<HALF, DK, NC, TF>>;
 template <bool HALF>
 __device__ __forceinline__ const typename Num<HALF>::Elem *head_of(const Plane &x, int64_t b, int64_t h)
 {
@@ -1171,84 +1202,85 @@ __device__ __forceinline__ const typename Num<HALF>::Elem *head_of(const Plane &
 }
 
 // P = scale (q . k) D as operands, slots first .. end - 1: its tile (s, t) as keys times
-// queries, row t of the operand, four s.
-template <bool HALF, int DK, int NC, bool TF>
-__device__ __forceinline__ void make_scores(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, bool near,
+// queries, row t of the operand, four s.  BACK: P^T, as queries times keys.
+template <bool BACK, bool HALF, int DK, int NC, bool TF>
+__device__ __forceinline__ void make_scores(const Args &A, Chained<BACK, HALF, DK, NC, TF> &sh, int buffer, bool near,
                                             int first, int end)
 {
     using N = Num<HALF>;
     constexpr int C = N::kChunk, KD = DK / 32;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const Factors<C> &F = sh.factors[buffer];
-    const auto &K = sh.keys_of(buffer);
+    const auto &rows = BACK ? sh.queries_of(buffer) : sh.keys_of(buffer);
+    const auto &columns = BACK ? sh.keys_of(buffer) : sh.queries_of(buffer);
     for (int s = first; s < end; ++s) {
         int tt = s, ss = 0;
         if constexpr (C == 64) {
-            tt = s < 2 ? s : s / 2 + 1;
-            ss = s < 2 ? 0 : s % 2;
+            tt = BACK ? (s < 4 ? s / 2 : s - 2) : s < 2 ? s : s / 2 + 1;
+            ss = BACK ? (s < 4 ? s % 2 : 1) : s < 2 ? 0 : s % 2;
         }
         f32x4 p[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        typename N::Exact q[KD], k[KD][2];
+        typename N::Exact c[KD], r[KD][2];
 #pragma unroll
         for (int d = 0; d < KD; ++d) {
-            q[d] = operand<!TF>(sh.queries, 16 * tt, 32 * d);
-            k[d][0] = operand<!TF>(K, 32 * ss, 32 * d);
-            k[d][1] = operand<!TF>(K, 32 * ss + 16, 32 * d);
+            c[d] = operand<!TF>(columns, 16 * tt, 32 * d);
+            r[d][0] = operand<!TF>(rows, 32 * ss, 32 * d);
+            r[d][1] = operand<!TF>(rows, 32 * ss + 16, 32 * d);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int d = 0; d < KD; ++d) mma_rows(p, k[d], q[d]);
+        for (int d = 0; d < KD; ++d) mma_rows(p, r[d], c[d]);
         settle(p);
         const int t = 16 * tt + col;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = 32 * ss + 16 * i + row4;
-            const f32x4 d = decays_to(F, t, j, near);
+            const f32x4 d = BACK ? decays_from(F, j, t, near) : decays_to(F, t, j, near);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[i][e] = j + e <= t ? A.scale * p[i][e] * d[e] : 0.0f;
+            for (int e = 0; e < 4; ++e) p[i][e] = (BACK ? j + e >= t : j + e <= t) ? A.scale * p[i][e] * d[e] : 0.0f;
         }
         store_fragment(sh.scores[s], stacked<HALF>(p[0], p[1]));
     }
 }
 
 // How the chains' waves share the work.  NC state's waves; as many that compute the
-// outputs; and with NC = 2 two that bring keys and queries and plan the visits, which
-// may wait for memory (they have 16 pieces a tensor each) while the others do not.
-// With NC = 4 the waves of the outputs do this too, as there is no room for more
-// waves' registers.
-template <int NC>
+// outputs (backwards: help); and with NC = 2 two that bring keys and queries and plan
+// the visits, which may wait for memory (they have 16 pieces a tensor each) while the
+// others do not.  With NC = 4 the waves of the outputs do this too, as there is no
+// room for more waves' registers, and so with 256 channels: there four waves have 512
+// registers each, and six would spill hundreds of their 256.
+template <int DK, int NC>
 struct Roles {
-    static constexpr bool kApart = NC == 2;
+    static constexpr bool kApart = NC == 2 && DK < 256;
     static constexpr int kServers = NC, kServer = kApart ? 2 * NC : NC;  // their first wave
     static constexpr int waves(bool output) { return NC + (output ? NC : 0) + (kApart || !output ? kServers : 0); }
-    static constexpr int server(bool output) { return output ? kServer : NC; }
 };
 
-// Forward.  Brings keys and queries (QUERIES), plans the visits.
-template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
+// Brings keys and queries (QUERIES), plans the visits.
+template <bool BACK, bool HALF, int DK, int NC, bool TF, bool QUERIES>
 struct Server {
-    using In = Pieces<HALF, DK, TF, Roles<NC>::kServers * kWave>;
+    using Lds = Chained<BACK, HALF, DK, NC, TF>;
+    using In = Pieces<HALF, DK, TF, Roles<DK, NC>::kServers * kWave>;
     static constexpr int C = Num<HALF>::kChunk;
     In k_raw, q_raw;
-    Planner<C, false> plan;
-    __device__ __forceinline__ void load(const Args &A, const Place &at, int64_t n, int tid)
-    {
-        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-        if constexpr (QUERIES) q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-    }
-    __device__ __forceinline__ void stage(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, const Visit &v,
-                                          int tid)
-    {
-        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], v.r0, v.r1, A.key, tid);
-        if constexpr (QUERIES) q_raw.store(sh.queries, v.r0, v.r1, A.key, tid);
-        // (also where the next visit has the same chunk: see the state's wave)
-        load(A, at_, v.leaves() && v.n + 1 < at_.n1 ? v.n + 1 : v.n, tid);
-    }
+    Planner<C, BACK> plan;
     Place at_;
-    __device__ __forceinline__ Visit start(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c, int tid)
+    __device__ __forceinline__ void load(const Args &A, int64_t n, int tid)
+    {
+        k_raw.load(A.k, head_of<HALF>(A.k, at_.b, at_.hk), 0, n * C, A.key, A.T, tid);
+        if constexpr (QUERIES) q_raw.load(A.q, head_of<HALF>(A.q, at_.b, at_.hk), 0, n * C, A.key, A.T, tid);
+    }
+    __device__ __forceinline__ void stage(const Args &A, Lds &sh, int buffer, const Visit &v, int tid)
+    {
+        k_raw.store(sh.keys_of(buffer), v.r0, v.r1, A.key, tid);
+        if constexpr (QUERIES) q_raw.store(sh.queries_of(buffer), v.r0, v.r1, A.key, tid);
+        // (also where the next visit has the same chunk: see the state's wave)
+        load(A, v.leaves() ? (BACK ? max(v.n - 1, at_.n0) : min(v.n + 1, at_.n1 - 1)) : v.n, tid);
+    }
+    __device__ __forceinline__ Visit start(const Args &A, Lds &sh, const Place &at, int c, int tid)
     {
         at_ = at;
-        load(A, at, at.n0, tid);
+        load(A, BACK ? at.n1 - 1 : at.n0, tid);
         if (c == 0) {
             plan.start(A, at);
             plan.write(sh.visits[0], sh.factors[0]);
@@ -1259,33 +1291,35 @@ struct Server {
         __syncthreads();
         return now;
     }
-    __device__ __forceinline__ void look(const Args &A, Forward<HALF, DK, NC, TF> &sh, int buffer, int c)
+    __device__ __forceinline__ void look(const Args &A, Lds &sh, int buffer, int c)
     {
         if (c != 0) return;
         plan.advance(A, at_);
         plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
-        if (A.ends && plan.n < 0 && at_.first == 0 && threadIdx.x % kWave == 0)
+        if (!BACK && A.ends && plan.n < 0 && at_.first == 0 && threadIdx.x % kWave == 0)
             A.cuts[at_.bh * A.segments + at_.seg] = plan.cut;
     }
 };
-template <bool HALF, int DK, int NC, bool TF, bool QUERIES>
-__device__ __forceinline__ void chain_server(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+template <bool BACK, bool HALF, int DK, int NC, bool TF, bool QUERIES>
+__device__ __forceinline__ void chain_server(const Args &A, Chained<BACK, HALF, DK, NC, TF> &shared, const Place &at,
+                                             int c)
 {
     const int tid = c * kWave + threadIdx.x % kWave;
-    constexpr int kSlots = Slots<Num<HALF>::kChunk>::kCount;
-    Server<HALF, DK, NC, TF, QUERIES> server;
-    Visit now = server.start(A, sh, at, c, tid);
+    constexpr bool kSix = Slots<Num<HALF>::kChunk>::kCount == 6;
+    // its slots of the scores: of six two each, backwards two to the one that does not
+    // plan; of two one each, backwards none
+    const int s0 = BACK ? 4 : kSix ? 2 * c : c, s1 = BACK ? (kSix && c == 1 ? 6 : 4) : kSix ? 2 * c + 2 : c + 1;
+    Server<BACK, HALF, DK, NC, TF, QUERIES> server;
+    Visit now = server.start(A, shared, at, c, tid);
     for (int buffer = 0; now.here(); buffer ^= 1) {
+        auto &sh = lds_afresh(shared);
         server.look(A, sh, buffer, c);
-        if constexpr (QUERIES)  // two slots of three to these
-            make_scores(A, sh, buffer, now.near(), kSlots == 6 ? 2 * c : c, kSlots == 6 ? 2 * c + 2 : c + 1);
+        if constexpr (QUERIES) make_scores<BACK, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         __syncthreads();
+        if constexpr (BACK) __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
-        if (sh.kTwo && then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
-        if (!sh.kTwo) {
-            __syncthreads();
-            if (then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
-        }
+        if (!sh.kTwo) __syncthreads();
+        if (then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
         __syncthreads();
         now = then;
     }
@@ -1293,7 +1327,7 @@ __device__ __forceinline__ void chain_server(const Args &A, Forward<HALF, DK, NC
 // P, q^T S and the outputs, from S and W as operands in LDS.  SERVES: also what a
 // server does.
 template <bool HALF, int DK, int NC, bool TF, bool SERVES>
-__device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+__device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
@@ -1302,32 +1336,36 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value;
     float *const o = static_cast<float *>(A.o.p) + at.b * A.o.b + at.h * A.o.h + v * A.o.d;
-    // its slots of P: with servers one of the last two; else a share of all
-    int s0 = kSlots == 6 ? 4 + c : 0, s1 = kSlots == 6 ? 5 + c : 0;
-    if constexpr (SERVES) {
-        s0 = kSlots == 6 ? (c < 2 ? 2 * c : 2 + c) : min(c, 2);
-        s1 = kSlots == 6 ? (c < 2 ? 2 * c + 2 : 3 + c) : min(c + 1, 2);
+    // its slots of P: with servers one of the last two; else a share of all, of four
+    // the first two waves two each
+    constexpr bool kSix = kSlots == 6;
+    int s0 = kSix ? 4 + c : 0, s1 = kSix ? 5 + c : 0;
+    if constexpr (SERVES && NC == 2) s0 = kSlots / 2 * c, s1 = s0 + kSlots / 2;
+    if constexpr (SERVES && NC == 4) {
+        s0 = kSix ? (c < 2 ? 2 * c : 2 + c) : min(c, 2);
+        s1 = kSix ? (c < 2 ? 2 * c + 2 : 3 + c) : min(c + 1, 2);
     }
-    [[maybe_unused]] Server<HALF, DK, NC, TF, true> server;
+    [[maybe_unused]] Server<false, HALF, DK, NC, TF, true> server;
     Visit now;
     if constexpr (SERVES) {
-        now = server.start(A, sh, at, c, tid);
+        now = server.start(A, shared, at, c, tid);
     } else {
         __syncthreads();
-        now = read_visit(sh.visits[0]);
+        now = read_visit(shared.visits[0]);
         __syncthreads();
     }
     for (int buffer = 0; now.here(); buffer ^= 1) {
+        auto &sh = lds_afresh(shared);
         const Factors<C> &F = sh.factors[buffer];
         if constexpr (SERVES) server.look(A, sh, buffer, c);
-        make_scores(A, sh, buffer, now.near(), s0, s1);
+        make_scores<false, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         f32x4 out[TT];
         {
             Wide s[KD];
 #pragma unroll
             for (int d = 0; d < KD; ++d) s[d] = load_fragment(sh.state[c][d], N());
             f32x4 start[TT];
-            times<!TF>(out, sh.queries, s, [&]() {
+            times<!TF>(out, sh.queries_of(buffer), s, [&]() {
 #pragma unroll
                 for (int t = 0; t < TT; ++t) start[t] = four(F.start + 16 * t + row4);
             });
@@ -1362,7 +1400,7 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
 // A state's wave: k^T S, R, W, S'.  OUTPUT: S and W for the helper, and the last
 // state; else for the backward pass, the states before each chunk and W to memory.
 template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
-__device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+__device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
@@ -1382,7 +1420,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         for (int s = 0; s < Sl::kCount; ++s)
             inverse[s] = load_fragment(A.inverse[(at.bh * A.chunks + n) * Sl::kCount + s], N());
     };
-    const auto make_operands = [&]() {
+    const auto make_operands = [&](Forward<HALF, DK, NC, TF> &sh) {
 #pragma unroll
         for (int d = 0; d < KD; ++d) {
             operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
@@ -1404,11 +1442,12 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     load_inverse(at.n0);
     if constexpr (!OUTPUT) keep(at.n0);
     __syncthreads();
-    Visit now = read_visit(sh.visits[0]);
+    Visit now = read_visit(shared.visits[0]);
     if (now.fresh()) S.zero();
-    make_operands();
+    make_operands(shared);
     __syncthreads();
     for (int buffer = 0; now.here(); buffer ^= 1) {
+        auto &sh = lds_afresh(shared);
         const Factors<C> &F = sh.factors[buffer];
         const auto &K = sh.keys_of(buffer);
         const bool whole = now.r0 == 0 && now.r1 == C;
@@ -1473,7 +1512,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
             if constexpr (!OUTPUT)
                 if (then.enters()) keep(then.n);
             if (then.fresh()) S.zero();
-            make_operands();
+            make_operands(sh);
         }
         if (!sh.kTwo) __syncthreads();
         __syncthreads();
@@ -1487,10 +1526,10 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     }
 }
 template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
-__global__ void __launch_bounds__(Roles<NC>::waves(OUTPUT) * kWave) delta_chain_kernel(Args A)
+__global__ void __launch_bounds__((Roles<DK, NC>::waves(OUTPUT) * kWave)) delta_chain_kernel(Args A)
 {
     __shared__ Forward<HALF, DK, NC, TF> sh;
-    using R = Roles<NC>;
+    using R = Roles<DK, NC>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Place at = place_of<NC>(A);
     if (A.chunks == 0) {  // the state goes through
@@ -1504,12 +1543,12 @@ __global__ void __launch_bounds__(Roles<NC>::waves(OUTPUT) * kWave) delta_chain_
     if (wave < NC) {
         chain_state<HALF, DK, NC, TF, OUTPUT>(A, sh, at, wave);
     } else if constexpr (!OUTPUT) {
-        chain_server<HALF, DK, NC, TF, false>(A, sh, at, wave - NC);
+        chain_server<false, HALF, DK, NC, TF, false>(A, sh, at, wave - NC);
     } else if constexpr (R::kApart) {
         if (wave < R::kServer)
             chain_output<HALF, DK, NC, TF, false>(A, sh, at, wave - NC);
         else
-            chain_server<HALF, DK, NC, TF, true>(A, sh, at, wave - R::kServer);
+            chain_server<false, HALF, DK, NC, TF, true>(A, sh, at, wave - R::kServer);
     } else {
         chain_output<HALF, DK, NC, TF, true>(A, sh, at, wave - NC);
     }
@@ -1541,135 +1580,100 @@ __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 }
 
 // The chain backwards: the gradient of the state, from the last chunk to the
-// first, and X, the gradient of R.  A helper: P^T dO, and scale (exp(G) Q)^T dO,
-// which joins the state a visit later.
-template <bool HALF, int DK, int NC, bool TF>
-__device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+// first, and X, the gradient of R.  A helper: P^T dO, which the state's wave needs
+// in the middle of a visit, and scale (exp(G) Q)^T dO, which joins the state a
+// visit later.  SERVES: also what a server does.
+template <bool HALF, int DK, int NC, bool TF, bool SERVES>
+__device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
-    using In = Pieces<HALF, DK, TF, NC * kWave>;
-    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, KD = DK / 32;
+    constexpr int C = N::kChunk, TT = C / 16, KC = C / 32, DT = DK / 16, kSlots = Slots<C>::kCount;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16, tid = c * kWave + lane;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_o = v < A.value && A.o.p, all_o = 16 * (at.first + c + 1) <= A.value && A.o.p;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    In k_raw, q_raw;
+    // its slots of P^T: two of six or one of two, of those that plan fewer
+    constexpr bool kSix = kSlots == 6;
+    int s0 = kSix ? 2 * c : c, s1 = kSix ? 2 * c + 2 : c + 1;
+    if constexpr (SERVES && NC == 2 && kSix) s1 = c == 0 ? 2 : 6;
+    if constexpr (SERVES && NC == 4) {
+        s0 = kSix ? max(2 * c - 2, 0) : min(max(c - 1, 0), 2);
+        s1 = c == 0 ? s0 : min(s0 + (kSix ? 2 : 1), kSlots);
+    }
     Columns<false, C> go;
-    const auto load = [&](int64_t n) {
-        k_raw.load(A.k, head_of<HALF>(A.k, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-        q_raw.load(A.q, head_of<HALF>(A.q, at.b, at.hk), 0, n * C, A.key, A.T, tid);
-    };
     const float *const gos = head_of<false>(A.o, at.b, at.h) + min(v, (int64_t)A.value - 1) * A.o.d;
     const auto load_go = [&](int64_t n) {
         if (A.o.p) go.load(gos, A.o.t, n * C, A.T);
     };
-    const auto stage = [&](int buffer, int r0, int r1) {
-        k_raw.store(sh.keys[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
-        q_raw.store(sh.queries[sh.kTwo ? buffer : 0], r0, r1, A.key, tid);
-    };
-    Planner<C, true> plan;
-    const int last = at.n1 - 1;
-    load(last);
-    load_go(last);
-    if (c == NC - 1) {
-        plan.start(A, at);
-        plan.write(sh.visits[0], sh.factors[0]);
+    [[maybe_unused]] Server<true, HALF, DK, NC, TF, true> server;
+    Visit now;
+    load_go(at.n1 - 1);
+    if constexpr (SERVES) {
+        now = server.start(A, shared, at, c, tid);
+    } else {
+        __syncthreads();
+        now = read_visit(shared.visits[0]);
+        __syncthreads();
     }
-    __syncthreads();
-    Visit now = read_visit(sh.visits[0]);
-    stage(0, now.r0, now.r1);
-    load(now.leaves() && last > at.n0 ? last - 1 : last);
-    __syncthreads();
     for (int buffer = 0; now.here(); buffer ^= 1) {
-        if (c == NC - 1) {
-            plan.advance(A, at);
-            plan.write(sh.visits[buffer ^ 1], sh.factors[buffer ^ 1]);
-        }
+        auto &sh = lds_afresh(shared);
         const Factors<C> &F = sh.factors[buffer];
-        const auto &K = sh.keys_of(buffer);
-        const auto &Q = sh.queries_of(buffer);
+        if constexpr (SERVES) server.look(A, sh, buffer, c);
+        make_scores<true, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         const bool whole = now.r0 == 0 && now.r1 == C;
-        f32x4 x[TT], y[TT];
+        f32x4 x[TT];
         Wide g[KC];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             x[t] = go.get(t);
             if (!whole || !all_o) x[t] = only_steps(x[t], 16 * t + row4, has_o ? now.r0 : C, now.r1);
-            y[t] = zero;
         }
 #pragma unroll
         for (int s = 0; s < KC; ++s) g[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
-        // P^T: its tile (s, t) as queries times keys, row t of the operand, four s
-        typename N::Exact k[TT][KD], q[2][KD];
+        __syncthreads();
+        {
+            Wide p[kSlots];
+            f32x4 y[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+            for (int s = 0; s < kSlots; ++s) p[s] = load_fragment(sh.scores[s], N());
 #pragma unroll
-            for (int d = 0; d < KD; ++d) k[t][d] = operand<!TF>(K, 16 * t, 32 * d);
+            for (int t = 0; t < TT; ++t) y[t] = zero;
+            triangle_times<false, C>(y, p, g);
 #pragma unroll
-        for (int ss = 0; ss < KC; ++ss) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int d = 0; d < KD; ++d) q[i][d] = operand<!TF>(Q, 32 * ss + 16 * i, 32 * d);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int t = 0; t < 2 * ss + 2; ++t) {
-                f32x4 a[2] = {zero, zero};
-#pragma unroll
-                for (int d = 0; d < KD; ++d)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (2 * ss + i >= t) a[i] = mma(a[i], q[i][d], k[t][d]);
-                const int j = 16 * t + col;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (2 * ss + i < t) continue;
-                    const int s = 32 * ss + 16 * i + row4;
-                    const f32x4 d = decays_from(F, s, j, now.near());
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) a[i][e] = s + e >= j ? A.scale * a[i][e] * d[e] : 0.0f;
-                }
-                y[t] = mma(y[t], stacked<HALF>(a[0], a[1]), g[ss]);
-            }
+            for (int t = 0; t < TT; ++t) sh.by_scores[c][t][lane] = y[t];
         }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) sh.by_scores[c][t][lane] = y[t];
         __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
-        const auto prepare = [&]() {
-            if (!then.here()) return;
-            stage(buffer ^ 1, then.r0, then.r1);
-            load(then.leaves() && then.n > at.n0 ? then.n - 1 : then.n);
-        };
-        if (sh.kTwo) prepare();
+        if constexpr (SERVES)
+            if (sh.kTwo && then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
+        load_go(then.here() ? then.n : now.n);
         if (!now.fresh()) {
+            typename N::Exact qt[KC][DT];
+            f32x4 start[TT], part[DT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) start[t] = four(F.start + 16 * t + row4);
+            read_channels<TF>(qt, sh.queries_of(buffer));
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const f32x4 start = four(F.start + 16 * t + row4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][e] *= A.scale * start[e];
+                x[t] *= A.scale * start[t];
                 if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
             }
-            load_go(then.here() ? then.n : now.n);
 #pragma unroll
             for (int s = 0; s < KC; ++s) g[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
-            typename N::Exact qt[KC][DT];
-            read_channels<TF>(qt, Q);
-            __builtin_amdgcn_sched_barrier(0);
-            f32x4 part[DT];
 #pragma unroll
             for (int d = 0; d < DT; ++d) part[d] = zero;
 #pragma unroll
             for (int s = 0; s < KC; ++s) mma_rows(part, qt[s], g[s]);
+            settle(part);
 #pragma unroll
             for (int d = 0; d < DT; ++d) sh.by_queries[c][d][lane] = part[d];
-        } else {
-            load_go(then.here() ? then.n : now.n);
         }
         if (!sh.kTwo) {
             __syncthreads();
-            prepare();
+            if constexpr (SERVES)
+                if (then.here()) server.stage(A, sh, buffer ^ 1, then, tid);
         }
         __syncthreads();
         now = then;
@@ -1678,7 +1682,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
 // A state's wave: K dS', X, dS.  Writes dS' behind each chunk, X, dV = b X and the
 // sums of X V over its columns.
 template <bool HALF, int DK, int NC, bool TF>
-__device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC, TF> &sh, const Place &at, int c)
+__device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
     using N = Num<HALF>;
     using Wide = typename N::Wide;
@@ -1688,7 +1692,6 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value && !A.ends, in_row = v < A.value_pad && !A.ends, all_v = 16 * (at.first + c + 1) <= A.value;
     auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h + v * A.dv.d;
-    constexpr bool kEarly = DK < 256 && NC == 2;
     State<DK> S;
     Wide inverse[Sl::kCount];
     Columns<HALF, C> value;
@@ -1700,7 +1703,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             inverse[s] = load_fragment(A.inverse_t[(at.bh * A.chunks + n) * Sl::kCount + s], N());
     };
     bool behind = false;  // the helper has a part of the state's gradient
-    const auto join = [&]() {
+    const auto join = [&](Backward<HALF, DK, NC, TF> &sh) {
         if (behind)
 #pragma unroll
             for (int d = 0; d < DT; ++d) S.s[d] += sh.by_queries[c][d][lane];
@@ -1716,41 +1719,47 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     load_value(at.n1 - 1);
     load_inverse(at.n1 - 1);
     __syncthreads();
-    Visit now = read_visit(sh.visits[0]);
+    Visit now = read_visit(shared.visits[0]);
     __syncthreads();
     for (int buffer = 0; now.here(); buffer ^= 1) {
+        auto &sh = lds_afresh(shared);
         const int64_t item = at.bh * A.chunks + now.n;
         const Factors<C> &F = sh.factors[buffer];
         const auto &K = sh.keys_of(buffer);
         const bool whole = now.r0 == 0 && now.r1 == C;
         const int64_t after = now.leaves() && now.n > at.n0 ? now.n - 1 : now.n;
         f32x4 x[TT];
-        join();
+        join(sh);
         if (now.enters()) S.store(A.dstates + item * DK * A.value_pad, v, in_row, DK, A.value_pad);
         Wide operands[KD];
 #pragma unroll
         for (int d = 0; d < KD; ++d) operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
-        f32x4 start[TT], beta[TT], end[TT];
-        typename N::Exact kt[KC][DT];
+        __syncthreads();
+        f32x4 end[TT];
         times<!TF>(x, K, operands, [&]() {
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                start[t] = four(F.start + 16 * t + row4);
-                beta[t] = four(F.beta + 16 * t + row4);
-                end[t] = four(F.end + 16 * t + row4);
-            }
-            if (kEarly) read_channels<TF>(kt, K);
+            for (int t = 0; t < TT; ++t) end[t] = four(F.end + 16 * t + row4);
         });
-        if (!kEarly) read_channels<TF>(kt, K);
         __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
         Wide p[KC];
+        {
+            f32x4 y[TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) y[t] = sh.by_scores[c][t][lane];
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[t][e], x[t][e], y[t][e]);
+        }
+        f32x4 start[TT], beta[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const f32x4 y = sh.by_scores[c][t][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[t][e], x[t][e], y[e]);
+            start[t] = four(F.start + 16 * t + row4);
+            beta[t] = four(F.beta + 16 * t + row4);
         }
+        typename N::Exact kt[KC][DT];
+        read_channels<TF>(kt, K);
         if (!whole)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
@@ -1797,7 +1806,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         __syncthreads();
         now = then;
     }
-    join();
+    join(shared);
     if (A.ends) {
         const int columns = A.value_pad + A.key_pad;
         S.store(A.maps + (at.bh * A.segments + at.seg) * DK * columns, v, v < A.value_pad, DK, columns);
@@ -1806,7 +1815,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     }
 }
 template <bool HALF, int DK, int NC, bool TF>
-__global__ void __launch_bounds__(2 * NC * kWave) delta_back_kernel(Args A)
+__global__ void __launch_bounds__((Roles<DK, NC>::waves(true) * kWave)) delta_back_kernel(Args A)
 {
     __shared__ Backward<HALF, DK, NC, TF> sh;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1819,10 +1828,13 @@ __global__ void __launch_bounds__(2 * NC * kWave) delta_back_kernel(Args A)
         S.store(A.dh0 + at.bh * A.key * A.value, v, here, A.key, A.value);
         return;
     }
+    using R = Roles<DK, NC>;
     if (wave < NC)
         back_state<HALF, DK, NC, TF>(A, sh, at, wave);
+    else if (R::kApart && wave >= R::kServer)
+        chain_server<true, HALF, DK, NC, TF, true>(A, sh, at, wave - R::kServer);
     else
-        back_helper<HALF, DK, NC, TF>(A, sh, at, wave - NC);
+        back_helper<HALF, DK, NC, TF, !R::kApart>(A, sh, at, wave - NC);
 }
 
 // ------------------------------------------------------------ segments ---

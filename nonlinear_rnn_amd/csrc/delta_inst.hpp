@@ -15,9 +15,11 @@ pararnn_status_t run_chain(const Args &A, bool wide, hipStream_t s)
     constexpr int W = DK < 256 ? 4 : 2;
     const dim3 grid((unsigned)(A.B * A.Hv * A.segments * A.blocks));
     if (wide)
-        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, W, TF, OUTPUT>), grid, dim3(Roles<W>::waves(OUTPUT) * kWave), 0, s, A);
+        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, W, TF, OUTPUT>), grid,
+                           dim3(Roles<DK, W>::waves(OUTPUT) * kWave), 0, s, A);
     else
-        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, 2, TF, OUTPUT>), grid, dim3(Roles<2>::waves(OUTPUT) * kWave), 0, s, A);
+        hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, 2, TF, OUTPUT>), grid,
+                           dim3(Roles<DK, 2>::waves(OUTPUT) * kWave), 0, s, A);
     return launched();
 }
 template <bool HALF, int DK, bool TF>
@@ -26,9 +28,11 @@ pararnn_status_t run_back_chain(const Args &A, bool wide, hipStream_t s)
     constexpr int W = DK < 256 ? 4 : 2;
     const dim3 grid((unsigned)(A.B * A.Hv * A.segments * A.blocks));
     if (wide)
-        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, W, TF>), grid, dim3(2 * W * kWave), 0, s, A);
+        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, W, TF>), grid,
+                           dim3(Roles<DK, W>::waves(true) * kWave), 0, s, A);
     else
-        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, 2, TF>), grid, dim3(4 * kWave), 0, s, A);
+        hipLaunchKernelGGL((delta_back_kernel<HALF, DK, 2, TF>), grid,
+                           dim3(Roles<DK, 2>::waves(true) * kWave), 0, s, A);
     return launched();
 }
 // The inverses, and where the chain goes in segments the state before each.

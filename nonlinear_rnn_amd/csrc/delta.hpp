@@ -609,6 +609,23 @@ __device__ __forceinline__ void store_column(typename Num<HALF>::Elem *base, int
     }
 }
 
+// Steps r0 .. r1 - 1 (whole: all) of a wave's columns to a workspace's rows of
+// `pitch` values, dv <= 2^20 of them.
+template <int TT>
+__device__ __forceinline__ void store_rows(float *p, int64_t pitch, int64_t v, int r0, int r1, bool whole,
+                                           const f32x4 (&x)[TT])
+{
+    const int row4 = threadIdx.x % kWave / 16 * 4;
+    pitch = afresh(pitch);
+    const uint32_t at = (uint32_t)(row4 * (int)pitch + (int)v) * 4u;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (whole || (16 * t + row4 + r >= r0 && 16 * t + row4 + r < r1))
+                *reinterpret_cast<float *>(reinterpret_cast<char *>(p + (16 * t + r) * pitch) + at) = x[t][r];
+}
+
 // The gates of a chunk's steps, one a lane; the same in every wave.
 struct StepGates {
     float g, beta;
@@ -993,9 +1010,9 @@ struct State {
     __device__ __forceinline__ void store(float *p, int64_t v, bool here, int key, int64_t pitch) const
     {
         const int row4 = threadIdx.x % kWave / 16 * 4;
+        pitch = afresh(pitch);
         const uint32_t at = (uint32_t)(row4 * (int)pitch + (int)v) * 4u;  // dv <= 2^20
         if (!here) return;
-        pitch = afresh(pitch);
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -1007,10 +1024,10 @@ struct State {
 
 // Products whose operands are read from LDS all at once, before the first is used:
 // left to itself the compiler reads two, waits for the LDS and multiplies.
-// x_t = the rows 16 t .. of a tile of steps times what `s` holds, over the channels.
+// x_t = the rows 16 t .. of a tile of steps times s(0) .. s(KD - 1), over the channels.
 // `meanwhile` is what else is to be read meanwhile.
-template <bool ALONG, class In, class Wide, int TT, int KD, class F>
-__device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide (&s)[KD], const F &meanwhile)
+template <bool ALONG, int KD, class In, int TT, class S, class F>
+__device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const S &s, const F &meanwhile)
 {
     constexpr int B = KD < 4 ? KD : 4;  // the registers of 16 operands at a time
     decltype(operand<ALONG>(tile, 0, 0)) k[B][TT];
@@ -1025,7 +1042,7 @@ __device__ __forceinline__ void times(f32x4 (&x)[TT], const In &tile, const Wide
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < B; ++d) {
-            mma_rows(x, k[d], s[d0 + d]);
+            mma_rows(x, k[d], s(d0 + d));
             if (d0 + d == KD - 2) {  // half of the operands' registers are free
                 __builtin_amdgcn_sched_barrier(0);
                 meanwhile();
@@ -1150,6 +1167,9 @@ struct Planner {
             n = -1;
         }
     }
+    // waits for the next chunk's gates, so that what is loaded from here on is not
+    // waited for with them
+    __device__ __forceinline__ void settle() { asm volatile("" : "+v"(next.g), "+v"(next.beta), "+v"(next.reset)); }
     // to LDS: the visit, and what its steps multiply with
     __device__ __forceinline__ void write(Visit &v, Factors<C> &F) const
     {
@@ -1244,23 +1264,25 @@ __device__ __forceinline__ void make_scores(const Args &A, Chained<BACK, HALF, D
 }
 
 // How the chains' waves share the work.  NC state's waves; as many that compute the
-// outputs (backwards: help); and with NC = 2 two that bring keys and queries and plan
-// the visits, which may wait for memory (they have 16 pieces a tensor each) while the
-// others do not.  With NC = 4 the waves of the outputs do this too, as there is no
-// room for more waves' registers, and so with 256 channels: there four waves have 512
-// registers each, and six would spill hundreds of their 256.
-template <int DK, int NC>
+// outputs (backwards: help); and with NC = 2 four that bring keys and queries and plan
+// the visits, which may wait for memory (they have 8 pieces a tensor each with 128
+// channels) while the others do not.  With NC = 4 the waves of the outputs do this
+// too, as there is no room for more waves' registers, and so with 256 channels: there
+// four waves have 512 registers each, and eight would spill hundreds of their 256.
+// Without outputs there are two servers or four.
+template <int DK, int NC, bool OUTPUT>
 struct Roles {
-    static constexpr bool kApart = NC == 2 && DK < 256;
-    static constexpr int kServers = NC, kServer = kApart ? 2 * NC : NC;  // their first wave
-    static constexpr int waves(bool output) { return NC + (output ? NC : 0) + (kApart || !output ? kServers : 0); }
+    static constexpr bool kApart = OUTPUT && NC == 2 && DK < 256;
+    static constexpr int kServers = kApart ? 4 : NC;
+    static constexpr int kServer = kApart ? 2 * NC : NC;  // their first wave
+    static constexpr int kWaves = OUTPUT && !kApart ? 2 * NC : kServer + kServers;
 };
 
 // Brings keys and queries (QUERIES), plans the visits.
 template <bool BACK, bool HALF, int DK, int NC, bool TF, bool QUERIES>
 struct Server {
     using Lds = Chained<BACK, HALF, DK, NC, TF>;
-    using In = Pieces<HALF, DK, TF, Roles<DK, NC>::kServers * kWave>;
+    using In = Pieces<HALF, DK, TF, Roles<DK, NC, QUERIES>::kServers * kWave>;
     static constexpr int C = Num<HALF>::kChunk;
     In k_raw, q_raw;
     Planner<C, BACK> plan;
@@ -1274,6 +1296,7 @@ struct Server {
     {
         k_raw.store(sh.keys_of(buffer), v.r0, v.r1, A.key, tid);
         if constexpr (QUERIES) q_raw.store(sh.queries_of(buffer), v.r0, v.r1, A.key, tid);
+        plan.settle();
         // (also where the next visit has the same chunk: see the state's wave)
         load(A, v.leaves() ? (BACK ? max(v.n - 1, at_.n0) : min(v.n + 1, at_.n1 - 1)) : v.n, tid);
     }
@@ -1306,9 +1329,10 @@ __device__ __forceinline__ void chain_server(const Args &A, Chained<BACK, HALF, 
 {
     const int tid = c * kWave + threadIdx.x % kWave;
     constexpr bool kSix = Slots<Num<HALF>::kChunk>::kCount == 6;
-    // its slots of the scores: of six two each, backwards two to the one that does not
-    // plan; of two one each, backwards none
-    const int s0 = BACK ? 4 : kSix ? 2 * c : c, s1 = BACK ? (kSix && c == 1 ? 6 : 4) : kSix ? 2 * c + 2 : c + 1;
+    // its slots of the scores: none to the first, which plans; of six one each and two to
+    // the last (the waves of the outputs have two), backwards two each; of two one each
+    const int s0 = c == 0 ? 0 : BACK && kSix ? 2 * c - 2 : min(c - 1, kSix ? 6 : 2);
+    const int s1 = c == 0 ? 0 : kSix ? (BACK ? 2 * c : c == 3 ? 4 : c) : min(c, 2);
     Server<BACK, HALF, DK, NC, TF, QUERIES> server;
     Visit now = server.start(A, shared, at, c, tid);
     for (int buffer = 0; now.here(); buffer ^= 1) {
@@ -1336,8 +1360,8 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value;
     float *const o = static_cast<float *>(A.o.p) + at.b * A.o.b + at.h * A.o.h + v * A.o.d;
-    // its slots of P: with servers one of the last two; else a share of all, of four
-    // the first two waves two each
+    // its slots of P: with servers one of the last two of six; else a share of all, of
+    // four waves two each to the first two
     constexpr bool kSix = kSlots == 6;
     int s0 = kSix ? 4 + c : 0, s1 = kSix ? 5 + c : 0;
     if constexpr (SERVES && NC == 2) s0 = kSlots / 2 * c, s1 = s0 + kSlots / 2;
@@ -1365,7 +1389,7 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
 #pragma unroll
             for (int d = 0; d < KD; ++d) s[d] = load_fragment(sh.state[c][d], N());
             f32x4 start[TT];
-            times<!TF>(out, sh.queries_of(buffer), s, [&]() {
+            times<!TF, KD>(out, sh.queries_of(buffer), [&](int d) { return s[d]; }, [&]() {
 #pragma unroll
                 for (int t = 0; t < TT; ++t) start[t] = four(F.start + 16 * t + row4);
             });
@@ -1457,7 +1481,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         f32x4 x[TT];
         f32x4 start[TT], beta[TT];
         typename N::Exact kt[KC][DT];
-        times<!TF>(x, K, operands, [&]() {
+        times<!TF, KD>(x, K, [&](int d) { return operands[d]; }, [&]() {
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 start[t] = four(F.start + 16 * t + row4);
@@ -1474,7 +1498,6 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         if (!whole)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
-        load_value(after);
         if (!kEarly) read_channels<TF>(kt, K);
         Wide rhs[KC];
 #pragma unroll
@@ -1485,16 +1508,14 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         if (!whole)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
+        load_value(after);
         load_inverse(after);
         if constexpr (OUTPUT) {
 #pragma unroll
             for (int s = 0; s < KC; ++s) store_fragment(sh.write[c][s], stacked<HALF>(x[2 * s], x[2 * s + 1]));
         } else {
             if (in_row)
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-                    store_column<false>(A.w + (at.bh * A.chunks + now.n) * C * A.value_pad + v, A.value_pad, 16 * t + row4,
-                                        now.r0, now.r1, whole, x[t]);
+                store_rows(A.w + (at.bh * A.chunks + now.n) * C * A.value_pad, A.value_pad, v, now.r0, now.r1, whole, x);
         }
 #pragma unroll
         for (int t = 0; t < TT; ++t) x[t] *= four(F.end + 16 * t + row4);
@@ -1526,10 +1547,10 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     }
 }
 template <bool HALF, int DK, int NC, bool TF, bool OUTPUT>
-__global__ void __launch_bounds__((Roles<DK, NC>::waves(OUTPUT) * kWave)) delta_chain_kernel(Args A)
+__global__ void __launch_bounds__((Roles<DK, NC, OUTPUT>::kWaves * kWave)) delta_chain_kernel(Args A)
 {
     __shared__ Forward<HALF, DK, NC, TF> sh;
-    using R = Roles<DK, NC>;
+    using R = Roles<DK, NC, OUTPUT>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const Place at = place_of<NC>(A);
     if (A.chunks == 0) {  // the state goes through
@@ -1593,10 +1614,10 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_o = v < A.value && A.o.p, all_o = 16 * (at.first + c + 1) <= A.value && A.o.p;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // its slots of P^T: two of six or one of two, of those that plan fewer
+    // its slots of P^T: with servers none; else a share, the smallest to the one that plans
     constexpr bool kSix = kSlots == 6;
-    int s0 = kSix ? 2 * c : c, s1 = kSix ? 2 * c + 2 : c + 1;
-    if constexpr (SERVES && NC == 2 && kSix) s1 = c == 0 ? 2 : 6;
+    int s0 = 0, s1 = 0;
+    if constexpr (SERVES && NC == 2) s0 = kSix ? 2 * c : c, s1 = kSix ? 2 + 4 * c : c + 1;
     if constexpr (SERVES && NC == 4) {
         s0 = kSix ? max(2 * c - 2, 0) : min(max(c - 1, 0), 2);
         s1 = c == 0 ? s0 : min(s0 + (kSix ? 2 : 1), kSlots);
@@ -1691,12 +1712,13 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value && !A.ends, in_row = v < A.value_pad && !A.ends, all_v = 16 * (at.first + c + 1) <= A.value;
-    auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h + v * A.dv.d;
+    auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h;
     State<DK> S;
     Wide inverse[Sl::kCount];
     Columns<HALF, C> value;
-    const auto *const values = head_of<HALF>(A.v, at.b, at.h) + min(v, (int64_t)A.value - 1) * A.v.d;
-    const auto load_value = [&](int64_t n) { value.load(values, A.v.t, n * C, A.T); };
+    const auto *const values = head_of<HALF>(A.v, at.b, at.h);
+    const int last = min((int)v, A.value - 1);
+    const auto load_value = [&](int64_t n) { value.load(values + last * afresh(A.v.d), A.v.t, n * C, A.T); };
     const auto load_inverse = [&](int64_t n) {
 #pragma unroll
         for (int s = 0; s < Sl::kCount; ++s)
@@ -1731,12 +1753,9 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         f32x4 x[TT];
         join(sh);
         if (now.enters()) S.store(A.dstates + item * DK * A.value_pad, v, in_row, DK, A.value_pad);
-        Wide operands[KD];
-#pragma unroll
-        for (int d = 0; d < KD; ++d) operands[d] = stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]);
         __syncthreads();
         f32x4 end[TT];
-        times<!TF>(x, K, operands, [&]() {
+        times<!TF, KD>(x, K, [&](int d) { return stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]); }, [&]() {
 #pragma unroll
             for (int t = 0; t < TT; ++t) end[t] = four(F.end + 16 * t + row4);
         });
@@ -1752,12 +1771,6 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[t][e] = fmaf_(end[t][e], x[t][e], y[t][e]);
         }
-        f32x4 start[TT], beta[TT];
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            start[t] = four(F.start + 16 * t + row4);
-            beta[t] = four(F.beta + 16 * t + row4);
-        }
         typename N::Exact kt[KC][DT];
         read_channels<TF>(kt, K);
         if (!whole)
@@ -1771,14 +1784,19 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         if (!whole)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
-        load_inverse(after);
+        f32x4 start[TT], beta[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            start[t] = four(F.start + 16 * t + row4);
+            beta[t] = four(F.beta + 16 * t + row4);
+        }
+        if (in_row) store_rows(A.x + item * C * A.value_pad, A.value_pad, v, now.r0, now.r1, whole, x);
+        auto *const dv_column = dv + (int64_t)now.n * C * A.dv.t + v * afresh(A.dv.d);
         float sums[4 * TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             f32x4 val = value.get(t), bx;
             if (!whole || !all_v) val = only_steps(val, 16 * t + row4, has_v ? now.r0 : C, now.r1);
-            if (in_row)
-                store_column<false>(A.x + item * C * A.value_pad + v, A.value_pad, 16 * t + row4, now.r0, now.r1, whole, x[t]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 sums[4 * t + e] = x[t][e] * val[e];
@@ -1786,10 +1804,9 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
                 x[t][e] = -start[t][e] * bx[e];
             }
             if (has_v)
-                store_column<HALF>(dv + (int64_t)now.n * C * A.dv.t, A.dv.t, 16 * t + row4, now.r0, now.r1, whole, bx);
+                store_column<HALF>(dv_column, A.dv.t, 16 * t + row4, now.r0, now.r1, whole, bx);
             if (!whole) x[t] = only_steps(x[t], 16 * t + row4, now.r0, now.r1);
         }
-        load_value(after);
         if (now.fresh()) {  // the state before this document's is no part of it
             S.zero();
         } else {
@@ -1797,6 +1814,8 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             for (int s = 0; s < KC; ++s) p[s] = stacked<HALF>(x[2 * s], x[2 * s + 1]);
             S.advance(F.across[0], kt, p);
         }
+        load_inverse(after);
+        load_value(after);
         behind = !now.fresh();
         int which;
         const float sum = sum_columns(sums, which);
@@ -1815,7 +1834,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     }
 }
 template <bool HALF, int DK, int NC, bool TF>
-__global__ void __launch_bounds__((Roles<DK, NC>::waves(true) * kWave)) delta_back_kernel(Args A)
+__global__ void __launch_bounds__((Roles<DK, NC, true>::kWaves * kWave)) delta_back_kernel(Args A)
 {
     __shared__ Backward<HALF, DK, NC, TF> sh;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1828,7 +1847,7 @@ __global__ void __launch_bounds__((Roles<DK, NC>::waves(true) * kWave)) delta_ba
         S.store(A.dh0 + at.bh * A.key * A.value, v, here, A.key, A.value);
         return;
     }
-    using R = Roles<DK, NC>;
+    using R = Roles<DK, NC, true>;
     if (wave < NC)
         back_state<HALF, DK, NC, TF>(A, sh, at, wave);
     else if (R::kApart && wave >= R::kServer)

@@ -16,10 +16,10 @@ pararnn_status_t run_chain(const Args &A, bool wide, hipStream_t s)
     const dim3 grid((unsigned)(A.B * A.Hv * A.segments * A.blocks));
     if (wide)
         hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, W, TF, OUTPUT>), grid,
-                           dim3(Roles<DK, W>::waves(OUTPUT) * kWave), 0, s, A);
+                           dim3(Roles<DK, W, OUTPUT>::kWaves * kWave), 0, s, A);
     else
         hipLaunchKernelGGL((delta_chain_kernel<HALF, DK, 2, TF, OUTPUT>), grid,
-                           dim3(Roles<DK, 2>::waves(OUTPUT) * kWave), 0, s, A);
+                           dim3(Roles<DK, 2, OUTPUT>::kWaves * kWave), 0, s, A);
     return launched();
 }
 template <bool HALF, int DK, bool TF>
@@ -29,10 +29,10 @@ pararnn_status_t run_back_chain(const Args &A, bool wide, hipStream_t s)
     const dim3 grid((unsigned)(A.B * A.Hv * A.segments * A.blocks));
     if (wide)
         hipLaunchKernelGGL((delta_back_kernel<HALF, DK, W, TF>), grid,
-                           dim3(Roles<DK, W>::waves(true) * kWave), 0, s, A);
+                           dim3(Roles<DK, W, true>::kWaves * kWave), 0, s, A);
     else
         hipLaunchKernelGGL((delta_back_kernel<HALF, DK, 2, TF>), grid,
-                           dim3(Roles<DK, 2>::waves(true) * kWave), 0, s, A);
+                           dim3(Roles<DK, 2, true>::kWaves * kWave), 0, s, A);
     return launched();
 }
 // The inverses, and where the chain goes in segments the state before each.

@@ -86,7 +86,7 @@ int64_t segments_of(const pararnn_delta_shape_t *s, int64_t chunks)
 }
 
 struct Layout {
-    size_t inverse, inverse_t, states, dstates, w, x, xv, maps, marks, cuts, total;
+    size_t inverse, inverse_t, states, dstates, w, x, maps, marks, cuts, total;
     int64_t per, segments;  // chunks a segment
 };
 Layout layout(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool adjoint)
@@ -109,7 +109,6 @@ Layout layout(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool adjoin
         l.dstates = take(items * room * pad * 4);
         l.w = take(items * C * pad * 4);
         l.x = take(items * C * pad * 4);
-        l.xv = take(items * C * (pad / 16) * 4);
     }
     const int64_t chunks = (s->T + C - 1) / C, want = segments_of(s, chunks);
     l.per = std::max<int64_t>(1, (chunks + want - 1) / want);
@@ -171,7 +170,6 @@ pararnn_status_t prepare(Args &A, const pararnn_delta_shape_t *s, pararnn_dtype_
         A.dstates = reinterpret_cast<float *>(base + l.dstates);
         A.w = reinterpret_cast<float *>(base + l.w);
         A.x = reinterpret_cast<float *>(base + l.x);
-        A.xv = reinterpret_cast<float *>(base + l.xv);
     }
     return PARARNN_OK;
 }

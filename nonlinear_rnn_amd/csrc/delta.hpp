@@ -79,9 +79,8 @@ struct Args {
     int32_t ends;      // only the segments' maps: their ends from zero, and from the identity
     // workspace
     struct Fragment *inverse, *inverse_t;  // [b h][chunk][slot] operands
-    float *states, *dstates;          // [b h][chunk][DK][value_pad]
-    float *w, *x;                     // [b h][chunk * C][value_pad]
-    float *xv;                        // [b h][chunk * C][value_pad / 16]: X . V of 16 columns
+    float *states, *dstates;          // [b h][chunk][value_pad][DK]
+    float *w, *x;                     // [b h][chunk][value_pad][C]
     float *maps;                      // [b h][segment][DK][value_pad + key_pad]: ends from zero, from the identity
     float *marks;                     // [b h][segment][DK][value_pad]: the state before, the gradient behind
     int32_t *cuts;                    // [b h][segment]: whether a document starts in it
@@ -349,6 +348,16 @@ __device__ __forceinline__ typename Num<HALF>::Wide operand(const WideTile<HALF,
     else
         return half(0);
 }
+// One value.
+template <bool HALF, int ROWS, int COLS>
+__device__ __forceinline__ float value_at(const WideTile<HALF, ROWS, COLS> &t, int row, int col)
+{
+    const int at = row * t.kPitch + col;
+    if constexpr (HALF)
+        return __uint_as_float((uint32_t)t.at[at] << 16) + __uint_as_float((uint32_t)t.at[ROWS * t.kPitch + at] << 16);
+    else
+        return t.at[at];
+}
 // Four values side by side at (row, col), col a multiple of 4.
 template <bool HALF, int ROWS, int COLS>
 __device__ __forceinline__ void store4(WideTile<HALF, ROWS, COLS> &t, int row, int col, f32x4 x)
@@ -609,21 +618,14 @@ __device__ __forceinline__ void store_column(typename Num<HALF>::Elem *base, int
     }
 }
 
-// Steps r0 .. r1 - 1 (whole: all) of a wave's columns to a workspace's rows of
-// `pitch` values, dv <= 2^20 of them.
+// Steps r0 .. r1 - 1 (whole: all) of a wave's columns to a workspace's rows of a
+// chunk's steps.
 template <int TT>
-__device__ __forceinline__ void store_rows(float *p, int64_t pitch, int64_t v, int r0, int r1, bool whole,
-                                           const f32x4 (&x)[TT])
+__device__ __forceinline__ void store_rows(float *p, int64_t v, int r0, int r1, bool whole, const f32x4 (&x)[TT])
 {
-    const int row4 = threadIdx.x % kWave / 16 * 4;
-    pitch = afresh(pitch);
-    const uint32_t at = (uint32_t)(row4 * (int)pitch + (int)v) * 4u;
 #pragma unroll
     for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (whole || (16 * t + row4 + r >= r0 && 16 * t + row4 + r < r1))
-                *reinterpret_cast<float *>(reinterpret_cast<char *>(p + (16 * t + r) * pitch) + at) = x[t][r];
+        store_column<false>(p + v * 16 * TT, 1, 16 * t + threadIdx.x % kWave / 16 * 4, r0, r1, whole, x[t]);
 }
 
 // The gates of a chunk's steps, one a lane; the same in every wave.
@@ -1006,6 +1008,14 @@ struct State {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (16 * i + row4 + r < key) s[i][r] = p[(16 * i + row4 + r) * pitch + v];
+    }
+    // column v as a row of DK values
+    __device__ __forceinline__ void store_row(float *p, int64_t v, bool here) const
+    {
+        const int row4 = threadIdx.x % kWave / 16 * 4;
+        if (!here) return;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4 *>(p + v * DK + 16 * i + row4) = s[i];
     }
     __device__ __forceinline__ void store(float *p, int64_t v, bool here, int key, int64_t pitch) const
     {
@@ -1452,7 +1462,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
         }
     };
     const auto keep = [&](int64_t n) {
-        S.store(A.states + (at.bh * A.chunks + n) * DK * A.value_pad, v, in_row, DK, A.value_pad);
+        S.store_row(A.states + (at.bh * A.chunks + n) * DK * A.value_pad, v, in_row);
     };
 
     if (!OUTPUT && A.ends) {
@@ -1515,7 +1525,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
             for (int s = 0; s < KC; ++s) store_fragment(sh.write[c][s], stacked<HALF>(x[2 * s], x[2 * s + 1]));
         } else {
             if (in_row)
-                store_rows(A.w + (at.bh * A.chunks + now.n) * C * A.value_pad, A.value_pad, v, now.r0, now.r1, whole, x);
+                store_rows(A.w + (at.bh * A.chunks + now.n) * C * A.value_pad, v, now.r0, now.r1, whole, x);
         }
 #pragma unroll
         for (int t = 0; t < TT; ++t) x[t] *= four(F.end + 16 * t + row4);
@@ -1700,8 +1710,7 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
         now = then;
     }
 }
-// A state's wave: K dS', X, dS.  Writes dS' behind each chunk, X, dV = b X and the
-// sums of X V over its columns.
+// A state's wave: K dS', X, dS.  Writes dS' behind each chunk, X and dV = b X.
 template <bool HALF, int DK, int NC, bool TF>
 __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
@@ -1711,14 +1720,10 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     using Sl = Slots<C>;
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
-    const bool has_v = v < A.value && !A.ends, in_row = v < A.value_pad && !A.ends, all_v = 16 * (at.first + c + 1) <= A.value;
+    const bool has_v = v < A.value && !A.ends, in_row = v < A.value_pad && !A.ends;
     auto *const dv = static_cast<typename N::Elem *>(A.dv.p) + at.b * A.dv.b + at.h * A.dv.h;
     State<DK> S;
     Wide inverse[Sl::kCount];
-    Columns<HALF, C> value;
-    const auto *const values = head_of<HALF>(A.v, at.b, at.h);
-    const int last = min((int)v, A.value - 1);
-    const auto load_value = [&](int64_t n) { value.load(values + last * afresh(A.v.d), A.v.t, n * C, A.T); };
     const auto load_inverse = [&](int64_t n) {
 #pragma unroll
         for (int s = 0; s < Sl::kCount; ++s)
@@ -1738,7 +1743,6 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
     } else {
         S.load(A.g_last + at.bh * A.key * A.value, v, A.g_last && has_v, A.key, A.value);
     }
-    load_value(at.n1 - 1);
     load_inverse(at.n1 - 1);
     __syncthreads();
     Visit now = read_visit(shared.visits[0]);
@@ -1752,7 +1756,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         const int64_t after = now.leaves() && now.n > at.n0 ? now.n - 1 : now.n;
         f32x4 x[TT];
         join(sh);
-        if (now.enters()) S.store(A.dstates + item * DK * A.value_pad, v, in_row, DK, A.value_pad);
+        if (now.enters()) S.store_row(A.dstates + item * DK * A.value_pad, v, in_row);
         __syncthreads();
         f32x4 end[TT];
         times<!TF, KD>(x, K, [&](int d) { return stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]); }, [&]() {
@@ -1790,16 +1794,13 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             start[t] = four(F.start + 16 * t + row4);
             beta[t] = four(F.beta + 16 * t + row4);
         }
-        if (in_row) store_rows(A.x + item * C * A.value_pad, A.value_pad, v, now.r0, now.r1, whole, x);
+        if (in_row) store_rows(A.x + item * C * A.value_pad, v, now.r0, now.r1, whole, x);
         auto *const dv_column = dv + (int64_t)now.n * C * A.dv.t + v * afresh(A.dv.d);
-        float sums[4 * TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            f32x4 val = value.get(t), bx;
-            if (!whole || !all_v) val = only_steps(val, 16 * t + row4, has_v ? now.r0 : C, now.r1);
+            f32x4 bx;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sums[4 * t + e] = x[t][e] * val[e];
                 bx[e] = beta[t][e] * x[t][e];
                 x[t][e] = -start[t][e] * bx[e];
             }
@@ -1815,12 +1816,7 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             S.advance(F.across[0], kt, p);
         }
         load_inverse(after);
-        load_value(after);
         behind = !now.fresh();
-        int which;
-        const float sum = sum_columns(sums, which);
-        const int row = 16 * (which / 4) + row4 + which % 4;
-        if (in_row && row >= now.r0 && row < now.r1) A.xv[(item * C + row) * (A.value_pad / 16) + at.first + c] = sum;
         if (!sh.kTwo) __syncthreads();
         __syncthreads();
         now = then;
@@ -1965,18 +1961,20 @@ struct Gradients {
     static constexpr int C = N::kChunk, TT = C / 16, DT = DK / 16, VB = 32, kT = 2, kD = 4, kPairs = TT * kD;
     using In = Pieces<HALF, DK, TF, kThreads>;
     typename In::Lds keys, queries;
+    static constexpr bool kBoth = DK < 256;  // room for both states' columns
     union {
         struct {
             WideTile<HALF, TF ? VB : C, TF ? C : VB> out;
-            WideTile<HALF, C, VB> x, w;
-        } block[2];
+            WideTile<HALF, VB, C> x, w;
+            WideTile<HALF, VB, DK> s[kBoth ? 2 : 1];
+        } block;
         struct {
             WideTile<HALF, C, C> e, h;  // E and b H by columns
         } t;
     };
     Factors<C> F;
     float row_sum[kPairs * 16], col_sum[kPairs * 16], h_sum[kPairs * 16];
-    float dots[3][kD][C], xv[C], inner[kWaves];
+    float dots[3][kD][C], xv[kWaves][C], inner[kWaves];
 };
 template <bool HALF, int DK, bool TF, bool SHARED>
 __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
@@ -1989,7 +1987,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
     using Sl = Slots<N::kChunk>;
     constexpr int C = L::C, TT = L::TT, KC = C / 32, KD = DK / 32, kT = L::kT, kD = L::kD, VB = L::VB;
     constexpr int ND = L::DT / kD, NT = TT / kT;
-    constexpr bool kAhead = ND <= 2;  // registers for the next states' parts
+    constexpr int kStates = VB * DK / 4 / kThreads;  // a thread's pieces of a state's columns
     __shared__ L sh;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), pd = wave % kD, pt = wave / kD;
     const unsigned chunks = (unsigned)A.chunks, heads = (unsigned)A.Hk, bk = blockIdx.x / chunks;
@@ -2009,99 +2007,90 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
             for (int c = 0; c < ND; ++c) dq[a][c] = dk[a][c] = zero;
     for (int head = 0; head < group; ++head) {
         const int64_t h = hk * group + head, bh = b * A.Hv + h, item = bh * A.chunks + n;
-        const StepGates gates = load_gates<C>(A, b, h, t0);
+        const LoadedGates loaded = fetch_gates<C>(A, b, h, t0);
+        StepGates gates;
+        const int rows = (int)min((int64_t)C, A.T - t0);
         const float *const s_before = A.states + item * DK * A.value_pad;
         const float *const s_behind = A.dstates + item * DK * A.value_pad;
-        for (int r0 = 0, r1; r0 < gates.rows; r0 = r1) {
-            r1 = document_end(gates.cut, r0, gates.rows);
+        const float *const x_at = A.x + item * C * A.value_pad, *const w_at = A.w + item * C * A.value_pad;
+        for (int r0 = 0, r1; r0 < rows; r0 = r1) {
             const int lane = lane_afresh(threadIdx.x % kWave), row4 = 4 * (lane / 16), col = lane % 16;
-            const bool before = !(gates.cut >> r0 & 1), behind = r1 == gates.rows, whole = r0 == 0 && r1 == C;
-            // a block of columns as loaded: a piece a thread, and the states' operands
+            // 32 columns as loaded, four values a piece: X and W, (v, t); dO and V as
+            // they lie side by side, (v, t) or (t, v); the states, (v, d)
             constexpr bool kAll = C * VB / 4 == kThreads;  // a piece for every thread
-            const int u = wave * kWave + lane, row = u / (VB / 4), v4 = u % (VB / 4) * 4;
-            const bool loads = kAll || u < C * VB / 4, mine = loads && row >= r0 && row < r1;
-            f32x4 xr, wr, orr, sr[ND][2], gr[ND][2];
-            const auto load_block = [&](int v0) {
-                const int64_t at = (item * C + min(row, C - 1)) * A.value_pad + v0 + v4;
-                xr = four(A.x + at);
-                wr = four(A.w + at);
-                orr = zero;
-                if (A.o.p && loads) {
-                    if constexpr (TF) {
-                        const int v = u / (C / 4), t4 = u % (C / 4) * 4;
-                        const float *p = head_of<false>(A.o, b, h) + min(v0 + v, A.value - 1) * A.o.d + t0 * A.o.t;
-                        if (A.o.t == 1 && t0 + C <= A.T) {
-                            const Words4 q = *reinterpret_cast<const Words4Any *>(p + t4);
-                            orr = __builtin_bit_cast(f32x4, q);
-                        } else {
-                            const int64_t step = afresh(A.o.t);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) orr[e] = p[min((int64_t)t4 + e, A.T - 1 - t0) * step];
-                        }
+            const int u = wave * kWave + lane;
+            const bool loads = kAll || u < C * VB / 4;
+            const int pv = u / (C / 4), pt4 = u % (C / 4) * 4, prow = u / (VB / 4), pv4 = u % (VB / 4) * 4;
+            f32x4 xr, wr, orr, sr[kStates], gr[kStates];
+            uint32_t vr[HALF ? 2 : 4];
+            // four elements side by side, or `step` apart from `first` to `last`
+            const auto load_four = [&](auto *p, int64_t step, bool beside, int first, int64_t last, uint32_t *w) {
+                using E = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
+                if (beside) {
+                    if constexpr (sizeof(E) == 2) {
+                        const Words2 q = *reinterpret_cast<const Words2Any *>(p + first);
+                        w[0] = q.x, w[1] = q.y;
                     } else {
-                        const float *p = head_of<false>(A.o, b, h) + (t0 + min((int64_t)row, A.T - 1 - t0)) * A.o.t;
-                        if (A.o.d == 1 && v0 + VB <= A.value) {
-                            const Words4 q = *reinterpret_cast<const Words4Any *>(p + v0 + v4);
-                            orr = __builtin_bit_cast(f32x4, q);
-                        } else {
-                            const int64_t step = afresh(A.o.d);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) orr[e] = p[min(v0 + v4 + e, A.value - 1) * step];
-                        }
+                        const Words4 q = *reinterpret_cast<const Words4Any *>(p + first);
+                        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
                     }
+                    return;
+                }
+                step = afresh(step);
+                uint32_t e4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const E *const at = p + min((int64_t)first + e, last) * step;
+                    if constexpr (sizeof(E) == 2)
+                        e4[e] = *at;
+                    else
+                        e4[e] = __float_as_uint(*at);
+                }
+                if constexpr (sizeof(E) == 2)
+                    w[0] = e4[0] | e4[1] << 16, w[1] = e4[2] | e4[3] << 16;
+                else
+                    w[0] = e4[0], w[1] = e4[1], w[2] = e4[2], w[3] = e4[3];
+            };
+            const auto load_plane = [&](const Plane &x, const auto *base, int v0, uint32_t *w) {
+                if constexpr (TF)
+                    load_four(base + min(v0 + pv, A.value - 1) * x.d + t0 * x.t, x.t, x.t == 1 && t0 + C <= A.T, pt4,
+                              A.T - 1 - t0, w);
+                else
+                    load_four(base + (t0 + min((int64_t)prow, A.T - 1 - t0)) * x.t + v0 * x.d, x.d,
+                              x.d == 1 && v0 + VB <= A.value, pv4, A.value - 1 - v0, w);
+            };
+            const auto load_block = [&](int v0) {
+                if (loads) {
+                    xr = four(x_at + (int64_t)v0 * C + 4 * u);
+                    wr = four(w_at + (int64_t)v0 * C + 4 * u);
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if (A.o.p) load_plane(A.o, head_of<false>(A.o, b, h), v0, w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) orr[e] = __uint_as_float(w[e]);
+                    load_plane(A.v, head_of<HALF>(A.v, b, h), v0, vr);
+                }
+#pragma unroll
+                for (int i = 0; i < kStates; ++i) {
+                    const int64_t at = (int64_t)v0 * DK + 4 * (u + i * kThreads);
+                    sr[i] = four(s_before + at);
+                    gr[i] = four(s_behind + at);
                 }
             };
-            const auto load_states = [&](int v0) {
-#pragma unroll
-                for (int c = 0; c < ND; ++c) {
-                    const int64_t at = (int64_t)(wd + 16 * c + col) * A.value_pad + v0 + row4;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        sr[c][i] = four(s_before + at + 16 * i);
-                        gr[c][i] = four(s_behind + at + 16 * i);
-                    }
-                }
-            };
-            const auto store_block = [&](int buffer, int v0) {
-                if (!loads) return;
-                auto &B = sh.block[buffer];
-                store4(B.x, row, v4, mine ? xr : zero);
-                store4(B.w, row, v4, mine ? wr : zero);
-                if constexpr (TF) {
-                    const int v = u / (C / 4), t4 = u % (C / 4) * 4;
-                    f32x4 o = v0 + v < A.value ? orr : zero;
-                    if (!whole) o = only_steps(o, t4, r0, r1);
-                    store4(B.out, v, t4, o);
-                } else {
-                    f32x4 o;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = mine && v0 + v4 + e < A.value ? orr[e] : 0.0f;
-                    store4(B.out, row, v4, o);
-                }
-            };
-            {
-                In k_raw, q_raw;
-                k_raw.load(A.k, head_of<HALF>(A.k, b, hk), 0, t0, A.key, A.T, u);
-                q_raw.load(A.q, head_of<HALF>(A.q, b, hk), 0, t0, A.key, A.T, u);
-                load_block(0);
-                if (kAhead) load_states(0);
-                // X_i . v_i: eight lanes for a step, from its parts of 16 columns
-                const int r = u / 8, parts = A.value_pad / 16;
-                const float *const p = A.xv + (item * C + min(r, C - 1)) * parts;
-                const int j = u % 8;
-                const float first = p[min(j, parts - 1)], second = p[min(j + 8, parts - 1)];
-                __syncthreads();
-                k_raw.store(sh.keys, r0, r1, A.key, u);
-                q_raw.store(sh.queries, r0, r1, A.key, u);
-                float xv = (16 * j < A.value ? first : 0.0f) + (16 * (j + 8) < A.value ? second : 0.0f);
-#pragma unroll
-                for (int o = 1; o < 8; o *= 2) xv += __shfl_xor(xv, o);
-                if (j == 0 && r < C) sh.xv[r] = xv;
-            }
+            In k_raw, q_raw;
+            k_raw.load(A.k, head_of<HALF>(A.k, b, hk), 0, t0, A.key, A.T, u);
+            q_raw.load(A.q, head_of<HALF>(A.q, b, hk), 0, t0, A.key, A.T, u);
+            load_block(0);
+            if (r0 == 0) gates = use_gates<C>(A, loaded, t0);
+            r1 = document_end(gates.cut, r0, rows);
+            const bool before = !(gates.cut >> r0 & 1), behind = r1 == rows, whole = r0 == 0 && r1 == C;
+            __syncthreads();
             if (wave == 0) write_factors(sh.F, gates, r0, r1);
+            k_raw.store(sh.keys, r0, r1, A.key, u);
+            q_raw.store(sh.queries, r0, r1, A.key, u);
             const Factors<C> &F = sh.F;
+            auto &B = sh.block;
 
-            f32x4 U[NT][ND], Y[NT][ND], Z[NT][ND], ow[NT], xw[NT];
+            f32x4 U[NT][ND], Y[NT][ND], Z[NT][ND], ow[NT], xw[NT], xv = zero;
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
                 ow[a] = xw[a] = zero;
@@ -2109,34 +2098,84 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                 for (int c = 0; c < ND; ++c) U[a][c] = Y[a][c] = Z[a][c] = zero;
             }
             float ss = 0.0f;
-            for (int v0 = 0, buffer = 0; v0 < A.value; v0 += VB, buffer ^= 1) {
-                store_block(buffer, v0);
-                if (!kAhead) load_states(v0);
-                Wide sw[ND], gw[ND];
+            const auto values = [&]() {
+                f32x4 x;
 #pragma unroll
-                for (int c = 0; c < ND; ++c) {
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (HALF)
+                        x[e] = __uint_as_float(e % 2 ? vr[e / 2] & 0xffff0000u : vr[e / 2] << 16);
+                    else
+                        x[e] = __uint_as_float(vr[e]);
+                }
+                return x;
+            };
+            const auto store_state = [&](int tile, const f32x4 (&x)[kStates], bool there) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!before) sr[c][i] = zero;
-                        if (!behind) gr[c][i] = zero;
+                for (int i = 0; i < kStates; ++i) {
+                    const int at = u + i * kThreads;
+                    store4(B.s[tile], at / (DK / 4), at % (DK / 4) * 4, there ? x[i] : zero);
+                }
+            };
+            for (int v0 = 0; v0 < A.value; v0 += VB) {
+                if (v0 > 0) __syncthreads();
+                if (loads) {
+                    if (!whole) xr = only_steps(xr, pt4, r0, r1), wr = only_steps(wr, pt4, r0, r1);
+                    store4(B.x, pv, pt4, xr);
+                    store4(B.w, pv, pt4, wr);
+                    f32x4 o;
+                    if constexpr (TF) {
+                        const bool here = v0 + pv < A.value;
+                        f32x4 val = here ? values() : zero;
+                        o = here ? orr : zero;
+                        if (!whole) o = only_steps(o, pt4, r0, r1), val = only_steps(val, pt4, r0, r1);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) ss = fmaf_(sr[c][i][e], gr[c][i][e], ss);
+                        for (int e = 0; e < 4; ++e) xv[e] = fmaf_(xr[e], val[e], xv[e]);
+                        store4(B.out, pv, pt4, o);
+                    } else {
+                        const bool here = prow >= r0 && prow < r1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = here && v0 + pv4 + e < A.value ? orr[e] : 0.0f;
+                        store4(B.out, prow, pv4, o);
                     }
-                    sw[c] = stacked<HALF>(sr[c][0], sr[c][1]);
-                    gw[c] = stacked<HALF>(gr[c][0], gr[c][1]);
                 }
+#pragma unroll
+                for (int i = 0; i < kStates; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ss = before && behind ? fmaf_(sr[i][e], gr[i][e], ss) : 0.0f;
+                store_state(0, sr, before);
+                if (L::kBoth) store_state(L::kBoth ? 1 : 0, gr, behind);
                 __syncthreads();
-                if (v0 + VB < A.value) {
-                    load_block(v0 + VB);
-                    if (kAhead) load_states(v0 + VB);
-                }
-                const auto &B = sh.block[buffer];
-                const Wide wj = operand<true>(B.w, 16 * (pd < TT ? pd : 0), 0);
+                if constexpr (!TF)
+                    if (loads) {
+                        const f32x4 val = values();
+                        const bool here = prow >= r0 && prow < r1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (here && v0 + pv4 + e < A.value) xv[0] = fmaf_(value_at(B.x, pv4 + e, prow), val[e], xv[0]);
+                    }
+                const bool more = v0 + VB < A.value;
+                if (L::kBoth && more) load_block(v0 + VB);
+                using P = Product<Wide, Wide>;
+                const auto multiply_behind = [&]() {
+                    Wide gw[ND];
+#pragma unroll
+                    for (int c = 0; c < ND; ++c) gw[c] = operand<false>(B.s[L::kBoth ? 1 : 0], wd + 16 * c, 0);
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        const Wide wo = operand<false>(B.w, wt + 16 * a, 0);
+#pragma unroll
+                        for (int i = 0; i < P::kParts; ++i)
+#pragma unroll
+                            for (int c = 0; c < ND; ++c) Z[a][c] = P::part(i, Z[a][c], wo, gw[c]);
+                    }
+                };
+                Wide sw[ND];
+#pragma unroll
+                for (int c = 0; c < ND; ++c) sw[c] = operand<false>(B.s[0], wd + 16 * c, 0);
+                const Wide wj = operand<false>(B.w, 16 * (pd < TT ? pd : 0), 0);
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    using P = Product<Wide, Wide>;
-                    const Wide oo = operand<!TF>(B.out, wt + 16 * a, 0), xo = operand<true>(B.x, wt + 16 * a, 0),
-                               wo = operand<true>(B.w, wt + 16 * a, 0);
+                    const Wide oo = operand<!TF>(B.out, wt + 16 * a, 0), xo = operand<false>(B.x, wt + 16 * a, 0);
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int i = 0; i < P::kParts; ++i) {
@@ -2144,12 +2183,31 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                         for (int c = 0; c < ND; ++c) {
                             U[a][c] = P::part(i, U[a][c], oo, sw[c]);
                             Y[a][c] = P::part(i, Y[a][c], xo, sw[c]);
-                            Z[a][c] = P::part(i, Z[a][c], wo, gw[c]);
                         }
                         ow[a] = P::part(i, ow[a], oo, wj);
                         xw[a] = P::part(i, xw[a], xo, wj);
                     }
                 }
+                if (!L::kBoth) {
+                    __syncthreads();
+                    store_state(0, gr, behind);
+                    if (more) load_block(v0 + VB);
+                    __syncthreads();
+                }
+                multiply_behind();
+            }
+            if constexpr (TF) {
+#pragma unroll
+                for (int o = C / 4; o < kWave; o *= 2)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xv[e] += __shfl_xor(xv[e], o);
+                if (lane < C / 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sh.xv[wave][4 * lane + e] = xv[e];
+            } else {
+#pragma unroll
+                for (int o = 1; o < VB / 4; o *= 2) xv[0] += __shfl_xor(xv[0], o);
+                if (loads && u % (VB / 4) == 0) sh.xv[0][prow] = xv[0];
             }
             settle(ow);
             settle(xw);
@@ -2231,7 +2289,6 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
 #pragma unroll
                 for (int i = 0; i < 3; ++i) sh.dots[i][pd][t] = sums[i];
             }
-            if (pt != 0) ss = 0.0f;  // another wave's channels
 #pragma unroll
             for (int o = 1; o < kWave; o *= 2) ss += __shfl_xor(ss, o);
             if (lane == 0) sh.inner[wave] = ss;
@@ -2299,7 +2356,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                 double dG = 0.0, z = 0.0;
                 if (in) {
                     const int tile = row / 16;
-                    float qu = 0.0f, ky = 0.0f, kz = 0.0f, hs = 0.0f;
+                    float qu = 0.0f, ky = 0.0f, kz = 0.0f, hs = 0.0f, xs = 0.0f;
                     for (int w = 0; w < kD; ++w) {
                         qu += sh.dots[0][w][row];
                         ky += sh.dots[1][w][row];
@@ -2310,10 +2367,11 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                         dG += sh.row_sum[(tile * kD + j) * 16 + row % 16];
                     }
                     for (int i = tile; i < TT; ++i) dG -= sh.col_sum[(i * kD + tile) * 16 + row % 16];
+                    for (int w = 0; w < (TF ? kWaves : 1); ++w) xs += sh.xv[w][row];
                     const float y = F.start[row] * ky;
                     z = (double)F.end[row] * kz;
                     dG += (double)(A.scale * F.start[row]) * qu - (double)F.beta[row] * y - z;
-                    A.dbeta[bh * A.T + t0 + row] = sh.xv[row] - y + hs;
+                    A.dbeta[bh * A.T + t0 + row] = xs - y + hs;
                 }
                 double all = z, suffix;
 #pragma unroll

@@ -603,7 +603,7 @@ __device__ __forceinline__ void store_column(typename Num<HALF>::Elem *base, int
 {
     if (whole && step == 1) {
         if constexpr (HALF) {
-            const Words2 w = {bf16_bits(x[0]) | bf16_bits(x[1]) << 16, bf16_bits(x[2]) | bf16_bits(x[3]) << 16};
+            const Words2 w = {rounded(x[0], x[1]), rounded(x[2], x[3])};
             *reinterpret_cast<Words2Any *>(base + t) = w;
         } else {
             const Words4 w = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
@@ -638,28 +638,27 @@ struct LoadedGates {
     float g, beta;
     uint32_t reset;
 };
-template <int C>
+// (lanes without a step read another's, and use_gates() drops it)
 __device__ __forceinline__ LoadedGates fetch_gates(const Args &A, int64_t b, int64_t h, int64_t t0)
 {
-    const int lane = threadIdx.x % kWave;
-    const int64_t t = t0 + lane, at = b * A.gate_b + h * A.gate_h + t * A.gate_t;
-    LoadedGates l = {0.0f, 0.0f, 0};
-    if (lane < C && t < A.T) {
-        if (A.decay) l.g = A.decay[at];
-        l.beta = A.beta[at];
-        if (A.resets) l.reset = A.resets[b * A.T + t];
-    }
+    const int64_t t = min(t0 + threadIdx.x % kWave, A.T - 1), at = b * A.gate_b + h * A.gate_h + t * A.gate_t;
+    LoadedGates l = {0.0f, A.beta[at], 0};
+    if (A.decay) l.g = A.decay[at];
+    if (A.resets) l.reset = A.resets[b * A.T + t];
     return l;
 }
 template <int C>
 __device__ __forceinline__ StepGates use_gates(const Args &A, const LoadedGates &l, int64_t t0)
 {
-    return {l.g, l.beta, __ballot(l.reset != 0 || l.g < kForget), (int)(A.T - t0 < C ? A.T - t0 : C)};
+    const int lane = threadIdx.x % kWave;
+    const bool here = lane < C && t0 + lane < A.T;
+    return {here ? l.g : 0.0f, here ? l.beta : 0.0f, __ballot(here && (l.reset != 0 || l.g < kForget)),
+            (int)(A.T - t0 < C ? A.T - t0 : C)};
 }
 template <int C>
 __device__ __forceinline__ StepGates load_gates(const Args &A, int64_t b, int64_t h, int64_t t0)
 {
-    return use_gates<C>(A, fetch_gates<C>(A, b, h, t0), t0);
+    return use_gates<C>(A, fetch_gates(A, b, h, t0), t0);
 }
 __device__ __forceinline__ uint64_t steps_below(int n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
 // The first step after r0 that starts a document, or `rows`.
@@ -841,7 +840,7 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
     const unsigned chunks = (unsigned)A.chunks;
     const int64_t item = blockIdx.x, bh = blockIdx.x / chunks, n = blockIdx.x % chunks;
     const int64_t b = bh / A.Hv, h = bh % A.Hv, t0 = n * C;
-    const LoadedGates loaded = fetch_gates<C>(A, b, h, t0);
+    const LoadedGates loaded = fetch_gates(A, b, h, t0);
     const auto *keys = static_cast<const typename N::Elem *>(A.k.p) + b * A.k.b + h / (A.Hv / A.Hk) * A.k.h;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -1160,7 +1159,7 @@ struct Planner {
         r0 = BACK ? document_start(gates.cut, gates.rows) : 0;
         r1 = BACK ? gates.rows : document_end(gates.cut, 0, gates.rows);
         cut |= gates.cut != 0;
-        if (beyond(at)) next = fetch_gates<C>(A, at.b, at.h, (int64_t)(BACK ? n - 1 : n + 1) * C);
+        if (beyond(at)) next = fetch_gates(A, at.b, at.h, (int64_t)(BACK ? n - 1 : n + 1) * C);
     }
     __device__ __forceinline__ void advance(const Args &A, const Place &at)
     {
@@ -1585,29 +1584,36 @@ __global__ void __launch_bounds__((Roles<DK, NC, OUTPUT>::kWaves * kWave)) delta
     }
 }
 
+// Another lane's value, of the 16 of a group: rotated by 8 or 4 lanes, of the mirrored
+// lane of 8, and of a neighbour (the instruction set's codes).
+constexpr int kRotate8 = 0x128, kRotate4 = 0x124, kMirror8 = 0x141, kNext = 0xb1, kNext2 = 0x4e;
+template <int CODE>
+__device__ __forceinline__ float from_lane(float x)
+{
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CODE, 0xf, 0xf, true));
+}
 // Sums over the 16 lanes of a group, of M values each: at the end a lane holds
 // the sum of value `which` (with M < 16 several lanes the same one).  Half of the
-// values go to the neighbour at each step.
+// values go to another lane at each step, first to one whose lower bits differ too.
 template <int M>
 __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 {
-    static_assert(M == 16 || M == 8 || M == 4, "halves");
+    static_assert(M == 8 || M == 4, "halves");
     const int lane = threadIdx.x % kWave;
     which = 0;
-    const auto halve = [&](auto half, int bit) {
+    const auto halve = [&](auto half, auto code, int bit) {
         constexpr int m = decltype(half)::value;
         const bool upper = lane & bit;
         which += upper ? m : 0;
 #pragma unroll
-        for (int i = 0; i < m; ++i) x[i] = (upper ? x[i + m] : x[i]) + __shfl_xor(upper ? x[i] : x[i + m], bit);
+        for (int i = 0; i < m; ++i)
+            x[i] = (upper ? x[i + m] : x[i]) + from_lane<decltype(code)::value>(upper ? x[i] : x[i + m]);
     };
-    if constexpr (M == 16) halve(std::integral_constant<int, 8>(), 8);
-    if constexpr (M >= 8) halve(std::integral_constant<int, 4>(), 4);
-    halve(std::integral_constant<int, 2>(), 1);
-    halve(std::integral_constant<int, 1>(), 2);
-    if constexpr (M <= 4) x[0] += __shfl_xor(x[0], 4);
-    if constexpr (M <= 8) x[0] += __shfl_xor(x[0], 8);
-    return x[0];
+    if constexpr (M == 8) halve(std::integral_constant<int, 4>(), std::integral_constant<int, kMirror8>(), 4);
+    halve(std::integral_constant<int, 2>(), std::integral_constant<int, kNext>(), 1);
+    halve(std::integral_constant<int, 1>(), std::integral_constant<int, kNext2>(), 2);
+    if constexpr (M == 4) x[0] += from_lane<kRotate4>(x[0]);
+    return x[0] + from_lane<kRotate8>(x[0]);
 }
 
 // The chain backwards: the gradient of the state, from the last chunk to the
@@ -1984,7 +1990,6 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
     using Exact = typename N::Exact;
     using L = Gradients<HALF, DK, TF>;
     using In = typename L::In;
-    using Sl = Slots<N::kChunk>;
     constexpr int C = L::C, TT = L::TT, KC = C / 32, KD = DK / 32, kT = L::kT, kD = L::kD, VB = L::VB;
     constexpr int ND = L::DT / kD, NT = TT / kT;
     constexpr int kStates = VB * DK / 4 / kThreads;  // a thread's pieces of a state's columns
@@ -2007,11 +2012,16 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
             for (int c = 0; c < ND; ++c) dq[a][c] = dk[a][c] = zero;
     for (int head = 0; head < group; ++head) {
         const int64_t h = hk * group + head, bh = b * A.Hv + h, item = bh * A.chunks + n;
-        const LoadedGates loaded = fetch_gates<C>(A, b, h, t0);
+        const LoadedGates loaded = fetch_gates(A, b, h, t0);
         StepGates gates;
         const int rows = (int)min((int64_t)C, A.T - t0);
         const float *const s_before = A.states + item * DK * A.value_pad;
         const float *const s_behind = A.dstates + item * DK * A.value_pad;
+        // (without a gradient of the output its place is read all the same: a load that may
+        // not be under way would be waited for)
+        const bool has_go = A.o.p != nullptr;
+        const Plane go = {has_go ? A.o.p : A.x, has_go ? A.o.b : 0, has_go ? A.o.h : 0, has_go ? A.o.d : 0,
+                          has_go ? A.o.t : 0};
         const float *const x_at = A.x + item * C * A.value_pad, *const w_at = A.w + item * C * A.value_pad;
         for (int r0 = 0, r1; r0 < rows; r0 = r1) {
             const int lane = lane_afresh(threadIdx.x % kWave), row4 = 4 * (lane / 16), col = lane % 16;
@@ -2063,8 +2073,8 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                 if (loads) {
                     xr = four(x_at + (int64_t)v0 * C + 4 * u);
                     wr = four(w_at + (int64_t)v0 * C + 4 * u);
-                    uint32_t w[4] = {0, 0, 0, 0};
-                    if (A.o.p) load_plane(A.o, head_of<false>(A.o, b, h), v0, w);
+                    uint32_t w[4];
+                    load_plane(go, head_of<false>(go, b, h), v0, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) orr[e] = __uint_as_float(w[e]);
                     load_plane(A.v, head_of<HALF>(A.v, b, h), v0, vr);
@@ -2126,7 +2136,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                     if constexpr (TF) {
                         const bool here = v0 + pv < A.value;
                         f32x4 val = here ? values() : zero;
-                        o = here ? orr : zero;
+                        o = here && has_go ? orr : zero;
                         if (!whole) o = only_steps(o, pt4, r0, r1), val = only_steps(val, pt4, r0, r1);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) xv[e] = fmaf_(xr[e], val[e], xv[e]);
@@ -2134,7 +2144,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                     } else {
                         const bool here = prow >= r0 && prow < r1;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = here && v0 + pv4 + e < A.value ? orr[e] : 0.0f;
+                        for (int e = 0; e < 4; ++e) o[e] = here && has_go && v0 + pv4 + e < A.value ? orr[e] : 0.0f;
                         store4(B.out, prow, pv4, o);
                     }
                 }
@@ -2304,30 +2314,39 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(Args A)
                 }
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                const int t = wt + 16 * a, tile = pt * NT + a;
+                const int t = wt + 16 * a;
                 using P = Product<Wide, Exact>;
+                // steps up to the tile's own, and from it on: the first 32 and the last 32
+                // always, and of 64 the others of the tile's own half
+                constexpr int kLast = KC - 1;
+                const auto earlier = [&](const Wide &e, const Wide &h, int s) {
 #pragma unroll
-                for (int s = 0; s < KC; ++s) {
-                    if (Sl::in_lower(tile, s)) {
-                        const Wide e = operand<false>(sh.t.e, t, 32 * s), h = operand<false>(sh.t.h, t, 32 * s);
+                    for (int i = 0; i < P::kParts; ++i)
 #pragma unroll
-                        for (int i = 0; i < P::kParts; ++i)
+                        for (int c = 0; c < ND; ++c) {
+                            U[a][c] = P::part(i, U[a][c], e, kt[s][c]);
+                            Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
+                        }
+                };
+                const auto later = [&](const Wide &e, const Wide &h, int s) {
 #pragma unroll
-                            for (int c = 0; c < ND; ++c) {
-                                U[a][c] = P::part(i, U[a][c], e, kt[s][c]);
-                                Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
-                            }
-                    }
-                    if (Sl::in_upper(tile, s)) {
-                        const Wide e = operand<true>(sh.t.e, t, 32 * s), h = operand<true>(sh.t.h, t, 32 * s);
+                    for (int i = 0; i < P::kParts; ++i)
 #pragma unroll
-                        for (int i = 0; i < P::kParts; ++i)
-#pragma unroll
-                            for (int c = 0; c < ND; ++c) {
-                                Z[a][c] = P::part(i, Z[a][c], e, qt[s][c]);
-                                Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
-                            }
-                    }
+                        for (int c = 0; c < ND; ++c) {
+                            Z[a][c] = P::part(i, Z[a][c], e, qt[s][c]);
+                            Z[a][c] = P::part(i, Z[a][c], h, kt[s][c]);
+                        }
+                };
+                const Wide e0 = operand<false>(sh.t.e, t, 0), h0 = operand<false>(sh.t.h, t, 0);
+                const Wide e1 = operand<true>(sh.t.e, t, 32 * kLast), h1 = operand<true>(sh.t.h, t, 32 * kLast);
+                __builtin_amdgcn_sched_barrier(0);
+                earlier(e0, h0, 0);
+                later(e1, h1, kLast);
+                if constexpr (KC == 2) {
+                    if (pt == 0)
+                        later(operand<true>(sh.t.e, t, 0), operand<true>(sh.t.h, t, 0), 0);
+                    else
+                        earlier(operand<false>(sh.t.e, t, 32), operand<false>(sh.t.h, t, 32), 1);
                 }
             }
 #pragma unroll

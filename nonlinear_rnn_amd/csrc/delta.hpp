@@ -1306,6 +1306,11 @@ struct Server {
         k_raw.store(sh.keys_of(buffer), v.r0, v.r1, A.key, tid);
         if constexpr (QUERIES) q_raw.store(sh.queries_of(buffer), v.r0, v.r1, A.key, tid);
         plan.settle();
+    }
+    // what the visit after v has; in the visit's first half, as in the second the others
+    // wait for stage()
+    __device__ __forceinline__ void fetch(const Args &A, const Visit &v, int tid)
+    {
         // (also where the next visit has the same chunk: see the state's wave)
         load(A, v.leaves() ? (BACK ? max(v.n - 1, at_.n0) : min(v.n + 1, at_.n1 - 1)) : v.n, tid);
     }
@@ -1347,6 +1352,7 @@ __device__ __forceinline__ void chain_server(const Args &A, Chained<BACK, HALF, 
     for (int buffer = 0; now.here(); buffer ^= 1) {
         auto &sh = lds_afresh(shared);
         server.look(A, sh, buffer, c);
+        server.fetch(A, now, tid);
         if constexpr (QUERIES) make_scores<BACK, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         __syncthreads();
         if constexpr (BACK) __syncthreads();
@@ -1370,13 +1376,13 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
     const bool has_v = v < A.value;
     float *const o = static_cast<float *>(A.o.p) + at.b * A.o.b + at.h * A.o.h + v * A.o.d;
     // its slots of P: with servers one of the last two of six; else a share of all, of
-    // four waves two each to the first two
+    // four waves none to the one that plans
     constexpr bool kSix = kSlots == 6;
     int s0 = kSix ? 4 + c : 0, s1 = kSix ? 5 + c : 0;
     if constexpr (SERVES && NC == 2) s0 = kSlots / 2 * c, s1 = s0 + kSlots / 2;
     if constexpr (SERVES && NC == 4) {
-        s0 = kSix ? (c < 2 ? 2 * c : 2 + c) : min(c, 2);
-        s1 = kSix ? (c < 2 ? 2 * c + 2 : 3 + c) : min(c + 1, 2);
+        s0 = kSix ? max(2 * c - 2, 0) : min(max(c - 1, 0), 2);
+        s1 = c == 0 ? s0 : min(s0 + (kSix ? 2 : 1), kSlots);
     }
     [[maybe_unused]] Server<false, HALF, DK, NC, TF, true> server;
     Visit now;
@@ -1390,7 +1396,10 @@ __device__ __forceinline__ void chain_output(const Args &A, Forward<HALF, DK, NC
     for (int buffer = 0; now.here(); buffer ^= 1) {
         auto &sh = lds_afresh(shared);
         const Factors<C> &F = sh.factors[buffer];
-        if constexpr (SERVES) server.look(A, sh, buffer, c);
+        if constexpr (SERVES) {
+            server.look(A, sh, buffer, c);
+            server.fetch(A, now, tid);
+        }
         make_scores<false, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         f32x4 out[TT];
         {
@@ -1656,7 +1665,10 @@ __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC
     for (int buffer = 0; now.here(); buffer ^= 1) {
         auto &sh = lds_afresh(shared);
         const Factors<C> &F = sh.factors[buffer];
-        if constexpr (SERVES) server.look(A, sh, buffer, c);
+        if constexpr (SERVES) {
+            server.look(A, sh, buffer, c);
+            server.fetch(A, now, tid);
+        }
         make_scores<true, HALF, DK, NC, TF>(A, sh, buffer, now.near(), s0, s1);
         const bool whole = now.r0 == 0 && now.r1 == C;
         f32x4 x[TT];

@@ -823,7 +823,7 @@ __device__ __forceinline__ f32x4 block_mma(f32x4 c, f32x4 a, f32x4 b)
 // computed.
 constexpr int kInverseThreads = 4 * kWave;
 template <bool HALF, bool TF>
-__global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
+__global__ void __launch_bounds__(kInverseThreads, 5) delta_inverse_kernel(Args A)
 {
     using N = Num<HALF>;
     using S = Slots<N::kChunk>;
@@ -836,12 +836,13 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
         };
     } sh;
     __shared__ Factors<C> F;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
-    const unsigned chunks = (unsigned)A.chunks;
-    const int64_t item = blockIdx.x, bh = blockIdx.x / chunks, n = blockIdx.x % chunks;
-    const int64_t b = bh / A.Hv, h = bh % A.Hv, t0 = n * C;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const unsigned chunks = (unsigned)A.chunks, heads = (unsigned)A.Hv, shared = heads / (unsigned)A.Hk;
+    const unsigned head = blockIdx.x / chunks;
+    const int64_t item = blockIdx.x, n = blockIdx.x % chunks, b = head / heads, h = head % heads, t0 = n * C;
     const LoadedGates loaded = fetch_gates(A, b, h, t0);
-    const auto *keys = static_cast<const typename N::Elem *>(A.k.p) + b * A.k.b + h / (A.Hv / A.Hk) * A.k.h;
+    const auto *keys = static_cast<const typename N::Elem *>(A.k.p) + b * A.k.b + head % heads / shared * A.k.h;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
     f32x4 acc[kMine];
@@ -885,6 +886,7 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
     const auto joined = [&](int i, int j) {  // j <= i in one document
         return !(gates.cut & steps_below(i + 1) & ~steps_below(j + 1));
     };
+    const bool several = (gates.cut & ~1ull) != 0;  // documents
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
         const int p = wave + 4 * m;
@@ -895,12 +897,15 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
         const f32x4 d = decays_from(F, i, j), beta = four(F.beta + i);
         f32x4 a;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = i + r > j && joined(i + r, j) ? beta[r] * acc[m][r] * d[r] : 0.0f;
+        for (int r = 0; r < 4; ++r) a[r] = i + r > j ? beta[r] * acc[m][r] * d[r] : 0.0f;
+        if (several)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[r] = joined(i + r, j) ? a[r] : 0.0f;
         *reinterpret_cast<f32x4 *>(sh.m + j * kPitch + i) = a;
     }
     __syncthreads();
-    if (wave < TT && lane < 16) {
-        const int first = 16 * wave;
+    if (wave == 3 && lane < C) {  // all 16 x 16 blocks in one wave: the instructions bound this kernel
+        const int first = lane - col;
         f32x4 m[4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i / 4][i % 4] = i == col ? 1.0f : 0.0f;
@@ -959,7 +964,8 @@ __global__ void __launch_bounds__(kInverseThreads) delta_inverse_kernel(Args A)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int k = 32 * kt + row4 + (e < 4 ? e : 12 + e), i = columns ? k : row, j = columns ? row : k;
-            x[e] = i >= j && joined(i, j) ? sh.m[j * kPitch + i] : 0.0f;
+            x[e] = i >= j ? sh.m[j * kPitch + i] : 0.0f;
+            if (several && !joined(i, j)) x[e] = 0.0f;
         }
         Fragment *const out = (columns ? A.inverse_t : A.inverse) + item * S::kCount + s;
         store_fragment(*out, split(x, typename N::Wide()));

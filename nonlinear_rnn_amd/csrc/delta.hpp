@@ -1892,10 +1892,10 @@ __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
     constexpr int DT = DK / 16, kMine = (DT + 3) / 4, kPitch = DK + 4;
     __shared__ f32x4 state4[16 * kPitch / 4];
     float *const state = reinterpret_cast<float *>(state4);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, row4 = 4 * (lane / 16), col = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int tiles = A.value_pad / 16;
     const int64_t bh = blockIdx.x / tiles, v = 16 * (blockIdx.x % tiles) + col;
-    const int columns = A.value_pad + A.key_pad;
     const float *const first = BACK ? A.g_last : A.h0;
     // the state by columns, in LDS: rows of DK channels
     f32x4 S[kMine];
@@ -1906,10 +1906,46 @@ __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
         for (int r = 0; r < 4; ++r)
             S[m][r] = first && d0 + r < A.key && v < A.value ? first[(bh * A.key + d0 + r) * A.value + v] : 0.0f;
     }
+    // a segment's map: N's rows that the wave has, and M's as operands
+    struct Map {
+        f32x4 n[kMine], m[kMine][DT];
+        int cut;
+        __device__ __forceinline__ void load(const Args &A, int64_t seg, int64_t v, int wave)
+        {
+            const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
+            const int columns = A.value_pad + A.key_pad;
+            const float *const map = A.maps + seg * DK * columns;
+            cut = A.cuts[seg];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int d0 = min(16 * (wave + 4 * i), DK - 16);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) n[i][r] = map[(int64_t)(d0 + row4 + r) * columns + v];
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    const int d = min(d0 + col, A.key_pad - 1), k = min(16 * t + row4, A.key_pad - 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m[i][t][e] = map[(int64_t)(BACK ? k + e : d) * columns + A.value_pad + (BACK ? d : k + e)];
+                }
+            }
+        }
+    };
+    constexpr bool kAhead = DK < 256;  // registers for the next one's
+    Map map, next;
+    const auto segment = [&](int i) {
+        const int at = min(i, A.segments - 1);
+        return bh * A.segments + (BACK ? A.segments - 1 - at : at);
+    };
+    if (kAhead) next.load(A, segment(0), v, wave);
     for (int i = 0; i < A.segments; ++i) {
-        const int64_t seg = bh * A.segments + (BACK ? A.segments - 1 - i : i);
-        const float *const map = A.maps + seg * DK * columns;
-        const bool cut = A.cuts[seg] != 0;
+        const int64_t seg = segment(i);
+        if (kAhead) {
+            map = next;
+            next.load(A, segment(i + 1), v, wave);
+        } else {
+            map.load(A, seg, v, wave);
+        }
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
@@ -1917,27 +1953,20 @@ __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
             if (d0 >= DK) break;
             *reinterpret_cast<f32x4 *>(state + col * kPitch + d0) = S[m];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                A.marks[(seg * DK + d0 + r) * A.value_pad + v] = S[m][r];
-                S[m][r] = map[(int64_t)(d0 + r) * columns + v];
-            }
+            for (int r = 0; r < 4; ++r) A.marks[(seg * DK + d0 + r) * A.value_pad + v] = S[m][r];
+            S[m] = map.n[m];
         }
         __syncthreads();
-        if (cut) continue;
+        if (map.cut) continue;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int d0 = 16 * (wave + 4 * m);
-            if (d0 >= A.key_pad) break;
-            for (int k0 = 0; k0 < A.key_pad; k0 += 16) {
-                f32x4 a;
+            if (16 * (wave + 4 * m) >= A.key_pad) break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int d = d0 + col, k = k0 + row4 + j;
-                    a[j] = map[(int64_t)(BACK ? k : d) * columns + A.value_pad + (BACK ? d : k)];
-                }
-                S[m] = block_mma(S[m], a, four(state + col * kPitch + k0 + row4));
-            }
+            for (int t = 0; t < DT; ++t)
+                if (16 * t < A.key_pad)
+                    S[m] = block_mma(S[m], map.m[m][t], four(state + col * kPitch + 16 * t + row4));
         }
+        settle(S);
     }
 }
 

@@ -14,6 +14,7 @@ namespace adjust {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 8192;  // of a row, a workgroup
+constexpr int kAtOnce = 8;     // tokens of the history that a thread has under way
 
 struct Args {
     const void *x;
@@ -60,16 +61,28 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(Args A)
         if (listed) entries4[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
+    // the part's tokens: `skip` places of its first vector belong to the row before
+    const int skip = base < 0 ? (int)-base : 0;
+    const uint64_t tokens = (uint64_t)max((int64_t)0, min(A.V - base, (int64_t)kTokens) - skip);
     const auto place = [&](int64_t j) {  // in the part, or -1
-        return j >= 0 && j < A.V && j >= base && j < base + kTokens ? (int)(j - base) : -1;
+        const uint64_t at = (uint64_t)j - (uint64_t)(base + skip);
+        return at < tokens ? (int)at + skip : -1;
     };
-    for (int64_t i = threadIdx.x; i < length; i += kThreads) {
-        const int at = place(A.tokens[n * A.token_stride + i]);
-        if (at < 0) continue;
-        if (i >= prompt)
-            atomicAdd(&counts[at], 1u);
-        else
-            atomicOr(&counts[at], kSeen);
+    for (int64_t i0 = threadIdx.x; i0 < length; i0 += kAtOnce * kThreads) {
+        int64_t token[kAtOnce];
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s)
+            token[s] = A.tokens[n * A.token_stride + min(i0 + s * kThreads, length - 1)];
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s) {
+            const int64_t i = i0 + s * kThreads;
+            const int at = place(token[s]);
+            if (at < 0 || i >= length) continue;
+            if (i >= prompt)
+                atomicAdd(&counts[at], 1u);
+            else
+                atomicOr(&counts[at], kSeen);
+        }
     }
     for (int64_t i = threadIdx.x; i < A.biases; i += kThreads) {
         const int at = place(A.bias_index[n * A.biases + i]);

@@ -1020,11 +1020,11 @@ def _like_steps(B, H, d, T, like):
 
 
 def _delta_plan(q, k, v, beta, log_decay, h0, resets, out, go, g_last, workspace, adjoint):
+    _require(_is_tensor(v) and v.dim() == 4, "v: expected a tensor [B][Hv][dv][T]")
     for name, t in (("out", out), ("go", go)):
         if t is not None and (not _is_tensor(t) or t.dtype != torch.float32 or t.shape != v.shape):
             raise ValueError(f"{name}: must be float32 of v's shape")
     given = go if adjoint else out
-    _require(_is_tensor(v) and v.dim() == 4, "v: expected a tensor [B][Hv][dv][T]")
     os = _like_steps(*v.shape, v) if given is None else given.stride()
     shape, dt = _delta_shape(q, k, v, beta, log_decay, os)
     B, Hv, dv, T = v.shape

@@ -19,7 +19,10 @@ gradient for u comes back as one [B][T][G*D] tensor written by the adjoint.
 ``gated_scan``, ``delta_scan``, ``block_norm``, ``token_logprobs`` and
 ``distill_top`` are the differentiable forms of the operators of recurrent
 language models.  They have first
-derivatives: differentiating a gradient of theirs raises.
+derivatives: differentiating a gradient of theirs raises.  Their backward passes
+can be captured in a HIP graph together with the forward ones; no eager graph of
+the same leaves may be alive then (``delta_scan`` and ``distill_top`` refuse the
+leaves that they are given).
 
 Non-convergence is not an error in the solve; pass ``strict=True`` to raise
 when a solve stops at the iteration cap without reaching the tolerance (this
@@ -247,9 +250,28 @@ def gated_scan(u, lam, h0=None, *, power=8.0, resets=None):
     return _GatedScan.apply(ur, ui, ux, lam, h0, power, resets)
 
 
+def _check_leaves(*tensors):
+    """Refuses a capture in which a leaf among the operator's inputs is held by a
+    graph that was recorded before it, on another stream.  The captured backward
+    pass would have to wait for that stream, which ends the capture and with it
+    the process.  (The node that collects a leaf's gradient lives as long as a
+    graph that holds it: it keeps the stream that it was first met on.)"""
+    for t in tensors:
+        if t is None or not (t.is_leaf and t.requires_grad and t.is_cuda):
+            continue
+        stream = pr._raw_stream(t.device.index)
+        met = torch.autograd.graph.get_gradient_edge(t).node.metadata
+        if not pr._capturing(t.device, stream):
+            met.setdefault("pararnn_stream", stream)
+        elif met.get("pararnn_stream", stream) != stream:
+            raise RuntimeError("an input's gradient would be captured while an eager graph of it is alive: let "
+                               "go of that graph's outputs first, or record it on the stream of the capture")
+
+
 class _DeltaScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, beta, log_decay, h0, scale, resets):
+        _check_leaves(q, k, v, beta, log_decay, h0)
         if log_decay is not None and log_decay.stride() != beta.stride():
             beta, log_decay = beta.contiguous(), log_decay.contiguous()
         o, last = pr.delta_scan(q, k, v, beta, log_decay, h0, scale=scale, resets=resets)
@@ -338,6 +360,7 @@ def token_logprobs(logits, tokens, *, top=0, scale=1.0):
 class _DistillTop(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_index, top_logprob, tail, scale):
+        _check_leaves(logits)
         out = pr.distill_top(logits, top_index, top_logprob, tail=tail, scale=scale)
         ctx.save_for_backward(logits, top_index, top_logprob, out["lse"], out["log_rest"])
         ctx.tail, ctx.scale = tail, scale

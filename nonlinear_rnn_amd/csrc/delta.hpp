@@ -1780,13 +1780,12 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
         const int64_t after = now.leaves() && now.n > at.n0 ? now.n - 1 : now.n;
         f32x4 x[TT];
         join(sh);
-        if (now.enters()) S.store_row(A.dstates + item * DK * A.value_pad, v, in_row);
-        __syncthreads();
         f32x4 end[TT];
         times<!TF, KD>(x, K, [&](int d) { return stacked<HALF>(S.s[2 * d], S.s[2 * d + 1]); }, [&]() {
 #pragma unroll
             for (int t = 0; t < TT; ++t) end[t] = four(F.end + 16 * t + row4);
         });
+        __syncthreads();  // (the scores are there, for the helper)
         __syncthreads();
         const Visit then = read_visit(sh.visits[buffer ^ 1]);
         Wide p[KC];
@@ -1818,6 +1817,8 @@ __device__ __forceinline__ void back_state(const Args &A, Backward<HALF, DK, NC,
             start[t] = four(F.start + 16 * t + row4);
             beta[t] = four(F.beta + 16 * t + row4);
         }
+        // (not before the product: what is stored would be waited for with the inverse)
+        if (now.enters()) S.store_row(A.dstates + item * DK * A.value_pad, v, in_row);
         if (in_row) store_rows(A.x + item * C * A.value_pad, v, now.r0, now.r1, whole, x);
         auto *const dv_column = dv + (int64_t)now.n * C * A.dv.t + v * afresh(A.dv.d);
 #pragma unroll

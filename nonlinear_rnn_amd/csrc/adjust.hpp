@@ -37,7 +37,10 @@ constexpr uint32_t kSeen = 0x80000000u;  // in the prompt; the lower bits count 
 
 // A workgroup for a part of a row.  It goes through the row's whole history and
 // counts in LDS what falls into its part (integers: in any order); of a token's
-// entries in the bias list the last is kept.
+// entries in the bias list the last is kept.  Bound by vector instructions, about
+// as many for the history as for the logits: 512 rows of 100003 bfloat16, histories
+// of 6000: 87 us, 2.6 TB/s (one token at a time 107; parts of 16384 by 512 threads
+// 89).  16 rows of 65536 float32: 13 us.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(Args A)
 {

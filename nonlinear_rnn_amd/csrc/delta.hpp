@@ -711,7 +711,9 @@ struct alignas(16) Factors {
     float beta[C];
     float across[4];     // exp(G_C)
 };
-// Within 2^+-kNear, where a factor exp(G_i - G_j) may be the product of two.
+// Within 2^+-kNear, where a factor exp(G_i - G_j) may be the product of two: with an
+// exponential for each, 8 x 4096 x 8 heads take 231 us instead of 226, 4 x 16384 x 32
+// heads 1157 instead of 1114.
 constexpr double kNear = 32.0;
 // 2^x, its argument's rounding made good
 __device__ __forceinline__ float power_of_two(double x)
@@ -820,7 +822,9 @@ __device__ __forceinline__ f32x4 block_mma(f32x4 c, f32x4 a, f32x4 b)
 // in float32 products, in the matrix's own place.  (A lane for a whole column of
 // 64 needs every element of A in every lane: 500 wide LDS reads a chunk, or 1600
 // spilled registers.)  Entries between documents are set to zero rather than
-// computed.
+// computed.  Bound by vector instructions (650 a wave, twice that while every wave
+// inverted a block and every element asked for its document): 4096 chunks of 64
+// steps, 128 channels 38 us, 32768 of them 240 us, 0.7 GB at 2.8 TB/s.
 constexpr int kInverseThreads = 4 * kWave;
 template <bool HALF, bool TF>
 __global__ void __launch_bounds__(kInverseThreads, 5) delta_inverse_kernel(Args A)
@@ -1097,12 +1101,19 @@ __device__ __forceinline__ void read_channels(Exact (&k)[KC][DT], const In &tile
 // ------------------------------------------------------------- the chain ---
 
 // The chains' waves.  A workgroup has a head and 16 NC columns of the values: NC
-// waves with 16 columns of the state each in their registers, and as many
-// helpers, each beside one of them.  A wave multiplies what it has computed
-// from its registers, so between two chunks only the state itself is waited
-// for: the helpers bring the next keys and queries to LDS and take over the
-// products that the state does not need.  A `visit` is a chunk, or one document
-// of it.
+// waves with 16 columns of the state each in their registers, and others that
+// bring the next keys and queries to LDS and take over the products that the
+// state does not need (Roles below).  A wave multiplies what it has computed from
+// its registers, so between two chunks only the state itself is waited for.  A
+// `visit` is a chunk, or one document of it.
+//
+// Bound by a visit's way through the state's wave: three products one after the
+// other, each with its operands' split into two bfloat16 between (about 500 vector
+// instructions and 82 matrix instructions of 16 cycles), two barriers and the LDS
+// reads: 3.5 us of 64 steps and 32 columns (8 x 4096 x 8 heads of 128 x 128
+// bfloat16: 226 us, 5 us a visit before every wave's registers sufficed: a spilled
+// address was reloaded behind all loads under way).  The matrix cores are busy 12%
+// of the time, LDS 20%.  4 x 16384 x 32 heads: 1114 us, 2.0 TB/s.
 
 // A workgroup's head, columns and segment.
 struct Place {
@@ -1457,7 +1468,7 @@ __device__ __forceinline__ void chain_state(const Args &A, Forward<HALF, DK, NC,
     const int lane = threadIdx.x % kWave, row4 = 4 * (lane / 16), col = lane % 16;
     const int64_t v = 16 * (int64_t)(at.first + c) + col;
     const bool has_v = v < A.value, in_row = v < A.value_pad && !A.ends;
-    constexpr bool kEarly = DK < 256 && NC == 2 && !OUTPUT;  // registers for all of the keys' operands
+    constexpr bool kEarly = DK < 256 && NC == 2 && !OUTPUT;  // registers for all of the keys' operands, of 512
     State<DK> S;
     Wide operands[KD], inverse[Sl::kCount];
     Columns<HALF, C> value;
@@ -1635,6 +1646,9 @@ __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 // first, and X, the gradient of R.  A helper: P^T dO, which the state's wave needs
 // in the middle of a visit, and scale (exp(G) Q)^T dO, which joins the state a
 // visit later.  SERVES: also what a server does.
+// Bound like the forward chain, three barriers a visit: 8 x 4096 x 8 heads of 128 x
+// 128 bfloat16 345 us, 5.4 a visit (the inverses through LDS instead of the state's
+// wave's own loads: 410 us).
 template <bool HALF, int DK, int NC, bool TF, bool SERVES>
 __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
@@ -1886,7 +1900,8 @@ __global__ void __launch_bounds__((Roles<DK, NC, true>::kWaves * kWave)) delta_b
 // leaves the state before each (BACK: the state's gradient behind each) in `marks`;
 // then the chains run again from there.  Where a document starts in a segment
 // nothing of S is kept, whatever is in it.  A workgroup for a head and 16 columns,
-// float32 products.
+// float32 products.  Bound by the way along the segments, 0.9 us each (the next one's
+// map is read meanwhile, else 1.6): 64 of them, 64 x 64, 60 us.
 template <int DK, bool BACK>
 __global__ void __launch_bounds__(4 * kWave) delta_segments_kernel(Args A)
 {
@@ -2007,8 +2022,16 @@ __device__ __forceinline__ f32x4 steps_of(const Tile<HALF, ROWS, COLS> &x, int d
 // Two halves of the steps by four parts of the channels: a wave's rows of dO, X and
 // W are read once for all its channels (a wave for a part of the channels and all
 // steps reads twice as much from LDS, which bounds it then).  32 columns of the
-// values at a time; the next ones are loaded meanwhile.  SHARED: several value heads
-// share a key head, whose gradients are summed in registers.
+// values at a time; the next ones are loaded meanwhile.  The workspace's rows are
+// columns of the values, as the chains' waves hold them, who store 16 bytes a lane.
+// SHARED: several value heads share a key head, whose gradients are summed in
+// registers.
+// Bound by latency: one workgroup fits a CU, and its phases (loads, four blocks of
+// columns, E and H, the last products, the stores: 50000 cycles) wait for one
+// another.  4096 chunks of 128 x 128 bfloat16, 1.2 GB: 530 us, 2.3 TB/s (1066 us
+// while it spilled registers).  float32 80 x 100, 288 workgroups of three heads
+// each: 184 us, two rounds for 32 of them.  With 256 channels it spills 60 to 310
+// registers.
 template <bool HALF, int DK, bool TF>
 struct Gradients {
     using N = Num<HALF>;

@@ -256,12 +256,14 @@ def _check_leaves(*tensors):
     pass would have to wait for that stream, which ends the capture and with it
     the process.  (The node that collects a leaf's gradient lives as long as a
     graph that holds it: it keeps the stream that it was first met on.)"""
+    if not torch.is_grad_enabled():
+        return
     for t in tensors:
-        if t is None or not (t.is_leaf and t.requires_grad and t.is_cuda):
+        if not isinstance(t, torch.Tensor) or not (t.is_leaf and t.requires_grad and t.is_cuda):
             continue
         stream = pr._raw_stream(t.device.index)
         met = torch.autograd.graph.get_gradient_edge(t).node.metadata
-        if not pr._capturing(t.device, stream):
+        if not (stream and pr._capturing(t.device, stream)):  # (the default stream, 0, cannot be captured)
             met.setdefault("pararnn_stream", stream)
         elif met.get("pararnn_stream", stream) != stream:
             raise RuntimeError("an input's gradient would be captured while an eager graph of it is alive: let "
@@ -271,7 +273,6 @@ def _check_leaves(*tensors):
 class _DeltaScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, beta, log_decay, h0, scale, resets):
-        _check_leaves(q, k, v, beta, log_decay, h0)
         if log_decay is not None and log_decay.stride() != beta.stride():
             beta, log_decay = beta.contiguous(), log_decay.contiguous()
         o, last = pr.delta_scan(q, k, v, beta, log_decay, h0, scale=scale, resets=resets)
@@ -298,6 +299,7 @@ def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=Non
     """Differentiable gated delta rule (``pararnn.delta_scan``): gradients for q,
     k, v, beta, log_decay and h0.  Returns (o [B][Hv][dv][T],
     last [B][Hv][dk][dv])."""
+    _check_leaves(q, k, v, beta, log_decay, h0)
     return _DeltaScan.apply(q, k, v, beta, log_decay, h0, scale, resets)
 
 
@@ -360,7 +362,6 @@ def token_logprobs(logits, tokens, *, top=0, scale=1.0):
 class _DistillTop(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_index, top_logprob, tail, scale):
-        _check_leaves(logits)
         out = pr.distill_top(logits, top_index, top_logprob, tail=tail, scale=scale)
         ctx.save_for_backward(logits, top_index, top_logprob, out["lse"], out["log_rest"])
         ctx.tail, ctx.scale = tail, scale
@@ -379,5 +380,6 @@ def distill_top(logits, top_index, top_logprob, *, tail=True, scale=1.0):
     """Differentiable distillation loss (``pararnn.distill_top``): the gradient
     of the loss for the student's logits; lse and log_rest carry none, and the
     teacher's list is taken as given."""
+    _check_leaves(logits)
     loss, lse, log_rest = _DistillTop.apply(logits, top_index, top_logprob, tail, scale)
     return dict(loss=loss, lse=lse, log_rest=log_rest)

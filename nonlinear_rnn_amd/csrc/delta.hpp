@@ -1112,8 +1112,8 @@ __device__ __forceinline__ void read_channels(Exact (&k)[KC][DT], const In &tile
 // instructions and 82 matrix instructions of 16 cycles), two barriers and the LDS
 // reads: 3.5 us of 64 steps and 32 columns (8 x 4096 x 8 heads of 128 x 128
 // bfloat16: 226 us, 5 us a visit before every wave's registers sufficed: a spilled
-// address was reloaded behind all loads under way).  The matrix cores are busy 12%
-// of the time, LDS 20%.  4 x 16384 x 32 heads: 1114 us, 2.0 TB/s.
+// address was reloaded behind all loads under way).  The matrix cores are busy 17%
+// of the time, LDS 38%.  4 x 16384 x 32 heads: 1114 us, 2.0 TB/s.
 
 // A workgroup's head, columns and segment.
 struct Place {

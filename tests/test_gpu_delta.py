@@ -198,6 +198,39 @@ def test_segments_of_a_document_that_is_not_finite(half):
         assert torch.equal(good[2][n][..., 2001:], got[2][n][..., 2001:]), n
 
 
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("layout", ["channel", "time", "apart"])
+@pytest.mark.parametrize("size", [(1, 131, 1, 2, 200, 40), (2, 64, 1, 1, 256, 65)])
+def test_many_key_channels(size, layout, half):
+    """More than 128: one visit's keys and queries in LDS."""
+    c = dc.inputs(*size, half, docs=0.03)
+    t = dc.tensors(c, half, layout, DEV)
+    a = [t[n] for n in ("q", "k", "v", "beta", "log_decay", "h0")]
+    want, S = dc.oracle(c, size[4] ** -0.5)
+    o, last = pr.delta_scan(*a, resets=t["resets"])
+    dc.check(o, want, dc.FORWARD[half], "o")
+    dc.check(last, S, dc.FORWARD[half], "last")
+    out = pr.delta_scan_adjoint(*a, t["go"], g_last=t["g_last"], resets=t["resets"])
+    check_gradients(out, dc.oracle(c, size[4] ** -0.5, True), half)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("layout", ["channel", "time"])
+@pytest.mark.parametrize("size,docs", [((32, 70, 4, 8, 20, 40), 0.05), ((64, 1, 4, 4, 64, 64), 0.0), ((16, 131, 8, 16, 70, 33), 0.0),
+                                       ((4, 70, 32, 32, 128, 100), 0.02)])
+def test_many_chains(size, docs, layout, half):
+    """Where the chains are many a workgroup takes 64 columns."""
+    c = dc.inputs(*size, half, docs=docs)
+    t = dc.tensors(c, half, layout, DEV)
+    a = [t[n] for n in ("q", "k", "v", "beta", "log_decay", "h0")]
+    want, S = dc.oracle(c, size[4] ** -0.5)
+    o, last = pr.delta_scan(*a, resets=t["resets"])
+    dc.check(o, want, dc.FORWARD[half], "o")
+    dc.check(last, S, dc.FORWARD[half], "last")
+    out = pr.delta_scan_adjoint(*a, t["go"], g_last=t["g_last"], resets=t["resets"])
+    check_gradients(out, dc.oracle(c, size[4] ** -0.5, True), half)
+
+
 def test_no_gradients_given_and_empty():
     c = dc.inputs(1, 70, 1, 1, 16, 16, True)
     t = dc.tensors(c, True, "channel", DEV)

@@ -199,6 +199,11 @@ def test_a_capture_beside_an_eager_graph_of_the_same_leaves_is_refused():
         with pytest.raises(RuntimeError, match="eager graph"):
             capture(fn)
         torch.cuda.synchronize()
+    with torch.no_grad():  # nothing is recorded, so nothing is in the way
+        graph, out = capture(lambda: (pag.delta_scan(*leaves)[0], pag.distill_top(x, index, logprob)["loss"]))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], alive[0]) and torch.equal(out[1], alive[1])
     (alive[0].sum() + alive[1].sum()).backward()  # the eager graph is as it was
     assert all(p.grad is not None and bool(p.grad.isfinite().all()) for p in leaves + [x])
 

@@ -7,7 +7,8 @@
 //     scale (q_j (P + r) - p_j)                 for listed tokens, P = sum p_e,
 //     scale q_j (P + r - r / q_rest)            for the others.
 // q_rest is summed over the tokens themselves: as 1 - sum q_{j_e} it would be
-// lost where the student agrees with the teacher.  Sums are float32 relative
+// lost where the student agrees with the teacher.  q_j / q_rest is one
+// exponential, a share of r however small the two are.  Sums are float32 relative
 // to a running maximum; those of the short list float64.
 #pragma once
 
@@ -20,7 +21,12 @@ constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kParts = 32;              // most parts of a row
 constexpr int kSection = 16384;         // vectors whose listed elements are marked at once
 constexpr int kMost = PARARNN_DISTILL_MAX, kEach = (kMost + kThreads - 1) / kThreads;
+constexpr int kSectionAgain = 2048;     // the same in the gradient
 constexpr float kRest = 1e-6f;          // a smaller r is what rounding left of the list
+// A log q_rest below leaves its tokens' shares to their own largest logit and sum:
+// as a float32 it holds them within 2^-24 of its size, 4e-6 here, and where a mask of
+// -1e9 made it, not at all.
+constexpr float kFar = -64.0f;
 
 struct Args {
     const void *x;
@@ -152,25 +158,15 @@ __device__ __forceinline__ void finish(const Args &A, int64_t n, Sum rest, Share
     }
 }
 
-// A workgroup per row, or per part of a row (PARTS) where there are few.  The
-// listed tokens are marked in LDS, a byte for each 16-byte vector of the row,
-// and left out of the sum; they join it at the end.  Bound by HBM: 4096 rows of
-// 50003 bfloat16 89 us, 4.6 TB/s.
-template <bool BF16, bool PARTS>
-__global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
+// A thread's sum over vectors v0 .. v1 - 1 of the row, without the listed tokens:
+// these are marked in LDS, a byte for each 16-byte vector, SECTION vectors at once.
+// U of them under way in a lane.
+template <bool BF16, int SECTION, int U>
+__device__ __forceinline__ Sum rest_of(const Args &A, const RowView<BF16> &row, int64_t v0, int64_t v1,
+                                       const Shared &sh, uint32_t (&marks)[SECTION / 4])
 {
-    using Row = RowView<BF16>;
-    constexpr int K = Row::K, U = kScoreUnroll;
-    __shared__ Shared sh;
-    __shared__ uint32_t marks[kSection / 4];
-    const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
-    const int64_t p = PARTS ? blockIdx.x - n * A.parts : 0;
+    constexpr int K = RowView<BF16>::K;
     const float c = A.scale * kLog2e;
-    const Row row(A.x, n * A.stride, A.V);
-    const int64_t per = PARTS ? (row.vectors + A.parts - 1) / A.parts : row.vectors;
-    const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
-    load_list(A, n, sh);
-
     Sum a = no_sum();
     const auto add = [&](float (&x)[K], uint32_t mark) {
         float m = a.m;
@@ -183,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
 #pragma unroll
         for (int k = 0; k < K; ++k) a.s += ex2(c * (x[k] - m));
     };
-    for (int64_t s0 = v0; s0 < v1; s0 += kSection) {
-        const int64_t s1 = min(v1, s0 + kSection);
+    for (int64_t s0 = v0; s0 < v1; s0 += SECTION) {
+        const int64_t s1 = min(v1, s0 + SECTION);
         __syncthreads();
         for (int i = threadIdx.x; i < (int)((s1 - s0 + 3) / 4); i += kThreads) marks[i] = 0;
         __syncthreads();
@@ -209,6 +205,27 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
             add(x, mark(i));
         }
     }
+    return a;
+}
+
+// A workgroup per row, or per part of a row (PARTS) where there are few.  The
+// listed tokens join the others' sum at the end.  Bound by HBM: 4096 rows of 50003
+// bfloat16 89 us, 4.6 TB/s.
+template <bool BF16, bool PARTS>
+__global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
+{
+    using Row = RowView<BF16>;
+    __shared__ Shared sh;
+    __shared__ uint32_t marks[kSection / 4];
+    const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
+    const int64_t p = PARTS ? blockIdx.x - n * A.parts : 0;
+    const float c = A.scale * kLog2e;
+    const Row row(A.x, n * A.stride, A.V);
+    const int64_t per = PARTS ? (row.vectors + A.parts - 1) / A.parts : row.vectors;
+    const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
+    load_list(A, n, sh);
+
+    Sum a = rest_of<BF16, kSection, kScoreUnroll>(A, row, v0, v1, sh, marks);
     a = join_all(a, c, sh.sums);
     if constexpr (PARTS) {
         if (threadIdx.x == 0) A.part_stats[blockIdx.x] = make_float2(a.m, a.s);
@@ -233,21 +250,25 @@ __global__ void __launch_bounds__(kThreads) distill_join_kernel(Args A)
 // The gradient, U vectors a lane as in the scores' gradient: every token as
 // one that is not listed; then, behind a wait for these stores, the list's
 // tokens once more.  Their logits are read before anything is written, for the
-// gradient may take the logits' place.  Bound by HBM: 8192 rows of 32000 bfloat16
-// 255 us, 4.1 TB/s.
+// gradient may take the logits' place.  Where the student leaves less than e^kFar
+// to the other tokens, a rare row, its first workgroup sums these again and writes
+// all of it (nobody may write a row that is still to be summed).
+// Bound by HBM and vector instructions: 8192 rows of 32000 bfloat16 226 us a call,
+// 4.6 TB/s, float32 415 us, 5.0 TB/s.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
 {
     using Row = RowView<BF16>;
     constexpr int K = Row::K, U = kScoreUnroll;
     __shared__ Shared sh;
+    __shared__ uint32_t marks[kSectionAgain / 4];
     const int64_t n = blockIdx.x / A.parts;
     const Row row(A.x, n * A.stride, A.V);
     const int64_t first = (blockIdx.x - n * A.parts) * (U * kThreads), i = first + threadIdx.x;
-    float x[U][K];
+    uint4 raw[U];  // (as loaded: with twice the registers fewer waves fit)
 #pragma unroll
     for (int q = 0; q < U; ++q)
-        if (i + q * kThreads < row.vectors) row.load(i + q * kThreads, x[q]);
+        if (i + q * kThreads < row.vectors) raw[q] = row.load_raw(i + q * kThreads);
     load_list(A, n, sh);
     __syncthreads();
     // the part's entries
@@ -267,43 +288,79 @@ __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
     }
     P = add_all(P, sh.adds);
     any = __syncthreads_or(any);
-    const float lse = A.lse_in[n], g = A.scale * A.g_loss[n];
+    const float lse = A.lse_in[n], log_rest = A.log_rest_in[n], g = A.scale * A.g_loss[n];
     const bool none = !any || lse == -__builtin_inff();
     float r = A.tail ? (float)(1.0 - P) : 0.0f;
     if (r < kRest) r = 0.0f;
-    const float listed = (float)P + r, other = r == 0.0f ? listed : listed - r * expf(-A.log_rest_in[n]);
-    const auto q_of = [&](float v) { return none ? 0.0f : ex2(kLog2e * fmaf_(A.scale, v, -lse)); };
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-        if (i + q * kThreads >= row.vectors) break;
-        const int64_t e = row.element(i + q * kThreads);
+    const float listed = (float)P + r;
+    // a vector of tokens that are not listed, from the exponents of their exponentials
+    const auto write = [&](int64_t at, float (&d)[K], float weight) {
+        const int64_t e = row.element(at);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const float p = q_of(x[q][k]);
-            x[q][k] = p == 0.0f ? 0.0f : g * (p * other);  // 0 times an infinite factor
+            const float p = none ? 0.0f : ex2(d[k]);
+            d[k] = p == 0.0f ? 0.0f : g * (p * weight);
         }
         if (e >= 0) {
-            store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, x[q]);
+            store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, d);
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, x[q][k]);
+                if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, d[k]);
         }
-    }
-    __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
-    __syncthreads();
-    if (none) return;
+    };
+    const auto write_list = [&](int64_t e0, int64_t e1) {
+        __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
+        __syncthreads();
+        if (none) return;
 #pragma unroll
-    for (int s = 0; s < kEach; ++s) {
-        const int e = s * kThreads + threadIdx.x;
-        if (e >= A.count) break;
-        const int64_t j = sh.list[e];
-        if (j < 0 || j >= A.V || j < e0 || j >= e1 || !leads(sh, e)) continue;
-        float p = 0.0f;
-        for (int d = e; d < A.count; ++d)
-            if (sh.list[d] == j) p += expf(A.logprob[n * A.count + d]);
-        store_gate<BF16>(A.dx, n * A.dstride + j, g * fmaf_(q_of(mine[s]), listed, -p));
+        for (int s = 0; s < kEach; ++s) {
+            const int e = s * kThreads + threadIdx.x;
+            if (e >= A.count) break;
+            const int64_t j = sh.list[e];
+            if (j < 0 || j >= A.V || j < e0 || j >= e1 || !leads(sh, e)) continue;
+            float p = 0.0f;
+            for (int d = e; d < A.count; ++d)
+                if (sh.list[d] == j) p += expf(A.logprob[n * A.count + d]);
+            const float q = ex2(kLog2e * fmaf_(A.scale, mine[s], -lse));
+            store_gate<BF16>(A.dx, n * A.dstride + j, g * fmaf_(q, listed, -p));
+        }
+    };
+    if (!none && r > 0.0f && log_rest < kFar) {
+        if (first > 0) return;
+        const float c = A.scale * kLog2e;
+#pragma unroll
+        for (int s = 0; s < kEach; ++s) {
+            const int e = s * kThreads + threadIdx.x;
+            if (e < A.count && sh.list[e] >= 0 && sh.list[e] < A.V)
+                mine[s] = load_gate<BF16>(A.x, n * A.stride + sh.list[e]);
+        }
+        const Sum rest = join_all(rest_of<BF16, kSectionAgain, 1>(A, row, 0, row.vectors, sh, marks), c, sh.sums);
+        // (q_rest listed is nothing beside r, which is kRest at least)
+        const float weight = rest.s == 0.0f ? 0.0f : -r / rest.s;
+        for (int64_t at = threadIdx.x; at < row.vectors; at += kThreads) {
+            float d[K];
+            row.load(at, d);
+#pragma unroll
+            for (int k = 0; k < K; ++k) d[k] = c * (d[k] - rest.m);
+            write(at, d, weight);
+        }
+        write_list(0, A.V);
+        return;
     }
+    // r shares of q_rest, or without an r q itself
+    const float from = r == 0.0f ? lse : lse + log_rest;
+    const float weight = r == 0.0f ? listed : fmaf_(expf(log_rest), listed, -r);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        if (i + q * kThreads >= row.vectors) break;
+        float x[K];
+        Row::values(raw[q], x);
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = kLog2e * fmaf_(A.scale, x[k], -from);
+        write(i + q * kThreads, x, weight);
+    }
+    write_list(e0, e1);
 }
 
 }  // namespace distill

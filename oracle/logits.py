@@ -17,6 +17,12 @@ def _row(x, scale):
     return z - lse, lse
 
 
+def _sum_of(z):
+    """log sum exp, also of numbers whose exponentials are 0 in float64."""
+    m = z.max(initial=-np.inf)
+    return m + np.log(np.exp(z - m).sum()) if np.isfinite(m) else m
+
+
 def _teacher(index, logprob, tail):
     used = index >= 0
     p = np.where(used, np.exp(np.where(used, logprob, -np.inf)), 0.0)
@@ -33,8 +39,7 @@ def distill_top(logits, index, logprob, tail=True, scale=1.0):
         logq, out["lse"][n] = _row(x[n], scale)
         used, p, r = _teacher(index[n], np.asarray(logprob[n], np.float64), tail)
         others = np.setdiff1d(np.arange(V), index[n][used])
-        with np.errstate(divide="ignore"):
-            out["log_rest"][n] = rest = np.log(np.exp(logq[others]).sum())
+        out["log_rest"][n] = rest = _sum_of(logq[others])
         if not used.any():
             continue
         if (index[n] >= V).any():
@@ -58,9 +63,10 @@ def distill_top_adjoint(logits, index, logprob, g_loss, tail=True, scale=1.0):
         q, P = np.exp(logq), p.sum()
         listed = np.zeros(V, bool)
         listed[index[n][used]] = True
-        rest = q[~listed].sum()
-        share = r / rest if r > 0 and rest > 0 else 0.0
-        grad = q * (P + r) - np.where(listed, 0.0, q * share)
+        grad = q * (P + r)
+        z = scale * x[n, ~listed]
+        if r > 0 and not np.isneginf(z.max(initial=-np.inf)):  # (not from log q: next to a mask of -1e38 it is the mask)
+            grad[~listed] -= r * np.exp(z - z.max() - _sum_of(z - z.max()))
         np.add.at(grad, index[n][used], -p[used])
         out[n] = g_loss[n] * scale * grad
     return out

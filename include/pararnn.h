@@ -566,9 +566,9 @@ pararnn_status_t pararnn_distill_top(int64_t N, int64_t V, const void *logits,
  *     g_loss scale (q_j (P + r) - p_j)            for listed tokens,
  *     g_loss scale q_j (P + r - r / q_rest)       for the others
  * (r = 0 without a tail), from the forward's lse and log_rest.  A row whose
- * logits are all -inf has gradient 0.  dlogits has the dtype of the logits,
- * rows d_stride elements apart, and may be the logits' own memory (same
- * stride).
+ * logits are all -inf has gradient 0, one with an index past the vocabulary NaN.
+ * dlogits has the dtype of the logits, rows d_stride elements apart, and may be
+ * the logits' own memory (same stride).
  */
 pararnn_status_t pararnn_distill_top_adjoint(int64_t N, int64_t V, const void *logits,
                                              pararnn_dtype_t dtype, int64_t row_stride,

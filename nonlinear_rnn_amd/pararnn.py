@@ -1376,7 +1376,8 @@ def distill_top(logits, top_index, top_logprob, *, tail=True, scale=1.0, workspa
     sum_e p_e (log p_e - log q_e) + r (log r - log q_rest) with q = softmax(scale
     logits), r what the list leaves and q_rest the student's probability of the
     tokens not listed (the second term only with ``tail``).  Returns dict(loss,
-    lse, log_rest), [N] float32; a row without an entry has loss 0."""
+    lse, log_rest), [N] float32; a row without an entry has loss 0, one with an
+    index past the vocabulary NaN, and so have their gradients."""
     lib = load()
     N, V, stride, dt, _, top, nws, dev = _planned(
         ("distill", _signature(logits, top_index, top_logprob, workspace)), _distill_plan, logits, top_index,

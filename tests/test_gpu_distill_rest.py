@@ -1,5 +1,5 @@
 """The distillation's gradient where the student leaves next to nothing to the
-tokens that are not listed.
+tokens that are not listed, and where an index is past the vocabulary.
 
 Bounds, u = 2^-24.  A token that is not listed has the share r exp(d) / s of the
 gradient, d = scale (x - max) and s the sum of these exponentials: d is rounded
@@ -8,8 +8,8 @@ itself; s within (V / 256 + 32) u (a thread's share, then a tree) and what its
 terms are off by; r = 1 - P within 4 u P + u.  Nearer than e^-64 the share comes
 from lse and log q_rest instead, which hold three such sums and are float32 numbers
 of up to 64 + |lse|, with five roundings of that size; q_j (P + r) comes with it.  A
-listed token has q within such a sum and 64 u, and p within 16 u.  Rounding to bfloat16: half a step,
-2^-8."""
+listed token has q within such a sum and 64 u, and p within 16 u.  Rounding to
+bfloat16: half a step, 2^-8."""
 import numpy as np
 import pytest
 import torch
@@ -82,3 +82,21 @@ def test_shares_of_next_to_nothing(far, V, scale, half):
         assert (np.abs(got.sum(1)) <= tol.sum(1)).all()
     inplace = pr.distill_top_adjoint(*args, scale=scale, out=dev[0])
     assert inplace.data_ptr() == dev[0].data_ptr() and torch.equal(inplace, grad)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("V", [300, 50001])
+def test_an_index_past_the_vocabulary(V, half):
+    """Its loss is NaN; so is the whole row's gradient, and no other's."""
+    g = torch.Generator(DEV).manual_seed(V)
+    x = torch.randn((4, V), generator=g, device=DEV).to(torch.bfloat16 if half else torch.float32)
+    x[3] = -float("inf")
+    index = torch.randint(0, V, (4, 6), generator=g, device=DEV)
+    lp = torch.full((4, 6), -2.0, device=DEV)
+    good, ones = index.clone(), torch.ones(4, device=DEV)
+    index[1, 4], index[3, 0] = V, 2 ** 40
+    out, fine = pr.distill_top(x, index, lp), pr.distill_top(x, good, lp)
+    assert out["loss"].isnan().tolist() == [False, True, False, True]
+    grad = pr.distill_top_adjoint(x, index, lp, out["lse"], out["log_rest"], ones)
+    want = pr.distill_top_adjoint(x, good, lp, fine["lse"], fine["log_rest"], ones)
+    assert bool(grad[[1, 3]].isnan().all()) and torch.equal(grad[[0, 2]], want[[0, 2]])

@@ -21,8 +21,10 @@ gradient for u comes back as one [B][T][G*D] tensor written by the adjoint.
 language models.  They have first
 derivatives: differentiating a gradient of theirs raises.  Their backward passes
 can be captured in a HIP graph together with the forward ones; no eager graph of
-the same leaves may be alive then (``delta_scan`` and ``distill_top`` refuse the
-leaves that they are given).
+the same leaves may be alive then, unless it was recorded on the stream of the
+capture.  ``delta_scan`` and ``distill_top`` refuse a leaf that they are given where
+such a graph is one of theirs, or was alive when they were last called on the leaf
+outside of a capture; a leaf behind other operations is not seen.
 
 Non-convergence is not an error in the solve; pass ``strict=True`` to raise
 when a solve stops at the iteration cap without reaching the tolerance (this
@@ -250,24 +252,48 @@ def gated_scan(u, lam, h0=None, *, power=8.0, resets=None):
     return _GatedScan.apply(ur, ui, ux, lam, h0, power, resets)
 
 
-def _check_leaves(*tensors):
-    """Refuses a capture in which a leaf among the operator's inputs is held by a
-    graph that was recorded before it, on another stream.  The captured backward
-    pass would have to wait for that stream, which ends the capture and with it
-    the process.  (The node that collects a leaf's gradient lives as long as a
-    graph that holds it: it keeps the stream that it was first met on.)"""
-    if not torch.is_grad_enabled():
-        return
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or not (t.is_leaf and t.requires_grad and t.is_cuda):
-            continue
-        stream = pr._raw_stream(t.device.index)
-        met = torch.autograd.graph.get_gradient_edge(t).node.metadata
-        if not (stream and pr._capturing(t.device, stream)):  # (the default stream, 0, cannot be captured)
-            met.setdefault("pararnn_stream", stream)
-        elif met.get("pararnn_stream", stream) != stream:
+_NOTE = "pararnn_stream"
+
+
+def _stream_of(t):
+    """(the current stream's handle on the tensor's device, whether it is being
+    captured); None for a tensor that is not on a GPU."""
+    if not t.is_cuda:
+        return None
+    stream = pr._raw_stream(t.device.index)
+    return stream, bool(stream) and pr._capturing(t.device, stream)  # (the default stream, 0, cannot be captured)
+
+
+def _record(function, *args):
+    """``function.apply(*args)``, but no capture in which a leaf among the inputs
+    is held by a graph that was recorded before it on another stream: the captured
+    backward pass would have to wait for that stream, which ends the capture and
+    with it the process.
+
+    The node that collects a leaf's gradient belongs to the stream that it was made
+    on, and lives as long as a graph holds it.  So the stream is noted on the nodes
+    that the new graph holds.  A node that had no note before an eager call, and
+    that another operator's graph holds, gets None: it may belong to any stream.
+    (In a capture such a node is taken for the capture's own.)"""
+    leaves = []
+    if torch.is_grad_enabled():
+        for t in args:
+            if isinstance(t, torch.Tensor) and t.is_leaf and t.requires_grad:
+                at = _stream_of(t)
+                if at is not None:
+                    leaves.append((t, *at))
+    for t, stream, captured in leaves:
+        # (a node that nobody holds is gone behind this statement, and its note with it)
+        known = torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault(_NOTE, stream if captured else None)
+        if captured and known != stream:
             raise RuntimeError("an input's gradient would be captured while an eager graph of it is alive: let "
                                "go of that graph's outputs first, or record it on the stream of the capture")
+    out = function.apply(*args)
+    if leaves:
+        for node, _ in out[0].grad_fn.next_functions:
+            if hasattr(node, "variable"):  # a leaf's
+                node.metadata.setdefault(_NOTE, leaves[0][1])
+    return out
 
 
 class _DeltaScan(torch.autograd.Function):
@@ -299,8 +325,7 @@ def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=Non
     """Differentiable gated delta rule (``pararnn.delta_scan``): gradients for q,
     k, v, beta, log_decay and h0.  Returns (o [B][Hv][dv][T],
     last [B][Hv][dk][dv])."""
-    _check_leaves(q, k, v, beta, log_decay, h0)
-    return _DeltaScan.apply(q, k, v, beta, log_decay, h0, scale, resets)
+    return _record(_DeltaScan, q, k, v, beta, log_decay, h0, scale, resets)
 
 
 class _BlockNorm(torch.autograd.Function):
@@ -380,6 +405,5 @@ def distill_top(logits, top_index, top_logprob, *, tail=True, scale=1.0):
     """Differentiable distillation loss (``pararnn.distill_top``): the gradient
     of the loss for the student's logits; lse and log_rest carry none, and the
     teacher's list is taken as given."""
-    _check_leaves(logits)
-    loss, lse, log_rest = _DistillTop.apply(logits, top_index, top_logprob, tail, scale)
+    loss, lse, log_rest = _record(_DistillTop, logits, top_index, top_logprob, tail, scale)
     return dict(loss=loss, lse=lse, log_rest=log_rest)

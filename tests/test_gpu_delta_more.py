@@ -1,0 +1,71 @@
+"""The gated delta rule on the GPU: segments of long chains in every layout, the
+gradients of equal keys, results that repeat."""
+import numpy as np
+import pytest
+import torch
+
+from nonlinear_rnn_amd import pararnn as pr
+from tests import delta_cases as dc
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("q", "k", "v", "beta", "log_decay", "h0")
+
+
+def check_all(c, t, half, scale, slack=1.0):
+    a = [t[n] for n in NAMES]
+    o, last = pr.delta_scan(*a, resets=t["resets"])
+    want, S = dc.oracle(c, scale)
+    dc.check(o, want, slack * dc.FORWARD[half], "o")
+    dc.check(last, S, slack * dc.FORWARD[half], "last")
+    out = pr.delta_scan_adjoint(*a, t["go"], g_last=t["g_last"], resets=t["resets"])
+    want = dc.oracle(c, scale, True)
+    for n in ("dq", "dk", "dv", "dbeta", "dlog_decay", "dh0"):
+        if out[n] is not None:
+            dc.check(out[n], want[n], 2 * slack * dc.FORWARD[half], n, half and n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("layout", ["time", "slices", "apart"])
+@pytest.mark.parametrize("size,docs", [((1, 2100, 1, 2, 64, 40), 0.0005), ((2, 2113, 1, 1, 100, 33), 0.0),
+                                       ((1, 2900, 1, 3, 200, 20), 0.002), ((1, 2048, 1, 1, 128, 128), 0.0)])
+def test_long_chains_of_few_heads_in_every_layout(size, docs, layout, half):
+    c = dc.inputs(*size, half, docs=docs)
+    c["log_decay"] = np.float32(0.02 * c["log_decay"]).astype(np.float64)  # a segment's state matters to the next
+    check_all(c, dc.tensors(c, half, layout, DEV), half, size[4] ** -0.5)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("rate", [0.0, 1.0, 2.0])
+def test_gradients_of_equal_keys_and_full_rates(rate, half):
+    """At rate 2 the maps keep every rounding of 128 steps: four times the forward
+    pass's bound, as its own test has it, and twice that for a gradient."""
+    c = dc.inputs(1, 128, 1, 1, 16, 16, half, decay="none")
+    c["k"][:] = 0.25  # 16 channels: unit length, and exact
+    c["beta"][:] = rate
+    check_all(c, dc.tensors(c, half, "channel", DEV), half, 0.25, 4.0)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("size,layout", [((4, 1500, 8, 8, 128, 128), "channel"), ((2, 700, 4, 12, 80, 100), "time"),
+                                         ((1, 4096, 1, 2, 64, 64), "channel"), ((2, 300, 1, 2, 256, 64), "channel"),
+                                         ((8, 1, 4, 4, 64, 64), "channel")])
+def test_results_repeat(size, layout, half):
+    """The same bits from every call, whatever the workspace held before."""
+    c = dc.inputs(*size, half, docs=0.003)
+    t = dc.tensors(c, half, layout, DEV)
+    a = [t[n] for n in NAMES]
+    first = None
+    for value in (0, 255, 63, 0, 127):  # 255: NaN
+        ws = [torch.full((pr_bytes(t, adjoint),), value, dtype=torch.uint8, device=DEV) for adjoint in (0, 1)]
+        o, last = pr.delta_scan(*a, resets=t["resets"], workspace=ws[0])
+        g = pr.delta_scan_adjoint(*a, t["go"], g_last=t["g_last"], resets=t["resets"], workspace=ws[1])
+        got = dict(g, o=o, last=last)
+        first = first or got
+        assert all(torch.equal(got[n], first[n]) for n in got), value
+
+
+def pr_bytes(t, adjoint):
+    plan = pr._delta_plan(*[t[n] for n in NAMES], t["resets"], None, t["go"] if adjoint else None, None, None, adjoint)
+    return max(16, plan[3])

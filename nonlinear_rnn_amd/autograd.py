@@ -299,7 +299,7 @@ def _record(function, *args):
 class _DeltaScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, beta, log_decay, h0, scale, resets):
-        if log_decay is not None and log_decay.stride() != beta.stride():
+        if log_decay is not None and log_decay.shape == beta.shape and not pr._same_steps(log_decay, beta):
             beta, log_decay = beta.contiguous(), log_decay.contiguous()
         o, last = pr.delta_scan(q, k, v, beta, log_decay, h0, scale=scale, resets=resets)
         ctx.save_for_backward(q, k, v, beta, log_decay, h0, resets)

@@ -986,6 +986,12 @@ def _call(dev, function, *args):
             _check(function(*args))
 
 
+def _same_steps(a, b):
+    """Whether two tensors of one shape have the same strides wherever something
+    steps along them."""
+    return not a.numel() or all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
 def _delta_shape(q, k, v, beta, log_decay, o):
     """Checks what all of the delta rule's calls take, with a last dimension of
     one step for `delta_step`; (shape record, dtype code).  o: strides."""
@@ -1004,7 +1010,7 @@ def _delta_shape(q, k, v, beta, log_decay, o):
             continue
         if not _is_tensor(t) or tuple(t.shape) != (B, Hv, T) or t.dtype != torch.float32:
             raise ValueError(f"{name}: must be float32 {[B, Hv, T]}")
-        if t.numel() and t.stride() != beta.stride():
+        if not _same_steps(t, beta):
             raise ValueError("beta and log_decay must share their strides")
     four, three = ctypes.c_int64 * 4, ctypes.c_int64 * 3
     return DeltaShape(B, T, Hk, Hv, dk, dv, four(*q.stride()), four(*k.stride()), four(*v.stride()),
@@ -1047,11 +1053,11 @@ def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=Non
     S <- exp(log_decay) S, w = beta (v - k^T S), S <- S + k w^T, o = scale q^T S.
     q, k [B][Hk][dk][T], v [B][Hv][dv][T] float32 or bfloat16 (Hv a multiple of
     Hk: neighbouring value heads share a key head; steps or channels side by
-    side are the fast layouts), beta and log_decay [B][Hv][T] float32 (None: no
-    decay), h0 [B][Hv][dk][dv] float32 or None (zero), scale None: dk ** -0.5,
-    resets [B][T] bool or None: True where a new document starts.  Returns
-    (o [B][Hv][dv][T], last [B][Hv][dk][dv]), float32; ``o.flatten(1, 2)`` is
-    the plane that ``block_norm`` takes."""
+    side are the fast layouts), beta and log_decay [B][Hv][T] float32 of the
+    same strides (log_decay None: no decay), h0 [B][Hv][dk][dv] float32 or None
+    (zero), scale None: dk ** -0.5, resets [B][T] bool or None: True where a new
+    document starts.  Returns (o [B][Hv][dv][T], last [B][Hv][dk][dv]), float32;
+    ``o.flatten(1, 2)`` is the plane that ``block_norm`` takes."""
     lib = load()
     shape, dt, os, nws, dev = _planned(
         ("delta", _signature(q, k, v, beta, log_decay, h0, resets, out, workspace)),
@@ -1125,7 +1131,8 @@ def _delta_step_plan(q, k, v, beta, log_decay, states, slots, out):
 
 def delta_step(q, k, v, beta, log_decay, states, *, slots=None, scale=None, out=None, stream=None):
     """One step of the gated delta rule for B requests: q, k [B][Hk][dk], v
-    [B][Hv][dv], beta and log_decay [B][Hv] (None: no decay), states
+    [B][Hv][dv], beta and log_decay [B][Hv] of the same strides (log_decay None:
+    no decay), states
     [pool][Hv][dk][dv] float32, updated in place, slots [B] int32 or None (row
     b has slot b).  A row whose slot is outside the pool (-1) is idle: it gives
     zeros and changes no state; live rows need distinct slots.  Returns o

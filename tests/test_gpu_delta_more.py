@@ -1,9 +1,11 @@
 """The gated delta rule on the GPU: segments of long chains in every layout, the
-gradients of equal keys, results that repeat."""
+gradients of equal keys, results that repeat, gates whose strides differ where
+nothing steps."""
 import numpy as np
 import pytest
 import torch
 
+from nonlinear_rnn_amd import autograd as pag
 from nonlinear_rnn_amd import pararnn as pr
 from tests import delta_cases as dc
 from tests.gpu_util import DEV
@@ -69,3 +71,27 @@ def test_results_repeat(size, layout, half):
 def pr_bytes(t, adjoint):
     plan = pr._delta_plan(*[t[n] for n in NAMES], t["resets"], None, t["go"] if adjoint else None, None, None, adjoint)
     return max(16, plan[3])
+
+
+@pytest.mark.parametrize("shape", [(3, 2, 1), (1, 1, 70), (1, 2, 1), (1, 2, 70)])
+def test_gates_whose_strides_differ_where_nothing_steps(shape):
+    """A slice of a wider projection beside a tensor of its own."""
+    B, Hv, T = shape
+    c = dc.inputs(B, T, 1, Hv, 16, 20, False)
+    t = dc.tensors(c, False, "channel", DEV)
+    wide = torch.zeros((B, 7, T), device=DEV) if B == 1 else torch.zeros((B, T, Hv), device=DEV).transpose(1, 2)
+    beta = wide[:, 2:2 + Hv] if B == 1 else wide
+    beta.copy_(t["beta"])
+    assert beta.stride() != t["log_decay"].stride()
+    t["beta"] = beta
+    check_all(c, t, False, 0.25)
+    a = [t[n] for n in NAMES]
+    want = pr.delta_scan(*a)
+    leaves = [x.clone(memory_format=torch.preserve_format).requires_grad_(True) for x in a]
+    got = pag.delta_scan(leaves[0], leaves[1], leaves[2], beta, leaves[4], leaves[5])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    (got[0].sum() + got[1].sum()).backward()
+    if T == 1:
+        states = t["h0"].clone()
+        o = pr.delta_step(*[x[..., 0] for x in a[:5]], states)
+        dc.check(o, dc.oracle(c, 0.25)[0][..., 0], 2.0 ** -19, "step")

@@ -499,7 +499,8 @@ pararnn_status_t pararnn_delta_scan(const pararnn_delta_shape_t *shape, const vo
                                     void *ws, size_t ws_bytes, void *stream);
 /*
  * Its backward pass, for L = sum <go, o> + <g_last, last>.
- *   go      : o's strides, or NULL (zero);  g_last : dense, or NULL (zero)
+ *   go      : at o_stride (elements may repeat), or NULL (zero)
+ *   g_last  : dense, or NULL (zero)
  *   dq, dk, dv : dtype, their own strides; heads that share a key head are
  *             summed in a fixed order
  *   dbeta, dlog_decay : [B][Hv][T] float32, dense (dlog_decay NULL without one)

@@ -39,7 +39,8 @@ bool fits(const int64_t (&size)[N], const int64_t *stride, bool apart)
 int64_t chunk_of(pararnn_dtype_t dtype) { return dtype == PARARNN_BF16 ? Bf::kChunk : Fl::kChunk; }
 int room_of(int64_t dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
 
-pararnn_status_t check_delta(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool step)
+// writes_o: the plane at o_stride is written, not the gradient that is read there.
+pararnn_status_t check_delta(const pararnn_delta_shape_t *s, pararnn_dtype_t dtype, bool step, bool writes_o)
 {
     if (!s) return PARARNN_ERR_INVALID;
     if (s->B < 0 || s->T < 0 || s->Hk < 0 || s->Hv < 0 || s->dk < 1 || s->dv < 1) return PARARNN_ERR_INVALID;
@@ -52,7 +53,7 @@ pararnn_status_t check_delta(const pararnn_delta_shape_t *s, pararnn_dtype_t dty
     const int64_t key[4] = {s->B, s->Hk, s->dk, s->T}, value[4] = {s->B, s->Hv, s->dv, s->T};
     const int64_t gate[3] = {s->B, s->Hv, s->T};
     if (!fits(key, s->q_stride, false) || !fits(key, s->k_stride, false) || !fits(value, s->v_stride, false) ||
-        !fits(value, s->o_stride, !step || s->T > 0) || !fits(gate, s->gate_stride, false))
+        !fits(value, s->o_stride, writes_o) || !fits(gate, s->gate_stride, false))
         return PARARNN_ERR_INVALID;
     // a dispatch counts its work-items in 32 bits
     const int64_t most = int64_t(1) << 32, heads = s->B * s->Hv;
@@ -136,7 +137,7 @@ pararnn_status_t prepare(Args &A, const pararnn_delta_shape_t *s, pararnn_dtype_
                          const void *v, const float *beta, const float *log_decay, const float *h0,
                          const uint8_t *resets, float scale, bool adjoint, void *ws, size_t ws_bytes)
 {
-    const pararnn_status_t st = check_delta(s, dtype, false);
+    const pararnn_status_t st = check_delta(s, dtype, false, !adjoint);
     if (st != PARARNN_OK) return st;
     if (!std::isfinite(scale)) return PARARNN_ERR_INVALID;
     if (s->B > 0 && s->Hv > 0 && s->T > 0 && (!q || !k || !v || !beta)) return PARARNN_ERR_INVALID;
@@ -210,7 +211,7 @@ extern "C" {
 
 size_t pararnn_delta_workspace_bytes(const pararnn_delta_shape_t *shape, pararnn_dtype_t dtype, int adjoint)
 {
-    if (check_delta(shape, dtype, false) != PARARNN_OK) return 0;
+    if (check_delta(shape, dtype, false, !adjoint) != PARARNN_OK) return 0;
     return layout(shape, dtype, adjoint != 0).total;
 }
 
@@ -261,7 +262,7 @@ pararnn_status_t pararnn_delta_step(const pararnn_delta_shape_t *shape, const vo
                                     const int32_t *slots, float *states, int64_t pool, float scale, float *o,
                                     void *stream)
 {
-    const pararnn_status_t st = check_delta(shape, dtype, true);
+    const pararnn_status_t st = check_delta(shape, dtype, true, true);
     if (st != PARARNN_OK) return st;
     if (pool < 0 || !std::isfinite(scale)) return PARARNN_ERR_INVALID;
     if (shape->B == 0 || shape->Hv == 0) return PARARNN_OK;

@@ -1079,7 +1079,8 @@ def delta_scan(q, k, v, beta, log_decay=None, h0=None, *, scale=None, resets=Non
 def delta_scan_adjoint(q, k, v, beta, log_decay, h0, go, *, g_last=None, scale=None, resets=None,
                        workspace=None, stream=None):
     """Backward pass of ``delta_scan`` for L = sum <go, o> + <g_last, last>; go
-    [B][Hv][dv][T] float32 or None (zero), g_last [B][Hv][dk][dv] or None.
+    [B][Hv][dv][T] float32 (it may be expanded) or None (zero), g_last
+    [B][Hv][dk][dv] or None.
     Returns dict(dq, dk, dv in the inputs' dtype, dbeta, dlog_decay [B][Hv][T],
     dh0 [B][Hv][dk][dv]); dlog_decay and dh0 are None where their input is."""
     lib = load()

@@ -1,10 +1,12 @@
 """Strides that the gated delta rule takes, on the CPU: tensors pass every check
-of the binding but the last one."""
+of the binding but the last one, and the C ABI gets as far as the workspace."""
+import ctypes
+
 import pytest
 import torch
 
 from nonlinear_rnn_amd import pararnn as pr
-from tests.test_delta_refusals import heads, step
+from tests.test_delta_refusals import INVALID, NULL, WORKSPACE, common, heads, shape, step
 
 
 @pytest.mark.parametrize("B,Hv,T", [(2, 3, 1), (1, 3, 5), (1, 1, 5), (1, 3, 1)])
@@ -26,3 +28,14 @@ def test_gates_that_differ_are_refused():
         pr.delta_scan(**heads(B=1, Hv=2, T=5, log_decay=torch.zeros(1, 5, 2).transpose(1, 2)))
     with pytest.raises(ValueError, match="strides"):
         step(log_decay=torch.zeros(2, 2).t(), beta=torch.zeros(2, 2))
+
+
+@pytest.mark.parametrize("o", [[0, 0, 0, 0], [120, 30, 0, 1], [30, 30, 5, 1]])
+def test_a_gradient_of_the_output_may_repeat_elements(o):
+    """It is only read; the output itself may not."""
+    a, head = common(dict(sh=shape(o=o)))
+    call = pr.load().pararnn_delta_scan_adjoint
+    assert call(*head, a["go"], NULL, ctypes.byref(a["g"]), NULL, 0, NULL) == WORKSPACE
+    assert pr.load().pararnn_delta_scan(*head, a["o"], NULL, NULL, 0, NULL) == INVALID
+    _, head = common(dict(sh=shape(o=[120, 30, -5, 1])))
+    assert call(*head, a["go"], NULL, ctypes.byref(a["g"]), NULL, 0, NULL) == INVALID

@@ -1,6 +1,6 @@
 """The gated delta rule on the GPU: segments of long chains in every layout, the
 gradients of equal keys, results that repeat, gates whose strides differ where
-nothing steps."""
+nothing steps, gradients that repeat elements."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +95,18 @@ def test_gates_whose_strides_differ_where_nothing_steps(shape):
         states = t["h0"].clone()
         o = pr.delta_step(*[x[..., 0] for x in a[:5]], states)
         dc.check(o, dc.oracle(c, 0.25)[0][..., 0], 2.0 ** -19, "step")
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("size", [(2, 70, 1, 2, 24, 40), (1, 2100, 1, 1, 64, 33)])
+def test_a_gradient_that_repeats_elements(size, half):
+    """The gradient of a sum, of which no copy is made."""
+    c = dc.inputs(*size, half, docs=0.01)
+    t = dc.tensors(c, half, "channel", DEV)
+    a = [t[n] for n in NAMES]
+    B, T, _, Hv, _, dv = size
+    for go in (torch.ones((), device=DEV).expand(B, Hv, dv, T), t["go"][..., :1].expand(B, Hv, dv, T),
+               t["go"][:, :, :1].expand(B, Hv, dv, T)):
+        got = pr.delta_scan_adjoint(*a, go, resets=t["resets"])
+        want = pr.delta_scan_adjoint(*a, go.contiguous(), resets=t["resets"])
+        assert all(torch.equal(got[n], want[n]) for n in got)

@@ -1619,8 +1619,9 @@ __device__ __forceinline__ float from_lane(float x)
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CODE, 0xf, 0xf, true));
 }
 // Sums over the 16 lanes of a group, of M values each: at the end a lane holds
-// the sum of value `which` (with M < 16 several lanes the same one).  Half of the
-// values go to another lane at each step, first to one whose lower bits differ too.
+// the sum of value `which` (with M < 16 several lanes the same one, to the last bit:
+// they all write it to one place).  Half of the values go to another lane at each
+// step, first to one whose lower bits differ too.
 template <int M>
 __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 {
@@ -1638,8 +1639,9 @@ __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
     if constexpr (M == 8) halve(std::integral_constant<int, 4>(), std::integral_constant<int, kMirror8>(), 4);
     halve(std::integral_constant<int, 2>(), std::integral_constant<int, kNext>(), 1);
     halve(std::integral_constant<int, 1>(), std::integral_constant<int, kNext2>(), 2);
-    if constexpr (M == 4) x[0] += from_lane<kRotate4>(x[0]);
-    return x[0] + from_lane<kRotate8>(x[0]);
+    // (lanes 8 apart first: the sums of both pairs are then the same in either order)
+    x[0] += from_lane<kRotate8>(x[0]);
+    return M == 4 ? x[0] + from_lane<kRotate4>(x[0]) : x[0];
 }
 
 // The chain backwards: the gradient of the state, from the last chunk to the

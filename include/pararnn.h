@@ -477,10 +477,29 @@ pararnn_status_t pararnn_token_logprobs_adjoint(int64_t N, int64_t V, const void
  *   o       : [B][Hv][dv][T]-indexed float32 out
  *   last    : [B][Hv][dk][dv] float32 out, the last state (h0 at T = 0), or NULL
  *   ws      : pararnn_delta_workspace_bytes(shape, dtype, 0) bytes
- * Strides are of (b, h, d, t), and of (b, h, t) for the gates.  The fast
- * layouts have the steps side by side (stride 1 along t) or the channels
- * (stride 1 along d), the same for all; inputs may repeat elements (stride
- * 0), outputs not.  dk is at most PARARNN_DELTA_KEY_MAX.
+ * Strides are of (b, h, d, t), and of (b, h, t) for the gates; inputs may
+ * repeat elements (stride 0), outputs not.  The fast layout has the steps side
+ * by side (stride 1 along t).  With the channels side by side, as a linear
+ * layer leaves them, a bfloat16 scan takes 1.5 times as long and its backward
+ * pass 1.15 times, and where dk is no multiple of 8 2.5 and 1.55 times; float32
+ * 1.0 to 1.15 times.  dk is at most PARARNN_DELTA_KEY_MAX.
+ *
+ * Numbers: with float32 inputs all products are float32's.  With bfloat16
+ * inputs what is multiplied with them (states, what the steps write, the
+ * gradients) is rounded to two bfloat16, 16 bits and more, so that float32
+ * results are about 5e-6 off in norm, not 3e-7; pass float32 copies where that
+ * matters.  A number that is not finite can make the steps before it NaN, too,
+ * of its document in its chunk of 64 steps (float32: 32), not those of earlier
+ * chunks or of other documents: padding whose content is undefined belongs into
+ * a document of its own.
+ *
+ * Workspace: forward 12 KB (float32: 4 KB) for a head's chunk of 64 (32)
+ * steps.  Backward twice that and the states before and behind each chunk, and
+ * two numbers for each value: 8 bytes times (K + chunk) times dv, K being dk
+ * rounded up to 64, 128 or 256 and dv to a multiple of 32.  That is 0.9 GB for
+ * B = 8, T = 4096, 8 heads of 128 x 128 in bfloat16, and 22 GB for B = 4, T =
+ * 16384, 32 heads of 256 x 256.  Rows of the batch do not meet: calls for some
+ * of them need as much less.
  */
 #define PARARNN_DELTA_KEY_MAX 256
 typedef struct {

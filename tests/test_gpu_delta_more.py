@@ -110,3 +110,21 @@ def test_a_gradient_that_repeats_elements(size, half):
         got = pr.delta_scan_adjoint(*a, go, resets=t["resets"])
         want = pr.delta_scan_adjoint(*a, go.contiguous(), resets=t["resets"])
         assert all(torch.equal(got[n], want[n]) for n in got)
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("bad", ["q", "k", "v", "beta", "log_decay"])
+def test_a_number_that_is_not_finite_leaves_earlier_chunks_alone(bad, half):
+    """And, where what holds it is a document of its own, all that is before it."""
+    c = dc.inputs(1, 200, 1, 2, 24, 16, half)
+    t = dc.tensors(c, half, "channel", DEV)
+    good = pr.delta_scan(*[t[n] for n in NAMES])[0]
+    padding = torch.arange(200, device=DEV)[None] == 150
+    alone = pr.delta_scan(*[t[n] for n in NAMES], resets=padding)[0]
+    t[bad][..., 150:] = float("nan")
+    got = pr.delta_scan(*[t[n] for n in NAMES])[0]
+    assert torch.equal(got[..., :128], good[..., :128])  # chunks of 64 steps, or of 32
+    got = pr.delta_scan(*[t[n] for n in NAMES], resets=padding)[0]
+    assert torch.equal(got[..., :150], alone[..., :150])
+    if bad != "q":
+        assert bool(got[..., 150:].isnan().any())

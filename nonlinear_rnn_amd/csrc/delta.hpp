@@ -34,6 +34,10 @@
 // differences of them are taken in two floats, so that a decay keeps its
 // precision behind a step that forgot everything.
 //
+// Times in these files are of the kernel under the kernel trace, both sides of a
+// choice in the same run; from run to run they differ by a tenth (the first calls
+// are the slow ones), so a call may take less than its kernels' times together.
+//
 // Documents.  A step where a document starts (its reset flag, or a log decay
 // below kForget, whose exponential float32 does not hold) keeps nothing of the
 // state, whatever is in it.  A chunk that holds several documents is visited
@@ -824,7 +828,7 @@ __device__ __forceinline__ f32x4 block_mma(f32x4 c, f32x4 a, f32x4 b)
 // spilled registers.)  Entries between documents are set to zero rather than
 // computed.  Bound by vector instructions (650 a wave, twice that while every wave
 // inverted a block and every element asked for its document): 4096 chunks of 64
-// steps, 128 channels 38 us, 32768 of them 240 us, 0.7 GB at 2.8 TB/s.
+// steps, 128 channels 38 us, 32768 of them 209 us, 0.7 GB at 3.2 TB/s.
 constexpr int kInverseThreads = 4 * kWave;
 template <bool HALF, bool TF>
 __global__ void __launch_bounds__(kInverseThreads, 5) delta_inverse_kernel(Args A)
@@ -1113,7 +1117,7 @@ __device__ __forceinline__ void read_channels(Exact (&k)[KC][DT], const In &tile
 // reads: 3.5 us of 64 steps and 32 columns (8 x 4096 x 8 heads of 128 x 128
 // bfloat16: 226 us, 5 us a visit before every wave's registers sufficed: a spilled
 // address was reloaded behind all loads under way).  The matrix cores are busy 17%
-// of the time, LDS 38%.  4 x 16384 x 32 heads: 1114 us, 2.0 TB/s.
+// of the time, LDS 38%.  4 x 16384 x 32 heads: 1020 us, 2.1 TB/s.
 
 // A workgroup's head, columns and segment.
 struct Place {
@@ -1649,8 +1653,8 @@ __device__ __forceinline__ float sum_columns(float (&x)[M], int &which)
 // in the middle of a visit, and scale (exp(G) Q)^T dO, which joins the state a
 // visit later.  SERVES: also what a server does.
 // Bound like the forward chain, three barriers a visit: 8 x 4096 x 8 heads of 128 x
-// 128 bfloat16 345 us, 5.4 a visit (the inverses through LDS instead of the state's
-// wave's own loads: 410 us).
+// 128 bfloat16 324 us, 5 a chunk (the inverses through LDS instead of the state's
+// wave's own loads: 410 us instead of 345).
 template <bool HALF, int DK, int NC, bool TF, bool SERVES>
 __device__ __forceinline__ void back_helper(const Args &A, Backward<HALF, DK, NC, TF> &shared, const Place &at, int c)
 {
@@ -2030,10 +2034,10 @@ __device__ __forceinline__ f32x4 steps_of(const Tile<HALF, ROWS, COLS> &x, int d
 // registers.
 // Bound by latency: one workgroup fits a CU, and its phases (loads, four blocks of
 // columns, E and H, the last products, the stores: 50000 cycles) wait for one
-// another.  4096 chunks of 128 x 128 bfloat16, 1.2 GB: 530 us, 2.3 TB/s (1066 us
+// another.  4096 chunks of 128 x 128 bfloat16, 1.2 GB: 510 us, 2.4 TB/s (1066 us
 // while it spilled registers).  float32 80 x 100, 288 workgroups of three heads
-// each: 184 us, two rounds for 32 of them.  With 256 channels it spills 60 to 310
-// registers.
+// each: 181 us, two rounds for 32 of them.  With 256 channels it spills 66 to 320
+// registers: 8 x 4096 x 8 heads of 256 x 128 bfloat16 take 3.8 ms a call, 1.1 of 128.
 template <bool HALF, int DK, bool TF>
 struct Gradients {
     using N = Num<HALF>;

@@ -52,7 +52,8 @@ __device__ __forceinline__ float4 sum_rows(float4 x, float4 (&part)[kStepThreads
 // A workgroup for a request's head and 64 columns of its state, which is read
 // and written once: 16 threads side by side along a row, R rows each, 16 apart.
 // Bound by HBM where there are many requests, else by latency: 256 requests of 16
-// heads of 128 x 128, 537 MB: 86 us, 6.2 TB/s; 4 of 4 heads of 64 x 64: 4.6 us.
+// heads of 128 x 128, 537 MB: 115 us, 4.7 TB/s (86 us where the last call's states
+// are still in the cache); 4 of 4 heads of 64 x 64: 4.7 us.
 template <bool HALF, int R>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(StepArgs A)
 {

@@ -210,7 +210,7 @@ __device__ __forceinline__ Sum rest_of(const Args &A, const RowView<BF16> &row, 
 
 // A workgroup per row, or per part of a row (PARTS) where there are few.  The
 // listed tokens join the others' sum at the end.  Bound by HBM: 4096 rows of 50003
-// bfloat16 89 us, 4.6 TB/s.
+// bfloat16 90 us a call, 4.6 TB/s, float32 157 us, 5.2 TB/s.
 template <bool BF16, bool PARTS>
 __global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
 {

@@ -8,7 +8,8 @@
 //     scale q_j (P + r - r / q_rest)            for the others.
 // q_rest is summed over the tokens themselves: as 1 - sum q_{j_e} it would be
 // lost where the student agrees with the teacher.  q_j / q_rest is one
-// exponential, a share of r however small the two are.  Sums are float32 relative
+// exponential, a share of r however small the two are.  Where lse or log q_rest
+// are too large to hold the sums that they come from, the gradient sums again.  Sums are float32 relative
 // to a running maximum; those of the short list float64.
 #pragma once
 
@@ -27,6 +28,9 @@ constexpr float kRest = 1e-6f;          // a smaller r is what rounding left of 
 // as a float32 it holds them within 2^-24 of its size, 4e-6 here, and where a mask of
 // -1e9 made it, not at all.
 constexpr float kFar = -64.0f;
+// The same for q and an lse beyond: 6e-5 here, and a row that a finite mask left
+// nothing of loses its log V.
+constexpr float kLarge = 1024.0f;
 
 struct Args {
     const void *x;
@@ -111,24 +115,33 @@ __device__ __forceinline__ bool leads(const Shared &sh, int e)
         if (sh.list[i] == sh.list[e]) return false;
     return true;
 }
-// The row's results from the sum over the tokens that are not listed.
+// A thread's sum over the listed tokens.
 template <bool BF16>
-__device__ __forceinline__ void finish(const Args &A, int64_t n, Sum rest, Shared &sh)
+__device__ __forceinline__ Sum listed_of(const Args &A, int64_t n, const Shared &sh)
 {
     const float c = A.scale * kLog2e;
     Sum all = no_sum();
-    bool past = false, any = false;
     for (int e = threadIdx.x; e < A.count; e += kThreads) {
         const int64_t j = sh.list[e];
-        any |= j >= 0;
-        past |= j >= A.V;
         if (j < 0 || j >= A.V || !leads(sh, e)) continue;
         const float x = load_gate<BF16>(A.x, n * A.stride + j);
         Sum one = {fmaxf(x, -__FLT_MAX__), x == -__builtin_inff() ? 0.0f : 1.0f};
         if (!(x < __builtin_inff())) one.s = __builtin_nanf("");  // as in the other tokens' sum
         all = join(all, one, c);
     }
-    all = join(join_all(all, c, sh.sums), rest, c);
+    return all;
+}
+// The row's results from the sum over the tokens that are not listed.
+template <bool BF16>
+__device__ __forceinline__ void finish(const Args &A, int64_t n, Sum rest, Shared &sh)
+{
+    const float c = A.scale * kLog2e;
+    bool past = false, any = false;
+    for (int e = threadIdx.x; e < A.count; e += kThreads) {
+        any |= sh.list[e] >= 0;
+        past |= sh.list[e] >= A.V;
+    }
+    const Sum all = join(join_all(listed_of<BF16>(A, n, sh), c, sh.sums), rest, c);
     const bool empty = all.s == 0.0f;
     const float ls = logf(all.s);
     const float lse = empty ? -__builtin_inff() : fmaf_(A.scale, all.m, ls);
@@ -158,63 +171,45 @@ __device__ __forceinline__ void finish(const Args &A, int64_t n, Sum rest, Share
     }
 }
 
-// A thread's sum over vectors v0 .. v1 - 1 of the row, without the listed tokens:
-// these are marked in LDS, a byte for each 16-byte vector, SECTION vectors at once.
-// U of them under way in a lane.
-template <bool BF16, int SECTION, int U>
-__device__ __forceinline__ Sum rest_of(const Args &A, const RowView<BF16> &row, int64_t v0, int64_t v1,
-                                       const Shared &sh, uint32_t (&marks)[SECTION / 4])
+// Marks the listed tokens of vectors s0 .. s1 - 1 of the row, a byte for each vector.
+template <bool BF16, int SECTION>
+__device__ __forceinline__ void mark_listed(const Args &A, const RowView<BF16> &row, int64_t s0, int64_t s1,
+                                            const Shared &sh, uint32_t (&marks)[SECTION / 4])
 {
     constexpr int K = RowView<BF16>::K;
-    const float c = A.scale * kLog2e;
-    Sum a = no_sum();
-    const auto add = [&](float (&x)[K], uint32_t mark) {
-        float m = a.m;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (mark >> k & 1) x[k] = -__builtin_inff();
-            m = fmaxf(m, x[k]);
-        }
-        rebase(a, m, c);
-#pragma unroll
-        for (int k = 0; k < K; ++k) a.s += ex2(c * (x[k] - m));
-    };
-    for (int64_t s0 = v0; s0 < v1; s0 += SECTION) {
-        const int64_t s1 = min(v1, s0 + SECTION);
-        __syncthreads();
-        for (int i = threadIdx.x; i < (int)((s1 - s0 + 3) / 4); i += kThreads) marks[i] = 0;
-        __syncthreads();
-        for (int e = threadIdx.x; e < A.count; e += kThreads) {
-            const int64_t j = sh.list[e] + row.shift, at = j / K - s0;
-            if (sh.list[e] >= 0 && sh.list[e] < A.V && at >= 0 && at < s1 - s0)
-                atomicOr(&marks[at / 4], 1u << (8 * (at % 4) + j % K));
-        }
-        __syncthreads();
-        const auto mark = [&](int64_t i) { return marks[(i - s0) / 4] >> (8 * ((i - s0) % 4)) & 0xffu; };
-        int64_t i = s0 + threadIdx.x;
-        for (; i + (U - 1) * kThreads < s1; i += U * kThreads) {
-            float x[U][K];
-#pragma unroll
-            for (int q = 0; q < U; ++q) row.load(i + q * kThreads, x[q]);
-#pragma unroll
-            for (int q = 0; q < U; ++q) add(x[q], mark(i + q * kThreads));
-        }
-        for (; i < s1; i += kThreads) {
-            float x[K];
-            row.load(i, x);
-            add(x, mark(i));
-        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)((s1 - s0 + 3) / 4); i += kThreads) marks[i] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < A.count; e += kThreads) {
+        const int64_t j = sh.list[e] + row.shift, at = j / K - s0;
+        if (sh.list[e] >= 0 && sh.list[e] < A.V && at >= 0 && at < s1 - s0)
+            atomicOr(&marks[at / 4], 1u << (8 * (at % 4) + j % K));
     }
-    return a;
+    __syncthreads();
+}
+// Adds a vector's tokens but the marked ones.
+template <int K>
+__device__ __forceinline__ void add_unmarked(Sum &a, float (&x)[K], uint32_t mark, float c)
+{
+    float m = a.m;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (mark >> k & 1) x[k] = -__builtin_inff();
+        m = fmaxf(m, x[k]);
+    }
+    rebase(a, m, c);
+#pragma unroll
+    for (int k = 0; k < K; ++k) a.s += ex2(c * (x[k] - m));
 }
 
 // A workgroup per row, or per part of a row (PARTS) where there are few.  The
-// listed tokens join the others' sum at the end.  Bound by HBM: 4096 rows of 50003
-// bfloat16 90 us a call, 4.6 TB/s, float32 157 us, 5.2 TB/s.
+// listed tokens are left out of the sum and join it at the end.  Bound by HBM: 4096
+// rows of 50003 bfloat16 90 us a call, 4.6 TB/s, float32 153 us, 5.3 TB/s.
 template <bool BF16, bool PARTS>
 __global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
 {
     using Row = RowView<BF16>;
+    constexpr int K = Row::K, U = kScoreUnroll;
     __shared__ Shared sh;
     __shared__ uint32_t marks[kSection / 4];
     const int64_t n = PARTS ? blockIdx.x / A.parts : blockIdx.x;
@@ -225,7 +220,25 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Args A)
     const int64_t v0 = p * per, v1 = min(row.vectors, v0 + per);
     load_list(A, n, sh);
 
-    Sum a = rest_of<BF16, kSection, kScoreUnroll>(A, row, v0, v1, sh, marks);
+    Sum a = no_sum();
+    for (int64_t s0 = v0; s0 < v1; s0 += kSection) {
+        const int64_t s1 = min(v1, s0 + kSection);
+        mark_listed<BF16, kSection>(A, row, s0, s1, sh, marks);
+        const auto mark = [&](int64_t i) { return marks[(i - s0) / 4] >> (8 * ((i - s0) % 4)) & 0xffu; };
+        int64_t i = s0 + threadIdx.x;
+        for (; i + (U - 1) * kThreads < s1; i += U * kThreads) {
+            float x[U][K];
+#pragma unroll
+            for (int q = 0; q < U; ++q) row.load(i + q * kThreads, x[q]);
+#pragma unroll
+            for (int q = 0; q < U; ++q) add_unmarked(a, x[q], mark(i + q * kThreads), c);
+        }
+        for (; i < s1; i += kThreads) {
+            float x[K];
+            row.load(i, x);
+            add_unmarked(a, x, mark(i), c);
+        }
+    }
     a = join_all(a, c, sh.sums);
     if constexpr (PARTS) {
         if (threadIdx.x == 0) A.part_stats[blockIdx.x] = make_float2(a.m, a.s);
@@ -247,14 +260,83 @@ __global__ void __launch_bounds__(kThreads) distill_join_kernel(Args A)
     finish<BF16>(A, n, join_all(a, A.scale * kLog2e, sh.sums), sh);
 }
 
+// A token's gradient where it is not listed: g times exp(d) weight, base 2.  The
+// row's vector `at`, from its tokens' d.
+template <bool BF16>
+__device__ __forceinline__ void write_vector(const Args &A, int64_t n, const RowView<BF16> &row, int64_t at,
+                                             float (&d)[RowView<BF16>::K], float g, float weight, bool none)
+{
+    constexpr int K = RowView<BF16>::K;
+    const int64_t e = row.element(at);
+#pragma unroll
+    for (int k = 0; k < K; ++k) d[k] = none ? 0.0f : g * (ex2(d[k]) * weight);
+    if (e >= 0) {
+        store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, d);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, d[k]);
+    }
+}
+// That of the listed token at entry e, from its q.
+template <bool BF16>
+__device__ __forceinline__ void write_listed(const Args &A, int64_t n, const Shared &sh, int e, float g, float q,
+                                             float listed)
+{
+    const int64_t j = sh.list[e];
+    if (!leads(sh, e)) return;
+    float p = 0.0f;
+#pragma unroll 8  // (by itself the compiler takes 82 registers, which leaves 5 of 8 waves)
+    for (int d = e; d < A.count; ++d)
+        if (sh.list[d] == j) p += expf(A.logprob[n * A.count + d]);
+    store_gate<BF16>(A.dx, n * A.dstride + j, g * fmaf_(q, listed, -p));
+}
+// A whole row, from sums of its own.
+template <bool BF16>
+__device__ __forceinline__ void write_row(const Args &A, int64_t n, const RowView<BF16> &row, Shared &sh,
+                                          uint32_t (&marks)[kSectionAgain / 4], float (&logit)[kMost], float g,
+                                          float r, float listed)
+{
+    constexpr int K = RowView<BF16>::K;
+    const float c = A.scale * kLog2e;
+    for (int e = threadIdx.x; e < A.count; e += kThreads)
+        logit[e] = sh.list[e] >= 0 && sh.list[e] < A.V ? load_gate<BF16>(A.x, n * A.stride + sh.list[e]) : 0.0f;
+    Sum rest = no_sum();
+    for (int64_t s0 = 0; s0 < row.vectors; s0 += kSectionAgain) {
+        const int64_t s1 = min(row.vectors, s0 + kSectionAgain);
+        mark_listed<BF16, kSectionAgain>(A, row, s0, s1, sh, marks);
+        for (int64_t at = s0 + threadIdx.x; at < s1; at += kThreads) {
+            float x[K];
+            row.load(at, x);
+            add_unmarked(rest, x, marks[(at - s0) / 4] >> (8 * ((at - s0) % 4)) & 0xffu, c);
+        }
+    }
+    rest = join_all(rest, c, sh.sums);
+    const Sum all = join(join_all(listed_of<BF16>(A, n, sh), c, sh.sums), rest, c);
+    const float q_rest = ex2(c * (rest.m - all.m)) / all.s;  // of a token at rest.m
+    const float weight = rest.s == 0.0f ? 0.0f : fmaf_(q_rest, listed, -r / rest.s);
+    for (int64_t at = threadIdx.x; at < row.vectors; at += kThreads) {
+        float d[K];
+        row.load(at, d);
+#pragma unroll
+        for (int k = 0; k < K; ++k) d[k] = c * (d[k] - rest.m);
+        write_vector<BF16>(A, n, row, at, d, g, weight, false);
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
+    __syncthreads();
+    for (int e = threadIdx.x; e < A.count; e += kThreads)
+        if (sh.list[e] >= 0 && sh.list[e] < A.V)
+            write_listed<BF16>(A, n, sh, e, g, ex2(c * (logit[e] - all.m)) / all.s, listed);
+}
+
 // The gradient, U vectors a lane as in the scores' gradient: every token as
 // one that is not listed; then, behind a wait for these stores, the list's
 // tokens once more.  Their logits are read before anything is written, for the
-// gradient may take the logits' place.  Where the student leaves less than e^kFar
-// to the other tokens, a rare row, its first workgroup sums these again and writes
-// all of it (nobody may write a row that is still to be summed).
-// Bound by HBM and vector instructions: 8192 rows of 32000 bfloat16 224 us a call,
-// 4.7 TB/s, float32 430 us, 4.9 TB/s.
+// gradient may take the logits' place.  A rare row, where the student leaves less
+// than e^kFar to the other tokens or lse is beyond kLarge, is summed again by its first
+// workgroup, which writes all of it (nobody may write a row that is still to be summed).
+// Bound by HBM and vector instructions: 8192 rows of 32000 bfloat16 232 us a call,
+// 4.5 TB/s, float32 416 us, 5.0 TB/s; all of them rare ones 960 us.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
 {
@@ -262,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
     constexpr int K = Row::K, U = kScoreUnroll;
     __shared__ Shared sh;
     __shared__ uint32_t marks[kSectionAgain / 4];
+    __shared__ float logit[kMost];
     const int64_t n = blockIdx.x / A.parts;
     const Row row(A.x, n * A.stride, A.V);
     const int64_t first = (blockIdx.x - n * A.parts) * (U * kThreads), i = first + threadIdx.x;
@@ -293,56 +376,8 @@ __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
     float r = A.tail ? (float)(1.0 - P) : 0.0f;
     if (r < kRest) r = 0.0f;
     const float listed = (float)P + r;
-    // a vector of tokens that are not listed, from the exponents of their exponentials
-    const auto write = [&](int64_t at, float (&d)[K], float weight) {
-        const int64_t e = row.element(at);
-#pragma unroll
-        for (int k = 0; k < K; ++k) d[k] = none ? 0.0f : g * (ex2(d[k]) * weight);
-        if (e >= 0) {
-            store_raw<BF16, K>(A.dx, n * A.dstride, e, A.V, d);
-        } else {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (e + k >= 0 && e + k < A.V) store_gate<BF16>(A.dx, n * A.dstride + e + k, d[k]);
-        }
-    };
-    const auto write_list = [&](int64_t e0, int64_t e1) {
-        __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
-        __syncthreads();
-        if (none) return;
-#pragma unroll
-        for (int s = 0; s < kEach; ++s) {
-            const int e = s * kThreads + threadIdx.x;
-            if (e >= A.count) break;
-            const int64_t j = sh.list[e];
-            if (j < 0 || j >= A.V || j < e0 || j >= e1 || !leads(sh, e)) continue;
-            float p = 0.0f;
-            for (int d = e; d < A.count; ++d)
-                if (sh.list[d] == j) p += expf(A.logprob[n * A.count + d]);
-            const float q = ex2(kLog2e * fmaf_(A.scale, mine[s], -lse));
-            store_gate<BF16>(A.dx, n * A.dstride + j, g * fmaf_(q, listed, -p));
-        }
-    };
-    if (!none && r > 0.0f && log_rest < kFar) {
-        if (first > 0) return;
-        const float c = A.scale * kLog2e;
-#pragma unroll
-        for (int s = 0; s < kEach; ++s) {
-            const int e = s * kThreads + threadIdx.x;
-            if (e < A.count && sh.list[e] >= 0 && sh.list[e] < A.V)
-                mine[s] = load_gate<BF16>(A.x, n * A.stride + sh.list[e]);
-        }
-        const Sum rest = join_all(rest_of<BF16, kSectionAgain, 1>(A, row, 0, row.vectors, sh, marks), c, sh.sums);
-        // (q_rest listed is nothing beside r, which is kRest at least)
-        const float weight = rest.s == 0.0f ? 0.0f : -r / rest.s;
-        for (int64_t at = threadIdx.x; at < row.vectors; at += kThreads) {
-            float d[K];
-            row.load(at, d);
-#pragma unroll
-            for (int k = 0; k < K; ++k) d[k] = c * (d[k] - rest.m);
-            write(at, d, weight);
-        }
-        write_list(0, A.V);
+    if (!none && P == P && ((r > 0.0f && log_rest < kFar) || fabsf(lse) > kLarge)) {
+        if (first == 0) write_row<BF16>(A, n, row, sh, marks, logit, g, r, listed);
         return;
     }
     // r shares of q_rest, or without an r q itself
@@ -355,9 +390,19 @@ __global__ void __launch_bounds__(kThreads) distill_adjoint_kernel(Args A)
         Row::values(raw[q], x);
 #pragma unroll
         for (int k = 0; k < K; ++k) x[k] = kLog2e * fmaf_(A.scale, x[k], -from);
-        write(i + q * kThreads, x, weight);
+        write_vector<BF16>(A, n, row, i + q * kThreads, x, g, weight, none);
     }
-    write_list(e0, e1);
+    __builtin_amdgcn_s_waitcnt(0);  // the stores above have arrived
+    __syncthreads();
+    if (none) return;
+#pragma unroll
+    for (int s = 0; s < kEach; ++s) {
+        const int e = s * kThreads + threadIdx.x;
+        if (e >= A.count) break;
+        const int64_t j = sh.list[e];
+        if (j < 0 || j >= A.V || j < e0 || j >= e1) continue;
+        write_listed<BF16>(A, n, sh, e, g, ex2(kLog2e * fmaf_(A.scale, mine[s], -lse)), listed);
+    }
 }
 
 }  // namespace distill

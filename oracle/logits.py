@@ -13,8 +13,8 @@ def _row(x, scale):
     if np.isneginf(z).all():
         return np.full_like(z, -np.inf), -np.inf
     m = z.max()
-    lse = m + np.log(np.exp(z - m).sum())
-    return z - lse, lse
+    log_s = np.log(np.exp(z - m).sum())
+    return z - m - log_s, m + log_s  # (next to a row of -1e38 the sum's logarithm is nothing)
 
 
 def _sum_of(z):

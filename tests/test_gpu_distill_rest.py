@@ -100,3 +100,46 @@ def test_an_index_past_the_vocabulary(V, half):
     grad = pr.distill_top_adjoint(x, index, lp, out["lse"], out["log_rest"], ones)
     want = pr.distill_top_adjoint(x, good, lp, fine["lse"], fine["log_rest"], ones)
     assert bool(grad[[1, 3]].isnan().all()) and torch.equal(grad[[0, 2]], want[[0, 2]])
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("V", [5, 1000, 40001])
+@pytest.mark.parametrize("at", [5000.0, -5000.0, -1e9, -3.5e38])
+def test_rows_far_from_zero(at, V, tail, half):
+    """Logits of 5000 and more, a row that a finite mask left nothing of: lse as a
+    float32 holds no log V beside them, so q comes from the row's own maximum and sum,
+    with the roundings of a share."""
+    r = np.random.default_rng(V)
+    dtype = torch.bfloat16 if half else torch.float32
+    x = np.full((3, V), at)
+    x[1] += 40 * r.standard_normal(V)
+    x[2] = r.standard_normal(V)
+    x = torch.from_numpy(x).float().clamp(min=torch.finfo(dtype).min).to(dtype)
+    index = np.stack([r.permutation(V)[:4] for _ in range(3)])
+    lp = np.float32(np.log(r.dirichlet(np.ones(4), 3) * 0.8)).astype(np.float64)
+    dev = [x.to(DEV), torch.from_numpy(index).to(DEV), torch.from_numpy(lp).float().to(DEV)]
+    out = pr.distill_top(*dev, tail=tail)
+    args = (*dev, out["lse"], out["log_rest"], torch.ones(3, device=DEV))
+    grad = pr.distill_top_adjoint(*args, tail=tail)
+    x = x.double().numpy()
+    want = ref.distill_top_adjoint(x, index, lp, np.ones(3), tail)
+    d = x - x.max(1, keepdims=True)
+    q = np.exp(d) / np.exp(d).sum(1, keepdims=True)
+    listed = np.zeros((3, V), bool)
+    np.put_along_axis(listed, index, True, 1)
+    p = np.exp(lp)
+    left = np.where(tail, 1 - p.sum(1, keepdims=True), 0.0)
+    e = np.where(listed, -np.inf, d)
+    e = e - e.max(1, keepdims=True)
+    share = np.exp(e) / np.exp(e).sum(1, keepdims=True)
+    terms = (3 * (V / 256 + 32) + 64) * U + 12 * U * (1 + np.where(np.abs(d) < 200, np.abs(d), 0.0) + 12)
+    most = np.where(np.abs(d) < 30, terms, 0.0).max(1, keepdims=True)
+    tol = (2 * q + left * share) * (terms + most + 5 * U / 0.2) + np.where(listed, 16 * U, 0.0) + 1e-36
+    if half:
+        tol += 2.0 ** -8 * (np.abs(want) + tol)
+    got = grad.double().cpu().numpy()
+    off = np.abs(got - want) - tol
+    assert (off <= 0).all(), (np.argwhere(~(off <= 0))[:5].tolist(), got[~(off <= 0)][:5], want[~(off <= 0)][:5])
+    inplace = pr.distill_top_adjoint(*args, tail=tail, out=dev[0])
+    assert torch.equal(inplace, grad)

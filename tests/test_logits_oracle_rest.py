@@ -30,3 +30,9 @@ def test_a_finite_mask_is_shared_evenly(mask):
     x[0, 5] = 0.0
     got = ref.distill_top_adjoint(x, np.array([[5]]), np.log([[0.7]]), np.ones(1))
     assert np.allclose(np.delete(got[0], 5), -0.3 / 1000, rtol=1e-12) and abs(got.sum()) < 1e-12
+
+
+@pytest.mark.parametrize("all_at", [-1e9, float(np.finfo(np.float32).min)])
+def test_a_row_of_one_finite_mask_is_even(all_at):
+    got = ref.distill_top_adjoint(np.full((1, 1001), all_at), np.array([[5]]), np.log([[0.7]]), np.ones(1))
+    assert np.allclose(np.delete(got[0], 5), 1 / 1001 - 0.3 / 1000, atol=1e-15) and abs(got[0, 5] - (1 / 1001 - 0.7)) < 1e-15

@@ -9,8 +9,8 @@
 // q_rest is summed over the tokens themselves: as 1 - sum q_{j_e} it would be
 // lost where the student agrees with the teacher.  q_j / q_rest is one
 // exponential, a share of r however small the two are.  Where lse or log q_rest
-// are too large to hold the sums that they come from, the gradient sums again.  Sums are float32 relative
-// to a running maximum; those of the short list float64.
+// are too large to hold the sums that they come from, the gradient sums again.
+// Sums are float32 relative to a running maximum; those of the short list float64.
 #pragma once
 
 #include "score.hpp"
